@@ -799,6 +799,194 @@ kvc_status kvc_tail_compact(kvc_bf16 *kpool, kvc_bf16 *vpool, int64_t n_slots, i
                             const int32_t *dst_slot, const int32_t *n_pairs, int32_t pair_cap,
                             int32_t n_req, int32_t *dev_status, cudaStream_t stream);
 
+/* ========================================================================
+ * Tree decoding on the paged layout, and eviction by accumulated weight (no
+ * counterpart on the pages, which leave decoding to an attention backend).
+ * The step a serving loop runs between two compressions:
+ *   kvc_tree_attn    per layer: the drafted nodes attend to the cache and to
+ *                    their ancestors (one node: plain decoding), with the LSE
+ *                    that kvc_recover_score and kvc_attn_mass take;
+ *   kvc_tree_commit  all layers: the accepted path's K and V rows move to the
+ *                    positions that follow the cache;
+ *   kvc_attn_mass    all layers: the accepted rows' attention weights are
+ *                    added up per (layer, KV head, cached row);
+ *   kvc_mass_evict   all layers: per (layer, KV head) the rows with the least
+ *                    weight leave, the cache is dense again.
+ * Same pools, block table and position → slot rule as above.  Every entry
+ * point takes any H ≥ 1, Hq a multiple of H with Hq ≤ 256, D ∈ {64, 128} and
+ * block_size in [1, 64].
+ * ====================================================================== */
+
+/* Most nodes of one request's tree. */
+#define KVC_TREE_MAX_NODES 1024
+/* Longest request (max_blocks · block_size) the calls below accept. */
+#define KVC_TREE_MAX_TOKENS (1 << 24)
+
+/* ------------------------------------------------------------------------
+ * Attention of drafted token trees over the cache, one layer.  Request r has
+ * c = ctx_len[r] cached positions and T = q_off[r+1] − q_off[r] ≤ max_tree
+ * nodes; node j's key and value are in the pools at position c + j, and row
+ * q_off[r] + i of q is node i's query.  Row i sees every cached position and
+ * node j iff bit j%32 of tree_mask[q_off[r] + i][j/32] is set (its ancestors
+ * and itself in a drafted tree; a node not marked for itself does not see
+ * itself).  tree_mask NULL: a chain, node i sees the nodes j ≤ i.
+ *   z_p = scale · q·k_p over the visible p;  lse = ln Σ exp z_p;
+ *   out = Σ exp(z_p − lse) · v_p
+ * A row that sees nothing (no cached position, no mask bit) gets out = 0 and
+ * lse = −inf.  Keys and values that a row does not see never reach its
+ * result, whatever they hold.
+ *   q           device bf16 [n_q][Hq][D]
+ *   kpool, vpool device bf16 [n_slots][H][D]: one layer of the pools
+ *   block_table device int32 [n_req][max_blocks]
+ *   ctx_len     device int32 [n_req];  q_off  device int32 [n_req+1]
+ *   tree_mask   device uint32 [n_q][mask_words], mask_words ≥ ⌈max_tree/32⌉
+ *   out         device bf16 [n_q][Hq][D];  lse  device fp32 [n_q][Hq]
+ *   ws          device scratch of kvc_tree_attn_workspace_size() bytes (the
+ *               size depends on the current device's SM count)
+ * Accuracy: logits, softmax statistics and the value sums are fp32; the
+ * weights exp(z − max) are rounded to bf16 for the product with V (their sum
+ * is taken before that rounding), out is rounded once to bf16.  Repeated
+ * calls give the same bits.
+ * A request whose ctx_len or q_off is out of range (negative, T > max_tree,
+ * c + T > max_blocks·block_size, rows past n_q) is recorded as
+ * KVC_ERR_BOUNDS and its rows are left untouched; a visible position whose
+ * block id is outside the pool is recorded and treated as not visible.
+ * Errors: KVC_ERR_INVALID_ARG (NULL, sizes < 1, scale not finite),
+ * KVC_ERR_SHAPE (D, Hq % H, Hq > 256, block_size > 64, max_tree >
+ * KVC_TREE_MAX_NODES, too many positions, mask_words too small),
+ * KVC_ERR_ALIGN, KVC_ERR_WORKSPACE.
+ * ---------------------------------------------------------------------- */
+size_t kvc_tree_attn_workspace_size(int32_t n_req, int32_t max_blocks, int32_t max_tree,
+                                    int32_t H, int32_t Hq, int32_t D, int32_t block_size);
+kvc_status kvc_tree_attn(const kvc_bf16 *q, const kvc_bf16 *kpool, const kvc_bf16 *vpool,
+                         int64_t n_slots, const int32_t *block_table, int32_t max_blocks,
+                         const int32_t *ctx_len, const int32_t *q_off,
+                         const uint32_t *tree_mask, int32_t mask_words, int32_t n_req,
+                         int32_t n_q, int32_t max_tree, int32_t H, int32_t Hq, int32_t D,
+                         int32_t block_size, float scale, kvc_bf16 *out, float *lse, void *ws,
+                         size_t ws_bytes, int32_t *dev_status, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Commit of the accepted path, all layers.  For request r with c =
+ * ctx_len[r], T = q_off[r+1] − q_off[r] nodes and the accepted nodes
+ * path[r][0] < path[r][1] < … (n = n_path[r] ≥ 0 of them):
+ *   K and V row of position c + path[r][i]  →  position c + i  (i < n),
+ * in place, every layer and KV head (bit copies; a row is read before
+ * another replaces it), and for the next calls
+ *   seq_out[r] = c + n
+ *   row_idx[r][i] = q_off[r] + path[r][i],  row_vis[r][i] = c + i + 1
+ *   (i < n; 0 and 0 for n ≤ i < max_path): kvc_attn_mass's rows.
+ *   kpool, vpool device bf16 [L][n_slots][H][D]  in/out
+ *   path         device int32 [n_req][max_path]; n_path device int32 [n_req]
+ *   seq_out      device int32 [n_req] out
+ *   row_idx, row_vis device int32 [n_req][max_path] out, may be NULL
+ * A request whose ctx_len, q_off, n_path or path is out of range (path not
+ * ascending or not below T) is recorded as KVC_ERR_BOUNDS: no row moves,
+ * seq_out[r] = max(c, 0), its row_vis are 0.  A block id outside the pool is
+ * recorded and the row's copy skipped.
+ * Errors: KVC_ERR_INVALID_ARG, KVC_ERR_SHAPE (D, block_size > 64, max_path >
+ * KVC_TREE_MAX_NODES, too many positions), KVC_ERR_ALIGN.
+ * ---------------------------------------------------------------------- */
+kvc_status kvc_tree_commit(kvc_bf16 *kpool, kvc_bf16 *vpool, int64_t n_slots,
+                           const int32_t *block_table, int32_t max_blocks,
+                           const int32_t *ctx_len, const int32_t *q_off, const int32_t *path,
+                           const int32_t *n_path, int32_t max_path, int32_t n_req, int32_t L,
+                           int32_t H, int32_t D, int32_t block_size, int32_t *seq_out,
+                           int32_t *row_idx, int32_t *row_vis, int32_t *dev_status,
+                           cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Accumulated attention weight, all layers: for every layer l, request r, KV
+ * head h and position p < seqused_k[r],
+ *   mass[l][r][h][p] ← (p < n_mass[r] ? decay·mass[l][r][h][p] : 0)
+ *       + Σ_{rows i of r with p < row_vis[i]} Σ_{g<G}
+ *             exp(scale·q[l][x_i][hG+g]·k_p − lse[l][x_i][hG+g])
+ * where the rows of request r are i in [row_off[r], row_off[r+1]) and row
+ * i's query is x_i = row_idx[i] (row_idx NULL: x_i = i).  The weights are
+ * attention's own, recovered from its LSE; the rows are the accepted path of
+ * a tree (kvc_tree_commit writes row_idx and row_vis), the last window of
+ * queries, or a whole prompt (row_vis ascending).  Positions at or past
+ * seqused_k[r] are left untouched; positions past n_mass[r] hold no weight
+ * yet and start from 0.
+ *   q           device bf16 [L][n_q][Hq][D]
+ *   lse         device fp32 [L][n_q][Hq], natural log; a row and head with
+ *               lse −inf (nothing visible) adds nothing
+ *   row_idx     device int32 [n_rows] or NULL;  row_vis device int32
+ *               [n_rows], < 1: the row adds nothing
+ *   row_off     device int32 [n_req+1], each request ≤ max_rows rows
+ *   kpool       device bf16 [L][n_slots][H][D]
+ *   seqused_k, n_mass device int32 [n_req]
+ *   mass        device fp32 [L][n_req][H][max_blocks·block_size] in/out
+ *   ws          device scratch of kvc_attn_mass_workspace_size() bytes (may
+ *               be NULL when that is 0)
+ * Accuracy: products, exponents and sums are fp32, each weight within 2^-18
+ * relative for |z|, |lse| ≤ 16.  No atomics: repeated calls on the same
+ * inputs give the same bits.
+ * A seqused_k or row_off out of range is recorded as KVC_ERR_BOUNDS and the
+ * request skipped; a row_idx outside [0, n_q) is recorded and the row
+ * ignored; a block id outside the pool is recorded and its positions gain
+ * nothing.
+ * Errors: KVC_ERR_INVALID_ARG (NULL, sizes < 1, scale not finite, decay
+ * outside [0, 1], n_q < n_rows without row_idx), KVC_ERR_SHAPE,
+ * KVC_ERR_ALIGN, KVC_ERR_WORKSPACE.
+ * ---------------------------------------------------------------------- */
+size_t kvc_attn_mass_workspace_size(int32_t n_req, int32_t max_blocks, int32_t max_rows,
+                                    int32_t L, int32_t H, int32_t Hq, int32_t D,
+                                    int32_t block_size);
+kvc_status kvc_attn_mass(const kvc_bf16 *q, const float *lse, int32_t n_q,
+                         const int32_t *row_idx, const int32_t *row_vis,
+                         const int32_t *row_off, int32_t n_rows, int32_t max_rows,
+                         const kvc_bf16 *kpool, int64_t n_slots, const int32_t *block_table,
+                         int32_t max_blocks, const int32_t *seqused_k, const int32_t *n_mass,
+                         int32_t n_req, int32_t L, int32_t H, int32_t Hq, int32_t D,
+                         int32_t block_size, float scale, float decay, float *mass, void *ws,
+                         size_t ws_bytes, int32_t *dev_status, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Eviction by accumulated weight, all layers, each (layer, KV head) by its
+ * own weights.  Request r holds n = seqused_k[r] rows per (layer, head), of
+ * t_end[r] tokens seen so far.  Row p's original position is pos[l][r][h][p]
+ * for p < n_pos[r] (rows carried over from an earlier eviction) and t_end[r]
+ * − (n − p) after them (rows appended since, in order).  With m = min(n,
+ * budget):
+ *   n ≤ budget: every row stays.
+ *   otherwise the rows are ranked: first those with original position
+ *   < n_sink or ≥ t_end[r] − n_recent (pinned), then by weight descending, a
+ *   lower row first among equals (−0 = +0, NaN last); the first `budget` stay.
+ *   The k-th staying row at or past `budget` (ascending) moves to the k-th
+ *   row below `budget` that does not stay: K, V, weight and position.  Rows
+ *   that stay below `budget` are not moved, so a step's traffic is what it
+ *   evicts; the cache is dense in [0, m), not in original order.
+ *   kpool, vpool  device bf16 [L][n_slots][H][D]  in/out
+ *   mass, pos     device fp32 / int32 [L][n_req][H][max_blocks·block_size]
+ *   mass_out, pos_out  same shapes, out: rows [0, m) written (the kept
+ *                 weights and original positions), the rest untouched; may
+ *                 be mass and pos themselves, not overlap them otherwise
+ *   n_out         device int32 [n_req] out: m (0 for a skipped request)
+ *   ws            device scratch of kvc_mass_evict_workspace_size() bytes
+ *                 (0, and ws may be NULL, while max_blocks·block_size ≤
+ *                 KVC_EVICT_STAGED_ROWS)
+ * Afterwards the blocks past ⌈m/block_size⌉ are free, and seqused_k = n_mass
+ * = n_pos = m for the next step.  A NaN weight is recorded as KVC_ERR_NAN.
+ * A seqused_k out of range is recorded as KVC_ERR_BOUNDS and the request
+ * skipped; a block id outside the pool is recorded and the row's K and V
+ * stay where they are.  n_pos is clamped to [0, n].
+ * Errors: KVC_ERR_INVALID_ARG, KVC_ERR_BUDGET (budget < 1, n_sink < 0,
+ * n_recent < 0, n_sink + n_recent > budget), KVC_ERR_SHAPE, KVC_ERR_ALIGN,
+ * KVC_ERR_WORKSPACE.
+ * ---------------------------------------------------------------------- */
+#define KVC_EVICT_STAGED_ROWS 49152
+size_t kvc_mass_evict_workspace_size(int32_t n_req, int32_t max_blocks, int32_t L, int32_t H,
+                                     int32_t block_size, int32_t budget);
+kvc_status kvc_mass_evict(kvc_bf16 *kpool, kvc_bf16 *vpool, int64_t n_slots,
+                          const int32_t *block_table, int32_t max_blocks,
+                          const int32_t *seqused_k, const int32_t *n_pos, const int32_t *t_end,
+                          const float *mass, const int32_t *pos, float *mass_out,
+                          int32_t *pos_out, int32_t *n_out, int32_t n_req, int32_t L, int32_t H,
+                          int32_t D, int32_t block_size, int32_t budget, int32_t n_sink,
+                          int32_t n_recent, void *ws, size_t ws_bytes, int32_t *dev_status,
+                          cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

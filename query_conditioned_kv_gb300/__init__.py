@@ -28,7 +28,10 @@ __all__ = [
     "kvc_recover_score", "kvc_recover_score_ex", "kvc_recover_score_workspace_size",
     "kvc_recover_tensor_core", "kvc_tail_plan", "kvc_tail_compact",
     "kvc_lrfu_update", "kvc_token_confidence", "kvc_conf_trend_budget",
-    "TAIL_MAX_TOKENS",
+    "TAIL_MAX_TOKENS", "TREE_MAX_NODES", "EVICT_STAGED_ROWS",
+    "kvc_tree_attn_workspace_size", "kvc_tree_attn", "kvc_tree_commit",
+    "kvc_attn_mass_workspace_size", "kvc_attn_mass",
+    "kvc_mass_evict_workspace_size", "kvc_mass_evict",
     "kvc_pack_tiered_slots", "kvc_repo_plan", "KvcRepo",
 ]
 
@@ -39,6 +42,8 @@ SELECT_MAX_SEG = 1 << 30
 LRFU_MAX_SEG = 49152
 SCORE_MAX_ROWS = 256
 TAIL_MAX_TOKENS = 1 << 20
+TREE_MAX_NODES = 1024
+EVICT_STAGED_ROWS = 49152
 
 # kvc_kernel values (include/kvc.h): the kernel an _ex entry point runs
 KERNELS = {
@@ -130,6 +135,18 @@ _SIGS = {
                                  _P, _P, _P, _P, _P, _P, _P, _P]),
     "kvc_tail_compact": (_c.c_int, [_P, _P, _I64, _I32, _I32, _I32, _P, _P, _P,
                                     _I32, _I32, _P, _P]),
+    "kvc_tree_attn_workspace_size": (_SZ, [_I32] * 7),
+    "kvc_tree_attn": (_c.c_int, [_P, _P, _P, _I64, _P, _I32, _P, _P, _P] + [_I32] * 8
+                      + [_c.c_float, _P, _P, _P, _SZ, _P, _P]),
+    "kvc_tree_commit": (_c.c_int, [_P, _P, _I64, _P, _I32, _P, _P, _P, _P] + [_I32] * 6
+                        + [_P, _P, _P, _P, _P]),
+    "kvc_attn_mass_workspace_size": (_SZ, [_I32] * 8),
+    "kvc_attn_mass": (_c.c_int, [_P, _P, _I32, _P, _P, _P, _I32, _I32, _P, _I64, _P, _I32, _P,
+                                 _P] + [_I32] * 6 + [_c.c_float, _c.c_float, _P, _P, _SZ, _P,
+                                                     _P]),
+    "kvc_mass_evict_workspace_size": (_SZ, [_I32] * 6),
+    "kvc_mass_evict": (_c.c_int, [_P, _P, _I64, _P, _I32] + [_P] * 8 + [_I32] * 8
+                       + [_P, _SZ, _P, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(lib, _name)
@@ -556,3 +573,66 @@ def kvc_conf_trend_budget(conf, trace_off, n_trace, max_trace_len, window, strid
                                   stride, float(bottom_pct), budget_step, max_budget,
                                   _ptr(slope), _ptr(budget), _ptr(n_kept), _ptr(dev_status),
                                   _stream(stream)), "kvc_conf_trend_budget")
+
+
+def _ws_bytes(ws) -> int:
+    return 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def kvc_tree_attn_workspace_size(n_req, max_blocks, max_tree, H, Hq, D, block_size) -> int:
+    return int(lib.kvc_tree_attn_workspace_size(n_req, max_blocks, max_tree, H, Hq, D,
+                                                block_size))
+
+
+def kvc_tree_attn(q, kpool, vpool, n_slots, block_table, max_blocks, ctx_len, q_off, tree_mask,
+                  mask_words, n_req, n_q, max_tree, H, Hq, D, block_size, scale, out, lse, ws,
+                  dev_status=None, stream=None):
+    """Attention of drafted token trees over one layer of a paged cache
+    (tree_mask None: a chain; max_tree 1: plain decoding)."""
+    _ok(lib.kvc_tree_attn(_ptr(q), _ptr(kpool), _ptr(vpool), n_slots, _ptr(block_table),
+                          max_blocks, _ptr(ctx_len), _ptr(q_off), _ptr(tree_mask), mask_words,
+                          n_req, n_q, max_tree, H, Hq, D, block_size, scale, _ptr(out),
+                          _ptr(lse), _ptr(ws), _ws_bytes(ws), _ptr(dev_status),
+                          _stream(stream)), "kvc_tree_attn")
+
+
+def kvc_tree_commit(kpool, vpool, n_slots, block_table, max_blocks, ctx_len, q_off, path,
+                    n_path, max_path, n_req, L, H, D, block_size, seq_out, row_idx=None,
+                    row_vis=None, dev_status=None, stream=None):
+    """Moves the accepted nodes' K/V rows behind the cache, all layers."""
+    _ok(lib.kvc_tree_commit(_ptr(kpool), _ptr(vpool), n_slots, _ptr(block_table), max_blocks,
+                            _ptr(ctx_len), _ptr(q_off), _ptr(path), _ptr(n_path), max_path,
+                            n_req, L, H, D, block_size, _ptr(seq_out), _ptr(row_idx),
+                            _ptr(row_vis), _ptr(dev_status), _stream(stream)),
+        "kvc_tree_commit")
+
+
+def kvc_attn_mass_workspace_size(n_req, max_blocks, max_rows, L, H, Hq, D, block_size) -> int:
+    return int(lib.kvc_attn_mass_workspace_size(n_req, max_blocks, max_rows, L, H, Hq, D,
+                                                block_size))
+
+
+def kvc_attn_mass(q, lse, n_q, row_idx, row_vis, row_off, n_rows, max_rows, kpool, n_slots,
+                  block_table, max_blocks, seqused_k, n_mass, n_req, L, H, Hq, D, block_size,
+                  scale, decay, mass, ws=None, dev_status=None, stream=None):
+    """Adds the rows' attention weights to mass, per (layer, KV head, position)."""
+    _ok(lib.kvc_attn_mass(_ptr(q), _ptr(lse), n_q, _ptr(row_idx), _ptr(row_vis), _ptr(row_off),
+                          n_rows, max_rows, _ptr(kpool), n_slots, _ptr(block_table), max_blocks,
+                          _ptr(seqused_k), _ptr(n_mass), n_req, L, H, Hq, D, block_size, scale,
+                          decay, _ptr(mass), _ptr(ws), _ws_bytes(ws), _ptr(dev_status),
+                          _stream(stream)), "kvc_attn_mass")
+
+
+def kvc_mass_evict_workspace_size(n_req, max_blocks, L, H, block_size, budget) -> int:
+    return int(lib.kvc_mass_evict_workspace_size(n_req, max_blocks, L, H, block_size, budget))
+
+
+def kvc_mass_evict(kpool, vpool, n_slots, block_table, max_blocks, seqused_k, n_pos, t_end, mass,
+                   pos, mass_out, pos_out, n_out, n_req, L, H, D, block_size, budget, n_sink,
+                   n_recent, ws=None, dev_status=None, stream=None):
+    """Keeps `budget` rows per (layer, KV head) by accumulated weight, in place."""
+    _ok(lib.kvc_mass_evict(_ptr(kpool), _ptr(vpool), n_slots, _ptr(block_table), max_blocks,
+                           _ptr(seqused_k), _ptr(n_pos), _ptr(t_end), _ptr(mass), _ptr(pos),
+                           _ptr(mass_out), _ptr(pos_out), _ptr(n_out), n_req, L, H, D,
+                           block_size, budget, n_sink, n_recent, _ptr(ws), _ws_bytes(ws),
+                           _ptr(dev_status), _stream(stream)), "kvc_mass_evict")

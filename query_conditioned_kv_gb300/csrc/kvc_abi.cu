@@ -22,6 +22,20 @@ kvc_status from_cuda_kernel(cudaError_t e) {
   return from_cuda(e);
 }
 
+// Sizes every call on the paged decoding layout shares: positive counts, the
+// head dimension, the page size, and products the kernels index with int32.
+kvc_status paged_status(int64_t L, int64_t n_req, int64_t H, int D, int64_t BS,
+                        int64_t max_blocks, int64_t n_slots) {
+  if (L < 1 || n_req < 1 || H < 1 || BS < 1 || max_blocks < 1 || n_slots < BS ||
+      n_slots > INT32_MAX)
+    return KVC_ERR_INVALID_ARG;
+  if (!head_dim_ok(D) || BS > 64 || H > 256 || max_blocks * BS > KVC_TREE_MAX_TOKENS ||
+      L * n_req * H > INT32_MAX || n_req * max_blocks > INT32_MAX || L > 65535 || n_req > 65535)
+    return KVC_ERR_SHAPE;
+  return KVC_OK;
+}
+bool heads_ok(int H, int Hq) { return Hq >= H && Hq % H == 0 && Hq <= 256; }
+
 bool score_kernel_ok(kvc_kernel k) {
   return k == KVC_KERNEL_AUTO || (k >= KVC_KERNEL_SCORE_FUSED && k <= KVC_KERNEL_SCORE_GROUP);
 }
@@ -485,6 +499,136 @@ kvc_status kvc_tail_compact(kvc_bf16 *kpool, kvc_bf16 *vpool, int64_t n_slots, i
   if (!aligned16(kpool) || !aligned16(vpool)) return KVC_ERR_ALIGN;
   return from_cuda(kvc::launch_tail_compact(kpool, vpool, n_slots, L, H, D, src_slot, dst_slot,
                                             n_pairs, pair_cap, n_req, dev_status, stream));
+}
+
+// ---- tree decoding and eviction by accumulated weight
+
+size_t kvc_tree_attn_workspace_size(int32_t n_req, int32_t max_blocks, int32_t max_tree,
+                                    int32_t H, int32_t Hq, int32_t D, int32_t block_size) {
+  if (n_req < 1 || max_tree < 1 || max_tree > KVC_TREE_MAX_NODES ||
+      paged_status(1, n_req, H, D, block_size, max_blocks, INT32_MAX) != KVC_OK ||
+      !heads_ok(H, Hq))
+    return 0;
+  return kvc::tree_attn_ws_bytes(n_req, max_blocks, max_tree, H, Hq, D, block_size);
+}
+
+kvc_status kvc_tree_attn(const kvc_bf16 *q, const kvc_bf16 *kpool, const kvc_bf16 *vpool,
+                         int64_t n_slots, const int32_t *block_table, int32_t max_blocks,
+                         const int32_t *ctx_len, const int32_t *q_off,
+                         const uint32_t *tree_mask, int32_t mask_words, int32_t n_req,
+                         int32_t n_q, int32_t max_tree, int32_t H, int32_t Hq, int32_t D,
+                         int32_t block_size, float scale, kvc_bf16 *out, float *lse, void *ws,
+                         size_t ws_bytes, int32_t *dev_status, cudaStream_t stream) {
+  if (!q || !kpool || !vpool || !block_table || !ctx_len || !q_off || !out || !lse || !ws)
+    return KVC_ERR_INVALID_ARG;
+  if (n_q < 1 || max_tree < 1 || !isfinite(scale)) return KVC_ERR_INVALID_ARG;
+  const kvc_status st = paged_status(1, n_req, H, D, block_size, max_blocks, n_slots);
+  if (st != KVC_OK) return st;
+  if (!heads_ok(H, Hq) || max_tree > KVC_TREE_MAX_NODES ||
+      (tree_mask && mask_words < (max_tree + 31) / 32))
+    return KVC_ERR_SHAPE;
+  if (!aligned16(q) || !aligned16(kpool) || !aligned16(vpool) || !aligned16(out) ||
+      !aligned16(lse) || !aligned16(ws))
+    return KVC_ERR_ALIGN;
+  if (ws_bytes < kvc_tree_attn_workspace_size(n_req, max_blocks, max_tree, H, Hq, D, block_size))
+    return KVC_ERR_WORKSPACE;
+  return from_cuda(kvc::launch_tree_attn(q, kpool, vpool, n_slots, block_table, max_blocks,
+                                         ctx_len, q_off, tree_mask, mask_words, n_req, n_q,
+                                         max_tree, H, Hq, D, block_size, scale, out, lse, ws,
+                                         dev_status, stream));
+}
+
+kvc_status kvc_tree_commit(kvc_bf16 *kpool, kvc_bf16 *vpool, int64_t n_slots,
+                           const int32_t *block_table, int32_t max_blocks,
+                           const int32_t *ctx_len, const int32_t *q_off, const int32_t *path,
+                           const int32_t *n_path, int32_t max_path, int32_t n_req, int32_t L,
+                           int32_t H, int32_t D, int32_t block_size, int32_t *seq_out,
+                           int32_t *row_idx, int32_t *row_vis, int32_t *dev_status,
+                           cudaStream_t stream) {
+  if (!kpool || !vpool || !block_table || !ctx_len || !q_off || !path || !n_path || !seq_out ||
+      max_path < 1)
+    return KVC_ERR_INVALID_ARG;
+  const kvc_status st = paged_status(L, n_req, H, D, block_size, max_blocks, n_slots);
+  if (st != KVC_OK) return st;
+  if (max_path > KVC_TREE_MAX_NODES) return KVC_ERR_SHAPE;
+  if (!aligned16(kpool) || !aligned16(vpool)) return KVC_ERR_ALIGN;
+  return from_cuda(kvc::launch_tree_commit(kpool, vpool, n_slots, block_table, max_blocks,
+                                           ctx_len, q_off, path, n_path, max_path, n_req, L, H,
+                                           D, block_size, seq_out, row_idx, row_vis, dev_status,
+                                           stream));
+}
+
+size_t kvc_attn_mass_workspace_size(int32_t n_req, int32_t max_blocks, int32_t max_rows,
+                                    int32_t L, int32_t H, int32_t Hq, int32_t D,
+                                    int32_t block_size) {
+  if (max_rows < 1 ||
+      paged_status(L, n_req, H, D, block_size, max_blocks, INT32_MAX) != KVC_OK ||
+      !heads_ok(H, Hq))
+    return 0;
+  return kvc::attn_mass_ws_bytes(n_req, max_blocks, max_rows, L, H, Hq, D, block_size);
+}
+
+kvc_status kvc_attn_mass(const kvc_bf16 *q, const float *lse, int32_t n_q,
+                         const int32_t *row_idx, const int32_t *row_vis,
+                         const int32_t *row_off, int32_t n_rows, int32_t max_rows,
+                         const kvc_bf16 *kpool, int64_t n_slots, const int32_t *block_table,
+                         int32_t max_blocks, const int32_t *seqused_k, const int32_t *n_mass,
+                         int32_t n_req, int32_t L, int32_t H, int32_t Hq, int32_t D,
+                         int32_t block_size, float scale, float decay, float *mass, void *ws,
+                         size_t ws_bytes, int32_t *dev_status, cudaStream_t stream) {
+  if (!q || !lse || !row_vis || !row_off || !kpool || !block_table || !seqused_k || !n_mass ||
+      !mass)
+    return KVC_ERR_INVALID_ARG;
+  if (n_q < 1 || n_rows < 1 || max_rows < 1 || (!row_idx && n_q < n_rows) || !isfinite(scale) ||
+      !(decay >= 0.f && decay <= 1.f))
+    return KVC_ERR_INVALID_ARG;
+  const kvc_status st = paged_status(L, n_req, H, D, block_size, max_blocks, n_slots);
+  if (st != KVC_OK) return st;
+  if (!heads_ok(H, Hq)) return KVC_ERR_SHAPE;
+  if (!aligned16(q) || !aligned16(lse) || !aligned16(kpool) || !aligned16(mass) ||
+      (ws && !aligned16(ws)))
+    return KVC_ERR_ALIGN;
+  const size_t need =
+      kvc_attn_mass_workspace_size(n_req, max_blocks, max_rows, L, H, Hq, D, block_size);
+  if (need && (!ws || ws_bytes < need)) return KVC_ERR_WORKSPACE;
+  return from_cuda(kvc::launch_attn_mass(q, lse, n_q, row_idx, row_vis, row_off, n_rows,
+                                         max_rows, kpool, n_slots, block_table, max_blocks,
+                                         seqused_k, n_mass, n_req, L, H, Hq, D, block_size,
+                                         scale, decay, mass, ws, dev_status, stream));
+}
+
+size_t kvc_mass_evict_workspace_size(int32_t n_req, int32_t max_blocks, int32_t L, int32_t H,
+                                     int32_t block_size, int32_t budget) {
+  if (budget < 1 || paged_status(L, n_req, H, 64, block_size, max_blocks, INT32_MAX) != KVC_OK)
+    return 0;
+  return kvc::mass_evict_ws_bytes(n_req, max_blocks, L, H, block_size, budget);
+}
+
+kvc_status kvc_mass_evict(kvc_bf16 *kpool, kvc_bf16 *vpool, int64_t n_slots,
+                          const int32_t *block_table, int32_t max_blocks,
+                          const int32_t *seqused_k, const int32_t *n_pos, const int32_t *t_end,
+                          const float *mass, const int32_t *pos, float *mass_out,
+                          int32_t *pos_out, int32_t *n_out, int32_t n_req, int32_t L, int32_t H,
+                          int32_t D, int32_t block_size, int32_t budget, int32_t n_sink,
+                          int32_t n_recent, void *ws, size_t ws_bytes, int32_t *dev_status,
+                          cudaStream_t stream) {
+  if (!kpool || !vpool || !block_table || !seqused_k || !n_pos || !t_end || !mass || !pos ||
+      !mass_out || !pos_out || !n_out)
+    return KVC_ERR_INVALID_ARG;
+  if (budget < 1 || n_sink < 0 || n_recent < 0 || (int64_t)n_sink + n_recent > budget)
+    return KVC_ERR_BUDGET;
+  const kvc_status st = paged_status(L, n_req, H, D, block_size, max_blocks, n_slots);
+  if (st != KVC_OK) return st;
+  if (!aligned16(kpool) || !aligned16(vpool) || !aligned16(mass) || !aligned16(pos) ||
+      !aligned16(mass_out) || !aligned16(pos_out) || (ws && !aligned16(ws)))
+    return KVC_ERR_ALIGN;
+  const size_t need =
+      kvc_mass_evict_workspace_size(n_req, max_blocks, L, H, block_size, budget);
+  if (need && (!ws || ws_bytes < need)) return KVC_ERR_WORKSPACE;
+  return from_cuda(kvc::launch_mass_evict(kpool, vpool, n_slots, block_table, max_blocks,
+                                          seqused_k, n_pos, t_end, mass, pos, mass_out, pos_out,
+                                          n_out, n_req, L, H, D, block_size, budget, n_sink,
+                                          n_recent, ws, dev_status, stream));
 }
 
 }  // extern "C"

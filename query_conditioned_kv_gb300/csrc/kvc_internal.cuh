@@ -202,4 +202,40 @@ cudaError_t launch_tail_compact(uint16_t *kpool, uint16_t *vpool, int64_t n_slot
                                 const int32_t *n_pairs, int cap, int n_req, int32_t *status,
                                 cudaStream_t s);
 
+// Tree decoding and eviction by accumulated weight (tree_attn.cu,
+// tree_commit.cu, attn_mass.cu, mass_evict.cu)
+size_t tree_attn_ws_bytes(int n_req, int max_blocks, int max_tree, int H, int Hq, int D, int BS);
+cudaError_t launch_tree_attn(const uint16_t *q, const uint16_t *kpool, const uint16_t *vpool,
+                             int64_t n_slots, const int32_t *block_table, int max_blocks,
+                             const int32_t *ctx_len, const int32_t *q_off,
+                             const uint32_t *tree_mask, int mask_words, int n_req, int n_q,
+                             int max_tree, int H, int Hq, int D, int BS, float scale,
+                             uint16_t *out, float *lse, void *ws, int32_t *status,
+                             cudaStream_t s);
+cudaError_t launch_tree_commit(uint16_t *kpool, uint16_t *vpool, int64_t n_slots,
+                               const int32_t *block_table, int max_blocks,
+                               const int32_t *ctx_len, const int32_t *q_off,
+                               const int32_t *path, const int32_t *n_path, int max_path,
+                               int n_req, int L, int H, int D, int BS, int32_t *seq_out,
+                               int32_t *row_idx, int32_t *row_vis, int32_t *status,
+                               cudaStream_t s);
+size_t attn_mass_ws_bytes(int n_req, int max_blocks, int max_rows, int L, int H, int Hq, int D,
+                          int BS);
+cudaError_t launch_attn_mass(const uint16_t *q, const float *lse, int n_q,
+                             const int32_t *row_idx, const int32_t *row_vis,
+                             const int32_t *row_off, int n_rows, int max_rows,
+                             const uint16_t *kpool, int64_t n_slots,
+                             const int32_t *block_table, int max_blocks,
+                             const int32_t *seqused, const int32_t *n_mass, int n_req, int L,
+                             int H, int Hq, int D, int BS, float scale, float decay, float *mass,
+                             void *ws, int32_t *status, cudaStream_t s);
+size_t mass_evict_ws_bytes(int n_req, int max_blocks, int L, int H, int BS, int budget);
+cudaError_t launch_mass_evict(uint16_t *kpool, uint16_t *vpool, int64_t n_slots,
+                              const int32_t *block_table, int max_blocks,
+                              const int32_t *seqused, const int32_t *n_pos,
+                              const int32_t *t_end, const float *mass, const int32_t *pos,
+                              float *mass_out, int32_t *pos_out, int32_t *n_out, int n_req,
+                              int L, int H, int D, int BS, int budget, int n_sink, int n_recent,
+                              void *ws, int32_t *status, cudaStream_t s);
+
 }  // namespace kvc
