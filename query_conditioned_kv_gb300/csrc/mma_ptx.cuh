@@ -1,0 +1,114 @@
+// mma_ptx.cuh — building blocks of the kernels that stream paged rows through
+// cp.async rings into mma.sync (tree_attn.cu, attn_mass.cu): the inline PTX,
+// the shared-memory row layout, and block-wide sums and searches over the
+// requests of a batch.
+#pragma once
+
+#include "tc_ptx.cuh"
+
+namespace kvc {
+namespace {
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(valid ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+
+// Byte offset of 16-byte chunk c of row `row` (rows of D elements): chunks
+// are permuted by the row so that ldmatrix's eight rows hit distinct banks.
+template <int D>
+__device__ __forceinline__ uint32_t swz(int row, int c) {
+  return (uint32_t)(row * D * 2 + ((c ^ (row & 7)) << 4));
+}
+
+// Sum over the CTA (a multiple of 32 threads); every thread gets it.  sh: 64
+// words of scratch, free again on return.
+__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t *sh) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0;
+  for (int w = 0; w < (int)(blockDim.x >> 5); w++) v += sh[w];
+  __syncthreads();
+  return v;
+}
+
+// Maximum over the CTA, likewise.
+__device__ __forceinline__ int64_t block_max(int64_t v, int64_t *sh) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v = max(v, (int64_t)__shfl_xor_sync(0xFFFFFFFFu, v, o));
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = sh[0];
+  for (int w = 1; w < (int)(blockDim.x >> 5); w++) v = max(v, sh[w]);
+  __syncthreads();
+  return v;
+}
+
+// The element i of [0, n) whose interval [Σ_{<i} size, Σ_{≤i} size) holds t
+// (t below the sum of all), and Σ_{<i} size; by the whole CTA, one scan per
+// blockDim.x elements.  sh: 66 words of scratch, free again on return.
+template <class F>
+__device__ __forceinline__ void block_find(int n, int64_t t, int64_t *sh, F size, int &found,
+                                           int64_t &before) {
+  int64_t carry = 0;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  for (int i0 = 0; i0 < n; i0 += blockDim.x) {
+    const int i = i0 + threadIdx.x;
+    const int64_t mine = i < n ? size(i) : 0;
+    int64_t x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) sh[warp] = x;
+    __syncthreads();
+    int64_t lo = carry + x - mine, tot = 0;
+    for (int w = 0; w < nw; w++) {
+      if (w < warp) lo += sh[w];
+      tot += sh[w];
+    }
+    if (mine > 0 && t >= lo && t < lo + mine) {
+      sh[64] = i;
+      sh[65] = lo;
+    }
+    __syncthreads();
+    if (t < carry + tot) break;
+    carry += tot;
+  }
+  found = (int)sh[64];
+  before = sh[65];
+  __syncthreads();
+}
+
+}  // namespace
+}  // namespace kvc

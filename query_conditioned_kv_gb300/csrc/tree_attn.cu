@@ -30,6 +30,7 @@
 #include <algorithm>
 
 #include "kvc_internal.cuh"
+#include "mma_ptx.cuh"
 #include "tc_ptx.cuh"
 
 namespace kvc {
@@ -87,110 +88,11 @@ __device__ __forceinline__ int run_owner(int64_t total, int n_cta, int64_t t) {
   return c;
 }
 
-// Tiles of the requests before `upto` and of all requests, by the whole CTA
-// (a multiple of 32 threads, at most 1024).
-__device__ __forceinline__ void tile_sums(const TreeArgs &a, int upto, int64_t *sh, int64_t &before,
-                                          int64_t &total) {
-  int64_t b = 0, t = 0;
-  for (int r = threadIdx.x; r < a.n_req; r += blockDim.x) {
-    int n_rt, n_kt;
-    tree_tiles(a, r, n_rt, n_kt);
-    const int64_t n = (int64_t)a.H * n_rt * n_kt;
-    t += n;
-    if (r < upto) b += n;
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
-    t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
-  }
-  const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) {
-    sh[2 * warp] = b;
-    sh[2 * warp + 1] = t;
-  }
-  __syncthreads();
-  before = total = 0;
-  for (int w = 0; w < nw; w++) {
-    before += sh[2 * w];
-    total += sh[2 * w + 1];
-  }
-  __syncthreads();
-}
-
-// The request that holds tile t (t < total) and the tiles before it; one
-// block scan per blockDim.x requests.
-__device__ __forceinline__ void find_request(const TreeArgs &a, int64_t t, int64_t *sh, int &req,
-                                             int64_t &before) {
-  int64_t carry = 0;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  for (int r0 = 0; r0 < a.n_req; r0 += blockDim.x) {
-    const int r = r0 + threadIdx.x;
-    int64_t n = 0;
-    if (r < a.n_req) {
-      int n_rt, n_kt;
-      tree_tiles(a, r, n_rt, n_kt);
-      n = (int64_t)a.H * n_rt * n_kt;
-    }
-    int64_t x = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) sh[warp] = x;
-    __syncthreads();
-    int64_t wb = carry, tot = 0;
-    for (int w = 0; w < nw; w++) {
-      if (w < warp) wb += sh[w];
-      tot += sh[w];
-    }
-    const int64_t lo = wb + x - n;
-    if (n > 0 && t >= lo && t < lo + n) {
-      sh[62] = r;
-      sh[63] = lo;
-    }
-    __syncthreads();
-    if (t < carry + tot) break;
-    carry += tot;
-  }
-  req = (int)sh[62];
-  before = sh[63];
-  __syncthreads();
-}
-
-// ------------------------------------------------------------ mma.sync
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(valid ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// Tiles of request r, all heads.
+__device__ __forceinline__ int64_t request_tiles(const TreeArgs &a, int r) {
+  int n_rt, n_kt;
+  tree_tiles(a, r, n_rt, n_kt);
+  return (int64_t)a.H * n_rt * n_kt;
 }
 
 constexpr int kRowWarps = 4;
@@ -198,19 +100,12 @@ constexpr int kRowThreads = kRowWarps * 32;
 constexpr int kRowStages = 3;
 constexpr int kWarpStage = 8192;  // bytes of one warp's stage: K rows, then V rows
 
-// Byte offset of 16-byte chunk c of row `row` (rows of D elements): chunks
-// are permuted by the row so that ldmatrix's eight rows hit distinct banks.
-template <int D>
-__device__ __forceinline__ uint32_t swz(int row, int c) {
-  return (uint32_t)(row * D * 2 + ((c ^ (row & 7)) << 4));
-}
-
 template <int D, int MT>
 struct RowSmem {
   static constexpr int kRing = kRowWarps * kRowStages * kWarpStage;
   static constexpr int kQ = kRing;                       // MT·16 rows of q
-  static constexpr int kMisc = kQ + MT * 16 * D * 2;     // scan scratch [64] int64
-  static constexpr int kValid = kMisc + 64 * 8;          // valid keys per (warp, stage)
+  static constexpr int kMisc = kQ + MT * 16 * D * 2;     // scan scratch [66] int64
+  static constexpr int kValid = kMisc + 66 * 8;          // valid keys per (warp, stage)
   static constexpr int kMl = kValid + kRowWarps * kRowStages * 4;  // (max, sum) per (warp, row)
   static constexpr int kBytes = kMl + kRowWarps * MT * 16 * 8;
   static_assert(kRowWarps * MT * 16 * D * 4 <= kRing, "the warps' O fits the ring");
@@ -262,14 +157,15 @@ k_tree_rows(TreeArgs a) {
       int c, q0, T;
       if (!tree_request(a, r, c, q0, T)) record_error(a.status, KVC_ERR_BOUNDS);
     }
-  int64_t before, total;
-  tile_sums(a, 0, sh, before, total);
+  int64_t total = 0, before;
+  for (int x = tid; x < a.n_req; x += kRowThreads) total += request_tiles(a, x);
+  total = block_sum(total, sh);
   const int n_cta = (int)min((int64_t)a.n_cta, total);  // every run holds a tile
   if ((int)blockIdx.x >= n_cta) return;
   const int64_t run0 = run_start(total, n_cta, blockIdx.x);
   const int64_t run1 = run_start(total, n_cta, blockIdx.x + 1);
   int r;
-  find_request(a, run0, sh, r, before);
+  block_find(a.n_req, run0, sh, [&](int x) { return request_tiles(a, x); }, r, before);
 
   const int64_t n_blocks = a.n_slots / a.BS;
   int64_t g = run0;  // next tile of the run
@@ -572,10 +468,16 @@ k_tree_rows(TreeArgs a) {
 template <int D>
 __global__ void __launch_bounds__(128)
 k_tree_join(TreeArgs a) {
-  __shared__ int64_t sh[64];
+  __shared__ int64_t sh[66];
   const int r = blockIdx.x / a.H, h = blockIdx.x % a.H, rt = blockIdx.y;
-  int64_t before, total;
-  tile_sums(a, r, sh, before, total);
+  int64_t before = 0, total = 0;
+  for (int x = threadIdx.x; x < a.n_req; x += blockDim.x) {
+    const int64_t n = request_tiles(a, x);
+    total += n;
+    if (x < r) before += n;
+  }
+  before = block_sum(before, sh);
+  total = block_sum(total, sh);
   int n_rt, n_kt;
   tree_tiles(a, r, n_rt, n_kt);
   // in every CTA: the grid may not end before the kernel whose partials it joins
