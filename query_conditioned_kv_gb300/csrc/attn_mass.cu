@@ -16,6 +16,7 @@
 // in equal contiguous runs to the CTAs; each of a CTA's four warps streams
 // its 16 (D 128) or 32 (D 64) keys of a tile through a private cp.async ring
 // (4 stages of 4 KB).  mma.sync m16n8k16, fp32 accumulators.
+#include <limits.h>
 #include <math.h>
 
 #include <algorithm>
@@ -55,6 +56,7 @@ __device__ __forceinline__ bool mass_request(const MassArgs &a, int r, int &seq,
 
 constexpr int kMrWarps = 4;
 constexpr int kMrThreads = kMrWarps * 32;
+constexpr int kMrMaxRows = 64;  // widest row set (rows · G) of this path
 constexpr int kMrStages = 4;
 constexpr int kMrStage = 4096;  // bytes of one warp's stage
 
@@ -316,62 +318,696 @@ cudaError_t launch_rows(const MassArgs &a, cudaStream_t s) {
 }
 
 // --------------------------------------------------------------- many rows
+//
+// tcgen05: D[key][row] = K tile (M 128 keys, A) × row tile (N rows, B), fp32 in
+// tensor memory; epilogue thread = one key (TMEM lane), its columns the rows.
+// Warps 0–7: two epilogue warpgroups, taking the key tiles in turn; 8–11:
+// producers (cp.async with the 128-byte swizzle, so any page size and any
+// row_idx); 12: MMA issue.
+//
+// ONE (all rows of a request in one row tile): the rows stay in shared memory
+// while the request's keys stream past; work is dealt out by key tile.
+// Otherwise a work item is a group of two key tiles (256 keys, resident) that
+// the row tiles stream past (a row tile's 64 KB from L2 feed two products).
+// k_mass_plan lists each group's row tiles, those with a row that sees the
+// group's first key: under a causal limit the work halves.  All items' row
+// tiles, in order, are dealt out in equal contiguous runs to the CTAs; a run
+// that holds part of a group writes partial sums, which k_mass_join adds in
+// order.
 
-// One warp per position; lanes split D.
-template <int D>
-__global__ void __launch_bounds__(256)
-k_attn_mass(MassArgs a) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int p = blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int seg = blockIdx.y + gridDim.y * blockIdx.z;
-  if (seg >= a.L * a.n_req * a.H) return;
-  const int h = seg % a.H, r = (seg / a.H) % a.n_req;
-  const int64_t l = seg / (a.H * a.n_req);
-  const int seq = a.seqused[r], r0 = a.row_off[r], r1 = a.row_off[r + 1];
-  if (seq < 0 || seq > a.cap || r0 < 0 || r1 < r0 || r1 > a.n_rows || r1 - r0 > a.max_rows) {
-    if (lane == 0) record_error(a.status, KVC_ERR_BOUNDS);
-    return;
+constexpr int kTcEpi = 8;                       // epilogue warps
+constexpr int kTcProd = 4;                      // producer warps
+constexpr int kTcThreads = (kTcEpi + kTcProd + 1) * 32;
+constexpr int kTcKeys = 128;                    // keys of a tile
+
+struct MassTc {
+  int n_cta;        // CTAs the work is dealt out to
+  int NR;           // rows per row tile: 128 or 256
+  int k_slots;      // K ring
+  int max_kg, max_rt;
+  uint32_t idesc;
+  int64_t *cum;     // [n_req][max_kg + 1]: row tiles before each group (at least one each)
+  int2 *span;       // [n_req][max_kg]: first row tile and their number (0: nobody sees the group)
+  int *rt_vis;      // [n_req][max_rt]: positions the widest row of the tile sees
+  float *part;      // [2·n_cta][256]: partial sums
+};
+
+template <bool ONE>
+struct TcShape {
+  static constexpr int kKG = ONE ? 1 : 2;   // key tiles of a group
+  static constexpr int kLs = ONE ? 2 : 4;   // LSE slots
+};
+
+struct TcSmem {
+  uint8_t *k, *q;
+  float *nlse;  // [kLs][NR]: −lse·log2e
+  int *vis;     // [kLs][NR]
+  int *lo;      // [kLs][4]: least limit, per producer warp
+  uint64_t *kfull, *kempty, *qfull, *qempty, *lfull, *lempty, *tfull, *tempty;
+  int64_t *scan;
+  uint32_t *tmem_holder;
+  volatile int *failed;
+  __host__ __device__ static size_t layout(int D, int NR, int ks, int qs, int ls, TcSmem *o,
+                                           uint8_t *base) {
+    size_t at = 0;
+    auto take = [&](size_t n) {
+      const size_t x = at;
+      at += (n + 15) & ~size_t(15);
+      return base + x;
+    };
+    uint8_t *k = take((size_t)ks * kTcKeys * D * 2), *q = take((size_t)qs * NR * D * 2);
+    uint8_t *nl = take((size_t)ls * NR * 4), *vi = take((size_t)ls * NR * 4), *lo = take(ls * 16);
+    uint8_t *bars = take((2 * ks + 2 * qs + 2 * ls + 8) * 8), *sc = take(66 * 8), *th = take(16);
+    if (o) {
+      o->k = k;
+      o->q = q;
+      o->nlse = reinterpret_cast<float *>(nl);
+      o->vis = reinterpret_cast<int *>(vi);
+      o->lo = reinterpret_cast<int *>(lo);
+      o->kfull = reinterpret_cast<uint64_t *>(bars);
+      o->kempty = o->kfull + ks;
+      o->qfull = o->kempty + ks;
+      o->qempty = o->qfull + qs;
+      o->lfull = o->qempty + qs;
+      o->lempty = o->lfull + ls;
+      o->tfull = o->lempty + ls;
+      o->tempty = o->tfull + 4;
+      o->scan = reinterpret_cast<int64_t *>(sc);
+      o->tmem_holder = reinterpret_cast<uint32_t *>(th);
+      o->failed = reinterpret_cast<volatile int *>(th + 4);
+    }
+    return at;
   }
-  if (p >= seq) return;
-  const int32_t b = a.block_table[(int64_t)r * a.max_blocks + p / a.BS];
-  float sum = 0.f;
-  if (b < 0 || b >= a.n_slots / a.BS) {
-    if (lane == 0) record_error(a.status, KVC_ERR_BOUNDS);
-  } else {
-    const int64_t at =
-        ((l * a.n_slots + (int64_t)b * a.BS + p % a.BS) * a.H + h) * D + lane * E;
-    float k[E];
-#pragma unroll
-    for (int e = 0; e < E; e++) k[e] = bf16_lo(a.kpool[at + e]);
-    for (int i = r0; i < r1; i++) {
-      if (p >= a.row_vis[i]) continue;
-      const int x = a.row_idx ? a.row_idx[i] : i;
-      if (x < 0 || x >= a.n_q) {
-        if (lane == 0) record_error(a.status, KVC_ERR_BOUNDS);
-        continue;
-      }
-      for (int g = 0; g < a.G; g++) {
-        const int64_t row = (l * a.n_q + x) * a.Hq + h * a.G + g;
-        float z = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; e++) z = fmaf(bf16_lo(a.q[row * D + lane * E + e]), k[e], z);
-#pragma unroll
-        for (int s = 16; s; s >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, s);
-        const float lse = a.lse[row];
-        if (lse != -INFINITY) sum += exp2f(fmaf(z, a.zscale, -lse * kLog2e));
-      }
+};
+
+// Groups of request r.
+__device__ __forceinline__ int tc_groups(const MassArgs &a, int r, int keys) {
+  return mass_tiles(a, r, keys);
+}
+
+// Where a run stands: group kg of (l, r, h), row tiles [off, cnt) of it left.
+template <bool ONE>
+struct TcPos {
+  int64_t l;
+  int r, h, kg, n_kg;
+  int rt0, cnt;  // the group's first row tile and their number (0: none)
+  int off;       // done by earlier CTAs
+  __device__ __forceinline__ void load(const MassArgs &a, const MassTc &p) {
+    if (ONE) {
+      rt0 = 0;
+      cnt = 1;
+    } else {
+      const int2 s = p.span[(int64_t)r * p.max_kg + kg];
+      rt0 = s.x;
+      cnt = s.y;
     }
   }
-  if (lane == 0) {
-    float *m = a.mass + (int64_t)seg * a.cap + p;
-    *m = (p < a.n_mass[r] ? a.decay * *m : 0.f) + sum;
+  // the next group (one exists while the run is not over)
+  __device__ __forceinline__ void next(const MassArgs &a, const MassTc &p) {
+    off = 0;
+    if (++kg == n_kg) {
+      kg = 0;
+      if (++h == a.H) {
+        h = 0;
+        do {
+          if (++r == a.n_req) {
+            r = 0;
+            l++;
+          }
+          n_kg = tc_groups(a, r, TcShape<ONE>::kKG * kTcKeys);
+        } while (n_kg == 0);
+      }
+    }
+    load(a, p);
   }
+};
+
+template <bool ONE>
+__device__ __forceinline__ int64_t tc_request_work(const MassArgs &a, const MassTc &p, int r) {
+  const int n = tc_groups(a, r, TcShape<ONE>::kKG * kTcKeys);
+  return n == 0 ? 0 : ONE ? n : p.cum[(int64_t)r * (p.max_kg + 1) + n];
+}
+
+// Position of work item t (by the whole CTA).
+template <bool ONE>
+__device__ __forceinline__ TcPos<ONE> tc_find(const MassArgs &a, const MassTc &p, int64_t t,
+                                              int64_t per, int64_t *sh) {
+  TcPos<ONE> x;
+  x.l = t / (per * a.H);
+  int64_t before;
+  const int64_t in_layer = t % (per * a.H);
+  block_find(
+      a.n_req, in_layer, sh, [&](int r) { return a.H * tc_request_work<ONE>(a, p, r); }, x.r, before);
+  const int64_t w = tc_request_work<ONE>(a, p, x.r);
+  x.h = (int)((in_layer - before) / w);
+  const int64_t in_head = (in_layer - before) % w;
+  x.n_kg = tc_groups(a, x.r, TcShape<ONE>::kKG * kTcKeys);
+  if (ONE) {
+    x.kg = (int)in_head;
+    x.off = 0;
+  } else {
+    const int64_t *cum = p.cum + (int64_t)x.r * (p.max_kg + 1);
+    int lo = 0, hi = x.n_kg - 1;  // the last group with cum ≤ in_head
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (cum[mid] <= in_head) lo = mid;
+      else hi = mid - 1;
+    }
+    x.kg = lo;
+    x.off = (int)(in_head - cum[lo]);
+  }
+  x.load(a, p);
+  return x;
+}
+
+template <int D, bool ONE>
+__global__ void __launch_bounds__(kTcThreads, 1)
+k_mass_tc(MassArgs a, MassTc p) {
+  constexpr int KG = TcShape<ONE>::kKG, LS = TcShape<ONE>::kLs, QS = 2;
+  constexpr int CH = D / 8, KB = D / 64;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *base = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int NR = p.NR, KS = p.k_slots, NACC = 512 / NR;
+  TcSmem sm;
+  TcSmem::layout(D, NR, KS, QS, LS, &sm, base);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    *sm.failed = 0;
+    for (int i = 0; i < KS; i++) {
+      mbar_init(smem_u32(sm.kfull + i), kTcProd * 32);
+      mbar_init(smem_u32(sm.kempty + i), 1);
+    }
+    for (int i = 0; i < QS; i++) {
+      mbar_init(smem_u32(sm.qfull + i), kTcProd * 32);
+      mbar_init(smem_u32(sm.qempty + i), 1);
+    }
+    for (int i = 0; i < LS; i++) {
+      mbar_init(smem_u32(sm.lfull + i), kTcProd * 32);
+      mbar_init(smem_u32(sm.lempty + i), kTcEpi);
+    }
+    for (int i = 0; i < NACC; i++) {
+      mbar_init(smem_u32(sm.tfull + i), 1);
+      mbar_init(smem_u32(sm.tempty + i), kTcEpi / 2);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kTcEpi + kTcProd) alloc_tmem_cols(sm.tmem_holder, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *sm.tmem_holder;
+
+  if (!ONE) asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan
+  int64_t per = 0;
+  for (int r = tid; r < a.n_req; r += kTcThreads) {
+    per += tc_request_work<ONE>(a, p, r);
+    int seq, r0, n;
+    if (ONE && blockIdx.x == 0 && !mass_request(a, r, seq, r0, n))
+      record_error(a.status, KVC_ERR_BOUNDS);
+  }
+  per = block_sum(per, sm.scan);
+  const int64_t total = per * a.L * a.H;
+  const int n_cta = (int)min((int64_t)p.n_cta, total);
+  const bool works = (int)blockIdx.x < n_cta;
+  const int64_t run0 = works ? total * blockIdx.x / n_cta : 0;
+  const int64_t run1 = works ? total * (blockIdx.x + 1) / n_cta : 0;
+  TcPos<ONE> pos{};
+  if (works) pos = tc_find<ONE>(a, p, run0, per, sm.scan);
+  if (!ONE) asm volatile("griddepcontrol.launch_dependents;");
+
+  bool ok = true;
+  if (warp >= kTcEpi && warp < kTcEpi + kTcProd) {
+    // ------------------------------------------------------- producers
+    const int pw = warp - kTcEpi;
+    const int64_t n_blocks = a.n_slots / a.BS;
+    uint32_t kc = 0, qc = 0;      // K tiles and row tiles loaded
+    uint32_t pend = 0;            // full barrier of the last stage not yet signalled
+    int64_t q_unit = -1;
+    auto signal = [&]() {         // the stage's copies have landed: hand them to the tensor core
+      if (!pend) return;
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      mbar_arrive(pend);
+      pend = 0;
+    };
+    // wait for a free slot; a stage whose copies may have landed is signalled
+    // first, so that its consumer never waits for a slot to become free
+    auto acquire = [&](uint64_t *bar, uint32_t parity) {
+      if (mbar_try(smem_u32(bar), parity)) return true;
+      if (pend) {
+        cp_wait<0>();
+        signal();
+      }
+      return mbar_wait_bounded(smem_u32(bar), parity, sm.failed);
+    };
+    auto committed = [&](uint64_t *bar) {  // stage issued: signal the one before it
+      cp_commit();
+      if (pend) {
+        cp_wait<1>();
+        signal();
+      }
+      pend = smem_u32(bar);
+    };
+    for (int64_t g = run0; g < run1 && ok;) {
+      const int todo = (int)min((int64_t)max(pos.cnt, 1) - pos.off, run1 - g);
+      if (pos.cnt > 0) {
+        int seq, r0, n;
+        mass_request(a, pos.r, seq, r0, n);
+        const int32_t *bt = a.block_table + (int64_t)pos.r * a.max_blocks;
+        const uint16_t *kl = a.kpool + (pos.l * a.n_slots * a.H + pos.h) * D;
+        const int64_t unit = (pos.l * a.n_req + pos.r) * a.H + pos.h;
+        auto load_k = [&](int kt) {
+          const int st = kc % KS;
+          if (!(ok = acquire(sm.kempty + st, ((kc / KS) & 1) ^ 1))) return;
+          const int pp = (pos.kg * KG + kt) * kTcKeys + pw * 32 + lane;
+          int32_t slot = -1;
+          if (pp < seq) {
+            const int32_t b = bt[pp / a.BS];
+            if (b >= 0 && b < n_blocks) slot = b * a.BS + pp % a.BS;
+            else record_error(a.status, KVC_ERR_BOUNDS);
+          }
+          constexpr int RPI = 32 / CH;
+          const int col = lane % CH;
+          const uint32_t dst = smem_u32(sm.k) + st * (kTcKeys * D * 2) + (col >> 3) * (kTcKeys * 128);
+#pragma unroll
+          for (int i = 0; i < 32 / RPI; i++) {
+            const int row = i * RPI + lane / CH;
+            const int32_t sl = __shfl_sync(0xFFFFFFFFu, slot, row);
+            cp_async16(dst + (pw * 32 + row) * 128 + (((col & 7) ^ (row & 7)) << 4),
+                       kl + (int64_t)max(sl, 0) * a.H * D + col * 8, sl >= 0);
+          }
+          committed(sm.kfull + st);
+          kc++;
+        };
+        auto load_q = [&](int rt) {
+          const int st = qc % QS, ls = qc % LS;
+          if (!(ok = acquire(sm.qempty + st, ((qc / QS) & 1) ^ 1))) return;
+          if (!(ok = acquire(sm.lempty + ls, ((qc / LS) & 1) ^ 1))) return;
+          int lo = INT_MAX;
+          for (int b = pw * 32; b < NR; b += kTcProd * 32) {
+            const int row = rt * NR + b + lane;
+            int64_t at = -1;
+            float nl = -INFINITY;
+            int vis = 0;
+            if (row < n * a.G) {
+              const int i = r0 + row / a.G, x = a.row_idx ? a.row_idx[i] : i;
+              vis = min(a.row_vis[i], seq);
+              if (vis > 0) {
+                if (x >= 0 && x < a.n_q) {
+                  at = (pos.l * a.n_q + x) * a.Hq + pos.h * a.G + row % a.G;
+                  const float l2 = a.lse[at] * kLog2e;
+                  if (fabsf(l2) != INFINITY) {
+                    nl = -l2;
+                    lo = min(lo, vis);
+                  }
+                } else {
+                  record_error(a.status, KVC_ERR_BOUNDS);
+                }
+              }
+            }
+            sm.nlse[ls * NR + b + lane] = nl;
+            sm.vis[ls * NR + b + lane] = nl == -INFINITY ? 0 : vis;
+            constexpr int RPI = 32 / CH;
+            const int col = lane % CH;
+            const uint32_t dst = smem_u32(sm.q) + st * (NR * D * 2) + (col >> 3) * (NR * 128);
+#pragma unroll
+            for (int i = 0; i < 32 / RPI; i++) {
+              const int rr = i * RPI + lane / CH;
+              const int64_t src = __shfl_sync(0xFFFFFFFFu, at, rr);
+              cp_async16(dst + (b + rr) * 128 + (((col & 7) ^ (rr & 7)) << 4),
+                         a.q + max(src, (int64_t)0) * D + col * 8, src >= 0);
+            }
+          }
+          lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+          if (lane == 0) sm.lo[ls * 4 + pw] = lo;
+          __syncwarp();
+          mbar_arrive(smem_u32(sm.lfull + ls));
+          committed(sm.qfull + st);
+          qc++;
+        };
+        load_k(0);
+        if (ONE) {
+          if (ok && unit != q_unit) load_q(0);
+        } else {
+          for (int i = 0; i < todo && ok; i++) {
+            load_q(pos.rt0 + pos.off + i);
+            if (i == 0 && ok) load_k(1);
+          }
+        }
+        q_unit = unit;
+      }
+      g += todo;
+      if (g < run1) pos.next(a, p);
+    }
+    cp_wait<0>();
+    signal();
+    if (!ok) *sm.failed = 1;
+  } else if (warp == kTcEpi + kTcProd) {
+    // ------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      uint32_t kc = 0, qc = 0, jc = 0;  // first K tile of the group, row tiles, products
+      int64_t q_unit = -1;
+      for (int64_t g = run0; g < run1 && ok;) {
+        const int todo = (int)min((int64_t)max(pos.cnt, 1) - pos.off, run1 - g);
+        if (pos.cnt > 0) {
+          const int64_t unit = (pos.l * a.n_req + pos.r) * a.H + pos.h;
+          for (int i = 0; i < todo && ok; i++) {
+            if (!ONE || unit != q_unit) {
+              if (ONE && qc > 0) mma_commit(smem_u32(sm.qempty + (qc - 1) % QS));
+              qc++;
+            }
+            const int qst = (qc - 1) % QS;
+            for (int kt = 0; kt < KG && ok; kt++) {
+              const uint32_t kx = kc + kt;
+              const int kst = kx % KS, acc = jc % NACC;
+              if (kt == 0 &&
+                  !(ok = mbar_wait_bounded(smem_u32(sm.qfull + qst), ((qc - 1) / QS) & 1, sm.failed)))
+                break;
+              if (!(ok = mbar_wait_bounded(smem_u32(sm.kfull + kst), (kx / KS) & 1, sm.failed))) break;
+              if (!(ok = mbar_wait_bounded(smem_u32(sm.tempty + acc), ((jc / NACC) & 1) ^ 1,
+                                           sm.failed)))
+                break;
+              tc_fence_after();
+              const uint32_t kb = smem_u32(sm.k) + kst * (kTcKeys * D * 2);
+              const uint32_t qb = smem_u32(sm.q) + qst * (NR * D * 2);
+#pragma unroll
+              for (int kk = 0; kk < 4 * KB; kk++)
+                mma_bf16(tmem + acc * NR,
+                         smem_desc(kb + (kk >> 2) * (kTcKeys * 128) + (kk & 3) * 32),
+                         smem_desc(qb + (kk >> 2) * (NR * 128) + (kk & 3) * 32), p.idesc, kk > 0);
+              mma_commit(smem_u32(sm.tfull + acc));
+              if (i == todo - 1) mma_commit(smem_u32(sm.kempty + kst));
+              jc++;
+            }
+            if (!ONE && ok) mma_commit(smem_u32(sm.qempty + qst));
+          }
+          kc += KG;
+          q_unit = unit;
+        }
+        g += todo;
+        if (g < run1) pos.next(a, p);
+      }
+      if (!ok) *sm.failed = 1;
+    }
+    __syncwarp();
+  } else if (warp < kTcEpi) {
+    // -------------------------------------------------------- epilogue
+    const int wg = warp >> 2, quarter = warp & 3;
+    const uint32_t lane_base = (uint32_t)(32 * quarter) << 16;
+    const uint64_t zs2 = pk2(a.zscale, a.zscale);
+    uint32_t qc = 0, jc = 0;
+    int64_t q_unit = -1;
+    int lo = 0;
+    for (int64_t g = run0; g < run1 && ok;) {
+      const int todo = (int)min((int64_t)max(pos.cnt, 1) - pos.off, run1 - g);
+      const int64_t unit = (pos.l * a.n_req + pos.r) * a.H + pos.h;
+      const int seq = a.seqused[pos.r];
+      const int kt = ONE ? 0 : wg;
+      const int p0 = (pos.kg * KG + kt) * kTcKeys, key = p0 + quarter * 32 + lane;
+      const bool mine = ONE ? (jc & 1) == (uint32_t)wg : true;
+      const bool whole = pos.off == 0 && todo == max(pos.cnt, 1);
+      float *out = a.mass + unit * a.cap + key;
+      float old = 0.f, total_w = 0.f;
+      bool valid = false;
+      if (mine && key < seq) {
+        if (whole && key < a.n_mass[pos.r]) old = *out;
+        const int32_t b = a.block_table[(int64_t)pos.r * a.max_blocks + key / a.BS];
+        valid = b >= 0 && b < a.n_slots / a.BS;
+      }
+      if (pos.cnt > 0)
+        for (int i = 0; i < todo && ok; i++) {
+          if (!ONE || unit != q_unit) {  // another row tile
+            if (ONE && qc > 0) {
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_u32(sm.lempty + (qc - 1) % LS));
+            }
+            qc++;
+            const int ls = (qc - 1) % LS;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.lfull + ls),
+                                                           ((qc - 1) / LS) & 1, sm.failed));
+            if (!ok) break;
+            lo = min(min(sm.lo[ls * 4], sm.lo[ls * 4 + 1]), min(sm.lo[ls * 4 + 2], sm.lo[ls * 4 + 3]));
+            if (lo == INT_MAX) lo = 0;
+          }
+          const int ls = (qc - 1) % LS;
+          const uint32_t job = ONE ? jc : jc + wg;
+          jc += KG;
+          if (mine) {
+            const int acc = job % NACC;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.tfull + acc),
+                                                           (job / NACC) & 1, sm.failed));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t taddr = tmem + lane_base + acc * NR;
+            const float *nl = sm.nlse + ls * NR;
+            const int *vi = sm.vis + ls * NR;
+            const bool masked = p0 + kTcKeys > lo;
+            uint64_t s0 = 0, s1 = 0;
+            uint32_t buf[2][32];
+            tmem_issue32(taddr, buf[0]);
+            for (int c = 0; c < NR; c += 64) {
+#pragma unroll
+              for (int hb = 0; hb < 2; hb++) {
+                tmem_wait32(buf[hb]);
+                const int cc = c + hb * 32;
+                if (cc + 32 < NR) tmem_issue32(taddr + cc + 32, buf[hb ^ 1]);
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                  const ulonglong2 n4 = *reinterpret_cast<const ulonglong2 *>(nl + cc + j);
+                  uint64_t x0 = fma2(pk2(__uint_as_float(buf[hb][j]), __uint_as_float(buf[hb][j + 1])),
+                                     zs2, n4.x);
+                  uint64_t x1 = fma2(pk2(__uint_as_float(buf[hb][j + 2]), __uint_as_float(buf[hb][j + 3])),
+                                     zs2, n4.y);
+                  float w0, w1, w2, w3;
+                  upk2(x0, w0, w1);
+                  upk2(x1, w2, w3);
+                  w0 = ex2(w0);
+                  w1 = ex2(w1);
+                  w2 = ex2(w2);
+                  w3 = ex2(w3);
+                  if (masked) {
+                    const int4 v4 = *reinterpret_cast<const int4 *>(vi + cc + j);
+                    w0 = key < v4.x ? w0 : 0.f;
+                    w1 = key < v4.y ? w1 : 0.f;
+                    w2 = key < v4.z ? w2 : 0.f;
+                    w3 = key < v4.w ? w3 : 0.f;
+                  }
+                  s0 = add2(s0, pk2(w0, w1));
+                  s1 = add2(s1, pk2(w2, w3));
+                }
+              }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(sm.tempty + acc));
+            float u0, u1, u2, u3;
+            upk2(s0, u0, u1);
+            upk2(s1, u2, u3);
+            total_w += (u0 + u2) + (u1 + u3);
+          }
+          if (!ONE) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(sm.lempty + ls));
+          }
+        }
+      q_unit = unit;
+      if (ok && mine) {
+        if (whole) {
+          if (key < seq) *out = fmaf(a.decay, old, valid ? total_w : 0.f);
+        } else {
+          p.part[(2 * (int64_t)blockIdx.x + (g != run0)) * (KG * kTcKeys) + kt * kTcKeys +
+                 quarter * 32 + lane] = valid ? total_w : 0.f;
+        }
+      }
+      g += todo;
+      if (g < run1) pos.next(a, p);
+    }
+    if (!ok) {
+      *sm.failed = 1;
+      if (lane == 0) record_error(a.status, KVC_ERR_TIMEOUT);
+    }
+  }
+
+  // -------------------------------------------------------- teardown
+  tc_fence_before();
+  __syncthreads();
+  if (*sm.failed && tid == 0) {
+    record_error(a.status, KVC_ERR_TIMEOUT);
+    // let this CTA's products finish before its memory is released
+    for (int i = 0; i < NACC; i++) {
+      mbar_drain(smem_u32(sm.tfull + i), 0);
+      mbar_drain(smem_u32(sm.tfull + i), 1);
+    }
+  }
+  __syncthreads();
+  if (warp == kTcEpi + kTcProd) {
+    tc_fence_after();
+    free_tmem_cols(tmem, 512);
+  }
+}
+
+// Row tiles of every key group of every request, one CTA per request.
+__global__ void __launch_bounds__(256)
+k_mass_plan(MassArgs a, MassTc p) {
+  __shared__ int64_t sh[66];
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int r = blockIdx.x, tid = threadIdx.x;
+  int seq, r0, n;
+  if (!mass_request(a, r, seq, r0, n)) {
+    if (tid == 0) record_error(a.status, KVC_ERR_BOUNDS);
+    return;
+  }
+  const int n_rt = (int)(((int64_t)n * a.G + p.NR - 1) / p.NR);
+  int *vis = p.rt_vis + (int64_t)r * p.max_rt;
+  const int warp = tid >> 5, lane = tid & 31;
+  for (int t = warp; t < n_rt; t += 8) {  // positions the widest row of each row tile sees
+    const int i0 = (int)((int64_t)t * p.NR / a.G);
+    const int i1 = min(n - 1, (int)((((int64_t)t + 1) * p.NR - 1) / a.G));
+    int v = 0;
+    for (int i = i0 + lane; i <= i1; i += 32) v = max(v, a.row_vis[r0 + i]);
+    v = __reduce_max_sync(0xFFFFFFFFu, v);
+    if (lane == 0) vis[t] = min(v, seq);
+  }
+  __syncthreads();
+  const int keys = 2 * kTcKeys, n_kg = (seq + keys - 1) / keys;
+  int64_t *cum = p.cum + (int64_t)r * (p.max_kg + 1);
+  int64_t carry = 0;
+  for (int k0 = 0; k0 < n_kg; k0 += 256) {
+    const int kg = k0 + tid;
+    int64_t mine = 0;
+    if (kg < n_kg) {
+      int first = 0, last = n_rt - 1;
+      while (first < n_rt && vis[first] <= kg * keys) first++;
+      while (last >= first && vis[last] <= kg * keys) last--;
+      const int cnt = last - first + 1;
+      p.span[(int64_t)r * p.max_kg + kg] = make_int2(first, cnt);
+      mine = max(cnt, 1);
+    }
+    int64_t x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) sh[warp] = x;
+    __syncthreads();
+    int64_t before = carry, tot = 0;
+    for (int w = 0; w < 8; w++) {
+      if (w < warp) before += sh[w];
+      tot += sh[w];
+    }
+    if (kg < n_kg) cum[kg] = before + x - mine;
+    carry += tot;
+    __syncthreads();
+  }
+  if (tid == 0) cum[n_kg] = carry;
+}
+
+// CTA c: the group that the boundary before run c falls inside, if it is the
+// first boundary inside that group.
+__global__ void __launch_bounds__(256)
+k_mass_join(MassArgs a, MassTc p) {
+  __shared__ int64_t sh[66];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int tid = threadIdx.x, c = blockIdx.x + 1;
+  int64_t per = 0;
+  for (int r = tid; r < a.n_req; r += 256) per += tc_request_work<false>(a, p, r);
+  per = block_sum(per, sh);
+  const int64_t total = per * a.L * a.H;
+  const int n_cta = (int)min((int64_t)p.n_cta, total);
+  if (c >= n_cta) return;
+  const int64_t t = total * c / n_cta, prev = total * (c - 1) / n_cta;
+  const TcPos<false> x = tc_find<false>(a, p, t, per, sh);
+  if (x.off == 0) return;                 // the run begins with a group
+  const int64_t g0 = t - x.off, g1 = g0 + max(x.cnt, 1);
+  if (prev > g0) return;                  // an earlier boundary joins this group
+  const int key = x.kg * 256 + tid, seq = a.seqused[x.r];
+  if (key >= seq) return;
+  // run c − 1 holds the group's beginning: its first part if it began there
+  float sum = p.part[(2 * (int64_t)(c - 1) + (prev != g0)) * 256 + tid];
+  for (int k = c; k < n_cta && total * k / n_cta < g1; k++) sum += p.part[2 * (int64_t)k * 256 + tid];
+  float *out = a.mass + ((x.l * a.n_req + x.r) * a.H + x.h) * a.cap + key;
+  *out = fmaf(a.decay, key < a.n_mass[x.r] ? *out : 0.f, sum);
+}
+
+// The shape of the tensor-core path for these sizes.
+MassTc tc_plan(int n_req, int cap, int max_rows, int G, int D, bool &one, size_t &smem, size_t &ws,
+               uint8_t *base) {
+  MassTc p{};
+  const int64_t R = (int64_t)max_rows * G;
+  one = R <= 256;
+  p.NR = R <= 128 ? 128 : 256;
+  // what the row tiles leave: K tiles in flight when keys stream, else two
+  const size_t tile = (size_t)kTcKeys * D * 2, q = 2 * (size_t)p.NR * D * 2;
+  p.k_slots = one ? (int)std::min<size_t>(8, (200 * 1024 - q) / tile) : 2;
+  p.n_cta = device_sm_count();
+  p.max_kg = (cap + 255) / 256;
+  p.max_rt = (int)((R + p.NR - 1) / p.NR);
+  p.idesc = make_idesc(128, p.NR);
+  smem = 1024 + TcSmem::layout(D, p.NR, p.k_slots, 2, one ? 2 : 4, nullptr, nullptr);
+  ws = 0;
+  if (one) return p;
+  auto take = [&](size_t n) {
+    const size_t x = ws;
+    ws += (n + 15) & ~size_t(15);
+    return base + x;
+  };
+  p.cum = reinterpret_cast<int64_t *>(take((size_t)n_req * (p.max_kg + 1) * 8));
+  p.span = reinterpret_cast<int2 *>(take((size_t)n_req * p.max_kg * 8));
+  p.rt_vis = reinterpret_cast<int *>(take((size_t)n_req * p.max_rt * 4));
+  p.part = reinterpret_cast<float *>(take((size_t)2 * p.n_cta * 256 * 4));
+  return p;
+}
+
+template <class K, class... Args>
+cudaError_t launch_dependent(K kern, dim3 grid, int threads, size_t smem, cudaStream_t s,
+                             Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <int D>
+cudaError_t launch_tc(const MassArgs &a, void *ws, cudaStream_t s) {
+  bool one;
+  size_t smem, ws_bytes;
+  const MassTc p = tc_plan(a.n_req, a.cap, a.max_rows, a.G, D, one, smem, ws_bytes,
+                           reinterpret_cast<uint8_t *>(ws));
+  auto *kern = one ? k_mass_tc<D, true> : k_mass_tc<D, false>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  if (one) {
+    kern<<<p.n_cta, kTcThreads, smem, s>>>(a, p);
+    return cudaGetLastError();
+  }
+  k_mass_plan<<<a.n_req, 256, 0, s>>>(a, p);
+  e = cudaGetLastError();
+  if (e == cudaSuccess) e = launch_dependent(kern, dim3(p.n_cta), kTcThreads, smem, s, a, p);
+  if (e == cudaSuccess && p.n_cta > 1)
+    e = launch_dependent(k_mass_join, dim3(p.n_cta - 1), 256, 0, s, a, p);
+  return e;
 }
 
 }  // namespace
 
-size_t attn_mass_ws_bytes(int, int, int, int, int, int, int, int) { return 0; }
+size_t attn_mass_ws_bytes(int n_req, int max_blocks, int max_rows, int, int H, int Hq, int D,
+                          int BS) {
+  if ((int64_t)max_rows * (Hq / H) <= kMrMaxRows) return 0;
+  bool one;
+  size_t smem, ws;
+  tc_plan(n_req, max_blocks * BS, max_rows, Hq / H, D, one, smem, ws, nullptr);
+  return ws;
+}
 
 cudaError_t launch_attn_mass(const uint16_t *q, const float *lse, int n_q,
                              const int32_t *row_idx, const int32_t *row_vis,
@@ -380,13 +1016,13 @@ cudaError_t launch_attn_mass(const uint16_t *q, const float *lse, int n_q,
                              const int32_t *block_table, int max_blocks,
                              const int32_t *seqused, const int32_t *n_mass, int n_req, int L,
                              int H, int Hq, int D, int BS, float scale, float decay, float *mass,
-                             void *, int32_t *status, cudaStream_t s) {
+                             void *ws, int32_t *status, cudaStream_t s) {
   MassArgs a{q,      kpool,   lse,    row_idx,  row_vis,    row_off,         block_table, seqused,
              n_mass, mass,    status, n_slots,  n_q,        n_rows,          max_rows,    max_blocks,
              max_blocks * BS, n_req,  L,        H,          Hq,              Hq / H,      BS,
              scale * kLog2e,  decay};
   const int64_t R = (int64_t)max_rows * a.G;
-  if (R <= 64) {
+  if (R <= kMrMaxRows) {
     if (D == 128)
       return R <= 8    ? launch_rows<128, 1>(a, s)
              : R <= 16 ? launch_rows<128, 2>(a, s)
@@ -397,11 +1033,7 @@ cudaError_t launch_attn_mass(const uint16_t *q, const float *lse, int n_q,
            : R <= 32 ? launch_rows<64, 4>(a, s)
                      : launch_rows<64, 8>(a, s);
   }
-  const int segs = L * n_req * H, y = segs < 32768 ? segs : 32768;
-  const dim3 grid((a.cap + 7) / 8, y, (segs + y - 1) / y);
-  if (D == 128) k_attn_mass<128><<<grid, 256, 0, s>>>(a);
-  else k_attn_mass<64><<<grid, 256, 0, s>>>(a);
-  return cudaGetLastError();
+  return D == 128 ? launch_tc<128>(a, ws, s) : launch_tc<64>(a, ws, s);
 }
 
 }  // namespace kvc
