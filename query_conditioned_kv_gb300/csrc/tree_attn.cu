@@ -462,6 +462,677 @@ k_tree_rows(TreeArgs a) {
   }
 }
 
+// ---------------------------------------------------------------- tcgen05
+//
+// k_tree_tc (more than 32 rows).  Per tile of 128 keys, both products with
+// the rows as the N dimension:
+//   Sᵀ[key][row] = K·Qᵀ          (M 128 keys,  N rows, K D)
+//   Oᵀ[d][row] += Vᵀ·Pᵀ          (M D (64 twice), N rows, K 128 keys)
+// so the tensor work grows with the rows instead of being padded to 128, and
+// at 256 rows each instruction is the widest (N 256).  V and P are taken
+// MN-major: V as it lies in the pool, P as the softmax threads hold it (one
+// key per thread), written with 16-byte stores.
+//
+// A softmax thread owns one key (TMEM lane) and CW rows (columns), so a row's
+// maximum is spread over 128 threads.  The exponent's reference is therefore
+// not the running maximum but a fixed value per row, the maximum of the first
+// tile, raised only when some logit exceeds it by 2^30: weights, their sums
+// and O stay far inside fp32 and bf16 range (bf16 has fp32's exponents), and
+// the result does not depend on the reference.  A per-tile vote of the
+// warpgroup (one barrier) finds the tiles that must raise it; they take the
+// exchange and rescale O in tensor memory.  The sums of the weights stay in
+// registers per (key lane, row) and are reduced once per run.
+//
+// Warps: NW softmax warpgroups, two producer warps (cp.async, any page
+// size), one MMA warp.  K and V tiles share one ring, in the order the MMA
+// warp consumes them: K0 K1 V0 K2 V1 …
+
+constexpr int kTtKeys = 128;
+constexpr int kTtProd = 2;
+constexpr int kTtThreads = 640;     // at most 4 softmax warpgroups, then the other warps
+constexpr float kUnset = -1e30f;   // reference of a row that has seen nothing
+constexpr float kExceed = 30.f;    // log2 of how far a logit may pass the reference
+
+struct TreeTc {
+  int NW;      // softmax warpgroups
+  int NS;      // ring slots
+  int PB, SB;  // P buffers, S buffers
+  uint32_t idesc_s, idesc_o;  // without N
+};
+
+struct TreeTcSmem {
+  uint8_t *q, *p, *ring;
+  float *nb;   // −reference per row
+  float *scr;  // [4 + 2][32] per warpgroup of 32 rows; warpgroups of 64 rows use their block of P
+  uint64_t *full, *empty, *qfull, *qempty, *sfull, *sfree, *pready, *pvdone, *ofree;
+  int64_t *scan;
+  uint32_t *tmem_holder;
+  volatile int *failed, *odd;
+  __host__ __device__ static size_t layout(int D, int rows, int NS, int PB, TreeTcSmem *o,
+                                           uint8_t *base) {
+    size_t at = 0;
+    auto take = [&](size_t n) {
+      const size_t x = at;
+      at += (n + 15) & ~size_t(15);
+      return base + x;
+    };
+    uint8_t *p = take((size_t)PB * ((rows + 63) / 64) * 16384);
+    uint8_t *ring = take((size_t)NS * kTtKeys * D * 2), *q = take((size_t)rows * D * 2);
+    uint8_t *scr = take(rows <= 128 ? (size_t)rows * 24 : 0);
+    uint8_t *nb = take((size_t)rows * 4), *bars = take((2 * NS + 11) * 8), *sc = take(66 * 8);
+    uint8_t *th = take(16);
+    if (o) {
+      o->p = p;
+      o->ring = ring;
+      o->q = q;
+      o->nb = reinterpret_cast<float *>(nb);
+      o->scr = reinterpret_cast<float *>(scr);
+      o->full = reinterpret_cast<uint64_t *>(bars);
+      o->empty = o->full + NS;
+      o->qfull = o->empty + NS;
+      o->qempty = o->qfull + 1;
+      o->sfull = o->qempty + 1;
+      o->sfree = o->sfull + 2;
+      o->pready = o->sfree + 2;
+      o->pvdone = o->pready + 2;
+      o->ofree = o->pvdone + 2;
+      o->scan = reinterpret_cast<int64_t *>(sc);
+      o->tmem_holder = reinterpret_cast<uint32_t *>(th);
+      o->failed = reinterpret_cast<volatile int *>(th + 4);
+      o->odd = reinterpret_cast<volatile int *>(th + 8);
+    }
+    return at;
+  }
+};
+
+// MN-major operand with the 128-byte swizzle: 64 MN elements (128 B) by 8 K
+// rows per 1024-byte atom; atoms along K are 1024 B apart, along MN `lbo`.
+__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t addr, uint32_t lbo) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) |
+         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+      "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+      "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])), "r"(__float_as_uint(v[8])),
+      "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])),
+      "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])),
+      "r"(__float_as_uint(v[15]))
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ bool named_sync_or(int id, int n, bool v) {
+  return !named_sync_and(id, n, !v);
+}
+
+// Where a run stands: tiles [t0, t1) of one (request, KV head, row tile).
+struct TreePos {
+  int r, unit, n_rt, n_kt, c, q0, T;
+  int64_t g, run0, run1;
+  int t0;
+  __device__ __forceinline__ void init(const TreeArgs &a, int64_t before) {
+    tree_request(a, r, c, q0, T);
+    tree_tiles(a, r, n_rt, n_kt);
+    unit = (int)((g - before) / n_kt);
+    t0 = (int)((g - before) % n_kt);
+  }
+  __device__ __forceinline__ int t1() const { return (int)min((int64_t)n_kt, t0 + (run1 - g)); }
+  __device__ __forceinline__ int h() const { return unit / n_rt; }
+  __device__ __forceinline__ int rt() const { return unit % n_rt; }
+  __device__ __forceinline__ int rows(const TreeArgs &a) const {
+    return min(a.rows, T * a.G - rt() * a.rows);
+  }
+  __device__ __forceinline__ void next(const TreeArgs &a) {
+    const int e = t1();
+    g += e - t0;
+    t0 = 0;
+    if (g < run1 && e == n_kt && ++unit == a.H * n_rt) {
+      unit = 0;
+      do {
+        r++;
+        tree_tiles(a, r, n_rt, n_kt);
+      } while (n_rt == 0);
+      tree_request(a, r, c, q0, T);
+    }
+  }
+};
+
+// Columns [c0, c0 + 16) of one key of a tile: the scaled logits, −inf where
+// the row does not see the key (node j; j < 0: a cached position).
+__device__ __forceinline__ void tree_logits16(const TreeArgs &a, uint32_t taddr, bool masked,
+                                              bool valid, int j, int T, int q0, int row0,
+                                              float (&v)[16]) {
+  tmem_ld16(taddr, v);
+#pragma unroll
+  for (int e = 0; e < 16; e++) v[e] *= a.zscale;
+  if (masked) {
+    const bool cached = valid && j < 0, node = valid && j >= 0 && j < T;
+#pragma unroll 1
+    for (int b = 0; b < 16; b += 4) {
+#pragma unroll
+      for (int e = 0; e < 16; e++) {
+        if ((e & ~3) != b) continue;
+        const int i = (row0 + e) / a.G;
+        bool see = cached;
+        if (node && i < T)
+          see = a.mask ? (a.mask[(int64_t)(q0 + i) * a.mask_words + (j >> 5)] >> (j & 31)) & 1u
+                       : j <= i;
+        if (!see) v[e] = -INFINITY;
+      }
+    }
+  }
+}
+
+template <int D, int CW>
+__global__ void __launch_bounds__(kTtThreads, 1)
+k_tree_tc(TreeArgs a, TreeTc p) {
+  constexpr int CH = D / 8, KB = D / 64;
+  constexpr uint32_t kSlot = kTtKeys * D * 2;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *base = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  TreeTcSmem sm;
+  TreeTcSmem::layout(D, a.rows, p.NS, p.PB, &sm, base);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int nsw = p.NW * 4;  // softmax warps
+  const uint32_t p_bytes = (uint32_t)((a.rows + 63) / 64) * 16384u;
+
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (tid == 0) {
+    *sm.failed = 0;
+    *sm.odd = 0;
+    for (int i = 0; i < p.NS; i++) {
+      mbar_init(smem_u32(sm.full + i), kTtProd * 32);
+      mbar_init(smem_u32(sm.empty + i), 1);
+    }
+    mbar_init(smem_u32(sm.qfull), kTtProd * 32);
+    mbar_init(smem_u32(sm.qempty), 1);
+    for (int i = 0; i < 2; i++) {
+      mbar_init(smem_u32(sm.sfull + i), 1);
+      mbar_init(smem_u32(sm.sfree + i), nsw);
+      mbar_init(smem_u32(sm.pready + i), nsw);
+      mbar_init(smem_u32(sm.pvdone + i), 1);
+    }
+    mbar_init(smem_u32(sm.ofree), nsw);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == nsw + kTtProd) alloc_tmem_cols(sm.tmem_holder, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *sm.tmem_holder;
+  const uint32_t tmem_o = tmem + p.SB * a.rows;
+
+  if (blockIdx.x == 0)  // one report per bad request
+    for (int r = tid; r < a.n_req; r += blockDim.x) {
+      int c, q0, T;
+      if (!tree_request(a, r, c, q0, T)) record_error(a.status, KVC_ERR_BOUNDS);
+    }
+  int64_t total = 0;
+  for (int x = tid; x < a.n_req; x += blockDim.x) total += request_tiles(a, x);
+  total = block_sum(total, sm.scan);
+  const int n_cta = (int)min((int64_t)a.n_cta, total);
+  const bool works = (int)blockIdx.x < n_cta;
+  TreePos pos{};
+  if (works) {
+    pos.run0 = pos.g = run_start(total, n_cta, blockIdx.x);
+    pos.run1 = run_start(total, n_cta, blockIdx.x + 1);
+    int64_t before;
+    block_find(a.n_req, pos.g, sm.scan, [&](int x) { return request_tiles(a, x); }, pos.r, before);
+    pos.init(a, before);
+  }
+
+  bool ok = true;
+  if (warp >= nsw && warp < nsw + kTtProd) {
+    // ------------------------------------------------------- producers
+    const int pw = warp - nsw;
+    const int64_t n_blocks = a.n_slots / a.BS;
+    uint32_t rc = 0, qc = 0, pend = 0;
+    auto signal = [&]() {  // the stage's copies have landed: hand them to the tensor core
+      if (!pend) return;
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      mbar_arrive(pend);
+      pend = 0;
+    };
+    auto acquire = [&](uint64_t *bar, uint32_t parity) {
+      if (mbar_try(smem_u32(bar), parity)) return true;
+      if (pend) {  // the consumer may be waiting for it
+        cp_wait<0>();
+        signal();
+      }
+      return mbar_wait_bounded(smem_u32(bar), parity, sm.failed);
+    };
+    auto committed = [&](uint64_t *bar) {
+      cp_commit();
+      if (pend) {
+        cp_wait<1>();
+        signal();
+      }
+      pend = smem_u32(bar);
+    };
+    while (pos.g < pos.run1 && ok) {
+      const int t1 = pos.t1(), h = pos.h(), rt = pos.rt(), n_rows = pos.rows(a);
+      const int32_t *bt = a.block_table + (int64_t)pos.r * a.max_blocks;
+      const int end = pos.c + pos.T;
+      constexpr int RPI = 32 / CH;
+      const int col = lane % CH;
+      auto load = [&](const uint16_t *pool, int t, bool is_v) {
+        const int st = rc % p.NS;
+        if (!(ok = acquire(sm.empty + st, ((rc / p.NS) & 1) ^ 1))) return;
+        const uint32_t dst = smem_u32(sm.ring) + st * kSlot + (col >> 3) * (kTtKeys * 128);
+#pragma unroll
+        for (int k0 = pw * 32; k0 < kTtKeys; k0 += kTtProd * 32) {
+          const int pp = t * kTtKeys + k0 + lane;
+          int32_t slot = -1;
+          if (pp < end) {
+            const int32_t b = bt[pp / a.BS];
+            if (b >= 0 && b < n_blocks) slot = b * a.BS + pp % a.BS;
+            else record_error(a.status, KVC_ERR_BOUNDS);
+          }
+#pragma unroll
+          for (int i = 0; i < 32 / RPI; i++) {
+            const int row = i * RPI + lane / CH;
+            const int32_t sl = __shfl_sync(0xFFFFFFFFu, slot, row);
+            cp_async16(dst + (k0 + row) * 128 + (((col & 7) ^ (row & 7)) << 4),
+                       pool + ((int64_t)max(sl, 0) * a.H + h) * D + col * 8, sl >= 0);
+          }
+        }
+        committed(sm.full + st);
+        if (is_v && (t + 1) * kTtKeys > pos.c) {
+          // A node's V may hold infinities or NaN that some rows do not see: the
+          // product gets zeros in their place, and the run's end adds them to
+          // the rows that do.
+          cp_wait<0>();
+          bool odd = false;
+#pragma unroll 1
+          for (int i = 0; i < kTtKeys / (RPI * kTtProd); i++) {
+            // the rows this thread copied: blocks of 32 keys, kTtProd·32 apart
+            const int u0 = i * RPI + lane / CH;
+            const int row = (u0 & 31) + pw * 32 + (u0 >> 5) * (kTtProd * 32);
+            const uint32_t at = dst + row * 128 + (((col & 7) ^ (row & 7)) << 4);
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(at));
+            bool mine = false;
+#pragma unroll
+            for (int u = 0; u < 4; u++) {
+              if ((w[u] & 0x7F80u) == 0x7F80u) mine = true, w[u] &= 0xFFFF0000u;
+              if ((w[u] & 0x7F800000u) == 0x7F800000u) mine = true, w[u] &= 0xFFFFu;
+            }
+            // (cached positions are seen by every row: their values stay)
+            if (mine && t * kTtKeys + row >= pos.c) {
+              odd = true;
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]),
+                           "r"(w[1]), "r"(w[2]), "r"(w[3])
+                           : "memory");
+            }
+          }
+          if (odd) *sm.odd = 1;
+          signal();
+        }
+        rc++;
+      };
+      auto load_q = [&]() {
+        if (!(ok = acquire(sm.qempty, (qc & 1) ^ 1))) return;
+        for (int b = pw * 8; b < a.rows; b += kTtProd * 8)
+#pragma unroll
+          for (int i = 0; i < 8 / RPI; i++) {
+            const int row = b + i * RPI + lane / CH, x = rt * a.rows + row;
+            const bool on = row < n_rows;
+            cp_async16(smem_u32(sm.q) + (col >> 3) * (a.rows * 128) + row * 128 +
+                           (((col & 7) ^ (row & 7)) << 4),
+                       on ? a.q + ((int64_t)(pos.q0 + x / a.G) * a.Hq + h * a.G + x % a.G) * D + col * 8
+                          : a.q,
+                       on);
+          }
+        committed(sm.qfull);
+        qc++;
+      };
+      load(a.kpool, pos.t0, false);
+      if (ok) load_q();
+      for (int t = pos.t0 + 1; t < t1 && ok; t++) {
+        load(a.kpool, t, false);
+        if (ok) load(a.vpool, t - 1, true);
+      }
+      if (ok) load(a.vpool, t1 - 1, true);
+      pos.next(a);
+    }
+    cp_wait<0>();
+    signal();
+    if (!ok) *sm.failed = 1;
+  } else if (warp == nsw + kTtProd) {
+    // ------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      uint32_t rc = 0, qc = 0, sc = 0, vc = 0;  // ring slots, runs, S and PV products issued
+      while (pos.g < pos.run1 && ok) {
+        const int t0 = pos.t0, t1 = pos.t1(), n_rows = pos.rows(a);
+        const uint32_t nbits = (uint32_t)((n_rows + 15) / 16 * 2) << 17;  // N / 8
+        auto wait_slot = [&]() {
+          const bool r = mbar_wait_bounded(smem_u32(sm.full + rc % p.NS), (rc / p.NS) & 1, sm.failed);
+          return r;
+        };
+        auto issue_s = [&](bool last) {
+          const int b = sc % p.SB;
+          if (!(ok = wait_slot())) return;
+          if (!(ok = mbar_wait_bounded(smem_u32(sm.sfree + b), ((sc / p.SB) & 1) ^ 1, sm.failed)))
+            return;
+          tc_fence_after();
+          const uint32_t kb = smem_u32(sm.ring) + (rc % p.NS) * kSlot, qb = smem_u32(sm.q);
+#pragma unroll
+          for (int kk = 0; kk < 4 * KB; kk++)
+            mma_bf16(tmem + b * a.rows,
+                     smem_desc(kb + (kk >> 2) * (kTtKeys * 128) + (kk & 3) * 32),
+                     smem_desc(qb + (kk >> 2) * (a.rows * 128) + (kk & 3) * 32), p.idesc_s | nbits,
+                     kk > 0);
+          mma_commit(smem_u32(sm.sfull + b));
+          mma_commit(smem_u32(sm.empty + rc % p.NS));
+          if (last) mma_commit(smem_u32(sm.qempty));
+          rc++;
+          sc++;
+        };
+        auto issue_pv = [&](bool first) {
+          if (!(ok = wait_slot())) return;
+          if (first &&  // O's previous contents have been read
+              !(ok = mbar_wait_bounded(smem_u32(sm.ofree), (qc & 1) ^ 1, sm.failed)))
+            return;
+          if (!(ok = mbar_wait_bounded(smem_u32(sm.pready + (vc & 1)), (vc >> 1) & 1, sm.failed)))
+            return;
+          tc_fence_after();
+          const uint32_t vb = smem_u32(sm.ring) + (rc % p.NS) * kSlot;
+          const uint32_t pb = smem_u32(sm.p) + (vc % p.PB) * p_bytes;
+#pragma unroll
+          for (int kk = 0; kk < kTtKeys / 16; kk++)
+            mma_bf16(tmem_o, smem_desc_mn(vb + kk * 2048, KB == 2 ? kTtKeys * 128 : 0),
+                     smem_desc_mn(pb + kk * 2048, 16384), p.idesc_o | nbits, !first || kk > 0);
+          mma_commit(smem_u32(sm.pvdone + (vc & 1)));
+          mma_commit(smem_u32(sm.empty + rc % p.NS));
+          rc++;
+          vc++;
+        };
+        ok = mbar_wait_bounded(smem_u32(sm.qfull), qc & 1, sm.failed);
+        if (ok) issue_s(t1 - t0 == 1);
+        for (int t = t0 + 1; t < t1 && ok; t++) {
+          issue_s(t == t1 - 1);
+          if (ok) issue_pv(t - 1 == t0);
+        }
+        if (ok) issue_pv(t1 - t0 == 1);
+        qc++;
+        pos.next(a);
+      }
+      if (!ok) *sm.failed = 1;
+    }
+    __syncwarp();
+  } else if (warp < nsw) {
+    // --------------------------------------------------------- softmax
+    const int wg = warp >> 2, quarter = warp & 3;
+    const int c0 = wg * CW;                                   // this warpgroup's first row
+    const int bar = 1 + wg, wt = tid & 127;
+    const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+    const int key = quarter * 32 + lane;
+    float *nb = sm.nb + c0;
+    const int64_t n_blocks = a.n_slots / a.BS;
+    uint32_t sc = 0, qc = 0;  // tiles and runs done
+    while (pos.g < pos.run1 && ok) {
+      const int t0 = pos.t0, t1 = pos.t1(), h = pos.h(), rt = pos.rt(), n_rows = pos.rows(a);
+      const int n_col = (n_rows + 15) / 16 * 16;              // columns the products compute
+      const int cols = max(0, min(CW, n_col - c0));           // of them this warpgroup's
+      const int32_t *bt = a.block_table + (int64_t)pos.r * a.max_blocks;
+      const int end = pos.c + pos.T;
+      named_sync(bar, 128);                                   // the last run's references are read
+      if (wt < CW && c0 + wt < a.rows) nb[wt] = -kUnset;
+      named_sync(bar, 128);
+      // sums of the weights: CW 32 per key lane; CW 64 per pair of lanes, the
+      // even lane keeping rows 0–7 of each 16 and the odd one rows 8–15
+      float l[32];
+#pragma unroll
+      for (int e = 0; e < 32; e++) l[e] = 0.f;
+      int32_t blk = 0;
+      if (t0 * kTtKeys + key < end) blk = bt[(t0 * kTtKeys + key) / a.BS];
+      // A wait that gives up only clears this warp's `ok`; the warpgroup leaves
+      // together, at the next vote.
+      for (int t = t0; t < t1; t++, sc++) {
+        const int pp = t * kTtKeys + key;
+        const bool valid = pp < end && blk >= 0 && blk < n_blocks;
+        int32_t blk_next = 0;
+        if (t + 1 < t1 && pp + kTtKeys < end) blk_next = bt[(pp + kTtKeys) / a.BS];
+        // (warp-uniform) a tile with nodes, past the end, or with a bad block
+        const bool masked = __any_sync(0xFFFFFFFFu, !valid || pp >= pos.c);
+        const int b = sc % p.SB;
+        ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.sfull + b),
+                                                             (sc / p.SB) & 1, sm.failed));
+        tc_fence_after();
+        const uint32_t ts = tmem + lanes + b * a.rows + c0;
+        const int j = pp - pos.c, row0 = rt * a.rows + c0;
+        // pass 1: does some logit pass its row's reference by too much?
+        float top = -INFINITY;
+        if (ok) {
+#pragma unroll 1
+          for (int cc = 0; cc < cols; cc += 16) {
+            float v[16];
+            tree_logits16(a, ts + cc, masked, valid, j, pos.T, pos.q0, row0 + cc, v);
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              const float4 n4 = *reinterpret_cast<const float4 *>(nb + cc + e);
+              top = max3(top, v[e] + n4.x, v[e + 1] + n4.y);
+              top = max3(top, v[e + 2] + n4.z, v[e + 3] + n4.w);
+            }
+          }
+        }
+        // the vote also keeps the warpgroup's warps within one tile of each other
+        const bool raise = named_sync_or(bar, 128, !ok || top > kExceed);
+        const uint32_t pv = sc - 1;  // the product before this tile's
+        if (raise) {
+          float *scr = CW == 32 ? sm.scr + wg * (6 * CW) : reinterpret_cast<float *>(sm.p + wg * 16384);
+          if (sc > 0 && ok)
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.pvdone + (pv & 1)),
+                                                           (pv >> 1) & 1, sm.failed));
+          // (every product that reads P is done: its memory may serve as scratch)
+          ok = named_sync_and(bar, 128, ok);
+          if (!ok) break;
+          {
+#pragma unroll 1
+            for (int cc = 0; cc < cols; cc += 16) {
+              float v[16];
+              tree_logits16(a, ts + cc, masked, valid, j, pos.T, pos.q0, row0 + cc, v);
+#pragma unroll
+              for (int e = 0; e < 16; e++) {
+                float m = v[e];
+#pragma unroll
+                for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+                if (lane == e) scr[quarter * CW + cc + e] = m;
+              }
+            }
+            named_sync(bar, 128);
+            if (wt < cols) {
+              const float was = -nb[wt];
+              const float m = fmaxf(fmaxf(scr[wt], scr[CW + wt]), fmaxf(scr[2 * CW + wt], scr[3 * CW + wt]));
+              const float now = fmaxf(was, m);
+              scr[4 * CW + wt] = ex2(was - now);
+              nb[wt] = -now;
+            }
+            named_sync(bar, 128);
+            const float *fac = scr + 4 * CW;
+#pragma unroll
+            for (int e = 0; e < 32; e++) {
+              const int col = CW == 32 ? e : (e >> 3) * 16 + (lane & 1) * 8 + (e & 7);
+              if (col < cols) l[e] *= fac[col];
+            }
+            if (t > t0) {
+#pragma unroll 1
+              for (int cc = 0; cc < cols; cc += 16) {
+                float v[16];
+                tmem_ld16(tmem_o + lanes + c0 + cc, v);
+#pragma unroll
+                for (int e = 0; e < 16; e++) v[e] *= fac[cc + e];
+                tmem_st16(tmem_o + lanes + c0 + cc, v);
+              }
+            }
+            named_sync(bar, 128);  // the factors are read before P replaces them
+          }
+        } else if (sc >= (uint32_t)p.PB && ok) {
+          const uint32_t u = sc - p.PB;  // P's buffer is free
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.pvdone + (u & 1)), (u >> 1) & 1,
+                                                         sm.failed));
+        }
+        // pass 2: the weights
+        if (ok) {
+          const uint32_t pbase = smem_u32(sm.p) + (sc % p.PB) * p_bytes + key * 128;
+#pragma unroll
+          for (int cc = 0; cc < CW; cc += 16) {
+            if (cc >= cols) break;
+            float v[16];
+            tree_logits16(a, ts + cc, masked, valid, j, pos.T, pos.q0, row0 + cc, v);
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              const float4 n4 = *reinterpret_cast<const float4 *>(nb + cc + e);
+              v[e] = ex2(v[e] + n4.x);
+              v[e + 1] = ex2(v[e + 1] + n4.y);
+              v[e + 2] = ex2(v[e + 2] + n4.z);
+              v[e + 3] = ex2(v[e + 3] + n4.w);
+              w[e / 2] = pack_bf16x2(v[e], v[e + 1]);
+              w[e / 2 + 1] = pack_bf16x2(v[e + 2], v[e + 3]);
+            }
+            if (CW == 32) {
+#pragma unroll
+              for (int e = 0; e < 16; e++) l[(cc + e) % 32] += v[e];
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; e++) {
+                const float keep = lane & 1 ? v[8 + e] : v[e], give = lane & 1 ? v[e] : v[8 + e];
+                l[cc / 2 + e] += keep + __shfl_xor_sync(0xFFFFFFFFu, give, 1);
+              }
+            }
+            const int x = c0 + cc;  // 16 rows = two 16-byte chunks of block x / 64
+            const uint32_t blkp = pbase + (x >> 6) * 16384;
+#pragma unroll
+            for (int u = 0; u < 2; u++)
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                               blkp + (((((x & 63) >> 3) + u) ^ (key & 7)) << 4)),
+                           "r"(w[4 * u]), "r"(w[4 * u + 1]), "r"(w[4 * u + 2]), "r"(w[4 * u + 3])
+                           : "memory");
+          }
+        }
+        tc_fence_before();
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(sm.sfree + b));
+          mbar_arrive(smem_u32(sm.pready + (sc & 1)));
+        }
+        blk = blk_next;
+      }
+      // ---- the run's result: sums over the key lanes, then O
+      const uint32_t pv = sc - 1;
+      if (ok)
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.pvdone + (pv & 1)), (pv >> 1) & 1,
+                                                       sm.failed));
+      ok = named_sync_and(bar, 128, ok);
+      if (!ok) break;
+      tc_fence_after();
+      // (P is free: its last product is done)
+      float *scr = CW == 32 ? sm.scr + wg * (6 * CW) : reinterpret_cast<float *>(sm.p + wg * 16384);
+#pragma unroll
+      for (int e = 0; e < 32; e++) {
+        float x = l[e];
+#pragma unroll
+        for (int o = 16; o >= (CW == 32 ? 1 : 2); o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+        const int col = CW == 32 ? e : (e >> 3) * 16 + (lane & 1) * 8 + (e & 7);
+        if (lane < CW / 32) scr[quarter * CW + col] = x;
+      }
+      named_sync(bar, 128);
+      const bool whole = t0 == 0 && t1 == pos.n_kt;
+      const int64_t slot = 2 * (int64_t)blockIdx.x + (pos.g != pos.run0);
+      const int real = min(cols, n_rows - c0);
+      if (wt < real) {
+        const float sum = (scr[wt] + scr[CW + wt]) + (scr[2 * CW + wt] + scr[3 * CW + wt]);
+        const float m = sum > 0.f || sum != sum ? -nb[wt] : -INFINITY;
+        const int x = rt * a.rows + c0 + wt;
+        if (whole) {
+          const int64_t qr = (int64_t)(pos.q0 + x / a.G) * a.Hq + h * a.G + x % a.G;
+          a.lse[qr] = m == -INFINITY ? -INFINITY : (m + log2f(sum)) * kLn2;
+        } else {
+          a.part_ml[slot * a.rows + c0 + wt] = make_float2(m, sum);
+        }
+        scr[4 * CW + wt] = whole ? (m == -INFINITY ? 0.f : 1.f / sum) : 1.f;
+      }
+      named_sync(bar, 128);
+      const float *fac = scr + 4 * CW;
+      const int d = D == 64 ? key & 63 : key;
+      const bool odd = *sm.odd != 0;
+#pragma unroll 1
+      for (int cc = 0; cc < real; cc += 16) {
+        float v[16];
+        tmem_ld16(tmem_o + lanes + c0 + cc, v);
+        if (odd) {  // infinities and NaN of the nodes this run covered, to the rows that see them
+          for (int jn = max(0, t0 * kTtKeys - pos.c); jn < min(pos.T, t1 * kTtKeys - pos.c); jn++) {
+            const int pn = pos.c + jn;
+            const int32_t bn = bt[pn / a.BS];
+            if (bn < 0 || bn >= n_blocks) continue;
+            const float vn = bf16_lo(a.vpool[(((int64_t)bn * a.BS + pn % a.BS) * a.H + h) * D + d]);
+            if (fabsf(vn) < INFINITY) continue;
+#pragma unroll
+            for (int e = 0; e < 16; e++) {
+              const int i = (rt * a.rows + c0 + cc + e) / a.G;
+              if (i >= pos.T) continue;
+              const bool see = a.mask ? (a.mask[(int64_t)(pos.q0 + i) * a.mask_words + (jn >> 5)] >> (jn & 31)) & 1u
+                                      : jn <= i;
+              if (see) v[e] += vn;
+            }
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 16; e++) {
+          if (cc + e >= real || (D == 64 && key >= 64)) continue;
+          const int x = rt * a.rows + c0 + cc + e;
+          const float o = v[e] * fac[cc + e];
+          if (whole) {
+            const __nv_bfloat16 ob = __float2bfloat16(fac[cc + e] == 0.f ? 0.f : o);
+            const int64_t qr = (int64_t)(pos.q0 + x / a.G) * a.Hq + h * a.G + x % a.G;
+            a.out[qr * D + d] = *reinterpret_cast<const uint16_t *>(&ob);
+          } else {
+            a.part_o[(slot * a.rows + c0 + cc + e) * D + d] = o;
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(sm.ofree));
+      qc++;
+      pos.next(a);
+    }
+    if (!ok) {
+      *sm.failed = 1;
+      if (lane == 0) record_error(a.status, KVC_ERR_TIMEOUT);
+    }
+  }
+
+  // -------------------------------------------------------- teardown
+  tc_fence_before();
+  __syncthreads();
+  if (*sm.failed && tid == 0) {
+    record_error(a.status, KVC_ERR_TIMEOUT);
+    // let this CTA's products finish before its memory is released
+    for (int i = 0; i < 2; i++) {
+      mbar_drain(smem_u32(sm.sfull + i), 0);
+      mbar_drain(smem_u32(sm.sfull + i), 1);
+      mbar_drain(smem_u32(sm.pvdone + i), 0);
+      mbar_drain(smem_u32(sm.pvdone + i), 1);
+    }
+  }
+  __syncthreads();
+  if (warp == nsw + kTtProd) {
+    tc_fence_after();
+    free_tmem_cols(tmem, 512);
+  }
+}
+
 // Joins the partials of one (request, KV head, row tile) that was split over
 // CTAs: blockIdx.x = (request, KV head), blockIdx.y = row tile, blockIdx.z a
 // group of four rows.
@@ -527,16 +1198,40 @@ k_tree_join(TreeArgs a) {
   if (d0 == 0) a.lse[qr] = mx == -INFINITY ? -INFINITY : (mx + log2f(sum)) * kLn2;
 }
 
+// Rows up to which the narrow instruction is used.
+constexpr int kRowsMax = 32;
+constexpr int kTcRowsMax = 256;
+
 // Rows per tile, keys per tile and grid of a call.
 void tree_plan(int n_req, int max_blocks, int max_tree, int H, int Hq, int D, int BS, int &rows,
                int &tile, int &n_cta, int &max_rt) {
   const int R = max_tree * (Hq / H);
-  rows = R <= 16 ? 16 : 32;
-  tile = kRowWarps * (2048 / D);
+  const bool tc = R > kRowsMax;
+  rows = tc ? std::min((R + 31) / 32 * 32, kTcRowsMax) : R <= 16 ? 16 : 32;
+  tile = tc ? kTtKeys : kRowWarps * (2048 / D);
   max_rt = (R + rows - 1) / rows;
   const int64_t most =
       (int64_t)n_req * H * max_rt * (((int64_t)max_blocks * BS + tile - 1) / tile);
-  n_cta = (int)std::min<int64_t>(2 * device_sm_count(), most);
+  n_cta = (int)std::min<int64_t>((tc ? 1 : 2) * device_sm_count(), most);
+}
+
+template <int D, int CW>
+cudaError_t launch_tc(const TreeArgs &a, cudaStream_t s) {
+  constexpr size_t kSmemMax = 232448;
+  TreeTc p;
+  p.NW = (a.rows + CW - 1) / CW;
+  p.PB = a.rows <= 128 ? 2 : 1;
+  p.SB = 3 * a.rows <= 512 ? 2 : 1;
+  for (p.NS = 8; p.NS > 3; p.NS--)
+    if (1024 + TreeTcSmem::layout(D, a.rows, p.NS, p.PB, nullptr, nullptr) <= kSmemMax) break;
+  p.idesc_s = make_idesc(128, 0);
+  p.idesc_o = make_idesc(128, 0) | (1u << 15) | (1u << 16);  // V and P MN-major
+  const size_t smem = 1024 + TreeTcSmem::layout(D, a.rows, p.NS, p.PB, nullptr, nullptr);
+  cudaError_t e = cudaFuncSetAttribute(k_tree_tc<D, CW>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  k_tree_tc<D, CW><<<a.n_cta, (p.NW * 4 + kTtProd + 1) * 32, smem, s>>>(a, p);
+  return cudaGetLastError();
 }
 
 template <int D, int MT>
@@ -590,8 +1285,13 @@ cudaError_t launch_tree_attn(const uint16_t *q, const uint16_t *kpool, const uin
   tree_plan(n_req, max_blocks, max_tree, H, Hq, D, BS, a.rows, a.tile, a.n_cta, max_rt);
   a.part_o = reinterpret_cast<float *>(ws);
   a.part_ml = reinterpret_cast<float2 *>(a.part_o + (size_t)2 * a.n_cta * a.rows * D);
-  cudaError_t e = D == 128 ? (a.rows == 16 ? launch_rows<128, 1>(a, s) : launch_rows<128, 2>(a, s))
-                           : (a.rows == 16 ? launch_rows<64, 1>(a, s) : launch_rows<64, 2>(a, s));
+  cudaError_t e;
+  if (a.tile == kTtKeys && max_tree * a.G > kRowsMax)
+    e = D == 128 ? (a.rows <= 128 ? launch_tc<128, 32>(a, s) : launch_tc<128, 64>(a, s))
+                 : (a.rows <= 128 ? launch_tc<64, 32>(a, s) : launch_tc<64, 64>(a, s));
+  else
+    e = D == 128 ? (a.rows == 16 ? launch_rows<128, 1>(a, s) : launch_rows<128, 2>(a, s))
+                 : (a.rows == 16 ? launch_rows<64, 1>(a, s) : launch_rows<64, 2>(a, s));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((int64_t)n_req * H), (unsigned)max_rt, (unsigned)(a.rows / 4));
