@@ -602,30 +602,57 @@ struct TreePos {
   }
 };
 
-// Columns [c0, c0 + 16) of one key of a tile: the scaled logits, −inf where
-// the row does not see the key (node j; j < 0: a cached position).
-__device__ __forceinline__ void tree_logits16(const TreeArgs &a, uint32_t taddr, bool masked,
-                                              bool valid, int j, int T, int q0, int row0,
-                                              float (&v)[16]) {
-  tmem_ld16(taddr, v);
+// 16 TMEM lanes × 8·NB columns (16x256b): register 4k + j of thread t holds
+// lane t/4 + 8·(j ≥ 2), column 8k + 2·(t%4) + (j & 1).
+template <int NB>
+__device__ __forceinline__ void tmem_frag(uint32_t taddr, uint32_t (&r)[4 * NB]);
+template <>
+__device__ __forceinline__ void tmem_frag<4>(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+template <>
+__device__ __forceinline__ void tmem_frag<8>(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+      "%28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void stsm4(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2,
+                                      uint32_t r3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+               "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+               : "memory");
+}
+
+// x = z·zscale + nb of one 16-lane half, as pairs of rows (x[2k]: key t/4,
+// x[2k + 1]: key t/4 + 8), −inf where bit 4k + j of `see` is clear.
+template <int NB>
+__device__ __forceinline__ void tree_exponents(const uint32_t (&z)[4 * NB], uint64_t zs2,
+                                               const uint64_t (&nb)[NB], bool masked, uint32_t see,
+                                               float (&x)[4 * NB]) {
 #pragma unroll
-  for (int e = 0; e < 16; e++) v[e] *= a.zscale;
-  if (masked) {
-    const bool cached = valid && j < 0, node = valid && j >= 0 && j < T;
-#pragma unroll 1
-    for (int b = 0; b < 16; b += 4) {
-#pragma unroll
-      for (int e = 0; e < 16; e++) {
-        if ((e & ~3) != b) continue;
-        const int i = (row0 + e) / a.G;
-        bool see = cached;
-        if (node && i < T)
-          see = a.mask ? (a.mask[(int64_t)(q0 + i) * a.mask_words + (j >> 5)] >> (j & 31)) & 1u
-                       : j <= i;
-        if (!see) v[e] = -INFINITY;
-      }
-    }
+  for (int k = 0; k < NB; k++) {
+    upk2(fma2(pk2(__uint_as_float(z[4 * k]), __uint_as_float(z[4 * k + 1])), zs2, nb[k]), x[4 * k],
+         x[4 * k + 1]);
+    upk2(fma2(pk2(__uint_as_float(z[4 * k + 2]), __uint_as_float(z[4 * k + 3])), zs2, nb[k]),
+         x[4 * k + 2], x[4 * k + 3]);
   }
+  if (masked)
+#pragma unroll
+    for (int e = 0; e < 4 * NB; e++)
+      if (!((see >> e) & 1u)) x[e] = -INFINITY;
 }
 
 template <int D, int CW>
@@ -692,91 +719,124 @@ k_tree_tc(TreeArgs a, TreeTc p) {
     // ------------------------------------------------------- producers
     const int pw = warp - nsw;
     const int64_t n_blocks = a.n_slots / a.BS;
-    uint32_t rc = 0, qc = 0, pend = 0;
-    auto signal = [&]() {  // the stage's copies have landed: hand them to the tensor core
-      if (!pend) return;
+    constexpr int RPI = 32 / CH, NU = kTtKeys / (32 * kTtProd);  // this warp's blocks of 32 keys
+    const int col = lane % CH;
+    uint32_t rc = 0, qc = 0;
+    uint32_t pend0 = 0, pend1 = 0;  // stages in flight, oldest first (the newest besides)
+    auto hand = [&](uint32_t bar) {  // the stage's copies have landed: to the tensor core
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      mbar_arrive(pend);
-      pend = 0;
+      mbar_arrive(bar);
     };
+    auto flush = [&]() {
+      if (pend1) {
+        cp_wait<1>();
+        hand(pend0);
+        pend0 = pend1;
+        pend1 = 0;
+      }
+      if (pend0) {
+        cp_wait<0>();
+        hand(pend0);
+        pend0 = 0;
+      }
+    };
+    // a full ring is waited for only after everything in flight is handed over
     auto acquire = [&](uint64_t *bar, uint32_t parity) {
       if (mbar_try(smem_u32(bar), parity)) return true;
-      if (pend) {  // the consumer may be waiting for it
-        cp_wait<0>();
-        signal();
-      }
+      flush();
       return mbar_wait_bounded(smem_u32(bar), parity, sm.failed);
     };
     auto committed = [&](uint64_t *bar) {
       cp_commit();
-      if (pend) {
-        cp_wait<1>();
-        signal();
+      if (pend1) {
+        cp_wait<2>();
+        hand(pend0);
+        pend0 = pend1;
+        pend1 = smem_u32(bar);
+      } else if (pend0) {
+        pend1 = smem_u32(bar);
+      } else {
+        pend0 = smem_u32(bar);
       }
-      pend = smem_u32(bar);
     };
     while (pos.g < pos.run1 && ok) {
       const int t1 = pos.t1(), h = pos.h(), rt = pos.rt(), n_rows = pos.rows(a);
       const int32_t *bt = a.block_table + (int64_t)pos.r * a.max_blocks;
       const int end = pos.c + pos.T;
-      constexpr int RPI = 32 / CH;
-      const int col = lane % CH;
-      auto load = [&](const uint16_t *pool, int t, bool is_v) {
+      int32_t blk[NU], ks[NU], vs[NU];  // block ids of the next tile; slots of this K, of this V
+      auto fetch = [&](int t) {
+#pragma unroll
+        for (int u = 0; u < NU; u++) {
+          const int pp = t * kTtKeys + pw * 32 + u * (32 * kTtProd) + lane;
+          blk[u] = pp < end && t < t1 ? bt[pp / a.BS] : 0;
+        }
+      };
+      auto resolve = [&](int t) {
+#pragma unroll
+        for (int u = 0; u < NU; u++) {
+          const int pp = t * kTtKeys + pw * 32 + u * (32 * kTtProd) + lane;
+          vs[u] = ks[u];
+          ks[u] = -1;
+          if (pp < end) {
+            if (blk[u] >= 0 && blk[u] < n_blocks) ks[u] = blk[u] * a.BS + pp % a.BS;
+            else record_error(a.status, KVC_ERR_BOUNDS);
+          }
+        }
+      };
+      auto load = [&](const uint16_t *pool, const int32_t (&slot)[NU]) {
         const int st = rc % p.NS;
         if (!(ok = acquire(sm.empty + st, ((rc / p.NS) & 1) ^ 1))) return;
         const uint32_t dst = smem_u32(sm.ring) + st * kSlot + (col >> 3) * (kTtKeys * 128);
 #pragma unroll
-        for (int k0 = pw * 32; k0 < kTtKeys; k0 += kTtProd * 32) {
-          const int pp = t * kTtKeys + k0 + lane;
-          int32_t slot = -1;
-          if (pp < end) {
-            const int32_t b = bt[pp / a.BS];
-            if (b >= 0 && b < n_blocks) slot = b * a.BS + pp % a.BS;
-            else record_error(a.status, KVC_ERR_BOUNDS);
-          }
+        for (int u = 0; u < NU; u++)
 #pragma unroll
           for (int i = 0; i < 32 / RPI; i++) {
             const int row = i * RPI + lane / CH;
-            const int32_t sl = __shfl_sync(0xFFFFFFFFu, slot, row);
-            cp_async16(dst + (k0 + row) * 128 + (((col & 7) ^ (row & 7)) << 4),
+            const int32_t sl = __shfl_sync(0xFFFFFFFFu, slot[u], row);
+            cp_async16(dst + (pw * 32 + u * (32 * kTtProd) + row) * 128 +
+                           (((col & 7) ^ (row & 7)) << 4),
                        pool + ((int64_t)max(sl, 0) * a.H + h) * D + col * 8, sl >= 0);
           }
-        }
         committed(sm.full + st);
-        if (is_v && (t + 1) * kTtKeys > pos.c) {
-          // A node's V may hold infinities or NaN that some rows do not see: the
-          // product gets zeros in their place, and the run's end adds them to
-          // the rows that do.
-          cp_wait<0>();
-          bool odd = false;
-#pragma unroll 1
-          for (int i = 0; i < kTtKeys / (RPI * kTtProd); i++) {
-            // the rows this thread copied: blocks of 32 keys, kTtProd·32 apart
-            const int u0 = i * RPI + lane / CH;
-            const int row = (u0 & 31) + pw * 32 + (u0 >> 5) * (kTtProd * 32);
-            const uint32_t at = dst + row * 128 + (((col & 7) ^ (row & 7)) << 4);
-            uint32_t w[4];
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                         : "r"(at));
-            bool mine = false;
-#pragma unroll
-            for (int u = 0; u < 4; u++) {
-              if ((w[u] & 0x7F80u) == 0x7F80u) mine = true, w[u] &= 0xFFFF0000u;
-              if ((w[u] & 0x7F800000u) == 0x7F800000u) mine = true, w[u] &= 0xFFFFu;
-            }
-            // (cached positions are seen by every row: their values stay)
-            if (mine && t * kTtKeys + row >= pos.c) {
-              odd = true;
-              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]),
-                           "r"(w[1]), "r"(w[2]), "r"(w[3])
-                           : "memory");
-            }
-          }
-          if (odd) *sm.odd = 1;
-          signal();
-        }
         rc++;
+      };
+      auto load_v = [&](int t, const int32_t (&slot)[NU]) {
+        const uint32_t dst =
+            smem_u32(sm.ring) + (rc % p.NS) * kSlot + (col >> 3) * (kTtKeys * 128);
+        load(a.vpool, slot);
+        if (!ok || (t + 1) * kTtKeys <= pos.c) return;
+        // A node's V may hold infinities or NaN that some rows do not see: the
+        // product gets zeros in their place, and the run's end adds them to
+        // the rows that do.  Each thread looks at what it copied, before the
+        // stage is handed over.
+        cp_wait<0>();
+        bool odd = false;
+#pragma unroll 1
+        for (int i = 0; i < NU * 32 / RPI; i++) {
+          const int u0 = i * RPI + lane / CH;
+          const int row = (u0 & 31) + pw * 32 + (u0 >> 5) * (kTtProd * 32);
+          const uint32_t at = dst + row * 128 + (((col & 7) ^ (row & 7)) << 4);
+          uint32_t w[4];
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                       : "r"(at)
+                       : "memory");
+          bool mine = false;
+#pragma unroll
+          for (int u = 0; u < 4; u++) {
+            if ((w[u] & 0x7F80u) == 0x7F80u) mine = true, w[u] &= 0xFFFF0000u;
+            if ((w[u] & 0x7F800000u) == 0x7F800000u) mine = true, w[u] &= 0xFFFFu;
+          }
+          // (cached positions are seen by every row: their values stay)
+          if (mine && t * kTtKeys + row >= pos.c) {
+            odd = true;
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]),
+                         "r"(w[2]), "r"(w[3])
+                         : "memory");
+          }
+        }
+        if (odd) *sm.odd = 1;
+        flush();
       };
       auto load_q = [&]() {
         if (!(ok = acquire(sm.qempty, (qc & 1) ^ 1))) return;
@@ -794,17 +854,22 @@ k_tree_tc(TreeArgs a, TreeTc p) {
         committed(sm.qfull);
         qc++;
       };
-      load(a.kpool, pos.t0, false);
+      fetch(pos.t0);
+      resolve(pos.t0);
+      fetch(pos.t0 + 1);
+      load(a.kpool, ks);
       if (ok) load_q();
       for (int t = pos.t0 + 1; t < t1 && ok; t++) {
-        load(a.kpool, t, false);
-        if (ok) load(a.vpool, t - 1, true);
+        resolve(t);
+        fetch(t + 1);
+        load(a.kpool, ks);
+        if (ok) load_v(t - 1, vs);
       }
-      if (ok) load(a.vpool, t1 - 1, true);
+      if (ok) load_v(t1 - 1, ks);
       pos.next(a);
     }
+    flush();
     cp_wait<0>();
-    signal();
     if (!ok) *sm.failed = 1;
   } else if (warp == nsw + kTtProd) {
     // ------------------------------------------------------ MMA issuer
@@ -870,28 +935,34 @@ k_tree_tc(TreeArgs a, TreeTc p) {
     __syncwarp();
   } else if (warp < nsw) {
     // --------------------------------------------------------- softmax
+    constexpr int NB = CW / 8;       // 8-row blocks of this warpgroup's rows
+    constexpr bool kKeep = CW == 32;  // both halves' exponents fit the registers between the passes
     const int wg = warp >> 2, quarter = warp & 3;
-    const int c0 = wg * CW;                                   // this warpgroup's first row
+    const int c0 = wg * CW;          // this warpgroup's first row
     const int bar = 1 + wg, wt = tid & 127;
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
     const int key = quarter * 32 + lane;
     float *nb = sm.nb + c0;
+    float *scr = CW == 32 ? sm.scr + wg * (6 * CW) : reinterpret_cast<float *>(sm.p + wg * 16384);
+    const uint64_t zs2 = pk2(a.zscale, a.zscale);
     const int64_t n_blocks = a.n_slots / a.BS;
+    // stmatrix: this lane's row address, matrices (keys 0–7 | 8–15) × (block k | k + 1)
+    const int mkey = quarter * 32 + ((lane >> 3) & 1) * 8 + (lane & 7);
     uint32_t sc = 0, qc = 0;  // tiles and runs done
     while (pos.g < pos.run1 && ok) {
       const int t0 = pos.t0, t1 = pos.t1(), h = pos.h(), rt = pos.rt(), n_rows = pos.rows(a);
-      const int n_col = (n_rows + 15) / 16 * 16;              // columns the products compute
-      const int cols = max(0, min(CW, n_col - c0));           // of them this warpgroup's
+      const int cols = max(0, min(CW, n_rows - c0));  // this warpgroup's rows of the run
       const int32_t *bt = a.block_table + (int64_t)pos.r * a.max_blocks;
       const int end = pos.c + pos.T;
-      named_sync(bar, 128);                                   // the last run's references are read
+      named_sync(bar, 128);                           // the last run's references are read
       if (wt < CW && c0 + wt < a.rows) nb[wt] = -kUnset;
-      named_sync(bar, 128);
-      // sums of the weights: CW 32 per key lane; CW 64 per pair of lanes, the
-      // even lane keeping rows 0–7 of each 16 and the odd one rows 8–15
-      float l[32];
+      uint64_t nbr[NB], l[NB];  // −reference and sum of weights of rows 8k + 2·(t%4) + {0, 1}
 #pragma unroll
-      for (int e = 0; e < 32; e++) l[e] = 0.f;
+      for (int k = 0; k < NB; k++) {
+        const int x = 8 * k + 2 * (lane & 3);
+        nbr[k] = pk2(x < cols ? -kUnset : -INFINITY, x + 1 < cols ? -kUnset : -INFINITY);
+        l[k] = 0;
+      }
       int32_t blk = 0;
       if (t0 * kTtKeys + key < end) blk = bt[(t0 * kTtKeys + key) / a.BS];
       // A wait that gives up only clears this warp's `ok`; the warpgroup leaves
@@ -902,33 +973,62 @@ k_tree_tc(TreeArgs a, TreeTc p) {
         int32_t blk_next = 0;
         if (t + 1 < t1 && pp + kTtKeys < end) blk_next = bt[(pp + kTtKeys) / a.BS];
         // (warp-uniform) a tile with nodes, past the end, or with a bad block
+        const uint32_t valid_keys = __ballot_sync(0xFFFFFFFFu, valid);
         const bool masked = __any_sync(0xFFFFFFFFu, !valid || pp >= pos.c);
+        uint32_t see[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+        if (masked) {
+          see[0] = see[1] = 0;
+#pragma unroll 1
+          for (int e = 0; e < 8 * NB; e++) {
+            const int hf = e / (4 * NB), k = (e >> 2) % NB, kk = hf * 16 + lane / 4 + 8 * ((e >> 1) & 1);
+            const int x = c0 + 8 * k + 2 * (lane & 3) + (e & 1);
+            const int j = t * kTtKeys + quarter * 32 + kk - pos.c, i = (rt * a.rows + x) / a.G;
+            bool v = (valid_keys >> kk) & 1u;
+            if (v && j >= 0)
+              v = i < pos.T &&
+                  (a.mask ? (a.mask[(int64_t)(pos.q0 + i) * a.mask_words + (j >> 5)] >> (j & 31)) & 1u
+                          : j <= i);
+            const uint32_t bit = (uint32_t)v << (e % (4 * NB));
+            if (hf == 0) see[0] |= bit;
+            else see[1] |= bit;
+          }
+        }
         const int b = sc % p.SB;
         ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.sfull + b),
                                                              (sc / p.SB) & 1, sm.failed));
         tc_fence_after();
         const uint32_t ts = tmem + lanes + b * a.rows + c0;
-        const int j = pp - pos.c, row0 = rt * a.rows + c0;
         // pass 1: does some logit pass its row's reference by too much?
         float top = -INFINITY;
+        float x[kKeep ? 2 : 1][4 * NB];
         if (ok) {
-#pragma unroll 1
-          for (int cc = 0; cc < cols; cc += 16) {
-            float v[16];
-            tree_logits16(a, ts + cc, masked, valid, j, pos.T, pos.q0, row0 + cc, v);
+          if constexpr (kKeep) {
+            uint32_t z[2][4 * NB];
+            tmem_frag<NB>(ts, z[0]);
+            tmem_frag<NB>(ts + (16u << 16), z[1]);
+            tmem_wait(z[0]);
+            tmem_wait(z[1]);
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-              const float4 n4 = *reinterpret_cast<const float4 *>(nb + cc + e);
-              top = max3(top, v[e] + n4.x, v[e + 1] + n4.y);
-              top = max3(top, v[e + 2] + n4.z, v[e + 3] + n4.w);
+            for (int hf = 0; hf < 2; hf++) tree_exponents<NB>(z[hf], zs2, nbr, masked, see[hf], x[hf]);
+#pragma unroll
+            for (int e = 0; e < 4 * NB; e += 2)
+              top = max3(max3(top, x[0][e], x[0][e + 1]), x[kKeep][e], x[kKeep][e + 1]);
+          } else {
+#pragma unroll
+            for (int hf = 0; hf < 2; hf++) {
+              uint32_t z[4 * NB];
+              tmem_frag<NB>(ts + ((uint32_t)(16 * hf) << 16), z);
+              tmem_wait(z);
+              tree_exponents<NB>(z, zs2, nbr, masked, see[hf], x[0]);
+#pragma unroll
+              for (int e = 0; e < 4 * NB; e += 2) top = max3(top, x[0][e], x[0][e + 1]);
             }
           }
         }
         // the vote also keeps the warpgroup's warps within one tile of each other
         const bool raise = named_sync_or(bar, 128, !ok || top > kExceed);
-        const uint32_t pv = sc - 1;  // the product before this tile's
         if (raise) {
-          float *scr = CW == 32 ? sm.scr + wg * (6 * CW) : reinterpret_cast<float *>(sm.p + wg * 16384);
+          const uint32_t pv = sc - 1;  // the product before this tile's
           if (sc > 0 && ok)
             ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.pvdone + (pv & 1)),
                                                            (pv >> 1) & 1, sm.failed));
@@ -936,88 +1036,108 @@ k_tree_tc(TreeArgs a, TreeTc p) {
           ok = named_sync_and(bar, 128, ok);
           if (!ok) break;
           {
+            float cm[2 * NB];
+#pragma unroll
+            for (int e = 0; e < 2 * NB; e++) cm[e] = -INFINITY;
+            uint64_t zero[NB];
+#pragma unroll
+            for (int k = 0; k < NB; k++) zero[k] = 0;
+#pragma unroll
+            for (int hf = 0; hf < 2; hf++) {
+              uint32_t z[4 * NB];
+              float y[4 * NB];
+              tmem_frag<NB>(ts + ((uint32_t)(16 * hf) << 16), z);
+              tmem_wait(z);
+              tree_exponents<NB>(z, zs2, zero, masked, see[hf], y);
+#pragma unroll
+              for (int k = 0; k < NB; k++) {
+                cm[2 * k] = max3(cm[2 * k], y[4 * k], y[4 * k + 2]);
+                cm[2 * k + 1] = max3(cm[2 * k + 1], y[4 * k + 1], y[4 * k + 3]);
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 2 * NB; e++) {
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1)
+                cm[e] = fmaxf(cm[e], __shfl_xor_sync(0xFFFFFFFFu, cm[e], o));
+              if (lane < 4) scr[quarter * CW + (e >> 1) * 8 + 2 * lane + (e & 1)] = cm[e];
+            }
+          }
+          named_sync(bar, 128);
+          if (wt < cols) {
+            const float was = -nb[wt];
+            const float m = fmaxf(fmaxf(scr[wt], scr[CW + wt]), fmaxf(scr[2 * CW + wt], scr[3 * CW + wt]));
+            const float now = fmaxf(was, m);
+            scr[4 * CW + wt] = ex2(was - now);
+            nb[wt] = -now;
+          }
+          named_sync(bar, 128);
+          const float *fac = scr + 4 * CW;
+#pragma unroll
+          for (int k = 0; k < NB; k++) {
+            const int x0 = 8 * k + 2 * (lane & 3);
+            float l0, l1;
+            upk2(l[k], l0, l1);
+            if (x0 < cols) l0 *= fac[x0];
+            if (x0 + 1 < cols) l1 *= fac[x0 + 1];
+            l[k] = pk2(l0, l1);
+            nbr[k] = pk2(x0 < cols ? nb[x0] : -INFINITY, x0 + 1 < cols ? nb[x0 + 1] : -INFINITY);
+          }
+          if (t > t0) {
 #pragma unroll 1
             for (int cc = 0; cc < cols; cc += 16) {
               float v[16];
-              tree_logits16(a, ts + cc, masked, valid, j, pos.T, pos.q0, row0 + cc, v);
+              tmem_ld16(tmem_o + lanes + c0 + cc, v);
 #pragma unroll
-              for (int e = 0; e < 16; e++) {
-                float m = v[e];
-#pragma unroll
-                for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-                if (lane == e) scr[quarter * CW + cc + e] = m;
-              }
+              for (int e = 0; e < 16; e++)
+                if (cc + e < cols) v[e] *= fac[cc + e];
+              tmem_st16(tmem_o + lanes + c0 + cc, v);
             }
-            named_sync(bar, 128);
-            if (wt < cols) {
-              const float was = -nb[wt];
-              const float m = fmaxf(fmaxf(scr[wt], scr[CW + wt]), fmaxf(scr[2 * CW + wt], scr[3 * CW + wt]));
-              const float now = fmaxf(was, m);
-              scr[4 * CW + wt] = ex2(was - now);
-              nb[wt] = -now;
-            }
-            named_sync(bar, 128);
-            const float *fac = scr + 4 * CW;
-#pragma unroll
-            for (int e = 0; e < 32; e++) {
-              const int col = CW == 32 ? e : (e >> 3) * 16 + (lane & 1) * 8 + (e & 7);
-              if (col < cols) l[e] *= fac[col];
-            }
-            if (t > t0) {
-#pragma unroll 1
-              for (int cc = 0; cc < cols; cc += 16) {
-                float v[16];
-                tmem_ld16(tmem_o + lanes + c0 + cc, v);
-#pragma unroll
-                for (int e = 0; e < 16; e++) v[e] *= fac[cc + e];
-                tmem_st16(tmem_o + lanes + c0 + cc, v);
-              }
-            }
-            named_sync(bar, 128);  // the factors are read before P replaces them
           }
-        } else if (sc >= (uint32_t)p.PB && ok) {
+          named_sync(bar, 128);  // the factors are read before P replaces them
+          if constexpr (kKeep) {
+#pragma unroll
+            for (int hf = 0; hf < 2; hf++) {
+              uint32_t z[4 * NB];
+              tmem_frag<NB>(ts + ((uint32_t)(16 * hf) << 16), z);
+              tmem_wait(z);
+              tree_exponents<NB>(z, zs2, nbr, masked, see[hf], x[hf]);
+            }
+          }
+        } else if (sc >= (uint32_t)p.PB) {
           const uint32_t u = sc - p.PB;  // P's buffer is free
           ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.pvdone + (u & 1)), (u >> 1) & 1,
                                                          sm.failed));
         }
         // pass 2: the weights
         if (ok) {
-          const uint32_t pbase = smem_u32(sm.p) + (sc % p.PB) * p_bytes + key * 128;
+          const uint32_t pbase = smem_u32(sm.p) + (sc % p.PB) * p_bytes;
 #pragma unroll
-          for (int cc = 0; cc < CW; cc += 16) {
-            if (cc >= cols) break;
-            float v[16];
-            tree_logits16(a, ts + cc, masked, valid, j, pos.T, pos.q0, row0 + cc, v);
-            uint32_t w[8];
-#pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-              const float4 n4 = *reinterpret_cast<const float4 *>(nb + cc + e);
-              v[e] = ex2(v[e] + n4.x);
-              v[e + 1] = ex2(v[e + 1] + n4.y);
-              v[e + 2] = ex2(v[e + 2] + n4.z);
-              v[e + 3] = ex2(v[e + 3] + n4.w);
-              w[e / 2] = pack_bf16x2(v[e], v[e + 1]);
-              w[e / 2 + 1] = pack_bf16x2(v[e + 2], v[e + 3]);
+          for (int hf = 0; hf < 2; hf++) {
+            float *w = x[kKeep ? hf : 0];
+            if constexpr (!kKeep) {
+              uint32_t z[4 * NB];
+              tmem_frag<NB>(ts + ((uint32_t)(16 * hf) << 16), z);
+              tmem_wait(z);
+              tree_exponents<NB>(z, zs2, nbr, masked, see[hf], x[0]);
             }
-            if (CW == 32) {
 #pragma unroll
-              for (int e = 0; e < 16; e++) l[(cc + e) % 32] += v[e];
-            } else {
+            for (int k = 0; k < NB; k++) {
 #pragma unroll
-              for (int e = 0; e < 8; e++) {
-                const float keep = lane & 1 ? v[8 + e] : v[e], give = lane & 1 ? v[e] : v[8 + e];
-                l[cc / 2 + e] += keep + __shfl_xor_sync(0xFFFFFFFFu, give, 1);
-              }
+              for (int e = 0; e < 4; e++) w[4 * k + e] = ex2(w[4 * k + e]);
+              l[k] = add2(l[k], add2(pk2(w[4 * k], w[4 * k + 1]), pk2(w[4 * k + 2], w[4 * k + 3])));
             }
-            const int x = c0 + cc;  // 16 rows = two 16-byte chunks of block x / 64
-            const uint32_t blkp = pbase + (x >> 6) * 16384;
+            const int mk = mkey + hf * 16;
 #pragma unroll
-            for (int u = 0; u < 2; u++)
-              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                               blkp + (((((x & 63) >> 3) + u) ^ (key & 7)) << 4)),
-                           "r"(w[4 * u]), "r"(w[4 * u + 1]), "r"(w[4 * u + 2]), "r"(w[4 * u + 3])
-                           : "memory");
+            for (int k = 0; k < NB; k += 2) {
+              const int cb = (c0 >> 3) + k + (lane >> 4);  // this lane's 8-row block
+              stsm4(pbase + (cb >> 3) * 16384 + mk * 128 + (((cb & 7) ^ (mk & 7)) << 4),
+                    pack_bf16x2(w[4 * k], w[4 * k + 1]), pack_bf16x2(w[4 * k + 2], w[4 * k + 3]),
+                    pack_bf16x2(w[4 * k + 4], w[4 * k + 5]), pack_bf16x2(w[4 * k + 6], w[4 * k + 7]));
+            }
           }
+        } else {
+          *sm.failed = 1;
         }
         tc_fence_before();
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -1037,20 +1157,24 @@ k_tree_tc(TreeArgs a, TreeTc p) {
       if (!ok) break;
       tc_fence_after();
       // (P is free: its last product is done)
-      float *scr = CW == 32 ? sm.scr + wg * (6 * CW) : reinterpret_cast<float *>(sm.p + wg * 16384);
 #pragma unroll
-      for (int e = 0; e < 32; e++) {
-        float x = l[e];
+      for (int k = 0; k < NB; k++) {
+        float l0, l1;
+        upk2(l[k], l0, l1);
 #pragma unroll
-        for (int o = 16; o >= (CW == 32 ? 1 : 2); o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
-        const int col = CW == 32 ? e : (e >> 3) * 16 + (lane & 1) * 8 + (e & 7);
-        if (lane < CW / 32) scr[quarter * CW + col] = x;
+        for (int o = 4; o < 32; o <<= 1) {
+          l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, o);
+          l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, o);
+        }
+        if (lane < 4) {
+          scr[quarter * CW + 8 * k + 2 * lane] = l0;
+          scr[quarter * CW + 8 * k + 2 * lane + 1] = l1;
+        }
       }
       named_sync(bar, 128);
       const bool whole = t0 == 0 && t1 == pos.n_kt;
       const int64_t slot = 2 * (int64_t)blockIdx.x + (pos.g != pos.run0);
-      const int real = min(cols, n_rows - c0);
-      if (wt < real) {
+      if (wt < cols) {
         const float sum = (scr[wt] + scr[CW + wt]) + (scr[2 * CW + wt] + scr[3 * CW + wt]);
         const float m = sum > 0.f || sum != sum ? -nb[wt] : -INFINITY;
         const int x = rt * a.rows + c0 + wt;
@@ -1067,7 +1191,7 @@ k_tree_tc(TreeArgs a, TreeTc p) {
       const int d = D == 64 ? key & 63 : key;
       const bool odd = *sm.odd != 0;
 #pragma unroll 1
-      for (int cc = 0; cc < real; cc += 16) {
+      for (int cc = 0; cc < cols; cc += 16) {
         float v[16];
         tmem_ld16(tmem_o + lanes + c0 + cc, v);
         if (odd) {  // infinities and NaN of the nodes this run covered, to the rows that see them
@@ -1089,7 +1213,7 @@ k_tree_tc(TreeArgs a, TreeTc p) {
         }
 #pragma unroll
         for (int e = 0; e < 16; e++) {
-          if (cc + e >= real || (D == 64 && key >= 64)) continue;
+          if (cc + e >= cols || (D == 64 && key >= 64)) continue;
           const int x = rt * a.rows + c0 + cc + e;
           const float o = v[e] * fac[cc + e];
           if (whole) {
