@@ -497,6 +497,7 @@ struct TreeTc {
   int NW;      // softmax warpgroups
   int NS;      // ring slots
   int PB, SB;  // P buffers, S buffers
+  int box;     // rows of a TMA box (a divisor of the page size), 0: no TMA
   uint32_t idesc_s, idesc_o;  // without N
 };
 
@@ -507,7 +508,7 @@ struct TreeTcSmem {
   uint64_t *full, *empty, *qfull, *qempty, *sfull, *sfree, *pready, *pvdone, *ofree;
   int64_t *scan;
   uint32_t *tmem_holder;
-  volatile int *failed, *odd;
+  volatile int *failed, *odd, *bad;
   __host__ __device__ static size_t layout(int D, int rows, int NS, int PB, TreeTcSmem *o,
                                            uint8_t *base) {
     size_t at = 0;
@@ -516,7 +517,7 @@ struct TreeTcSmem {
       at += (n + 15) & ~size_t(15);
       return base + x;
     };
-    uint8_t *p = take((size_t)PB * ((rows + 63) / 64) * 16384);
+    uint8_t *p = take((size_t)PB * rows * (kTtKeys * 2));
     uint8_t *ring = take((size_t)NS * kTtKeys * D * 2), *q = take((size_t)rows * D * 2);
     uint8_t *scr = take(rows <= 128 ? (size_t)rows * 24 : 0);
     uint8_t *nb = take((size_t)rows * 4), *bars = take((2 * NS + 11) * 8), *sc = take(66 * 8);
@@ -540,6 +541,7 @@ struct TreeTcSmem {
       o->tmem_holder = reinterpret_cast<uint32_t *>(th);
       o->failed = reinterpret_cast<volatile int *>(th + 4);
       o->odd = reinterpret_cast<volatile int *>(th + 8);
+      o->bad = reinterpret_cast<volatile int *>(th + 12);
     }
     return at;
   }
@@ -629,9 +631,9 @@ __device__ __forceinline__ void tmem_frag<8>(uint32_t taddr, uint32_t (&r)[32]) 
         "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
-__device__ __forceinline__ void stsm4(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2,
+__device__ __forceinline__ void stsm4t(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2,
                                       uint32_t r3) {
-  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
                "r"(r0), "r"(r1), "r"(r2), "r"(r3)
                : "memory");
 }
@@ -657,7 +659,8 @@ __device__ __forceinline__ void tree_exponents(const uint32_t (&z)[4 * NB], uint
 
 template <int D, int CW>
 __global__ void __launch_bounds__(kTtThreads, 1)
-k_tree_tc(TreeArgs a, TreeTc p) {
+k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+          TreeArgs a, TreeTc p) {
   constexpr int CH = D / 8, KB = D / 64;
   constexpr uint32_t kSlot = kTtKeys * D * 2;
   extern __shared__ uint8_t smem_raw[];
@@ -667,12 +670,13 @@ k_tree_tc(TreeArgs a, TreeTc p) {
   TreeTcSmem::layout(D, a.rows, p.NS, p.PB, &sm, base);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nsw = p.NW * 4;  // softmax warps
-  const uint32_t p_bytes = (uint32_t)((a.rows + 63) / 64) * 16384u;
+  const uint32_t p_bytes = (uint32_t)a.rows * (kTtKeys * 2);
 
   asm volatile("griddepcontrol.launch_dependents;");
   if (tid == 0) {
     *sm.failed = 0;
     *sm.odd = 0;
+    *sm.bad = 0;
     for (int i = 0; i < p.NS; i++) {
       mbar_init(smem_u32(sm.full + i), kTtProd * 32);
       mbar_init(smem_u32(sm.empty + i), 1);
@@ -778,15 +782,45 @@ k_tree_tc(TreeArgs a, TreeTc p) {
           vs[u] = ks[u];
           ks[u] = -1;
           if (pp < end) {
-            if (blk[u] >= 0 && blk[u] < n_blocks) ks[u] = blk[u] * a.BS + pp % a.BS;
-            else record_error(a.status, KVC_ERR_BOUNDS);
+            if (blk[u] >= 0 && blk[u] < n_blocks) {
+              ks[u] = blk[u] * a.BS + pp % a.BS;
+            } else {
+              *sm.bad = 1;  // (read by the softmax warps after this stage's product)
+              record_error(a.status, KVC_ERR_BOUNDS);
+            }
           }
         }
       };
-      auto load = [&](const uint16_t *pool, const int32_t (&slot)[NU]) {
+      // One stage: TMA boxes of whole page rows where every key of the warp's
+      // blocks is cached, else row by row with cp.async (zeros past the end).
+      auto load = [&](const uint16_t *pool, const CUtensorMap *tm, int t, const int32_t (&slot)[NU]) {
         const int st = rc % p.NS;
         if (!(ok = acquire(sm.empty + st, ((rc / p.NS) & 1) ^ 1))) return;
-        const uint32_t dst = smem_u32(sm.ring) + st * kSlot + (col >> 3) * (kTtKeys * 128);
+        const uint32_t slot0 = smem_u32(sm.ring) + st * kSlot;
+        bool whole = p.box > 0 && (t + 1) * kTtKeys <= pos.c;
+        if (whole) {
+#pragma unroll
+          for (int u = 0; u < NU; u++) whole &= __all_sync(0xFFFFFFFFu, slot[u] >= 0);
+        }
+        if (whole) {
+          const uint32_t bar = smem_u32(sm.full + st);
+          if (lane == 0) mbar_expect_tx(bar, kSlot / kTtProd);
+          else mbar_arrive(bar);
+          __syncwarp();
+          if (lane % p.box == 0)  // a box's first key
+#pragma unroll
+            for (int u = 0; u < NU; u++)
+#pragma unroll
+              for (int kb = 0; kb < KB; kb++)
+                tma_load_3d(slot0 + kb * (kTtKeys * 128) +
+                                (pw * 32 + u * (32 * kTtProd) + lane) * 128,
+                            tm, kb * 64, h, slot[u], bar);
+          __syncwarp();
+          flush();  // (the run's queries, if they are still in flight)
+          rc++;
+          return;
+        }
+        const uint32_t dst = slot0 + (col >> 3) * (kTtKeys * 128);
 #pragma unroll
         for (int u = 0; u < NU; u++)
 #pragma unroll
@@ -803,7 +837,7 @@ k_tree_tc(TreeArgs a, TreeTc p) {
       auto load_v = [&](int t, const int32_t (&slot)[NU]) {
         const uint32_t dst =
             smem_u32(sm.ring) + (rc % p.NS) * kSlot + (col >> 3) * (kTtKeys * 128);
-        load(a.vpool, slot);
+        load(a.vpool, &tm_v, t, slot);
         if (!ok || (t + 1) * kTtKeys <= pos.c) return;
         // A node's V may hold infinities or NaN that some rows do not see: the
         // product gets zeros in their place, and the run's end adds them to
@@ -857,12 +891,12 @@ k_tree_tc(TreeArgs a, TreeTc p) {
       fetch(pos.t0);
       resolve(pos.t0);
       fetch(pos.t0 + 1);
-      load(a.kpool, ks);
+      load(a.kpool, &tm_k, pos.t0, ks);
       if (ok) load_q();
       for (int t = pos.t0 + 1; t < t1 && ok; t++) {
         resolve(t);
         fetch(t + 1);
-        load(a.kpool, ks);
+        load(a.kpool, &tm_k, t, ks);
         if (ok) load_v(t - 1, vs);
       }
       if (ok) load_v(t1 - 1, ks);
@@ -914,7 +948,8 @@ k_tree_tc(TreeArgs a, TreeTc p) {
 #pragma unroll
           for (int kk = 0; kk < kTtKeys / 16; kk++)
             mma_bf16(tmem_o, smem_desc_mn(vb + kk * 2048, KB == 2 ? kTtKeys * 128 : 0),
-                     smem_desc_mn(pb + kk * 2048, 16384), p.idesc_o | nbits, !first || kk > 0);
+                     smem_desc(pb + (kk >> 2) * (a.rows * 128) + (kk & 3) * 32), p.idesc_o | nbits,
+                     !first || kk > 0);
           mma_commit(smem_u32(sm.pvdone + (vc & 1)));
           mma_commit(smem_u32(sm.empty + rc % p.NS));
           rc++;
@@ -943,11 +978,13 @@ k_tree_tc(TreeArgs a, TreeTc p) {
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
     const int key = quarter * 32 + lane;
     float *nb = sm.nb + c0;
-    float *scr = CW == 32 ? sm.scr + wg * (6 * CW) : reinterpret_cast<float *>(sm.p + wg * 16384);
+    float *scr = CW == 32 ? sm.scr + wg * (6 * CW) : reinterpret_cast<float *>(sm.p + c0 * 128);
     const uint64_t zs2 = pk2(a.zscale, a.zscale);
     const int64_t n_blocks = a.n_slots / a.BS;
-    // stmatrix: this lane's row address, matrices (keys 0–7 | 8–15) × (block k | k + 1)
-    const int mkey = quarter * 32 + ((lane >> 3) & 1) * 8 + (lane & 7);
+    // stmatrix (transposing): matrices (keys 0–7 | 8–15) × (block k | k + 1);
+    // this lane's query row of block 0, and its chunk of eight keys
+    const int mrow = c0 + (lane >> 4) * 8 + (lane & 7);
+    const int mchunk = quarter * 4 + ((lane >> 3) & 1);
     uint32_t sc = 0, qc = 0;  // tiles and runs done
     while (pos.g < pos.run1 && ok) {
       const int t0 = pos.t0, t1 = pos.t1(), h = pos.h(), rt = pos.rt(), n_rows = pos.rows(a);
@@ -963,20 +1000,24 @@ k_tree_tc(TreeArgs a, TreeTc p) {
         nbr[k] = pk2(x < cols ? -kUnset : -INFINITY, x + 1 < cols ? -kUnset : -INFINITY);
         l[k] = 0;
       }
-      int32_t blk = 0;
-      if (t0 * kTtKeys + key < end) blk = bt[(t0 * kTtKeys + key) / a.BS];
       // A wait that gives up only clears this warp's `ok`; the warpgroup leaves
       // together, at the next vote.
       for (int t = t0; t < t1; t++, sc++) {
-        const int pp = t * kTtKeys + key;
-        const bool valid = pp < end && blk >= 0 && blk < n_blocks;
-        int32_t blk_next = 0;
-        if (t + 1 < t1 && pp + kTtKeys < end) blk_next = bt[(pp + kTtKeys) / a.BS];
-        // (warp-uniform) a tile with nodes, past the end, or with a bad block
-        const uint32_t valid_keys = __ballot_sync(0xFFFFFFFFu, valid);
-        const bool masked = __any_sync(0xFFFFFFFFu, !valid || pp >= pos.c);
+        const int b = sc % p.SB;
+        ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.sfull + b),
+                                                             (sc / p.SB) & 1, sm.failed));
+        tc_fence_after();
+        // a tile with nodes, past the end, or (after some bad block) any tile
         uint32_t see[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+        const bool masked = (t + 1) * kTtKeys > pos.c || *sm.bad;
         if (masked) {
+          const int pp = t * kTtKeys + key;
+          bool valid = pp < end;
+          if (valid) {
+            const int32_t blk = bt[pp / a.BS];
+            valid = blk >= 0 && blk < n_blocks;
+          }
+          const uint32_t valid_keys = __ballot_sync(0xFFFFFFFFu, valid);
           see[0] = see[1] = 0;
 #pragma unroll 1
           for (int e = 0; e < 8 * NB; e++) {
@@ -993,10 +1034,6 @@ k_tree_tc(TreeArgs a, TreeTc p) {
             else see[1] |= bit;
           }
         }
-        const int b = sc % p.SB;
-        ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.sfull + b),
-                                                             (sc / p.SB) & 1, sm.failed));
-        tc_fence_after();
         const uint32_t ts = tmem + lanes + b * a.rows + c0;
         // pass 1: does some logit pass its row's reference by too much?
         float top = -INFINITY;
@@ -1127,14 +1164,15 @@ k_tree_tc(TreeArgs a, TreeTc p) {
               for (int e = 0; e < 4; e++) w[4 * k + e] = ex2(w[4 * k + e]);
               l[k] = add2(l[k], add2(pk2(w[4 * k], w[4 * k + 1]), pk2(w[4 * k + 2], w[4 * k + 3])));
             }
-            const int mk = mkey + hf * 16;
+            const int ch = mchunk + hf * 2;
+            const uint32_t pa = pbase + (ch >> 3) * (a.rows * 128) + mrow * 128 +
+                                (((ch & 7) ^ (mrow & 7)) << 4);
 #pragma unroll
-            for (int k = 0; k < NB; k += 2) {
-              const int cb = (c0 >> 3) + k + (lane >> 4);  // this lane's 8-row block
-              stsm4(pbase + (cb >> 3) * 16384 + mk * 128 + (((cb & 7) ^ (mk & 7)) << 4),
-                    pack_bf16x2(w[4 * k], w[4 * k + 1]), pack_bf16x2(w[4 * k + 2], w[4 * k + 3]),
-                    pack_bf16x2(w[4 * k + 4], w[4 * k + 5]), pack_bf16x2(w[4 * k + 6], w[4 * k + 7]));
-            }
+            for (int k = 0; k < NB; k += 2)
+              if (8 * k < cols)
+                stsm4t(pa + k * 1024,
+                       pack_bf16x2(w[4 * k], w[4 * k + 1]), pack_bf16x2(w[4 * k + 2], w[4 * k + 3]),
+                       pack_bf16x2(w[4 * k + 4], w[4 * k + 5]), pack_bf16x2(w[4 * k + 6], w[4 * k + 7]));
           }
         } else {
           *sm.failed = 1;
@@ -1146,7 +1184,6 @@ k_tree_tc(TreeArgs a, TreeTc p) {
           mbar_arrive(smem_u32(sm.sfree + b));
           mbar_arrive(smem_u32(sm.pready + (sc & 1)));
         }
-        blk = blk_next;
       }
       // ---- the run's result: sums over the key lanes, then O
       const uint32_t pv = sc - 1;
@@ -1242,7 +1279,11 @@ k_tree_tc(TreeArgs a, TreeTc p) {
   __syncthreads();
   if (*sm.failed && tid == 0) {
     record_error(a.status, KVC_ERR_TIMEOUT);
-    // let this CTA's products finish before its memory is released
+    // let this CTA's copies and products finish before its memory is released
+    for (int i = 0; i < p.NS; i++) {
+      mbar_drain(smem_u32(sm.full + i), 0);
+      mbar_drain(smem_u32(sm.full + i), 1);
+    }
     for (int i = 0; i < 2; i++) {
       mbar_drain(smem_u32(sm.sfull + i), 0);
       mbar_drain(smem_u32(sm.sfull + i), 1);
@@ -1339,6 +1380,18 @@ void tree_plan(int n_req, int max_blocks, int max_tree, int H, int Hq, int D, in
   n_cta = (int)std::min<int64_t>((tc ? 1 : 2) * device_sm_count(), most);
 }
 
+// Boxes of `box` consecutive slots of one head, 64 columns, 128-byte swizzle.
+bool pool_map(CUtensorMap *m, const void *pool, int64_t n_slots, int H, int D, int box) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)n_slots};
+  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)H * D * 2};
+  cuuint32_t bx[3] = {64, 1, (cuuint32_t)box}, es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(pool), dims, strides, bx, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, int CW>
 cudaError_t launch_tc(const TreeArgs &a, cudaStream_t s) {
   constexpr size_t kSmemMax = 232448;
@@ -1348,13 +1401,18 @@ cudaError_t launch_tc(const TreeArgs &a, cudaStream_t s) {
   p.SB = 3 * a.rows <= 512 ? 2 : 1;
   for (p.NS = 8; p.NS > 3; p.NS--)
     if (1024 + TreeTcSmem::layout(D, a.rows, p.NS, p.PB, nullptr, nullptr) <= kSmemMax) break;
+  CUtensorMap tm_k{}, tm_v{};
+  p.box = a.BS % 32 == 0 ? 32 : a.BS % 16 == 0 ? 16 : a.BS % 8 == 0 ? 8 : 0;
+  if (p.box && !(pool_map(&tm_k, a.kpool, a.n_slots, a.H, D, p.box) &&
+                 pool_map(&tm_v, a.vpool, a.n_slots, a.H, D, p.box)))
+    return cudaErrorUnknown;
   p.idesc_s = make_idesc(128, 0);
-  p.idesc_o = make_idesc(128, 0) | (1u << 15) | (1u << 16);  // V and P MN-major
+  p.idesc_o = make_idesc(128, 0) | (1u << 15);  // A (V) MN-major
   const size_t smem = 1024 + TreeTcSmem::layout(D, a.rows, p.NS, p.PB, nullptr, nullptr);
   cudaError_t e = cudaFuncSetAttribute(k_tree_tc<D, CW>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  k_tree_tc<D, CW><<<a.n_cta, (p.NW * 4 + kTtProd + 1) * 32, smem, s>>>(a, p);
+  k_tree_tc<D, CW><<<a.n_cta, (p.NW * 4 + kTtProd + 1) * 32, smem, s>>>(tm_k, tm_v, a, p);
   return cudaGetLastError();
 }
 
