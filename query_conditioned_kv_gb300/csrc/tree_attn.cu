@@ -52,7 +52,8 @@ struct TreeArgs {
   float *part_o;    // [2·grid][rows][D]
   int64_t n_slots;
   int max_blocks, mask_words, n_req, n_q, max_tree, H, Hq, G, BS;
-  int rows;      // rows per row tile
+  int rows;      // rows of a row tile's buffers
+  int rstep;     // rows of a row tile (whole nodes where the tile holds several)
   int tile;      // keys per tile
   int n_cta;     // CTAs the tiles are dealt out to
   float zscale;  // scale·log2(e)
@@ -73,7 +74,7 @@ __device__ __forceinline__ void tree_tiles(const TreeArgs &a, int r, int &n_rt, 
   int c, q0, T;
   n_rt = n_kt = 0;
   if (!tree_request(a, r, c, q0, T)) return;
-  n_rt = (T * a.G + a.rows - 1) / a.rows;
+  n_rt = (T * a.G + a.rstep - 1) / a.rstep;
   n_kt = (c + T + a.tile - 1) / a.tile;
 }
 
@@ -177,7 +178,7 @@ k_tree_rows(TreeArgs a) {
   while (g < run1) {
     const int h = unit / n_rt, rt = unit % n_rt;
     const int t1 = (int)min((int64_t)n_kt, t0 + (run1 - g));
-    const int n_rows = min(R, T * a.G - rt * R);
+    const int n_rows = min(a.rstep, T * a.G - rt * a.rstep);
     const int32_t *bt = a.block_table + (int64_t)r * a.max_blocks;
     const int end = c + T;
 
@@ -213,7 +214,7 @@ k_tree_rows(TreeArgs a) {
     }
     // the row tile's queries
     for (int e = tid; e < R * CH; e += kRowThreads) {
-      const int row = e / CH, col = e % CH, x = rt * R + row;
+      const int row = e / CH, col = e % CH, x = rt * a.rstep + row;
       uint4 v = make_uint4(0, 0, 0, 0);
       if (row < n_rows)
         v = *reinterpret_cast<const uint4 *>(
@@ -285,7 +286,7 @@ k_tree_rows(TreeArgs a) {
         if (masked) {  // warp-uniform
 #pragma unroll
           for (int hf = 0; hf < 2; hf++) {
-            const int x = rt * R + mt * 16 + hf * 8 + lane / 4;
+            const int x = rt * a.rstep + mt * 16 + hf * 8 + lane / 4;
             uint32_t vis = 0;
             if (x < T * a.G) vis = visible_bits<KT>(a, x / a.G, q0, c, T, p0) & okb;
 #pragma unroll
@@ -435,7 +436,7 @@ k_tree_rows(TreeArgs a) {
         acc.w = fmaf(v.w, f, acc.w);
       }
       if (whole) {
-        const int x = rt * R + row;
+        const int x = rt * a.rstep + row;
         const int64_t qr = (int64_t)(q0 + x / a.G) * a.Hq + h * a.G + x % a.G;
         const float inv = mx == -INFINITY ? 0.f : 1.f / sum;
         uint2 w2 = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
@@ -498,52 +499,33 @@ struct TreeTc {
   int NS;      // ring slots
   int PB, SB;  // P buffers, S buffers
   int box;     // rows of a TMA box (a divisor of the page size), 0: no TMA
+  int q_nodes; // nodes of a row tile
   uint32_t idesc_s, idesc_o;  // without N
 };
 
+constexpr int kTtSlots = 8;  // ring slots, at most
+
+// Head of the dynamic shared memory, at fixed offsets (few live registers);
+// then the scratch of the warpgroups of 32 rows, P, the ring and q.
+struct TreeTcHead {
+  uint64_t full[kTtSlots], empty[kTtSlots], qfull, qempty;
+  uint64_t sfull[2], sfree[2], pready[2], pvdone[2], ofree;
+  int64_t scan[66];
+  uint32_t tmem_holder;
+  volatile int failed, odd, bad;
+  float nb[256];  // −reference per row
+};
+constexpr uint32_t kTtHead = 2048;
+static_assert(sizeof(TreeTcHead) <= kTtHead, "the head's room");
+
+// Byte offsets (multiples of 1024) from the head.
 struct TreeTcSmem {
-  uint8_t *q, *p, *ring;
-  float *nb;   // −reference per row
-  float *scr;  // [4 + 2][32] per warpgroup of 32 rows; warpgroups of 64 rows use their block of P
-  uint64_t *full, *empty, *qfull, *qempty, *sfull, *sfree, *pready, *pvdone, *ofree;
-  int64_t *scan;
-  uint32_t *tmem_holder;
-  volatile int *failed, *odd, *bad;
-  __host__ __device__ static size_t layout(int D, int rows, int NS, int PB, TreeTcSmem *o,
-                                           uint8_t *base) {
-    size_t at = 0;
-    auto take = [&](size_t n) {
-      const size_t x = at;
-      at += (n + 15) & ~size_t(15);
-      return base + x;
-    };
-    uint8_t *p = take((size_t)PB * rows * (kTtKeys * 2));
-    uint8_t *ring = take((size_t)NS * kTtKeys * D * 2), *q = take((size_t)rows * D * 2);
-    uint8_t *scr = take(rows <= 128 ? (size_t)rows * 24 : 0);
-    uint8_t *nb = take((size_t)rows * 4), *bars = take((2 * NS + 11) * 8), *sc = take(66 * 8);
-    uint8_t *th = take(16);
-    if (o) {
-      o->p = p;
-      o->ring = ring;
-      o->q = q;
-      o->nb = reinterpret_cast<float *>(nb);
-      o->scr = reinterpret_cast<float *>(scr);
-      o->full = reinterpret_cast<uint64_t *>(bars);
-      o->empty = o->full + NS;
-      o->qfull = o->empty + NS;
-      o->qempty = o->qfull + 1;
-      o->sfull = o->qempty + 1;
-      o->sfree = o->sfull + 2;
-      o->pready = o->sfree + 2;
-      o->pvdone = o->pready + 2;
-      o->ofree = o->pvdone + 2;
-      o->scan = reinterpret_cast<int64_t *>(sc);
-      o->tmem_holder = reinterpret_cast<uint32_t *>(th);
-      o->failed = reinterpret_cast<volatile int *>(th + 4);
-      o->odd = reinterpret_cast<volatile int *>(th + 8);
-      o->bad = reinterpret_cast<volatile int *>(th + 12);
-    }
-    return at;
+  uint32_t p, ring, q, bytes;
+  __host__ __device__ TreeTcSmem(int D, int rows, int NS, int PB) {
+    p = kTtHead + (rows <= 128 ? 128 * 24 : 0);
+    ring = p + PB * rows * (kTtKeys * 2);
+    q = ring + NS * kTtKeys * D * 2;
+    bytes = q + rows * D * 2;
   }
 };
 
@@ -587,7 +569,7 @@ struct TreePos {
   __device__ __forceinline__ int h() const { return unit / n_rt; }
   __device__ __forceinline__ int rt() const { return unit % n_rt; }
   __device__ __forceinline__ int rows(const TreeArgs &a) const {
-    return min(a.rows, T * a.G - rt() * a.rows);
+    return min(a.rstep, T * a.G - rt() * a.rstep);
   }
   __device__ __forceinline__ void next(const TreeArgs &a) {
     const int e = t1();
@@ -638,65 +620,65 @@ __device__ __forceinline__ void stsm4t(uint32_t addr, uint32_t r0, uint32_t r1, 
                : "memory");
 }
 
-// x = z·zscale + nb of one 16-lane half, as pairs of rows (x[2k]: key t/4,
-// x[2k + 1]: key t/4 + 8), −inf where bit 4k + j of `see` is clear.
+// x = z·zscale + nb of one 16-lane half (nb[2k + e]: rows 8k + 2·(t%4) + e),
+// −inf where bit 4k + j of `see` is clear.  Scalar FMAs: the packed form
+// costs more in register moves than it saves.
 template <int NB>
-__device__ __forceinline__ void tree_exponents(const uint32_t (&z)[4 * NB], uint64_t zs2,
-                                               const uint64_t (&nb)[NB], bool masked, uint32_t see,
+__device__ __forceinline__ void tree_exponents(const uint32_t (&z)[4 * NB], float zs,
+                                               const float (&nb)[2 * NB], bool masked, uint32_t see,
                                                float (&x)[4 * NB]) {
 #pragma unroll
-  for (int k = 0; k < NB; k++) {
-    upk2(fma2(pk2(__uint_as_float(z[4 * k]), __uint_as_float(z[4 * k + 1])), zs2, nb[k]), x[4 * k],
-         x[4 * k + 1]);
-    upk2(fma2(pk2(__uint_as_float(z[4 * k + 2]), __uint_as_float(z[4 * k + 3])), zs2, nb[k]),
-         x[4 * k + 2], x[4 * k + 3]);
-  }
-  if (masked)
+  for (int e = 0; e < 4 * NB; e++)
+    x[e] = fmaf(__uint_as_float(z[e]), zs, nb[(e >> 2) * 2 + (e & 1)]);
+  if (masked) {
+    asm volatile("");  // a branch, not 4·NB selects in every tile
 #pragma unroll
     for (int e = 0; e < 4 * NB; e++)
       if (!((see >> e) & 1u)) x[e] = -INFINITY;
+  }
 }
 
 template <int D, int CW>
 __global__ void __launch_bounds__(kTtThreads, 1)
 k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-          TreeArgs a, TreeTc p) {
+          const __grid_constant__ CUtensorMap tm_q, TreeArgs a, TreeTc p) {
   constexpr int CH = D / 8, KB = D / 64;
   constexpr uint32_t kSlot = kTtKeys * D * 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  TreeTcSmem sm;
-  TreeTcSmem::layout(D, a.rows, p.NS, p.PB, &sm, base);
+  TreeTcHead &sm = *reinterpret_cast<TreeTcHead *>(base);
+  const TreeTcSmem at(D, a.rows, p.NS, p.PB);
+  const uint32_t base_u = smem_u32(base);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nsw = p.NW * 4;  // softmax warps
   const uint32_t p_bytes = (uint32_t)a.rows * (kTtKeys * 2);
 
   asm volatile("griddepcontrol.launch_dependents;");
   if (tid == 0) {
-    *sm.failed = 0;
-    *sm.odd = 0;
-    *sm.bad = 0;
+    sm.failed = 0;
+    sm.odd = 0;
+    sm.bad = 0;
     for (int i = 0; i < p.NS; i++) {
       mbar_init(smem_u32(sm.full + i), kTtProd * 32);
       mbar_init(smem_u32(sm.empty + i), 1);
     }
-    mbar_init(smem_u32(sm.qfull), kTtProd * 32);
-    mbar_init(smem_u32(sm.qempty), 1);
+    mbar_init(smem_u32(&sm.qfull), 1);
+    mbar_init(smem_u32(&sm.qempty), 1);
     for (int i = 0; i < 2; i++) {
       mbar_init(smem_u32(sm.sfull + i), 1);
       mbar_init(smem_u32(sm.sfree + i), nsw);
       mbar_init(smem_u32(sm.pready + i), nsw);
       mbar_init(smem_u32(sm.pvdone + i), 1);
     }
-    mbar_init(smem_u32(sm.ofree), nsw);
+    mbar_init(smem_u32(&sm.ofree), nsw);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == nsw + kTtProd) alloc_tmem_cols(sm.tmem_holder, 512);
+  if (warp == nsw + kTtProd) alloc_tmem_cols(&sm.tmem_holder, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *sm.tmem_holder;
+  const uint32_t tmem = sm.tmem_holder;
   const uint32_t tmem_o = tmem + p.SB * a.rows;
 
   if (blockIdx.x == 0)  // one report per bad request
@@ -718,7 +700,7 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
     pos.init(a, before);
   }
 
-  bool ok = true;
+bool ok = true;
   if (warp >= nsw && warp < nsw + kTtProd) {
     // ------------------------------------------------------- producers
     const int pw = warp - nsw;
@@ -748,7 +730,7 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
     auto acquire = [&](uint64_t *bar, uint32_t parity) {
       if (mbar_try(smem_u32(bar), parity)) return true;
       flush();
-      return mbar_wait_bounded(smem_u32(bar), parity, sm.failed);
+      return mbar_wait_bounded(smem_u32(bar), parity, &sm.failed);
     };
     auto committed = [&](uint64_t *bar) {
       cp_commit();
@@ -785,7 +767,7 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
             if (blk[u] >= 0 && blk[u] < n_blocks) {
               ks[u] = blk[u] * a.BS + pp % a.BS;
             } else {
-              *sm.bad = 1;  // (read by the softmax warps after this stage's product)
+              sm.bad = 1;  // (read by the softmax warps after this stage's product)
               record_error(a.status, KVC_ERR_BOUNDS);
             }
           }
@@ -796,7 +778,7 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
       auto load = [&](const uint16_t *pool, const CUtensorMap *tm, int t, const int32_t (&slot)[NU]) {
         const int st = rc % p.NS;
         if (!(ok = acquire(sm.empty + st, ((rc / p.NS) & 1) ^ 1))) return;
-        const uint32_t slot0 = smem_u32(sm.ring) + st * kSlot;
+        const uint32_t slot0 = (base_u + at.ring) + st * kSlot;
         bool whole = p.box > 0 && (t + 1) * kTtKeys <= pos.c;
         if (whole) {
 #pragma unroll
@@ -816,7 +798,7 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
                                 (pw * 32 + u * (32 * kTtProd) + lane) * 128,
                             tm, kb * 64, h, slot[u], bar);
           __syncwarp();
-          flush();  // (the run's queries, if they are still in flight)
+          flush();  // (a stage copied row by row may still be in flight)
           rc++;
           return;
         }
@@ -836,7 +818,7 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
       };
       auto load_v = [&](int t, const int32_t (&slot)[NU]) {
         const uint32_t dst =
-            smem_u32(sm.ring) + (rc % p.NS) * kSlot + (col >> 3) * (kTtKeys * 128);
+            (base_u + at.ring) + (rc % p.NS) * kSlot + (col >> 3) * (kTtKeys * 128);
         load(a.vpool, &tm_v, t, slot);
         if (!ok || (t + 1) * kTtKeys <= pos.c) return;
         // A node's V may hold infinities or NaN that some rows do not see: the
@@ -869,23 +851,22 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
                          : "memory");
           }
         }
-        if (odd) *sm.odd = 1;
+        if (odd) sm.odd = 1;
         flush();
       };
+      // the row tile's queries, in one box of nodes × heads of the group; rows
+      // past the request's own (another request's, or zeros) are columns that
+      // the softmax leaves out
       auto load_q = [&]() {
-        if (!(ok = acquire(sm.qempty, (qc & 1) ^ 1))) return;
-        for (int b = pw * 8; b < a.rows; b += kTtProd * 8)
+        if (!(ok = acquire(&sm.qempty, (qc & 1) ^ 1))) return;
+        if (pw == 0 && lane == 0) {
+          const uint32_t bar = smem_u32(&sm.qfull);
+          mbar_expect_tx(bar, p.q_nodes * a.G * D * 2);
 #pragma unroll
-          for (int i = 0; i < 8 / RPI; i++) {
-            const int row = b + i * RPI + lane / CH, x = rt * a.rows + row;
-            const bool on = row < n_rows;
-            cp_async16(smem_u32(sm.q) + (col >> 3) * (a.rows * 128) + row * 128 +
-                           (((col & 7) ^ (row & 7)) << 4),
-                       on ? a.q + ((int64_t)(pos.q0 + x / a.G) * a.Hq + h * a.G + x % a.G) * D + col * 8
-                          : a.q,
-                       on);
-          }
-        committed(sm.qfull);
+          for (int kb = 0; kb < KB; kb++)
+            tma_load_3d((base_u + at.q) + kb * (a.rows * 128), &tm_q, kb * 64, h * a.G,
+                        pos.q0 + rt * p.q_nodes, bar);
+        }
         qc++;
       };
       fetch(pos.t0);
@@ -904,7 +885,7 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
     }
     flush();
     cp_wait<0>();
-    if (!ok) *sm.failed = 1;
+    if (!ok) sm.failed = 1;
   } else if (warp == nsw + kTtProd) {
     // ------------------------------------------------------ MMA issuer
     if (lane == 0) {
@@ -913,16 +894,16 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
         const int t0 = pos.t0, t1 = pos.t1(), n_rows = pos.rows(a);
         const uint32_t nbits = (uint32_t)((n_rows + 15) / 16 * 2) << 17;  // N / 8
         auto wait_slot = [&]() {
-          const bool r = mbar_wait_bounded(smem_u32(sm.full + rc % p.NS), (rc / p.NS) & 1, sm.failed);
+          const bool r = mbar_wait_bounded(smem_u32(sm.full + rc % p.NS), (rc / p.NS) & 1, &sm.failed);
           return r;
         };
         auto issue_s = [&](bool last) {
           const int b = sc % p.SB;
           if (!(ok = wait_slot())) return;
-          if (!(ok = mbar_wait_bounded(smem_u32(sm.sfree + b), ((sc / p.SB) & 1) ^ 1, sm.failed)))
+          if (!(ok = mbar_wait_bounded(smem_u32(sm.sfree + b), ((sc / p.SB) & 1) ^ 1, &sm.failed)))
             return;
           tc_fence_after();
-          const uint32_t kb = smem_u32(sm.ring) + (rc % p.NS) * kSlot, qb = smem_u32(sm.q);
+          const uint32_t kb = (base_u + at.ring) + (rc % p.NS) * kSlot, qb = (base_u + at.q);
 #pragma unroll
           for (int kk = 0; kk < 4 * KB; kk++)
             mma_bf16(tmem + b * a.rows,
@@ -931,20 +912,20 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
                      kk > 0);
           mma_commit(smem_u32(sm.sfull + b));
           mma_commit(smem_u32(sm.empty + rc % p.NS));
-          if (last) mma_commit(smem_u32(sm.qempty));
+          if (last) mma_commit(smem_u32(&sm.qempty));
           rc++;
           sc++;
         };
         auto issue_pv = [&](bool first) {
           if (!(ok = wait_slot())) return;
           if (first &&  // O's previous contents have been read
-              !(ok = mbar_wait_bounded(smem_u32(sm.ofree), (qc & 1) ^ 1, sm.failed)))
+              !(ok = mbar_wait_bounded(smem_u32(&sm.ofree), (qc & 1) ^ 1, &sm.failed)))
             return;
-          if (!(ok = mbar_wait_bounded(smem_u32(sm.pready + (vc & 1)), (vc >> 1) & 1, sm.failed)))
+          if (!(ok = mbar_wait_bounded(smem_u32(sm.pready + (vc & 1)), (vc >> 1) & 1, &sm.failed)))
             return;
           tc_fence_after();
-          const uint32_t vb = smem_u32(sm.ring) + (rc % p.NS) * kSlot;
-          const uint32_t pb = smem_u32(sm.p) + (vc % p.PB) * p_bytes;
+          const uint32_t vb = (base_u + at.ring) + (rc % p.NS) * kSlot;
+          const uint32_t pb = (base_u + at.p) + (vc % p.PB) * p_bytes;
 #pragma unroll
           for (int kk = 0; kk < kTtKeys / 16; kk++)
             mma_bf16(tmem_o, smem_desc_mn(vb + kk * 2048, KB == 2 ? kTtKeys * 128 : 0),
@@ -955,7 +936,7 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
           rc++;
           vc++;
         };
-        ok = mbar_wait_bounded(smem_u32(sm.qfull), qc & 1, sm.failed);
+        ok = mbar_wait_bounded(smem_u32(&sm.qfull), qc & 1, &sm.failed);
         if (ok) issue_s(t1 - t0 == 1);
         for (int t = t0 + 1; t < t1 && ok; t++) {
           issue_s(t == t1 - 1);
@@ -965,7 +946,7 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
         qc++;
         pos.next(a);
       }
-      if (!ok) *sm.failed = 1;
+      if (!ok) sm.failed = 1;
     }
     __syncwarp();
   } else if (warp < nsw) {
@@ -978,8 +959,9 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
     const int key = quarter * 32 + lane;
     float *nb = sm.nb + c0;
-    float *scr = CW == 32 ? sm.scr + wg * (6 * CW) : reinterpret_cast<float *>(sm.p + c0 * 128);
-    const uint64_t zs2 = pk2(a.zscale, a.zscale);
+    float *scr = reinterpret_cast<float *>(CW == 32 ? base + kTtHead + wg * (24 * CW)
+                                               : base + at.p + c0 * 128);
+    const float zs = a.zscale;
     const int64_t n_blocks = a.n_slots / a.BS;
     // stmatrix (transposing): matrices (keys 0–7 | 8–15) × (block k | k + 1);
     // this lane's query row of block 0, and its chunk of eight keys
@@ -993,23 +975,24 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
       const int end = pos.c + pos.T;
       named_sync(bar, 128);                           // the last run's references are read
       if (wt < CW && c0 + wt < a.rows) nb[wt] = -kUnset;
-      uint64_t nbr[NB], l[NB];  // −reference and sum of weights of rows 8k + 2·(t%4) + {0, 1}
+      // −reference and sum of weights of rows 8k + 2·(t%4) + {0, 1}, and the
+      // greatest −reference of them
+      float nbr[2 * NB], l[2 * NB], nb_top = -kUnset;
 #pragma unroll
-      for (int k = 0; k < NB; k++) {
-        const int x = 8 * k + 2 * (lane & 3);
-        nbr[k] = pk2(x < cols ? -kUnset : -INFINITY, x + 1 < cols ? -kUnset : -INFINITY);
-        l[k] = 0;
+      for (int e = 0; e < 2 * NB; e++) {
+        nbr[e] = 8 * (e >> 1) + 2 * (lane & 3) + (e & 1) < cols ? -kUnset : -INFINITY;
+        l[e] = 0.f;
       }
       // A wait that gives up only clears this warp's `ok`; the warpgroup leaves
       // together, at the next vote.
       for (int t = t0; t < t1; t++, sc++) {
         const int b = sc % p.SB;
         ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.sfull + b),
-                                                             (sc / p.SB) & 1, sm.failed));
+                                                             (sc / p.SB) & 1, &sm.failed));
         tc_fence_after();
         // a tile with nodes, past the end, or (after some bad block) any tile
         uint32_t see[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
-        const bool masked = (t + 1) * kTtKeys > pos.c || *sm.bad;
+        const bool masked = (t + 1) * kTtKeys > pos.c || sm.bad;
         if (masked) {
           const int pp = t * kTtKeys + key;
           bool valid = pp < end;
@@ -1023,7 +1006,7 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
           for (int e = 0; e < 8 * NB; e++) {
             const int hf = e / (4 * NB), k = (e >> 2) % NB, kk = hf * 16 + lane / 4 + 8 * ((e >> 1) & 1);
             const int x = c0 + 8 * k + 2 * (lane & 3) + (e & 1);
-            const int j = t * kTtKeys + quarter * 32 + kk - pos.c, i = (rt * a.rows + x) / a.G;
+            const int j = t * kTtKeys + quarter * 32 + kk - pos.c, i = (rt * a.rstep + x) / a.G;
             bool v = (valid_keys >> kk) & 1u;
             if (v && j >= 0)
               v = i < pos.T &&
@@ -1035,30 +1018,42 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
           }
         }
         const uint32_t ts = tmem + lanes + b * a.rows + c0;
-        // pass 1: does some logit pass its row's reference by too much?
+        // Pass 1: does some logit pass its row's reference by too much?  The
+        // greatest logit against the least reference answers for almost every
+        // tile; a tile that this does not clear is looked at row by row.
         float top = -INFINITY;
-        float x[kKeep ? 2 : 1][4 * NB];
-        if (ok) {
+        uint32_t z[kKeep ? 2 : 1][4 * NB];
+        if (ok && cols > 0) {
           if constexpr (kKeep) {
-            uint32_t z[2][4 * NB];
             tmem_frag<NB>(ts, z[0]);
             tmem_frag<NB>(ts + (16u << 16), z[1]);
             tmem_wait(z[0]);
             tmem_wait(z[1]);
 #pragma unroll
-            for (int hf = 0; hf < 2; hf++) tree_exponents<NB>(z[hf], zs2, nbr, masked, see[hf], x[hf]);
-#pragma unroll
-            for (int e = 0; e < 4 * NB; e += 2)
-              top = max3(max3(top, x[0][e], x[0][e + 1]), x[kKeep][e], x[kKeep][e + 1]);
+            for (int e = 0; e < 4 * NB; e++)
+              top = max3(top, __uint_as_float(z[0][e]), __uint_as_float(z[kKeep][e]));
           } else {
-#pragma unroll
+#pragma unroll 1
             for (int hf = 0; hf < 2; hf++) {
-              uint32_t z[4 * NB];
-              tmem_frag<NB>(ts + ((uint32_t)(16 * hf) << 16), z);
-              tmem_wait(z);
-              tree_exponents<NB>(z, zs2, nbr, masked, see[hf], x[0]);
+              tmem_frag<NB>(ts + ((uint32_t)(16 * hf) << 16), z[0]);
+              tmem_wait(z[0]);
 #pragma unroll
-              for (int e = 0; e < 4 * NB; e += 2) top = max3(top, x[0][e], x[0][e + 1]);
+              for (int e = 0; e < 4 * NB; e += 2)
+                top = max3(top, __uint_as_float(z[0][e]), __uint_as_float(z[0][e + 1]));
+            }
+          }
+          top = fmaf(top, zs, nb_top);
+          if (masked || zs < 0.f || __any_sync(0xFFFFFFFFu, !(top <= kExceed))) {
+            top = -INFINITY;
+#pragma unroll 1
+            for (int hf = 0; hf < 2; hf++) {
+              uint32_t y[4 * NB];
+              float x[4 * NB];
+              tmem_frag<NB>(ts + ((uint32_t)(16 * hf) << 16), y);
+              tmem_wait(y);
+              tree_exponents<NB>(y, zs, nbr, masked, see[hf], x);
+#pragma unroll
+              for (int e = 0; e < 4 * NB; e += 2) top = max3(top, x[e], x[e + 1]);
             }
           }
         }
@@ -1068,7 +1063,7 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
           const uint32_t pv = sc - 1;  // the product before this tile's
           if (sc > 0 && ok)
             ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.pvdone + (pv & 1)),
-                                                           (pv >> 1) & 1, sm.failed));
+                                                           (pv >> 1) & 1, &sm.failed));
           // (every product that reads P is done: its memory may serve as scratch)
           ok = named_sync_and(bar, 128, ok);
           if (!ok) break;
@@ -1076,20 +1071,20 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
             float cm[2 * NB];
 #pragma unroll
             for (int e = 0; e < 2 * NB; e++) cm[e] = -INFINITY;
-            uint64_t zero[NB];
+            float zero[2 * NB];
 #pragma unroll
-            for (int k = 0; k < NB; k++) zero[k] = 0;
-#pragma unroll
+            for (int e = 0; e < 2 * NB; e++) zero[e] = 0.f;
+#pragma unroll 1
             for (int hf = 0; hf < 2; hf++) {
-              uint32_t z[4 * NB];
-              float y[4 * NB];
-              tmem_frag<NB>(ts + ((uint32_t)(16 * hf) << 16), z);
-              tmem_wait(z);
-              tree_exponents<NB>(z, zs2, zero, masked, see[hf], y);
+              uint32_t y[4 * NB];
+              float x[4 * NB];
+              tmem_frag<NB>(ts + ((uint32_t)(16 * hf) << 16), y);
+              tmem_wait(y);
+              tree_exponents<NB>(y, zs, zero, masked, see[hf], x);
 #pragma unroll
               for (int k = 0; k < NB; k++) {
-                cm[2 * k] = max3(cm[2 * k], y[4 * k], y[4 * k + 2]);
-                cm[2 * k + 1] = max3(cm[2 * k + 1], y[4 * k + 1], y[4 * k + 3]);
+                cm[2 * k] = max3(cm[2 * k], x[4 * k], x[4 * k + 2]);
+                cm[2 * k + 1] = max3(cm[2 * k + 1], x[4 * k + 1], x[4 * k + 3]);
               }
             }
 #pragma unroll
@@ -1110,15 +1105,15 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
           }
           named_sync(bar, 128);
           const float *fac = scr + 4 * CW;
+          nb_top = -INFINITY;
 #pragma unroll
-          for (int k = 0; k < NB; k++) {
-            const int x0 = 8 * k + 2 * (lane & 3);
-            float l0, l1;
-            upk2(l[k], l0, l1);
-            if (x0 < cols) l0 *= fac[x0];
-            if (x0 + 1 < cols) l1 *= fac[x0 + 1];
-            l[k] = pk2(l0, l1);
-            nbr[k] = pk2(x0 < cols ? nb[x0] : -INFINITY, x0 + 1 < cols ? nb[x0 + 1] : -INFINITY);
+          for (int e = 0; e < 2 * NB; e++) {
+            const int x = 8 * (e >> 1) + 2 * (lane & 3) + (e & 1);
+            if (x < cols) {
+              l[e] *= fac[x];
+              nbr[e] = nb[x];
+              nb_top = fmaxf(nb_top, nbr[e]);
+            }
           }
           if (t > t0) {
 #pragma unroll 1
@@ -1132,37 +1127,23 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
             }
           }
           named_sync(bar, 128);  // the factors are read before P replaces them
-          if constexpr (kKeep) {
-#pragma unroll
-            for (int hf = 0; hf < 2; hf++) {
-              uint32_t z[4 * NB];
-              tmem_frag<NB>(ts + ((uint32_t)(16 * hf) << 16), z);
-              tmem_wait(z);
-              tree_exponents<NB>(z, zs2, nbr, masked, see[hf], x[hf]);
-            }
-          }
         } else if (sc >= (uint32_t)p.PB) {
           const uint32_t u = sc - p.PB;  // P's buffer is free
           ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.pvdone + (u & 1)), (u >> 1) & 1,
-                                                         sm.failed));
+                                                         &sm.failed));
         }
         // pass 2: the weights
         if (ok) {
-          const uint32_t pbase = smem_u32(sm.p) + (sc % p.PB) * p_bytes;
+          const uint32_t pbase = (base_u + at.p) + (sc % p.PB) * p_bytes;
+          auto weights = [&](int hf, const uint32_t (&zz)[4 * NB]) {
+            float w[4 * NB];
+            tree_exponents<NB>(zz, zs, nbr, masked, see[hf], w);
 #pragma unroll
-          for (int hf = 0; hf < 2; hf++) {
-            float *w = x[kKeep ? hf : 0];
-            if constexpr (!kKeep) {
-              uint32_t z[4 * NB];
-              tmem_frag<NB>(ts + ((uint32_t)(16 * hf) << 16), z);
-              tmem_wait(z);
-              tree_exponents<NB>(z, zs2, nbr, masked, see[hf], x[0]);
-            }
+            for (int e = 0; e < 4 * NB; e++) w[e] = ex2(w[e]);
 #pragma unroll
             for (int k = 0; k < NB; k++) {
-#pragma unroll
-              for (int e = 0; e < 4; e++) w[4 * k + e] = ex2(w[4 * k + e]);
-              l[k] = add2(l[k], add2(pk2(w[4 * k], w[4 * k + 1]), pk2(w[4 * k + 2], w[4 * k + 3])));
+              l[2 * k] += w[4 * k] + w[4 * k + 2];
+              l[2 * k + 1] += w[4 * k + 1] + w[4 * k + 3];
             }
             const int ch = mchunk + hf * 2;
             const uint32_t pa = pbase + (ch >> 3) * (a.rows * 128) + mrow * 128 +
@@ -1173,9 +1154,20 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
                 stsm4t(pa + k * 1024,
                        pack_bf16x2(w[4 * k], w[4 * k + 1]), pack_bf16x2(w[4 * k + 2], w[4 * k + 3]),
                        pack_bf16x2(w[4 * k + 4], w[4 * k + 5]), pack_bf16x2(w[4 * k + 6], w[4 * k + 7]));
+          };
+          if constexpr (kKeep) {
+            weights(0, z[0]);
+            weights(1, z[kKeep]);
+          } else {
+#pragma unroll 1
+            for (int hf = 0; hf < 2; hf++) {
+              tmem_frag<NB>(ts + ((uint32_t)(16 * hf) << 16), z[0]);
+              tmem_wait(z[0]);
+              weights(hf, z[0]);
+            }
           }
         } else {
-          *sm.failed = 1;
+          sm.failed = 1;
         }
         tc_fence_before();
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -1189,24 +1181,17 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
       const uint32_t pv = sc - 1;
       if (ok)
         ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.pvdone + (pv & 1)), (pv >> 1) & 1,
-                                                       sm.failed));
+                                                       &sm.failed));
       ok = named_sync_and(bar, 128, ok);
       if (!ok) break;
       tc_fence_after();
       // (P is free: its last product is done)
 #pragma unroll
-      for (int k = 0; k < NB; k++) {
-        float l0, l1;
-        upk2(l[k], l0, l1);
+      for (int e = 0; e < 2 * NB; e++) {
+        float x = l[e];
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-          l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, o);
-          l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, o);
-        }
-        if (lane < 4) {
-          scr[quarter * CW + 8 * k + 2 * lane] = l0;
-          scr[quarter * CW + 8 * k + 2 * lane + 1] = l1;
-        }
+        for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+        if (lane < 4) scr[quarter * CW + 8 * (e >> 1) + 2 * lane + (e & 1)] = x;
       }
       named_sync(bar, 128);
       const bool whole = t0 == 0 && t1 == pos.n_kt;
@@ -1214,7 +1199,7 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
       if (wt < cols) {
         const float sum = (scr[wt] + scr[CW + wt]) + (scr[2 * CW + wt] + scr[3 * CW + wt]);
         const float m = sum > 0.f || sum != sum ? -nb[wt] : -INFINITY;
-        const int x = rt * a.rows + c0 + wt;
+        const int x = rt * a.rstep + c0 + wt;
         if (whole) {
           const int64_t qr = (int64_t)(pos.q0 + x / a.G) * a.Hq + h * a.G + x % a.G;
           a.lse[qr] = m == -INFINITY ? -INFINITY : (m + log2f(sum)) * kLn2;
@@ -1226,12 +1211,13 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
       named_sync(bar, 128);
       const float *fac = scr + 4 * CW;
       const int d = D == 64 ? key & 63 : key;
-      const bool odd = *sm.odd != 0;
+      const bool odd = sm.odd != 0;
 #pragma unroll 1
       for (int cc = 0; cc < cols; cc += 16) {
         float v[16];
         tmem_ld16(tmem_o + lanes + c0 + cc, v);
         if (odd) {  // infinities and NaN of the nodes this run covered, to the rows that see them
+#pragma unroll 1
           for (int jn = max(0, t0 * kTtKeys - pos.c); jn < min(pos.T, t1 * kTtKeys - pos.c); jn++) {
             const int pn = pos.c + jn;
             const int32_t bn = bt[pn / a.BS];
@@ -1240,7 +1226,7 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
             if (fabsf(vn) < INFINITY) continue;
 #pragma unroll
             for (int e = 0; e < 16; e++) {
-              const int i = (rt * a.rows + c0 + cc + e) / a.G;
+              const int i = (rt * a.rstep + c0 + cc + e) / a.G;
               if (i >= pos.T) continue;
               const bool see = a.mask ? (a.mask[(int64_t)(pos.q0 + i) * a.mask_words + (jn >> 5)] >> (jn & 31)) & 1u
                                       : jn <= i;
@@ -1248,28 +1234,38 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
             }
           }
         }
+        if (D == 64 && key >= 64) continue;  // (the second copy of V)
+        if (whole) {
+          int x = rt * a.rstep + c0 + cc, i = x / a.G, gg = x % a.G;
+          uint16_t *o = a.out + ((int64_t)(pos.q0 + i) * a.Hq + h * a.G + gg) * D + d;
 #pragma unroll
-        for (int e = 0; e < 16; e++) {
-          if (cc + e >= cols || (D == 64 && key >= 64)) continue;
-          const int x = rt * a.rows + c0 + cc + e;
-          const float o = v[e] * fac[cc + e];
-          if (whole) {
-            const __nv_bfloat16 ob = __float2bfloat16(fac[cc + e] == 0.f ? 0.f : o);
-            const int64_t qr = (int64_t)(pos.q0 + x / a.G) * a.Hq + h * a.G + x % a.G;
-            a.out[qr * D + d] = *reinterpret_cast<const uint16_t *>(&ob);
-          } else {
-            a.part_o[(slot * a.rows + c0 + cc + e) * D + d] = o;
+          for (int e = 0; e < 16; e++) {
+            if (cc + e < cols) {
+              const float f = fac[cc + e];
+              const __nv_bfloat16 ob = __float2bfloat16(f == 0.f ? 0.f : v[e] * f);
+              *o = *reinterpret_cast<const uint16_t *>(&ob);
+              o += D;
+              if (++gg == a.G) {
+                gg = 0;
+                o += (int64_t)(a.Hq - a.G) * D;
+              }
+            }
           }
+        } else {
+          float *o = a.part_o + (slot * a.rows + c0 + cc) * D + d;
+#pragma unroll
+          for (int e = 0; e < 16; e++)
+            if (cc + e < cols) o[e * D] = v[e];
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(sm.ofree));
+      if (lane == 0) mbar_arrive(smem_u32(&sm.ofree));
       qc++;
       pos.next(a);
     }
     if (!ok) {
-      *sm.failed = 1;
+      sm.failed = 1;
       if (lane == 0) record_error(a.status, KVC_ERR_TIMEOUT);
     }
   }
@@ -1277,7 +1273,7 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
   // -------------------------------------------------------- teardown
   tc_fence_before();
   __syncthreads();
-  if (*sm.failed && tid == 0) {
+  if (sm.failed && tid == 0) {
     record_error(a.status, KVC_ERR_TIMEOUT);
     // let this CTA's copies and products finish before its memory is released
     for (int i = 0; i < p.NS; i++) {
@@ -1325,8 +1321,8 @@ k_tree_join(TreeArgs a) {
   if (c0 == c1) return;  // written whole
   int c, q0, T;
   tree_request(a, r, c, q0, T);
-  const int row = blockIdx.z * 4 + threadIdx.x / 32, x = rt * a.rows + row;
-  if (row >= a.rows || x >= T * a.G) return;
+  const int row = blockIdx.z * 4 + threadIdx.x / 32, x = rt * a.rstep + row;
+  if (row >= a.rstep || x >= T * a.G) return;
   const int64_t first = 2 * (int64_t)c0 + (run_start(total, n_cta, c0) != g0);
   const int n_part = c1 - c0 + 1;
   // part i is slot first (i = 0) or 2·(c0 + i): later CTAs begin inside the unit
@@ -1369,12 +1365,13 @@ constexpr int kTcRowsMax = 256;
 
 // Rows per tile, keys per tile and grid of a call.
 void tree_plan(int n_req, int max_blocks, int max_tree, int H, int Hq, int D, int BS, int &rows,
-               int &tile, int &n_cta, int &max_rt) {
-  const int R = max_tree * (Hq / H);
+               int &rstep, int &tile, int &n_cta, int &max_rt) {
+  const int G = Hq / H, R = max_tree * G;
   const bool tc = R > kRowsMax;
   rows = tc ? std::min((R + 31) / 32 * 32, kTcRowsMax) : R <= 16 ? 16 : 32;
   tile = tc ? kTtKeys : kRowWarps * (2048 / D);
-  max_rt = (R + rows - 1) / rows;
+  rstep = tc ? std::min(max_tree, rows / G) * G : rows;
+  max_rt = (R + rstep - 1) / rstep;
   const int64_t most =
       (int64_t)n_req * H * max_rt * (((int64_t)max_blocks * BS + tile - 1) / tile);
   n_cta = (int)std::min<int64_t>((tc ? 1 : 2) * device_sm_count(), most);
@@ -1392,6 +1389,18 @@ bool pool_map(CUtensorMap *m, const void *pool, int64_t n_slots, int H, int D, i
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Boxes of `nodes` consecutive rows of q, the G heads of one group, 64 columns.
+bool q_map(CUtensorMap *m, const void *q, int n_q, int Hq, int D, int G, int nodes) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)n_q};
+  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)Hq * D * 2};
+  cuuint32_t bx[3] = {64, (cuuint32_t)G, (cuuint32_t)nodes}, es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, bx, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, int CW>
 cudaError_t launch_tc(const TreeArgs &a, cudaStream_t s) {
   constexpr size_t kSmemMax = 232448;
@@ -1399,20 +1408,22 @@ cudaError_t launch_tc(const TreeArgs &a, cudaStream_t s) {
   p.NW = (a.rows + CW - 1) / CW;
   p.PB = a.rows <= 128 ? 2 : 1;
   p.SB = 3 * a.rows <= 512 ? 2 : 1;
-  for (p.NS = 8; p.NS > 3; p.NS--)
-    if (1024 + TreeTcSmem::layout(D, a.rows, p.NS, p.PB, nullptr, nullptr) <= kSmemMax) break;
-  CUtensorMap tm_k{}, tm_v{};
+  for (p.NS = kTtSlots; p.NS > 3; p.NS--)
+    if (1024 + TreeTcSmem(D, a.rows, p.NS, p.PB).bytes <= kSmemMax) break;
+  CUtensorMap tm_k{}, tm_v{}, tm_q{};
   p.box = a.BS % 32 == 0 ? 32 : a.BS % 16 == 0 ? 16 : a.BS % 8 == 0 ? 8 : 0;
   if (p.box && !(pool_map(&tm_k, a.kpool, a.n_slots, a.H, D, p.box) &&
                  pool_map(&tm_v, a.vpool, a.n_slots, a.H, D, p.box)))
     return cudaErrorUnknown;
+  p.q_nodes = a.rstep / a.G;
+  if (!q_map(&tm_q, a.q, a.n_q, a.Hq, D, a.G, p.q_nodes)) return cudaErrorUnknown;
   p.idesc_s = make_idesc(128, 0);
   p.idesc_o = make_idesc(128, 0) | (1u << 15);  // A (V) MN-major
-  const size_t smem = 1024 + TreeTcSmem::layout(D, a.rows, p.NS, p.PB, nullptr, nullptr);
+  const size_t smem = 1024 + TreeTcSmem(D, a.rows, p.NS, p.PB).bytes;
   cudaError_t e = cudaFuncSetAttribute(k_tree_tc<D, CW>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  k_tree_tc<D, CW><<<a.n_cta, (p.NW * 4 + kTtProd + 1) * 32, smem, s>>>(tm_k, tm_v, a, p);
+  k_tree_tc<D, CW><<<a.n_cta, (p.NW * 4 + kTtProd + 1) * 32, smem, s>>>(tm_k, tm_v, tm_q, a, p);
   return cudaGetLastError();
 }
 
@@ -1429,8 +1440,8 @@ cudaError_t launch_rows(const TreeArgs &a, cudaStream_t s) {
 }  // namespace
 
 size_t tree_attn_ws_bytes(int n_req, int max_blocks, int max_tree, int H, int Hq, int D, int BS) {
-  int rows, tile, n_cta, max_rt;
-  tree_plan(n_req, max_blocks, max_tree, H, Hq, D, BS, rows, tile, n_cta, max_rt);
+  int rows, rstep, tile, n_cta, max_rt;
+  tree_plan(n_req, max_blocks, max_tree, H, Hq, D, BS, rows, rstep, tile, n_cta, max_rt);
   return (size_t)2 * n_cta * rows * (D * sizeof(float) + sizeof(float2));
 }
 
@@ -1464,7 +1475,7 @@ cudaError_t launch_tree_attn(const uint16_t *q, const uint16_t *kpool, const uin
   a.BS = BS;
   a.zscale = scale * kLog2e;
   int max_rt;
-  tree_plan(n_req, max_blocks, max_tree, H, Hq, D, BS, a.rows, a.tile, a.n_cta, max_rt);
+  tree_plan(n_req, max_blocks, max_tree, H, Hq, D, BS, a.rows, a.rstep, a.tile, a.n_cta, max_rt);
   a.part_o = reinterpret_cast<float *>(ws);
   a.part_ml = reinterpret_cast<float2 *>(a.part_o + (size_t)2 * a.n_cta * a.rows * D);
   cudaError_t e;
