@@ -40,6 +40,7 @@ struct MassArgs {
   int32_t *status;
   int64_t n_slots;
   int n_q, n_rows, max_rows, max_blocks, cap, n_req, L, H, Hq, G, BS;
+  uint32_t bs_inv;  // page_inverse(BS)
   float zscale, decay;
 };
 
@@ -127,8 +128,8 @@ k_mass_rows(MassArgs a, int n_cta_max) {
       int32_t slot = -1;
       if (lane < KT && p0 + lane < seq) {
         const int p = p0 + lane;
-        const int32_t b = bt[p / a.BS];
-        if (b >= 0 && b < n_blocks) slot = b * a.BS + p % a.BS;
+        const int32_t b = bt[page_of(p, a.bs_inv)];
+        if (b >= 0 && b < n_blocks) slot = b * a.BS + p - page_of(p, a.bs_inv) * a.BS;
         else record_error(a.status, KVC_ERR_BOUNDS);
       }
       const uint32_t ok = __ballot_sync(0xFFFFFFFFu, slot >= 0);
@@ -583,8 +584,8 @@ k_mass_tc(MassArgs a, MassTc p) {
           const int pp = (pos.kg * KG + kt) * kTcKeys + pw * 32 + lane;
           int32_t slot = -1;
           if (pp < seq) {
-            const int32_t b = bt[pp / a.BS];
-            if (b >= 0 && b < n_blocks) slot = b * a.BS + pp % a.BS;
+            const int32_t b = bt[page_of(pp, a.bs_inv)];
+            if (b >= 0 && b < n_blocks) slot = b * a.BS + pp - page_of(pp, a.bs_inv) * a.BS;
             else record_error(a.status, KVC_ERR_BOUNDS);
           }
           constexpr int RPI = 32 / CH;
@@ -732,7 +733,7 @@ k_mass_tc(MassArgs a, MassTc p) {
       bool valid = false;
       if (mine && key < seq) {
         if (whole && key < a.n_mass[pos.r]) old = *out;
-        const int32_t b = a.block_table[(int64_t)pos.r * a.max_blocks + key / a.BS];
+        const int32_t b = a.block_table[(int64_t)pos.r * a.max_blocks + page_of(key, a.bs_inv)];
         valid = b >= 0 && b < a.n_slots / a.BS;
       }
       if (pos.cnt > 0)
@@ -1020,7 +1021,7 @@ cudaError_t launch_attn_mass(const uint16_t *q, const float *lse, int n_q,
   MassArgs a{q,      kpool,   lse,    row_idx,  row_vis,    row_off,         block_table, seqused,
              n_mass, mass,    status, n_slots,  n_q,        n_rows,          max_rows,    max_blocks,
              max_blocks * BS, n_req,  L,        H,          Hq,              Hq / H,      BS,
-             scale * kLog2e,  decay};
+             page_inverse(BS), scale * kLog2e, decay};
   const int64_t R = (int64_t)max_rows * a.G;
   if (R <= kMrMaxRows) {
     if (D == 128)

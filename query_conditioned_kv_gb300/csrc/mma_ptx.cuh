@@ -48,6 +48,15 @@ __device__ __forceinline__ uint32_t swz(int row, int c) {
   return (uint32_t)(row * D * 2 + ((c ^ (row & 7)) << 4));
 }
 
+// p / BS for 0 ≤ p < 2^24 and BS ≤ 64, from page_inverse(BS) = ⌈2^32 / BS⌉: the
+// product's error, p·(⌈2^32/BS⌉·BS − 2^32) < 2^30, stays below 2^32.
+__device__ __forceinline__ int page_of(int p, uint32_t inverse) {
+  return inverse ? (int)__umulhi((uint32_t)p, inverse) : p;
+}
+inline uint32_t page_inverse(int BS) {
+  return BS == 1 ? 0u : (uint32_t)(((1ull << 32) + BS - 1) / BS);
+}
+
 // Sum over the CTA (a multiple of 32 threads); every thread gets it.  sh: 64
 // words of scratch, free again on return.
 __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t *sh) {

@@ -56,6 +56,7 @@ struct TreeArgs {
   int rstep;     // rows of a row tile (whole nodes where the tile holds several)
   int tile;      // keys per tile
   int n_cta;     // CTAs the tiles are dealt out to
+  uint32_t bs_inv;  // ⌈2^32 / BS⌉ (0: BS = 1)
   float zscale;  // scale·log2(e)
 };
 
@@ -188,8 +189,8 @@ k_tree_rows(TreeArgs a) {
       int32_t slot = -1;
       if (lane < KT && p0 + lane < end) {
         const int p = p0 + lane;
-        const int32_t b = bt[p / a.BS];
-        if (b >= 0 && b < n_blocks) slot = b * a.BS + p % a.BS;
+        const int32_t b = bt[page_of(p, a.bs_inv)];
+        if (b >= 0 && b < n_blocks) slot = b * a.BS + p - page_of(p, a.bs_inv) * a.BS;
         else record_error(a.status, KVC_ERR_BOUNDS);
       }
       const uint32_t ok = __ballot_sync(0xFFFFFFFFu, slot >= 0);
@@ -465,66 +466,70 @@ k_tree_rows(TreeArgs a) {
 
 // ---------------------------------------------------------------- tcgen05
 //
-// k_tree_tc (more than 32 rows).  Per tile of 128 keys, both products with
-// the rows as the N dimension:
-//   Sᵀ[key][row] = K·Qᵀ          (M 128 keys,  N rows, K D)
-//   Oᵀ[d][row] += Vᵀ·Pᵀ          (M D (64 twice), N rows, K 128 keys)
-// so the tensor work grows with the rows instead of being padded to 128, and
-// at 256 rows each instruction is the widest (N 256).  V and P are taken
-// MN-major: V as it lies in the pool, P as the softmax threads hold it (one
-// key per thread), written with 16-byte stores.
+// k_tree_tc (more than 32 rows).  Per job, 128 keys and up to 128 rows:
+//   Sᵀ[key][row] = K·Qᵀ     (M 128 keys, N rows, K D; both K-major)
+//   O[row][d]  += P·V       (M 128 rows, N D, K 128 keys; V as it lies in the
+//                            pool, MN-major; P written K-major)
+// Two softmax warpgroups (teams) take the jobs in turn, each with its own Sᵀ,
+// P and O, so that one team's softmax runs under the other's
+// products: at most 128 rows, a job is a tile and the teams' results are
+// joined when the run ends; with more rows each tile is two jobs, team 0
+// taking rows 0–127 and team 1 the others.
 //
-// A softmax thread owns one key (TMEM lane) and CW rows (columns), so a row's
-// maximum is spread over 128 threads.  The exponent's reference is therefore
-// not the running maximum but a fixed value per row, the maximum of the first
-// tile, raised only when some logit exceeds it by 2^30: weights, their sums
-// and O stay far inside fp32 and bf16 range (bf16 has fp32's exponents), and
-// the result does not depend on the reference.  A per-tile vote of the
-// warpgroup (one barrier) finds the tiles that must raise it; they take the
-// exchange and rescale O in tensor memory.  The sums of the weights stay in
-// registers per (key lane, row) and are reduced once per run.
+// A softmax thread owns four keys and 32 rows of a job (16x256b fragments),
+// so a row's maximum is spread over a warpgroup.  The exponent's reference is
+// therefore not the running maximum but a fixed value per row, the maximum of
+// the team's first tile, raised only when some logit exceeds it by 2^30:
+// weights, their sums and O stay far inside fp32 and bf16 range (bf16 has
+// fp32's exponents), and the result does not depend on the reference.  A job
+// is worked out on the references at hand; a vote of the warpgroup (one
+// barrier) then passes it on, or raises the references, rescales O in tensor
+// memory and works the job out again.  A tile that holds nodes, or the end,
+// first gets −inf written into Sᵀ where a row does not see a key, so the loop
+// over the tiles has no masks.
 //
-// Warps: NW softmax warpgroups, two producer warps (cp.async, any page
-// size), one MMA warp.  K and V tiles share one ring, in the order the MMA
-// warp consumes them: K0 K1 V0 K2 V1 …
+// Warps: 0–7 softmax; 8–9 load K (64 keys each; 8 the queries too), 10–11
+// load V: TMA boxes of whole page rows, or cp.async row by row where a tile
+// holds nodes, the end, or a page size has no box; 12 issues Sᵀ, 13 issues O.
 
 constexpr int kTtKeys = 128;
-constexpr int kTtProd = 2;
-constexpr int kTtThreads = 640;     // at most 4 softmax warpgroups, then the other warps
+constexpr int kTtSoft = 8;
+constexpr int kTtThreads = (kTtSoft + 8) * 32;  // (two warps fill the last warpgroup)
+constexpr int kTtMore = 168, kTtLess = 88;  // registers of a softmax thread, of the others
 constexpr float kUnset = -1e30f;   // reference of a row that has seen nothing
 constexpr float kExceed = 30.f;    // log2 of how far a logit may pass the reference
 
 struct TreeTc {
-  int NW;      // softmax warpgroups
-  int NS;      // ring slots
-  int PB, SB;  // P buffers, S buffers
+  int NK, NV;  // slots of the K ring, of the V ring
   int box;     // rows of a TMA box (a divisor of the page size), 0: no TMA
   int q_nodes; // nodes of a row tile
-  uint32_t idesc_s, idesc_o;  // without N
+  uint32_t idesc_s, idesc_o;  // idesc_s without N
 };
 
-constexpr int kTtSlots = 8;  // ring slots, at most
+constexpr int kTtSlots = 4;  // slots of a ring, at most
 
 // Head of the dynamic shared memory, at fixed offsets (few live registers);
-// then the scratch of the warpgroups of 32 rows, P, the ring and q.
+// then P of both teams, the K ring, the V ring and q.
 struct TreeTcHead {
-  uint64_t full[kTtSlots], empty[kTtSlots], qfull, qempty;
-  uint64_t sfull[2], sfree[2], pready[2], pvdone[2], ofree;
+  uint64_t full[2][kTtSlots], empty[2][kTtSlots];  // [K, V]
+  uint64_t qfull, qempty;
+  uint64_t sfull[2], sfree[2], pready[2], pvdone[2], ofree;  // [team]
   int64_t scan[66];
   uint32_t tmem_holder;
   volatile int failed, odd, bad;
-  float nb[256];  // −reference per row
+  float nb[2][128];  // −reference per team and row
 };
 constexpr uint32_t kTtHead = 2048;
 static_assert(sizeof(TreeTcHead) <= kTtHead, "the head's room");
+constexpr uint32_t kTtP = 128 * kTtKeys * 2;  // bytes of a team's P: [key half][row][64 keys]
 
 // Byte offsets (multiples of 1024) from the head.
 struct TreeTcSmem {
-  uint32_t p, ring, q, bytes;
-  __host__ __device__ TreeTcSmem(int D, int rows, int NS, int PB) {
-    p = kTtHead + (rows <= 128 ? 128 * 24 : 0);
-    ring = p + PB * rows * (kTtKeys * 2);
-    q = ring + NS * kTtKeys * D * 2;
+  uint32_t ring[2], q, bytes;
+  __host__ __device__ TreeTcSmem(int D, int rows, int NK, int NV) {
+    ring[0] = kTtHead + 2 * kTtP;
+    ring[1] = ring[0] + NK * kTtKeys * D * 2;
+    q = ring[1] + NV * kTtKeys * D * 2;
     bytes = q + rows * D * 2;
   }
 };
@@ -548,6 +553,39 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) 
       "r"(__float_as_uint(v[15]))
       : "memory");
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// tcgen05.mma / commit by the lanes with `lead` set (one of the warp); the
+// whole warp must execute it.
+__device__ __forceinline__ void mma_bf16_if(uint32_t lead, uint32_t d_tmem, uint64_t a, uint64_t b,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit_if(uint32_t lead, uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
+          bar),
+      "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_if(uint32_t lead, uint32_t dst, const CUtensorMap *map,
+                                               int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %6, 0;\n"
+      " @q cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];\n}\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(lead)
+      : "memory");
+}
+// The same value in every lane, for the compiler too.
+__device__ __forceinline__ uint32_t uniform32(uint32_t x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
+__device__ __forceinline__ uint64_t uniform64(uint64_t x) {
+  return (uint64_t)uniform32((uint32_t)(x >> 32)) << 32 | uniform32((uint32_t)x);
 }
 
 __device__ __forceinline__ bool named_sync_or(int id, int n, bool v) {
@@ -591,16 +629,6 @@ struct TreePos {
 template <int NB>
 __device__ __forceinline__ void tmem_frag(uint32_t taddr, uint32_t (&r)[4 * NB]);
 template <>
-__device__ __forceinline__ void tmem_frag<4>(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-template <>
 __device__ __forceinline__ void tmem_frag<8>(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
@@ -620,25 +648,22 @@ __device__ __forceinline__ void stsm4t(uint32_t addr, uint32_t r0, uint32_t r1, 
                : "memory");
 }
 
-// x = z·zscale + nb of one 16-lane half (nb[2k + e]: rows 8k + 2·(t%4) + e),
-// −inf where bit 4k + j of `see` is clear.  Scalar FMAs: the packed form
-// costs more in register moves than it saves.
-template <int NB>
-__device__ __forceinline__ void tree_exponents(const uint32_t (&z)[4 * NB], float zs,
-                                               const float (&nb)[2 * NB], bool masked, uint32_t see,
-                                               float (&x)[4 * NB]) {
-#pragma unroll
-  for (int e = 0; e < 4 * NB; e++)
-    x[e] = fmaf(__uint_as_float(z[e]), zs, nb[(e >> 2) * 2 + (e & 1)]);
-  if (masked) {
-    asm volatile("");  // a branch, not 4·NB selects in every tile
-#pragma unroll
-    for (int e = 0; e < 4 * NB; e++)
-      if (!((see >> e) & 1u)) x[e] = -INFINITY;
-  }
+// The same fragment written back.
+__device__ __forceinline__ void tmem_put(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+      "%28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-template <int D, int CW>
+template <int D>
 __global__ void __launch_bounds__(kTtThreads, 1)
 k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
           const __grid_constant__ CUtensorMap tm_q, TreeArgs a, TreeTc p) {
@@ -648,38 +673,35 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
   uint8_t *base = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   TreeTcHead &sm = *reinterpret_cast<TreeTcHead *>(base);
-  const TreeTcSmem at(D, a.rows, p.NS, p.PB);
+  const TreeTcSmem at(D, a.rows, p.NK, p.NV);
   const uint32_t base_u = smem_u32(base);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int nsw = p.NW * 4;  // softmax warps
-  const uint32_t p_bytes = (uint32_t)a.rows * (kTtKeys * 2);
 
   asm volatile("griddepcontrol.launch_dependents;");
   if (tid == 0) {
     sm.failed = 0;
     sm.odd = 0;
     sm.bad = 0;
-    for (int i = 0; i < p.NS; i++) {
-      mbar_init(smem_u32(sm.full + i), kTtProd * 32);
-      mbar_init(smem_u32(sm.empty + i), 1);
+    for (int i = 0; i < 2 * kTtSlots; i++) {
+      mbar_init(smem_u32(sm.full[0] + i), 64);
+      mbar_init(smem_u32(sm.empty[0] + i), 1);
     }
     mbar_init(smem_u32(&sm.qfull), 1);
     mbar_init(smem_u32(&sm.qempty), 1);
     for (int i = 0; i < 2; i++) {
       mbar_init(smem_u32(sm.sfull + i), 1);
-      mbar_init(smem_u32(sm.sfree + i), nsw);
-      mbar_init(smem_u32(sm.pready + i), nsw);
+      mbar_init(smem_u32(sm.sfree + i), kTtSoft / 2);
+      mbar_init(smem_u32(sm.pready + i), kTtSoft / 2);
       mbar_init(smem_u32(sm.pvdone + i), 1);
     }
-    mbar_init(smem_u32(&sm.ofree), nsw);
+    mbar_init(smem_u32(&sm.ofree), kTtSoft);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == nsw + kTtProd) alloc_tmem_cols(&sm.tmem_holder, 512);
+  if (warp == kTtSoft + 4) alloc_tmem_cols(&sm.tmem_holder, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sm.tmem_holder;
-  const uint32_t tmem_o = tmem + p.SB * a.rows;
+  const uint32_t tmem = sm.tmem_holder;  // Sᵀ of team 0, of team 1, O of team 0, of team 1
 
   if (blockIdx.x == 0)  // one report per bad request
     for (int r = tid; r < a.n_req; r += blockDim.x) {
@@ -700,31 +722,33 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
     pos.init(a, before);
   }
 
-bool ok = true;
-  if (warp >= nsw && warp < nsw + kTtProd) {
+  bool ok = true;
+  // Registers move from the producers and MMA warps to the softmax: 256·kTtMore
+  // + 256·kTtLess is the 512·128 of the launch.
+  if (warp >= kTtSoft && warp < kTtSoft + 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTtLess));
     // ------------------------------------------------------- producers
-    const int pw = warp - nsw;
+    // (two warps each for K and V, 64 keys a warp: issuing a tile's boxes takes
+    // one warp longer than the tile lasts.  K and V have a ring each, filled in
+    // order: a slot's parity only tells its next two uses apart)
+    const bool is_v = warp >= kTtSoft + 2;
+    const int key0 = (warp & 1) * 64;  // this warp's keys of a tile
+    const uint16_t *pool = is_v ? a.vpool : a.kpool;
+    const CUtensorMap *tm = is_v ? &tm_v : &tm_k;
     const int64_t n_blocks = a.n_slots / a.BS;
-    constexpr int RPI = 32 / CH, NU = kTtKeys / (32 * kTtProd);  // this warp's blocks of 32 keys
+    constexpr int RPI = 32 / CH, NU = 2;
     const int col = lane % CH;
-    uint32_t rc = 0, qc = 0;
-    uint32_t pend0 = 0, pend1 = 0;  // stages in flight, oldest first (the newest besides)
-    auto hand = [&](uint32_t bar) {  // the stage's copies have landed: to the tensor core
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      mbar_arrive(bar);
-    };
+    const uint32_t n_slot = is_v ? p.NV : p.NK;
+    uint64_t *full = sm.full[is_v], *empty = sm.empty[is_v];
+    const uint32_t ring = base_u + (is_v ? at.ring[1] : at.ring[0]);
+    uint32_t rc = 0, qc = 0;  // stages filled, runs done
+    uint32_t pend = 0;  // a stage copied by cp.async and not yet handed over
     auto flush = [&]() {
-      if (pend1) {
-        cp_wait<1>();
-        hand(pend0);
-        pend0 = pend1;
-        pend1 = 0;
-      }
-      if (pend0) {
-        cp_wait<0>();
-        hand(pend0);
-        pend0 = 0;
-      }
+      if (!pend) return;
+      cp_wait<0>();
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      mbar_arrive(pend);
+      pend = 0;
     };
     // a full ring is waited for only after everything in flight is handed over
     auto acquire = [&](uint64_t *bar, uint32_t parity) {
@@ -732,536 +756,517 @@ bool ok = true;
       flush();
       return mbar_wait_bounded(smem_u32(bar), parity, &sm.failed);
     };
-    auto committed = [&](uint64_t *bar) {
-      cp_commit();
-      if (pend1) {
-        cp_wait<2>();
-        hand(pend0);
-        pend0 = pend1;
-        pend1 = smem_u32(bar);
-      } else if (pend0) {
-        pend1 = smem_u32(bar);
-      } else {
-        pend0 = smem_u32(bar);
-      }
-    };
     while (pos.g < pos.run1 && ok) {
-      const int t1 = pos.t1(), h = pos.h(), rt = pos.rt(), n_rows = pos.rows(a);
+      const int t0 = pos.t0, t1 = pos.t1(), h = pos.h(), rt = pos.rt();
       const int32_t *bt = a.block_table + (int64_t)pos.r * a.max_blocks;
       const int end = pos.c + pos.T;
-      int32_t blk[NU], ks[NU], vs[NU];  // block ids of the next tile; slots of this K, of this V
+      const uint32_t uh = uniform32(h);
+      int32_t blk[NU];  // block ids of the next tile's keys
       auto fetch = [&](int t) {
 #pragma unroll
         for (int u = 0; u < NU; u++) {
-          const int pp = t * kTtKeys + pw * 32 + u * (32 * kTtProd) + lane;
-          blk[u] = pp < end && t < t1 ? bt[pp / a.BS] : 0;
+          const int pp = t * kTtKeys + key0 + u * 32 + lane;
+          blk[u] = pp < end && t < t1 ? bt[page_of(pp, a.bs_inv)] : 0;
         }
       };
-      auto resolve = [&](int t) {
+      fetch(t0);
+      for (int t = t0; t < t1 && ok; t++) {
+        int32_t slot[NU];
+        bool all = true;
 #pragma unroll
         for (int u = 0; u < NU; u++) {
-          const int pp = t * kTtKeys + pw * 32 + u * (32 * kTtProd) + lane;
-          vs[u] = ks[u];
-          ks[u] = -1;
+          const int pp = t * kTtKeys + key0 + u * 32 + lane;
+          slot[u] = -1;
           if (pp < end) {
             if (blk[u] >= 0 && blk[u] < n_blocks) {
-              ks[u] = blk[u] * a.BS + pp % a.BS;
+              slot[u] = blk[u] * a.BS + pp - page_of(pp, a.bs_inv) * a.BS;
             } else {
               sm.bad = 1;  // (read by the softmax warps after this stage's product)
               record_error(a.status, KVC_ERR_BOUNDS);
             }
           }
+          all &= slot[u] >= 0;
         }
-      };
-      // One stage: TMA boxes of whole page rows where every key of the warp's
-      // blocks is cached, else row by row with cp.async (zeros past the end).
-      auto load = [&](const uint16_t *pool, const CUtensorMap *tm, int t, const int32_t (&slot)[NU]) {
-        const int st = rc % p.NS;
-        if (!(ok = acquire(sm.empty + st, ((rc / p.NS) & 1) ^ 1))) return;
-        const uint32_t slot0 = (base_u + at.ring) + st * kSlot;
-        bool whole = p.box > 0 && (t + 1) * kTtKeys <= pos.c;
-        if (whole) {
-#pragma unroll
-          for (int u = 0; u < NU; u++) whole &= __all_sync(0xFFFFFFFFu, slot[u] >= 0);
-        }
-        if (whole) {
-          const uint32_t bar = smem_u32(sm.full + st);
-          if (lane == 0) mbar_expect_tx(bar, kSlot / kTtProd);
+        fetch(t + 1);
+        const uint32_t st = rc % n_slot;
+        if (!(ok = acquire(empty + st, ((rc / n_slot) & 1) ^ 1))) break;
+        rc++;
+        const uint32_t slot0 = ring + st * kSlot;
+        const uint32_t bar = smem_u32(full + st);
+        // TMA boxes of whole page rows where every key is cached, else row by
+        // row with cp.async (zeros past the end)
+        if (__all_sync(0xFFFFFFFFu, all) && p.box > 0 && (t + 1) * kTtKeys <= pos.c) {
+          if (lane == 0) mbar_expect_tx(bar, kSlot / 2);
           else mbar_arrive(bar);
           __syncwarp();
-          if (lane % p.box == 0)  // a box's first key
+          // (warp-uniform operands, one lane enabled: see the MMA warps)
+          const uint32_t ubar = uniform32(bar);
 #pragma unroll
-            for (int u = 0; u < NU; u++)
+          for (int u = 0; u < NU; u++)
+            for (int k = 0; k < 32; k += p.box) {  // a box's first key
+              const uint32_t sl = __shfl_sync(0xFFFFFFFFu, slot[u], k);
+              const uint32_t dst = uniform32(slot0 + (key0 + u * 32 + k) * 128);
 #pragma unroll
               for (int kb = 0; kb < KB; kb++)
-                tma_load_3d(slot0 + kb * (kTtKeys * 128) +
-                                (pw * 32 + u * (32 * kTtProd) + lane) * 128,
-                            tm, kb * 64, h, slot[u], bar);
-          __syncwarp();
-          flush();  // (a stage copied row by row may still be in flight)
-          rc++;
-          return;
-        }
-        const uint32_t dst = slot0 + (col >> 3) * (kTtKeys * 128);
+                tma_load_3d_if(lane == 0, dst + kb * (kTtKeys * 128), tm, kb * 64, uh, sl, ubar);
+            }
+        } else {
+          flush();
+          const uint32_t dst = slot0 + (col >> 3) * (kTtKeys * 128);
 #pragma unroll
-        for (int u = 0; u < NU; u++)
-#pragma unroll
-          for (int i = 0; i < 32 / RPI; i++) {
-            const int row = i * RPI + lane / CH;
-            const int32_t sl = __shfl_sync(0xFFFFFFFFu, slot[u], row);
-            cp_async16(dst + (pw * 32 + u * (32 * kTtProd) + row) * 128 +
-                           (((col & 7) ^ (row & 7)) << 4),
-                       pool + ((int64_t)max(sl, 0) * a.H + h) * D + col * 8, sl >= 0);
-          }
-        committed(sm.full + st);
-        rc++;
-      };
-      auto load_v = [&](int t, const int32_t (&slot)[NU]) {
-        const uint32_t dst =
-            (base_u + at.ring) + (rc % p.NS) * kSlot + (col >> 3) * (kTtKeys * 128);
-        load(a.vpool, &tm_v, t, slot);
-        if (!ok || (t + 1) * kTtKeys <= pos.c) return;
-        // A node's V may hold infinities or NaN that some rows do not see: the
-        // product gets zeros in their place, and the run's end adds them to
-        // the rows that do.  Each thread looks at what it copied, before the
-        // stage is handed over.
-        cp_wait<0>();
-        bool odd = false;
+          for (int u = 0; u < NU; u++)
+#pragma unroll 4
+            for (int k = 0; k < 32 / RPI; k++) {
+              const int row = k * RPI + lane / CH;
+              const int32_t sl = __shfl_sync(0xFFFFFFFFu, slot[u], row);
+              cp_async16(dst + (key0 + u * 32 + row) * 128 + (((col & 7) ^ (row & 7)) << 4),
+                         pool + ((int64_t)max(sl, 0) * a.H + h) * D + col * 8, sl >= 0);
+            }
+          cp_commit();
+          pend = bar;
+          if (is_v && (t + 1) * kTtKeys > pos.c) {
+            // A node's V may hold infinities or NaN that some rows do not see: the
+            // product gets zeros in their place, and the run's end adds them to
+            // the rows that do.  Each thread looks at what it copied, before the
+            // stage is handed over.
+            cp_wait<0>();
+            bool odd = false;
 #pragma unroll 1
-        for (int i = 0; i < NU * 32 / RPI; i++) {
-          const int u0 = i * RPI + lane / CH;
-          const int row = (u0 & 31) + pw * 32 + (u0 >> 5) * (kTtProd * 32);
-          const uint32_t at = dst + row * 128 + (((col & 7) ^ (row & 7)) << 4);
-          uint32_t w[4];
-          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                       : "r"(at)
-                       : "memory");
-          bool mine = false;
+            for (int k = 0; k < 64 / RPI; k++) {
+              const int row = key0 + k * RPI + lane / CH;
+              const uint32_t ad = dst + row * 128 + (((col & 7) ^ (row & 7)) << 4);
+              uint32_t w[4];
+              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                           : "r"(ad)
+                           : "memory");
+              bool mine = false;
 #pragma unroll
-          for (int u = 0; u < 4; u++) {
-            if ((w[u] & 0x7F80u) == 0x7F80u) mine = true, w[u] &= 0xFFFF0000u;
-            if ((w[u] & 0x7F800000u) == 0x7F800000u) mine = true, w[u] &= 0xFFFFu;
-          }
-          // (cached positions are seen by every row: their values stay)
-          if (mine && t * kTtKeys + row >= pos.c) {
-            odd = true;
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]),
-                         "r"(w[2]), "r"(w[3])
-                         : "memory");
+              for (int u = 0; u < 4; u++) {
+                if ((w[u] & 0x7F80u) == 0x7F80u) mine = true, w[u] &= 0xFFFF0000u;
+                if ((w[u] & 0x7F800000u) == 0x7F800000u) mine = true, w[u] &= 0xFFFFu;
+              }
+              // (cached positions are seen by every row: their values stay)
+              if (mine && t * kTtKeys + row >= pos.c) {
+                odd = true;
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(ad), "r"(w[0]),
+                             "r"(w[1]), "r"(w[2]), "r"(w[3])
+                             : "memory");
+              }
+            }
+            if (odd) sm.odd = 1;
+            flush();
           }
         }
-        if (odd) sm.odd = 1;
-        flush();
-      };
-      // the row tile's queries, in one box of nodes × heads of the group; rows
-      // past the request's own (another request's, or zeros) are columns that
-      // the softmax leaves out
-      auto load_q = [&]() {
-        if (!(ok = acquire(&sm.qempty, (qc & 1) ^ 1))) return;
-        if (pw == 0 && lane == 0) {
-          const uint32_t bar = smem_u32(&sm.qfull);
-          mbar_expect_tx(bar, p.q_nodes * a.G * D * 2);
+        if (warp == kTtSoft && t == t0) {
+          // the row tile's queries, in one box of nodes × heads of the group; rows
+          // past the request's own (another request's, or zeros) are columns that
+          // the softmax leaves out
+          if (!(ok = acquire(&sm.qempty, (qc & 1) ^ 1))) break;
+          if (lane == 0) {
+            const uint32_t qbar = smem_u32(&sm.qfull);
+            mbar_expect_tx(qbar, p.q_nodes * a.G * D * 2);
 #pragma unroll
-          for (int kb = 0; kb < KB; kb++)
-            tma_load_3d((base_u + at.q) + kb * (a.rows * 128), &tm_q, kb * 64, h * a.G,
-                        pos.q0 + rt * p.q_nodes, bar);
+            for (int kb = 0; kb < KB; kb++)
+              tma_load_3d(base_u + at.q + kb * (a.rows * 128), &tm_q, kb * 64, h * a.G,
+                          pos.q0 + rt * p.q_nodes, qbar);
+          }
+          __syncwarp();
         }
-        qc++;
-      };
-      fetch(pos.t0);
-      resolve(pos.t0);
-      fetch(pos.t0 + 1);
-      load(a.kpool, &tm_k, pos.t0, ks);
-      if (ok) load_q();
-      for (int t = pos.t0 + 1; t < t1 && ok; t++) {
-        resolve(t);
-        fetch(t + 1);
-        load(a.kpool, &tm_k, t, ks);
-        if (ok) load_v(t - 1, vs);
       }
-      if (ok) load_v(t1 - 1, ks);
+      qc++;
       pos.next(a);
     }
     flush();
     cp_wait<0>();
     if (!ok) sm.failed = 1;
-  } else if (warp == nsw + kTtProd) {
-    // ------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      uint32_t rc = 0, qc = 0, sc = 0, vc = 0;  // ring slots, runs, S and PV products issued
-      while (pos.g < pos.run1 && ok) {
-        const int t0 = pos.t0, t1 = pos.t1(), n_rows = pos.rows(a);
-        const uint32_t nbits = (uint32_t)((n_rows + 15) / 16 * 2) << 17;  // N / 8
-        auto wait_slot = [&]() {
-          const bool r = mbar_wait_bounded(smem_u32(sm.full + rc % p.NS), (rc / p.NS) & 1, &sm.failed);
-          return r;
-        };
-        auto issue_s = [&](bool last) {
-          const int b = sc % p.SB;
-          if (!(ok = wait_slot())) return;
-          if (!(ok = mbar_wait_bounded(smem_u32(sm.sfree + b), ((sc / p.SB) & 1) ^ 1, &sm.failed)))
-            return;
+  } else if (warp >= kTtSoft + 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTtLess));
+    if (warp < kTtSoft + 6) {
+    // ----------------------------------------------------- MMA issuers
+    // One warp for each product: a warp stands still while its instructions
+    // queue, and the tensor core would idle while it then waits for the other
+    // product's operands.
+    // The whole warp runs the loop and one lane's products are enabled by a
+    // predicate: the descriptors then live in uniform registers.  (In a branch
+    // of one lane every product cost some 100 cycles to issue.)
+    const uint32_t lead = lane == 0;
+    const bool first = warp == kTtSoft + 4;  // Sᵀ, or O
+    uint32_t rc = 0, qc = 0;  // tiles of this product's ring used, runs done
+    uint32_t done[2];         // jobs issued per team, by bit 0 (constant indexes only)
+    done[0] = done[1] = 0;
+    while (pos.g < pos.run1 && ok) {
+      const int nT = pos.t1() - pos.t0, n_rows = pos.rows(a);
+      const bool halves = n_rows > 128;
+      if (first) {
+        ok = mbar_wait_bounded(smem_u32(&sm.qfull), qc & 1, &sm.failed);
+        const uint64_t qb = uniform64(smem_desc(base_u + at.q));
+        const uint32_t qk = (uint32_t)a.rows * 8;  // next 64 columns of q, in 16 bytes
+        const uint32_t n8 = uniform32((min(n_rows, 256) + 15) / 16 * 2);  // N / 8
+        for (int t = 0; t < nT && ok; t++, rc++) {
+          // halves: one product for both teams' rows (Sᵀ of team 1 follows team 0's)
+          const int st = rc % p.NK;
+          const bool t0on = halves || !(t & 1), t1on = halves || (t & 1);
+          ok = mbar_wait_bounded(smem_u32(sm.full[0] + st), (rc / p.NK) & 1, &sm.failed);
+          if (ok && t0on) ok = mbar_wait_bounded(smem_u32(sm.sfree), (done[0] & 1) ^ 1, &sm.failed);
+          if (ok && t1on) ok = mbar_wait_bounded(smem_u32(sm.sfree + 1), (done[1] & 1) ^ 1, &sm.failed);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t kb = (base_u + at.ring) + (rc % p.NS) * kSlot, qb = (base_u + at.q);
+          const uint64_t ka = uniform64(smem_desc(base_u + at.ring[0] + st * kSlot));
+          const uint32_t dst = uniform32(tmem + (t0on ? 0 : 128));
+          const uint32_t idesc = uniform32(p.idesc_s | (n8 << 17));
 #pragma unroll
           for (int kk = 0; kk < 4 * KB; kk++)
-            mma_bf16(tmem + b * a.rows,
-                     smem_desc(kb + (kk >> 2) * (kTtKeys * 128) + (kk & 3) * 32),
-                     smem_desc(qb + (kk >> 2) * (a.rows * 128) + (kk & 3) * 32), p.idesc_s | nbits,
-                     kk > 0);
-          mma_commit(smem_u32(sm.sfull + b));
-          mma_commit(smem_u32(sm.empty + rc % p.NS));
-          if (last) mma_commit(smem_u32(&sm.qempty));
-          rc++;
-          sc++;
-        };
-        auto issue_pv = [&](bool first) {
-          if (!(ok = wait_slot())) return;
-          if (first &&  // O's previous contents have been read
-              !(ok = mbar_wait_bounded(smem_u32(&sm.ofree), (qc & 1) ^ 1, &sm.failed)))
-            return;
-          if (!(ok = mbar_wait_bounded(smem_u32(sm.pready + (vc & 1)), (vc >> 1) & 1, &sm.failed)))
-            return;
+            mma_bf16_if(lead, dst, ka + (kk >> 2) * (kTtKeys * 8) + (kk & 3) * 2,
+                        qb + (kk >> 2) * qk + (kk & 3) * 2, idesc, kk > 0);
+          if (t0on) {
+            mma_commit_if(lead, smem_u32(sm.sfull));
+            done[0]++;
+          }
+          if (t1on) {
+            mma_commit_if(lead, smem_u32(sm.sfull + 1));
+            done[1]++;
+          }
+          mma_commit_if(lead, smem_u32(sm.empty[0] + st));
+          if (t == nT - 1) mma_commit_if(lead, smem_u32(&sm.qempty));
+        }
+      } else {
+        const int nJ = halves ? 2 * nT : nT;
+        for (int j = 0; j < nJ && ok; j++) {
+          const int tm = j & 1, st = rc % p.NV;
+          ok = mbar_wait_bounded(smem_u32(sm.full[1] + st), (rc / p.NV) & 1, &sm.failed);
+          if (ok && j == 0)  // both O's previous contents have been read
+            ok = mbar_wait_bounded(smem_u32(&sm.ofree), (qc & 1) ^ 1, &sm.failed);
+          if (ok)
+            ok = mbar_wait_bounded(smem_u32(sm.pready + tm), (tm ? done[1] : done[0]) & 1, &sm.failed);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t vb = (base_u + at.ring) + (rc % p.NS) * kSlot;
-          const uint32_t pb = (base_u + at.p) + (vc % p.PB) * p_bytes;
+          const uint64_t vb =
+              uniform64(smem_desc_mn(base_u + at.ring[1] + st * kSlot, kTtKeys * 128));
+          const uint64_t pa = uniform64(smem_desc(base_u + kTtHead + tm * kTtP));
+          const uint32_t dst = uniform32(tmem + 256 + tm * 128);
 #pragma unroll
           for (int kk = 0; kk < kTtKeys / 16; kk++)
-            mma_bf16(tmem_o, smem_desc_mn(vb + kk * 2048, KB == 2 ? kTtKeys * 128 : 0),
-                     smem_desc(pb + (kk >> 2) * (a.rows * 128) + (kk & 3) * 32), p.idesc_o | nbits,
-                     !first || kk > 0);
-          mma_commit(smem_u32(sm.pvdone + (vc & 1)));
-          mma_commit(smem_u32(sm.empty + rc % p.NS));
-          rc++;
-          vc++;
-        };
-        ok = mbar_wait_bounded(smem_u32(&sm.qfull), qc & 1, &sm.failed);
-        if (ok) issue_s(t1 - t0 == 1);
-        for (int t = t0 + 1; t < t1 && ok; t++) {
-          issue_s(t == t1 - 1);
-          if (ok) issue_pv(t - 1 == t0);
+            mma_bf16_if(lead, dst, pa + (kk >> 2) * (kTtP / 32) + (kk & 3) * 2, vb + kk * 128, p.idesc_o,
+                        j > 1 || kk > 0);
+          mma_commit_if(lead, smem_u32(sm.pvdone + tm));
+          if (tm) done[1]++;
+          else done[0]++;
+          if (!halves || tm == 1) {
+            mma_commit_if(lead, smem_u32(sm.empty[1] + st));
+            rc++;
+          }
         }
-        if (ok) issue_pv(t1 - t0 == 1);
-        qc++;
-        pos.next(a);
       }
-      if (!ok) sm.failed = 1;
+      qc++;
+      pos.next(a);
     }
+    if (!ok) sm.failed = 1;
     __syncwarp();
-  } else if (warp < nsw) {
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTtMore));
     // --------------------------------------------------------- softmax
-    constexpr int NB = CW / 8;       // 8-row blocks of this warpgroup's rows
-    constexpr bool kKeep = CW == 32;  // both halves' exponents fit the registers between the passes
-    const int wg = warp >> 2, quarter = warp & 3;
-    const int c0 = wg * CW;          // this warpgroup's first row
-    const int bar = 1 + wg, wt = tid & 127;
+    const int team = warp >> 2, quarter = warp & 3;
+    const int bar = 1 + team, wt = tid & 127;
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
-    const int key = quarter * 32 + lane;
-    float *nb = sm.nb + c0;
-    float *scr = reinterpret_cast<float *>(CW == 32 ? base + kTtHead + wg * (24 * CW)
-                                               : base + at.p + c0 * 128);
+    const uint32_t ts = tmem + team * 128 + lanes, to = tmem + 256 + team * 128 + lanes;
+    float *nb = sm.nb[team];
+    uint8_t *p_team = base + kTtHead + team * kTtP;
+    float *scr = reinterpret_cast<float *>(p_team);  // scratch while P is free
     const float zs = a.zscale;
     const int64_t n_blocks = a.n_slots / a.BS;
-    // stmatrix (transposing): matrices (keys 0–7 | 8–15) × (block k | k + 1);
-    // this lane's query row of block 0, and its chunk of eight keys
-    const int mrow = c0 + (lane >> 4) * 8 + (lane & 7);
-    const int mchunk = quarter * 4 + ((lane >> 3) & 1);
-    uint32_t sc = 0, qc = 0;  // tiles and runs done
+    // stmatrix (transposing): matrices (keys 0–7 | 8–15) × (8-row block k | k + 1);
+    // this lane's row of block 0, and its chunk of eight keys
+    const int mrow = (lane >> 4) * 8 + (lane & 7);
+    const uint32_t pst = smem_u32(p_team) + (quarter >> 1) * (kTtP / 2) + mrow * 128;
+    const int mchunk = (quarter & 1) * 4 + ((lane >> 3) & 1);
+    uint32_t sc = 0;  // this team's jobs done
     while (pos.g < pos.run1 && ok) {
-      const int t0 = pos.t0, t1 = pos.t1(), h = pos.h(), rt = pos.rt(), n_rows = pos.rows(a);
-      const int cols = max(0, min(CW, n_rows - c0));  // this warpgroup's rows of the run
+      const int t0 = pos.t0, t1 = pos.t1(), n_rows = pos.rows(a);
+      const bool halves = n_rows > 128;
+      const int row0 = halves ? team * 128 : 0;          // the team's first row
+      const int cols = min(128, n_rows - row0);          // its rows
       const int32_t *bt = a.block_table + (int64_t)pos.r * a.max_blocks;
-      const int end = pos.c + pos.T;
-      named_sync(bar, 128);                           // the last run's references are read
-      if (wt < CW && c0 + wt < a.rows) nb[wt] = -kUnset;
-      // −reference and sum of weights of rows 8k + 2·(t%4) + {0, 1}, and the
-      // greatest −reference of them
-      float nbr[2 * NB], l[2 * NB], nb_top = -kUnset;
+      named_sync(bar, 128);  // the last run's references are read
+      nb[wt] = -kUnset;
+      // −reference and sum of weights of rows 8k + 2·(t%4) + {0, 1}
+      float nbr[32], l[32];
 #pragma unroll
-      for (int e = 0; e < 2 * NB; e++) {
+      for (int e = 0; e < 32; e++) {
         nbr[e] = 8 * (e >> 1) + 2 * (lane & 3) + (e & 1) < cols ? -kUnset : -INFINITY;
         l[e] = 0.f;
       }
-      // A wait that gives up only clears this warp's `ok`; the warpgroup leaves
+      // A wait that gives up only clears this warp's `ok`; the team leaves
       // together, at the next vote.
-      for (int t = t0; t < t1; t++, sc++) {
-        const int b = sc % p.SB;
-        ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.sfull + b),
-                                                             (sc / p.SB) & 1, &sm.failed));
+      bool fresh = true;
+      for (int t = halves ? t0 : t0 + team; t < t1; t += halves ? 1 : 2, sc++) {
+        ok = ok && __all_sync(0xFFFFFFFFu,
+                              mbar_wait_bounded(smem_u32(sm.sfull + team), sc & 1, &sm.failed));
         tc_fence_after();
         // a tile with nodes, past the end, or (after some bad block) any tile
-        uint32_t see[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
-        const bool masked = (t + 1) * kTtKeys > pos.c || sm.bad;
-        if (masked) {
-          const int pp = t * kTtKeys + key;
-          bool valid = pp < end;
+        if (ok && ((t + 1) * kTtKeys > pos.c || sm.bad)) {
+          const int pp = t * kTtKeys + quarter * 32 + lane;
+          bool valid = pp < pos.c + pos.T;
           if (valid) {
-            const int32_t blk = bt[pp / a.BS];
+            const int32_t blk = bt[page_of(pp, a.bs_inv)];
             valid = blk >= 0 && blk < n_blocks;
           }
           const uint32_t valid_keys = __ballot_sync(0xFFFFFFFFu, valid);
-          see[0] = see[1] = 0;
+          const float hidden = zs < 0.f ? INFINITY : -INFINITY;  // −inf once scaled
 #pragma unroll 1
-          for (int e = 0; e < 8 * NB; e++) {
-            const int hf = e / (4 * NB), k = (e >> 2) % NB, kk = hf * 16 + lane / 4 + 8 * ((e >> 1) & 1);
-            const int x = c0 + 8 * k + 2 * (lane & 3) + (e & 1);
-            const int j = t * kTtKeys + quarter * 32 + kk - pos.c, i = (rt * a.rstep + x) / a.G;
-            bool v = (valid_keys >> kk) & 1u;
-            if (v && j >= 0)
-              v = i < pos.T &&
-                  (a.mask ? (a.mask[(int64_t)(pos.q0 + i) * a.mask_words + (j >> 5)] >> (j & 31)) & 1u
-                          : j <= i);
-            const uint32_t bit = (uint32_t)v << (e % (4 * NB));
-            if (hf == 0) see[0] |= bit;
-            else see[1] |= bit;
+          for (int w = 0; w < 4; w++) {
+            const uint32_t ta = ts + ((uint32_t)(16 * (w >> 1)) << 16) + 64 * (w & 1);
+            uint32_t bits = 0;
+#pragma unroll 1
+            for (int e = 0; e < 32; e++) {  // register e: see tmem_frag
+              const int kk = (w >> 1) * 16 + lane / 4 + 8 * ((e >> 1) & 1);
+              const int x = pos.rt() * a.rstep + row0 + 64 * (w & 1) + 8 * (e >> 2) + 2 * (lane & 3) + (e & 1);
+              const int j = t * kTtKeys + quarter * 32 + kk - pos.c, i = x / a.G;
+              bool v = (valid_keys >> kk) & 1u;
+              if (v && j >= 0)
+                v = i < pos.T &&
+                    (a.mask ? (a.mask[(int64_t)(pos.q0 + i) * a.mask_words + (j >> 5)] >> (j & 31)) & 1u
+                            : j <= i);
+              bits |= (uint32_t)v << e;
+            }
+            uint32_t z[32];
+            tmem_frag<8>(ta, z);
+            tmem_wait(z);
+#pragma unroll
+            for (int e = 0; e < 32; e++)
+              if (!((bits >> e) & 1u)) z[e] = __float_as_uint(hidden);
+            tmem_put(ta, z);
           }
         }
-        const uint32_t ts = tmem + lanes + b * a.rows + c0;
-        // Pass 1: does some logit pass its row's reference by too much?  The
-        // greatest logit against the least reference answers for almost every
-        // tile; a tile that this does not clear is looked at row by row.
-        float top = -INFINITY;
-        uint32_t z[kKeep ? 2 : 1][4 * NB];
-        if (ok && cols > 0) {
-          if constexpr (kKeep) {
-            tmem_frag<NB>(ts, z[0]);
-            tmem_frag<NB>(ts + (16u << 16), z[1]);
-            tmem_wait(z[0]);
-            tmem_wait(z[1]);
+        for (;;) {
+          // the job's weights on the references at hand, their sums apart from
+          // the run's until the vote
+          float ls[32], top = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 4 * NB; e++)
-              top = max3(top, __uint_as_float(z[0][e]), __uint_as_float(z[kKeep][e]));
-          } else {
-#pragma unroll 1
-            for (int hf = 0; hf < 2; hf++) {
-              tmem_frag<NB>(ts + ((uint32_t)(16 * hf) << 16), z[0]);
-              tmem_wait(z[0]);
-#pragma unroll
-              for (int e = 0; e < 4 * NB; e += 2)
-                top = max3(top, __uint_as_float(z[0][e]), __uint_as_float(z[0][e + 1]));
-            }
-          }
-          top = fmaf(top, zs, nb_top);
-          if (masked || zs < 0.f || __any_sync(0xFFFFFFFFu, !(top <= kExceed))) {
-            top = -INFINITY;
-#pragma unroll 1
-            for (int hf = 0; hf < 2; hf++) {
-              uint32_t y[4 * NB];
-              float x[4 * NB];
-              tmem_frag<NB>(ts + ((uint32_t)(16 * hf) << 16), y);
-              tmem_wait(y);
-              tree_exponents<NB>(y, zs, nbr, masked, see[hf], x);
-#pragma unroll
-              for (int e = 0; e < 4 * NB; e += 2) top = max3(top, x[e], x[e + 1]);
-            }
-          }
-        }
-        // the vote also keeps the warpgroup's warps within one tile of each other
-        const bool raise = named_sync_or(bar, 128, !ok || top > kExceed);
-        if (raise) {
-          const uint32_t pv = sc - 1;  // the product before this tile's
+          for (int e = 0; e < 32; e++) ls[e] = 0.f;
+          // P of the team's last job has been read, O holds its product
           if (sc > 0 && ok)
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.pvdone + (pv & 1)),
-                                                           (pv >> 1) & 1, &sm.failed));
-          // (every product that reads P is done: its memory may serve as scratch)
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.pvdone + team), (sc - 1) & 1,
+                                                           &sm.failed));
+          if (ok) {
+#pragma unroll
+            for (int w = 0; w < 4; w++) {
+              const int ch = w & 1, hf = w >> 1;
+              uint32_t z[32];
+              float x[32];
+              tmem_frag<8>(ts + ((uint32_t)(16 * hf) << 16) + 64 * ch, z);
+              tmem_wait(z);
+#pragma unroll
+              for (int e = 0; e < 32; e++)
+                x[e] = fmaf(__uint_as_float(z[e]), zs, nbr[16 * ch + (e >> 2) * 2 + (e & 1)]);
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) top = max3(top, x[e], x[e + 1]);
+#pragma unroll
+              for (int e = 0; e < 32; e++) x[e] = ex2(x[e]);
+#pragma unroll
+              for (int k = 0; k < 8; k++) {
+                ls[16 * ch + 2 * k] += x[4 * k] + x[4 * k + 2];
+                ls[16 * ch + 2 * k + 1] += x[4 * k + 1] + x[4 * k + 3];
+              }
+              const uint32_t pa = pst + ch * 8192 + (((mchunk + hf * 2) ^ (mrow & 7)) << 4);
+#pragma unroll
+              for (int k = 0; k < 8; k += 2)
+                stsm4t(pa + k * 1024, pack_bf16x2(x[4 * k], x[4 * k + 1]),
+                       pack_bf16x2(x[4 * k + 2], x[4 * k + 3]),
+                       pack_bf16x2(x[4 * k + 4], x[4 * k + 5]),
+                       pack_bf16x2(x[4 * k + 6], x[4 * k + 7]));
+            }
+          }
+          // the vote also keeps the team's warps within one job of each other
+          const bool raise = named_sync_or(bar, 128, !ok || top > kExceed);
+          if (!raise) {
+#pragma unroll
+            for (int e = 0; e < 32; e++) l[e] += ls[e];
+            break;
+          }
           ok = named_sync_and(bar, 128, ok);
           if (!ok) break;
-          {
-            float cm[2 * NB];
+#pragma unroll 1
+          for (int ch = 0; ch < 2; ch++) {
+            float cm[16];
 #pragma unroll
-            for (int e = 0; e < 2 * NB; e++) cm[e] = -INFINITY;
-            float zero[2 * NB];
-#pragma unroll
-            for (int e = 0; e < 2 * NB; e++) zero[e] = 0.f;
+            for (int e = 0; e < 16; e++) cm[e] = -INFINITY;
 #pragma unroll 1
             for (int hf = 0; hf < 2; hf++) {
-              uint32_t y[4 * NB];
-              float x[4 * NB];
-              tmem_frag<NB>(ts + ((uint32_t)(16 * hf) << 16), y);
-              tmem_wait(y);
-              tree_exponents<NB>(y, zs, zero, masked, see[hf], x);
+              uint32_t z[32];
+              tmem_frag<8>(ts + ((uint32_t)(16 * hf) << 16) + 64 * ch, z);
+              tmem_wait(z);
 #pragma unroll
-              for (int k = 0; k < NB; k++) {
-                cm[2 * k] = max3(cm[2 * k], x[4 * k], x[4 * k + 2]);
-                cm[2 * k + 1] = max3(cm[2 * k + 1], x[4 * k + 1], x[4 * k + 3]);
-              }
+              for (int e = 0; e < 32; e++)
+                cm[(e >> 2) * 2 + (e & 1)] = fmaxf(cm[(e >> 2) * 2 + (e & 1)], __uint_as_float(z[e]) * zs);
             }
 #pragma unroll
-            for (int e = 0; e < 2 * NB; e++) {
+            for (int e = 0; e < 16; e++) {
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1)
                 cm[e] = fmaxf(cm[e], __shfl_xor_sync(0xFFFFFFFFu, cm[e], o));
-              if (lane < 4) scr[quarter * CW + (e >> 1) * 8 + 2 * lane + (e & 1)] = cm[e];
+              if (lane < 4) scr[quarter * 128 + 64 * ch + (e >> 1) * 8 + 2 * lane + (e & 1)] = cm[e];
             }
           }
           named_sync(bar, 128);
-          if (wt < cols) {
-            const float was = -nb[wt];
-            const float m = fmaxf(fmaxf(scr[wt], scr[CW + wt]), fmaxf(scr[2 * CW + wt], scr[3 * CW + wt]));
-            const float now = fmaxf(was, m);
-            scr[4 * CW + wt] = ex2(was - now);
-            nb[wt] = -now;
+          {
+            float f = 1.f;
+            if (wt < cols) {
+              const float was = -nb[wt];
+              const float m =
+                  fmaxf(fmaxf(scr[wt], scr[128 + wt]), fmaxf(scr[256 + wt], scr[384 + wt]));
+              const float now = fmaxf(was, m);
+              f = ex2(was - now);
+              nb[wt] = -now;
+            }
+            scr[512 + wt] = f;
           }
           named_sync(bar, 128);
-          const float *fac = scr + 4 * CW;
-          nb_top = -INFINITY;
+          const float *fac = scr + 512;
 #pragma unroll
-          for (int e = 0; e < 2 * NB; e++) {
+          for (int e = 0; e < 32; e++) {
             const int x = 8 * (e >> 1) + 2 * (lane & 3) + (e & 1);
             if (x < cols) {
               l[e] *= fac[x];
               nbr[e] = nb[x];
-              nb_top = fmaxf(nb_top, nbr[e]);
             }
           }
-          if (t > t0) {
+          if (!fresh) {  // O's lanes are the team's rows
+            const float f = fac[quarter * 32 + lane];
 #pragma unroll 1
-            for (int cc = 0; cc < cols; cc += 16) {
+            for (int cc = 0; cc < D; cc += 16) {
               float v[16];
-              tmem_ld16(tmem_o + lanes + c0 + cc, v);
+              tmem_ld16(to + cc, v);
 #pragma unroll
-              for (int e = 0; e < 16; e++)
-                if (cc + e < cols) v[e] *= fac[cc + e];
-              tmem_st16(tmem_o + lanes + c0 + cc, v);
+              for (int e = 0; e < 16; e++) v[e] *= f;
+              tmem_st16(to + cc, v);
             }
           }
           named_sync(bar, 128);  // the factors are read before P replaces them
-        } else if (sc >= (uint32_t)p.PB) {
-          const uint32_t u = sc - p.PB;  // P's buffer is free
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.pvdone + (u & 1)), (u >> 1) & 1,
-                                                         &sm.failed));
         }
-        // pass 2: the weights
-        if (ok) {
-          const uint32_t pbase = (base_u + at.p) + (sc % p.PB) * p_bytes;
-          auto weights = [&](int hf, const uint32_t (&zz)[4 * NB]) {
-            float w[4 * NB];
-            tree_exponents<NB>(zz, zs, nbr, masked, see[hf], w);
-#pragma unroll
-            for (int e = 0; e < 4 * NB; e++) w[e] = ex2(w[e]);
-#pragma unroll
-            for (int k = 0; k < NB; k++) {
-              l[2 * k] += w[4 * k] + w[4 * k + 2];
-              l[2 * k + 1] += w[4 * k + 1] + w[4 * k + 3];
-            }
-            const int ch = mchunk + hf * 2;
-            const uint32_t pa = pbase + (ch >> 3) * (a.rows * 128) + mrow * 128 +
-                                (((ch & 7) ^ (mrow & 7)) << 4);
-#pragma unroll
-            for (int k = 0; k < NB; k += 2)
-              if (8 * k < cols)
-                stsm4t(pa + k * 1024,
-                       pack_bf16x2(w[4 * k], w[4 * k + 1]), pack_bf16x2(w[4 * k + 2], w[4 * k + 3]),
-                       pack_bf16x2(w[4 * k + 4], w[4 * k + 5]), pack_bf16x2(w[4 * k + 6], w[4 * k + 7]));
-          };
-          if constexpr (kKeep) {
-            weights(0, z[0]);
-            weights(1, z[kKeep]);
-          } else {
-#pragma unroll 1
-            for (int hf = 0; hf < 2; hf++) {
-              tmem_frag<NB>(ts + ((uint32_t)(16 * hf) << 16), z[0]);
-              tmem_wait(z[0]);
-              weights(hf, z[0]);
-            }
-          }
-        } else {
-          sm.failed = 1;
-        }
+        if (!ok) break;
         tc_fence_before();
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(smem_u32(sm.sfree + b));
-          mbar_arrive(smem_u32(sm.pready + (sc & 1)));
+          mbar_arrive(smem_u32(sm.sfree + team));
+          mbar_arrive(smem_u32(sm.pready + team));
         }
+        fresh = false;
       }
       // ---- the run's result: sums over the key lanes, then O
-      const uint32_t pv = sc - 1;
-      if (ok)
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.pvdone + (pv & 1)), (pv >> 1) & 1,
+      if (ok && !fresh)
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.pvdone + team), (sc - 1) & 1,
                                                        &sm.failed));
       ok = named_sync_and(bar, 128, ok);
-      if (!ok) break;
       tc_fence_after();
-      // (P is free: its last product is done)
+      // (max, sum) per row in the second half of P, free like the first (its last
+      // product is done)
+      float2 *ml = reinterpret_cast<float2 *>(p_team + kTtP / 2);
+      if (ok) {
 #pragma unroll
-      for (int e = 0; e < 2 * NB; e++) {
-        float x = l[e];
+        for (int e = 0; e < 32; e++) {
+          float x = l[e];
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
-        if (lane < 4) scr[quarter * CW + 8 * (e >> 1) + 2 * lane + (e & 1)] = x;
+          for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+          if (lane < 4) scr[quarter * 128 + 8 * (e >> 1) + 2 * lane + (e & 1)] = x;
+        }
       }
       named_sync(bar, 128);
+      if (ok) {
+        const float sum = (scr[wt] + scr[128 + wt]) + (scr[256 + wt] + scr[384 + wt]);
+        const bool any = wt < cols && (sum > 0.f || sum != sum);
+        ml[wt] = make_float2(any ? -nb[wt] : -INFINITY, any ? sum : 0.f);
+      }
+      ok = named_sync_and(7, kTtSoft * 32, ok);
+      if (!ok) break;
+      // every warp: its quarter's row of each team, half of the columns
+      const int lr = quarter * 32 + lane;
+      const float2 *mls = reinterpret_cast<const float2 *>(base + kTtHead + kTtP / 2) + lr;
+      const float2 ml0 = mls[0], ml1 = mls[kTtP / 8];
+      named_sync(7, kTtSoft * 32);
       const bool whole = t0 == 0 && t1 == pos.n_kt;
       const int64_t slot = 2 * (int64_t)blockIdx.x + (pos.g != pos.run0);
-      if (wt < cols) {
-        const float sum = (scr[wt] + scr[CW + wt]) + (scr[2 * CW + wt] + scr[3 * CW + wt]);
-        const float m = sum > 0.f || sum != sum ? -nb[wt] : -INFINITY;
-        const int x = rt * a.rstep + c0 + wt;
-        if (whole) {
-          const int64_t qr = (int64_t)(pos.q0 + x / a.G) * a.Hq + h * a.G + x % a.G;
-          a.lse[qr] = m == -INFINITY ? -INFINITY : (m + log2f(sum)) * kLn2;
-        } else {
-          a.part_ml[slot * a.rows + c0 + wt] = make_float2(m, sum);
-        }
-        scr[4 * CW + wt] = whole ? (m == -INFINITY ? 0.f : 1.f / sum) : 1.f;
-      }
-      named_sync(bar, 128);
-      const float *fac = scr + 4 * CW;
-      const int d = D == 64 ? key & 63 : key;
+      const int h = pos.h();
       const bool odd = sm.odd != 0;
+      constexpr int W = D / 2;  // columns per warp
+      const int d0 = team * W;
 #pragma unroll 1
-      for (int cc = 0; cc < cols; cc += 16) {
-        float v[16];
-        tmem_ld16(tmem_o + lanes + c0 + cc, v);
-        if (odd) {  // infinities and NaN of the nodes this run covered, to the rows that see them
-#pragma unroll 1
-          for (int jn = max(0, t0 * kTtKeys - pos.c); jn < min(pos.T, t1 * kTtKeys - pos.c); jn++) {
-            const int pn = pos.c + jn;
-            const int32_t bn = bt[pn / a.BS];
-            if (bn < 0 || bn >= n_blocks) continue;
-            const float vn = bf16_lo(a.vpool[(((int64_t)bn * a.BS + pn % a.BS) * a.H + h) * D + d]);
-            if (fabsf(vn) < INFINITY) continue;
-#pragma unroll
-            for (int e = 0; e < 16; e++) {
-              const int i = (rt * a.rstep + c0 + cc + e) / a.G;
-              if (i >= pos.T) continue;
-              const bool see = a.mask ? (a.mask[(int64_t)(pos.q0 + i) * a.mask_words + (jn >> 5)] >> (jn & 31)) & 1u
-                                      : jn <= i;
-              if (see) v[e] += vn;
-            }
-          }
+      for (int part = 0; part < (halves ? 2 : 1); part++) {
+        const int row = part * 128 + lr;
+        if (part * 128 + quarter * 32 >= n_rows) break;  // warp-uniform
+        // one team's rows, or both teams' shares of the same rows
+        const float2 mlp = part ? ml1 : ml0;
+        const float m = halves ? mlp.x : fmaxf(ml0.x, ml1.x);
+        const float m_use = m == -INFINITY ? 0.f : m;
+        float f0, f1 = 0.f, sum;
+        if (halves) {
+          f0 = 1.f;
+          sum = mlp.y;
+        } else {
+          f0 = ex2(ml0.x - m_use);
+          f1 = ex2(ml1.x - m_use);
+          sum = fmaf(ml0.y, f0, ml1.y * f1);
         }
-        if (D == 64 && key >= 64) continue;  // (the second copy of V)
-        if (whole) {
-          int x = rt * a.rstep + c0 + cc, i = x / a.G, gg = x % a.G;
-          uint16_t *o = a.out + ((int64_t)(pos.q0 + i) * a.Hq + h * a.G + gg) * D + d;
+        if (m == -INFINITY) f0 = f1 = 0.f;
+        const float inv = whole ? (m == -INFINITY ? 0.f : 1.f / sum) : 1.f;
+        const bool two = !halves && t1 - t0 > 1;
+        const int x = pos.rt() * a.rstep + row, i = x / a.G;
+        const int64_t qr = (int64_t)(pos.q0 + i) * a.Hq + h * a.G + x % a.G;
+        const bool mine = row < n_rows;
+#pragma unroll 1
+        for (int cc = 0; cc < W; cc += 16) {
+          float v[16], u[16];
+          tmem_ld16(tmem + 256 + (halves ? part * 128 : 0) + lanes + d0 + cc, v);
+          if (two) tmem_ld16(tmem + 256 + 128 + lanes + d0 + cc, u);
 #pragma unroll
           for (int e = 0; e < 16; e++) {
-            if (cc + e < cols) {
-              const float f = fac[cc + e];
-              const __nv_bfloat16 ob = __float2bfloat16(f == 0.f ? 0.f : v[e] * f);
-              *o = *reinterpret_cast<const uint16_t *>(&ob);
-              o += D;
-              if (++gg == a.G) {
-                gg = 0;
-                o += (int64_t)(a.Hq - a.G) * D;
+            v[e] = f0 == 0.f ? 0.f : v[e] * f0;
+            if (two && f1 != 0.f) v[e] = fmaf(u[e], f1, v[e]);
+          }
+          if (odd && mine) {  // infinities and NaN of the nodes this run covered that the row sees
+            const int j1 = min(pos.T, t1 * kTtKeys - pos.c);
+#pragma unroll 1
+            for (int jn = max(0, t0 * kTtKeys - pos.c); jn < j1; jn++) {
+              const bool see_n = a.mask ? (a.mask[(int64_t)(pos.q0 + i) * a.mask_words + (jn >> 5)] >> (jn & 31)) & 1u
+                                        : jn <= i;
+              const int pn = pos.c + jn, pg = page_of(pn, a.bs_inv);
+              const int32_t bn = bt[pg];
+              if (!see_n || bn < 0 || bn >= n_blocks) continue;
+              const uint16_t *vr =
+                  a.vpool + (((int64_t)bn * a.BS + pn - pg * a.BS) * a.H + h) * D + d0 + cc;
+#pragma unroll
+              for (int e = 0; e < 16; e++) {
+                const float vn = bf16_lo(vr[e]);
+                if (!(fabsf(vn) < INFINITY)) v[e] += vn;
               }
             }
           }
-        } else {
-          float *o = a.part_o + (slot * a.rows + c0 + cc) * D + d;
+          if (!mine) continue;
+          if (whole) {
+            uint4 o[2];
+            uint32_t *ow = reinterpret_cast<uint32_t *>(o);
 #pragma unroll
-          for (int e = 0; e < 16; e++)
-            if (cc + e < cols) o[e * D] = v[e];
+            for (int e = 0; e < 8; e++) ow[e] = pack_bf16x2(v[2 * e] * inv, v[2 * e + 1] * inv);
+            uint4 *dst = reinterpret_cast<uint4 *>(a.out + qr * D + d0 + cc);
+            dst[0] = o[0];
+            dst[1] = o[1];
+          } else {
+            float4 *dst = reinterpret_cast<float4 *>(a.part_o + (slot * a.rows + row) * D + d0 + cc);
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+              dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          }
+        }
+        if (mine && d0 == 0) {
+          if (whole) a.lse[qr] = m == -INFINITY ? -INFINITY : (m + log2f(sum)) * kLn2;
+          else a.part_ml[slot * a.rows + row] = make_float2(m, sum);
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.ofree));
-      qc++;
       pos.next(a);
     }
     if (!ok) {
@@ -1276,10 +1281,12 @@ bool ok = true;
   if (sm.failed && tid == 0) {
     record_error(a.status, KVC_ERR_TIMEOUT);
     // let this CTA's copies and products finish before its memory is released
-    for (int i = 0; i < p.NS; i++) {
-      mbar_drain(smem_u32(sm.full + i), 0);
-      mbar_drain(smem_u32(sm.full + i), 1);
+    for (int i = 0; i < 2 * kTtSlots; i++) {
+      mbar_drain(smem_u32(sm.full[0] + i), 0);
+      mbar_drain(smem_u32(sm.full[0] + i), 1);
     }
+    mbar_drain(smem_u32(&sm.qfull), 0);
+    mbar_drain(smem_u32(&sm.qfull), 1);
     for (int i = 0; i < 2; i++) {
       mbar_drain(smem_u32(sm.sfull + i), 0);
       mbar_drain(smem_u32(sm.sfull + i), 1);
@@ -1288,7 +1295,7 @@ bool ok = true;
     }
   }
   __syncthreads();
-  if (warp == nsw + kTtProd) {
+  if (warp == kTtSoft + 4) {
     tc_fence_after();
     free_tmem_cols(tmem, 512);
   }
@@ -1401,15 +1408,16 @@ bool q_map(CUtensorMap *m, const void *q, int n_q, int Hq, int D, int G, int nod
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int CW>
+template <int D>
 cudaError_t launch_tc(const TreeArgs &a, cudaStream_t s) {
   constexpr size_t kSmemMax = 232448;
   TreeTc p;
-  p.NW = (a.rows + CW - 1) / CW;
-  p.PB = a.rows <= 128 ? 2 : 1;
-  p.SB = 3 * a.rows <= 512 ? 2 : 1;
-  for (p.NS = kTtSlots; p.NS > 3; p.NS--)
-    if (1024 + TreeTcSmem(D, a.rows, p.NS, p.PB).bytes <= kSmemMax) break;
+  // V is held longer than K (until the second team's product with it)
+  for (int n = 2 * kTtSlots;; n--) {
+    p.NK = n / 2;
+    p.NV = n - p.NK;
+    if (n == 3 || 1024 + TreeTcSmem(D, a.rows, p.NK, p.NV).bytes <= kSmemMax) break;
+  }
   CUtensorMap tm_k{}, tm_v{}, tm_q{};
   p.box = a.BS % 32 == 0 ? 32 : a.BS % 16 == 0 ? 16 : a.BS % 8 == 0 ? 8 : 0;
   if (p.box && !(pool_map(&tm_k, a.kpool, a.n_slots, a.H, D, p.box) &&
@@ -1418,12 +1426,20 @@ cudaError_t launch_tc(const TreeArgs &a, cudaStream_t s) {
   p.q_nodes = a.rstep / a.G;
   if (!q_map(&tm_q, a.q, a.n_q, a.Hq, D, a.G, p.q_nodes)) return cudaErrorUnknown;
   p.idesc_s = make_idesc(128, 0);
-  p.idesc_o = make_idesc(128, 0) | (1u << 15);  // A (V) MN-major
-  const size_t smem = 1024 + TreeTcSmem(D, a.rows, p.NS, p.PB).bytes;
-  cudaError_t e = cudaFuncSetAttribute(k_tree_tc<D, CW>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  p.idesc_o = make_idesc(128, D) | (1u << 16);  // B (V) MN-major
+  const size_t smem = 1024 + TreeTcSmem(D, a.rows, p.NK, p.NV).bytes;
+  cudaError_t e =
+      cudaFuncSetAttribute(k_tree_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  k_tree_tc<D, CW><<<a.n_cta, (p.NW * 4 + kTtProd + 1) * 32, smem, s>>>(tm_k, tm_v, tm_q, a, p);
+  static int regs = 0;  // a thread's registers at launch
+  if (!regs) {
+    cudaFuncAttributes fa{};
+    if ((e = cudaFuncGetAttributes(&fa, k_tree_tc<D>)) != cudaSuccess) return e;
+    regs = fa.numRegs;
+  }
+  // setmaxnreg.inc draws on what the block was launched with
+  if (regs * kTtThreads < 256 * (kTtMore + kTtLess)) return cudaErrorLaunchOutOfResources;
+  k_tree_tc<D><<<a.n_cta, kTtThreads, smem, s>>>(tm_k, tm_v, tm_q, a, p);
   return cudaGetLastError();
 }
 
@@ -1473,15 +1489,15 @@ cudaError_t launch_tree_attn(const uint16_t *q, const uint16_t *kpool, const uin
   a.Hq = Hq;
   a.G = Hq / H;
   a.BS = BS;
-  a.zscale = scale * kLog2e;
+  a.bs_inv = page_inverse(BS);
+  a.zscale = scale != 0.f ? scale * kLog2e : 1e-30f;  // (so that −inf stays −inf when scaled)
   int max_rt;
   tree_plan(n_req, max_blocks, max_tree, H, Hq, D, BS, a.rows, a.rstep, a.tile, a.n_cta, max_rt);
   a.part_o = reinterpret_cast<float *>(ws);
   a.part_ml = reinterpret_cast<float2 *>(a.part_o + (size_t)2 * a.n_cta * a.rows * D);
   cudaError_t e;
   if (a.tile == kTtKeys && max_tree * a.G > kRowsMax)
-    e = D == 128 ? (a.rows <= 128 ? launch_tc<128, 32>(a, s) : launch_tc<128, 64>(a, s))
-                 : (a.rows <= 128 ? launch_tc<64, 32>(a, s) : launch_tc<64, 64>(a, s));
+    e = D == 128 ? launch_tc<128>(a, s) : launch_tc<64>(a, s);
   else
     e = D == 128 ? (a.rows == 16 ? launch_rows<128, 1>(a, s) : launch_rows<128, 2>(a, s))
                  : (a.rows == 16 ? launch_rows<64, 1>(a, s) : launch_rows<64, 2>(a, s));

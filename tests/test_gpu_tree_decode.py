@@ -161,6 +161,15 @@ def test_attn_long_context(kvc, T, G, kind, BS):
     check(kvc, Tree(5, [5000, 3, 1700, 0, 9000], [T] * 5, 2, G, 128, BS, kind))
 
 
+@pytest.mark.parametrize("D,BS,G,T", [(128, 16, 4, (64, 20, 33, 9)), (64, 8, 8, (30, 12, 17, 5)),
+                                      (128, 12, 4, (40, 64, 10, 25)), (128, 32, 4, (30, 9, 16, 31))])
+def test_attn_many_units(kvc, D, BS, G, T):
+    """More (request, head) units than CTAs, trees of very different size: a CTA works on several in
+    turn, with one or two teams' rows each."""
+    ctx = [300 + 37 * r for r in range(16)]
+    check(kvc, Tree(D + BS, ctx, [T[r % 4] for r in range(16)], 12, G, D, BS))
+
+
 def test_attn_longest_tree(kvc):
     check(kvc, Tree(3, [10], [1024], 1, 1, 64, 16, "chain"))
 
