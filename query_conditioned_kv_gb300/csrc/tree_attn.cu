@@ -488,9 +488,14 @@ k_tree_rows(TreeArgs a) {
 // first gets −inf written into Sᵀ where a row does not see a key, so the loop
 // over the tiles has no masks.
 //
-// Warps: 0–7 softmax; 8–9 load K (64 keys each; 8 the queries too), 10–11
-// load V: TMA boxes of whole page rows, or cp.async row by row where a tile
+// Warps: 0–7 softmax; 8–11 load K and V, 32 keys of a tile each (8 the queries
+// too): TMA boxes of whole page rows, or cp.async row by row where a tile
 // holds nodes, the end, or a page size has no box; 12 issues Sᵀ, 13 issues O.
+// K and V share one ring of NS slots, filled in the order K0 K1 V0 K2 V1 …:
+// with three slots (256 rows leave no room for more) a tile's K and V still
+// have about a tile's time to arrive.  The barriers are per kind, not per
+// slot: a barrier's parity tells only two uses apart, and two consumers of one
+// ring may be further apart than that.
 
 constexpr int kTtKeys = 128;
 constexpr int kTtSoft = 8;
@@ -500,18 +505,18 @@ constexpr float kUnset = -1e30f;   // reference of a row that has seen nothing
 constexpr float kExceed = 30.f;    // log2 of how far a logit may pass the reference
 
 struct TreeTc {
-  int NK, NV;  // slots of the K ring, of the V ring
+  int NS;      // ring slots: 3 or 4
   int box;     // rows of a TMA box (a divisor of the page size), 0: no TMA
   int q_nodes; // nodes of a row tile
   uint32_t idesc_s, idesc_o;  // idesc_s without N
 };
 
-constexpr int kTtSlots = 4;  // slots of a ring, at most
+constexpr int kTtSlots = 4;  // ring slots, at most; barriers of a kind
 
 // Head of the dynamic shared memory, at fixed offsets (few live registers);
-// then P of both teams, the K ring, the V ring and q.
+// then P of both teams, the ring and q.
 struct TreeTcHead {
-  uint64_t full[2][kTtSlots], empty[2][kTtSlots];  // [K, V]
+  uint64_t full[2][kTtSlots], empty[2][kTtSlots];  // [K, V][tile mod kTtSlots]
   uint64_t qfull, qempty;
   uint64_t sfull[2], sfree[2], pready[2], pvdone[2], ofree;  // [team]
   int64_t scan[66];
@@ -525,14 +530,17 @@ constexpr uint32_t kTtP = 128 * kTtKeys * 2;  // bytes of a team's P: [key half]
 
 // Byte offsets (multiples of 1024) from the head.
 struct TreeTcSmem {
-  uint32_t ring[2], q, bytes;
-  __host__ __device__ TreeTcSmem(int D, int rows, int NK, int NV) {
-    ring[0] = kTtHead + 2 * kTtP;
-    ring[1] = ring[0] + NK * kTtKeys * D * 2;
-    q = ring[1] + NV * kTtKeys * D * 2;
+  uint32_t ring, q, bytes;
+  __host__ __device__ TreeTcSmem(int D, int rows, int NS) {
+    ring = kTtHead + 2 * kTtP;
+    q = ring + NS * kTtKeys * D * 2;
     bytes = q + rows * D * 2;
   }
 };
+
+// Place of K tile t and V tile t of a run of nT tiles among its 2·nT stages.
+__device__ __forceinline__ int stage_k(int t) { return t == 0 ? 0 : 2 * t - 1; }
+__device__ __forceinline__ int stage_v(int t, int nT) { return t < nT - 1 ? 2 * t + 2 : 2 * nT - 1; }
 
 // MN-major operand with the 128-byte swizzle: 64 MN elements (128 B) by 8 K
 // rows per 1024-byte atom; atoms along K are 1024 B apart, along MN `lbo`.
@@ -673,7 +681,7 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
   uint8_t *base = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   TreeTcHead &sm = *reinterpret_cast<TreeTcHead *>(base);
-  const TreeTcSmem at(D, a.rows, p.NK, p.NV);
+  const TreeTcSmem at(D, a.rows, p.NS);
   const uint32_t base_u = smem_u32(base);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -683,7 +691,7 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
     sm.odd = 0;
     sm.bad = 0;
     for (int i = 0; i < 2 * kTtSlots; i++) {
-      mbar_init(smem_u32(sm.full[0] + i), 64);
+      mbar_init(smem_u32(sm.full[0] + i), 128);
       mbar_init(smem_u32(sm.empty[0] + i), 1);
     }
     mbar_init(smem_u32(&sm.qfull), 1);
@@ -728,20 +736,15 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
   if (warp >= kTtSoft && warp < kTtSoft + 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTtLess));
     // ------------------------------------------------------- producers
-    // (two warps each for K and V, 64 keys a warp: issuing a tile's boxes takes
-    // one warp longer than the tile lasts.  K and V have a ring each, filled in
-    // order: a slot's parity only tells its next two uses apart)
-    const bool is_v = warp >= kTtSoft + 2;
-    const int key0 = (warp & 1) * 64;  // this warp's keys of a tile
-    const uint16_t *pool = is_v ? a.vpool : a.kpool;
-    const CUtensorMap *tm = is_v ? &tm_v : &tm_k;
+    const int key0 = (warp & 3) * 32;  // this warp's keys of a tile
     const int64_t n_blocks = a.n_slots / a.BS;
-    constexpr int RPI = 32 / CH, NU = 2;
+    constexpr int RPI = 32 / CH;
     const int col = lane % CH;
-    const uint32_t n_slot = is_v ? p.NV : p.NK;
-    uint64_t *full = sm.full[is_v], *empty = sm.empty[is_v];
-    const uint32_t ring = base_u + (is_v ? at.ring[1] : at.ring[0]);
-    uint32_t rc = 0, qc = 0;  // stages filled, runs done
+    uint32_t rc = 0, qc = 0;            // stages filled, runs done
+    uint32_t kc = 0, vc = 0;            // K tiles, V tiles filled
+    uint32_t before[kTtSlots];          // what the last stages held: 2·tile + kind
+#pragma unroll
+    for (int i = 0; i < kTtSlots; i++) before[i] = 0;
     uint32_t pend = 0;  // a stage copied by cp.async and not yet handed over
     auto flush = [&]() {
       if (!pend) return;
@@ -751,129 +754,139 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
       pend = 0;
     };
     // a full ring is waited for only after everything in flight is handed over
-    auto acquire = [&](uint64_t *bar, uint32_t parity) {
-      if (mbar_try(smem_u32(bar), parity)) return true;
+    auto acquire = [&](uint32_t bar, uint32_t parity) {
+      if (mbar_try(bar, parity)) return true;
       flush();
-      return mbar_wait_bounded(smem_u32(bar), parity, &sm.failed);
+      return mbar_wait_bounded(bar, parity, &sm.failed);
     };
     while (pos.g < pos.run1 && ok) {
       const int t0 = pos.t0, t1 = pos.t1(), h = pos.h(), rt = pos.rt();
       const int32_t *bt = a.block_table + (int64_t)pos.r * a.max_blocks;
       const int end = pos.c + pos.T;
       const uint32_t uh = uniform32(h);
-      int32_t blk[NU];  // block ids of the next tile's keys
+      int32_t blk, slot = -1;  // block id of the next tile's key, slot of this tile's
       auto fetch = [&](int t) {
+        const int pp = t * kTtKeys + key0 + lane;
+        blk = pp < end && t < t1 ? bt[page_of(pp, a.bs_inv)] : 0;
+      };
+      auto resolve = [&](int t) {
+        const int pp = t * kTtKeys + key0 + lane;
+        slot = -1;
+        if (pp < end) {
+          if (blk >= 0 && blk < n_blocks) {
+            slot = blk * a.BS + pp - page_of(pp, a.bs_inv) * a.BS;
+          } else {
+            sm.bad = 1;  // (read by the softmax warps after this stage's product)
+            record_error(a.status, KVC_ERR_BOUNDS);
+          }
+        }
+      };
+      // One stage: tile t of K or V, this warp's keys in `slot`.
+      auto load = [&](int t, bool is_v, int32_t slot) {
+        // the ring slot's last use has been consumed
+        const uint32_t was = p.NS == 3 ? before[2] : before[3];
+        if (rc >= (uint32_t)p.NS &&
+            !(ok = acquire(smem_u32(sm.empty[was & 1] + (was >> 1) % kTtSlots),
+                           ((was >> 1) / kTtSlots) & 1)))
+          return;
+        const uint32_t c = is_v ? vc++ : kc++;
 #pragma unroll
-        for (int u = 0; u < NU; u++) {
-          const int pp = t * kTtKeys + key0 + u * 32 + lane;
-          blk[u] = pp < end && t < t1 ? bt[page_of(pp, a.bs_inv)] : 0;
+        for (int i = kTtSlots - 1; i > 0; i--) before[i] = before[i - 1];
+        before[0] = 2 * c + is_v;
+        const uint32_t slot0 = base_u + at.ring + (rc % p.NS) * kSlot + key0 * 128;
+        rc++;
+        const uint32_t bar = smem_u32(sm.full[is_v] + c % kTtSlots);
+        // TMA boxes of whole page rows where every key is cached, else row by
+        // row with cp.async (zeros past the end)
+        if (p.box > 0 && (t + 1) * kTtKeys <= pos.c && __all_sync(0xFFFFFFFFu, slot >= 0)) {
+          if (lane == 0) mbar_expect_tx(bar, kSlot / 4);
+          else mbar_arrive(bar);
+          __syncwarp();
+          // (warp-uniform operands, one lane enabled: see the MMA warps)
+          const uint32_t ubar = uniform32(bar), udst = uniform32(slot0);
+          const CUtensorMap *tm = is_v ? &tm_v : &tm_k;
+          for (int k = 0; k < 32; k += p.box) {  // a box's first key
+            const uint32_t sl = __shfl_sync(0xFFFFFFFFu, slot, k);
+#pragma unroll
+            for (int kb = 0; kb < KB; kb++)
+              tma_load_3d_if(lane == 0, udst + k * 128 + kb * (kTtKeys * 128), tm, kb * 64, uh, sl, ubar);
+          }
+          return;
+        }
+        flush();
+        const uint16_t *pool = is_v ? a.vpool : a.kpool;
+        const uint32_t dst = slot0 + (col >> 3) * (kTtKeys * 128);
+#pragma unroll 4
+        for (int k = 0; k < 32 / RPI; k++) {
+          const int row = k * RPI + lane / CH;
+          const int32_t sl = __shfl_sync(0xFFFFFFFFu, slot, row);
+          cp_async16(dst + row * 128 + (((col & 7) ^ (row & 7)) << 4),
+                     pool + ((int64_t)max(sl, 0) * a.H + h) * D + col * 8, sl >= 0);
+        }
+        cp_commit();
+        pend = bar;
+        if (is_v && (t + 1) * kTtKeys > pos.c) {
+          // A node's V may hold infinities or NaN that some rows do not see: the
+          // product gets zeros in their place, and the run's end adds them to
+          // the rows that do.  Each thread looks at what it copied, before the
+          // stage is handed over.
+          cp_wait<0>();
+          bool odd = false;
+#pragma unroll 1
+          for (int k = 0; k < 32 / RPI; k++) {
+            const int row = k * RPI + lane / CH;
+            const uint32_t ad = dst + row * 128 + (((col & 7) ^ (row & 7)) << 4);
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(ad)
+                         : "memory");
+            bool mine = false;
+#pragma unroll
+            for (int u = 0; u < 4; u++) {
+              if ((w[u] & 0x7F80u) == 0x7F80u) mine = true, w[u] &= 0xFFFF0000u;
+              if ((w[u] & 0x7F800000u) == 0x7F800000u) mine = true, w[u] &= 0xFFFFu;
+            }
+            // (cached positions are seen by every row: their values stay)
+            if (mine && t * kTtKeys + key0 + row >= pos.c) {
+              odd = true;
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(ad), "r"(w[0]),
+                           "r"(w[1]), "r"(w[2]), "r"(w[3])
+                           : "memory");
+            }
+          }
+          if (odd) sm.odd = 1;
+          flush();
         }
       };
       fetch(t0);
       for (int t = t0; t < t1 && ok; t++) {
-        int32_t slot[NU];
-        bool all = true;
-#pragma unroll
-        for (int u = 0; u < NU; u++) {
-          const int pp = t * kTtKeys + key0 + u * 32 + lane;
-          slot[u] = -1;
-          if (pp < end) {
-            if (blk[u] >= 0 && blk[u] < n_blocks) {
-              slot[u] = blk[u] * a.BS + pp - page_of(pp, a.bs_inv) * a.BS;
-            } else {
-              sm.bad = 1;  // (read by the softmax warps after this stage's product)
-              record_error(a.status, KVC_ERR_BOUNDS);
-            }
-          }
-          all &= slot[u] >= 0;
-        }
+        const int32_t slot_v = slot;  // of tile t − 1
+        resolve(t);
         fetch(t + 1);
-        const uint32_t st = rc % n_slot;
-        if (!(ok = acquire(empty + st, ((rc / n_slot) & 1) ^ 1))) break;
-        rc++;
-        const uint32_t slot0 = ring + st * kSlot;
-        const uint32_t bar = smem_u32(full + st);
-        // TMA boxes of whole page rows where every key is cached, else row by
-        // row with cp.async (zeros past the end)
-        if (__all_sync(0xFFFFFFFFu, all) && p.box > 0 && (t + 1) * kTtKeys <= pos.c) {
-          if (lane == 0) mbar_expect_tx(bar, kSlot / 2);
-          else mbar_arrive(bar);
-          __syncwarp();
-          // (warp-uniform operands, one lane enabled: see the MMA warps)
-          const uint32_t ubar = uniform32(bar);
-#pragma unroll
-          for (int u = 0; u < NU; u++)
-            for (int k = 0; k < 32; k += p.box) {  // a box's first key
-              const uint32_t sl = __shfl_sync(0xFFFFFFFFu, slot[u], k);
-              const uint32_t dst = uniform32(slot0 + (key0 + u * 32 + k) * 128);
-#pragma unroll
-              for (int kb = 0; kb < KB; kb++)
-                tma_load_3d_if(lane == 0, dst + kb * (kTtKeys * 128), tm, kb * 64, uh, sl, ubar);
-            }
-        } else {
-          flush();
-          const uint32_t dst = slot0 + (col >> 3) * (kTtKeys * 128);
-#pragma unroll
-          for (int u = 0; u < NU; u++)
-#pragma unroll 4
-            for (int k = 0; k < 32 / RPI; k++) {
-              const int row = k * RPI + lane / CH;
-              const int32_t sl = __shfl_sync(0xFFFFFFFFu, slot[u], row);
-              cp_async16(dst + (key0 + u * 32 + row) * 128 + (((col & 7) ^ (row & 7)) << 4),
-                         pool + ((int64_t)max(sl, 0) * a.H + h) * D + col * 8, sl >= 0);
-            }
-          cp_commit();
-          pend = bar;
-          if (is_v && (t + 1) * kTtKeys > pos.c) {
-            // A node's V may hold infinities or NaN that some rows do not see: the
-            // product gets zeros in their place, and the run's end adds them to
-            // the rows that do.  Each thread looks at what it copied, before the
-            // stage is handed over.
-            cp_wait<0>();
-            bool odd = false;
-#pragma unroll 1
-            for (int k = 0; k < 64 / RPI; k++) {
-              const int row = key0 + k * RPI + lane / CH;
-              const uint32_t ad = dst + row * 128 + (((col & 7) ^ (row & 7)) << 4);
-              uint32_t w[4];
-              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                           : "r"(ad)
-                           : "memory");
-              bool mine = false;
-#pragma unroll
-              for (int u = 0; u < 4; u++) {
-                if ((w[u] & 0x7F80u) == 0x7F80u) mine = true, w[u] &= 0xFFFF0000u;
-                if ((w[u] & 0x7F800000u) == 0x7F800000u) mine = true, w[u] &= 0xFFFFu;
-              }
-              // (cached positions are seen by every row: their values stay)
-              if (mine && t * kTtKeys + row >= pos.c) {
-                odd = true;
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(ad), "r"(w[0]),
-                             "r"(w[1]), "r"(w[2]), "r"(w[3])
-                             : "memory");
-              }
-            }
-            if (odd) sm.odd = 1;
-            flush();
-          }
-        }
-        if (warp == kTtSoft && t == t0) {
+        load(t, false, slot);
+        if (!ok) break;
+        if (t == t0) {
           // the row tile's queries, in one box of nodes × heads of the group; rows
           // past the request's own (another request's, or zeros) are columns that
           // the softmax leaves out
-          if (!(ok = acquire(&sm.qempty, (qc & 1) ^ 1))) break;
-          if (lane == 0) {
-            const uint32_t qbar = smem_u32(&sm.qfull);
-            mbar_expect_tx(qbar, p.q_nodes * a.G * D * 2);
+          if (warp == kTtSoft) {
+            if (!(ok = acquire(smem_u32(&sm.qempty), (qc & 1) ^ 1))) break;
+            if (lane == 0) {
+              const uint32_t qbar = smem_u32(&sm.qfull);
+              mbar_expect_tx(qbar, p.q_nodes * a.G * D * 2);
 #pragma unroll
-            for (int kb = 0; kb < KB; kb++)
-              tma_load_3d(base_u + at.q + kb * (a.rows * 128), &tm_q, kb * 64, h * a.G,
-                          pos.q0 + rt * p.q_nodes, qbar);
+              for (int kb = 0; kb < KB; kb++)
+                tma_load_3d(base_u + at.q + kb * (a.rows * 128), &tm_q, kb * 64, h * a.G,
+                            pos.q0 + rt * p.q_nodes, qbar);
+            }
+            __syncwarp();
           }
-          __syncwarp();
+        } else {
+          load(t - 1, true, slot_v);
         }
       }
+      if (ok) load(t1 - 1, true, slot);
       qc++;
       pos.next(a);
     }
@@ -892,7 +905,8 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
     // of one lane every product cost some 100 cycles to issue.)
     const uint32_t lead = lane == 0;
     const bool first = warp == kTtSoft + 4;  // Sᵀ, or O
-    uint32_t rc = 0, qc = 0;  // tiles of this product's ring used, runs done
+    uint32_t rc = 0, qc = 0;  // stages before this run, runs done
+    uint32_t tc = 0;          // tiles used
     uint32_t done[2];         // jobs issued per team, by bit 0 (constant indexes only)
     done[0] = done[1] = 0;
     while (pos.g < pos.run1 && ok) {
@@ -902,47 +916,49 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
         ok = mbar_wait_bounded(smem_u32(&sm.qfull), qc & 1, &sm.failed);
         const uint64_t qb = uniform64(smem_desc(base_u + at.q));
         const uint32_t qk = (uint32_t)a.rows * 8;  // next 64 columns of q, in 16 bytes
-        const uint32_t n8 = uniform32((min(n_rows, 256) + 15) / 16 * 2);  // N / 8
-        for (int t = 0; t < nT && ok; t++, rc++) {
-          // halves: one product for both teams' rows (Sᵀ of team 1 follows team 0's)
-          const int st = rc % p.NK;
-          const bool t0on = halves || !(t & 1), t1on = halves || (t & 1);
-          ok = mbar_wait_bounded(smem_u32(sm.full[0] + st), (rc / p.NK) & 1, &sm.failed);
-          if (ok && t0on) ok = mbar_wait_bounded(smem_u32(sm.sfree), (done[0] & 1) ^ 1, &sm.failed);
-          if (ok && t1on) ok = mbar_wait_bounded(smem_u32(sm.sfree + 1), (done[1] & 1) ^ 1, &sm.failed);
+        const int nJ = halves ? 2 * nT : nT;
+        for (int j = 0; j < nJ && ok; j++) {
+          const int tm = j & 1, t = halves ? j >> 1 : j, row0 = halves ? 128 * tm : 0;
+          const uint32_t st = tc % kTtSlots;
+          ok = mbar_wait_bounded(smem_u32(sm.full[0] + st), (tc / kTtSlots) & 1, &sm.failed);
+          if (ok)
+            ok = mbar_wait_bounded(smem_u32(sm.sfree + tm), ((tm ? done[1] : done[0]) & 1) ^ 1,
+                                   &sm.failed);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t ka = uniform64(smem_desc(base_u + at.ring[0] + st * kSlot));
-          const uint32_t dst = uniform32(tmem + (t0on ? 0 : 128));
+          const uint64_t ka =
+              uniform64(smem_desc(base_u + at.ring + ((rc + stage_k(t)) % p.NS) * kSlot));
+          const uint32_t dst = uniform32(tmem + tm * 128);
+          const uint32_t n8 = (min(n_rows - row0, 128) + 15) / 16 * 2;  // N / 8
           const uint32_t idesc = uniform32(p.idesc_s | (n8 << 17));
+          const uint64_t qt = qb + uniform32(row0 * 8);
 #pragma unroll
           for (int kk = 0; kk < 4 * KB; kk++)
             mma_bf16_if(lead, dst, ka + (kk >> 2) * (kTtKeys * 8) + (kk & 3) * 2,
-                        qb + (kk >> 2) * qk + (kk & 3) * 2, idesc, kk > 0);
-          if (t0on) {
-            mma_commit_if(lead, smem_u32(sm.sfull));
-            done[0]++;
+                        qt + (kk >> 2) * qk + (kk & 3) * 2, idesc, kk > 0);
+          mma_commit_if(lead, smem_u32(sm.sfull + tm));
+          if (tm) done[1]++;
+          else done[0]++;
+          if (!halves || tm == 1) {
+            mma_commit_if(lead, smem_u32(sm.empty[0] + st));
+            tc++;
           }
-          if (t1on) {
-            mma_commit_if(lead, smem_u32(sm.sfull + 1));
-            done[1]++;
-          }
-          mma_commit_if(lead, smem_u32(sm.empty[0] + st));
-          if (t == nT - 1) mma_commit_if(lead, smem_u32(&sm.qempty));
+          if (j == nJ - 1) mma_commit_if(lead, smem_u32(&sm.qempty));
         }
       } else {
         const int nJ = halves ? 2 * nT : nT;
         for (int j = 0; j < nJ && ok; j++) {
-          const int tm = j & 1, st = rc % p.NV;
-          ok = mbar_wait_bounded(smem_u32(sm.full[1] + st), (rc / p.NV) & 1, &sm.failed);
+          const int tm = j & 1, t = halves ? j >> 1 : j;
+          const uint32_t st = tc % kTtSlots;
+          ok = mbar_wait_bounded(smem_u32(sm.full[1] + st), (tc / kTtSlots) & 1, &sm.failed);
           if (ok && j == 0)  // both O's previous contents have been read
             ok = mbar_wait_bounded(smem_u32(&sm.ofree), (qc & 1) ^ 1, &sm.failed);
           if (ok)
             ok = mbar_wait_bounded(smem_u32(sm.pready + tm), (tm ? done[1] : done[0]) & 1, &sm.failed);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t vb =
-              uniform64(smem_desc_mn(base_u + at.ring[1] + st * kSlot, kTtKeys * 128));
+          const uint64_t vb = uniform64(smem_desc_mn(
+              base_u + at.ring + ((rc + stage_v(t, nT)) % p.NS) * kSlot, kTtKeys * 128));
           const uint64_t pa = uniform64(smem_desc(base_u + kTtHead + tm * kTtP));
           const uint32_t dst = uniform32(tmem + 256 + tm * 128);
 #pragma unroll
@@ -954,10 +970,11 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
           else done[0]++;
           if (!halves || tm == 1) {
             mma_commit_if(lead, smem_u32(sm.empty[1] + st));
-            rc++;
+            tc++;
           }
         }
       }
+      rc += 2 * nT;
       qc++;
       pos.next(a);
     }
@@ -989,14 +1006,11 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
       const int cols = min(128, n_rows - row0);          // its rows
       const int32_t *bt = a.block_table + (int64_t)pos.r * a.max_blocks;
       named_sync(bar, 128);  // the last run's references are read
-      nb[wt] = -kUnset;
-      // −reference and sum of weights of rows 8k + 2·(t%4) + {0, 1}
-      float nbr[32], l[32];
+      nb[wt] = wt < cols ? -kUnset : -INFINITY;  // (columns that hold no row: weight 0)
+      named_sync(bar, 128);
+      float l[32];  // sums of the weights of rows 8k + 2·(t%4) + {0, 1}
 #pragma unroll
-      for (int e = 0; e < 32; e++) {
-        nbr[e] = 8 * (e >> 1) + 2 * (lane & 3) + (e & 1) < cols ? -kUnset : -INFINITY;
-        l[e] = 0.f;
-      }
+      for (int e = 0; e < 32; e++) l[e] = 0.f;
       // A wait that gives up only clears this warp's `ok`; the team leaves
       // together, at the next vote.
       bool fresh = true;
@@ -1041,41 +1055,55 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
         }
         for (;;) {
           // the job's weights on the references at hand, their sums apart from
-          // the run's until the vote
+          // the run's until the vote; 64 rows by 16 keys of the warp at a time,
+          // the next ones on their way from tensor memory meanwhile
           float ls[32], top = -INFINITY;
-#pragma unroll
-          for (int e = 0; e < 32; e++) ls[e] = 0.f;
-          // P of the team's last job has been read, O holds its product
-          if (sc > 0 && ok)
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.pvdone + team), (sc - 1) & 1,
-                                                           &sm.failed));
           if (ok) {
+            uint32_t z[2][32];
+            tmem_frag<8>(ts, z[0]);
+            // P of the team's last job has been read, O holds its product
+            if (sc > 0)
+              ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.pvdone + team), (sc - 1) & 1,
+                                                             &sm.failed));
 #pragma unroll
-            for (int w = 0; w < 4; w++) {
-              const int ch = w & 1, hf = w >> 1;
-              uint32_t z[32];
-              float x[32];
-              tmem_frag<8>(ts + ((uint32_t)(16 * hf) << 16) + 64 * ch, z);
-              tmem_wait(z);
-#pragma unroll
-              for (int e = 0; e < 32; e++)
-                x[e] = fmaf(__uint_as_float(z[e]), zs, nbr[16 * ch + (e >> 2) * 2 + (e & 1)]);
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) top = max3(top, x[e], x[e + 1]);
-#pragma unroll
-              for (int e = 0; e < 32; e++) x[e] = ex2(x[e]);
+            for (int ch = 0; ch < 2; ch++) {
+              float nbr[16];  // −reference of rows 64·ch + 8k + 2·(t%4) + {0, 1}
 #pragma unroll
               for (int k = 0; k < 8; k++) {
-                ls[16 * ch + 2 * k] += x[4 * k] + x[4 * k + 2];
-                ls[16 * ch + 2 * k + 1] += x[4 * k + 1] + x[4 * k + 3];
+                const float2 n2 =
+                    *reinterpret_cast<const float2 *>(nb + 64 * ch + 8 * k + 2 * (lane & 3));
+                nbr[2 * k] = n2.x;
+                nbr[2 * k + 1] = n2.y;
               }
-              const uint32_t pa = pst + ch * 8192 + (((mchunk + hf * 2) ^ (mrow & 7)) << 4);
 #pragma unroll
-              for (int k = 0; k < 8; k += 2)
-                stsm4t(pa + k * 1024, pack_bf16x2(x[4 * k], x[4 * k + 1]),
-                       pack_bf16x2(x[4 * k + 2], x[4 * k + 3]),
-                       pack_bf16x2(x[4 * k + 4], x[4 * k + 5]),
-                       pack_bf16x2(x[4 * k + 6], x[4 * k + 7]));
+              for (int hf = 0; hf < 2; hf++) {
+                const int w = 2 * ch + hf;
+                tmem_wait(z[w & 1]);
+                if (w < 3)
+                  tmem_frag<8>(ts + ((uint32_t)(16 * ((w + 1) & 1)) << 16) + 64 * ((w + 1) >> 1),
+                               z[(w + 1) & 1]);
+                float x[32];
+#pragma unroll
+                for (int e = 0; e < 32; e++)
+                  x[e] = fmaf(__uint_as_float(z[w & 1][e]), zs, nbr[(e >> 2) * 2 + (e & 1)]);
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) top = max3(top, x[e], x[e + 1]);
+#pragma unroll
+                for (int e = 0; e < 32; e++) x[e] = ex2(x[e]);
+#pragma unroll
+                for (int k = 0; k < 8; k++) {
+                  const float s0 = x[4 * k] + x[4 * k + 2], s1 = x[4 * k + 1] + x[4 * k + 3];
+                  ls[16 * ch + 2 * k] = hf ? ls[16 * ch + 2 * k] + s0 : s0;
+                  ls[16 * ch + 2 * k + 1] = hf ? ls[16 * ch + 2 * k + 1] + s1 : s1;
+                }
+                const uint32_t pa = pst + ch * 8192 + (((mchunk + hf * 2) ^ (mrow & 7)) << 4);
+#pragma unroll
+                for (int k = 0; k < 8; k += 2)
+                  stsm4t(pa + k * 1024, pack_bf16x2(x[4 * k], x[4 * k + 1]),
+                         pack_bf16x2(x[4 * k + 2], x[4 * k + 3]),
+                         pack_bf16x2(x[4 * k + 4], x[4 * k + 5]),
+                         pack_bf16x2(x[4 * k + 6], x[4 * k + 7]));
+              }
             }
           }
           // the vote also keeps the team's warps within one job of each other
@@ -1127,10 +1155,7 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
 #pragma unroll
           for (int e = 0; e < 32; e++) {
             const int x = 8 * (e >> 1) + 2 * (lane & 3) + (e & 1);
-            if (x < cols) {
-              l[e] *= fac[x];
-              nbr[e] = nb[x];
-            }
+            if (x < cols) l[e] *= fac[x];
           }
           if (!fresh) {  // O's lanes are the team's rows
             const float f = fac[quarter * 32 + lane];
@@ -1412,12 +1437,7 @@ template <int D>
 cudaError_t launch_tc(const TreeArgs &a, cudaStream_t s) {
   constexpr size_t kSmemMax = 232448;
   TreeTc p;
-  // V is held longer than K (until the second team's product with it)
-  for (int n = 2 * kTtSlots;; n--) {
-    p.NK = n / 2;
-    p.NV = n - p.NK;
-    if (n == 3 || 1024 + TreeTcSmem(D, a.rows, p.NK, p.NV).bytes <= kSmemMax) break;
-  }
+  p.NS = 1024 + TreeTcSmem(D, a.rows, kTtSlots).bytes <= kSmemMax ? kTtSlots : 3;
   CUtensorMap tm_k{}, tm_v{}, tm_q{};
   p.box = a.BS % 32 == 0 ? 32 : a.BS % 16 == 0 ? 16 : a.BS % 8 == 0 ? 8 : 0;
   if (p.box && !(pool_map(&tm_k, a.kpool, a.n_slots, a.H, D, p.box) &&
@@ -1427,7 +1447,7 @@ cudaError_t launch_tc(const TreeArgs &a, cudaStream_t s) {
   if (!q_map(&tm_q, a.q, a.n_q, a.Hq, D, a.G, p.q_nodes)) return cudaErrorUnknown;
   p.idesc_s = make_idesc(128, 0);
   p.idesc_o = make_idesc(128, D) | (1u << 16);  // B (V) MN-major
-  const size_t smem = 1024 + TreeTcSmem(D, a.rows, p.NK, p.NV).bytes;
+  const size_t smem = 1024 + TreeTcSmem(D, a.rows, p.NS).bytes;
   cudaError_t e =
       cudaFuncSetAttribute(k_tree_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
