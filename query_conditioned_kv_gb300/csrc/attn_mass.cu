@@ -149,22 +149,12 @@ k_mass_rows(MassArgs a, int n_cta_max) {
       if (t0 + s < t1) issue(t0 + s, s);
       cp_commit();
     }
-    // this unit's query rows, their LSE and limits
+    // this unit's rows: LSE and limits, then the queries.  A row that adds
+    // nothing (past the request's rows, no limit, LSE ±inf) gets lse = +inf and
+    // q = 0, so its weight is 0 wherever K is finite; `lo`, the least limit of
+    // the others, tells the tiles that every one of them sees (there a NaN key
+    // is a NaN result in any case).
     const int n_rows = n * a.G;
-    for (int e = tid; e < NT * 8 * CH; e += kMrThreads) {
-      const int row = e / CH, col = e % CH;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (row < n_rows) {
-        const int i = r0 + row / a.G, x = a.row_idx ? a.row_idx[i] : i;
-        if (x >= 0 && x < a.n_q)
-          v = *reinterpret_cast<const uint4 *>(
-              a.q + ((l * a.n_q + x) * a.Hq + h * a.G + row % a.G) * D + col * 8);
-      }
-      *reinterpret_cast<uint4 *>(sm + S::kQ + swz<D>(row, col)) = v;
-    }
-    // Rows that add nothing get lse = +inf, so their weight is 0 wherever K is
-    // finite; `lo`, the least limit of the others, tells the tiles that every
-    // one of them sees (there a NaN key is a NaN result in any case).
     int lo = seq + 1;
     for (int row = tid; row < NT * 8; row += kMrThreads) {
       float ls = INFINITY;
@@ -174,7 +164,7 @@ k_mass_rows(MassArgs a, int n_cta_max) {
         vis = min(a.row_vis[i], seq);
         if (vis > 0 && x >= 0 && x < a.n_q) {
           ls = a.lse[(l * a.n_q + x) * a.Hq + h * a.G + row % a.G] * kLog2e;
-          if (ls == -INFINITY) ls = INFINITY;
+          if (fabsf(ls) == INFINITY) ls = INFINITY;
           else lo = min(lo, vis);
         } else if (vis > 0) {
           record_error(a.status, KVC_ERR_BOUNDS);
@@ -183,9 +173,19 @@ k_mass_rows(MassArgs a, int n_cta_max) {
       lse_s[row] = ls;
       vis_s[row] = ls == INFINITY ? 0 : vis;
     }
-    lo = -(int)block_max(-lo, sh);  // (its barriers publish q, lse and limits)
+    lo = -(int)block_max(-lo, sh);  // (its barriers publish lse and limits)
     if (lo > seq) lo = 0;           // no row adds anything
-
+    for (int e = tid; e < NT * 8 * CH; e += kMrThreads) {
+      const int row = e / CH, col = e % CH;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (lse_s[row] != INFINITY) {
+        const int i = r0 + row / a.G, x = a.row_idx ? a.row_idx[i] : i;
+        v = *reinterpret_cast<const uint4 *>(
+            a.q + ((l * a.n_q + x) * a.Hq + h * a.G + row % a.G) * D + col * 8);
+      }
+      *reinterpret_cast<uint4 *>(sm + S::kQ + swz<D>(row, col)) = v;
+    }
+    __syncthreads();
     uint32_t qf[kQRegs ? KS : 1][NT][2];
     if (kQRegs)
 #pragma unroll
@@ -323,8 +323,7 @@ cudaError_t launch_rows(const MassArgs &a, cudaStream_t s) {
 // tcgen05: D[key][row] = K tile (M 128 keys, A) × row tile (N rows, B), fp32 in
 // tensor memory; epilogue thread = one key (TMEM lane), its columns the rows.
 // Warps 0–7: two epilogue warpgroups, taking the key tiles in turn; 8–11:
-// producers (cp.async with the 128-byte swizzle, so any page size and any
-// row_idx); 12: MMA issue.
+// producers; 12: MMA issue (predicated, from uniform registers).
 //
 // ONE (all rows of a request in one row tile): the rows stay in shared memory
 // while the request's keys stream past; work is dealt out by key tile.
@@ -340,11 +339,15 @@ constexpr int kTcEpi = 8;                       // epilogue warps
 constexpr int kTcProd = 4;                      // producer warps
 constexpr int kTcThreads = (kTcEpi + kTcProd + 1) * 32;
 constexpr int kTcKeys = 128;                    // keys of a tile
+constexpr int kTcMaxK = 8;                      // K slots, at most
 
 struct MassTc {
   int n_cta;        // CTAs the work is dealt out to
-  int NR;           // rows per row tile: 128 or 256
+  int NR;           // rows of a row tile's buffers: 128 or 256
+  int tokens;       // rows i (tokens) of a row tile: tokens·G ≤ NR rows
   int k_slots;      // K ring
+  int box;          // rows of a TMA box of K (a divisor of the page size), 0: none
+  int q_box;        // queries by TMA (no row_idx)
   int max_kg, max_rt;
   uint32_t idesc;
   int64_t *cum;     // [n_req][max_kg + 1]: row tiles before each group (at least one each)
@@ -359,45 +362,27 @@ struct TcShape {
   static constexpr int kLs = ONE ? 2 : 4;   // LSE slots
 };
 
+// Head of the dynamic shared memory (fixed offsets), then K, q, and the LSE
+// slots: −lse·log2e [slot][NR], limits [slot][NR].
+struct TcHead {
+  uint64_t kfull[kTcMaxK], kempty[kTcMaxK], qfull[2], qempty[2], lfull[4], lempty[4];
+  uint64_t tfull[4], tempty[4];
+  int64_t scan[66];
+  int lo[4][4];  // least limit of the slot's rows, per producer warp
+  uint32_t tmem_holder;
+  volatile int failed;
+};
+constexpr uint32_t kTcHead = 1024;
+static_assert(sizeof(TcHead) <= kTcHead, "the head's room");
+
 struct TcSmem {
-  uint8_t *k, *q;
-  float *nlse;  // [kLs][NR]: −lse·log2e
-  int *vis;     // [kLs][NR]
-  int *lo;      // [kLs][4]: least limit, per producer warp
-  uint64_t *kfull, *kempty, *qfull, *qempty, *lfull, *lempty, *tfull, *tempty;
-  int64_t *scan;
-  uint32_t *tmem_holder;
-  volatile int *failed;
-  __host__ __device__ static size_t layout(int D, int NR, int ks, int qs, int ls, TcSmem *o,
-                                           uint8_t *base) {
-    size_t at = 0;
-    auto take = [&](size_t n) {
-      const size_t x = at;
-      at += (n + 15) & ~size_t(15);
-      return base + x;
-    };
-    uint8_t *k = take((size_t)ks * kTcKeys * D * 2), *q = take((size_t)qs * NR * D * 2);
-    uint8_t *nl = take((size_t)ls * NR * 4), *vi = take((size_t)ls * NR * 4), *lo = take(ls * 16);
-    uint8_t *bars = take((2 * ks + 2 * qs + 2 * ls + 8) * 8), *sc = take(66 * 8), *th = take(16);
-    if (o) {
-      o->k = k;
-      o->q = q;
-      o->nlse = reinterpret_cast<float *>(nl);
-      o->vis = reinterpret_cast<int *>(vi);
-      o->lo = reinterpret_cast<int *>(lo);
-      o->kfull = reinterpret_cast<uint64_t *>(bars);
-      o->kempty = o->kfull + ks;
-      o->qfull = o->kempty + ks;
-      o->qempty = o->qfull + qs;
-      o->lfull = o->qempty + qs;
-      o->lempty = o->lfull + ls;
-      o->tfull = o->lempty + ls;
-      o->tempty = o->tfull + 4;
-      o->scan = reinterpret_cast<int64_t *>(sc);
-      o->tmem_holder = reinterpret_cast<uint32_t *>(th);
-      o->failed = reinterpret_cast<volatile int *>(th + 4);
-    }
-    return at;
+  uint32_t k, q, nlse, vis, bytes;
+  __host__ __device__ TcSmem(int D, int NR, int ks, int ls) {
+    k = kTcHead;
+    q = k + ks * kTcKeys * D * 2;
+    nlse = q + 2 * NR * D * 2;
+    vis = nlse + ls * NR * 4;
+    bytes = vis + ls * NR * 4;
   }
 };
 
@@ -483,19 +468,22 @@ __device__ __forceinline__ TcPos<ONE> tc_find(const MassArgs &a, const MassTc &p
 
 template <int D, bool ONE>
 __global__ void __launch_bounds__(kTcThreads, 1)
-k_mass_tc(MassArgs a, MassTc p) {
+k_mass_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
+          MassArgs a, MassTc p) {
   constexpr int KG = TcShape<ONE>::kKG, LS = TcShape<ONE>::kLs, QS = 2;
   constexpr int CH = D / 8, KB = D / 64;
+  constexpr uint32_t kSlot = kTcKeys * D * 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int NR = p.NR, KS = p.k_slots, NACC = 512 / NR;
-  TcSmem sm;
-  TcSmem::layout(D, NR, KS, QS, LS, &sm, base);
+  TcHead &sm = *reinterpret_cast<TcHead *>(base);
+  const TcSmem at(D, NR, KS, LS);
+  const uint32_t base_u = smem_u32(base);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
-    *sm.failed = 0;
+    sm.failed = 0;
     for (int i = 0; i < KS; i++) {
       mbar_init(smem_u32(sm.kfull + i), kTcProd * 32);
       mbar_init(smem_u32(sm.kempty + i), 1);
@@ -514,11 +502,17 @@ k_mass_tc(MassArgs a, MassTc p) {
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kTcEpi + kTcProd) alloc_tmem_cols(sm.tmem_holder, 512);
+  // rows that no row tile fills stay zero
+  if (p.tokens * a.G < NR) {
+    for (uint32_t i = tid; i < 2u * NR * D * 2 / 16; i += kTcThreads)
+      *reinterpret_cast<uint4 *>(base + at.q + i * 16) = make_uint4(0, 0, 0, 0);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == kTcEpi + kTcProd) alloc_tmem_cols(&sm.tmem_holder, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *sm.tmem_holder;
+  const uint32_t tmem = sm.tmem_holder;
 
   if (!ONE) asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan
   int64_t per = 0;
@@ -541,35 +535,50 @@ k_mass_tc(MassArgs a, MassTc p) {
   bool ok = true;
   if (warp >= kTcEpi && warp < kTcEpi + kTcProd) {
     // ------------------------------------------------------- producers
+    // K: 32 keys of a tile a warp, by TMA boxes of whole page rows or row by row
+    // with cp.async (bad blocks, the end, page sizes without a box).  Rows: the
+    // whole tile in one TMA box, or row by row through row_idx; their LSE and
+    // limits through registers, a tile ahead.
     const int pw = warp - kTcEpi;
     const int64_t n_blocks = a.n_slots / a.BS;
+    constexpr int RPI = 32 / CH;
+    const int col = lane % CH;
     uint32_t kc = 0, qc = 0;      // K tiles and row tiles loaded
-    uint32_t pend = 0;            // full barrier of the last stage not yet signalled
+    uint32_t pend0 = 0, pend1 = 0;  // stages copied by cp.async and not handed over, oldest first
     int64_t q_unit = -1;
-    auto signal = [&]() {         // the stage's copies have landed: hand them to the tensor core
-      if (!pend) return;
+    auto hand = [&](uint32_t bar) {
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      mbar_arrive(pend);
-      pend = 0;
+      mbar_arrive(bar);
     };
-    // wait for a free slot; a stage whose copies may have landed is signalled
-    // first, so that its consumer never waits for a slot to become free
+    auto flush = [&]() {
+      if (!pend0) return;
+      cp_wait<0>();
+      hand(pend0);
+      if (pend1) hand(pend1);
+      pend0 = pend1 = 0;
+    };
+    auto committed = [&](uint32_t bar) {
+      cp_commit();
+      if (pend1) {
+        cp_wait<2>();
+        hand(pend0);
+        pend0 = pend1;
+        pend1 = bar;
+      } else if (pend0) {
+        pend1 = bar;
+      } else {
+        pend0 = bar;
+      }
+    };
+    // a full ring is waited for only after everything in flight is handed over
     auto acquire = [&](uint64_t *bar, uint32_t parity) {
       if (mbar_try(smem_u32(bar), parity)) return true;
-      if (pend) {
-        cp_wait<0>();
-        signal();
-      }
-      return mbar_wait_bounded(smem_u32(bar), parity, sm.failed);
+      flush();
+      return mbar_wait_bounded(smem_u32(bar), parity, &sm.failed);
     };
-    auto committed = [&](uint64_t *bar) {  // stage issued: signal the one before it
-      cp_commit();
-      if (pend) {
-        cp_wait<1>();
-        signal();
-      }
-      pend = smem_u32(bar);
-    };
+    // this lane's rows of a row tile: lr = 32·pw + 128·u + lane
+    const int tok0 = (32 * pw + lane) / a.G, g0 = (32 * pw + lane) % a.G;
+    const int tok1 = (32 * pw + lane + 128) / a.G, g1 = (32 * pw + lane + 128) % a.G;
     for (int64_t g = run0; g < run1 && ok;) {
       const int todo = (int)min((int64_t)max(pos.cnt, 1) - pos.off, run1 - g);
       if (pos.cnt > 0) {
@@ -577,82 +586,132 @@ k_mass_tc(MassArgs a, MassTc p) {
         mass_request(a, pos.r, seq, r0, n);
         const int32_t *bt = a.block_table + (int64_t)pos.r * a.max_blocks;
         const uint16_t *kl = a.kpool + (pos.l * a.n_slots * a.H + pos.h) * D;
+        const float *lse = a.lse + pos.l * a.n_q * a.Hq + pos.h * a.G;
         const int64_t unit = (pos.l * a.n_req + pos.r) * a.H + pos.h;
+        const uint32_t uh = uniform32(pos.h);
         auto load_k = [&](int kt) {
-          const int st = kc % KS;
-          if (!(ok = acquire(sm.kempty + st, ((kc / KS) & 1) ^ 1))) return;
-          const int pp = (pos.kg * KG + kt) * kTcKeys + pw * 32 + lane;
+          const uint32_t st = kc % KS;
+          const int t = pos.kg * KG + kt, pp = t * kTcKeys + pw * 32 + lane;
           int32_t slot = -1;
           if (pp < seq) {
-            const int32_t b = bt[page_of(pp, a.bs_inv)];
-            if (b >= 0 && b < n_blocks) slot = b * a.BS + pp - page_of(pp, a.bs_inv) * a.BS;
+            const int pg = page_of(pp, a.bs_inv);
+            const int32_t b = bt[pg];
+            if (b >= 0 && b < n_blocks) slot = b * a.BS + pp - pg * a.BS;
             else record_error(a.status, KVC_ERR_BOUNDS);
           }
-          constexpr int RPI = 32 / CH;
-          const int col = lane % CH;
-          const uint32_t dst = smem_u32(sm.k) + st * (kTcKeys * D * 2) + (col >> 3) * (kTcKeys * 128);
+          if (!(ok = acquire(sm.kempty + st, ((kc / KS) & 1) ^ 1))) return;
+          kc++;
+          const uint32_t bar = smem_u32(sm.kfull + st);
+          const uint32_t slot0 = base_u + at.k + st * kSlot + pw * 32 * 128;
+          if (p.box > 0 && __all_sync(0xFFFFFFFFu, slot >= 0)) {
+            if (lane == 0) mbar_expect_tx(bar, kSlot / kTcProd);
+            else mbar_arrive(bar);
+            __syncwarp();
+            const uint32_t ubar = uniform32(bar), udst = uniform32(slot0);
+            const uint32_t row0 = uniform32((uint32_t)(pos.l * a.n_slots));
+            for (int k = 0; k < 32; k += p.box) {
+              const uint32_t sl = __shfl_sync(0xFFFFFFFFu, slot, k);
 #pragma unroll
+              for (int kb = 0; kb < KB; kb++)
+                tma_load_3d_if(lane == 0, udst + k * 128 + kb * (kTcKeys * 128), &tm_k, kb * 64, uh,
+                               row0 + sl, ubar);
+            }
+            return;
+          }
+          const uint32_t dst = slot0 + (col >> 3) * (kTcKeys * 128);
+#pragma unroll 4
           for (int i = 0; i < 32 / RPI; i++) {
             const int row = i * RPI + lane / CH;
             const int32_t sl = __shfl_sync(0xFFFFFFFFu, slot, row);
-            cp_async16(dst + (pw * 32 + row) * 128 + (((col & 7) ^ (row & 7)) << 4),
+            cp_async16(dst + row * 128 + (((col & 7) ^ (row & 7)) << 4),
                        kl + (int64_t)max(sl, 0) * a.H * D + col * 8, sl >= 0);
           }
-          committed(sm.kfull + st);
-          kc++;
+          committed(bar);
         };
-        auto load_q = [&](int rt) {
-          const int st = qc % QS, ls = qc % LS;
-          if (!(ok = acquire(sm.qempty + st, ((qc / QS) & 1) ^ 1))) return;
-          if (!(ok = acquire(sm.lempty + ls, ((qc / LS) & 1) ^ 1))) return;
-          int lo = INT_MAX;
-          for (int b = pw * 32; b < NR; b += kTcProd * 32) {
-            const int row = rt * NR + b + lane;
-            int64_t at = -1;
-            float nl = -INFINITY;
-            int vis = 0;
-            if (row < n * a.G) {
-              const int i = r0 + row / a.G, x = a.row_idx ? a.row_idx[i] : i;
-              vis = min(a.row_vis[i], seq);
-              if (vis > 0) {
-                if (x >= 0 && x < a.n_q) {
-                  at = (pos.l * a.n_q + x) * a.Hq + pos.h * a.G + row % a.G;
-                  const float l2 = a.lse[at] * kLog2e;
-                  if (fabsf(l2) != INFINITY) {
-                    nl = -l2;
-                    lo = min(lo, vis);
-                  }
-                } else {
-                  record_error(a.status, KVC_ERR_BOUNDS);
-                }
+        // LSE, limit and query row of this lane's rows of row tile rt
+        float nl[2];
+        int vi[2], qx[2];
+        auto fetch = [&](int rt) {
+#pragma unroll
+          for (int u = 0; u < 2; u++) {
+            const int tok = u ? tok1 : tok0, gg = u ? g1 : g0, i = rt * p.tokens + tok;
+            nl[u] = -INFINITY;
+            vi[u] = 0;
+            qx[u] = -1;
+            if (tok < p.tokens && i < n && (u == 0 || NR > 128)) {
+              const int x = a.row_idx ? a.row_idx[r0 + i] : r0 + i;
+              vi[u] = min(a.row_vis[r0 + i], seq);
+              if (x >= 0 && x < a.n_q) {
+                nl[u] = -lse[(int64_t)x * a.Hq + gg] * kLog2e;
+                qx[u] = x;
+              } else if (vi[u] > 0) {
+                record_error(a.status, KVC_ERR_BOUNDS);
               }
             }
-            sm.nlse[ls * NR + b + lane] = nl;
-            sm.vis[ls * NR + b + lane] = nl == -INFINITY ? 0 : vis;
-            constexpr int RPI = 32 / CH;
-            const int col = lane % CH;
-            const uint32_t dst = smem_u32(sm.q) + st * (NR * D * 2) + (col >> 3) * (NR * 128);
+          }
+        };
+        auto load_q = [&](int rt, bool more) {
+          const uint32_t st = qc % QS, ls = qc % LS;
+          if (!(ok = acquire(sm.qempty + st, ((qc / QS) & 1) ^ 1))) return;
+          if (!(ok = acquire(sm.lempty + ls, ((qc / LS) & 1) ^ 1))) return;
+          qc++;
+          const uint32_t bar = smem_u32(sm.qfull + st), dst = base_u + at.q + st * (NR * D * 2);
+          float *nls = reinterpret_cast<float *>(base + at.nlse) + ls * NR + 32 * pw + lane;
+          int *vis = reinterpret_cast<int *>(base + at.vis) + ls * NR + 32 * pw + lane;
+          if (p.q_box) {
+            if (pw == 0 && lane == 0) {
+              mbar_expect_tx(bar, p.tokens * a.G * D * 2);
 #pragma unroll
-            for (int i = 0; i < 32 / RPI; i++) {
-              const int rr = i * RPI + lane / CH;
-              const int64_t src = __shfl_sync(0xFFFFFFFFu, at, rr);
-              cp_async16(dst + (b + rr) * 128 + (((col & 7) ^ (rr & 7)) << 4),
-                         a.q + max(src, (int64_t)0) * D + col * 8, src >= 0);
+              for (int kb = 0; kb < KB; kb++)
+                tma_load_3d(dst + kb * (NR * 128), &tm_q, kb * 64, pos.h * a.G,
+                            (int)(pos.l * a.n_q) + r0 + rt * p.tokens, bar);
+            } else {
+              mbar_arrive(bar);
+            }
+          }
+          // A row that adds nothing (past the request's rows, no limit, LSE ±inf)
+          // has weight 0 by its LSE where its product is finite: its query is
+          // zeros, or, where a box brought it along and it may be anything, the
+          // tile is masked for every key (lo = 0).
+          int lo = INT_MAX;
+#pragma unroll
+          for (int u = 0; u < 2; u++) {
+            if (u == 1 && NR == 128) break;
+            const bool on = qx[u] >= 0 && vi[u] > 0 && fabsf(nl[u]) != INFINITY;
+            nls[128 * u] = on ? nl[u] : -INFINITY;
+            vis[128 * u] = on ? vi[u] : 0;
+            if (on) lo = min(lo, vi[u]);
+            else if (p.q_box && (u ? tok1 : tok0) < p.tokens) lo = 0;
+            if (!p.q_box) {
+              const int64_t q0 = pos.l * a.n_q * a.Hq + pos.h * a.G + (u ? g1 : g0);
+              const int64_t src_row = on ? q0 + (int64_t)qx[u] * a.Hq : -1;
+              const uint32_t d2 = dst + (col >> 3) * (NR * 128) + (128 * u + 32 * pw) * 128;
+#pragma unroll 4
+              for (int i = 0; i < 32 / RPI; i++) {
+                const int rr = i * RPI + lane / CH;
+                const int64_t src = __shfl_sync(0xFFFFFFFFu, src_row, rr);
+                cp_async16(d2 + rr * 128 + (((col & 7) ^ (rr & 7)) << 4),
+                           a.q + max(src, (int64_t)0) * D + col * 8, src >= 0);
+              }
             }
           }
           lo = __reduce_min_sync(0xFFFFFFFFu, lo);
-          if (lane == 0) sm.lo[ls * 4 + pw] = lo;
+          if (lane == 0) sm.lo[ls][pw] = lo;
           __syncwarp();
           mbar_arrive(smem_u32(sm.lfull + ls));
-          committed(sm.qfull + st);
-          qc++;
+          if (!p.q_box) committed(bar);
+          if (more) fetch(rt + 1);
         };
+        if (!ONE || unit != q_unit) fetch(pos.rt0 + pos.off);
         load_k(0);
         if (ONE) {
-          if (ok && unit != q_unit) load_q(0);
+          if (ok && unit != q_unit) {
+            load_q(0, false);
+            flush();  // (the next stages may all be boxes)
+          }
         } else {
           for (int i = 0; i < todo && ok; i++) {
-            load_q(pos.rt0 + pos.off + i);
+            load_q(pos.rt0 + pos.off + i, i + 1 < todo);
             if (i == 0 && ok) load_k(1);
           }
         }
@@ -661,56 +720,53 @@ k_mass_tc(MassArgs a, MassTc p) {
       g += todo;
       if (g < run1) pos.next(a, p);
     }
+    flush();
     cp_wait<0>();
-    signal();
-    if (!ok) *sm.failed = 1;
+    if (!ok) sm.failed = 1;
   } else if (warp == kTcEpi + kTcProd) {
     // ------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      uint32_t kc = 0, qc = 0, jc = 0;  // first K tile of the group, row tiles, products
-      int64_t q_unit = -1;
-      for (int64_t g = run0; g < run1 && ok;) {
-        const int todo = (int)min((int64_t)max(pos.cnt, 1) - pos.off, run1 - g);
-        if (pos.cnt > 0) {
-          const int64_t unit = (pos.l * a.n_req + pos.r) * a.H + pos.h;
-          for (int i = 0; i < todo && ok; i++) {
-            if (!ONE || unit != q_unit) {
-              if (ONE && qc > 0) mma_commit(smem_u32(sm.qempty + (qc - 1) % QS));
-              qc++;
-            }
-            const int qst = (qc - 1) % QS;
-            for (int kt = 0; kt < KG && ok; kt++) {
-              const uint32_t kx = kc + kt;
-              const int kst = kx % KS, acc = jc % NACC;
-              if (kt == 0 &&
-                  !(ok = mbar_wait_bounded(smem_u32(sm.qfull + qst), ((qc - 1) / QS) & 1, sm.failed)))
-                break;
-              if (!(ok = mbar_wait_bounded(smem_u32(sm.kfull + kst), (kx / KS) & 1, sm.failed))) break;
-              if (!(ok = mbar_wait_bounded(smem_u32(sm.tempty + acc), ((jc / NACC) & 1) ^ 1,
-                                           sm.failed)))
-                break;
-              tc_fence_after();
-              const uint32_t kb = smem_u32(sm.k) + kst * (kTcKeys * D * 2);
-              const uint32_t qb = smem_u32(sm.q) + qst * (NR * D * 2);
-#pragma unroll
-              for (int kk = 0; kk < 4 * KB; kk++)
-                mma_bf16(tmem + acc * NR,
-                         smem_desc(kb + (kk >> 2) * (kTcKeys * 128) + (kk & 3) * 32),
-                         smem_desc(qb + (kk >> 2) * (NR * 128) + (kk & 3) * 32), p.idesc, kk > 0);
-              mma_commit(smem_u32(sm.tfull + acc));
-              if (i == todo - 1) mma_commit(smem_u32(sm.kempty + kst));
-              jc++;
-            }
-            if (!ONE && ok) mma_commit(smem_u32(sm.qempty + qst));
+    const uint32_t lead = lane == 0;
+    uint32_t kc = 0, qc = 0, jc = 0;  // first K tile of the group, row tiles, products
+    int64_t q_unit = -1;
+    for (int64_t g = run0; g < run1 && ok;) {
+      const int todo = (int)min((int64_t)max(pos.cnt, 1) - pos.off, run1 - g);
+      if (pos.cnt > 0) {
+        const int64_t unit = (pos.l * a.n_req + pos.r) * a.H + pos.h;
+        for (int i = 0; i < todo && ok; i++) {
+          if (!ONE || unit != q_unit) {
+            if (ONE && qc > 0) mma_commit_if(lead, smem_u32(sm.qempty + (qc - 1) % QS));
+            qc++;
           }
-          kc += KG;
-          q_unit = unit;
+          const uint32_t qst = (qc - 1) % QS;
+          ok = mbar_wait_bounded(smem_u32(sm.qfull + qst), ((qc - 1) / QS) & 1, &sm.failed);
+          const uint64_t qb = uniform64(smem_desc(base_u + at.q + qst * (NR * D * 2)));
+          const uint32_t qk = uniform32(NR * 8);
+          for (int kt = 0; kt < KG && ok; kt++) {
+            const uint32_t kx = kc + kt, kst = kx % KS, acc = jc % NACC;
+            ok = mbar_wait_bounded(smem_u32(sm.kfull + kst), (kx / KS) & 1, &sm.failed);
+            if (ok)
+              ok = mbar_wait_bounded(smem_u32(sm.tempty + acc), ((jc / NACC) & 1) ^ 1, &sm.failed);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t kb = uniform64(smem_desc(base_u + at.k + kst * kSlot));
+            const uint32_t dst = uniform32(tmem + acc * NR);
+#pragma unroll
+            for (int kk = 0; kk < 4 * KB; kk++)
+              mma_bf16_if(lead, dst, kb + (kk >> 2) * (kTcKeys * 8) + (kk & 3) * 2,
+                          qb + (kk >> 2) * qk + (kk & 3) * 2, p.idesc, kk > 0);
+            mma_commit_if(lead, smem_u32(sm.tfull + acc));
+            if (i == todo - 1) mma_commit_if(lead, smem_u32(sm.kempty + kst));
+            jc++;
+          }
+          if (!ONE && ok) mma_commit_if(lead, smem_u32(sm.qempty + qst));
         }
-        g += todo;
-        if (g < run1) pos.next(a, p);
+        kc += KG;
+        q_unit = unit;
       }
-      if (!ok) *sm.failed = 1;
+      g += todo;
+      if (g < run1) pos.next(a, p);
     }
+    if (!ok) sm.failed = 1;
     __syncwarp();
   } else if (warp < kTcEpi) {
     // -------------------------------------------------------- epilogue
@@ -730,11 +786,10 @@ k_mass_tc(MassArgs a, MassTc p) {
       const bool whole = pos.off == 0 && todo == max(pos.cnt, 1);
       float *out = a.mass + unit * a.cap + key;
       float old = 0.f, total_w = 0.f;
-      bool valid = false;
+      int32_t blk = -1;
       if (mine && key < seq) {
         if (whole && key < a.n_mass[pos.r]) old = *out;
-        const int32_t b = a.block_table[(int64_t)pos.r * a.max_blocks + page_of(key, a.bs_inv)];
-        valid = b >= 0 && b < a.n_slots / a.BS;
+        blk = a.block_table[(int64_t)pos.r * a.max_blocks + page_of(key, a.bs_inv)];
       }
       if (pos.cnt > 0)
         for (int i = 0; i < todo && ok; i++) {
@@ -746,9 +801,9 @@ k_mass_tc(MassArgs a, MassTc p) {
             qc++;
             const int ls = (qc - 1) % LS;
             ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.lfull + ls),
-                                                           ((qc - 1) / LS) & 1, sm.failed));
+                                                           ((qc - 1) / LS) & 1, &sm.failed));
             if (!ok) break;
-            lo = min(min(sm.lo[ls * 4], sm.lo[ls * 4 + 1]), min(sm.lo[ls * 4 + 2], sm.lo[ls * 4 + 3]));
+            lo = min(min(sm.lo[ls][0], sm.lo[ls][1]), min(sm.lo[ls][2], sm.lo[ls][3]));
             if (lo == INT_MAX) lo = 0;
           }
           const int ls = (qc - 1) % LS;
@@ -757,45 +812,49 @@ k_mass_tc(MassArgs a, MassTc p) {
           if (mine) {
             const int acc = job % NACC;
             ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.tfull + acc),
-                                                           (job / NACC) & 1, sm.failed));
+                                                           (job / NACC) & 1, &sm.failed));
             if (!ok) break;
             tc_fence_after();
             const uint32_t taddr = tmem + lane_base + acc * NR;
-            const float *nl = sm.nlse + ls * NR;
-            const int *vi = sm.vis + ls * NR;
-            const bool masked = p0 + kTcKeys > lo;
+            const float *nl = reinterpret_cast<const float *>(base + at.nlse) + ls * NR;
+            const int *vi = reinterpret_cast<const int *>(base + at.vis) + ls * NR;
             uint64_t s0 = 0, s1 = 0;
-            uint32_t buf[2][32];
-            tmem_issue32(taddr, buf[0]);
-            for (int c = 0; c < NR; c += 64) {
+            if (p0 + kTcKeys <= lo) {
+              // every row sees every key of the tile
+              uint32_t buf[2][32];
+              tmem_issue32(taddr, buf[0]);
+#pragma unroll 1
+              for (int c = 0; c < NR; c += 64) {
 #pragma unroll
-              for (int hb = 0; hb < 2; hb++) {
-                tmem_wait32(buf[hb]);
-                const int cc = c + hb * 32;
-                if (cc + 32 < NR) tmem_issue32(taddr + cc + 32, buf[hb ^ 1]);
+                for (int hb = 0; hb < 2; hb++) {
+                  tmem_wait32(buf[hb]);
+                  const int cc = c + hb * 32;
+                  if (cc + 32 < NR) tmem_issue32(taddr + cc + 32, buf[hb ^ 1]);
 #pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                  const ulonglong2 n4 = *reinterpret_cast<const ulonglong2 *>(nl + cc + j);
-                  uint64_t x0 = fma2(pk2(__uint_as_float(buf[hb][j]), __uint_as_float(buf[hb][j + 1])),
-                                     zs2, n4.x);
-                  uint64_t x1 = fma2(pk2(__uint_as_float(buf[hb][j + 2]), __uint_as_float(buf[hb][j + 3])),
-                                     zs2, n4.y);
-                  float w0, w1, w2, w3;
-                  upk2(x0, w0, w1);
-                  upk2(x1, w2, w3);
-                  w0 = ex2(w0);
-                  w1 = ex2(w1);
-                  w2 = ex2(w2);
-                  w3 = ex2(w3);
-                  if (masked) {
-                    const int4 v4 = *reinterpret_cast<const int4 *>(vi + cc + j);
-                    w0 = key < v4.x ? w0 : 0.f;
-                    w1 = key < v4.y ? w1 : 0.f;
-                    w2 = key < v4.z ? w2 : 0.f;
-                    w3 = key < v4.w ? w3 : 0.f;
+                  for (int j = 0; j < 32; j += 4) {
+                    const ulonglong2 n4 = *reinterpret_cast<const ulonglong2 *>(nl + cc + j);
+                    float w0, w1, w2, w3;
+                    upk2(fma2(pk2(__uint_as_float(buf[hb][j]), __uint_as_float(buf[hb][j + 1])), zs2,
+                              n4.x), w0, w1);
+                    upk2(fma2(pk2(__uint_as_float(buf[hb][j + 2]), __uint_as_float(buf[hb][j + 3])),
+                              zs2, n4.y), w2, w3);
+                    s0 = add2(s0, pk2(ex2(w0), ex2(w1)));
+                    s1 = add2(s1, pk2(ex2(w2), ex2(w3)));
                   }
-                  s0 = add2(s0, pk2(w0, w1));
-                  s1 = add2(s1, pk2(w2, w3));
+                }
+              }
+            } else {
+#pragma unroll 1
+              for (int c = 0; c < NR; c += 16) {
+                float z[16];
+                tmem_ld16(taddr + c, z);
+#pragma unroll
+                for (int j = 0; j < 16; j += 2) {
+                  const float2 n2 = *reinterpret_cast<const float2 *>(nl + c + j);
+                  const int2 v2 = *reinterpret_cast<const int2 *>(vi + c + j);
+                  const float w0 = ex2(fmaf(z[j], a.zscale, n2.x));
+                  const float w1 = ex2(fmaf(z[j + 1], a.zscale, n2.y));
+                  s0 = add2(s0, pk2(key < v2.x ? w0 : 0.f, key < v2.y ? w1 : 0.f));
                 }
               }
             }
@@ -814,18 +873,19 @@ k_mass_tc(MassArgs a, MassTc p) {
         }
       q_unit = unit;
       if (ok && mine) {
+        const float add = blk >= 0 && blk < a.n_slots / a.BS ? total_w : 0.f;
         if (whole) {
-          if (key < seq) *out = fmaf(a.decay, old, valid ? total_w : 0.f);
+          if (key < seq) *out = fmaf(a.decay, old, add);
         } else {
           p.part[(2 * (int64_t)blockIdx.x + (g != run0)) * (KG * kTcKeys) + kt * kTcKeys +
-                 quarter * 32 + lane] = valid ? total_w : 0.f;
+                 quarter * 32 + lane] = add;
         }
       }
       g += todo;
       if (g < run1) pos.next(a, p);
     }
     if (!ok) {
-      *sm.failed = 1;
+      sm.failed = 1;
       if (lane == 0) record_error(a.status, KVC_ERR_TIMEOUT);
     }
   }
@@ -833,9 +893,17 @@ k_mass_tc(MassArgs a, MassTc p) {
   // -------------------------------------------------------- teardown
   tc_fence_before();
   __syncthreads();
-  if (*sm.failed && tid == 0) {
+  if (sm.failed && tid == 0) {
     record_error(a.status, KVC_ERR_TIMEOUT);
-    // let this CTA's products finish before its memory is released
+    // let this CTA's copies and products finish before its memory is released
+    for (int i = 0; i < KS; i++) {
+      mbar_drain(smem_u32(sm.kfull + i), 0);
+      mbar_drain(smem_u32(sm.kfull + i), 1);
+    }
+    for (int i = 0; i < QS; i++) {
+      mbar_drain(smem_u32(sm.qfull + i), 0);
+      mbar_drain(smem_u32(sm.qfull + i), 1);
+    }
     for (int i = 0; i < NACC; i++) {
       mbar_drain(smem_u32(sm.tfull + i), 0);
       mbar_drain(smem_u32(sm.tfull + i), 1);
@@ -859,12 +927,11 @@ k_mass_plan(MassArgs a, MassTc p) {
     if (tid == 0) record_error(a.status, KVC_ERR_BOUNDS);
     return;
   }
-  const int n_rt = (int)(((int64_t)n * a.G + p.NR - 1) / p.NR);
+  const int n_rt = (n + p.tokens - 1) / p.tokens;
   int *vis = p.rt_vis + (int64_t)r * p.max_rt;
   const int warp = tid >> 5, lane = tid & 31;
   for (int t = warp; t < n_rt; t += 8) {  // positions the widest row of each row tile sees
-    const int i0 = (int)((int64_t)t * p.NR / a.G);
-    const int i1 = min(n - 1, (int)((((int64_t)t + 1) * p.NR - 1) / a.G));
+    const int i0 = t * p.tokens, i1 = min(n, i0 + p.tokens) - 1;
     int v = 0;
     for (int i = i0 + lane; i <= i1; i += 32) v = max(v, a.row_vis[r0 + i]);
     v = __reduce_max_sync(0xFFFFFFFFu, v);
@@ -939,14 +1006,15 @@ MassTc tc_plan(int n_req, int cap, int max_rows, int G, int D, bool &one, size_t
   const int64_t R = (int64_t)max_rows * G;
   one = R <= 256;
   p.NR = R <= 128 ? 128 : 256;
+  p.tokens = std::min(max_rows, p.NR / G);
   // what the row tiles leave: K tiles in flight when keys stream, else two
   const size_t tile = (size_t)kTcKeys * D * 2, q = 2 * (size_t)p.NR * D * 2;
-  p.k_slots = one ? (int)std::min<size_t>(8, (200 * 1024 - q) / tile) : 2;
+  p.k_slots = one ? (int)std::min<size_t>(kTcMaxK, (200 * 1024 - q) / tile) : 2;
   p.n_cta = device_sm_count();
   p.max_kg = (cap + 255) / 256;
-  p.max_rt = (int)((R + p.NR - 1) / p.NR);
+  p.max_rt = (max_rows + p.tokens - 1) / p.tokens;
   p.idesc = make_idesc(128, p.NR);
-  smem = 1024 + TcSmem::layout(D, p.NR, p.k_slots, 2, one ? 2 : 4, nullptr, nullptr);
+  smem = 1024 + TcSmem(D, p.NR, p.k_slots, one ? 2 : 4).bytes;
   ws = 0;
   if (one) return p;
   auto take = [&](size_t n) {
@@ -981,19 +1049,27 @@ template <int D>
 cudaError_t launch_tc(const MassArgs &a, void *ws, cudaStream_t s) {
   bool one;
   size_t smem, ws_bytes;
-  const MassTc p = tc_plan(a.n_req, a.cap, a.max_rows, a.G, D, one, smem, ws_bytes,
+  MassTc p = tc_plan(a.n_req, a.cap, a.max_rows, a.G, D, one, smem, ws_bytes,
                            reinterpret_cast<uint8_t *>(ws));
   auto *kern = one ? k_mass_tc<D, true> : k_mass_tc<D, false>;
+  CUtensorMap tm_k{}, tm_q{};
+  p.box = a.BS % 32 == 0 ? 32 : a.BS % 16 == 0 ? 16 : a.BS % 8 == 0 ? 8 : 0;
+  if ((int64_t)a.L * a.n_slots > INT32_MAX) p.box = 0;  // (a map coordinate is an int32)
+  p.q_box = !a.row_idx && (int64_t)a.L * a.n_q + a.n_rows <= INT32_MAX;
+  if (p.box && !pool_map(&tm_k, a.kpool, (int64_t)a.L * a.n_slots, a.H, D, p.box))
+    return cudaErrorUnknown;
+  if (p.q_box && !q_map(&tm_q, a.q, (int64_t)a.L * a.n_q, a.Hq, D, a.G, p.tokens))
+    return cudaErrorUnknown;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   if (one) {
-    kern<<<p.n_cta, kTcThreads, smem, s>>>(a, p);
+    kern<<<p.n_cta, kTcThreads, smem, s>>>(tm_k, tm_q, a, p);
     return cudaGetLastError();
   }
   k_mass_plan<<<a.n_req, 256, 0, s>>>(a, p);
   e = cudaGetLastError();
-  if (e == cudaSuccess) e = launch_dependent(kern, dim3(p.n_cta), kTcThreads, smem, s, a, p);
+  if (e == cudaSuccess) e = launch_dependent(kern, dim3(p.n_cta), kTcThreads, smem, s, tm_k, tm_q, a, p);
   if (e == cudaSuccess && p.n_cta > 1)
     e = launch_dependent(k_mass_join, dim3(p.n_cta - 1), 256, 0, s, a, p);
   return e;

@@ -1,7 +1,8 @@
-// mma_ptx.cuh — building blocks of the kernels that stream paged rows through
-// cp.async rings into mma.sync (tree_attn.cu, attn_mass.cu): the inline PTX,
-// the shared-memory row layout, and block-wide sums and searches over the
-// requests of a batch.
+// mma_ptx.cuh — building blocks of the kernels that stream paged rows into
+// tensor-core products (tree_attn.cu, attn_mass.cu): cp.async and mma.sync,
+// tcgen05 and TMA issued under a predicate, tensor maps of the pools and of
+// the queries, the shared-memory row layout, and block-wide sums and searches
+// over the requests of a batch.
 #pragma once
 
 #include "tc_ptx.cuh"
@@ -46,6 +47,63 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 template <int D>
 __device__ __forceinline__ uint32_t swz(int row, int c) {
   return (uint32_t)(row * D * 2 + ((c ^ (row & 7)) << 4));
+}
+
+// tcgen05.mma / commit by the lanes with `lead` set (one of the warp); the
+// whole warp must execute it.
+__device__ __forceinline__ void mma_bf16_if(uint32_t lead, uint32_t d_tmem, uint64_t a, uint64_t b,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit_if(uint32_t lead, uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
+          bar),
+      "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_if(uint32_t lead, uint32_t dst, const CUtensorMap *map,
+                                               int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %6, 0;\n"
+      " @q cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];\n}\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(lead)
+      : "memory");
+}
+// The same value in every lane, for the compiler too.
+__device__ __forceinline__ uint32_t uniform32(uint32_t x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
+__device__ __forceinline__ uint64_t uniform64(uint64_t x) {
+  return (uint64_t)uniform32((uint32_t)(x >> 32)) << 32 | uniform32((uint32_t)x);
+}
+
+// Boxes of `box` consecutive slots of one head, 64 columns, 128-byte swizzle.
+inline bool pool_map(CUtensorMap *m, const void *pool, int64_t n_slots, int H, int D, int box) {
+  auto fn = tc::encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)n_slots};
+  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)H * D * 2};
+  cuuint32_t bx[3] = {64, 1, (cuuint32_t)box}, es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(pool), dims, strides, bx, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Boxes of `nodes` consecutive rows of q, the G heads of one group, 64 columns.
+inline bool q_map(CUtensorMap *m, const void *q, int64_t n_q, int Hq, int D, int G, int nodes) {
+  auto fn = tc::encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)n_q};
+  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)Hq * D * 2};
+  cuuint32_t bx[3] = {64, (cuuint32_t)G, (cuuint32_t)nodes}, es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, bx, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // p / BS for 0 ≤ p < 2^24 and BS ≤ 64, from page_inverse(BS) = ⌈2^32 / BS⌉: the
