@@ -321,9 +321,12 @@ cudaError_t launch_rows(const MassArgs &a, cudaStream_t s) {
 // --------------------------------------------------------------- many rows
 //
 // tcgen05: D[key][row] = K tile (M 128 keys, A) × row tile (N rows, B), fp32 in
-// tensor memory; epilogue thread = one key (TMEM lane), its columns the rows.
-// Warps 0–7: two epilogue warpgroups, taking the key tiles in turn; 8–11:
-// producers; 12: MMA issue (predicated, from uniform registers).
+// tensor memory.  Warps 0–7: two epilogue warpgroups, taking the key tiles in
+// turn; 8–11: producers; 12–13: one MMA warp for each epilogue warpgroup (a
+// warp's waits run under the other's products).  An epilogue thread owns four
+// keys and a quarter of the rows (16x256b fragments): the rows' LSE, stored in
+// that order, costs it a quarter of the shared-memory reads that one key a
+// thread would, and the sum over rows stays in registers until the group ends.
 //
 // ONE (all rows of a request in one row tile): the rows stay in shared memory
 // while the request's keys stream past; work is dealt out by key tile.
@@ -337,9 +340,10 @@ cudaError_t launch_rows(const MassArgs &a, cudaStream_t s) {
 
 constexpr int kTcEpi = 8;                       // epilogue warps
 constexpr int kTcProd = 4;                      // producer warps
-constexpr int kTcThreads = (kTcEpi + kTcProd + 1) * 32;
+constexpr int kTcThreads = (kTcEpi + kTcProd + 2) * 32;
 constexpr int kTcKeys = 128;                    // keys of a tile
 constexpr int kTcMaxK = 8;                      // K slots, at most
+constexpr int kTcQs = 4;                        // slots of 64 columns of a row tile
 
 struct MassTc {
   int n_cta;        // CTAs the work is dealt out to
@@ -363,9 +367,9 @@ struct TcShape {
 };
 
 // Head of the dynamic shared memory (fixed offsets), then K, q, and the LSE
-// slots: −lse·log2e [slot][NR], limits [slot][NR].
+// slots: −lse·log2e and limits, [slot][NR + 16] in the order of lse_at.
 struct TcHead {
-  uint64_t kfull[kTcMaxK], kempty[kTcMaxK], qfull[2], qempty[2], lfull[4], lempty[4];
+  uint64_t kfull[kTcMaxK], kempty[kTcMaxK], qfull[kTcQs], qempty[kTcQs], lfull[4], lempty[4];
   uint64_t tfull[4], tempty[4];
   int64_t scan[66];
   int lo[4][4];  // least limit of the slot's rows, per producer warp
@@ -380,11 +384,17 @@ struct TcSmem {
   __host__ __device__ TcSmem(int D, int NR, int ks, int ls) {
     k = kTcHead;
     q = k + ks * kTcKeys * D * 2;
-    nlse = q + 2 * NR * D * 2;
-    vis = nlse + ls * NR * 4;
-    bytes = vis + ls * NR * 4;
+    nlse = q + kTcQs * NR * 128;
+    vis = nlse + ls * (NR + 16) * 4;
+    bytes = vis + ls * (NR + 16) * 4;
   }
 };
+
+// Place of row r in an LSE slot: the rows 8k + 2q + {0, 1} of an epilogue
+// thread (q = lane mod 4) together, quarters four words apart in the banks.
+__device__ __forceinline__ int lse_at(int r, int NR) {
+  return ((r >> 1) & 3) * (NR / 4 + 4) + (r >> 3) * 2 + (r & 1);
+}
 
 // Groups of request r.
 __device__ __forceinline__ int tc_groups(const MassArgs &a, int r, int keys) {
@@ -470,7 +480,7 @@ template <int D, bool ONE>
 __global__ void __launch_bounds__(kTcThreads, 1)
 k_mass_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
           MassArgs a, MassTc p) {
-  constexpr int KG = TcShape<ONE>::kKG, LS = TcShape<ONE>::kLs, QS = 2;
+  constexpr int KG = TcShape<ONE>::kKG, LS = TcShape<ONE>::kLs, QS = kTcQs;
   constexpr int CH = D / 8, KB = D / 64;
   constexpr uint32_t kSlot = kTcKeys * D * 2;
   extern __shared__ uint8_t smem_raw[];
@@ -490,7 +500,7 @@ k_mass_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
     }
     for (int i = 0; i < QS; i++) {
       mbar_init(smem_u32(sm.qfull + i), kTcProd * 32);
-      mbar_init(smem_u32(sm.qempty + i), 1);
+      mbar_init(smem_u32(sm.qempty + i), 2);
     }
     for (int i = 0; i < LS; i++) {
       mbar_init(smem_u32(sm.lfull + i), kTcProd * 32);
@@ -504,7 +514,7 @@ k_mass_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
   }
   // rows that no row tile fills stay zero
   if (p.tokens * a.G < NR) {
-    for (uint32_t i = tid; i < 2u * NR * D * 2 / 16; i += kTcThreads)
+    for (uint32_t i = tid; i < (uint32_t)kTcQs * NR * 128 / 16; i += kTcThreads)
       *reinterpret_cast<uint4 *>(base + at.q + i * 16) = make_uint4(0, 0, 0, 0);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -651,56 +661,61 @@ k_mass_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
           }
         };
         auto load_q = [&](int rt, bool more) {
-          const uint32_t st = qc % QS, ls = qc % LS;
-          if (!(ok = acquire(sm.qempty + st, ((qc / QS) & 1) ^ 1))) return;
-          if (!(ok = acquire(sm.lempty + ls, ((qc / LS) & 1) ^ 1))) return;
-          qc++;
-          const uint32_t bar = smem_u32(sm.qfull + st), dst = base_u + at.q + st * (NR * D * 2);
-          float *nls = reinterpret_cast<float *>(base + at.nlse) + ls * NR + 32 * pw + lane;
-          int *vis = reinterpret_cast<int *>(base + at.vis) + ls * NR + 32 * pw + lane;
-          if (p.q_box) {
-            if (pw == 0 && lane == 0) {
-              mbar_expect_tx(bar, p.tokens * a.G * D * 2);
-#pragma unroll
-              for (int kb = 0; kb < KB; kb++)
-                tma_load_3d(dst + kb * (NR * 128), &tm_q, kb * 64, pos.h * a.G,
-                            (int)(pos.l * a.n_q) + r0 + rt * p.tokens, bar);
-            } else {
-              mbar_arrive(bar);
-            }
-          }
+          const uint32_t ls = (qc / KB) % LS;
+          if (!(ok = acquire(sm.lempty + ls, (((qc / KB) / LS) & 1) ^ 1))) return;
+          float *nls = reinterpret_cast<float *>(base + at.nlse) + ls * (NR + 16);
+          int *vis = reinterpret_cast<int *>(base + at.vis) + ls * (NR + 16);
           // A row that adds nothing (past the request's rows, no limit, LSE ±inf)
           // has weight 0 by its LSE where its product is finite: its query is
           // zeros, or, where a box brought it along and it may be anything, the
           // tile is masked for every key (lo = 0).
           int lo = INT_MAX;
+          int64_t src_row[2];
 #pragma unroll
           for (int u = 0; u < 2; u++) {
+            src_row[u] = -1;
             if (u == 1 && NR == 128) break;
             const bool on = qx[u] >= 0 && vi[u] > 0 && fabsf(nl[u]) != INFINITY;
-            nls[128 * u] = on ? nl[u] : -INFINITY;
-            vis[128 * u] = on ? vi[u] : 0;
+            const int r = lse_at(128 * u + 32 * pw + lane, NR);
+            nls[r] = on ? nl[u] : -INFINITY;
+            vis[r] = on ? vi[u] : 0;
             if (on) lo = min(lo, vi[u]);
             else if (p.q_box && (u ? tok1 : tok0) < p.tokens) lo = 0;
-            if (!p.q_box) {
-              const int64_t q0 = pos.l * a.n_q * a.Hq + pos.h * a.G + (u ? g1 : g0);
-              const int64_t src_row = on ? q0 + (int64_t)qx[u] * a.Hq : -1;
-              const uint32_t d2 = dst + (col >> 3) * (NR * 128) + (128 * u + 32 * pw) * 128;
-#pragma unroll 4
-              for (int i = 0; i < 32 / RPI; i++) {
-                const int rr = i * RPI + lane / CH;
-                const int64_t src = __shfl_sync(0xFFFFFFFFu, src_row, rr);
-                cp_async16(d2 + rr * 128 + (((col & 7) ^ (rr & 7)) << 4),
-                           a.q + max(src, (int64_t)0) * D + col * 8, src >= 0);
-              }
-            }
+            if (on)
+              src_row[u] = (pos.l * a.n_q + qx[u]) * a.Hq + pos.h * a.G + (u ? g1 : g0);
           }
           lo = __reduce_min_sync(0xFFFFFFFFu, lo);
           if (lane == 0) sm.lo[ls][pw] = lo;
           __syncwarp();
           mbar_arrive(smem_u32(sm.lfull + ls));
-          if (!p.q_box) committed(bar);
           if (more) fetch(rt + 1);
+          for (int kb = 0; kb < KB; kb++, qc++) {
+            const uint32_t st = qc % QS;
+            if (!(ok = acquire(sm.qempty + st, ((qc / QS) & 1) ^ 1))) return;
+            const uint32_t bar = smem_u32(sm.qfull + st), dst = base_u + at.q + st * (NR * 128);
+            if (p.q_box) {
+              if (pw == 0 && lane == 0) {
+                mbar_expect_tx(bar, p.tokens * a.G * 128);
+                tma_load_3d(dst, &tm_q, kb * 64, pos.h * a.G,
+                            (int)(pos.l * a.n_q) + r0 + rt * p.tokens, bar);
+              } else {
+                mbar_arrive(bar);
+              }
+              continue;
+            }
+#pragma unroll
+            for (int u = 0; u < 2; u++) {
+              if (u == 1 && NR == 128) break;
+#pragma unroll
+              for (int i = 0; i < 8; i++) {
+                const int rr = i * 4 + lane / 8, c8 = lane % 8;
+                const int64_t src = __shfl_sync(0xFFFFFFFFu, src_row[u], rr);
+                cp_async16(dst + (128 * u + 32 * pw + rr) * 128 + ((c8 ^ (rr & 7)) << 4),
+                           a.q + max(src, (int64_t)0) * D + kb * 64 + c8 * 8, src >= 0);
+              }
+            }
+            committed(bar);
+          }
         };
         if (!ONE || unit != q_unit) fetch(pos.rt0 + pos.off);
         load_k(0);
@@ -723,10 +738,12 @@ k_mass_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
     flush();
     cp_wait<0>();
     if (!ok) sm.failed = 1;
-  } else if (warp == kTcEpi + kTcProd) {
-    // ------------------------------------------------------ MMA issuer
+  } else if (warp >= kTcEpi + kTcProd) {
+    // ----------------------------------------------------- MMA issuers
+    // (the whole warp runs the loop; one lane's products are enabled)
+    const int wg = warp - kTcEpi - kTcProd;  // the epilogue warpgroup it works for
     const uint32_t lead = lane == 0;
-    uint32_t kc = 0, qc = 0, jc = 0;  // first K tile of the group, row tiles, products
+    uint32_t kc = 0, qc = 0, jc = 0;  // first K tile of the group, q stages, products of both
     int64_t q_unit = -1;
     for (int64_t g = run0; g < run1 && ok;) {
       const int todo = (int)min((int64_t)max(pos.cnt, 1) - pos.off, run1 - g);
@@ -734,31 +751,40 @@ k_mass_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
         const int64_t unit = (pos.l * a.n_req + pos.r) * a.H + pos.h;
         for (int i = 0; i < todo && ok; i++) {
           if (!ONE || unit != q_unit) {
-            if (ONE && qc > 0) mma_commit_if(lead, smem_u32(sm.qempty + (qc - 1) % QS));
-            qc++;
+            if (ONE && qc > 0)
+              for (int kb = 0; kb < KB; kb++) mma_commit_if(lead, smem_u32(sm.qempty + (qc - KB + kb) % QS));
+            qc += KB;
+            // (also for a unit without a tile of this warp's: a barrier's parity
+            // tells only two uses apart)
+            for (int kb = 0; ONE && kb < KB && ok; kb++)
+              ok = mbar_wait_bounded(smem_u32(sm.qfull + (qc - KB + kb) % QS),
+                                     ((qc - KB + kb) / QS) & 1, &sm.failed);
+            if (!ok) break;
           }
-          const uint32_t qst = (qc - 1) % QS;
-          ok = mbar_wait_bounded(smem_u32(sm.qfull + qst), ((qc - 1) / QS) & 1, &sm.failed);
-          const uint64_t qb = uniform64(smem_desc(base_u + at.q + qst * (NR * D * 2)));
-          const uint32_t qk = uniform32(NR * 8);
-          for (int kt = 0; kt < KG && ok; kt++) {
-            const uint32_t kx = kc + kt, kst = kx % KS, acc = jc % NACC;
-            ok = mbar_wait_bounded(smem_u32(sm.kfull + kst), (kx / KS) & 1, &sm.failed);
-            if (ok)
-              ok = mbar_wait_bounded(smem_u32(sm.tempty + acc), ((jc / NACC) & 1) ^ 1, &sm.failed);
+          const uint32_t job = ONE ? jc : jc + wg;
+          jc += KG;
+          if (ONE && (job & 1) != (uint32_t)wg) continue;
+          const uint32_t kx = kc + (ONE ? 0 : wg), kst = kx % KS, acc = job % NACC;
+          ok = mbar_wait_bounded(smem_u32(sm.kfull + kst), (kx / KS) & 1, &sm.failed);
+          if (ok) ok = mbar_wait_bounded(smem_u32(sm.tempty + acc), ((job / NACC) & 1) ^ 1, &sm.failed);
+          const uint64_t kd = uniform64(smem_desc(base_u + at.k + kst * kSlot));
+          const uint32_t dst = uniform32(tmem + acc * NR);
+#pragma unroll
+          for (int kb = 0; kb < KB; kb++) {
+            const uint32_t qi = qc - KB + kb, qst = qi % QS;
+            if (ok) ok = mbar_wait_bounded(smem_u32(sm.qfull + qst), (qi / QS) & 1, &sm.failed);
             if (!ok) break;
             tc_fence_after();
-            const uint64_t kb = uniform64(smem_desc(base_u + at.k + kst * kSlot));
-            const uint32_t dst = uniform32(tmem + acc * NR);
+            const uint64_t qd = uniform64(smem_desc(base_u + at.q + qst * (NR * 128)));
 #pragma unroll
-            for (int kk = 0; kk < 4 * KB; kk++)
-              mma_bf16_if(lead, dst, kb + (kk >> 2) * (kTcKeys * 8) + (kk & 3) * 2,
-                          qb + (kk >> 2) * qk + (kk & 3) * 2, p.idesc, kk > 0);
-            mma_commit_if(lead, smem_u32(sm.tfull + acc));
-            if (i == todo - 1) mma_commit_if(lead, smem_u32(sm.kempty + kst));
-            jc++;
+            for (int kk = 0; kk < 4; kk++)
+              mma_bf16_if(lead, dst, kd + kb * (kTcKeys * 8) + kk * 2, qd + kk * 2, p.idesc,
+                          kb > 0 || kk > 0);
+            if (!ONE) mma_commit_if(lead, smem_u32(sm.qempty + qst));
           }
-          if (!ONE && ok) mma_commit_if(lead, smem_u32(sm.qempty + qst));
+          if (!ok) break;
+          mma_commit_if(lead, smem_u32(sm.tfull + acc));
+          if (i == todo - 1) mma_commit_if(lead, smem_u32(sm.kempty + kst));
         }
         kc += KG;
         q_unit = unit;
@@ -772,7 +798,7 @@ k_mass_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
     // -------------------------------------------------------- epilogue
     const int wg = warp >> 2, quarter = warp & 3;
     const uint32_t lane_base = (uint32_t)(32 * quarter) << 16;
-    const uint64_t zs2 = pk2(a.zscale, a.zscale);
+    const float zs = a.zscale;
     uint32_t qc = 0, jc = 0;
     int64_t q_unit = -1;
     int lo = 0;
@@ -785,7 +811,9 @@ k_mass_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
       const bool mine = ONE ? (jc & 1) == (uint32_t)wg : true;
       const bool whole = pos.off == 0 && todo == max(pos.cnt, 1);
       float *out = a.mass + unit * a.cap + key;
-      float old = 0.f, total_w = 0.f;
+      float old = 0.f;
+      // this thread's rows added up, keys lane/4 + 8·i of the warp's 32
+      float s4[4] = {0.f, 0.f, 0.f, 0.f};
       int32_t blk = -1;
       if (mine && key < seq) {
         if (whole && key < a.n_mass[pos.r]) old = *out;
@@ -816,55 +844,58 @@ k_mass_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
             if (!ok) break;
             tc_fence_after();
             const uint32_t taddr = tmem + lane_base + acc * NR;
-            const float *nl = reinterpret_cast<const float *>(base + at.nlse) + ls * NR;
-            const int *vi = reinterpret_cast<const int *>(base + at.vis) + ls * NR;
-            uint64_t s0 = 0, s1 = 0;
+            const int qoff = ls * (NR + 16) + (lane & 3) * (NR / 4 + 4);
+            const float *nl = reinterpret_cast<const float *>(base + at.nlse) + qoff;
+            const int *vi = reinterpret_cast<const int *>(base + at.vis) + qoff;
+            float t4[4] = {0.f, 0.f, 0.f, 0.f};  // this tile's, apart from the others'
             if (p0 + kTcKeys <= lo) {
               // every row sees every key of the tile
-              uint32_t buf[2][32];
-              tmem_issue32(taddr, buf[0]);
+              uint32_t z[2][32];
+              tmem_frag8(taddr, z[0]);
 #pragma unroll 1
               for (int c = 0; c < NR; c += 64) {
+                float n16[16];
 #pragma unroll
-                for (int hb = 0; hb < 2; hb++) {
-                  tmem_wait32(buf[hb]);
-                  const int cc = c + hb * 32;
-                  if (cc + 32 < NR) tmem_issue32(taddr + cc + 32, buf[hb ^ 1]);
+                for (int j = 0; j < 16; j += 4)
+                  *reinterpret_cast<float4 *>(n16 + j) = *reinterpret_cast<const float4 *>(nl + c / 4 + j);
 #pragma unroll
-                  for (int j = 0; j < 32; j += 4) {
-                    const ulonglong2 n4 = *reinterpret_cast<const ulonglong2 *>(nl + cc + j);
-                    float w0, w1, w2, w3;
-                    upk2(fma2(pk2(__uint_as_float(buf[hb][j]), __uint_as_float(buf[hb][j + 1])), zs2,
-                              n4.x), w0, w1);
-                    upk2(fma2(pk2(__uint_as_float(buf[hb][j + 2]), __uint_as_float(buf[hb][j + 3])),
-                              zs2, n4.y), w2, w3);
-                    s0 = add2(s0, pk2(ex2(w0), ex2(w1)));
-                    s1 = add2(s1, pk2(ex2(w2), ex2(w3)));
+                for (int hf = 0; hf < 2; hf++) {
+                  tmem_wait(z[hf]);
+                  if (hf == 0) tmem_frag8(taddr + c + (16u << 16), z[1]);
+                  else if (c + 64 < NR) tmem_frag8(taddr + c + 64, z[0]);
+#pragma unroll
+                  for (int e = 0; e < 32; e += 4) {
+                    const float w0 = ex2(fmaf(__uint_as_float(z[hf][e]), zs, n16[e / 2]));
+                    const float w1 = ex2(fmaf(__uint_as_float(z[hf][e + 1]), zs, n16[e / 2 + 1]));
+                    const float w2 = ex2(fmaf(__uint_as_float(z[hf][e + 2]), zs, n16[e / 2]));
+                    const float w3 = ex2(fmaf(__uint_as_float(z[hf][e + 3]), zs, n16[e / 2 + 1]));
+                    t4[2 * hf] += w0 + w1;
+                    t4[2 * hf + 1] += w2 + w3;
                   }
                 }
               }
             } else {
 #pragma unroll 1
-              for (int c = 0; c < NR; c += 16) {
-                float z[16];
-                tmem_ld16(taddr + c, z);
+              for (int c = 0; c < NR; c += 64)
 #pragma unroll
-                for (int j = 0; j < 16; j += 2) {
-                  const float2 n2 = *reinterpret_cast<const float2 *>(nl + c + j);
-                  const int2 v2 = *reinterpret_cast<const int2 *>(vi + c + j);
-                  const float w0 = ex2(fmaf(z[j], a.zscale, n2.x));
-                  const float w1 = ex2(fmaf(z[j + 1], a.zscale, n2.y));
-                  s0 = add2(s0, pk2(key < v2.x ? w0 : 0.f, key < v2.y ? w1 : 0.f));
+                for (int hf = 0; hf < 2; hf++) {
+                  uint32_t z[32];
+                  tmem_frag8(taddr + c + ((uint32_t)(16 * hf) << 16), z);
+                  tmem_wait(z);
+                  const int k0 = p0 + quarter * 32 + hf * 16 + lane / 4;
+#pragma unroll
+                  for (int e = 0; e < 32; e++) {
+                    const int col = c / 4 + (e >> 2) * 2 + (e & 1), k = k0 + 8 * ((e >> 1) & 1);
+                    const float w = ex2(fmaf(__uint_as_float(z[e]), zs, nl[col]));
+                    t4[2 * hf + ((e >> 1) & 1)] += k < vi[col] ? w : 0.f;
+                  }
                 }
-              }
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(sm.tempty + acc));
-            float u0, u1, u2, u3;
-            upk2(s0, u0, u1);
-            upk2(s1, u2, u3);
-            total_w += (u0 + u2) + (u1 + u3);
+#pragma unroll
+            for (int k = 0; k < 4; k++) s4[k] += t4[k];
           }
           if (!ONE) {
             __syncwarp();
@@ -872,6 +903,16 @@ k_mass_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
           }
         }
       q_unit = unit;
+      // the four lanes of a key, then each lane its own key
+      float total_w = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; k++) {
+        float x = s4[k];
+        x += __shfl_xor_sync(0xFFFFFFFFu, x, 1);
+        x += __shfl_xor_sync(0xFFFFFFFFu, x, 2);
+        x = __shfl_sync(0xFFFFFFFFu, x, (lane & 7) << 2);
+        if ((lane >> 3) == k) total_w = x;
+      }
       if (ok && mine) {
         const float add = blk >= 0 && blk < a.n_slots / a.BS ? total_w : 0.f;
         if (whole) {
@@ -1008,8 +1049,8 @@ MassTc tc_plan(int n_req, int cap, int max_rows, int G, int D, bool &one, size_t
   p.NR = R <= 128 ? 128 : 256;
   p.tokens = std::min(max_rows, p.NR / G);
   // what the row tiles leave: K tiles in flight when keys stream, else two
-  const size_t tile = (size_t)kTcKeys * D * 2, q = 2 * (size_t)p.NR * D * 2;
-  p.k_slots = one ? (int)std::min<size_t>(kTcMaxK, (200 * 1024 - q) / tile) : 2;
+  const size_t tile = (size_t)kTcKeys * D * 2, q = (size_t)kTcQs * p.NR * 128;
+  p.k_slots = one ? (int)std::min<size_t>(kTcMaxK, (200 * 1024 - q) / tile) & ~1 : 2;  // even: a slot keeps its MMA warp
   p.n_cta = device_sm_count();
   p.max_kg = (cap + 255) / 256;
   p.max_rt = (max_rows + p.tokens - 1) / p.tokens;

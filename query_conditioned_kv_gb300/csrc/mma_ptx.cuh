@@ -10,6 +10,7 @@
 namespace kvc {
 namespace {
 
+
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(valid ? 16 : 0)
@@ -80,6 +81,21 @@ __device__ __forceinline__ void tma_load_3d_if(uint32_t lead, uint32_t dst, cons
 __device__ __forceinline__ uint32_t uniform32(uint32_t x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
 __device__ __forceinline__ uint64_t uniform64(uint64_t x) {
   return (uint64_t)uniform32((uint32_t)(x >> 32)) << 32 | uniform32((uint32_t)x);
+}
+
+// 16 TMEM lanes × 64 columns (16x256b): register 4k + j of thread t holds lane
+// t/4 + 8·(j ≥ 2), column 8k + 2·(t%4) + (j & 1).
+__device__ __forceinline__ void tmem_frag8(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+      "%28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
 }
 
 // Boxes of `box` consecutive slots of one head, 64 columns, 128-byte swizzle.

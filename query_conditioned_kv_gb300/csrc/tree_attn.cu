@@ -599,23 +599,6 @@ struct TreePos {
   }
 };
 
-// 16 TMEM lanes × 8·NB columns (16x256b): register 4k + j of thread t holds
-// lane t/4 + 8·(j ≥ 2), column 8k + 2·(t%4) + (j & 1).
-template <int NB>
-__device__ __forceinline__ void tmem_frag(uint32_t taddr, uint32_t (&r)[4 * NB]);
-template <>
-__device__ __forceinline__ void tmem_frag<8>(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
-      "%28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-}
 __device__ __forceinline__ void stsm4t(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2,
                                       uint32_t r3) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
@@ -1000,7 +983,7 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
             const uint32_t ta = ts + ((uint32_t)(16 * (w >> 1)) << 16) + 64 * (w & 1);
             uint32_t bits = 0;
 #pragma unroll 1
-            for (int e = 0; e < 32; e++) {  // register e: see tmem_frag
+            for (int e = 0; e < 32; e++) {  // register e: see tmem_frag8
               const int kk = (w >> 1) * 16 + lane / 4 + 8 * ((e >> 1) & 1);
               const int x = pos.rt() * a.rstep + row0 + 64 * (w & 1) + 8 * (e >> 2) + 2 * (lane & 3) + (e & 1);
               const int j = t * kTtKeys + quarter * 32 + kk - pos.c, i = x / a.G;
@@ -1012,7 +995,7 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
               bits |= (uint32_t)v << e;
             }
             uint32_t z[32];
-            tmem_frag<8>(ta, z);
+            tmem_frag8(ta, z);
             tmem_wait(z);
 #pragma unroll
             for (int e = 0; e < 32; e++)
@@ -1027,7 +1010,7 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
           float ls[32], top = -INFINITY;
           if (ok) {
             uint32_t z[2][32];
-            tmem_frag<8>(ts, z[0]);
+            tmem_frag8(ts, z[0]);
             // P of the team's last job has been read, O holds its product
             if (sc > 0)
               ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.pvdone + team), (sc - 1) & 1,
@@ -1047,7 +1030,7 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
                 const int w = 2 * ch + hf;
                 tmem_wait(z[w & 1]);
                 if (w < 3)
-                  tmem_frag<8>(ts + ((uint32_t)(16 * ((w + 1) & 1)) << 16) + 64 * ((w + 1) >> 1),
+                  tmem_frag8(ts + ((uint32_t)(16 * ((w + 1) & 1)) << 16) + 64 * ((w + 1) >> 1),
                                z[(w + 1) & 1]);
                 float x[32];
 #pragma unroll
@@ -1090,7 +1073,7 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
 #pragma unroll 1
             for (int hf = 0; hf < 2; hf++) {
               uint32_t z[32];
-              tmem_frag<8>(ts + ((uint32_t)(16 * hf) << 16) + 64 * ch, z);
+              tmem_frag8(ts + ((uint32_t)(16 * hf) << 16) + 64 * ch, z);
               tmem_wait(z);
 #pragma unroll
               for (int e = 0; e < 32; e++)
