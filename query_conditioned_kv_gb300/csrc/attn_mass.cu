@@ -321,29 +321,33 @@ cudaError_t launch_rows(const MassArgs &a, cudaStream_t s) {
 // --------------------------------------------------------------- many rows
 //
 // tcgen05: D[key][row] = K tile (M 128 keys, A) × row tile (N rows, B), fp32 in
-// tensor memory.  Warps 0–7: two epilogue warpgroups, taking the key tiles in
-// turn; 8–11: producers; 12–13: one MMA warp for each epilogue warpgroup (a
-// warp's waits run under the other's products).  An epilogue thread owns four
-// keys and a quarter of the rows (16x256b fragments): the rows' LSE, stored in
-// that order, costs it a quarter of the shared-memory reads that one key a
-// thread would, and the sum over rows stays in registers until the group ends.
+// tensor memory.  The rows stay in shared memory while the keys stream past.
+// Warps 0–15: two epilogue groups of eight; 16–19: producers; 20–21: an MMA
+// warp for each epilogue group (a warp's waits run under the other's products);
+// 22: the rows' TMA boxes.  An epilogue thread owns two keys and a quarter of
+// the rows (16x256b fragments): the rows' LSE, stored in that order, costs it
+// half of the shared-memory reads that one key a thread would.
 //
-// ONE (all rows of a request in one row tile): the rows stay in shared memory
-// while the request's keys stream past; work is dealt out by key tile.
-// Otherwise a work item is a group of two key tiles (256 keys, resident) that
-// the row tiles stream past (a row tile's 64 KB from L2 feed two products).
-// k_mass_plan lists each group's row tiles, those with a row that sees the
-// group's first key: under a causal limit the work halves.  All items' row
-// tiles, in order, are dealt out in equal contiguous runs to the CTAs; a run
-// that holds part of a group writes partial sums, which k_mass_join adds in
-// order.
+// RT = 1 (a request's rows fit one row tile): the key tiles alternate between
+// the groups, and a tile's sums go straight into `mass`.
+// RT = 2: a unit is a pair of row tiles, one for each group, with the keys
+// that some row of it sees (under a causal limit, half of them); every row
+// tile writes its sums to the workspace, and k_mass_join adds them in order.
+// Streaming the rows past resident keys instead moves 64 KB per two products
+// where this moves 32 KB, and could not be kept ahead of the tensor core
+// (measured: 2080 cycles a product against 1008).
+//
+// Work is dealt out by key tile in equal contiguous runs, one per CTA.
 
-constexpr int kTcEpi = 8;                       // epilogue warps
+constexpr int kTcEpi = 16;                      // epilogue warps, half for each accumulator
 constexpr int kTcProd = 4;                      // producer warps
-constexpr int kTcThreads = (kTcEpi + kTcProd + 2) * 32;
+constexpr int kTcThreads = (kTcEpi + kTcProd + 4) * 32;  // (the last warp idles)
+// Registers a thread after setmaxnreg: what the launch holds, 768 · 80, split
+// 512 · 88 + 256 · 64.
+constexpr int kTcMore = 88, kTcLess = 64;
 constexpr int kTcKeys = 128;                    // keys of a tile
 constexpr int kTcMaxK = 8;                      // K slots, at most
-constexpr int kTcQs = 4;                        // slots of 64 columns of a row tile
+constexpr size_t kTcPartBytes = size_t(1) << 29;  // partial sums of one launch, about
 
 struct MassTc {
   int n_cta;        // CTAs the work is dealt out to
@@ -352,41 +356,31 @@ struct MassTc {
   int k_slots;      // K ring
   int box;          // rows of a TMA box of K (a divisor of the page size), 0: none
   int q_box;        // queries by TMA (no row_idx)
-  int max_kg, max_rt;
+  int rg0, n_rg;    // RT 2: this launch's pairs of row tiles, [rg0, rg0 + n_rg)
   uint32_t idesc;
-  int64_t *cum;     // [n_req][max_kg + 1]: row tiles before each group (at least one each)
-  int2 *span;       // [n_req][max_kg]: first row tile and their number (0: nobody sees the group)
-  int *rt_vis;      // [n_req][max_rt]: positions the widest row of the tile sees
-  float *part;      // [2·n_cta][256]: partial sums
+  int64_t *cum;     // [n_req][n_rg + 1]: key tiles before each pair
+  float *part;      // [L·n_req·H][2·n_rg][cap]: each row tile's sums
 };
 
-template <bool ONE>
-struct TcShape {
-  static constexpr int kKG = ONE ? 1 : 2;   // key tiles of a group
-  static constexpr int kLs = ONE ? 2 : 4;   // LSE slots
-};
-
-// Head of the dynamic shared memory (fixed offsets), then K, q, and the LSE
-// slots: −lse·log2e and limits, [slot][NR + 16] in the order of lse_at.
+// Head of the dynamic shared memory (fixed offsets), behind K and q; then the
+// LSE slots: −lse·log2e, [slot][NR + 16] in the order of lse_at.
 struct TcHead {
-  uint64_t kfull[kTcMaxK], kempty[kTcMaxK], qfull[kTcQs], qempty[kTcQs], lfull[4], lempty[4];
+  uint64_t kfull[kTcMaxK], kempty[kTcMaxK], qfull[2], qempty[2], lfull[2], lempty[2];
   uint64_t tfull[4], tempty[4];
-  int64_t scan[66];
-  int lo[4][4];  // least limit of the slot's rows, per producer warp
+  int lo[2][4];  // least limit of the slot's rows, per producer warp
   uint32_t tmem_holder;
   volatile int failed;
 };
-constexpr uint32_t kTcHead = 1024;
+constexpr uint32_t kTcHead = 384;
 static_assert(sizeof(TcHead) <= kTcHead, "the head's room");
 
 struct TcSmem {
-  uint32_t k, q, nlse, vis, bytes;
-  __host__ __device__ TcSmem(int D, int NR, int ks, int ls) {
-    k = kTcHead;
-    q = k + ks * kTcKeys * D * 2;
-    nlse = q + kTcQs * NR * 128;
-    vis = nlse + ls * (NR + 16) * 4;
-    bytes = vis + ls * (NR + 16) * 4;
+  uint32_t q, head, nlse, bytes;  // K at 0
+  __host__ __device__ TcSmem(int D, int NR, int ks) {
+    q = ks * kTcKeys * D * 2;
+    head = q + 2 * NR * D * 2;
+    nlse = head + kTcHead;
+    bytes = nlse + 2 * (NR + 16) * 4;
   }
 };
 
@@ -396,99 +390,90 @@ __device__ __forceinline__ int lse_at(int r, int NR) {
   return ((r >> 1) & 3) * (NR / 4 + 4) + (r >> 3) * 2 + (r & 1);
 }
 
-// Groups of request r.
-__device__ __forceinline__ int tc_groups(const MassArgs &a, int r, int keys) {
-  return mass_tiles(a, r, keys);
+// Key tiles of request r, per layer and head.
+template <int RT>
+__device__ __forceinline__ int64_t tc_request_work(const MassArgs &a, const MassTc &p, int r) {
+  return RT == 1 ? mass_tiles(a, r, kTcKeys) : p.cum[(int64_t)r * (p.n_rg + 1) + p.n_rg];
 }
 
-// Where a run stands: group kg of (l, r, h), row tiles [off, cnt) of it left.
-template <bool ONE>
+// Where a run stands: key tile t of unit (l, r, h, pair rg), n_t tiles in it.
+template <int RT>
 struct TcPos {
   int64_t l;
-  int r, h, kg, n_kg;
-  int rt0, cnt;  // the group's first row tile and their number (0: none)
-  int off;       // done by earlier CTAs
-  __device__ __forceinline__ void load(const MassArgs &a, const MassTc &p) {
-    if (ONE) {
-      rt0 = 0;
-      cnt = 1;
+  int r, h, rg, t, n_t;
+  __device__ __forceinline__ void pair(const MassArgs &a, const MassTc &p) {
+    if (RT == 1) {
+      n_t = mass_tiles(a, r, kTcKeys);
     } else {
-      const int2 s = p.span[(int64_t)r * p.max_kg + kg];
-      rt0 = s.x;
-      cnt = s.y;
+      const int64_t *c = p.cum + (int64_t)r * (p.n_rg + 1) + rg;
+      n_t = (int)(c[1] - c[0]);
     }
   }
-  // the next group (one exists while the run is not over)
+  // the next tile (one exists while the run is not over)
   __device__ __forceinline__ void next(const MassArgs &a, const MassTc &p) {
-    off = 0;
-    if (++kg == n_kg) {
-      kg = 0;
-      if (++h == a.H) {
-        h = 0;
-        do {
+    if (++t < n_t) return;
+    t = 0;
+    do {
+      if (++rg == (RT == 1 ? 1 : p.n_rg)) {
+        rg = 0;
+        if (++h == a.H) {
+          h = 0;
           if (++r == a.n_req) {
             r = 0;
             l++;
           }
-          n_kg = tc_groups(a, r, TcShape<ONE>::kKG * kTcKeys);
-        } while (n_kg == 0);
+        }
       }
-    }
-    load(a, p);
+      pair(a, p);
+    } while (n_t == 0);
+  }
+  __device__ __forceinline__ int64_t unit(const MassArgs &a) const {
+    return (l * a.n_req + r) * a.H + h;
   }
 };
 
-template <bool ONE>
-__device__ __forceinline__ int64_t tc_request_work(const MassArgs &a, const MassTc &p, int r) {
-  const int n = tc_groups(a, r, TcShape<ONE>::kKG * kTcKeys);
-  return n == 0 ? 0 : ONE ? n : p.cum[(int64_t)r * (p.max_kg + 1) + n];
-}
-
-// Position of work item t (by the whole CTA).
-template <bool ONE>
-__device__ __forceinline__ TcPos<ONE> tc_find(const MassArgs &a, const MassTc &p, int64_t t,
-                                              int64_t per, int64_t *sh) {
-  TcPos<ONE> x;
-  x.l = t / (per * a.H);
+// Position of tile x (by the whole CTA).
+template <int RT>
+__device__ __forceinline__ TcPos<RT> tc_find(const MassArgs &a, const MassTc &p, int64_t x,
+                                             int64_t per, int64_t *sh) {
+  TcPos<RT> f;
+  f.l = x / (per * a.H);
   int64_t before;
-  const int64_t in_layer = t % (per * a.H);
+  const int64_t in_layer = x % (per * a.H);
   block_find(
-      a.n_req, in_layer, sh, [&](int r) { return a.H * tc_request_work<ONE>(a, p, r); }, x.r, before);
-  const int64_t w = tc_request_work<ONE>(a, p, x.r);
-  x.h = (int)((in_layer - before) / w);
+      a.n_req, in_layer, sh, [&](int r) { return a.H * tc_request_work<RT>(a, p, r); }, f.r, before);
+  const int64_t w = tc_request_work<RT>(a, p, f.r);
+  f.h = (int)((in_layer - before) / w);
   const int64_t in_head = (in_layer - before) % w;
-  x.n_kg = tc_groups(a, x.r, TcShape<ONE>::kKG * kTcKeys);
-  if (ONE) {
-    x.kg = (int)in_head;
-    x.off = 0;
+  if (RT == 1) {
+    f.rg = 0;
+    f.t = (int)in_head;
   } else {
-    const int64_t *cum = p.cum + (int64_t)x.r * (p.max_kg + 1);
-    int lo = 0, hi = x.n_kg - 1;  // the last group with cum ≤ in_head
+    const int64_t *cum = p.cum + (int64_t)f.r * (p.n_rg + 1);
+    int lo = 0, hi = p.n_rg - 1;  // the last pair with cum ≤ in_head
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (cum[mid] <= in_head) lo = mid;
       else hi = mid - 1;
     }
-    x.kg = lo;
-    x.off = (int)(in_head - cum[lo]);
+    f.rg = lo;
+    f.t = (int)(in_head - cum[lo]);
   }
-  x.load(a, p);
-  return x;
+  f.pair(a, p);
+  return f;
 }
 
-template <int D, bool ONE>
+template <int D, int RT>
 __global__ void __launch_bounds__(kTcThreads, 1)
 k_mass_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
           MassArgs a, MassTc p) {
-  constexpr int KG = TcShape<ONE>::kKG, LS = TcShape<ONE>::kLs, QS = kTcQs;
   constexpr int CH = D / 8, KB = D / 64;
   constexpr uint32_t kSlot = kTcKeys * D * 2;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *base = reinterpret_cast<uint8_t *>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t base[];
   const int NR = p.NR, KS = p.k_slots, NACC = 512 / NR;
-  TcHead &sm = *reinterpret_cast<TcHead *>(base);
-  const TcSmem at(D, NR, KS, LS);
+  const TcSmem at(D, NR, KS);
+  TcHead &sm = *reinterpret_cast<TcHead *>(base + at.head);
+  float *nlse = reinterpret_cast<float *>(base + at.nlse);
   const uint32_t base_u = smem_u32(base);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -496,15 +481,15 @@ k_mass_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
     sm.failed = 0;
     for (int i = 0; i < KS; i++) {
       mbar_init(smem_u32(sm.kfull + i), kTcProd * 32);
-      mbar_init(smem_u32(sm.kempty + i), 1);
+      mbar_init(smem_u32(sm.kempty + i), RT);
     }
-    for (int i = 0; i < QS; i++) {
-      mbar_init(smem_u32(sm.qfull + i), kTcProd * 32);
-      mbar_init(smem_u32(sm.qempty + i), 2);
-    }
-    for (int i = 0; i < LS; i++) {
+    for (int i = 0; i < 2; i++) {
+      // RT 1: both MMA warps and both epilogue groups use a unit's rows;
+      // RT 2: slot i is group i's
+      mbar_init(smem_u32(sm.qfull + i), p.q_box ? 1 : kTcProd * 32);
+      mbar_init(smem_u32(sm.qempty + i), RT == 1 ? 2 : 1);
       mbar_init(smem_u32(sm.lfull + i), kTcProd * 32);
-      mbar_init(smem_u32(sm.lempty + i), kTcEpi);
+      mbar_init(smem_u32(sm.lempty + i), RT == 1 ? kTcEpi : kTcEpi / 2);
     }
     for (int i = 0; i < NACC; i++) {
       mbar_init(smem_u32(sm.tfull + i), 1);
@@ -514,7 +499,7 @@ k_mass_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
   }
   // rows that no row tile fills stay zero
   if (p.tokens * a.G < NR) {
-    for (uint32_t i = tid; i < (uint32_t)kTcQs * NR * 128 / 16; i += kTcThreads)
+    for (uint32_t i = tid; i < 2u * NR * D * 2 / 16; i += kTcThreads)
       *reinterpret_cast<uint4 *>(base + at.q + i * 16) = make_uint4(0, 0, 0, 0);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -524,38 +509,44 @@ k_mass_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
   tc_fence_after();
   const uint32_t tmem = sm.tmem_holder;
 
-  if (!ONE) asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan
+  int64_t *scan = reinterpret_cast<int64_t *>(nlse);  // (before the first LSE is stored)
+  if (RT == 2) asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan
   int64_t per = 0;
   for (int r = tid; r < a.n_req; r += kTcThreads) {
-    per += tc_request_work<ONE>(a, p, r);
+    per += tc_request_work<RT>(a, p, r);
     int seq, r0, n;
-    if (ONE && blockIdx.x == 0 && !mass_request(a, r, seq, r0, n))
+    if (RT == 1 && blockIdx.x == 0 && !mass_request(a, r, seq, r0, n))
       record_error(a.status, KVC_ERR_BOUNDS);
   }
-  per = block_sum(per, sm.scan);
+  per = block_sum(per, scan);
   const int64_t total = per * a.L * a.H;
   const int n_cta = (int)min((int64_t)p.n_cta, total);
-  const bool works = (int)blockIdx.x < n_cta;
+  // (a misaligned base cannot hold swizzled tiles: nothing would be right)
+  const bool works = (int)blockIdx.x < n_cta && (base_u & 1023u) == 0;
+  if ((base_u & 1023u) != 0 && tid == 0) record_error(a.status, KVC_ERR_CUDA);
   const int64_t run0 = works ? total * blockIdx.x / n_cta : 0;
   const int64_t run1 = works ? total * (blockIdx.x + 1) / n_cta : 0;
-  TcPos<ONE> pos{};
-  if (works) pos = tc_find<ONE>(a, p, run0, per, sm.scan);
-  if (!ONE) asm volatile("griddepcontrol.launch_dependents;");
+  TcPos<RT> pos{};
+  if (works) pos = tc_find<RT>(a, p, run0, per, scan);
+  __syncthreads();
+  if (RT == 2) asm volatile("griddepcontrol.launch_dependents;");
 
   bool ok = true;
+  uint32_t uc = 0;    // units begun
   if (warp >= kTcEpi && warp < kTcEpi + kTcProd) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTcLess));
     // ------------------------------------------------------- producers
     // K: 32 keys of a tile a warp, by TMA boxes of whole page rows or row by row
-    // with cp.async (bad blocks, the end, page sizes without a box).  Rows: the
-    // whole tile in one TMA box, or row by row through row_idx; their LSE and
-    // limits through registers, a tile ahead.
+    // with cp.async (bad blocks, the end, page sizes without a box).  Rows: by
+    // another warp's TMA boxes, or row by row here, through row_idx; their LSE
+    // here.
     const int pw = warp - kTcEpi;
     const int64_t n_blocks = a.n_slots / a.BS;
     constexpr int RPI = 32 / CH;
     const int col = lane % CH;
-    uint32_t kc = 0, qc = 0;      // K tiles and row tiles loaded
+    uint32_t kc = 0;                // K tiles loaded
     uint32_t pend0 = 0, pend1 = 0;  // stages copied by cp.async and not handed over, oldest first
-    int64_t q_unit = -1;
+    int32_t blk = 0;                // block id of this lane's key of the next tile
     auto hand = [&](uint32_t bar) {
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(bar);
@@ -586,344 +577,322 @@ k_mass_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
       flush();
       return mbar_wait_bounded(smem_u32(bar), parity, &sm.failed);
     };
-    // this lane's rows of a row tile: lr = 32·pw + 128·u + lane
+    // this lane's rows of a row tile: 32·pw + 128·u + lane
     const int tok0 = (32 * pw + lane) / a.G, g0 = (32 * pw + lane) % a.G;
     const int tok1 = (32 * pw + lane + 128) / a.G, g1 = (32 * pw + lane + 128) % a.G;
-    for (int64_t g = run0; g < run1 && ok;) {
-      const int todo = (int)min((int64_t)max(pos.cnt, 1) - pos.off, run1 - g);
-      if (pos.cnt > 0) {
-        int seq, r0, n;
-        mass_request(a, pos.r, seq, r0, n);
-        const int32_t *bt = a.block_table + (int64_t)pos.r * a.max_blocks;
+    for (int64_t g = run0; g < run1 && ok; g++) {
+      int seq, r0, n;
+      mass_request(a, pos.r, seq, r0, n);
+      const int32_t *bt = a.block_table + (int64_t)pos.r * a.max_blocks;
+      const bool begins = g == run0 || pos.t == 0;  // of a unit, in this run
+      auto look = [&](int t) {
+        const int pp = t * kTcKeys + pw * 32 + lane;
+        blk = pp < seq ? bt[page_of(pp, a.bs_inv)] : 0;
+      };
+      if (begins) look(pos.t);
+      // ---- the tile of K
+      const int pp = pos.t * kTcKeys + pw * 32 + lane;
+      int32_t slot = -1;
+      if (pp < seq) {
+        if (blk >= 0 && blk < n_blocks) slot = blk * a.BS + pp - page_of(pp, a.bs_inv) * a.BS;
+        else record_error(a.status, KVC_ERR_BOUNDS);
+      }
+      look(pos.t + 1);
+      const uint32_t st = kc % KS;
+      if (!(ok = acquire(sm.kempty + st, ((kc / KS) & 1) ^ 1))) break;
+      kc++;
+      const uint32_t bar = smem_u32(sm.kfull + st);
+      const uint32_t slot0 = base_u + st * kSlot + pw * 32 * 128;
+      if (p.box > 0 && __all_sync(0xFFFFFFFFu, slot >= 0)) {
+        if (lane == 0) mbar_expect_tx(bar, kSlot / kTcProd);
+        else mbar_arrive(bar);
+        __syncwarp();
+        // (warp-uniform operands, one lane enabled)
+        const uint32_t ubar = uniform32(bar), udst = uniform32(slot0), uh = uniform32(pos.h);
+        const uint32_t row0 = uniform32((uint32_t)(pos.l * a.n_slots));
+        for (int k = 0; k < 32; k += p.box) {
+          const uint32_t sl = __shfl_sync(0xFFFFFFFFu, slot, k);
+#pragma unroll
+          for (int kb = 0; kb < KB; kb++)
+            tma_load_3d_if(lane == 0, udst + k * 128 + kb * (kTcKeys * 128), &tm_k, kb * 64, uh,
+                           row0 + sl, ubar);
+        }
+      } else {
         const uint16_t *kl = a.kpool + (pos.l * a.n_slots * a.H + pos.h) * D;
-        const float *lse = a.lse + pos.l * a.n_q * a.Hq + pos.h * a.G;
-        const int64_t unit = (pos.l * a.n_req + pos.r) * a.H + pos.h;
-        const uint32_t uh = uniform32(pos.h);
-        auto load_k = [&](int kt) {
-          const uint32_t st = kc % KS;
-          const int t = pos.kg * KG + kt, pp = t * kTcKeys + pw * 32 + lane;
-          int32_t slot = -1;
-          if (pp < seq) {
-            const int pg = page_of(pp, a.bs_inv);
-            const int32_t b = bt[pg];
-            if (b >= 0 && b < n_blocks) slot = b * a.BS + pp - pg * a.BS;
-            else record_error(a.status, KVC_ERR_BOUNDS);
-          }
-          if (!(ok = acquire(sm.kempty + st, ((kc / KS) & 1) ^ 1))) return;
-          kc++;
-          const uint32_t bar = smem_u32(sm.kfull + st);
-          const uint32_t slot0 = base_u + at.k + st * kSlot + pw * 32 * 128;
-          if (p.box > 0 && __all_sync(0xFFFFFFFFu, slot >= 0)) {
-            if (lane == 0) mbar_expect_tx(bar, kSlot / kTcProd);
-            else mbar_arrive(bar);
-            __syncwarp();
-            const uint32_t ubar = uniform32(bar), udst = uniform32(slot0);
-            const uint32_t row0 = uniform32((uint32_t)(pos.l * a.n_slots));
-            for (int k = 0; k < 32; k += p.box) {
-              const uint32_t sl = __shfl_sync(0xFFFFFFFFu, slot, k);
-#pragma unroll
-              for (int kb = 0; kb < KB; kb++)
-                tma_load_3d_if(lane == 0, udst + k * 128 + kb * (kTcKeys * 128), &tm_k, kb * 64, uh,
-                               row0 + sl, ubar);
-            }
-            return;
-          }
-          const uint32_t dst = slot0 + (col >> 3) * (kTcKeys * 128);
+        const uint32_t dst = slot0 + (col >> 3) * (kTcKeys * 128);
 #pragma unroll 4
-          for (int i = 0; i < 32 / RPI; i++) {
-            const int row = i * RPI + lane / CH;
-            const int32_t sl = __shfl_sync(0xFFFFFFFFu, slot, row);
-            cp_async16(dst + row * 128 + (((col & 7) ^ (row & 7)) << 4),
-                       kl + (int64_t)max(sl, 0) * a.H * D + col * 8, sl >= 0);
-          }
-          committed(bar);
-        };
-        // LSE, limit and query row of this lane's rows of row tile rt
-        float nl[2];
-        int vi[2], qx[2];
-        auto fetch = [&](int rt) {
-#pragma unroll
-          for (int u = 0; u < 2; u++) {
-            const int tok = u ? tok1 : tok0, gg = u ? g1 : g0, i = rt * p.tokens + tok;
-            nl[u] = -INFINITY;
-            vi[u] = 0;
-            qx[u] = -1;
-            if (tok < p.tokens && i < n && (u == 0 || NR > 128)) {
-              const int x = a.row_idx ? a.row_idx[r0 + i] : r0 + i;
-              vi[u] = min(a.row_vis[r0 + i], seq);
-              if (x >= 0 && x < a.n_q) {
-                nl[u] = -lse[(int64_t)x * a.Hq + gg] * kLog2e;
-                qx[u] = x;
-              } else if (vi[u] > 0) {
-                record_error(a.status, KVC_ERR_BOUNDS);
-              }
-            }
-          }
-        };
-        auto load_q = [&](int rt, bool more) {
-          const uint32_t ls = (qc / KB) % LS;
-          if (!(ok = acquire(sm.lempty + ls, (((qc / KB) / LS) & 1) ^ 1))) return;
-          float *nls = reinterpret_cast<float *>(base + at.nlse) + ls * (NR + 16);
-          int *vis = reinterpret_cast<int *>(base + at.vis) + ls * (NR + 16);
+        for (int i = 0; i < 32 / RPI; i++) {
+          const int row = i * RPI + lane / CH;
+          const int32_t sl = __shfl_sync(0xFFFFFFFFu, slot, row);
+          cp_async16(dst + row * 128 + (((col & 7) ^ (row & 7)) << 4),
+                     kl + (int64_t)max(sl, 0) * a.H * D + col * 8, sl >= 0);
+        }
+        committed(bar);
+      }
+      // ---- a new unit's rows
+      if (begins) {
+        const float *lse = a.lse + pos.l * a.n_q * a.Hq + pos.h * a.G;
+#pragma unroll 1
+        for (int j = 0; j < RT && ok; j++) {
+          const uint32_t s = RT == 1 ? uc & 1 : j, use = RT == 1 ? uc >> 1 : uc;
+          const int rt = RT == 1 ? 0 : 2 * (p.rg0 + pos.rg) + j;
+          if (!(ok = acquire(sm.lempty + s, (use & 1) ^ 1))) break;
           // A row that adds nothing (past the request's rows, no limit, LSE ±inf)
           // has weight 0 by its LSE where its product is finite: its query is
           // zeros, or, where a box brought it along and it may be anything, the
-          // tile is masked for every key (lo = 0).
+          // tiles are masked for every key (lo = 0).
           int lo = INT_MAX;
           int64_t src_row[2];
 #pragma unroll
           for (int u = 0; u < 2; u++) {
             src_row[u] = -1;
             if (u == 1 && NR == 128) break;
-            const bool on = qx[u] >= 0 && vi[u] > 0 && fabsf(nl[u]) != INFINITY;
-            const int r = lse_at(128 * u + 32 * pw + lane, NR);
-            nls[r] = on ? nl[u] : -INFINITY;
-            vis[r] = on ? vi[u] : 0;
-            if (on) lo = min(lo, vi[u]);
-            else if (p.q_box && (u ? tok1 : tok0) < p.tokens) lo = 0;
-            if (on)
-              src_row[u] = (pos.l * a.n_q + qx[u]) * a.Hq + pos.h * a.G + (u ? g1 : g0);
+            const int tok = u ? tok1 : tok0, i = rt * p.tokens + tok;
+            float nl = -INFINITY;
+            if (tok < p.tokens) {
+              if (i < n) {
+                const int vis = min(a.row_vis[r0 + i], seq), x = a.row_idx ? a.row_idx[r0 + i] : r0 + i;
+                if (vis > 0 && x >= 0 && x < a.n_q) {
+                  const float l2 = lse[(int64_t)x * a.Hq + (u ? g1 : g0)] * kLog2e;
+                  if (fabsf(l2) != INFINITY) {
+                    nl = -l2;
+                    lo = min(lo, vis);
+                    src_row[u] = (pos.l * a.n_q + x) * a.Hq + pos.h * a.G + (u ? g1 : g0);
+                  }
+                } else if (vis > 0) {
+                  record_error(a.status, KVC_ERR_BOUNDS);
+                }
+              }
+              if (p.q_box && nl == -INFINITY) lo = 0;
+            }
+            nlse[s * (NR + 16) + lse_at(128 * u + 32 * pw + lane, NR)] = nl;
           }
           lo = __reduce_min_sync(0xFFFFFFFFu, lo);
-          if (lane == 0) sm.lo[ls][pw] = lo;
+          if (lane == 0) sm.lo[s][pw] = lo;
           __syncwarp();
-          mbar_arrive(smem_u32(sm.lfull + ls));
-          if (more) fetch(rt + 1);
-          for (int kb = 0; kb < KB; kb++, qc++) {
-            const uint32_t st = qc % QS;
-            if (!(ok = acquire(sm.qempty + st, ((qc / QS) & 1) ^ 1))) return;
-            const uint32_t bar = smem_u32(sm.qfull + st), dst = base_u + at.q + st * (NR * 128);
-            if (p.q_box) {
-              if (pw == 0 && lane == 0) {
-                mbar_expect_tx(bar, p.tokens * a.G * 128);
-                tma_load_3d(dst, &tm_q, kb * 64, pos.h * a.G,
-                            (int)(pos.l * a.n_q) + r0 + rt * p.tokens, bar);
-              } else {
-                mbar_arrive(bar);
-              }
-              continue;
-            }
+          mbar_arrive(smem_u32(sm.lfull + s));
+          if (p.q_box) continue;
+          if (!(ok = acquire(sm.qempty + s, (use & 1) ^ 1))) break;
+          const uint32_t dst = base_u + at.q + s * (NR * D * 2) + (col >> 3) * (NR * 128);
 #pragma unroll
-            for (int u = 0; u < 2; u++) {
-              if (u == 1 && NR == 128) break;
-#pragma unroll
-              for (int i = 0; i < 8; i++) {
-                const int rr = i * 4 + lane / 8, c8 = lane % 8;
-                const int64_t src = __shfl_sync(0xFFFFFFFFu, src_row[u], rr);
-                cp_async16(dst + (128 * u + 32 * pw + rr) * 128 + ((c8 ^ (rr & 7)) << 4),
-                           a.q + max(src, (int64_t)0) * D + kb * 64 + c8 * 8, src >= 0);
-              }
+          for (int u = 0; u < 2; u++) {
+            if (u == 1 && NR == 128) break;
+#pragma unroll 4
+            for (int i = 0; i < 32 / RPI; i++) {
+              const int rr = i * RPI + lane / CH;
+              const int64_t src = __shfl_sync(0xFFFFFFFFu, src_row[u], rr);
+              cp_async16(dst + (128 * u + 32 * pw + rr) * 128 + (((col & 7) ^ (rr & 7)) << 4),
+                         a.q + max(src, (int64_t)0) * D + col * 8, src >= 0);
             }
-            committed(bar);
           }
-        };
-        if (!ONE || unit != q_unit) fetch(pos.rt0 + pos.off);
-        load_k(0);
-        if (ONE) {
-          if (ok && unit != q_unit) {
-            load_q(0, false);
-            flush();  // (the next stages may all be boxes)
-          }
-        } else {
-          for (int i = 0; i < todo && ok; i++) {
-            load_q(pos.rt0 + pos.off + i, i + 1 < todo);
-            if (i == 0 && ok) load_k(1);
-          }
+          committed(smem_u32(sm.qfull + s));
         }
-        q_unit = unit;
+        flush();  // (the next stages may all be boxes)
+        uc++;
       }
-      g += todo;
-      if (g < run1) pos.next(a, p);
+      if (g + 1 < run1) pos.next(a, p);
     }
     flush();
     cp_wait<0>();
     if (!ok) sm.failed = 1;
   } else if (warp >= kTcEpi + kTcProd) {
-    // ----------------------------------------------------- MMA issuers
-    // (the whole warp runs the loop; one lane's products are enabled)
-    const int wg = warp - kTcEpi - kTcProd;  // the epilogue warpgroup it works for
-    const uint32_t lead = lane == 0;
-    uint32_t kc = 0, qc = 0, jc = 0;  // first K tile of the group, q stages, products of both
-    int64_t q_unit = -1;
-    for (int64_t g = run0; g < run1 && ok;) {
-      const int todo = (int)min((int64_t)max(pos.cnt, 1) - pos.off, run1 - g);
-      if (pos.cnt > 0) {
-        const int64_t unit = (pos.l * a.n_req + pos.r) * a.H + pos.h;
-        for (int i = 0; i < todo && ok; i++) {
-          if (!ONE || unit != q_unit) {
-            if (ONE && qc > 0)
-              for (int kb = 0; kb < KB; kb++) mma_commit_if(lead, smem_u32(sm.qempty + (qc - KB + kb) % QS));
-            qc += KB;
-            // (also for a unit without a tile of this warp's: a barrier's parity
-            // tells only two uses apart)
-            for (int kb = 0; ONE && kb < KB && ok; kb++)
-              ok = mbar_wait_bounded(smem_u32(sm.qfull + (qc - KB + kb) % QS),
-                                     ((qc - KB + kb) / QS) & 1, &sm.failed);
-            if (!ok) break;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTcLess));
+    if (warp == kTcEpi + kTcProd + 2) {
+      // ----------------------------------------------- rows by TMA boxes
+      if (p.q_box && lane == 0)
+        for (int64_t g = run0; g < run1 && ok; g++) {
+          if (g == run0 || pos.t == 0) {
+            for (int j = 0; j < RT && ok; j++) {
+              const uint32_t s = RT == 1 ? uc & 1 : j, use = RT == 1 ? uc >> 1 : uc;
+              const int rt = RT == 1 ? 0 : 2 * (p.rg0 + pos.rg) + j;
+              const uint32_t bar = smem_u32(sm.qfull + s);
+              if (!(ok = mbar_wait_bounded(smem_u32(sm.qempty + s), (use & 1) ^ 1, &sm.failed))) break;
+              mbar_expect_tx(bar, p.tokens * a.G * D * 2);
+  #pragma unroll
+              for (int kb = 0; kb < KB; kb++)
+                tma_load_3d(base_u + at.q + s * (NR * D * 2) + kb * (NR * 128), &tm_q, kb * 64,
+                            pos.h * a.G, (int)(pos.l * a.n_q) + a.row_off[pos.r] + rt * p.tokens, bar);
+            }
+            uc++;
           }
-          const uint32_t job = ONE ? jc : jc + wg;
-          jc += KG;
-          if (ONE && (job & 1) != (uint32_t)wg) continue;
-          const uint32_t kx = kc + (ONE ? 0 : wg), kst = kx % KS, acc = job % NACC;
-          ok = mbar_wait_bounded(smem_u32(sm.kfull + kst), (kx / KS) & 1, &sm.failed);
-          if (ok) ok = mbar_wait_bounded(smem_u32(sm.tempty + acc), ((job / NACC) & 1) ^ 1, &sm.failed);
-          const uint64_t kd = uniform64(smem_desc(base_u + at.k + kst * kSlot));
-          const uint32_t dst = uniform32(tmem + acc * NR);
-#pragma unroll
-          for (int kb = 0; kb < KB; kb++) {
-            const uint32_t qi = qc - KB + kb, qst = qi % QS;
-            if (ok) ok = mbar_wait_bounded(smem_u32(sm.qfull + qst), (qi / QS) & 1, &sm.failed);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t qd = uniform64(smem_desc(base_u + at.q + qst * (NR * 128)));
-#pragma unroll
-            for (int kk = 0; kk < 4; kk++)
-              mma_bf16_if(lead, dst, kd + kb * (kTcKeys * 8) + kk * 2, qd + kk * 2, p.idesc,
-                          kb > 0 || kk > 0);
-            if (!ONE) mma_commit_if(lead, smem_u32(sm.qempty + qst));
-          }
+          if (g + 1 < run1) pos.next(a, p);
+        }
+      if (!ok) sm.failed = 1;
+      __syncwarp();
+    } else if (warp < kTcEpi + kTcProd + 2) {
+      // ----------------------------------------------------- MMA issuers
+      // (the whole warp runs the loop; one lane's products are enabled)
+      const int wg = warp - kTcEpi - kTcProd;  // the epilogue group it works for
+      const uint32_t lead = lane == 0;
+      uint32_t kc = 0, jc = 0;  // K tiles, this group's products
+      uint64_t qd = 0;
+      for (int64_t g = run0; g < run1 && ok; g++, kc++) {
+        if (g == run0 || pos.t == 0) {
+          if (RT == 1 && uc > 0) mma_commit_if(lead, smem_u32(sm.qempty + ((uc - 1) & 1)));
+          const uint32_t s = RT == 1 ? uc & 1 : wg, use = RT == 1 ? uc >> 1 : uc;
+          // (RT 1: also for a unit without a tile of this warp's: a barrier's parity
+          // tells only two uses apart)
+          if (!(ok = mbar_wait_bounded(smem_u32(sm.qfull + s), use & 1, &sm.failed))) break;
+          qd = uniform64(smem_desc(base_u + at.q + s * (NR * D * 2)));
+          uc++;
+        }
+        const bool last = g + 1 == run1 || pos.t + 1 == pos.n_t;  // of the unit, in this run
+        if (RT == 2 || (kc & 1) == (uint32_t)wg) {
+          const uint32_t st = kc % KS, acc = RT == 2 ? wg : kc % NACC;
+          // acc's products: RT 2 every one of the warp's, RT 1 every NACC-th tile
+          const uint32_t use = RT == 2 ? jc : kc / NACC;
+          ok = mbar_wait_bounded(smem_u32(sm.kfull + st), (kc / KS) & 1, &sm.failed);
+          if (ok) ok = mbar_wait_bounded(smem_u32(sm.tempty + acc), (use & 1) ^ 1, &sm.failed);
           if (!ok) break;
+          tc_fence_after();
+          const uint64_t kd = uniform64(smem_desc(base_u + st * kSlot));
+          const uint32_t dst = uniform32(tmem + acc * NR), qk = uniform32(NR * 8);
+  #pragma unroll
+          for (int kk = 0; kk < 4 * KB; kk++)
+            mma_bf16_if(lead, dst, kd + (kk >> 2) * (kTcKeys * 8) + (kk & 3) * 2,
+                        qd + (kk >> 2) * qk + (kk & 3) * 2, p.idesc, kk > 0);
           mma_commit_if(lead, smem_u32(sm.tfull + acc));
-          if (i == todo - 1) mma_commit_if(lead, smem_u32(sm.kempty + kst));
+          mma_commit_if(lead, smem_u32(sm.kempty + st));
+          if (RT == 2 && last) mma_commit_if(lead, smem_u32(sm.qempty + wg));
+          jc++;
         }
-        kc += KG;
-        q_unit = unit;
+        if (g + 1 < run1) pos.next(a, p);
       }
-      g += todo;
-      if (g < run1) pos.next(a, p);
+      if (!ok) sm.failed = 1;
+      __syncwarp();
     }
-    if (!ok) sm.failed = 1;
-    __syncwarp();
-  } else if (warp < kTcEpi) {
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTcMore));
     // -------------------------------------------------------- epilogue
-    const int wg = warp >> 2, quarter = warp & 3;
-    const uint32_t lane_base = (uint32_t)(32 * quarter) << 16;
-    const float zs = a.zscale;
-    uint32_t qc = 0, jc = 0;
-    int64_t q_unit = -1;
+    const int wg = warp >> 3, quarter = warp & 3, half = (warp >> 2) & 1;
+    const int key0 = quarter * 32 + half * 16;  // the warp's 16 keys of a tile
+    const uint32_t lane_base = (uint32_t)key0 << 16;
+    const uint64_t zs2 = pk2(a.zscale, a.zscale);
+    uint32_t kc = 0, jc = 0;
     int lo = 0;
-    for (int64_t g = run0; g < run1 && ok;) {
-      const int todo = (int)min((int64_t)max(pos.cnt, 1) - pos.off, run1 - g);
-      const int64_t unit = (pos.l * a.n_req + pos.r) * a.H + pos.h;
-      const int seq = a.seqused[pos.r];
-      const int kt = ONE ? 0 : wg;
-      const int p0 = (pos.kg * KG + kt) * kTcKeys, key = p0 + quarter * 32 + lane;
-      const bool mine = ONE ? (jc & 1) == (uint32_t)wg : true;
-      const bool whole = pos.off == 0 && todo == max(pos.cnt, 1);
-      float *out = a.mass + unit * a.cap + key;
-      float old = 0.f;
-      // this thread's rows added up, keys lane/4 + 8·i of the warp's 32
-      float s4[4] = {0.f, 0.f, 0.f, 0.f};
-      int32_t blk = -1;
-      if (mine && key < seq) {
-        if (whole && key < a.n_mass[pos.r]) old = *out;
-        blk = a.block_table[(int64_t)pos.r * a.max_blocks + page_of(key, a.bs_inv)];
+    const float *nl = nlse;  // the slot's LSE
+    const int nl_q = (lane & 3) * (NR / 4 + 4);
+    const int64_t n_blocks = a.n_slots / a.BS;
+    // lanes 0–15's key: its sum's place, its block id and its weight so far, the
+    // last two fetched a tile of the group ahead
+    constexpr int kStep = RT == 1 ? 2 * kTcKeys : kTcKeys;
+    int seq = 0, n_old = 0;
+    float *out0 = nullptr, old = 0.f, next_old = 0.f;
+    const int32_t *bt = nullptr;
+    int32_t blk = -1, next_blk = -1;
+    auto fetch = [&](int key) {
+      next_blk = key < seq ? bt[page_of(key, a.bs_inv)] : -1;
+      if (RT == 1) next_old = key < n_old ? out0[key] : 0.f;
+    };
+    for (int64_t g = run0; g < run1 && ok; g++, kc++) {
+      const bool mine = RT == 2 || (kc & 1) == (uint32_t)wg;
+      const int p0 = pos.t * kTcKeys, key = p0 + key0 + (lane & 15);
+      if (g == run0 || pos.t == 0) {
+        __syncwarp();
+        if (uc > 0 && lane == 0) mbar_arrive(smem_u32(sm.lempty + (RT == 1 ? (uc - 1) & 1 : wg)));
+        const int64_t u = pos.unit(a);
+        seq = a.seqused[pos.r];
+        bt = a.block_table + (int64_t)pos.r * a.max_blocks;
+        if (RT == 1) n_old = min(seq, a.n_mass[pos.r]);
+        out0 = RT == 1 ? a.mass + u * a.cap : p.part + (u * 2 * p.n_rg + 2 * pos.rg + wg) * a.cap;
+        fetch(mine ? key : key + kTcKeys);
+        const uint32_t s = RT == 1 ? uc & 1 : wg, use = RT == 1 ? uc >> 1 : uc;
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.lfull + s), use & 1, &sm.failed));
+        if (!ok) break;
+        lo = min(min(sm.lo[s][0], sm.lo[s][1]), min(sm.lo[s][2], sm.lo[s][3]));
+        if (lo == INT_MAX) lo = 0;
+        nl = nlse + s * (NR + 16);
+        uc++;
       }
-      if (pos.cnt > 0)
-        for (int i = 0; i < todo && ok; i++) {
-          if (!ONE || unit != q_unit) {  // another row tile
-            if (ONE && qc > 0) {
-              __syncwarp();
-              if (lane == 0) mbar_arrive(smem_u32(sm.lempty + (qc - 1) % LS));
-            }
-            qc++;
-            const int ls = (qc - 1) % LS;
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.lfull + ls),
-                                                           ((qc - 1) / LS) & 1, &sm.failed));
-            if (!ok) break;
-            lo = min(min(sm.lo[ls][0], sm.lo[ls][1]), min(sm.lo[ls][2], sm.lo[ls][3]));
-            if (lo == INT_MAX) lo = 0;
-          }
-          const int ls = (qc - 1) % LS;
-          const uint32_t job = ONE ? jc : jc + wg;
-          jc += KG;
-          if (mine) {
-            const int acc = job % NACC;
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.tfull + acc),
-                                                           (job / NACC) & 1, &sm.failed));
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t taddr = tmem + lane_base + acc * NR;
-            const int qoff = ls * (NR + 16) + (lane & 3) * (NR / 4 + 4);
-            const float *nl = reinterpret_cast<const float *>(base + at.nlse) + qoff;
-            const int *vi = reinterpret_cast<const int *>(base + at.vis) + qoff;
-            float t4[4] = {0.f, 0.f, 0.f, 0.f};  // this tile's, apart from the others'
-            if (p0 + kTcKeys <= lo) {
-              // every row sees every key of the tile
-              uint32_t z[2][32];
-              tmem_frag8(taddr, z[0]);
+      if (mine) {
+        const uint32_t acc = RT == 2 ? wg : kc % NACC, use = RT == 2 ? jc : kc / NACC;
+        blk = next_blk;
+        old = next_old;
+        fetch(key + kStep);
+        ok = __all_sync(0xFFFFFFFFu,
+                        mbar_wait_bounded(smem_u32(sm.tfull + acc), use & 1, &sm.failed));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t taddr = tmem + lane_base + acc * NR;
+        uint64_t s2[2] = {0, 0};  // keys lane/4 and lane/4 + 8, even and odd rows
+        if (p0 + kTcKeys <= lo) {
+          // every row sees every key of the tile
+          uint32_t z[2][16];
+          tmem_frag4(taddr, z[0]);
 #pragma unroll 1
-              for (int c = 0; c < NR; c += 64) {
-                float n16[16];
+          for (int c = 0; c < NR; c += 64) {
+            uint64_t t2[2] = {0, 0};
 #pragma unroll
-                for (int j = 0; j < 16; j += 4)
-                  *reinterpret_cast<float4 *>(n16 + j) = *reinterpret_cast<const float4 *>(nl + c / 4 + j);
+            for (int hf = 0; hf < 2; hf++) {
+              float n8[8];
 #pragma unroll
-                for (int hf = 0; hf < 2; hf++) {
-                  tmem_wait(z[hf]);
-                  if (hf == 0) tmem_frag8(taddr + c + (16u << 16), z[1]);
-                  else if (c + 64 < NR) tmem_frag8(taddr + c + 64, z[0]);
+              for (int j = 0; j < 8; j += 4)
+                *reinterpret_cast<float4 *>(n8 + j) =
+                    *reinterpret_cast<const float4 *>(nl + nl_q + c / 4 + 8 * hf + j);
+              tmem_wait(z[hf]);
+              if (hf == 0 || c + 64 < NR) tmem_frag4(taddr + c + 32 * hf + 32, z[hf ^ 1]);
 #pragma unroll
-                  for (int e = 0; e < 32; e += 4) {
-                    const float w0 = ex2(fmaf(__uint_as_float(z[hf][e]), zs, n16[e / 2]));
-                    const float w1 = ex2(fmaf(__uint_as_float(z[hf][e + 1]), zs, n16[e / 2 + 1]));
-                    const float w2 = ex2(fmaf(__uint_as_float(z[hf][e + 2]), zs, n16[e / 2]));
-                    const float w3 = ex2(fmaf(__uint_as_float(z[hf][e + 3]), zs, n16[e / 2 + 1]));
-                    t4[2 * hf] += w0 + w1;
-                    t4[2 * hf + 1] += w2 + w3;
-                  }
-                }
+              for (int e = 0; e < 16; e += 2) {
+                const int j = (e >> 2) * 2;
+                float w0, w1;
+                upk2(fma2(pk2(__uint_as_float(z[hf][e]), __uint_as_float(z[hf][e + 1])), zs2,
+                          pk2(n8[j], n8[j + 1])),
+                     w0, w1);
+                t2[(e >> 1) & 1] = add2(t2[(e >> 1) & 1], pk2(ex2(w0), ex2(w1)));
               }
-            } else {
-#pragma unroll 1
-              for (int c = 0; c < NR; c += 64)
-#pragma unroll
-                for (int hf = 0; hf < 2; hf++) {
-                  uint32_t z[32];
-                  tmem_frag8(taddr + c + ((uint32_t)(16 * hf) << 16), z);
-                  tmem_wait(z);
-                  const int k0 = p0 + quarter * 32 + hf * 16 + lane / 4;
-#pragma unroll
-                  for (int e = 0; e < 32; e++) {
-                    const int col = c / 4 + (e >> 2) * 2 + (e & 1), k = k0 + 8 * ((e >> 1) & 1);
-                    const float w = ex2(fmaf(__uint_as_float(z[e]), zs, nl[col]));
-                    t4[2 * hf + ((e >> 1) & 1)] += k < vi[col] ? w : 0.f;
-                  }
-                }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(sm.tempty + acc));
-#pragma unroll
-            for (int k = 0; k < 4; k++) s4[k] += t4[k];
+            s2[0] = add2(s2[0], t2[0]);
+            s2[1] = add2(s2[1], t2[1]);
           }
-          if (!ONE) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(sm.lempty + ls));
-          }
-        }
-      q_unit = unit;
-      // the four lanes of a key, then each lane its own key
-      float total_w = 0.f;
-#pragma unroll
-      for (int k = 0; k < 4; k++) {
-        float x = s4[k];
-        x += __shfl_xor_sync(0xFFFFFFFFu, x, 1);
-        x += __shfl_xor_sync(0xFFFFFFFFu, x, 2);
-        x = __shfl_sync(0xFFFFFFFFu, x, (lane & 7) << 2);
-        if ((lane >> 3) == k) total_w = x;
-      }
-      if (ok && mine) {
-        const float add = blk >= 0 && blk < a.n_slots / a.BS ? total_w : 0.f;
-        if (whole) {
-          if (key < seq) *out = fmaf(a.decay, old, add);
         } else {
-          p.part[(2 * (int64_t)blockIdx.x + (g != run0)) * (KG * kTcKeys) + kt * kTcKeys +
-                 quarter * 32 + lane] = add;
+          // the rows' limits: 32 rows a lane-wide load, one exchange per two rows
+          const int r0 = a.row_off[pos.r], n = a.row_off[pos.r + 1] - r0;
+          const int i0 = RT == 1 ? 0 : (2 * (p.rg0 + pos.rg) + wg) * p.tokens;
+          const int k0 = p0 + key0 + lane / 4;
+          float m0 = 0.f, m1 = 0.f;
+#pragma unroll 1
+          for (int c = 0; c < NR; c += 32) {
+            uint32_t z[16];
+            tmem_frag4(taddr + c, z);
+            const int i = i0 + (c + lane) / a.G;
+            int vis = 0;
+            if (i < n && nl[lse_at(c + lane, NR)] != -INFINITY) vis = a.row_vis[r0 + i];
+            tmem_wait(z);
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+#pragma unroll
+              for (int b = 0; b < 2; b++) {
+                const int v = __shfl_sync(0xFFFFFFFFu, vis, 2 * e + 2 * (lane & 3) + b);
+                const float nb = nl[nl_q + c / 4 + e / 2 + b];
+                const float w0 = ex2(fmaf(__uint_as_float(z[e + b]), a.zscale, nb));
+                const float w1 = ex2(fmaf(__uint_as_float(z[e + 2 + b]), a.zscale, nb));
+                m0 += k0 < v ? w0 : 0.f;
+                m1 += k0 + 8 < v ? w1 : 0.f;
+              }
+          }
+          s2[0] = pk2(m0, 0.f);
+          s2[1] = pk2(m1, 0.f);
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(sm.tempty + acc));
+        // the four lanes of a key, then lanes 0–15 each their own key
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+          float x, y;
+          upk2(s2[k], x, y);
+          x += y;
+          x += __shfl_xor_sync(0xFFFFFFFFu, x, 1);
+          x += __shfl_xor_sync(0xFFFFFFFFu, x, 2);
+          x = __shfl_sync(0xFFFFFFFFu, x, (lane & 7) << 2);
+          if (((lane >> 3) & 1) == k) sum = x;
+        }
+        if (blk < 0 || blk >= n_blocks) sum = 0.f;
+        if (key < seq && lane < 16) out0[key] = RT == 1 ? fmaf(a.decay, old, sum) : sum;
+        jc++;
       }
-      g += todo;
-      if (g < run1) pos.next(a, p);
+      if (g + 1 < run1) pos.next(a, p);
     }
     if (!ok) {
       sm.failed = 1;
@@ -941,7 +910,7 @@ k_mass_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
       mbar_drain(smem_u32(sm.kfull + i), 0);
       mbar_drain(smem_u32(sm.kfull + i), 1);
     }
-    for (int i = 0; i < QS; i++) {
+    for (int i = 0; i < 2; i++) {
       mbar_drain(smem_u32(sm.qfull + i), 0);
       mbar_drain(smem_u32(sm.qfull + i), 1);
     }
@@ -957,42 +926,32 @@ k_mass_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
   }
 }
 
-// Row tiles of every key group of every request, one CTA per request.
+// Key tiles of each pair of row tiles (up to the widest limit among its rows)
+// and their running sums, one CTA per request.
 __global__ void __launch_bounds__(256)
 k_mass_plan(MassArgs a, MassTc p) {
-  __shared__ int64_t sh[66];
+  __shared__ int64_t sh[64];
   asm volatile("griddepcontrol.launch_dependents;");
-  const int r = blockIdx.x, tid = threadIdx.x;
+  const int r = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int64_t *cum = p.cum + (int64_t)r * (p.n_rg + 1);
   int seq, r0, n;
-  if (!mass_request(a, r, seq, r0, n)) {
-    if (tid == 0) record_error(a.status, KVC_ERR_BOUNDS);
-    return;
-  }
-  const int n_rt = (n + p.tokens - 1) / p.tokens;
-  int *vis = p.rt_vis + (int64_t)r * p.max_rt;
-  const int warp = tid >> 5, lane = tid & 31;
-  for (int t = warp; t < n_rt; t += 8) {  // positions the widest row of each row tile sees
-    const int i0 = t * p.tokens, i1 = min(n, i0 + p.tokens) - 1;
+  const bool ok = mass_request(a, r, seq, r0, n);
+  if (!ok && tid == 0) record_error(a.status, KVC_ERR_BOUNDS);
+  for (int rg = warp; rg < p.n_rg; rg += 8) {
     int v = 0;
-    for (int i = i0 + lane; i <= i1; i += 32) v = max(v, a.row_vis[r0 + i]);
+    if (ok) {
+      const int64_t i0 = (int64_t)2 * (p.rg0 + rg) * p.tokens;
+      const int i1 = (int)min((int64_t)n, i0 + 2 * p.tokens);
+      for (int64_t i = i0 + lane; i < i1; i += 32) v = max(v, min(a.row_vis[r0 + i], seq));
+    }
     v = __reduce_max_sync(0xFFFFFFFFu, v);
-    if (lane == 0) vis[t] = min(v, seq);
+    if (lane == 0) cum[rg + 1] = (v + kTcKeys - 1) / kTcKeys;
   }
   __syncthreads();
-  const int keys = 2 * kTcKeys, n_kg = (seq + keys - 1) / keys;
-  int64_t *cum = p.cum + (int64_t)r * (p.max_kg + 1);
   int64_t carry = 0;
-  for (int k0 = 0; k0 < n_kg; k0 += 256) {
-    const int kg = k0 + tid;
-    int64_t mine = 0;
-    if (kg < n_kg) {
-      int first = 0, last = n_rt - 1;
-      while (first < n_rt && vis[first] <= kg * keys) first++;
-      while (last >= first && vis[last] <= kg * keys) last--;
-      const int cnt = last - first + 1;
-      p.span[(int64_t)r * p.max_kg + kg] = make_int2(first, cnt);
-      mine = max(cnt, 1);
-    }
+  for (int k0 = 0; k0 < p.n_rg; k0 += 256) {
+    const int rg = k0 + tid;
+    const int64_t mine = rg < p.n_rg ? cum[rg + 1] : 0;
     int64_t x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -1006,67 +965,69 @@ k_mass_plan(MassArgs a, MassTc p) {
       if (w < warp) before += sh[w];
       tot += sh[w];
     }
-    if (kg < n_kg) cum[kg] = before + x - mine;
+    if (rg < p.n_rg) cum[rg + 1] = before + x;
     carry += tot;
     __syncthreads();
   }
-  if (tid == 0) cum[n_kg] = carry;
+  if (tid == 0) cum[0] = 0;
 }
 
-// CTA c: the group that the boundary before run c falls inside, if it is the
-// first boundary inside that group.
+// The row tiles' sums added in order, on top of what is there (the first
+// launch's: the decayed weight).  blockIdx.x: 256 positions, y · z: unit.
 __global__ void __launch_bounds__(256)
 k_mass_join(MassArgs a, MassTc p) {
-  __shared__ int64_t sh[66];
+  const int64_t unit = blockIdx.y + (int64_t)gridDim.y * blockIdx.z;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int tid = threadIdx.x, c = blockIdx.x + 1;
-  int64_t per = 0;
-  for (int r = tid; r < a.n_req; r += 256) per += tc_request_work<false>(a, p, r);
-  per = block_sum(per, sh);
-  const int64_t total = per * a.L * a.H;
-  const int n_cta = (int)min((int64_t)p.n_cta, total);
-  if (c >= n_cta) return;
-  const int64_t t = total * c / n_cta, prev = total * (c - 1) / n_cta;
-  const TcPos<false> x = tc_find<false>(a, p, t, per, sh);
-  if (x.off == 0) return;                 // the run begins with a group
-  const int64_t g0 = t - x.off, g1 = g0 + max(x.cnt, 1);
-  if (prev > g0) return;                  // an earlier boundary joins this group
-  const int key = x.kg * 256 + tid, seq = a.seqused[x.r];
-  if (key >= seq) return;
-  // run c − 1 holds the group's beginning: its first part if it began there
-  float sum = p.part[(2 * (int64_t)(c - 1) + (prev != g0)) * 256 + tid];
-  for (int k = c; k < n_cta && total * k / n_cta < g1; k++) sum += p.part[2 * (int64_t)k * 256 + tid];
-  float *out = a.mass + ((x.l * a.n_req + x.r) * a.H + x.h) * a.cap + key;
-  *out = fmaf(a.decay, key < a.n_mass[x.r] ? *out : 0.f, sum);
+  if (unit >= (int64_t)a.L * a.n_req * a.H) return;
+  const int r = (int)(unit / a.H % a.n_req), key = blockIdx.x * 256 + threadIdx.x;
+  int seq, r0, n;
+  if (!mass_request(a, r, seq, r0, n) || key >= seq) return;
+  const int64_t *cum = p.cum + (int64_t)r * (p.n_rg + 1);
+  const float *part = p.part + unit * 2 * p.n_rg * a.cap + key;
+  float sum = 0.f;
+  int64_t before = cum[0];
+#pragma unroll 4
+  for (int rg = 0; rg < p.n_rg; rg++) {
+    const int64_t next = cum[rg + 1];
+    if (key < (next - before) * kTcKeys) {
+      const float *x = part + (int64_t)2 * rg * a.cap;
+      sum += x[0] + x[a.cap];
+    }
+    before = next;
+  }
+  float *out = a.mass + unit * a.cap + key;
+  if (p.rg0 == 0) *out = fmaf(a.decay, key < a.n_mass[r] ? *out : 0.f, sum);
+  else *out += sum;
 }
 
-// The shape of the tensor-core path for these sizes.
-MassTc tc_plan(int n_req, int cap, int max_rows, int G, int D, bool &one, size_t &smem, size_t &ws,
-               uint8_t *base) {
+// The shape of the tensor-core path for these sizes; n_rg pairs of row tiles a
+// launch when they do not fit one tile.
+MassTc tc_plan(int n_req, int cap, int max_rows, int L, int H, int G, int D, int &pairs,
+               size_t &smem, size_t &ws, uint8_t *base) {
   MassTc p{};
   const int64_t R = (int64_t)max_rows * G;
-  one = R <= 256;
+  const bool one = R <= 256;
   p.NR = R <= 128 ? 128 : 256;
   p.tokens = std::min(max_rows, p.NR / G);
-  // what the row tiles leave: K tiles in flight when keys stream, else two
-  const size_t tile = (size_t)kTcKeys * D * 2, q = (size_t)kTcQs * p.NR * 128;
-  p.k_slots = one ? (int)std::min<size_t>(kTcMaxK, (200 * 1024 - q) / tile) & ~1 : 2;  // even: a slot keeps its MMA warp
+  // K tiles in flight: what the two row tiles leave.  Even for RT 1, so that a
+  // slot's tiles are all one MMA warp's.
+  const size_t most = 232448;
+  p.k_slots = kTcMaxK;
+  while (p.k_slots > 2 && (TcSmem(D, p.NR, p.k_slots).bytes > most || (one && (p.k_slots & 1))))
+    p.k_slots--;
   p.n_cta = device_sm_count();
-  p.max_kg = (cap + 255) / 256;
-  p.max_rt = (max_rows + p.tokens - 1) / p.tokens;
   p.idesc = make_idesc(128, p.NR);
-  smem = 1024 + TcSmem(D, p.NR, p.k_slots, one ? 2 : 4).bytes;
+  smem = TcSmem(D, p.NR, p.k_slots).bytes;
   ws = 0;
+  pairs = 0;
   if (one) return p;
-  auto take = [&](size_t n) {
-    const size_t x = ws;
-    ws += (n + 15) & ~size_t(15);
-    return base + x;
-  };
-  p.cum = reinterpret_cast<int64_t *>(take((size_t)n_req * (p.max_kg + 1) * 8));
-  p.span = reinterpret_cast<int2 *>(take((size_t)n_req * p.max_kg * 8));
-  p.rt_vis = reinterpret_cast<int *>(take((size_t)n_req * p.max_rt * 4));
-  p.part = reinterpret_cast<float *>(take((size_t)2 * p.n_cta * 256 * 4));
+  pairs = (int)(((int64_t)max_rows + 2 * p.tokens - 1) / (2 * p.tokens));
+  const size_t per = (size_t)L * n_req * H * 2 * cap * sizeof(float);
+  p.n_rg = (int)std::min<size_t>(pairs, std::max<size_t>(8, kTcPartBytes / per));
+  p.cum = reinterpret_cast<int64_t *>(base);
+  ws = ((size_t)n_req * (p.n_rg + 1) * 8 + 15) & ~size_t(15);
+  p.part = reinterpret_cast<float *>(base + ws);
+  ws += per * p.n_rg;
   return p;
 }
 
@@ -1088,15 +1049,15 @@ cudaError_t launch_dependent(K kern, dim3 grid, int threads, size_t smem, cudaSt
 
 template <int D>
 cudaError_t launch_tc(const MassArgs &a, void *ws, cudaStream_t s) {
-  bool one;
+  int pairs;
   size_t smem, ws_bytes;
-  MassTc p = tc_plan(a.n_req, a.cap, a.max_rows, a.G, D, one, smem, ws_bytes,
-                           reinterpret_cast<uint8_t *>(ws));
-  auto *kern = one ? k_mass_tc<D, true> : k_mass_tc<D, false>;
+  MassTc p = tc_plan(a.n_req, a.cap, a.max_rows, a.L, a.H, a.G, D, pairs, smem, ws_bytes,
+                     reinterpret_cast<uint8_t *>(ws));
+  auto *kern = pairs == 0 ? k_mass_tc<D, 1> : k_mass_tc<D, 2>;
   CUtensorMap tm_k{}, tm_q{};
   p.box = a.BS % 32 == 0 ? 32 : a.BS % 16 == 0 ? 16 : a.BS % 8 == 0 ? 8 : 0;
   if ((int64_t)a.L * a.n_slots > INT32_MAX) p.box = 0;  // (a map coordinate is an int32)
-  p.q_box = !a.row_idx && (int64_t)a.L * a.n_q + a.n_rows <= INT32_MAX;
+  p.q_box = !a.row_idx && (int64_t)a.L * a.n_q + a.n_rows + 2 * p.tokens <= INT32_MAX;
   if (p.box && !pool_map(&tm_k, a.kpool, (int64_t)a.L * a.n_slots, a.H, D, p.box))
     return cudaErrorUnknown;
   if (p.q_box && !q_map(&tm_q, a.q, (int64_t)a.L * a.n_q, a.Hq, D, a.G, p.tokens))
@@ -1104,26 +1065,33 @@ cudaError_t launch_tc(const MassArgs &a, void *ws, cudaStream_t s) {
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  if (one) {
+  if (pairs == 0) {
     kern<<<p.n_cta, kTcThreads, smem, s>>>(tm_k, tm_q, a, p);
     return cudaGetLastError();
   }
-  k_mass_plan<<<a.n_req, 256, 0, s>>>(a, p);
-  e = cudaGetLastError();
-  if (e == cudaSuccess) e = launch_dependent(kern, dim3(p.n_cta), kTcThreads, smem, s, tm_k, tm_q, a, p);
-  if (e == cudaSuccess && p.n_cta > 1)
-    e = launch_dependent(k_mass_join, dim3(p.n_cta - 1), 256, 0, s, a, p);
+  const int64_t units = (int64_t)a.L * a.n_req * a.H;
+  const int y = (int)std::min<int64_t>(units, 32768);
+  for (p.rg0 = 0; p.rg0 < pairs && e == cudaSuccess; p.rg0 += p.n_rg) {
+    k_mass_plan<<<a.n_req, 256, 0, s>>>(a, p);
+    e = cudaGetLastError();
+    if (e == cudaSuccess)
+      e = launch_dependent(kern, dim3(p.n_cta), kTcThreads, smem, s, tm_k, tm_q, a, p);
+    if (e == cudaSuccess)
+      e = launch_dependent(k_mass_join,
+                           dim3((a.cap + 255) / 256, y, (unsigned)((units + y - 1) / y)), 256, 0, s,
+                           a, p);
+  }
   return e;
 }
 
 }  // namespace
 
-size_t attn_mass_ws_bytes(int n_req, int max_blocks, int max_rows, int, int H, int Hq, int D,
+size_t attn_mass_ws_bytes(int n_req, int max_blocks, int max_rows, int L, int H, int Hq, int D,
                           int BS) {
   if ((int64_t)max_rows * (Hq / H) <= kMrMaxRows) return 0;
-  bool one;
+  int pairs;
   size_t smem, ws;
-  tc_plan(n_req, max_blocks * BS, max_rows, Hq / H, D, one, smem, ws, nullptr);
+  tc_plan(n_req, max_blocks * BS, max_rows, L, H, Hq / H, D, pairs, smem, ws, nullptr);
   return ws;
 }
 

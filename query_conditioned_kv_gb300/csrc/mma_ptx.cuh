@@ -98,6 +98,17 @@ __device__ __forceinline__ void tmem_frag8(uint32_t taddr, uint32_t (&r)[32]) {
       : "r"(taddr));
 }
 
+// The same with 32 columns.
+__device__ __forceinline__ void tmem_frag4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
 // Boxes of `box` consecutive slots of one head, 64 columns, 128-byte swizzle.
 inline bool pool_map(CUtensorMap *m, const void *pool, int64_t n_slots, int H, int D, int box) {
   auto fn = tc::encode_fn();
