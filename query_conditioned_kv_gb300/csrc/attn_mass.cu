@@ -322,9 +322,10 @@ cudaError_t launch_rows(const MassArgs &a, cudaStream_t s) {
 //
 // tcgen05: D[key][row] = K tile (M 128 keys, A) × row tile (N rows, B), fp32 in
 // tensor memory.  The rows stay in shared memory while the keys stream past.
-// Warps 0–15: two epilogue groups of eight; 16–19: producers; 20–21: an MMA
-// warp for each epilogue group (a warp's waits run under the other's products);
-// 22: the rows' TMA boxes.  An epilogue thread owns two keys and a quarter of
+// Warps 0–15: two epilogue groups of eight; 16–19: producers; then the
+// products' issuers (RT = 1: a warp for each group, so that a warp's waits run
+// under the other's products; RT = 2: one, in order, as two warps' products
+// would interleave and both end late) and a warp for the rows' TMA boxes.  An epilogue thread owns two keys and a quarter of
 // the rows (16x256b fragments): the rows' LSE, stored in that order, costs it
 // half of the shared-memory reads that one key a thread would.
 //
@@ -341,7 +342,7 @@ cudaError_t launch_rows(const MassArgs &a, cudaStream_t s) {
 
 constexpr int kTcEpi = 16;                      // epilogue warps, half for each accumulator
 constexpr int kTcProd = 4;                      // producer warps
-constexpr int kTcThreads = (kTcEpi + kTcProd + 4) * 32;  // (the last warp idles)
+constexpr int kTcThreads = (kTcEpi + kTcProd + 4) * 32;  // (the last warps idle)
 // Registers a thread after setmaxnreg: what the launch holds, 768 · 80, split
 // 512 · 88 + 256 · 64.
 constexpr int kTcMore = 88, kTcLess = 64;
@@ -359,7 +360,8 @@ struct MassTc {
   int rg0, n_rg;    // RT 2: this launch's pairs of row tiles, [rg0, rg0 + n_rg)
   uint32_t idesc;
   int64_t *cum;     // [n_req][n_rg + 1]: key tiles before each pair
-  float *part;      // [L·n_req·H][2·n_rg][cap]: each row tile's sums
+  int64_t cap4;     // cap rounded up to whole float4
+  float *part;      // [L·n_req·H][2·n_rg][cap4]: each row tile's sums
 };
 
 // Head of the dynamic shared memory (fixed offsets), behind K and q; then the
@@ -469,6 +471,7 @@ k_mass_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
           MassArgs a, MassTc p) {
   constexpr int CH = D / 8, KB = D / 64;
   constexpr uint32_t kSlot = kTcKeys * D * 2;
+  constexpr int kMma = RT == 1 ? 2 : 1;  // MMA warps
   extern __shared__ __align__(1024) uint8_t base[];
   const int NR = p.NR, KS = p.k_slots, NACC = 512 / NR;
   const TcSmem at(D, NR, KS);
@@ -481,13 +484,13 @@ k_mass_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
     sm.failed = 0;
     for (int i = 0; i < KS; i++) {
       mbar_init(smem_u32(sm.kfull + i), kTcProd * 32);
-      mbar_init(smem_u32(sm.kempty + i), RT);
+      mbar_init(smem_u32(sm.kempty + i), 1);
     }
     for (int i = 0; i < 2; i++) {
       // RT 1: both MMA warps and both epilogue groups use a unit's rows;
       // RT 2: slot i is group i's
       mbar_init(smem_u32(sm.qfull + i), p.q_box ? 1 : kTcProd * 32);
-      mbar_init(smem_u32(sm.qempty + i), RT == 1 ? 2 : 1);
+      mbar_init(smem_u32(sm.qempty + i), kMma);
       mbar_init(smem_u32(sm.lfull + i), kTcProd * 32);
       mbar_init(smem_u32(sm.lempty + i), RT == 1 ? kTcEpi : kTcEpi / 2);
     }
@@ -697,7 +700,7 @@ k_mass_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
     if (!ok) sm.failed = 1;
   } else if (warp >= kTcEpi + kTcProd) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTcLess));
-    if (warp == kTcEpi + kTcProd + 2) {
+    if (warp == kTcEpi + kTcProd + kMma) {
       // ----------------------------------------------- rows by TMA boxes
       if (p.q_box && lane == 0)
         for (int64_t g = run0; g < run1 && ok; g++) {
@@ -719,43 +722,49 @@ k_mass_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
         }
       if (!ok) sm.failed = 1;
       __syncwarp();
-    } else if (warp < kTcEpi + kTcProd + 2) {
+    } else if (warp < kTcEpi + kTcProd + kMma) {
       // ----------------------------------------------------- MMA issuers
       // (the whole warp runs the loop; one lane's products are enabled)
-      const int wg = warp - kTcEpi - kTcProd;  // the epilogue group it works for
+      const uint32_t wg = warp - kTcEpi - kTcProd;  // RT 1: the group it works for
       const uint32_t lead = lane == 0;
-      uint32_t kc = 0, jc = 0;  // K tiles, this group's products
-      uint64_t qd = 0;
+      uint32_t kc = 0;  // K tiles
+      uint64_t qd[2] = {0, 0};
       for (int64_t g = run0; g < run1 && ok; g++, kc++) {
         if (g == run0 || pos.t == 0) {
-          if (RT == 1 && uc > 0) mma_commit_if(lead, smem_u32(sm.qempty + ((uc - 1) & 1)));
-          const uint32_t s = RT == 1 ? uc & 1 : wg, use = RT == 1 ? uc >> 1 : uc;
-          // (RT 1: also for a unit without a tile of this warp's: a barrier's parity
-          // tells only two uses apart)
-          if (!(ok = mbar_wait_bounded(smem_u32(sm.qfull + s), use & 1, &sm.failed))) break;
-          qd = uniform64(smem_desc(base_u + at.q + s * (NR * D * 2)));
+          if (uc > 0) {
+#pragma unroll
+            for (int j = 0; j < RT; j++)
+              mma_commit_if(lead, smem_u32(sm.qempty + (RT == 1 ? (uc - 1) & 1 : j)));
+          }
           uc++;
         }
-        const bool last = g + 1 == run1 || pos.t + 1 == pos.n_t;  // of the unit, in this run
-        if (RT == 2 || (kc & 1) == (uint32_t)wg) {
-          const uint32_t st = kc % KS, acc = RT == 2 ? wg : kc % NACC;
-          // acc's products: RT 2 every one of the warp's, RT 1 every NACC-th tile
-          const uint32_t use = RT == 2 ? jc : kc / NACC;
-          ok = mbar_wait_bounded(smem_u32(sm.kfull + st), (kc / KS) & 1, &sm.failed);
+        const uint32_t st = kc % KS;
+        const uint64_t kd = uniform64(smem_desc(base_u + st * kSlot));
+        const bool mine = RT == 2 || (kc & 1) == wg;
+#pragma unroll
+        for (int j = 0; j < RT; j++) {
+          // (RT 1: also for a unit without a tile of this warp's: a barrier's parity
+          // tells only two uses apart)
+          if (g == run0 || pos.t == 0) {
+            const uint32_t s = RT == 1 ? (uc - 1) & 1 : j, use = RT == 1 ? (uc - 1) >> 1 : uc - 1;
+            if (!(ok = mbar_wait_bounded(smem_u32(sm.qfull + s), use & 1, &sm.failed))) break;
+            qd[j] = uniform64(smem_desc(base_u + at.q + s * (NR * D * 2)));
+          }
+          const uint32_t acc = RT == 2 ? j : kc % NACC, use = RT == 2 ? kc : kc / NACC;
+          if (!mine) break;
+          if (j == 0) ok = mbar_wait_bounded(smem_u32(sm.kfull + st), (kc / KS) & 1, &sm.failed);
           if (ok) ok = mbar_wait_bounded(smem_u32(sm.tempty + acc), (use & 1) ^ 1, &sm.failed);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t kd = uniform64(smem_desc(base_u + st * kSlot));
           const uint32_t dst = uniform32(tmem + acc * NR), qk = uniform32(NR * 8);
-  #pragma unroll
+#pragma unroll
           for (int kk = 0; kk < 4 * KB; kk++)
             mma_bf16_if(lead, dst, kd + (kk >> 2) * (kTcKeys * 8) + (kk & 3) * 2,
-                        qd + (kk >> 2) * qk + (kk & 3) * 2, p.idesc, kk > 0);
+                        qd[j] + (kk >> 2) * qk + (kk & 3) * 2, p.idesc, kk > 0);
           mma_commit_if(lead, smem_u32(sm.tfull + acc));
-          mma_commit_if(lead, smem_u32(sm.kempty + st));
-          if (RT == 2 && last) mma_commit_if(lead, smem_u32(sm.qempty + wg));
-          jc++;
         }
+        if (!ok) break;
+        if (mine) mma_commit_if(lead, smem_u32(sm.kempty + st));
         if (g + 1 < run1) pos.next(a, p);
       }
       if (!ok) sm.failed = 1;
@@ -767,13 +776,14 @@ k_mass_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
     const int wg = warp >> 3, quarter = warp & 3, half = (warp >> 2) & 1;
     const int key0 = quarter * 32 + half * 16;  // the warp's 16 keys of a tile
     const uint32_t lane_base = (uint32_t)key0 << 16;
+    const int my_key = key0 + lane / 4 + 8 * (lane & 1);  // the one this lane writes (lane & 2: none)
     const uint64_t zs2 = pk2(a.zscale, a.zscale);
     uint32_t kc = 0, jc = 0;
     int lo = 0;
     const float *nl = nlse;  // the slot's LSE
     const int nl_q = (lane & 3) * (NR / 4 + 4);
     const int64_t n_blocks = a.n_slots / a.BS;
-    // lanes 0–15's key: its sum's place, its block id and its weight so far, the
+    // the lane's key: its sum's place, its block id and its weight so far, the
     // last two fetched a tile of the group ahead
     constexpr int kStep = RT == 1 ? 2 * kTcKeys : kTcKeys;
     int seq = 0, n_old = 0;
@@ -786,7 +796,7 @@ k_mass_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
     };
     for (int64_t g = run0; g < run1 && ok; g++, kc++) {
       const bool mine = RT == 2 || (kc & 1) == (uint32_t)wg;
-      const int p0 = pos.t * kTcKeys, key = p0 + key0 + (lane & 15);
+      const int p0 = pos.t * kTcKeys, key = p0 + my_key;
       if (g == run0 || pos.t == 0) {
         __syncwarp();
         if (uc > 0 && lane == 0) mbar_arrive(smem_u32(sm.lempty + (RT == 1 ? (uc - 1) & 1 : wg)));
@@ -794,7 +804,7 @@ k_mass_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
         seq = a.seqused[pos.r];
         bt = a.block_table + (int64_t)pos.r * a.max_blocks;
         if (RT == 1) n_old = min(seq, a.n_mass[pos.r]);
-        out0 = RT == 1 ? a.mass + u * a.cap : p.part + (u * 2 * p.n_rg + 2 * pos.rg + wg) * a.cap;
+        out0 = RT == 1 ? a.mass + u * a.cap : p.part + (u * 2 * p.n_rg + 2 * pos.rg + wg) * p.cap4;
         fetch(mine ? key : key + kTcKeys);
         const uint32_t s = RT == 1 ? uc & 1 : wg, use = RT == 1 ? uc >> 1 : uc;
         ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.lfull + s), use & 1, &sm.failed));
@@ -876,20 +886,21 @@ k_mass_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(sm.tempty + acc));
-        // the four lanes of a key, then lanes 0–15 each their own key
-        float sum = 0.f;
-#pragma unroll
-        for (int k = 0; k < 2; k++) {
-          float x, y;
-          upk2(s2[k], x, y);
-          x += y;
-          x += __shfl_xor_sync(0xFFFFFFFFu, x, 1);
-          x += __shfl_xor_sync(0xFFFFFFFFu, x, 2);
-          x = __shfl_sync(0xFFFFFFFFu, x, (lane & 7) << 2);
-          if (((lane >> 3) & 1) == k) sum = x;
+        // the four lanes of two keys: each pair of lanes keeps one key
+        float x, y, sum, away;
+        upk2(s2[0], x, y);
+        sum = x + y;
+        upk2(s2[1], x, y);
+        away = x + y;
+        if (lane & 1) {
+          const float h = sum;
+          sum = away;
+          away = h;
         }
+        sum += __shfl_xor_sync(0xFFFFFFFFu, away, 1);
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
         if (blk < 0 || blk >= n_blocks) sum = 0.f;
-        if (key < seq && lane < 16) out0[key] = RT == 1 ? fmaf(a.decay, old, sum) : sum;
+        if (key < seq && !(lane & 2)) out0[key] = RT == 1 ? fmaf(a.decay, old, sum) : sum;
         jc++;
       }
       if (g + 1 < run1) pos.next(a, p);
@@ -937,6 +948,7 @@ k_mass_plan(MassArgs a, MassTc p) {
   int seq, r0, n;
   const bool ok = mass_request(a, r, seq, r0, n);
   if (!ok && tid == 0) record_error(a.status, KVC_ERR_BOUNDS);
+#pragma unroll 4
   for (int rg = warp; rg < p.n_rg; rg += 8) {
     int v = 0;
     if (ok) {
@@ -972,32 +984,45 @@ k_mass_plan(MassArgs a, MassTc p) {
   if (tid == 0) cum[0] = 0;
 }
 
-// The row tiles' sums added in order, on top of what is there (the first
-// launch's: the decayed weight).  blockIdx.x: 256 positions, y · z: unit.
+// The row tiles' sums added up, on top of what is there (the first launch's: the
+// decayed weight): warp w takes the pairs w, w + 8, …, then the warps' sums are
+// added in order.  blockIdx.x: a key tile, y · z: unit.
 __global__ void __launch_bounds__(256)
 k_mass_join(MassArgs a, MassTc p) {
+  static_assert(kTcKeys == 128, "a float4 a lane");
+  __shared__ float4 sh[8][32];
   const int64_t unit = blockIdx.y + (int64_t)gridDim.y * blockIdx.z;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = blockIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (unit >= (int64_t)a.L * a.n_req * a.H) return;
-  const int r = (int)(unit / a.H % a.n_req), key = blockIdx.x * 256 + threadIdx.x;
+  const int r = (int)(unit / a.H % a.n_req);
   int seq, r0, n;
-  if (!mass_request(a, r, seq, r0, n) || key >= seq) return;
+  if (!mass_request(a, r, seq, r0, n) || t * kTcKeys >= seq) return;
   const int64_t *cum = p.cum + (int64_t)r * (p.n_rg + 1);
-  const float *part = p.part + unit * 2 * p.n_rg * a.cap + key;
-  float sum = 0.f;
-  int64_t before = cum[0];
+  const float *part = p.part + unit * 2 * p.n_rg * p.cap4 + t * kTcKeys + 4 * lane;
+  const bool in = t * kTcKeys + 4 * lane < p.cap4;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int rg = 0; rg < p.n_rg; rg++) {
-    const int64_t next = cum[rg + 1];
-    if (key < (next - before) * kTcKeys) {
-      const float *x = part + (int64_t)2 * rg * a.cap;
-      sum += x[0] + x[a.cap];
+  for (int rg = warp; rg < p.n_rg; rg += 8)
+    if (in && t < (int)(cum[rg + 1] - cum[rg])) {
+      const float *x = part + (int64_t)2 * rg * p.cap4;
+      const float4 u = *reinterpret_cast<const float4 *>(x);
+      const float4 v = *reinterpret_cast<const float4 *>(x + p.cap4);
+      sum.x += u.x + v.x;
+      sum.y += u.y + v.y;
+      sum.z += u.z + v.z;
+      sum.w += u.w + v.w;
     }
-    before = next;
-  }
+  sh[warp][lane] = sum;
+  __syncthreads();
+  const int key = t * kTcKeys + threadIdx.x;
+  if (threadIdx.x >= kTcKeys || key >= seq) return;
+  float s = 0.f;
+#pragma unroll
+  for (int w = 0; w < 8; w++) s += reinterpret_cast<const float *>(sh[w])[threadIdx.x];
   float *out = a.mass + unit * a.cap + key;
-  if (p.rg0 == 0) *out = fmaf(a.decay, key < a.n_mass[r] ? *out : 0.f, sum);
-  else *out += sum;
+  if (p.rg0 == 0) *out = fmaf(a.decay, key < a.n_mass[r] ? *out : 0.f, s);
+  else *out += s;
 }
 
 // The shape of the tensor-core path for these sizes; n_rg pairs of row tiles a
@@ -1022,7 +1047,8 @@ MassTc tc_plan(int n_req, int cap, int max_rows, int L, int H, int G, int D, int
   pairs = 0;
   if (one) return p;
   pairs = (int)(((int64_t)max_rows + 2 * p.tokens - 1) / (2 * p.tokens));
-  const size_t per = (size_t)L * n_req * H * 2 * cap * sizeof(float);
+  p.cap4 = ((int64_t)cap + 3) & ~(int64_t)3;
+  const size_t per = (size_t)L * n_req * H * 2 * p.cap4 * sizeof(float);
   p.n_rg = (int)std::min<size_t>(pairs, std::max<size_t>(8, kTcPartBytes / per));
   p.cum = reinterpret_cast<int64_t *>(base);
   ws = ((size_t)n_req * (p.n_rg + 1) * 8 + 15) & ~size_t(15);
@@ -1078,7 +1104,7 @@ cudaError_t launch_tc(const MassArgs &a, void *ws, cudaStream_t s) {
       e = launch_dependent(kern, dim3(p.n_cta), kTcThreads, smem, s, tm_k, tm_q, a, p);
     if (e == cudaSuccess)
       e = launch_dependent(k_mass_join,
-                           dim3((a.cap + 255) / 256, y, (unsigned)((units + y - 1) / y)), 256, 0, s,
+                           dim3((a.cap + kTcKeys - 1) / kTcKeys, y, (unsigned)((units + y - 1) / y)), 256, 0, s,
                            a, p);
   }
   return e;
