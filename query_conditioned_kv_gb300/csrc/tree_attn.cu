@@ -58,6 +58,7 @@ struct TreeArgs {
   int n_cta;     // CTAs the tiles are dealt out to
   uint32_t bs_inv;  // ⌈2^32 / BS⌉ (0: BS = 1)
   float zscale;  // scale·log2(e)
+  int join_rows;  // rows of a join CTA
 };
 
 // Request r's sizes; false when they are out of range.
@@ -79,15 +80,17 @@ __device__ __forceinline__ void tree_tiles(const TreeArgs &a, int r, int &n_rt, 
   n_kt = (c + T + a.tile - 1) / a.tile;
 }
 
-__device__ __forceinline__ int64_t run_start(int64_t total, int n_cta, int cta) {
-  return total * cta / n_cta;
+// How `total` tiles are dealt out: CTA c begins at ⌊total·c / n_cta⌋.
+__device__ __forceinline__ int64_t run_div(int64_t x, int64_t y) {
+  // (64-bit division is a long call: most sizes fit 32 bits)
+  return x >> 32 || y >> 32 ? x / y : (uint32_t)x / (uint32_t)y;
 }
-// The CTA whose run holds tile t.
+__device__ __forceinline__ int64_t run_start(int64_t total, int n_cta, int cta) {
+  return run_div(total * cta, n_cta);
+}
+// The CTA whose run holds tile t: the last c with total·c < (t + 1)·n_cta.
 __device__ __forceinline__ int run_owner(int64_t total, int n_cta, int64_t t) {
-  int c = (int)(t * n_cta / total);
-  while (c + 1 < n_cta && run_start(total, n_cta, c + 1) <= t) c++;
-  while (c > 0 && run_start(total, n_cta, c) > t) c--;
-  return c;
+  return (int)run_div((t + 1) * n_cta - 1, total);
 }
 
 // Tiles of request r, all heads.
@@ -1278,22 +1281,39 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
 
 // Joins the partials of one (request, KV head, row tile) that was split over
 // CTAs: blockIdx.x = (request, KV head), blockIdx.y = row tile, blockIdx.z a
-// group of four rows.
-template <int D>
+// group of rows.  W warps share a row's partials (W 4: warp w takes the parts w,
+// w + 4, …, all in flight at once; their results are added in order), or each
+// takes join_rows / 4 rows of its own (W 1).  Bound by latency, so the fewest
+// dependent loads: sizes, then maxima and sums, then O.
+template <int D, int W>
 __global__ void __launch_bounds__(128)
 k_tree_join(TreeArgs a) {
-  __shared__ int64_t sh[66];
+  constexpr int E = D / 32;
+  __shared__ float sh_o[W][D];
+  __shared__ float2 sh_ml[W];
   const int r = blockIdx.x / a.H, h = blockIdx.x % a.H, rt = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int64_t before = 0, total = 0;
-  for (int x = threadIdx.x; x < a.n_req; x += blockDim.x) {
-    const int64_t n = request_tiles(a, x);
+  int n_rt = 0, n_kt = 0;
+#pragma unroll 2
+  for (int x0 = 0; x0 < a.n_req; x0 += 32) {  // (every warp for itself)
+    const int x = x0 + lane;
+    int rt_x = 0, kt_x = 0;
+    if (x < a.n_req) tree_tiles(a, x, rt_x, kt_x);
+    const int64_t n = (int64_t)a.H * rt_x * kt_x;
     total += n;
     if (x < r) before += n;
+    if (x0 <= r && r < x0 + 32) {
+      n_rt = __shfl_sync(0xFFFFFFFFu, rt_x, r - x0);
+      n_kt = __shfl_sync(0xFFFFFFFFu, kt_x, r - x0);
+    }
   }
-  before = block_sum(before, sh);
-  total = block_sum(total, sh);
-  int n_rt, n_kt;
-  tree_tiles(a, r, n_rt, n_kt);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
+    total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+  }
+  const int q0 = a.q_off[r], T = a.q_off[r + 1] - q0;
   // in every CTA: the grid may not end before the kernel whose partials it joins
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (rt >= n_rt) return;
@@ -1301,44 +1321,77 @@ k_tree_join(TreeArgs a) {
   const int n_cta = (int)min((int64_t)a.n_cta, total);
   const int c0 = run_owner(total, n_cta, g0), c1 = run_owner(total, n_cta, g0 + n_kt - 1);
   if (c0 == c1) return;  // written whole
-  int c, q0, T;
-  tree_request(a, r, c, q0, T);
-  const int row = blockIdx.z * 4 + threadIdx.x / 32, x = rt * a.rstep + row;
-  if (row >= a.rstep || x >= T * a.G) return;
   const int64_t first = 2 * (int64_t)c0 + (run_start(total, n_cta, c0) != g0);
   const int n_part = c1 - c0 + 1;
-  // part i is slot first (i = 0) or 2·(c0 + i): later CTAs begin inside the unit
-  float mx = -INFINITY;
-  for (int i = threadIdx.x & 31; i < n_part; i += 32)
-    mx = fmaxf(mx, a.part_ml[(i == 0 ? first : 2 * (int64_t)(c0 + i)) * a.rows + row].x);
+  const int n_rows = min(a.rstep, T * a.G - rt * a.rstep), d0 = lane * E;
+  const int row0 = W == 1 ? blockIdx.z * a.join_rows + warp : blockIdx.z;
+  const int row1 = W == 1 ? min(n_rows, (int)(blockIdx.z + 1) * a.join_rows) : min(n_rows, row0 + 1);
+  for (int row = row0; row < row1; row += 4) {
+    float mx = -INFINITY, sum = 0.f, acc[E];
 #pragma unroll
-  for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-  const float base = mx == -INFINITY ? 0.f : mx;
-  constexpr int E = D / 32;
-  float acc[E], sum = 0.f;
+    for (int e = 0; e < E; e++) acc[e] = 0.f;
+    for (int i0 = W == 1 ? 0 : warp; i0 < n_part; i0 += 32 * W) {
+      // part i is slot first (i = 0) or 2·(c0 + i): later CTAs begin inside the unit
+      const int mine = i0 + W * lane;
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (mine < n_part)
+        ml = a.part_ml[(mine == 0 ? first : 2 * (int64_t)(c0 + mine)) * a.rows + row];
+      float m = ml.x;
 #pragma unroll
-  for (int e = 0; e < E; e++) acc[e] = 0.f;
-  const int d0 = (threadIdx.x & 31) * E;
-#pragma unroll 4
-  for (int i = 0; i < n_part; i++) {
-    const int64_t at = (i == 0 ? first : 2 * (int64_t)(c0 + i)) * a.rows + row;
-    const float2 ml = a.part_ml[at];
-    const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - base);
-    sum = fmaf(ml.y, f, sum);
-    float v[E];
-    if constexpr (E == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(a.part_o + at * D + d0);
-    else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(a.part_o + at * D + d0);
+      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+      const float now = fmaxf(mx, m), base = now == -INFINITY ? 0.f : now;
+      const float keep = mx == -INFINITY ? 0.f : ex2(mx - base);
+      const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - base);
+      float s = ml.y * f;
 #pragma unroll
-    for (int e = 0; e < E; e++) acc[e] = fmaf(v[e], f, acc[e]);
+      for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+      sum = fmaf(sum, keep, s);
+#pragma unroll
+      for (int e = 0; e < E; e++) acc[e] *= keep;
+      mx = now;
+      const int n = min(32, (n_part - i0 + W - 1) / W);
+#pragma unroll 8
+      for (int k = 0; k < n; k++) {
+        const int i = i0 + W * k;
+        const float *o = a.part_o + ((i == 0 ? first : 2 * (int64_t)(c0 + i)) * a.rows + row) * D + d0;
+        const float fk = __shfl_sync(0xFFFFFFFFu, f, k);
+        float v[E];
+        if constexpr (E == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(o);
+        else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(o);
+#pragma unroll
+        for (int e = 0; e < E; e++) acc[e] = fmaf(v[e], fk, acc[e]);
+      }
+    }
+    if constexpr (W > 1) {
+#pragma unroll
+      for (int e = 0; e < E; e++) sh_o[warp][d0 + e] = acc[e];
+      if (lane == 0) sh_ml[warp] = make_float2(mx, sum);
+      __syncthreads();
+      if (warp != 0) return;
+      mx = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < W; w++) mx = fmaxf(mx, sh_ml[w].x);
+      sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; e++) acc[e] = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; w++) {
+        const float f = sh_ml[w].x == -INFINITY ? 0.f : ex2(sh_ml[w].x - mx);
+        sum = fmaf(sh_ml[w].y, f, sum);
+#pragma unroll
+        for (int e = 0; e < E; e++) acc[e] = fmaf(sh_o[w][d0 + e], f, acc[e]);
+      }
+    }
+    const float inv = mx == -INFINITY ? 0.f : 1.f / sum;
+    const int x = rt * a.rstep + row;
+    const int64_t qr = (int64_t)(q0 + x / a.G) * a.Hq + h * a.G + x % a.G;
+    uint32_t w[E / 2];
+#pragma unroll
+    for (int e = 0; e < E / 2; e++) w[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    if constexpr (E == 4) *reinterpret_cast<uint2 *>(a.out + qr * D + d0) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t *>(a.out + qr * D + d0) = w[0];
+    if (d0 == 0) a.lse[qr] = mx == -INFINITY ? -INFINITY : (mx + log2f(sum)) * kLn2;
   }
-  const float inv = mx == -INFINITY ? 0.f : 1.f / sum;
-  const int64_t qr = (int64_t)(q0 + x / a.G) * a.Hq + h * a.G + x % a.G;
-  uint32_t w[E / 2];
-#pragma unroll
-  for (int e = 0; e < E / 2; e++) w[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-  if constexpr (E == 4) *reinterpret_cast<uint2 *>(a.out + qr * D + d0) = make_uint2(w[0], w[1]);
-  else *reinterpret_cast<uint32_t *>(a.out + qr * D + d0) = w[0];
-  if (d0 == 0) a.lse[qr] = mx == -INFINITY ? -INFINITY : (mx + log2f(sum)) * kLn2;
 }
 
 // Rows up to which the narrow instruction is used.
@@ -1448,8 +1501,18 @@ cudaError_t launch_tree_attn(const uint16_t *q, const uint16_t *kpool, const uin
     e = D == 128 ? (a.rows == 16 ? launch_rows<128, 1>(a, s) : launch_rows<128, 2>(a, s))
                  : (a.rows == 16 ? launch_rows<64, 1>(a, s) : launch_rows<64, 2>(a, s));
   if (e != cudaSuccess) return e;
+  // four warps a row where a unit is cut into many parts
+  const bool many = a.n_cta >= 6 * (int64_t)n_req * H * max_rt;
+  auto *join = D == 128 ? (many ? k_tree_join<128, 4> : k_tree_join<128, 1>)
+                        : (many ? k_tree_join<64, 4> : k_tree_join<64, 1>);
+  // as many CTAs as the GPU holds at once, so that no warp's rows wait for one another
+  a.join_rows = many ? 1 : 4;
+  while (!many && a.join_rows < a.rstep &&
+         (int64_t)n_req * H * max_rt * a.rstep > (int64_t)a.join_rows * 16 * device_sm_count())
+    a.join_rows *= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)n_req * H), (unsigned)max_rt, (unsigned)(a.rows / 4));
+  cfg.gridDim = dim3((unsigned)((int64_t)n_req * H), (unsigned)max_rt,
+                     (unsigned)((a.rstep + a.join_rows - 1) / a.join_rows));
   cfg.blockDim = dim3(128);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -1457,8 +1520,7 @@ cudaError_t launch_tree_attn(const uint16_t *q, const uint16_t *kpool, const uin
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return D == 128 ? cudaLaunchKernelEx(&cfg, k_tree_join<128>, a)
-                  : cudaLaunchKernelEx(&cfg, k_tree_join<64>, a);
+  return cudaLaunchKernelEx(&cfg, join, a);
 }
 
 }  // namespace kvc
