@@ -15,18 +15,23 @@
 // selects by itself (the weights come from L2 after the first reader), rank 0
 // writes the weights and positions, and the row copies are split over the
 // ranks, so a few segments still use the whole GPU.  The cluster barrier
-// before the first write lets mass_out/pos_out be mass/pos.
+// before a leaving row's weight is overwritten lets mass_out/pos_out be
+// mass/pos.  After the first radix level only the keys in its digit are looked
+// at (a list in shared memory), and the levels end once all of them stay.
 #include <algorithm>
 
 #include "kvc_internal.cuh"
+#include "mma_ptx.cuh"
 #include "radix_select.cuh"
 #include "tc_ptx.cuh"
 
 namespace kvc {
 namespace {
 
-constexpr int kEvThreads = 512;     // segments of up to 32,768 rows
-constexpr int kEvThreadsBig = 1024;
+constexpr int kEvThreads = 512;      // few segments
+constexpr int kEvThreadsMany = 256;  // many: more CTAs per SM, one's copies under another's selection
+constexpr int kEvThreadsBig = 1024;  // segments of more than 16,384 rows
+constexpr int kEvList = 1024;        // keys listed after the first level
 
 struct EvictArgs {
   uint16_t *kpool, *vpool;  // [L][n_slots][H][D]
@@ -39,6 +44,7 @@ struct EvictArgs {
   int32_t *lists;  // streaming segments: [n_seg][2][cap]
   int64_t n_slots;
   int n_req, H, D, BS, max_blocks, cap, budget, n_sink, n_recent;
+  uint32_t bs_inv;  // page_inverse(BS)
 };
 
 struct Row {
@@ -47,26 +53,27 @@ struct Row {
   int n, n_pos, t_end, n_sink;
   int64_t recent0;
   __device__ int origin(int i) const { return i < n_pos ? pos[i] : t_end - (n - i); }
-  __device__ uint32_t key(int i, bool &nan) const {
-    const uint32_t k = order_key(mass[i], nan);
-    const int o = origin(i);
+  __device__ uint32_t key(float m, int o, bool &nan) const {
+    const uint32_t k = order_key(m, nan);
     return o < n_sink || o >= recent0 ? 0xFFFFFFFFu : k;
   }
+  __device__ uint32_t key(int i, bool &nan) const { return key(mass[i], origin(i), nan); }
 };
 
-template <bool STAGED>
-__global__ void __launch_bounds__(kEvThreadsBig)
+template <bool STAGED, int NT>
+__global__ void __launch_bounds__(NT)
 k_mass_evict(EvictArgs a) {
   extern __shared__ uint32_t dyn[];  // keys [kp(cap)], then the two lists in their place
   __shared__ uint32_t hist[kSelHist * 256];
   __shared__ uint32_t s_red[2][32], warp_tot[32];
-  __shared__ uint32_t s_kmax, s_kmin, s_prefix, s_need;
+  __shared__ uint32_t s_kmax, s_kmin, s_prefix, s_need, s_have, n_list;
+  __shared__ uint32_t list[STAGED ? kEvList : 1];
 
   const int S = (int)tc::cluster_nrank(), rank = (int)tc::cluster_rank();
   const int seg = blockIdx.x / S;
   const int h = seg % a.H, r = (seg / a.H) % a.n_req;
   const int64_t l = seg / (a.H * a.n_req);
-  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = a.seqused[r], B = a.budget;
   const bool bad = n < 0 || n > a.cap;
   const int64_t base = (int64_t)seg * a.cap;
@@ -86,7 +93,7 @@ k_mass_evict(EvictArgs a) {
   }
   if (bad || n <= B) {  // every CTA of the cluster alike
     if (rank == 0)
-      for (int i = tid; i < n && !bad; i += nt) {
+      for (int i = tid; i < n && !bad; i += NT) {
         mass_out[i] = row.mass[i];
         pos_out[i] = row.origin(i);
       }
@@ -96,11 +103,33 @@ k_mass_evict(EvictArgs a) {
   uint32_t *keys = dyn;
   bool nan = false;
   uint32_t kmax = 0u, kmin = 0xFFFFFFFFu;
-  for (int i = tid; i < n; i += nt) {
-    const uint32_t key = row.key(i, nan);
-    if (STAGED) keys[kp(i)] = key;
-    kmax = max(kmax, key);
-    kmin = min(kmin, key);
+  // rows below B keep their place (the ones that leave are overwritten below);
+  // in place, rewriting a weight changes nothing
+  const bool writes = rank == 0 && (a.mass_out != a.mass || a.pos_out != a.pos || row.n_pos < B);
+  constexpr int U1 = 4;
+  for (int b0 = 0; b0 < n; b0 += NT * U1) {
+    float m[U1];
+    int o[U1];
+#pragma unroll
+    for (int u = 0; u < U1; u++) {
+      const int i = b0 + u * NT + tid;
+      m[u] = i < n ? row.mass[i] : 0.f;
+      o[u] = i < n ? row.origin(i) : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < U1; u++) {
+      const int i = b0 + u * NT + tid;
+      if (i < n) {
+        const uint32_t key = row.key(m[u], o[u], nan);
+        if (STAGED) keys[kp(i)] = key;
+        kmax = max(kmax, key);
+        kmin = min(kmin, key);
+        if (i < B && writes) {
+          mass_out[i] = m[u];
+          pos_out[i] = o[u];
+        }
+      }
+    }
   }
   if (nan) record_error(a.status, KVC_ERR_NAN);
   kmax = __reduce_max_sync(0xFFFFFFFFu, kmax);
@@ -111,9 +140,9 @@ k_mass_evict(EvictArgs a) {
   }
   __syncthreads();
   if (warp == 0) {
-    const uint32_t mx = __reduce_max_sync(0xFFFFFFFFu, lane < nt / 32 ? s_red[0][lane] : 0u);
+    const uint32_t mx = __reduce_max_sync(0xFFFFFFFFu, lane < NT / 32 ? s_red[0][lane] : 0u);
     const uint32_t mn =
-        __reduce_min_sync(0xFFFFFFFFu, lane < nt / 32 ? s_red[1][lane] : 0xFFFFFFFFu);
+        __reduce_min_sync(0xFFFFFFFFu, lane < NT / 32 ? s_red[1][lane] : 0xFFFFFFFFu);
     if (lane == 0) {
       s_kmax = mx;
       s_kmin = mn;
@@ -127,61 +156,96 @@ k_mass_evict(EvictArgs a) {
   uint32_t need = (uint32_t)B;
   int hi = kmax == kmin ? -1 : 31 - __clz(kmax ^ kmin);
   uint32_t prefix = hi < 0 ? kmax : hi == 31 ? 0u : (kmax >> (hi + 1)) << (hi + 1);
-  while (hi >= 0) {
+  uint32_t have = (uint32_t)n;  // keys with the prefix
+  bool listed = false;
+  while (hi >= 0 && have > need) {
     const int lo = hi >= 7 ? hi - 7 : 0;
     const uint32_t dmask = (2u << (hi - lo)) - 1u;
     const uint32_t pmask = hi == 31 ? 0u : ~((2u << hi) - 1u);
     uint32_t *hw = hist + (warp % kSelHist) * 256;
-    for (int j = tid; j < kSelHist * 256; j += nt) hist[j] = 0u;
+    for (int j = tid; j < kSelHist * 256; j += NT) hist[j] = 0u;
     __syncthreads();
-    for (int i = tid; i < n; i += nt) {
-      const uint32_t key = STAGED ? keys[kp(i)] : row.key(i, nan);
-      if ((key & pmask) == prefix) atomicAdd(&hw[(key >> lo) & dmask], 1u);
+    if (listed) {
+      for (int i = tid; i < (int)n_list; i += NT)
+        if ((list[i] & pmask) == prefix) atomicAdd(&hw[(list[i] >> lo) & dmask], 1u);
+    } else {
+#pragma unroll 4
+      for (int i = tid; i < n; i += NT) {
+        const uint32_t key = STAGED ? keys[kp(i)] : row.key(i, nan);
+        if ((key & pmask) == prefix) atomicAdd(&hw[(key >> lo) & dmask], 1u);
+      }
     }
+    if (tid == 0 && !listed) n_list = 0;
     __syncthreads();
-    if (warp == 0) pick_digit(hist, lane, prefix, need, lo, &s_prefix, &s_need);
+    if (warp == 0) pick_digit(hist, lane, prefix, need, lo, &s_prefix, &s_need, &s_have);
     __syncthreads();
     prefix = s_prefix;
     need = s_need;
+    have = s_have;
     hi = lo - 1;
+    if (STAGED && !listed && have <= kEvList && hi >= 0 && have > need) {
+      const uint32_t next = ~((2u << hi) - 1u);  // (its order does not matter)
+#pragma unroll 4
+      for (int i = tid; i < n; i += NT) {
+        const uint32_t key = keys[kp(i)];
+        if ((key & next) == prefix) list[atomicAdd(&n_list, 1u)] = key;
+      }
+      listed = true;
+    }
   }
-  const uint32_t thr = prefix;
+  // all that have the prefix stay: no row is equal to the threshold (prefix > 0,
+  // for some key is lower, unless all are equal)
+  const bool ties = have > need;
+  const uint32_t thr = ties ? prefix : prefix - 1;
+  if (!ties) need = 0;
 
   // Ordered sweep in rounds of up to 64 rows per thread: stay = key > thr or
-  // one of the first `need` rows with key == thr.  Rows below B that leave
-  // and rows past B that stay are numbered by a block scan (two 32-bit counts
-  // never meet in one row, so one scan of each).
+  // one of the first `need` rows with key == thr.  Rows below B that leave and
+  // rows past B that stay are numbered by a block scan.
   int32_t *holes = STAGED ? reinterpret_cast<int32_t *>(keys) : a.lists + 2 * base;
   int32_t *tails = holes + (STAGED ? a.cap / 2 + 1 : a.cap);
-  const int ipt = STAGED ? (n + nt - 1) / nt : 64;
+  const int ipt = STAGED ? (n + NT - 1) / NT : 64;
   uint32_t eq_carry = 0, hole_carry = 0, tail_carry = 0;
-  for (int b0 = 0; b0 < n; b0 += nt * ipt) {
+  for (int b0 = 0; b0 < n; b0 += NT * ipt) {
     const int i0 = min(n, b0 + tid * ipt), cnt = min(n, i0 + ipt) - i0;
     uint64_t eqm = 0, km = 0;
+#pragma unroll 4
     for (int e = 0; e < cnt; e++) {
       const uint32_t key = STAGED ? keys[kp(i0 + e)] : row.key(i0 + e, nan);
       km |= (uint64_t)(key > thr) << e;
       eqm |= (uint64_t)(key == thr) << e;
     }
     uint32_t tot;
-    const uint32_t eq_before =
-        eq_carry + block_excl_scan((uint32_t)__popcll(eqm), &tot, warp_tot);
-    eq_carry += tot;
-    if (eq_before < need) {
-      const uint32_t take = min((uint32_t)__popcll(eqm), need - eq_before);
-      for (uint32_t t = 0; t < take; t++) {
-        km |= eqm & (~eqm + 1);  // lowest remaining equal row
-        eqm &= eqm - 1;
+    if (ties) {
+      const uint32_t eq_before =
+          eq_carry + block_excl_scan((uint32_t)__popcll(eqm), &tot, warp_tot);
+      eq_carry += tot;
+      if (eq_before < need) {
+        const uint32_t take = min((uint32_t)__popcll(eqm), need - eq_before);
+        for (uint32_t t = 0; t < take; t++) {
+          km |= eqm & (~eqm + 1);  // lowest remaining equal row
+          eqm &= eqm - 1;
+        }
       }
     }
     // rows of this chunk below B: bits [0, nb)
     const int nb = max(0, min(cnt, B - i0));
     const uint64_t below = nb >= 64 ? ~0ull : (1ull << nb) - 1ull;
     uint64_t hm = ~km & below, tm = km & ~below;
-    uint32_t hk = hole_carry + block_excl_scan((uint32_t)__popcll(hm), &tot, warp_tot);
-    hole_carry += tot;
-    uint32_t tk = tail_carry + block_excl_scan((uint32_t)__popcll(tm), &tot, warp_tot);
-    tail_carry += tot;
+    uint32_t hk, tk;
+    if (STAGED) {  // at most min(B, n − B) < 2^16 of each: one scan of both
+      const uint32_t both = block_excl_scan(
+          (uint32_t)__popcll(hm) | (uint32_t)__popcll(tm) << 16, &tot, warp_tot);
+      hk = both & 0xFFFFu;
+      tk = both >> 16;
+      hole_carry = tot & 0xFFFFu;
+      tail_carry = tot >> 16;
+    } else {
+      hk = hole_carry + block_excl_scan((uint32_t)__popcll(hm), &tot, warp_tot);
+      hole_carry += tot;
+      tk = tail_carry + block_excl_scan((uint32_t)__popcll(tm), &tot, warp_tot);
+      tail_carry += tot;
+    }
     // (the scans' barriers: every thread has read its keys, which the lists replace)
     for (; hm; hm &= hm - 1) holes[hk++] = i0 + __ffsll((long long)hm) - 1;
     for (; tm; tm &= tm - 1) tails[tk++] = i0 + __ffsll((long long)tm) - 1;
@@ -190,22 +254,12 @@ k_mass_evict(EvictArgs a) {
   else __syncthreads();
   const int n_pairs = (int)tail_carry;  // = hole_carry
 
-  if (rank == 0) {
-    // rows below B keep their place; the holes among them are overwritten below
-    if (a.mass_out != a.mass || a.pos_out != a.pos || row.n_pos < min(n, B))
-      for (int i = tid; i < B; i += nt) {
-        const float m = row.mass[i];
-        const int o = row.origin(i);
-        mass_out[i] = m;
-        pos_out[i] = o;
-      }
-    __syncthreads();
-    for (int k = tid; k < n_pairs; k += nt) {
+  if (rank == 0)
+    for (int k = tid; k < n_pairs; k += NT) {
       const int d = holes[k], s = tails[k];
       mass_out[d] = row.mass[s];
       pos_out[d] = row.origin(s);
     }
-  }
 
   // K and V rows: 16-byte columns, a warp takes pairs in turn
   const int cols = a.D / 8;          // columns of one row: 8 or 16
@@ -215,9 +269,9 @@ k_mass_evict(EvictArgs a) {
                    (c2 % cols) * 8;
   const int32_t *bt = a.block_table + (int64_t)r * a.max_blocks;
   const int64_t n_blocks = a.n_slots / a.BS, stride = (int64_t)a.H * a.D;
-  const int step = (nt / 32) * S * per;
+  const int step = (NT / 32) * S * per;
   constexpr int U = 4;
-  for (int k0 = (rank * (nt / 32) + warp) * per + sub; k0 < n_pairs; k0 += step * U) {
+  for (int k0 = (rank * (NT / 32) + warp) * per + sub; k0 < n_pairs; k0 += step * U) {
     uint4 v[U];
     int64_t d[U];
 #pragma unroll
@@ -226,10 +280,11 @@ k_mass_evict(EvictArgs a) {
       d[u] = -1;
       if (k < n_pairs) {
         const int pd = holes[k], ps = tails[k];
-        const int32_t bd = bt[pd / a.BS], bs = bt[ps / a.BS];
+        const int gd = page_of(pd, a.bs_inv), gs = page_of(ps, a.bs_inv);
+        const int32_t bd = bt[gd], bs = bt[gs];
         if (bd >= 0 && bd < n_blocks && bs >= 0 && bs < n_blocks) {
-          d[u] = ((int64_t)bd * a.BS + pd % a.BS) * stride;
-          v[u] = ld_stream(pool + ((int64_t)bs * a.BS + ps % a.BS) * stride);
+          d[u] = ((int64_t)bd * a.BS + pd - gd * a.BS) * stride;
+          v[u] = ld_stream(pool + ((int64_t)bs * a.BS + ps - gs * a.BS) * stride);
         } else {
           record_error(a.status, KVC_ERR_BOUNDS);
         }
@@ -260,10 +315,14 @@ cudaError_t launch_mass_evict(uint16_t *kpool, uint16_t *vpool, int64_t n_slots,
               mass,      pos,      mass_out,    pos_out, n_out,   status,
               reinterpret_cast<int32_t *>(ws),  n_slots, n_req,   H,
               D,         BS,       max_blocks,  max_blocks * BS,  budget,
-              n_sink,    n_recent};
+              n_sink,    n_recent, page_inverse(BS)};
   const int n_seg = L * n_req * H;
-  const bool staged = a.cap <= KVC_EVICT_STAGED_ROWS;
-  auto *kern = staged ? k_mass_evict<true> : k_mass_evict<false>;
+  const bool staged = a.cap <= KVC_EVICT_STAGED_ROWS, many = n_seg >= 4 * device_sm_count();
+  const int nt = a.cap > 16384 ? kEvThreadsBig : many ? kEvThreadsMany : kEvThreads;
+  auto *kern = !staged               ? k_mass_evict<false, kEvThreadsBig>
+               : nt == kEvThreadsBig ? k_mass_evict<true, kEvThreadsBig>
+               : many                ? k_mass_evict<true, kEvThreadsMany>
+                                     : k_mass_evict<true, kEvThreads>;
   size_t smem = 0;
   if (staged) {
     smem = ((size_t)a.cap + a.cap / 32 + 2) * sizeof(uint32_t);
@@ -277,7 +336,7 @@ cudaError_t launch_mass_evict(uint16_t *kpool, uint16_t *vpool, int64_t n_slots,
     while (S < 8 && n_seg * S * 2 <= 2 * device_sm_count()) S *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((int64_t)n_seg * S));
-  cfg.blockDim = dim3(a.cap > 32768 ? kEvThreadsBig : kEvThreads);
+  cfg.blockDim = dim3(nt);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];

@@ -56,10 +56,11 @@ __device__ __forceinline__ uint32_t block_excl_scan(uint32_t v, uint32_t *total,
 
 // Warp 0: from the radix level's histograms (kSelHist copies of 256 bins),
 // the largest digit d whose count from the top reaches `need`; writes the
-// extended prefix and the count still needed among the keys equal to it.
+// extended prefix, the count still needed among the keys with that prefix and
+// (where asked for) how many keys have it.
 __device__ __forceinline__ void pick_digit(const uint32_t *hist, int lane, uint32_t prefix,
                                            uint32_t need, int lo, uint32_t *s_prefix,
-                                           uint32_t *s_need) {
+                                           uint32_t *s_need, uint32_t *s_have = nullptr) {
   // lane l: bins 8l … 8l+7 summed over the histogram copies
   uint32_t loc[8], lsum = 0;
 #pragma unroll
@@ -77,18 +78,20 @@ __device__ __forceinline__ void pick_digit(const uint32_t *hist, int lane, uint3
   }
   const uint32_t above = sfx - lsum;  // Σ of the bins ≥ 8·(lane + 1)
   if (above < need && sfx >= need) {  // exactly one lane
-    uint32_t acc = above;
+    uint32_t acc = above, have = 0;
     int d = 8 * lane;
 #pragma unroll
     for (int b = 7; b >= 0; b--)
       if (acc + loc[b] >= need) {
         d = 8 * lane + b;
+        have = loc[b];
         break;
       } else {
         acc += loc[b];
       }
     *s_prefix = prefix | ((uint32_t)d << lo);
     *s_need = need - acc;
+    if (s_have) *s_have = have;
   }
 }
 
