@@ -106,7 +106,7 @@ k_mass_evict(EvictArgs a) {
   // rows below B keep their place (the ones that leave are overwritten below);
   // in place, rewriting a weight changes nothing
   const bool writes = rank == 0 && (a.mass_out != a.mass || a.pos_out != a.pos || row.n_pos < B);
-  constexpr int U1 = 4;
+  constexpr int U1 = 8;
   for (int b0 = 0; b0 < n; b0 += NT * U1) {
     float m[U1];
     int o[U1];
@@ -175,7 +175,11 @@ k_mass_evict(EvictArgs a) {
         if ((key & pmask) == prefix) atomicAdd(&hw[(key >> lo) & dmask], 1u);
       }
     }
-    if (tid == 0 && !listed) n_list = 0;
+    if (tid == 0 && !listed) {
+      n_list = 0;
+      s_kmax = 0u;
+      s_kmin = 0xFFFFFFFFu;
+    }
     __syncthreads();
     if (warp == 0) pick_digit(hist, lane, prefix, need, lo, &s_prefix, &s_need, &s_have);
     __syncthreads();
@@ -185,11 +189,25 @@ k_mass_evict(EvictArgs a) {
     hi = lo - 1;
     if (STAGED && !listed && have <= kEvList && hi >= 0 && have > need) {
       const uint32_t next = ~((2u << hi) - 1u);  // (its order does not matter)
+      uint32_t mx = 0u, mn = 0xFFFFFFFFu;
 #pragma unroll 4
       for (int i = tid; i < n; i += NT) {
         const uint32_t key = keys[kp(i)];
-        if ((key & next) == prefix) list[atomicAdd(&n_list, 1u)] = key;
+        if ((key & next) == prefix) {
+          list[atomicAdd(&n_list, 1u)] = key;
+          mx = max(mx, key);
+          mn = min(mn, key);
+        }
       }
+      // their common leading bits need no level (equal weights: none at all)
+      if (mx >= mn) {
+        atomicMax(&s_kmax, mx);
+        atomicMin(&s_kmin, mn);
+      }
+      __syncthreads();
+      const uint32_t diff = s_kmax ^ s_kmin;
+      hi = diff ? 31 - __clz(diff) : -1;
+      prefix = hi < 0 ? s_kmax : (s_kmax >> (hi + 1)) << (hi + 1);
       listed = true;
     }
   }
@@ -345,7 +363,7 @@ cudaError_t launch_mass_evict(uint16_t *kpool, uint16_t *vpool, int64_t n_slots,
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = S > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
