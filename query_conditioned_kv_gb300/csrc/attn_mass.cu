@@ -67,8 +67,8 @@ struct MassRowSmem {
   static constexpr int kQ = kRing;
   static constexpr int kLse = kQ + NT * 8 * D * 2;  // lse·log2e per row
   static constexpr int kVis = kLse + NT * 8 * 4;    // positions each row sees
-  static constexpr int kMisc = kVis + NT * 8 * 4;   // scan scratch [66] int64
-  static constexpr int kValid = kMisc + 66 * 8;
+  static constexpr int kMisc = kVis + NT * 8 * 4;   // scratch [32] int64
+  static constexpr int kValid = kMisc + 32 * 8;
   static constexpr int kBytes = kValid + kMrWarps * kMrStages * 4;
 };
 
@@ -95,25 +95,29 @@ k_mass_rows(MassArgs a, int n_cta_max) {
   const uint32_t qbase = smem_u32(sm + S::kQ);
 
   // tiles of all requests (one layer and head)
-  int64_t per = 0;
-  for (int r = tid; r < a.n_req; r += kMrThreads) {
-    per += mass_tiles(a, r, kTile);
-    int seq, r0, n;
-    if (blockIdx.x == 0 && !mass_request(a, r, seq, r0, n)) record_error(a.status, KVC_ERR_BOUNDS);
-  }
-  per = block_sum(per, sh);
+  if (blockIdx.x == 0)  // one report per bad request
+    for (int r = tid; r < a.n_req; r += kMrThreads) {
+      int seq, r0, n;
+      if (!mass_request(a, r, seq, r0, n)) record_error(a.status, KVC_ERR_BOUNDS);
+    }
+  auto tiles = [&](int x) { return (int64_t)mass_tiles(a, x, kTile); };
+  const WarpSums sums = warp_sums(a.n_req, tiles);
+  const int64_t per = sums.total;
   const int64_t total = per * a.L * a.H;
   const int n_cta = (int)min((int64_t)n_cta_max, total);
   if ((int)blockIdx.x >= n_cta) return;
-  const int64_t run0 = total * blockIdx.x / n_cta, run1 = total * (blockIdx.x + 1) / n_cta;
+  const int64_t run0 = div64(total * blockIdx.x, n_cta);
+  const int64_t run1 = div64(total * (blockIdx.x + 1), n_cta);
 
-  // run0 → (layer, request, head, tile): order l, r, h, tile
-  int64_t l = run0 / (per * a.H), in_layer = run0 % (per * a.H), before;
+  // run0 → (layer, request, head, tile): order l, r, h, tile.  H heads of a
+  // request of w tiles: place x of a layer is place x / H of the sums, less what
+  // the division drops.
+  int64_t l = div64(run0, per * a.H), in_layer = run0 - l * per * a.H, before;
   int r;
-  block_find(
-      a.n_req, in_layer, sh, [&](int x) { return (int64_t)a.H * mass_tiles(a, x, kTile); }, r, before);
+  warp_find(sums, a.n_req, div64(in_layer, a.H), tiles, r, before);
+  const int64_t in_request = in_layer - before * a.H;
   int n_kt = mass_tiles(a, r, kTile);
-  int h = (int)((in_layer - before) / n_kt), t0 = (int)((in_layer - before) % n_kt);
+  int h = (int)div64(in_request, n_kt), t0 = (int)(in_request - (int64_t)h * n_kt);
   const int64_t n_blocks = a.n_slots / a.BS;
 
   for (int64_t g = run0; g < run1;) {
@@ -434,19 +438,22 @@ struct TcPos {
   }
 };
 
-// Position of tile x (by the whole CTA).
+// Position of tile x; sums: of the requests' tiles per layer and head.
 template <int RT>
 __device__ __forceinline__ TcPos<RT> tc_find(const MassArgs &a, const MassTc &p, int64_t x,
-                                             int64_t per, int64_t *sh) {
+                                             const WarpSums &sums) {
   TcPos<RT> f;
-  f.l = x / (per * a.H);
+  const int64_t layer = sums.total * a.H;
+  f.l = div64(x, layer);
   int64_t before;
-  const int64_t in_layer = x % (per * a.H);
-  block_find(
-      a.n_req, in_layer, sh, [&](int r) { return a.H * tc_request_work<RT>(a, p, r); }, f.r, before);
+  const int64_t in_layer = x - f.l * layer;
+  warp_find(
+      sums, a.n_req, div64(in_layer, a.H), [&](int r) { return tc_request_work<RT>(a, p, r); }, f.r,
+      before);
+  before *= a.H;
   const int64_t w = tc_request_work<RT>(a, p, f.r);
-  f.h = (int)((in_layer - before) / w);
-  const int64_t in_head = (in_layer - before) % w;
+  f.h = (int)div64(in_layer - before, w);
+  const int64_t in_head = in_layer - before - f.h * w;
   if (RT == 1) {
     f.rg = 0;
     f.t = (int)in_head;
@@ -512,26 +519,23 @@ k_mass_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
   tc_fence_after();
   const uint32_t tmem = sm.tmem_holder;
 
-  int64_t *scan = reinterpret_cast<int64_t *>(nlse);  // (before the first LSE is stored)
   if (RT == 2) asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan
-  int64_t per = 0;
-  for (int r = tid; r < a.n_req; r += kTcThreads) {
-    per += tc_request_work<RT>(a, p, r);
-    int seq, r0, n;
-    if (RT == 1 && blockIdx.x == 0 && !mass_request(a, r, seq, r0, n))
-      record_error(a.status, KVC_ERR_BOUNDS);
-  }
-  per = block_sum(per, scan);
+  if (RT == 1 && blockIdx.x == 0)  // one report per bad request
+    for (int r = tid; r < a.n_req; r += kTcThreads) {
+      int seq, r0, n;
+      if (!mass_request(a, r, seq, r0, n)) record_error(a.status, KVC_ERR_BOUNDS);
+    }
+  const WarpSums sums = warp_sums(a.n_req, [&](int r) { return tc_request_work<RT>(a, p, r); });
+  const int64_t per = sums.total;
   const int64_t total = per * a.L * a.H;
   const int n_cta = (int)min((int64_t)p.n_cta, total);
   // (a misaligned base cannot hold swizzled tiles: nothing would be right)
   const bool works = (int)blockIdx.x < n_cta && (base_u & 1023u) == 0;
   if ((base_u & 1023u) != 0 && tid == 0) record_error(a.status, KVC_ERR_CUDA);
-  const int64_t run0 = works ? total * blockIdx.x / n_cta : 0;
-  const int64_t run1 = works ? total * (blockIdx.x + 1) / n_cta : 0;
+  const int64_t run0 = works ? div64(total * blockIdx.x, n_cta) : 0;
+  const int64_t run1 = works ? div64(total * (blockIdx.x + 1), n_cta) : 0;
   TcPos<RT> pos{};
-  if (works) pos = tc_find<RT>(a, p, run0, per, scan);
-  __syncthreads();
+  if (works) pos = tc_find<RT>(a, p, run0, sums);
   if (RT == 2) asm volatile("griddepcontrol.launch_dependents;");
 
   bool ok = true;

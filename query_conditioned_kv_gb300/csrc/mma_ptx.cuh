@@ -142,20 +142,8 @@ inline uint32_t page_inverse(int BS) {
   return BS == 1 ? 0u : (uint32_t)(((1ull << 32) + BS - 1) / BS);
 }
 
-// Sum over the CTA (a multiple of 32 threads); every thread gets it.  sh: 64
+// Maximum over the CTA (a multiple of 32 threads); every thread gets it.  sh: 32
 // words of scratch, free again on return.
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t *sh) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0;
-  for (int w = 0; w < (int)(blockDim.x >> 5); w++) v += sh[w];
-  __syncthreads();
-  return v;
-}
-
-// Maximum over the CTA, likewise.
 __device__ __forceinline__ int64_t block_max(int64_t v, int64_t *sh) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v = max(v, (int64_t)__shfl_xor_sync(0xFFFFFFFFu, v, o));
@@ -167,41 +155,60 @@ __device__ __forceinline__ int64_t block_max(int64_t v, int64_t *sh) {
   return v;
 }
 
-// The element i of [0, n) whose interval [Σ_{<i} size, Σ_{≤i} size) holds t
-// (t below the sum of all), and Σ_{<i} size; by the whole CTA, one scan per
-// blockDim.x elements.  sh: 66 words of scratch, free again on return.
-template <class F>
-__device__ __forceinline__ void block_find(int n, int64_t t, int64_t *sh, F size, int &found,
-                                           int64_t &before) {
-  int64_t carry = 0;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  for (int i0 = 0; i0 < n; i0 += blockDim.x) {
-    const int i = i0 + threadIdx.x;
-    const int64_t mine = i < n ? size(i) : 0;
-    int64_t x = mine;
+// x / y for x ≥ 0, y > 0 (64-bit division is a long call: most sizes fit 32 bits).
+__device__ __forceinline__ int64_t div64(int64_t x, int64_t y) {
+  return x >> 32 || y >> 32 ? x / y : (uint32_t)x / (uint32_t)y;
+}
+
+// Σ size(i) over [0, n), and which element holds place t of the sum.  By every
+// warp for itself: a short kernel's beginning is latency, and barriers between
+// its steps would add to it.
+struct WarpSums {
+  int64_t total;
+  int64_t mine, upto;  // the lane's among the first 32: its size, the sum up to and with it
+};
+__device__ __forceinline__ int64_t warp_prefix(int64_t x) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) sh[warp] = x;
-    __syncthreads();
-    int64_t lo = carry + x - mine, tot = 0;
-    for (int w = 0; w < nw; w++) {
-      if (w < warp) lo += sh[w];
-      tot += sh[w];
-    }
-    if (mine > 0 && t >= lo && t < lo + mine) {
-      sh[64] = i;
-      sh[65] = lo;
-    }
-    __syncthreads();
-    if (t < carry + tot) break;
-    carry += tot;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+    if ((threadIdx.x & 31) >= o) x += y;
   }
-  found = (int)sh[64];
-  before = sh[65];
-  __syncthreads();
+  return x;
+}
+template <class F>
+__device__ __forceinline__ WarpSums warp_sums(int n, F size) {
+  const int lane = threadIdx.x & 31;
+  WarpSums w;
+  w.mine = lane < n ? size(lane) : 0;
+  w.upto = warp_prefix(w.mine);
+  w.total = __shfl_sync(0xFFFFFFFFu, w.upto, 31);
+  if (n > 32) {
+    int64_t x = 0;
+#pragma unroll 4
+    for (int i = 32 + lane; i < n; i += 32) x += size(i);
+    w.total += __shfl_sync(0xFFFFFFFFu, warp_prefix(x), 31);
+  }
+  return w;
+}
+// The element i whose interval [Σ_{<i}, Σ_{≤i}) holds t < total, and Σ_{<i}.
+template <class F>
+__device__ __forceinline__ void warp_find(const WarpSums &w, int n, int64_t t, F size, int &found,
+                                          int64_t &before) {
+  int64_t mine = w.mine, upto = w.upto, carry = 0;
+  for (int i0 = 0;;) {
+    const uint32_t past = __ballot_sync(0xFFFFFFFFu, t < carry + upto);
+    if (past || i0 + 32 >= n) {
+      const int at = past ? __ffs(past) - 1 : 0;
+      found = i0 + at;
+      before = carry + __shfl_sync(0xFFFFFFFFu, upto - mine, at);
+      return;
+    }
+    carry += __shfl_sync(0xFFFFFFFFu, upto, 31);
+    i0 += 32;
+    const int i = i0 + (int)(threadIdx.x & 31);
+    mine = i < n ? size(i) : 0;
+    upto = warp_prefix(mine);
+  }
 }
 
 }  // namespace

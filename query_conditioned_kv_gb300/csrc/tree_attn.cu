@@ -81,16 +81,12 @@ __device__ __forceinline__ void tree_tiles(const TreeArgs &a, int r, int &n_rt, 
 }
 
 // How `total` tiles are dealt out: CTA c begins at ⌊total·c / n_cta⌋.
-__device__ __forceinline__ int64_t run_div(int64_t x, int64_t y) {
-  // (64-bit division is a long call: most sizes fit 32 bits)
-  return x >> 32 || y >> 32 ? x / y : (uint32_t)x / (uint32_t)y;
-}
 __device__ __forceinline__ int64_t run_start(int64_t total, int n_cta, int cta) {
-  return run_div(total * cta, n_cta);
+  return div64(total * cta, n_cta);
 }
 // The CTA whose run holds tile t: the last c with total·c < (t + 1)·n_cta.
 __device__ __forceinline__ int run_owner(int64_t total, int n_cta, int64_t t) {
-  return (int)run_div((t + 1) * n_cta - 1, total);
+  return (int)div64((t + 1) * n_cta - 1, total);
 }
 
 // Tiles of request r, all heads.
@@ -109,8 +105,7 @@ template <int D, int MT>
 struct RowSmem {
   static constexpr int kRing = kRowWarps * kRowStages * kWarpStage;
   static constexpr int kQ = kRing;                       // MT·16 rows of q
-  static constexpr int kMisc = kQ + MT * 16 * D * 2;     // scan scratch [66] int64
-  static constexpr int kValid = kMisc + 66 * 8;          // valid keys per (warp, stage)
+  static constexpr int kValid = kQ + MT * 16 * D * 2;  // valid keys per (warp, stage)
   static constexpr int kMl = kValid + kRowWarps * kRowStages * 4;  // (max, sum) per (warp, row)
   static constexpr int kBytes = kMl + kRowWarps * MT * 16 * 8;
   static_assert(kRowWarps * MT * 16 * D * 4 <= kRing, "the warps' O fits the ring");
@@ -150,7 +145,6 @@ k_tree_rows(TreeArgs a) {
   constexpr int R = MT * 16;
   extern __shared__ __align__(1024) uint8_t sm[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  int64_t *sh = reinterpret_cast<int64_t *>(sm + S::kMisc);
   const uint32_t ring = smem_u32(sm) + warp * kRowStages * kWarpStage;
   uint32_t *valid_s = reinterpret_cast<uint32_t *>(sm + S::kValid) + warp * kRowStages;
   const uint32_t qbase = smem_u32(sm + S::kQ);
@@ -162,23 +156,24 @@ k_tree_rows(TreeArgs a) {
       int c, q0, T;
       if (!tree_request(a, r, c, q0, T)) record_error(a.status, KVC_ERR_BOUNDS);
     }
-  int64_t total = 0, before;
-  for (int x = tid; x < a.n_req; x += kRowThreads) total += request_tiles(a, x);
-  total = block_sum(total, sh);
+  auto tiles = [&](int x) { return request_tiles(a, x); };
+  const WarpSums sums = warp_sums(a.n_req, tiles);
+  const int64_t total = sums.total;
+  int64_t before;
   const int n_cta = (int)min((int64_t)a.n_cta, total);  // every run holds a tile
   if ((int)blockIdx.x >= n_cta) return;
   const int64_t run0 = run_start(total, n_cta, blockIdx.x);
   const int64_t run1 = run_start(total, n_cta, blockIdx.x + 1);
   int r;
-  block_find(a.n_req, run0, sh, [&](int x) { return request_tiles(a, x); }, r, before);
+  warp_find(sums, a.n_req, run0, tiles, r, before);
 
   const int64_t n_blocks = a.n_slots / a.BS;
   int64_t g = run0;  // next tile of the run
   int c, q0, T, n_rt, n_kt;
   tree_request(a, r, c, q0, T);
   tree_tiles(a, r, n_rt, n_kt);
-  int unit = (int)((g - before) / n_kt);  // h·n_rt + row tile
-  int t0 = (int)((g - before) % n_kt);
+  int unit = (int)div64(g - before, n_kt);  // h·n_rt + row tile
+  int t0 = (int)(g - before - (int64_t)unit * n_kt);
   while (g < run1) {
     const int h = unit / n_rt, rt = unit % n_rt;
     const int t1 = (int)min((int64_t)n_kt, t0 + (run1 - g));
@@ -522,7 +517,6 @@ struct TreeTcHead {
   uint64_t full[2][kTtSlots], empty[2][kTtSlots];  // [K, V][tile mod kTtSlots]
   uint64_t qfull, qempty;
   uint64_t sfull[2], sfree[2], pready[2], pvdone[2], ofree;  // [team]
-  int64_t scan[66];
   uint32_t tmem_holder;
   volatile int failed, odd, bad;
   float nb[2][128];  // −reference per team and row
@@ -578,8 +572,8 @@ struct TreePos {
   __device__ __forceinline__ void init(const TreeArgs &a, int64_t before) {
     tree_request(a, r, c, q0, T);
     tree_tiles(a, r, n_rt, n_kt);
-    unit = (int)((g - before) / n_kt);
-    t0 = (int)((g - before) % n_kt);
+    unit = (int)div64(g - before, n_kt);
+    t0 = (int)(g - before - (int64_t)unit * n_kt);
   }
   __device__ __forceinline__ int t1() const { return (int)min((int64_t)n_kt, t0 + (run1 - g)); }
   __device__ __forceinline__ int h() const { return unit / n_rt; }
@@ -669,9 +663,9 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
       int c, q0, T;
       if (!tree_request(a, r, c, q0, T)) record_error(a.status, KVC_ERR_BOUNDS);
     }
-  int64_t total = 0;
-  for (int x = tid; x < a.n_req; x += blockDim.x) total += request_tiles(a, x);
-  total = block_sum(total, sm.scan);
+  auto tiles = [&](int x) { return request_tiles(a, x); };
+  const WarpSums sums = warp_sums(a.n_req, tiles);
+  const int64_t total = sums.total;
   const int n_cta = (int)min((int64_t)a.n_cta, total);
   const bool works = (int)blockIdx.x < n_cta;
   TreePos pos{};
@@ -679,7 +673,7 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
     pos.run0 = pos.g = run_start(total, n_cta, blockIdx.x);
     pos.run1 = run_start(total, n_cta, blockIdx.x + 1);
     int64_t before;
-    block_find(a.n_req, pos.g, sm.scan, [&](int x) { return request_tiles(a, x); }, pos.r, before);
+    warp_find(sums, a.n_req, pos.g, tiles, pos.r, before);
     pos.init(a, before);
   }
 
