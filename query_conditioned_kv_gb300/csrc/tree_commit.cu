@@ -12,7 +12,10 @@
 // What bounds it: latency.  A path of 8 rows of 2 KB (8 KV heads, D 128) is
 // 64 KB of traffic a layer; one CTA per (request, layer) reads all its rows
 // before it writes the first.
+#include <algorithm>
+
 #include "kvc_internal.cuh"
+#include "mma_ptx.cuh"
 
 namespace kvc {
 namespace {
@@ -27,6 +30,8 @@ struct CommitArgs {
   int32_t *seq_out, *row_idx, *row_vis, *status;
   int64_t n_slots;
   int max_blocks, max_path, row_elems, BS;  // row_elems = H·D
+  int L, layers;                            // layers of one CTA
+  uint32_t bs_inv;                          // page_inverse(BS)
 };
 
 __global__ void __launch_bounds__(kCommitThreads)
@@ -37,6 +42,8 @@ k_tree_commit(CommitArgs a) {
   const int64_t T = (int64_t)a.q_off[r + 1] - q0;
   const int64_t cap = (int64_t)a.max_blocks * a.BS;
   const int32_t *path = a.path + (int64_t)r * a.max_path;
+  // (asked for with the sizes, so that the loops below find it in L1)
+  if (tid < a.max_path) asm volatile("prefetch.global.L1 [%0];" ::"l"(path + tid));
   bool bad = c < 0 || q0 < 0 || T < 0 || c + T > cap || n < 0 || n > a.max_path || n > T;
   if (!bad)
     for (int i = tid; i < n; i += kCommitThreads) {
@@ -61,16 +68,19 @@ k_tree_commit(CommitArgs a) {
   int32_t *src = s_slot, *dst = s_slot + a.max_path;
   for (int i = tid; i < n; i += kCommitThreads) {
     const int p = c + path[i], d = c + i;
-    const int32_t bp = bt[p / a.BS], bd = bt[d / a.BS];
+    const int gp = page_of(p, a.bs_inv), gd = page_of(d, a.bs_inv);
+    const int32_t bp = bt[gp], bd = bt[gd];
     const bool ok = bp >= 0 && bp < n_blocks && bd >= 0 && bd < n_blocks;
     if (!ok) record_error(a.status, KVC_ERR_BOUNDS);
-    src[i] = bp * a.BS + p % a.BS;
-    dst[i] = ok && p != d ? bd * a.BS + d % a.BS : -1;
+    src[i] = bp * a.BS + p - gp * a.BS;
+    dst[i] = ok && p != d ? bd * a.BS + d - gd * a.BS : -1;
   }
   __syncthreads();
-  const int64_t layer = (int64_t)blockIdx.y * a.n_slots;
+  const int l0 = blockIdx.y * a.layers, n_l = min(a.layers, a.L - l0);
   const int cols = a.row_elems / 8;  // 16-byte columns of one row
-  for (int t = tid; t < 2 * cols; t += kCommitThreads) {
+  for (int x = tid; x < 2 * cols * n_l; x += kCommitThreads) {
+    const int l = x / (2 * cols), t = x - l * 2 * cols;
+    const int64_t layer = (int64_t)(l0 + l) * a.n_slots;
     uint16_t *pool = t < cols ? a.kpool : a.vpool;
     const int col = (t < cols ? t : t - cols) * 8;
     for (int i0 = 0; i0 < n; i0 += kCommitAhead) {
@@ -99,7 +109,13 @@ cudaError_t launch_tree_commit(uint16_t *kpool, uint16_t *vpool, int64_t n_slots
   CommitArgs a{kpool,   vpool,   block_table, ctx_len, q_off, path,       n_path,
                seq_out, row_idx, row_vis,     status,  n_slots, max_blocks, max_path,
                H * D,   BS};
-  k_tree_commit<<<dim3(n_req, L), kCommitThreads, 2 * max_path * sizeof(int32_t), s>>>(a);
+  // one CTA a layer until the GPU is full (4 CTAs of 256 threads an SM), then several
+  // layers a CTA, which share the lookups
+  const int64_t full = 4 * (int64_t)device_sm_count();
+  a.L = L;
+  a.layers = (int)std::min<int64_t>(L, ((int64_t)n_req * L + full - 1) / full);
+  a.bs_inv = page_inverse(BS);
+  k_tree_commit<<<dim3(n_req, (L + a.layers - 1) / a.layers), kCommitThreads, 2 * max_path * sizeof(int32_t), s>>>(a);
   return cudaGetLastError();
 }
 
