@@ -975,29 +975,44 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
           }
           const uint32_t valid_keys = __ballot_sync(0xFFFFFFFFu, valid);
           const float hidden = zs < 0.f ? INFINITY : -INFINITY;  // −inf once scaled
-#pragma unroll 1
-          for (int w = 0; w < 4; w++) {
-            const uint32_t ta = ts + ((uint32_t)(16 * (w >> 1)) << 16) + 64 * (w & 1);
-            uint32_t bits = 0;
-#pragma unroll 1
-            for (int e = 0; e < 32; e++) {  // register e: see tmem_frag8
-              const int kk = (w >> 1) * 16 + lane / 4 + 8 * ((e >> 1) & 1);
-              const int x = pos.rt() * a.rstep + row0 + 64 * (w & 1) + 8 * (e >> 2) + 2 * (lane & 3) + (e & 1);
-              const int j = t * kTtKeys + quarter * 32 + kk - pos.c, i = x / a.G;
-              bool v = (valid_keys >> kk) & 1u;
-              if (v && j >= 0)
-                v = i < pos.T &&
-                    (a.mask ? (a.mask[(int64_t)(pos.q0 + i) * a.mask_words + (j >> 5)] >> (j & 31)) & 1u
-                            : j <= i);
-              bits |= (uint32_t)v << e;
-            }
-            uint32_t z[32];
-            tmem_frag8(ta, z);
-            tmem_wait(z);
+          // which of the warp's 32 keys the rows lane + 32·m see
+          uint32_t sees[4];
+          const int p0 = t * kTtKeys + quarter * 32, j0 = p0 - pos.c;
 #pragma unroll
-            for (int e = 0; e < 32; e++)
-              if (!((bits >> e) & 1u)) z[e] = __float_as_uint(hidden);
-            tmem_put(ta, z);
+          for (int m = 0; m < 4; m++) {
+            const int i = (pos.rt() * a.rstep + row0 + 32 * m + lane) / a.G;
+            uint32_t v = j0 <= -32 ? 0xFFFFFFFFu : j0 < 0 ? (1u << -j0) - 1u : 0u;
+            if (i < pos.T) v = visible_bits<32>(a, i, pos.q0, pos.c, pos.T, p0);
+            sees[m] = v & valid_keys;
+          }
+#pragma unroll 1
+          for (int ch = 0; ch < 2; ch++) {
+            uint32_t bits[2] = {0, 0};  // of the registers of the two fragments (see tmem_frag8)
+#pragma unroll
+            for (int k = 0; k < 8; k++)
+#pragma unroll
+              for (int e = 0; e < 2; e++) {
+                const uint32_t mine = ch ? sees[2 + (k >> 2)] : sees[k >> 2];
+                const uint32_t v =
+                    __shfl_sync(0xFFFFFFFFu, mine, 8 * (k & 3) + 2 * (lane & 3) + e) >> (lane / 4);
+#pragma unroll
+                for (int j = 0; j < 2; j++) {
+                  bits[0] |= ((v >> (8 * j)) & 1u) << (4 * k + 2 * j + e);
+                  bits[1] |= ((v >> (16 + 8 * j)) & 1u) << (4 * k + 2 * j + e);
+                }
+              }
+#pragma unroll 1
+            for (int hf = 0; hf < 2; hf++) {
+              const uint32_t ta = ts + ((uint32_t)(16 * hf) << 16) + 64 * ch;
+              const uint32_t bh = hf ? bits[1] : bits[0];
+              uint32_t z[32];
+              tmem_frag8(ta, z);
+              tmem_wait(z);
+#pragma unroll
+              for (int e = 0; e < 32; e++)
+                if (!((bh >> e) & 1u)) z[e] = __float_as_uint(hidden);
+              tmem_put(ta, z);
+            }
           }
         }
         for (;;) {
