@@ -373,6 +373,8 @@ struct MassTc {
 struct TcHead {
   uint64_t kfull[kTcMaxK], kempty[kTcMaxK], qfull[2], qempty[2], lfull[2], lempty[2];
   uint64_t tfull[4], tempty[4];
+  int64_t run[2], at_l;  // the CTA's run of tiles, and where it begins
+  int at[5];
   int lo[2][4];  // least limit of the slot's rows, per producer warp
   uint32_t tmem_holder;
   volatile int failed;
@@ -487,7 +489,32 @@ k_mass_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
   const uint32_t base_u = smem_u32(base);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  if (tid == 0) {
+  if (RT == 2) asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan
+  if (warp == 0) {
+    const WarpSums sums = warp_sums(a.n_req, [&](int r) { return tc_request_work<RT>(a, p, r); });
+    const int64_t total = sums.total * a.L * a.H;
+    const int n_cta = (int)min((int64_t)p.n_cta, total);
+    // (a misaligned base cannot hold swizzled tiles: nothing would be right)
+    const bool works = (int)blockIdx.x < n_cta && (base_u & 1023u) == 0;
+    if ((base_u & 1023u) != 0 && lane == 0) record_error(a.status, KVC_ERR_CUDA);
+    TcPos<RT> f{};
+    int64_t run0 = 0, run1 = 0;
+    if (works) {
+      run0 = div64(total * blockIdx.x, n_cta);
+      run1 = div64(total * (blockIdx.x + 1), n_cta);
+      f = tc_find<RT>(a, p, run0, sums);
+    }
+    if (lane == 0) {
+      sm.run[0] = run0;
+      sm.run[1] = run1;
+      sm.at_l = f.l;
+      sm.at[0] = f.r;
+      sm.at[1] = f.h;
+      sm.at[2] = f.rg;
+      sm.at[3] = f.t;
+      sm.at[4] = f.n_t;
+    }
+  } else if (warp == 1 && lane == 0) {
     sm.failed = 0;
     for (int i = 0; i < KS; i++) {
       mbar_init(smem_u32(sm.kfull + i), kTcProd * 32);
@@ -519,23 +546,13 @@ k_mass_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
   tc_fence_after();
   const uint32_t tmem = sm.tmem_holder;
 
-  if (RT == 2) asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan
   if (RT == 1 && blockIdx.x == 0)  // one report per bad request
     for (int r = tid; r < a.n_req; r += kTcThreads) {
       int seq, r0, n;
       if (!mass_request(a, r, seq, r0, n)) record_error(a.status, KVC_ERR_BOUNDS);
     }
-  const WarpSums sums = warp_sums(a.n_req, [&](int r) { return tc_request_work<RT>(a, p, r); });
-  const int64_t per = sums.total;
-  const int64_t total = per * a.L * a.H;
-  const int n_cta = (int)min((int64_t)p.n_cta, total);
-  // (a misaligned base cannot hold swizzled tiles: nothing would be right)
-  const bool works = (int)blockIdx.x < n_cta && (base_u & 1023u) == 0;
-  if ((base_u & 1023u) != 0 && tid == 0) record_error(a.status, KVC_ERR_CUDA);
-  const int64_t run0 = works ? div64(total * blockIdx.x, n_cta) : 0;
-  const int64_t run1 = works ? div64(total * (blockIdx.x + 1), n_cta) : 0;
-  TcPos<RT> pos{};
-  if (works) pos = tc_find<RT>(a, p, run0, sums);
+  const int64_t run0 = sm.run[0], run1 = sm.run[1];
+  TcPos<RT> pos{sm.at_l, sm.at[0], sm.at[1], sm.at[2], sm.at[3], sm.at[4]};
   if (RT == 2) asm volatile("griddepcontrol.launch_dependents;");
 
   bool ok = true;
