@@ -127,15 +127,21 @@ k_mass_rows(MassArgs a, int n_cta_max) {
     const int32_t *bt = a.block_table + (int64_t)r * a.max_blocks;
     const uint16_t *kl = a.kpool + (l * a.n_slots * a.H + h) * D;
 
+    // block id of this lane's key, looked up a tile ahead of its copies
+    int32_t blk = 0;
+    auto look = [&](int t) {
+      const int p = t * kTile + warp * KT + lane;
+      if (lane < KT && p < seq) blk = bt[page_of(p, a.bs_inv)];
+    };
     auto issue = [&](int t, int st) {
       const int p0 = t * kTile + warp * KT;
       int32_t slot = -1;
       if (lane < KT && p0 + lane < seq) {
         const int p = p0 + lane;
-        const int32_t b = bt[page_of(p, a.bs_inv)];
-        if (b >= 0 && b < n_blocks) slot = b * a.BS + p - page_of(p, a.bs_inv) * a.BS;
+        if (blk >= 0 && blk < n_blocks) slot = blk * a.BS + p - page_of(p, a.bs_inv) * a.BS;
         else record_error(a.status, KVC_ERR_BOUNDS);
       }
+      look(t + 1);
       const uint32_t ok = __ballot_sync(0xFFFFFFFFu, slot >= 0);
       if (lane == 0) valid_s[st] = ok;
       constexpr int RPI = 32 / CH;
@@ -148,6 +154,7 @@ k_mass_rows(MassArgs a, int n_cta_max) {
                    kl + (int64_t)max(sl, 0) * a.H * D + col * 8, sl >= 0);
       }
     };
+    look(t0);
 #pragma unroll
     for (int s = 0; s < kMrStages - 1; s++) {
       if (t0 + s < t1) issue(t0 + s, s);
