@@ -854,7 +854,8 @@ kvc_status kvc_tail_compact(kvc_bf16 *kpool, kvc_bf16 *vpool, int64_t n_slots, i
  * Errors: KVC_ERR_INVALID_ARG (NULL, sizes < 1, scale not finite),
  * KVC_ERR_SHAPE (D, Hq % H, Hq > 256, block_size > 64, max_tree >
  * KVC_TREE_MAX_NODES, too many positions, mask_words too small),
- * KVC_ERR_ALIGN, KVC_ERR_WORKSPACE.
+ * KVC_ERR_ALIGN (16 bytes; lse 4, so that one layer of an [L][n_q][Hq] buffer can be
+ * passed), KVC_ERR_WORKSPACE.
  * ---------------------------------------------------------------------- */
 size_t kvc_tree_attn_workspace_size(int32_t n_req, int32_t max_blocks, int32_t max_tree,
                                     int32_t H, int32_t Hq, int32_t D, int32_t block_size);

@@ -528,7 +528,7 @@ kvc_status kvc_tree_attn(const kvc_bf16 *q, const kvc_bf16 *kpool, const kvc_bf1
       (tree_mask && mask_words < (max_tree + 31) / 32))
     return KVC_ERR_SHAPE;
   if (!aligned16(q) || !aligned16(kpool) || !aligned16(vpool) || !aligned16(out) ||
-      !aligned16(lse) || !aligned16(ws))
+      reinterpret_cast<uintptr_t>(lse) % 4 != 0 || !aligned16(ws))
     return KVC_ERR_ALIGN;
   if (ws_bytes < kvc_tree_attn_workspace_size(n_req, max_blocks, max_tree, H, Hq, D, block_size))
     return KVC_ERR_WORKSPACE;

@@ -6,8 +6,11 @@
                  in-place compaction
 ``TieredMeanKEvent`` the Mean-K event with the index and the raw history in
                  host memory: score in bounded layer tiles, select, tiered pack
+``TreeDecodeEvent`` a decoding step with drafted trees on a paged cache: tree
+                 attention per layer → commit of the accepted path →
+                 accumulated weight → eviction to a budget
 
-Both only allocate caller-side buffers with torch and call the library's
+All only allocate caller-side buffers with torch and call the library's
 entry points; an event can be captured in a CUDA graph (``capture()``) so
 that its launches replay without host overhead.
 
@@ -32,7 +35,10 @@ from . import (BLOCK_TOKENS, kvc_pack_rerope, kvc_pack_tiered, kvc_pack_tiered_s
                kvc_redirect_free,
                kvc_redirect_free_workspace_size, kvc_rope_table, kvc_score,
                kvc_lrfu_update, kvc_score_qmem, kvc_score_qmem_workspace_size,
-               kvc_score_workspace_size, kvc_select, kvc_tail_compact, kvc_tail_plan)
+               kvc_score_workspace_size, kvc_select, kvc_tail_compact, kvc_tail_plan,
+               kvc_attn_mass, kvc_attn_mass_workspace_size, kvc_mass_evict,
+               kvc_mass_evict_workspace_size, kvc_tree_attn, kvc_tree_attn_workspace_size,
+               kvc_tree_commit)
 
 
 def _dev_i64(x, device) -> torch.Tensor:
@@ -505,6 +511,118 @@ class PagedEvent:
         self.select(stream, self.keep_score if lrfu else None)
         self.plan(seqused, block_table, stream)
         self.compact(kpool, vpool, stream)
+
+
+class TreeDecodeEvent:
+    """Buffers and calls of a decoding step with drafted trees on a paged KV
+    cache that is held to `budget` rows per (layer, KV head).
+
+    A step: the model writes the nodes' keys and values at the positions after
+    each request's cache and calls ``attend`` per layer; once the accepted path
+    is known, ``finish`` commits its rows (kvc_tree_commit), adds their attention
+    weights to ``mass`` (kvc_attn_mass), evicts what exceeds the budget by it
+    (kvc_mass_evict) and carries the lengths over to the next step.  Per request,
+    on the device: ``ctx`` rows held, ``t_end`` tokens seen; ``mass`` and ``pos``
+    (weight and original position per row) are updated in place.  With max_tree 1
+    it is plain decoding.  ``start`` begins with a prefilled cache and ``observe``
+    adds the weights of its last queries (a window, or the whole prompt), so that
+    the first eviction has something to go by.
+
+    The launches depend on the constructor's sizes only, so a step can be captured
+    in a CUDA graph.  ``stream`` None is the current stream; the buffers belong to
+    the stream they are first used on."""
+
+    def __init__(self, n_req: int, max_blocks: int, block_size: int, L: int, H: int, Hq: int,
+                 D: int, n_slots: int, n_q: int, max_tree: int, budget: int, n_sink: int = 0,
+                 n_recent: int = 0, max_path: Optional[int] = None, max_observe: int = 0,
+                 decay: float = 1.0, scale: Optional[float] = None, device="cuda"):
+        self.n_req, self.max_blocks, self.BS = n_req, max_blocks, block_size
+        self.L, self.H, self.Hq, self.D = L, H, Hq, D
+        self.n_slots, self.n_q, self.max_tree = n_slots, n_q, max_tree
+        self.max_path = max_tree if max_path is None else max_path
+        self.budget, self.n_sink, self.n_recent = budget, n_sink, n_recent
+        self.max_observe, self.decay = max_observe, decay
+        self.scale = D ** -0.5 if scale is None else scale
+        dev = self.device = torch.device(device)
+        i32 = dict(dtype=torch.int32, device=dev)
+        cap = max_blocks * block_size
+        self.out = torch.empty(L, n_q, Hq, D, dtype=torch.bfloat16, device=dev)
+        self.lse = torch.empty(L, n_q, Hq, dtype=torch.float32, device=dev)
+        self.mass = torch.zeros(L, n_req, H, cap, dtype=torch.float32, device=dev)
+        self.pos = torch.zeros(L, n_req, H, cap, **i32)
+        self.ctx = torch.zeros(n_req, **i32)
+        self.t_end = torch.zeros(n_req, **i32)
+        self.n_mass = torch.zeros(n_req, **i32)
+        self.n_pos = torch.zeros(n_req, **i32)
+        self.seq = torch.zeros(n_req, **i32)
+        self.n_out = torch.zeros(n_req, **i32)
+        self.row_idx = torch.zeros(n_req, self.max_path, **i32)
+        self.row_vis = torch.zeros(n_req, self.max_path, **i32)
+        self.row_off = torch.arange(n_req + 1, **i32) * self.max_path
+        rows = max(self.max_path, max_observe)
+        self.ws = _ws(max(
+            kvc_tree_attn_workspace_size(n_req, max_blocks, max_tree, H, Hq, D, block_size),
+            kvc_attn_mass_workspace_size(n_req, max_blocks, rows, L, H, Hq, D, block_size),
+            kvc_mass_evict_workspace_size(n_req, max_blocks, L, H, block_size, budget)), dev)
+        self.dev_status = torch.zeros(1, **i32)
+
+    def start(self, ctx):
+        """A cache of ctx[r] rows per request, the first tokens of its request."""
+        self.ctx.copy_(ctx)
+        self.t_end.copy_(ctx)
+        self.n_mass.zero_()
+        self.n_pos.zero_()
+
+    def observe(self, q, lse, row_vis, row_off, kpool, block_table, stream=None):
+        """Adds the weights of queries q [L][n][Hq][D] with the given LSE (requests
+        one after another, row_off) to the cached rows they see."""
+        n = q.shape[1]
+        kvc_attn_mass(q, lse, n, None, row_vis, row_off, n, self.max_observe, kpool,
+                      self.n_slots, block_table, self.max_blocks, self.ctx, self.n_mass,
+                      self.n_req, self.L, self.H, self.Hq, self.D, self.BS, self.scale,
+                      self.decay, self.mass, self.ws, self.dev_status, stream)
+        with torch.cuda.stream(stream):
+            self.n_mass.copy_(self.ctx)
+
+    def attend(self, layer, q, kpool, vpool, block_table, q_off, tree_mask=None, stream=None):
+        """One layer's attention: q [n_q][Hq][D], the layer's pools; out[layer] and
+        lse[layer] are written.  tree_mask None: chains."""
+        words = 0 if tree_mask is None else tree_mask.shape[1]
+        kvc_tree_attn(q, kpool, vpool, self.n_slots, block_table, self.max_blocks, self.ctx,
+                      q_off, tree_mask, words, self.n_req, self.n_q, self.max_tree, self.H,
+                      self.Hq, self.D, self.BS, self.scale, self.out[layer], self.lse[layer],
+                      self.ws, self.dev_status, stream)
+        return self.out[layer]
+
+    def commit(self, kpool, vpool, block_table, q_off, path, n_path, stream=None):
+        kvc_tree_commit(kpool, vpool, self.n_slots, block_table, self.max_blocks, self.ctx,
+                        q_off, path, n_path, self.max_path, self.n_req, self.L, self.H, self.D,
+                        self.BS, self.seq, self.row_idx, self.row_vis, self.dev_status, stream)
+
+    def accumulate(self, q, kpool, block_table, stream=None):
+        """Weights of the committed rows; q [L][n_q][Hq][D] are the step's queries."""
+        kvc_attn_mass(q, self.lse, self.n_q, self.row_idx, self.row_vis, self.row_off,
+                      self.n_req * self.max_path, self.max_path, kpool, self.n_slots,
+                      block_table, self.max_blocks, self.seq, self.n_mass, self.n_req, self.L,
+                      self.H, self.Hq, self.D, self.BS, self.scale, self.decay, self.mass,
+                      self.ws, self.dev_status, stream)
+
+    def evict(self, kpool, vpool, block_table, stream=None):
+        kvc_mass_evict(kpool, vpool, self.n_slots, block_table, self.max_blocks, self.seq,
+                       self.n_pos, self.t_end, self.mass, self.pos, self.mass, self.pos,
+                       self.n_out, self.n_req, self.L, self.H, self.D, self.BS, self.budget,
+                       self.n_sink, self.n_recent, self.ws, self.dev_status, stream)
+
+    def finish(self, q, kpool, vpool, block_table, q_off, path, n_path, stream=None):
+        """The step after the last layer, on the path accepted from its outputs."""
+        self.commit(kpool, vpool, block_table, q_off, path, n_path, stream)
+        self.accumulate(q, kpool, block_table, stream)
+        with torch.cuda.stream(stream):
+            self.t_end.add_(self.seq).sub_(self.ctx)
+        self.evict(kpool, vpool, block_table, stream)
+        with torch.cuda.stream(stream):
+            for n in (self.ctx, self.n_mass, self.n_pos):
+                n.copy_(self.n_out)
 
 
 def paged_bytes(n_req: int, seq: int, L: int, H: int, Hq: int, D: int, n_pairs: int) -> dict:
