@@ -1403,7 +1403,9 @@ k_tree_join(TreeArgs a) {
   }
 }
 
-// Rows up to which the narrow instruction is used.
+// Rows up to which the narrow instruction is used.  Both sides, 64 requests of
+// 8K: 4 rows 251 us here and 294 on the tensor cores, 16 rows 256 and 304, 32
+// rows 294 and 310; 128K of one request, 32 rows 100 and 103.
 constexpr int kRowsMax = 32;
 constexpr int kTcRowsMax = 256;
 
