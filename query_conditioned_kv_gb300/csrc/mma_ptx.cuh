@@ -142,6 +142,24 @@ inline uint32_t page_inverse(int BS) {
   return BS == 1 ? 0u : (uint32_t)(((1ull << 32) + BS - 1) / BS);
 }
 
+// Another CTA's shared memory (addr from mapa).
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+               : "=f"(v.x), "=f"(v.y)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
 // Maximum over the CTA (a multiple of 32 threads); every thread gets it.  sh: 32
 // words of scratch, free again on return.
 __device__ __forceinline__ int64_t block_max(int64_t v, int64_t *sh) {

@@ -107,8 +107,10 @@ struct RowSmem {
   static constexpr int kQ = kRing;                       // MT·16 rows of q
   static constexpr int kValid = kQ + MT * 16 * D * 2;  // valid keys per (warp, stage)
   static constexpr int kMl = kValid + kRowWarps * kRowStages * 4;  // (max, sum) per (warp, row)
-  static constexpr int kBytes = kMl + kRowWarps * MT * 16 * 8;
-  static_assert(kRowWarps * MT * 16 * D * 4 <= kRing, "the warps' O fits the ring");
+  static constexpr int kClMl = kMl + kRowWarps * MT * 16 * 8;      // (max, sum) of the CTA, per row
+  static constexpr int kBytes = kClMl + MT * 16 * 8;
+  static constexpr int kClO = kRowWarps * MT * 16 * D * 4;  // the CTA's O, behind the warps'
+  static_assert(kClO + MT * 16 * D * 4 <= kRing, "the warps' and the CTA's O fit the ring");
 };
 
 // Bits k < KT of the keys p0 + k that row `i` (node) of the request sees.
@@ -137,7 +139,7 @@ __device__ __forceinline__ uint32_t visible_bits(const TreeArgs &a, int i, int q
   return bits & full;
 }
 
-template <int D, int MT>
+template <int D, int MT, bool CL>
 __global__ void __launch_bounds__(kRowThreads, 2)
 k_tree_rows(TreeArgs a) {
   using S = RowSmem<D, MT>;
@@ -150,31 +152,42 @@ k_tree_rows(TreeArgs a) {
   const uint32_t qbase = smem_u32(sm + S::kQ);
   float2 *ml_s = reinterpret_cast<float2 *>(sm + S::kMl);
 
-  asm volatile("griddepcontrol.launch_dependents;");
-  if (blockIdx.x == 0)  // one report per bad request
-    for (int r = tid; r < a.n_req; r += kRowThreads) {
-      int c, q0, T;
-      if (!tree_request(a, r, c, q0, T)) record_error(a.status, KVC_ERR_BOUNDS);
-    }
-  auto tiles = [&](int x) { return request_tiles(a, x); };
-  const WarpSums sums = warp_sums(a.n_req, tiles);
-  const int64_t total = sums.total;
-  int64_t before;
-  const int n_cta = (int)min((int64_t)a.n_cta, total);  // every run holds a tile
-  if ((int)blockIdx.x >= n_cta) return;
-  const int64_t run0 = run_start(total, n_cta, blockIdx.x);
-  const int64_t run1 = run_start(total, n_cta, blockIdx.x + 1);
-  int r;
-  warp_find(sums, a.n_req, run0, tiles, r, before);
-
+  int r, c, q0, T, n_rt, n_kt, unit, t0;
+  int64_t g, run0, run1;  // next tile of the run, its begin and end
+  if constexpr (CL) {
+    const int S = (int)cluster_nrank(), rank = (int)cluster_rank(), u = blockIdx.x / S;
+    r = u / a.H;
+    unit = u % a.H;
+    const bool valid = tree_request(a, r, c, q0, T);
+    if (!valid && unit == 0 && rank == 0 && tid == 0) record_error(a.status, KVC_ERR_BOUNDS);
+    tree_tiles(a, r, n_rt, n_kt);
+    if (n_rt == 0) return;  // (the whole cluster)
+    t0 = n_kt * rank / S;
+    g = run0 = 0;
+    run1 = n_kt * (rank + 1) / S - t0;
+  } else {
+    asm volatile("griddepcontrol.launch_dependents;");
+    if (blockIdx.x == 0)  // one report per bad request
+      for (int r = tid; r < a.n_req; r += kRowThreads) {
+        int c, q0, T;
+        if (!tree_request(a, r, c, q0, T)) record_error(a.status, KVC_ERR_BOUNDS);
+      }
+    auto tiles = [&](int x) { return request_tiles(a, x); };
+    const WarpSums sums = warp_sums(a.n_req, tiles);
+    const int64_t total = sums.total;
+    int64_t before;
+    const int n_cta = (int)min((int64_t)a.n_cta, total);  // every run holds a tile
+    if ((int)blockIdx.x >= n_cta) return;
+    run0 = g = run_start(total, n_cta, blockIdx.x);
+    run1 = run_start(total, n_cta, blockIdx.x + 1);
+    warp_find(sums, a.n_req, run0, tiles, r, before);
+    tree_request(a, r, c, q0, T);
+    tree_tiles(a, r, n_rt, n_kt);
+    unit = (int)div64(g - before, n_kt);  // h·n_rt + row tile
+    t0 = (int)(g - before - (int64_t)unit * n_kt);
+  }
   const int64_t n_blocks = a.n_slots / a.BS;
-  int64_t g = run0;  // next tile of the run
-  int c, q0, T, n_rt, n_kt;
-  tree_request(a, r, c, q0, T);
-  tree_tiles(a, r, n_rt, n_kt);
-  int unit = (int)div64(g - before, n_kt);  // h·n_rt + row tile
-  int t0 = (int)(g - before - (int64_t)unit * n_kt);
-  while (g < run1) {
+  while (CL || g < run1) {
     const int h = unit / n_rt, rt = unit % n_rt;
     const int t1 = (int)min((int64_t)n_kt, t0 + (run1 - g));
     const int n_rows = min(a.rstep, T * a.G - rt * a.rstep);
@@ -411,7 +424,7 @@ k_tree_rows(TreeArgs a) {
               make_float2(o[mt][n][hf * 2], o[mt][n][hf * 2 + 1]);
       }
     __syncthreads();
-    const bool whole = t0 == 0 && t1 == n_kt;
+    const bool whole = !CL && t0 == 0 && t1 == n_kt;
     const int64_t slot = 2 * (int64_t)blockIdx.x + (g != run0);
     for (int e = tid; e < n_rows * (D / 4); e += kRowThreads) {
       const int row = e / (D / 4), d4 = (e % (D / 4)) * 4;
@@ -441,10 +454,50 @@ k_tree_rows(TreeArgs a) {
         uint2 w2 = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
         *reinterpret_cast<uint2 *>(a.out + qr * D + d4) = w2;
         if (d4 == 0) a.lse[qr] = mx == -INFINITY ? -INFINITY : (mx + log2f(sum)) * kLn2;
+      } else if (CL) {
+        *reinterpret_cast<float4 *>(sm + S::kClO + (row * D + d4) * 4) = acc;
+        if (d4 == 0) reinterpret_cast<float2 *>(sm + S::kClMl)[row] = make_float2(mx, sum);
       } else {
         *reinterpret_cast<float4 *>(a.part_o + (slot * R + row) * D + d4) = acc;
         if (d4 == 0) a.part_ml[slot * R + row] = make_float2(mx, sum);
       }
+    }
+    if constexpr (CL) {
+      // the cluster's CTAs hold the unit's parts: added up in order, the elements
+      // dealt out to all of them
+      __syncwarp();
+      cluster_sync_all();
+      const int n_cl = (int)cluster_nrank();
+      const uint32_t o_at = smem_u32(sm + S::kClO), ml_at = smem_u32(sm + S::kClMl);
+      for (int e = (int)cluster_rank() * kRowThreads + tid; e < n_rows * (D / 4);
+           e += n_cl * kRowThreads) {
+        const int row = e / (D / 4), d4 = (e % (D / 4)) * 4;
+        float mx = -INFINITY;
+#pragma unroll 4
+        for (int k = 0; k < n_cl; k++) mx = fmaxf(mx, ld_cluster_f2(mapa_u32(ml_at + row * 8, k)).x);
+        float sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = 0; k < n_cl; k++) {
+          const float2 ml = ld_cluster_f2(mapa_u32(ml_at + row * 8, k));
+          const float4 v = ld_cluster_f4(mapa_u32(o_at + (row * D + d4) * 4, k));
+          const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mx);
+          sum = fmaf(ml.y, f, sum);
+          acc.x = fmaf(v.x, f, acc.x);
+          acc.y = fmaf(v.y, f, acc.y);
+          acc.z = fmaf(v.z, f, acc.z);
+          acc.w = fmaf(v.w, f, acc.w);
+        }
+        const int x = rt * a.rstep + row;
+        const int64_t qr = (int64_t)(q0 + x / a.G) * a.Hq + h * a.G + x % a.G;
+        const float inv = mx == -INFINITY ? 0.f : 1.f / sum;
+        *reinterpret_cast<uint2 *>(a.out + qr * D + d4) =
+            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        if (d4 == 0) a.lse[qr] = mx == -INFINITY ? -INFINITY : (mx + log2f(sum)) * kLn2;
+      }
+      __syncwarp();
+      cluster_sync_all();  // (no CTA leaves while another reads its part)
+      return;
     }
     g += n_t;
     t0 = 0;
@@ -1453,14 +1506,54 @@ cudaError_t launch_tc(const TreeArgs &a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+// CTAs of the cluster that shares a unit, 0: the tiles are dealt out and joined.
+// In tiles that a CTA takes one after another: dealing out costs an even share
+// and about 17 (the join's launch and dependent loads, a second start, neighbour
+// heads read at different times); a cluster its share for every wave of CTAs
+// (clusters of few tiles want one wave; 16 CTAs leave some SMs empty) and 3.5.  One
+// token, 8 KV heads, 1 request: 4K 10.8 us by clusters of 16 and 12.6 dealt out,
+// 16K 21.7 and 17.4; 4 requests of 4K 14.6 (clusters of 8) and 18.3; 32 of 8K
+// 145 (clusters of two) and 133; 24 of 6K, 16 heads of D 64, 92 (of two) and 109.
+int tree_cluster(const TreeArgs &a) {
+  const double units = (double)a.n_req * a.H, sms = device_sm_count();
+  const double kt = ceil((double)a.max_blocks * a.BS / a.tile);
+  int best = 0;
+  double least = units * kt / (2 * sms) + 17;
+  for (int S = 1; S <= 16 && S <= kt; S *= 2) {
+    // (two CTAs per SM; a GPC's 16 to 20 SMs hold fewer large clusters)
+    const double room = S == 16 ? 0.85 * sms : S == 8 ? 1.69 * sms : S == 4 ? 1.9 * sms : 2 * sms;
+    const double waves = ceil(units * S / room);
+    if (waves > 1 && S > 1 && kt / S < 24) break;
+    const double cost = waves * ceil(kt / S) * (S == 16 ? 1.25 : 1) + 3.5;
+    if (cost < least) {
+      least = cost;
+      best = S;
+    }
+  }
+  return units * best <= INT32_MAX ? best : 0;
+}
+
 template <int D, int MT>
-cudaError_t launch_rows(const TreeArgs &a, cudaStream_t s) {
+cudaError_t launch_rows(const TreeArgs &a, int cluster, cudaStream_t s) {
   constexpr int smem = RowSmem<D, MT>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(k_tree_rows<D, MT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  auto *kern = cluster ? k_tree_rows<D, MT, true> : k_tree_rows<D, MT, false>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess && cluster > 8)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
-  k_tree_rows<D, MT><<<a.n_cta, kRowThreads, smem, s>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cluster ? (unsigned)(a.n_req * a.H * cluster) : (unsigned)a.n_cta);
+  cfg.blockDim = dim3(kRowThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)cluster;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 }  // namespace
@@ -1506,12 +1599,13 @@ cudaError_t launch_tree_attn(const uint16_t *q, const uint16_t *kpool, const uin
   a.part_o = reinterpret_cast<float *>(ws);
   a.part_ml = reinterpret_cast<float2 *>(a.part_o + (size_t)2 * a.n_cta * a.rows * D);
   cudaError_t e;
-  if (a.tile == kTtKeys && max_tree * a.G > kRowsMax)
+  const int cluster = max_tree * a.G > kRowsMax ? 0 : tree_cluster(a);
+  if (max_tree * a.G > kRowsMax)
     e = D == 128 ? launch_tc<128>(a, s) : launch_tc<64>(a, s);
   else
-    e = D == 128 ? (a.rows == 16 ? launch_rows<128, 1>(a, s) : launch_rows<128, 2>(a, s))
-                 : (a.rows == 16 ? launch_rows<64, 1>(a, s) : launch_rows<64, 2>(a, s));
-  if (e != cudaSuccess) return e;
+    e = D == 128 ? (a.rows == 16 ? launch_rows<128, 1>(a, cluster, s) : launch_rows<128, 2>(a, cluster, s))
+                 : (a.rows == 16 ? launch_rows<64, 1>(a, cluster, s) : launch_rows<64, 2>(a, cluster, s));
+  if (e != cudaSuccess || cluster) return e;
   // four warps a row where a unit is cut into many parts
   const bool many = a.n_cta >= 6 * (int64_t)n_req * H * max_rt;
   auto *join = D == 128 ? (many ? k_tree_join<128, 4> : k_tree_join<128, 1>)
