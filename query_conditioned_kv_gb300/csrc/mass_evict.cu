@@ -18,6 +18,12 @@
 // before a leaving row's weight is overwritten lets mass_out/pos_out be
 // mass/pos.  After the first radix level only the keys in its digit are looked
 // at (a list in shared memory), and the levels end once all of them stay.
+//
+// Bound: few rows leave, latency (64 of 4160 rows, 288 segments: 18.5 us, 2 TB/s;
+// sizes, weights, levels, sweep, block ids and rows wait for one another, 18
+// thousand cycles); many, random 256-byte pieces read and written (6K to 4K, 1152
+// segments: 206 to 220 us, 72 to 77 % of a plain copy's rate; 512 threads a CTA
+// 240 us, eight rows in flight a warp slower than four).
 #include <algorithm>
 
 #include "kvc_internal.cuh"

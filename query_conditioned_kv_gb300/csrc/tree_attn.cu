@@ -15,7 +15,9 @@
 // holds all of a unit writes its result; otherwise it writes a partial
 // (max, sum, unnormalised O in fp32) to the workspace, at most two per CTA,
 // and k_tree_join adds a unit's partials in order.  No atomics: the result
-// does not depend on timing.
+// does not depend on timing.  Where requests are short, a cluster of up to 16
+// CTAs takes a unit instead and joins its parts from one another's shared
+// memory: one launch, and no search for the run (tree_cluster says when).
 //
 // k_tree_rows (up to 32 rows a tile): each of a CTA's four warps streams its
 // own quarter of every tile through a private cp.async ring (3 stages of
@@ -24,7 +26,9 @@
 // products are mma.sync m16n8k16 with fp32 accumulators: at 16 rows the
 // tensor work per key is a few per cent of the time its bytes take, so the
 // narrow instruction, which needs no shared-memory round trip for the
-// weights, is enough.
+// weights, is enough.  Measured: one token of 64 requests, 4K to 8K, 8 KV heads,
+// D 128: 250 us, 6.45 TB/s, 96 % of a plain copy's rate; one request of 4K 12 us,
+// of which launch and the chain sizes → block ids → rows → join are all but 3.
 #include <math.h>
 
 #include <algorithm>
@@ -547,6 +551,12 @@ k_tree_rows(TreeArgs a) {
 // have about a tile's time to arrive.  The barriers are per kind, not per
 // slot: a barrier's parity tells only two uses apart, and two consumers of one
 // ring may be further apart than that.
+//
+// Bound: with 128 rows the K and V stream (128K of one request, 108 us, 5.0
+// TB/s); with 256 the products, about 105 cycles an instruction at N = 128 where
+// N = 256 would take 126 (tensor memory holds S 256 + O 256 columns, so S of 256
+// columns could not be worked on while the next is made): 64 nodes × 4 heads, 16
+// requests of 16K to 32K, 415 us, 745 TFLOP/s and 3.9 TB/s.
 
 constexpr int kTtKeys = 128;
 constexpr int kTtSoft = 8;

