@@ -19,8 +19,8 @@
 // mass/pos.  After the first radix level only the keys in its digit are looked
 // at (a list in shared memory), and the levels end once all of them stay.
 //
-// Bound: few rows leave, latency (64 of 4160 rows, 288 segments: 18.5 us, 2 TB/s;
-// sizes, weights, levels, sweep, block ids and rows wait for one another, 18
+// Bound: few rows leave, latency (64 of 4160 rows, 288 segments: 16.5 us, 2.3 TB/s;
+// weights, levels, sweep, block ids and rows wait for one another, about 15
 // thousand cycles); many, random 256-byte pieces read and written (6K to 4K, 1152
 // segments: 206 to 220 us, 72 to 77 % of a plain copy's rate; 512 threads a CTA
 // 240 us, eight rows in flight a warp slower than four).
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(NT)
 k_mass_evict(EvictArgs a) {
   extern __shared__ uint32_t dyn[];  // keys [kp(cap)], then the two lists in their place
   __shared__ uint32_t hist[kSelHist * 256];
-  __shared__ uint32_t s_red[2][32], warp_tot[32];
+  __shared__ uint32_t warp_tot[32];
   __shared__ uint32_t s_kmax, s_kmin, s_prefix, s_need, s_have, n_list;
   __shared__ uint32_t list[STAGED ? kEvList : 1];
 
@@ -80,9 +80,30 @@ k_mass_evict(EvictArgs a) {
   const int h = seg % a.H, r = (seg / a.H) % a.n_req;
   const int64_t l = seg / (a.H * a.n_req);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // a thread's first rows, asked for together with the sizes (any row below cap
+  // may be read); the block ids on their way to L1, and the first level's
+  // histogram cleared, meanwhile
+  constexpr int U1 = 10;
+  const int64_t base = (int64_t)seg * a.cap;
+  float m[U1];
+  int o[U1];
+#pragma unroll
+  for (int u = 0; u < U1; u++) {
+    const int i = u * NT + tid;
+    m[u] = i < a.cap ? a.mass[base + i] : 0.f;
+    o[u] = i < a.cap ? a.pos[base + i] : 0;
+  }
+  const int32_t *bt = a.block_table + (int64_t)r * a.max_blocks;
+  for (int i = 32 * tid; i < a.max_blocks; i += 32 * NT)
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(bt + i));
+  for (int j = tid; j < kSelHist * 256; j += NT) hist[j] = 0u;
+  if (tid == 0) {
+    s_kmax = 0u;
+    s_kmin = 0xFFFFFFFFu;
+  }
+  __syncthreads();
   const int n = a.seqused[r], B = a.budget;
   const bool bad = n < 0 || n > a.cap;
-  const int64_t base = (int64_t)seg * a.cap;
   float *mass_out = a.mass_out + base;
   int32_t *pos_out = a.pos_out + base;
   Row row;
@@ -112,20 +133,12 @@ k_mass_evict(EvictArgs a) {
   // rows below B keep their place (the ones that leave are overwritten below);
   // in place, rewriting a weight changes nothing
   const bool writes = rank == 0 && (a.mass_out != a.mass || a.pos_out != a.pos || row.n_pos < B);
-  constexpr int U1 = 8;
-  for (int b0 = 0; b0 < n; b0 += NT * U1) {
-    float m[U1];
-    int o[U1];
-#pragma unroll
-    for (int u = 0; u < U1; u++) {
-      const int i = b0 + u * NT + tid;
-      m[u] = i < n ? row.mass[i] : 0.f;
-      o[u] = i < n ? row.origin(i) : 0;
-    }
+  for (int b0 = 0;;) {
 #pragma unroll
     for (int u = 0; u < U1; u++) {
       const int i = b0 + u * NT + tid;
       if (i < n) {
+        if (i >= row.n_pos) o[u] = row.t_end - (n - i);
         const uint32_t key = row.key(m[u], o[u], nan);
         if (STAGED) keys[kp(i)] = key;
         kmax = max(kmax, key);
@@ -136,23 +149,21 @@ k_mass_evict(EvictArgs a) {
         }
       }
     }
+    b0 += NT * U1;
+    if (b0 >= n) break;
+#pragma unroll
+    for (int u = 0; u < U1; u++) {
+      const int i = b0 + u * NT + tid;
+      m[u] = i < n ? row.mass[i] : 0.f;
+      o[u] = i < row.n_pos ? row.pos[i] : 0;
+    }
   }
   if (nan) record_error(a.status, KVC_ERR_NAN);
   kmax = __reduce_max_sync(0xFFFFFFFFu, kmax);
   kmin = __reduce_min_sync(0xFFFFFFFFu, kmin);
   if (lane == 0) {
-    s_red[0][warp] = kmax;
-    s_red[1][warp] = kmin;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    const uint32_t mx = __reduce_max_sync(0xFFFFFFFFu, lane < NT / 32 ? s_red[0][lane] : 0u);
-    const uint32_t mn =
-        __reduce_min_sync(0xFFFFFFFFu, lane < NT / 32 ? s_red[1][lane] : 0xFFFFFFFFu);
-    if (lane == 0) {
-      s_kmax = mx;
-      s_kmin = mn;
-    }
+    atomicMax(&s_kmax, kmax);
+    atomicMin(&s_kmin, kmin);
   }
   __syncthreads();
   kmax = s_kmax;
@@ -163,14 +174,16 @@ k_mass_evict(EvictArgs a) {
   int hi = kmax == kmin ? -1 : 31 - __clz(kmax ^ kmin);
   uint32_t prefix = hi < 0 ? kmax : hi == 31 ? 0u : (kmax >> (hi + 1)) << (hi + 1);
   uint32_t have = (uint32_t)n;  // keys with the prefix
-  bool listed = false;
+  bool listed = false, clear = true;  // (the histogram is)
   while (hi >= 0 && have > need) {
     const int lo = hi >= 7 ? hi - 7 : 0;
     const uint32_t dmask = (2u << (hi - lo)) - 1u;
     const uint32_t pmask = hi == 31 ? 0u : ~((2u << hi) - 1u);
     uint32_t *hw = hist + (warp % kSelHist) * 256;
-    for (int j = tid; j < kSelHist * 256; j += NT) hist[j] = 0u;
+    if (!clear)
+      for (int j = tid; j < kSelHist * 256; j += NT) hist[j] = 0u;
     __syncthreads();
+    clear = false;
     if (listed) {
       for (int i = tid; i < (int)n_list; i += NT)
         if ((list[i] & pmask) == prefix) atomicAdd(&hw[(list[i] >> lo) & dmask], 1u);
@@ -278,12 +291,15 @@ k_mass_evict(EvictArgs a) {
   else __syncthreads();
   const int n_pairs = (int)tail_carry;  // = hole_carry
 
-  if (rank == 0)
-    for (int k = tid; k < n_pairs; k += NT) {
-      const int d = holes[k], s = tails[k];
-      mass_out[d] = row.mass[s];
-      pos_out[d] = row.origin(s);
-    }
+  // the moved rows' weights and positions, by the threads whose rows below come last
+  const int k_mine = NT - 1 - tid;
+  float m_moved = 0.f;
+  int o_moved = 0;
+  const bool moves = rank == 0 && k_mine < n_pairs;
+  if (moves) {
+    m_moved = row.mass[tails[k_mine]];
+    o_moved = row.origin(tails[k_mine]);
+  }
 
   // K and V rows: 16-byte columns, a warp takes pairs in turn
   const int cols = a.D / 8;          // columns of one row: 8 or 16
@@ -291,7 +307,6 @@ k_mass_evict(EvictArgs a) {
   const int sub = lane / (2 * cols), c2 = lane % (2 * cols);
   uint16_t *pool = (c2 < cols ? a.kpool : a.vpool) + l * a.n_slots * a.H * a.D + h * a.D +
                    (c2 % cols) * 8;
-  const int32_t *bt = a.block_table + (int64_t)r * a.max_blocks;
   const int64_t n_blocks = a.n_slots / a.BS, stride = (int64_t)a.H * a.D;
   const int step = (NT / 32) * S * per;
   constexpr int U = 4;
@@ -318,6 +333,17 @@ k_mass_evict(EvictArgs a) {
     for (int u = 0; u < U; u++)
       if (d[u] >= 0) st_stream(pool + d[u], v[u]);
   }
+
+  if (moves) {
+    mass_out[holes[k_mine]] = m_moved;
+    pos_out[holes[k_mine]] = o_moved;
+  }
+  if (rank == 0)
+    for (int k = k_mine + NT; k < n_pairs; k += NT) {
+      const int d = holes[k], s = tails[k];
+      mass_out[d] = row.mass[s];
+      pos_out[d] = row.origin(s);
+    }
 }
 
 }  // namespace
