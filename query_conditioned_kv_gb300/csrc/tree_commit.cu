@@ -6,13 +6,15 @@
 // position c + a_i → c + i.  Since a is ascending, a_i ≥ i and every later
 // source a_j (j > i) is above i: a thread that owns one 16-byte column and
 // walks i upwards never overwrites a row it still has to read, also when it
-// reads eight rows ahead of the first write.  So one pass over the rows, no
+// reads four rows ahead of the first write.  So one pass over the rows, no
 // scratch, and the columns are independent.
 //
 // What bounds it: latency.  A path of 8 rows of 2 KB (8 KV heads, D 128) is
-// 64 KB of traffic a layer; a CTA reads all its rows of a layer before it writes
-// the first.  Measured: 36 layers, 8 KV heads, D 128: one path of 5 nodes 7.6 us
-// with the call, 64 paths of up to 8 nodes 16.7 us, 4 TB/s.
+// 64 KB of traffic a layer; a thread reads four rows before it writes the first
+// (eight take the registers of two more CTAs per SM: 12.0 us against 10.4 for 64
+// paths whose rows are in L2, the same otherwise).  Measured: 36 layers, 8 KV
+// heads, D 128: one path of 5 nodes 7.8 us with the call, 64 paths of up to 8
+// nodes 16.8 us, 4 TB/s.
 #include <algorithm>
 
 #include "kvc_internal.cuh"
@@ -22,7 +24,7 @@ namespace kvc {
 namespace {
 
 constexpr int kCommitThreads = 256;
-constexpr int kCommitAhead = 8;  // rows read before the first of them is written
+constexpr int kCommitAhead = 4;  // rows read before the first of them is written
 
 struct CommitArgs {
   uint16_t *kpool, *vpool;      // [L][n_slots][H][D]
@@ -35,7 +37,7 @@ struct CommitArgs {
   uint32_t bs_inv;                          // page_inverse(BS)
 };
 
-__global__ void __launch_bounds__(kCommitThreads)
+__global__ void __launch_bounds__(kCommitThreads, 6)
 k_tree_commit(CommitArgs a) {
   extern __shared__ int32_t s_slot[];  // [2][max_path]: source, destination (−1: no copy)
   const int r = blockIdx.x, tid = threadIdx.x;
@@ -110,9 +112,9 @@ cudaError_t launch_tree_commit(uint16_t *kpool, uint16_t *vpool, int64_t n_slots
   CommitArgs a{kpool,   vpool,   block_table, ctx_len, q_off, path,       n_path,
                seq_out, row_idx, row_vis,     status,  n_slots, max_blocks, max_path,
                H * D,   BS};
-  // one CTA a layer until the GPU is full (4 CTAs of 256 threads an SM), then several
+  // one CTA a layer until the GPU is full (6 CTAs of 256 threads an SM), then several
   // layers a CTA, which share the lookups
-  const int64_t full = 4 * (int64_t)device_sm_count();
+  const int64_t full = 6 * (int64_t)device_sm_count();
   a.L = L;
   a.layers = (int)std::min<int64_t>(L, ((int64_t)n_req * L + full - 1) / full);
   a.bs_inv = page_inverse(BS);
