@@ -9,7 +9,8 @@
 // the group) the N dimension: each thread then holds weights of its own keys
 // and adds them up in registers, so the sum over rows costs no exchange
 // beyond one step across four lanes, and every position is owned by one
-// warp: no atomics, no partial sums in memory.
+// warp: no atomics, and partial sums in memory only where a request has more
+// rows than one row tile holds.
 //
 // k_mass_rows (few rows): bound by the stream of K, 2·D bytes per key.  All
 // key tiles of all (layer, request, KV head) units, in order, are dealt out

@@ -561,7 +561,9 @@ k_tree_rows(TreeArgs a) {
 constexpr int kTtKeys = 128;
 constexpr int kTtSoft = 8;
 constexpr int kTtThreads = (kTtSoft + 8) * 32;  // (two warps fill the last warpgroup)
-constexpr int kTtMore = 168, kTtLess = 88;  // registers of a softmax thread, of the others
+// Registers of a softmax thread, of the others (64 nodes, 16 requests: 420 us; 168
+// and 88 423, 184 and 72 419 but 3 % slower with 128 rows, 160 and 96 426).
+constexpr int kTtMore = 176, kTtLess = 80;
 constexpr float kUnset = -1e30f;   // reference of a row that has seen nothing
 constexpr float kExceed = 30.f;    // log2 of how far a logit may pass the reference
 
