@@ -326,9 +326,13 @@ cudaError_t launch_rows(const MassArgs &a, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(k_mass_rows<D, NT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  int per_sm = 0;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k_mass_rows<D, NT>, kMrThreads, smem);
-  if (e != cudaSuccess) return e;
+  static int per_sm = 0;  // (a property of the kernel; the query takes as long as a launch)
+  if (!per_sm) {
+    int n = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k_mass_rows<D, NT>, kMrThreads, smem);
+    if (e != cudaSuccess) return e;
+    per_sm = n;
+  }
   constexpr int tile = kMrWarps * 2048 / D;
   const int64_t most = (int64_t)a.L * a.n_req * a.H * ((a.cap + tile - 1) / tile);
   const int n_cta = (int)std::min<int64_t>((int64_t)std::min(per_sm, 3) * device_sm_count(), most);
