@@ -1521,11 +1521,11 @@ cudaError_t launch_tc(const TreeArgs &a, cudaStream_t s) {
 // CTAs of the cluster that shares a unit, 0: the tiles are dealt out and joined.
 // In tiles that a CTA takes one after another: dealing out costs an even share
 // and about 17 (the join's launch and dependent loads, a second start); a cluster
-// its share for every wave of CTAs
-// (clusters of few tiles want one wave; 16 CTAs leave some SMs empty) and 3.5.  One
-// token, 8 KV heads, 1 request: 4K 10.8 us by clusters of 16 and 12.6 dealt out,
-// 16K 21.7 and 17.4; 4 requests of 4K 14.6 (clusters of 8) and 18.3; 32 of 8K
-// 145 (clusters of two) and 133; 24 of 6K, 16 heads of D 64, 92 (of two) and 109.
+// its share for every wave of CTAs (clusters of few tiles want one wave; 16 CTAs
+// leave some SMs empty) and 3.5.  One token, 8 KV heads, 1 request: 4K 10.8 us by
+// clusters of 16 and 12.6 dealt out, 16K 21.7 and 17.4; 4 requests of 4K 14.6
+// (clusters of 8) and 18.3; 32 of 8K 145 (clusters of two) and 133; 24 of 6K, 16
+// heads of D 64, 92 (of two) and 109.
 int tree_cluster(const TreeArgs &a) {
   const double units = (double)a.n_req * a.H, sms = device_sm_count();
   const double kt = ceil((double)a.max_blocks * a.BS / a.tile);
