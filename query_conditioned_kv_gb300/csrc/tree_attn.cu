@@ -29,6 +29,7 @@
 // weights, is enough.  Measured: one token of 64 requests, 4K to 8K, 8 KV heads,
 // D 128: 250 us, 6.45 TB/s, 96 % of a plain copy's rate; one request of 4K 12 us,
 // of which launch and the chain sizes → block ids → rows → join are all but 3.
+#include <float.h>
 #include <math.h>
 
 #include <algorithm>
@@ -539,9 +540,14 @@ k_tree_rows(TreeArgs a) {
 // fp32's exponents), and the result does not depend on the reference.  A job
 // is worked out on the references at hand; a vote of the warpgroup (one
 // barrier) then passes it on, or raises the references, rescales O in tensor
-// memory and works the job out again.  A tile that holds nodes, or the end,
-// first gets −inf written into Sᵀ where a row does not see a key, so the loop
-// over the tiles has no masks.
+// memory and works the job out again.  Once is enough: the reference is the largest
+// rounded product S·zscale, and a logit taken as fma(S, zscale, −reference) passes
+// it, or the largest falls short of it, by half a step of the reference at most:
+// less than 1 below 2^24.  From there on (kRoundFrom) half a step may be hundreds.
+// Then every job of the run raises the references first and writes the differences
+// of the rounded products to them into Sᵀ, where the largest is 0.  A tile that
+// holds nodes, or the end, first gets −inf written into Sᵀ where a row does not see
+// a key, so the loop over the tiles has no masks.
 //
 // Warps: 0–7 softmax; 8–11 load K and V, 32 keys of a tile each (8 the queries
 // too): TMA boxes of whole page rows, or cp.async row by row where a tile
@@ -564,8 +570,9 @@ constexpr int kTtThreads = (kTtSoft + 8) * 32;  // (two warps fill the last warp
 // Registers of a softmax thread, of the others (64 nodes, 16 requests: 420 us; 168
 // and 88 423, 184 and 72 419 but 3 % slower with 128 rows, 160 and 96 426).
 constexpr int kTtMore = 176, kTtLess = 80;
-constexpr float kUnset = -1e30f;   // reference of a row that has seen nothing
+constexpr float kUnset = -FLT_MAX;  // reference of a row that has seen nothing
 constexpr float kExceed = 30.f;    // log2 of how far a logit may pass the reference
+constexpr float kRoundFrom = 16777216.f;  // |reference| from which Sᵀ gets rounded differences
 
 struct TreeTc {
   int NS;      // ring slots: 3 or 4
@@ -583,7 +590,15 @@ struct TreeTcHead {
   uint64_t qfull, qempty;
   uint64_t sfull[2], sfree[2], pready[2], pvdone[2], ofree;  // [team]
   uint32_t tmem_holder;
-  volatile int failed, odd, bad;
+  volatile int failed, odd;
+  // Per team, what makes a job unlike the others: some bad block was met; a
+  // reference of this run is past kRoundFrom.
+  volatile union {
+    uint16_t any;
+    struct {
+      uint8_t bad, large;
+    };
+  } special[2];
   float nb[2][128];  // −reference per team and row
 };
 constexpr uint32_t kTtHead = 2048;
@@ -701,7 +716,7 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
   if (tid == 0) {
     sm.failed = 0;
     sm.odd = 0;
-    sm.bad = 0;
+    sm.special[0].any = sm.special[1].any = 0;
     for (int i = 0; i < 2 * kTtSlots; i++) {
       mbar_init(smem_u32(sm.full[0] + i), 128);
       mbar_init(smem_u32(sm.empty[0] + i), 1);
@@ -788,7 +803,8 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
           if (blk >= 0 && blk < n_blocks) {
             slot = blk * a.BS + pp - page_of(pp, a.bs_inv) * a.BS;
           } else {
-            sm.bad = 1;  // (read by the softmax warps after this stage's product)
+            // (read by the softmax warps after this stage's product)
+            sm.special[0].bad = sm.special[1].bad = 1;
             record_error(a.status, KVC_ERR_BOUNDS);
           }
         }
@@ -1019,7 +1035,11 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
       const int32_t *bt = a.block_table + (int64_t)pos.r * a.max_blocks;
       named_sync(bar, 128);  // the last run's references are read
       nb[wt] = wt < cols ? -kUnset : -INFINITY;  // (columns that hold no row: weight 0)
+      sm.special[team].large = 0;
       named_sync(bar, 128);
+      // This thread's row's reference while they are large (in local memory: the loop
+      // has no register to spare for it, 3 to 9 % of its time).
+      volatile float large_ref[1];
       float l[32];  // sums of the weights of rows 8k + 2·(t%4) + {0, 1}
 #pragma unroll
       for (int e = 0; e < 32; e++) l[e] = 0.f;
@@ -1030,54 +1050,61 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
         ok = ok && __all_sync(0xFFFFFFFFu,
                               mbar_wait_bounded(smem_u32(sm.sfull + team), sc & 1, &sm.failed));
         tc_fence_after();
-        // a tile with nodes, past the end, or (after some bad block) any tile
-        if (ok && ((t + 1) * kTtKeys > pos.c || sm.bad)) {
-          const int pp = t * kTtKeys + quarter * 32 + lane;
-          bool valid = pp < pos.c + pos.T;
-          if (valid) {
-            const int32_t blk = bt[page_of(pp, a.bs_inv)];
-            valid = blk >= 0 && blk < n_blocks;
-          }
-          const uint32_t valid_keys = __ballot_sync(0xFFFFFFFFu, valid);
-          const float hidden = zs < 0.f ? INFINITY : -INFINITY;  // −inf once scaled
-          // which of the warp's 32 keys the rows lane + 32·m see
-          uint32_t sees[4];
-          const int p0 = t * kTtKeys + quarter * 32, j0 = p0 - pos.c;
-#pragma unroll
-          for (int m = 0; m < 4; m++) {
-            const int i = (pos.rt() * a.rstep + row0 + 32 * m + lane) / a.G;
-            uint32_t v = j0 <= -32 ? 0xFFFFFFFFu : j0 < 0 ? (1u << -j0) - 1u : 0u;
-            if (i < pos.T) v = visible_bits<32>(a, i, pos.q0, pos.c, pos.T, p0);
-            sees[m] = v & valid_keys;
-          }
-#pragma unroll 1
-          for (int ch = 0; ch < 2; ch++) {
-            uint32_t bits[2] = {0, 0};  // of the registers of the two fragments (see tmem_frag8)
-#pragma unroll
-            for (int k = 0; k < 8; k++)
-#pragma unroll
-              for (int e = 0; e < 2; e++) {
-                const uint32_t mine = ch ? sees[2 + (k >> 2)] : sees[k >> 2];
-                const uint32_t v =
-                    __shfl_sync(0xFFFFFFFFu, mine, 8 * (k & 3) + 2 * (lane & 3) + e) >> (lane / 4);
-#pragma unroll
-                for (int j = 0; j < 2; j++) {
-                  bits[0] |= ((v >> (8 * j)) & 1u) << (4 * k + 2 * j + e);
-                  bits[1] |= ((v >> (16 + 8 * j)) & 1u) << (4 * k + 2 * j + e);
-                }
-              }
-#pragma unroll 1
-            for (int hf = 0; hf < 2; hf++) {
-              const uint32_t ta = ts + ((uint32_t)(16 * hf) << 16) + 64 * ch;
-              const uint32_t bh = hf ? bits[1] : bits[0];
-              uint32_t z[32];
-              tmem_frag8(ta, z);
-              tmem_wait(z);
-#pragma unroll
-              for (int e = 0; e < 32; e++)
-                if (!((bh >> e) & 1u)) z[e] = __float_as_uint(hidden);
-              tmem_put(ta, z);
+        // a tile with nodes, past the end, or (after some bad block, or with large
+        // references) any tile
+        if ((t + 1) * kTtKeys > pos.c || sm.special[team].any) {
+          if (ok) {
+            const int pp = t * kTtKeys + quarter * 32 + lane;
+            bool valid = pp < pos.c + pos.T;
+            if (valid) {
+              const int32_t blk = bt[page_of(pp, a.bs_inv)];
+              valid = blk >= 0 && blk < n_blocks;
             }
+            const uint32_t valid_keys = __ballot_sync(0xFFFFFFFFu, valid);
+            const float hidden = zs < 0.f ? INFINITY : -INFINITY;  // −inf once scaled
+            // which of the warp's 32 keys the rows lane + 32·m see
+            uint32_t sees[4];
+            const int p0 = t * kTtKeys + quarter * 32, j0 = p0 - pos.c;
+#pragma unroll
+            for (int m = 0; m < 4; m++) {
+              const int i = (pos.rt() * a.rstep + row0 + 32 * m + lane) / a.G;
+              uint32_t v = j0 <= -32 ? 0xFFFFFFFFu : j0 < 0 ? (1u << -j0) - 1u : 0u;
+              if (i < pos.T) v = visible_bits<32>(a, i, pos.q0, pos.c, pos.T, p0);
+              sees[m] = v & valid_keys;
+            }
+#pragma unroll 1
+            for (int ch = 0; ch < 2; ch++) {
+              uint32_t bits[2] = {0, 0};  // of the registers of the two fragments (see tmem_frag8)
+#pragma unroll
+              for (int k = 0; k < 8; k++)
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                  const uint32_t mine = ch ? sees[2 + (k >> 2)] : sees[k >> 2];
+                  const uint32_t v =
+                      __shfl_sync(0xFFFFFFFFu, mine, 8 * (k & 3) + 2 * (lane & 3) + e) >> (lane / 4);
+#pragma unroll
+                  for (int j = 0; j < 2; j++) {
+                    bits[0] |= ((v >> (8 * j)) & 1u) << (4 * k + 2 * j + e);
+                    bits[1] |= ((v >> (16 + 8 * j)) & 1u) << (4 * k + 2 * j + e);
+                  }
+                }
+#pragma unroll 1
+              for (int hf = 0; hf < 2; hf++) {
+                const uint32_t ta = ts + ((uint32_t)(16 * hf) << 16) + 64 * ch;
+                const uint32_t bh = hf ? bits[1] : bits[0];
+                uint32_t z[32];
+                tmem_frag8(ta, z);
+                tmem_wait(z);
+#pragma unroll
+                for (int e = 0; e < 32; e++)
+                  if (!((bh >> e) & 1u)) z[e] = __float_as_uint(hidden);
+                tmem_put(ta, z);
+              }
+            }
+          }
+          if (sm.special[team].large) {  // (team-uniform: this job raises the references first)
+            if (wt < cols) nb[wt] = -kUnset;
+            named_sync(bar, 128);
           }
         }
         for (;;) {
@@ -1154,7 +1181,8 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
               tmem_wait(z);
 #pragma unroll
               for (int e = 0; e < 32; e++)
-                cm[(e >> 2) * 2 + (e & 1)] = fmaxf(cm[(e >> 2) * 2 + (e & 1)], __uint_as_float(z[e]) * zs);
+                cm[(e >> 2) * 2 + (e & 1)] =
+                    fmaxf(cm[(e >> 2) * 2 + (e & 1)], __fmul_rn(__uint_as_float(z[e]), zs));
             }
 #pragma unroll
             for (int e = 0; e < 16; e++) {
@@ -1165,19 +1193,22 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
             }
           }
           named_sync(bar, 128);
+          bool large = false;
           {
             float f = 1.f;
             if (wt < cols) {
-              const float was = -nb[wt];
+              const float was = sm.special[team].large ? large_ref[0] : -nb[wt];
               const float m =
                   fmaxf(fmaxf(scr[wt], scr[128 + wt]), fmaxf(scr[256 + wt], scr[384 + wt]));
               const float now = fmaxf(was, m);
               f = ex2(was - now);
               nb[wt] = -now;
+              large_ref[0] = now;
+              large = m > -INFINITY && fabsf(now) >= kRoundFrom;
             }
             scr[512 + wt] = f;
           }
-          named_sync(bar, 128);
+          large = named_sync_or(bar, 128, large || sm.special[team].large);
           const float *fac = scr + 512;
 #pragma unroll
           for (int e = 0; e < 32; e++) {
@@ -1194,6 +1225,24 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
               for (int e = 0; e < 16; e++) v[e] *= f;
               tmem_st16(to + cc, v);
             }
+          }
+          if (large) {  // Sᵀ ← (fl(Sᵀ·zscale) − reference) / zscale; the loop's references are 0
+#pragma unroll 1
+            for (int w = 0; w < 4; w++) {
+              const uint32_t ta = ts + ((uint32_t)(16 * (w & 1)) << 16) + 64 * (w >> 1);
+              uint32_t z[32];
+              tmem_frag8(ta, z);
+              tmem_wait(z);
+#pragma unroll
+              for (int e = 0; e < 32; e++)
+                z[e] = __float_as_uint(
+                    __fadd_rn(__fmul_rn(__uint_as_float(z[e]), zs),
+                              nb[64 * (w >> 1) + 8 * (e >> 2) + 2 * (lane & 3) + (e & 1)]) / zs);
+              tmem_put(ta, z);
+            }
+            named_sync(bar, 128);
+            if (wt < cols) nb[wt] = 0.f;
+            sm.special[team].large = 1;
           }
           named_sync(bar, 128);  // the factors are read before P replaces them
         }
@@ -1229,7 +1278,8 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
       if (ok) {
         const float sum = (scr[wt] + scr[128 + wt]) + (scr[256 + wt] + scr[384 + wt]);
         const bool any = wt < cols && (sum > 0.f || sum != sum);
-        ml[wt] = make_float2(any ? -nb[wt] : -INFINITY, any ? sum : 0.f);
+        const float m = sm.special[team].large ? large_ref[0] : -nb[wt];
+        ml[wt] = make_float2(any ? m : -INFINITY, any ? sum : 0.f);
       }
       ok = named_sync_and(7, kTtSoft * 32, ok);
       if (!ok) break;

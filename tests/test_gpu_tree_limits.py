@@ -1,0 +1,61 @@
+"""Tree decoding on the GPU at the limits of its types, against 64-bit forms: logits far past the range
+in which fp32 resolves single units."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+import tree_ref as ref  # noqa: E402
+from test_gpu_tree_decode import Tree, inside, kvc  # noqa: E402,F401
+
+
+def evenly(t):
+    """Attention with the maximum taken off the logits first (an lse of 2^66 does not hold ln n in 64
+    bits)."""
+    o = torch.zeros(t.n_q, t.Hq, t.D, dtype=torch.float64)
+    for r in range(t.n_req):
+        s = ref.slots(t.bt[r], t.BS, t.ctx[r] + t.T[r])
+        for i in range(t.T[r]):
+            row = int(t.q_off[r]) + i
+            nodes = ref.sees(None if t.mask is None else t.mask[row], i, t.T[r], t.mask is None)
+            at = s[torch.from_numpy(np.flatnonzero(np.concatenate([np.ones(t.ctx[r], bool), nodes])))]
+            for h in range(t.Hq):
+                z = t.k[at, h // t.G].double() @ t.q[row, h].double() * t.scale
+                o[row, h] = torch.softmax(z, 0) @ t.v[at, h // t.G].double()
+    return o
+
+
+@pytest.mark.parametrize("T,G,D", [(3, 4, 128), (12, 4, 64), (20, 5, 128), (64, 4, 128), (50, 4, 64)])
+@pytest.mark.parametrize("exponent", [20, 27, 33, 40, 66, 99])
+@pytest.mark.parametrize("order", ["rising", "falling", "mixed", "equal"])
+def test_attn_huge_logits(kvc, T, G, D, exponent, order):  # noqa: F811
+    """Logits of ±2^20 to ±2^99, exact in fp32, whose distinct levels lie 2^-7 of them apart: the rows
+    attend to their highest level's keys alone, evenly.  Few rows and many, several tiles and CTAs."""
+    for sign in (1.0, -1.0):
+        t = Tree(exponent + T, [1100, 70], [T, T - 1], 1, G, D, 16, "tree")
+        t.scale = 1.0
+        t.q.zero_()
+        t.q[..., 0] = 1.0
+        rng = np.random.default_rng(exponent)
+        for r in range(2):
+            n = t.ctx[r] + t.T[r]
+            j = {"rising": np.arange(n) * 100 // n, "falling": 100 - np.arange(n) * 100 // n,
+                 "mixed": rng.integers(0, 100, n), "equal": np.full(n, 77)}[order]
+            level = torch.from_numpy(sign * 2.0 ** exponent * (1 + j / 128.0)).to(torch.bfloat16)
+            t.k[ref.slots(t.bt[r], 16, n), 0, 0] = level
+        out, lse = t.gpu().call(kvc)
+        torch.cuda.synchronize()
+        assert kvc.kvc_device_status(t.d["status"]) == 0
+        _, ls, _, _ = t.want()
+        o = evenly(t)
+        # weights of 1 and 0 (of 2^r, |r| < 1, in bf16 where references are below 2^24), n keys summed
+        # in fp32, one rounding of out; the lse: scale·log2e, the product, the sum, ·ln2
+        wv = torch.where(torch.isfinite(t.v), t.v.double().abs(), torch.zeros_like(t.v.double())).max()
+        ob = 2 * ref.UBF * o.abs() + (ref.UBF + 1200 * ref.U32 + 2 ** -21) * wv
+        inside(out, o, ob, f"out {sign}")
+        inside(lse, ls, 8 * ref.U32 * ls.abs() + 1200 * ref.U32 + 2 ** -20, f"lse {sign}")
