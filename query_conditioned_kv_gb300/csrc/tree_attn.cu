@@ -1217,6 +1217,7 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
           }
           if (!fresh) {  // O's lanes are the team's rows
             const float f = fac[quarter * 32 + lane];
+            tc_fence_after();  // (after the wait for pvdone: the product that wrote O)
 #pragma unroll 1
             for (int cc = 0; cc < D; cc += 16) {
               float v[16];
