@@ -23,6 +23,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "kvc_internal.cuh"
 #include "mma_ptx.cuh"
@@ -1137,6 +1138,16 @@ cudaError_t launch_tc(const MassArgs &a, void *ws, cudaStream_t s) {
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
+  static std::atomic<int> regs[2];  // a thread's registers at launch (RT 1, RT 2)
+  if (!regs[pairs != 0].load(std::memory_order_relaxed)) {
+    cudaFuncAttributes fa{};
+    if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
+    regs[pairs != 0].store(fa.numRegs, std::memory_order_relaxed);
+  }
+  // setmaxnreg.inc draws on what the block was launched with
+  if (regs[pairs != 0].load(std::memory_order_relaxed) * kTcThreads <
+      kTcEpi * 32 * kTcMore + (kTcThreads - kTcEpi * 32) * kTcLess)
+    return cudaErrorLaunchOutOfResources;
   if (pairs == 0) {
     kern<<<p.n_cta, kTcThreads, smem, s>>>(tm_k, tm_q, a, p);
     return cudaGetLastError();
