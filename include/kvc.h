@@ -815,6 +815,11 @@ kvc_status kvc_tail_compact(kvc_bf16 *kpool, kvc_bf16 *vpool, int64_t n_slots, i
  * Same pools, block table and position → slot rule as above.  Every entry
  * point takes any H ≥ 1, Hq a multiple of H with Hq ≤ 256, D ∈ {64, 128} and
  * block_size in [1, 64].
+ * The model, commit and eviction write rows in place: a page that holds a row
+ * they write (a position from ctx_len on; any position of a request that is
+ * over its budget) must be one page of one request.  A prefix page that several
+ * requests refer to stays as it is only while none of them is over its budget;
+ * give a request its own copy before that.
  * ====================================================================== */
 
 /* Most nodes of one request's tree. */
@@ -881,12 +886,15 @@ kvc_status kvc_tree_attn(const kvc_bf16 *q, const kvc_bf16 *kpool, const kvc_bf1
  *   path         device int32 [n_req][max_path]; n_path device int32 [n_req]
  *   seq_out      device int32 [n_req] out
  *   row_idx, row_vis device int32 [n_req][max_path] out, may be NULL
+ * The outputs share no memory with the inputs or with each other (seq_out is
+ * not ctx_len, which other layers' blocks still read).
  * A request whose ctx_len, q_off, n_path or path is out of range (path not
  * ascending or not below T) is recorded as KVC_ERR_BOUNDS: no row moves,
  * seq_out[r] = max(c, 0), its row_vis are 0.  A block id outside the pool is
  * recorded and the row's copy skipped.
- * Errors: KVC_ERR_INVALID_ARG, KVC_ERR_SHAPE (D, block_size > 64, max_path >
- * KVC_TREE_MAX_NODES, too many positions), KVC_ERR_ALIGN.
+ * Errors: KVC_ERR_INVALID_ARG (also outputs that overlap), KVC_ERR_SHAPE (D,
+ * block_size > 64, max_path > KVC_TREE_MAX_NODES, too many positions),
+ * KVC_ERR_ALIGN.
  * ---------------------------------------------------------------------- */
 kvc_status kvc_tree_commit(kvc_bf16 *kpool, kvc_bf16 *vpool, int64_t n_slots,
                            const int32_t *block_table, int32_t max_blocks,
@@ -963,7 +971,8 @@ kvc_status kvc_attn_mass(const kvc_bf16 *q, const float *lse, int32_t n_q,
  *   mass_out, pos_out  same shapes, out: rows [0, m) written (the kept
  *                 weights and original positions), the rest untouched; may
  *                 be mass and pos themselves, not overlap them otherwise
- *   n_out         device int32 [n_req] out: m (0 for a skipped request)
+ *   n_out         device int32 [n_req] out: m (0 for a skipped request); not
+ *                 seqused_k or n_pos, which other segments still read
  *   ws            device scratch of kvc_mass_evict_workspace_size() bytes
  *                 (0, and ws may be NULL, while max_blocks·block_size ≤
  *                 KVC_EVICT_STAGED_ROWS)
@@ -972,7 +981,8 @@ kvc_status kvc_attn_mass(const kvc_bf16 *q, const float *lse, int32_t n_q,
  * A seqused_k out of range is recorded as KVC_ERR_BOUNDS and the request
  * skipped; a block id outside the pool is recorded and the row's K and V
  * stay where they are.  n_pos is clamped to [0, n].
- * Errors: KVC_ERR_INVALID_ARG, KVC_ERR_BUDGET (budget < 1, n_sink < 0,
+ * Errors: KVC_ERR_INVALID_ARG (also outputs that overlap anything but mass
+ * and pos as above), KVC_ERR_BUDGET (budget < 1, n_sink < 0,
  * n_recent < 0, n_sink + n_recent > budget), KVC_ERR_SHAPE, KVC_ERR_ALIGN,
  * KVC_ERR_WORKSPACE.
  * ---------------------------------------------------------------------- */

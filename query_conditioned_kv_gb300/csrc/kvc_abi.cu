@@ -3,6 +3,8 @@
 // directory on the caller's stream.  No allocation, no state.
 #include <math.h>
 
+#include <initializer_list>
+
 #include "kvc_internal.cuh"
 #include "tc_ptx.cuh"
 
@@ -33,6 +35,26 @@ kvc_status paged_status(int64_t L, int64_t n_req, int64_t H, int D, int64_t BS,
       L * n_req * H > INT32_MAX || n_req * max_blocks > INT32_MAX || L > 65535 || n_req > 65535)
     return KVC_ERR_SHAPE;
   return KVC_OK;
+}
+// Whether n bytes at a and m bytes at b share a byte (NULL or 0: nothing there).
+bool overlap(const void *a, size_t n, const void *b, size_t m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && n && m && x < y + m && y < x + n;
+}
+struct Span {
+  const void *p;
+  size_t bytes;
+};
+// Whether an output shares memory with an input or another output: CTAs of one
+// launch write the one while others still read the other.
+bool outputs_overlap(std::initializer_list<Span> out, std::initializer_list<Span> in) {
+  for (auto o = out.begin(); o != out.end(); ++o) {
+    for (const Span &i : in)
+      if (overlap(o->p, o->bytes, i.p, i.bytes)) return true;
+    for (auto u = out.begin(); u != o; ++u)
+      if (overlap(o->p, o->bytes, u->p, u->bytes)) return true;
+  }
+  return false;
 }
 bool heads_ok(int H, int Hq) { return Hq >= H && Hq % H == 0 && Hq <= 256; }
 
@@ -552,6 +574,18 @@ kvc_status kvc_tree_commit(kvc_bf16 *kpool, kvc_bf16 *vpool, int64_t n_slots,
   if (st != KVC_OK) return st;
   if (max_path > KVC_TREE_MAX_NODES) return KVC_ERR_SHAPE;
   if (!aligned16(kpool) || !aligned16(vpool)) return KVC_ERR_ALIGN;
+  const size_t pool = (size_t)L * n_slots * H * D * 2, reqs = (size_t)n_req * 4;
+  if (outputs_overlap({{kpool, pool},
+                       {vpool, pool},
+                       {seq_out, reqs},
+                       {row_idx, reqs * max_path},
+                       {row_vis, reqs * max_path}},
+                      {{block_table, reqs * max_blocks},
+                       {ctx_len, reqs},
+                       {q_off, reqs + 4},
+                       {path, reqs * max_path},
+                       {n_path, reqs}}))
+    return KVC_ERR_INVALID_ARG;
   return from_cuda(kvc::launch_tree_commit(kpool, vpool, n_slots, block_table, max_blocks,
                                            ctx_len, q_off, path, n_path, max_path, n_req, L, H,
                                            D, block_size, seq_out, row_idx, row_vis, dev_status,
@@ -625,6 +659,21 @@ kvc_status kvc_mass_evict(kvc_bf16 *kpool, kvc_bf16 *vpool, int64_t n_slots,
   const size_t need =
       kvc_mass_evict_workspace_size(n_req, max_blocks, L, H, block_size, budget);
   if (need && (!ws || ws_bytes < need)) return KVC_ERR_WORKSPACE;
+  const size_t pool = (size_t)L * n_slots * H * D * 2, reqs = (size_t)n_req * 4;
+  const size_t rows = (size_t)L * n_req * H * max_blocks * block_size * 4;
+  if (outputs_overlap({{kpool, pool},
+                       {vpool, pool},
+                       {mass_out, rows},
+                       {pos_out, rows},
+                       {n_out, reqs},
+                       {ws, need}},
+                      {{block_table, reqs * max_blocks},
+                       {seqused_k, reqs},
+                       {n_pos, reqs},
+                       {t_end, reqs},
+                       {mass_out == mass ? nullptr : mass, rows},
+                       {pos_out == pos ? nullptr : pos, rows}}))
+    return KVC_ERR_INVALID_ARG;
   return from_cuda(kvc::launch_mass_evict(kpool, vpool, n_slots, block_table, max_blocks,
                                           seqused_k, n_pos, t_end, mass, pos, mass_out, pos_out,
                                           n_out, n_req, L, H, D, block_size, budget, n_sink,

@@ -57,3 +57,40 @@ def test_one_raise_a_job_is_enough(mag, sign):
             best = (order * F(0.08838835 * LOG2E)).max(1)
             got = ref + np.log2(total)
             assert (np.abs(got - best) <= 10 + np.abs(best) * 2.0 ** -22).all()
+
+
+# ------------------------------------------------ buffers of the in-place calls
+
+MB = 1 << 20
+COMMIT = dict(kpool=512 * MB, vpool=640 * MB, n_slots=1 << 12, block_table=1 * MB, max_blocks=8,
+              ctx_len=2 * MB, q_off=3 * MB, path=4 * MB, n_path=5 * MB, max_path=4, n_req=2, L=3, H=2,
+              D=128, block_size=16, seq_out=6 * MB, row_idx=7 * MB, row_vis=8 * MB, dev_status=None,
+              stream=None)
+EVICT = dict(kpool=512 * MB, vpool=640 * MB, n_slots=1 << 12, block_table=1 * MB, max_blocks=8,
+             seqused_k=2 * MB, n_pos=3 * MB, t_end=4 * MB, mass=5 * MB, pos=6 * MB, mass_out=7 * MB,
+             pos_out=8 * MB, n_out=9 * MB, n_req=2, L=3, H=2, D=128, block_size=16, budget=64, n_sink=4,
+             n_recent=8, ws=None, ws_bytes=0, dev_status=None, stream=None)
+ROWS = 3 * 2 * 2 * 8 * 16 * 4   # bytes of a mass or pos buffer
+POOL = 3 * 4096 * 2 * 128 * 2   # bytes of a pool
+
+
+@pytest.mark.parametrize("call,change", [
+    (COMMIT, dict(seq_out=2 * MB)), (COMMIT, dict(seq_out=2 * MB + 4)), (COMMIT, dict(seq_out=3 * MB + 8)),
+    (COMMIT, dict(seq_out=5 * MB)), (COMMIT, dict(row_idx=4 * MB)), (COMMIT, dict(row_vis=4 * MB + 28)),
+    (COMMIT, dict(row_vis=7 * MB)), (COMMIT, dict(seq_out=1 * MB + 60)), (COMMIT, dict(vpool=512 * MB)),
+    (COMMIT, dict(vpool=512 * MB + POOL - 16)), (COMMIT, dict(seq_out=7 * MB, row_vis=None)),
+    (EVICT, dict(n_out=2 * MB)), (EVICT, dict(n_out=2 * MB + 4)), (EVICT, dict(n_out=3 * MB)),
+    (EVICT, dict(n_out=4 * MB)), (EVICT, dict(n_out=1 * MB)), (EVICT, dict(mass_out=5 * MB + 16)),
+    (EVICT, dict(mass_out=5 * MB + ROWS - 16)), (EVICT, dict(pos_out=6 * MB - ROWS + 16)),
+    (EVICT, dict(mass_out=6 * MB)), (EVICT, dict(pos_out=5 * MB)), (EVICT, dict(pos_out=7 * MB)),
+    (EVICT, dict(vpool=512 * MB))])
+def test_outputs_that_overlap_are_refused(call, change):
+    """A launch writes its outputs while other blocks of it still read the inputs: lengths updated in
+    place would evict nothing, or move the wrong rows, in some layers."""
+    import __graft_entry__
+    __graft_entry__.build()
+    import query_conditioned_kv_gb300 as kvc
+    name = "kvc_tree_commit" if call is COMMIT else "kvc_mass_evict"
+    args = dict(call, **change)
+    assert list(args) == list(call)
+    assert getattr(kvc.lib, name)(*args.values()) == 1
