@@ -442,7 +442,9 @@ k_tree_rows(TreeArgs a) {
 #pragma unroll
       for (int w = 0; w < kRowWarps; w++) {
         const float2 ml = ml_s[w * R + row];
-        if (ml.x == -INFINITY) continue;  // this warp saw nothing of the row
+        // This warp saw nothing of the row.  (Logits that are all NaN leave the
+        // maximum at −inf too, but a NaN sum, which has to reach the result.)
+        if (ml.x == -INFINITY && ml.y == 0.f) continue;
         const float f = ex2(ml.x - base);
         sum = fmaf(ml.y, f, sum);
         const float4 v = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(sm) +
@@ -455,10 +457,10 @@ k_tree_rows(TreeArgs a) {
       if (whole) {
         const int x = rt * a.rstep + row;
         const int64_t qr = (int64_t)(q0 + x / a.G) * a.Hq + h * a.G + x % a.G;
-        const float inv = mx == -INFINITY ? 0.f : 1.f / sum;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
         uint2 w2 = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
         *reinterpret_cast<uint2 *>(a.out + qr * D + d4) = w2;
-        if (d4 == 0) a.lse[qr] = mx == -INFINITY ? -INFINITY : (mx + log2f(sum)) * kLn2;
+        if (d4 == 0) a.lse[qr] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
       } else if (CL) {
         *reinterpret_cast<float4 *>(sm + S::kClO + (row * D + d4) * 4) = acc;
         if (d4 == 0) reinterpret_cast<float2 *>(sm + S::kClMl)[row] = make_float2(mx, sum);
@@ -495,10 +497,10 @@ k_tree_rows(TreeArgs a) {
         }
         const int x = rt * a.rstep + row;
         const int64_t qr = (int64_t)(q0 + x / a.G) * a.Hq + h * a.G + x % a.G;
-        const float inv = mx == -INFINITY ? 0.f : 1.f / sum;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
         *reinterpret_cast<uint2 *>(a.out + qr * D + d4) =
             make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-        if (d4 == 0) a.lse[qr] = mx == -INFINITY ? -INFINITY : (mx + log2f(sum)) * kLn2;
+        if (d4 == 0) a.lse[qr] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
       }
       __syncwarp();
       cluster_sync_all();  // (no CTA leaves while another reads its part)
@@ -1507,7 +1509,7 @@ k_tree_join(TreeArgs a) {
         for (int e = 0; e < E; e++) acc[e] = fmaf(sh_o[w][d0 + e], f, acc[e]);
       }
     }
-    const float inv = mx == -INFINITY ? 0.f : 1.f / sum;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const int x = rt * a.rstep + row;
     const int64_t qr = (int64_t)(q0 + x / a.G) * a.Hq + h * a.G + x % a.G;
     uint32_t w[E / 2];
@@ -1515,7 +1517,7 @@ k_tree_join(TreeArgs a) {
     for (int e = 0; e < E / 2; e++) w[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
     if constexpr (E == 4) *reinterpret_cast<uint2 *>(a.out + qr * D + d0) = make_uint2(w[0], w[1]);
     else *reinterpret_cast<uint32_t *>(a.out + qr * D + d0) = w[0];
-    if (d0 == 0) a.lse[qr] = mx == -INFINITY ? -INFINITY : (mx + log2f(sum)) * kLn2;
+    if (d0 == 0) a.lse[qr] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
   }
 }
 

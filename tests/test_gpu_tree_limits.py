@@ -13,6 +13,8 @@ if not torch.cuda.is_available():
 import tree_ref as ref  # noqa: E402
 from test_gpu_tree_decode import Tree, inside, kvc  # noqa: E402,F401
 
+NAN = float("nan")
+
 
 def evenly(t):
     """Attention with the maximum taken off the logits first (an lse of 2^66 does not hold ln n in 64
@@ -59,3 +61,42 @@ def test_attn_huge_logits(kvc, T, G, D, exponent, order):  # noqa: F811
         ob = 2 * ref.UBF * o.abs() + (ref.UBF + 1200 * ref.U32 + 2 ** -21) * wv
         inside(out, o, ob, f"out {sign}")
         inside(lse, ls, 8 * ref.U32 * ls.abs() + 1200 * ref.U32 + 2 ** -20, f"lse {sign}")
+
+
+# ------------------------------------------------------- NaN among the logits
+
+@pytest.mark.parametrize("T,G,D", [(1, 4, 128), (3, 4, 64), (12, 4, 128), (20, 4, 128), (64, 4, 64)])
+@pytest.mark.parametrize("ctx", [[700, 3, 40], [0, 9, 16], [6000, 5000, 30], [40000, 64, 9]])
+def test_attn_nan_logits(kvc, T, G, D, ctx):  # noqa: F811
+    """A NaN in a query, a whole page of NaN keys, the only keys of a request NaN, a NaN node: NaN in
+    exactly the rows that see it, whichever path takes them (a row that sees nothing has 0 and -inf)."""
+    if max(ctx) > 10000 and T > 3:
+        pytest.skip("long caches with short trees only")
+    t = Tree(sum(ctx) + T, ctx, [T] * 3, 2, G, D, 16, "tree", poison=False)
+    t.q[1 % (3 * T), 1, 5] = NAN                       # one head of one row
+    t.q[T + T // 2, 2] = NAN
+    s2 = ref.slots(t.bt[2], 16, ctx[2] + T)
+    t.k[s2[:min(16, ctx[2])], 0] = NAN                 # a page (or less) of the last request, one KV head
+    s0 = ref.slots(t.bt[0], 16, ctx[0] + T)
+    t.k[s0[ctx[0] + T - 1], 1, 7] = NAN                # the last node of the first, the other KV head
+    out, lse = t.gpu().call(kvc)
+    torch.cuda.synchronize()
+    assert kvc.kvc_device_status(t.d["status"]) == 0
+    o, ls, ob, lb = t.want()
+    assert torch.isnan(ls).any() and not torch.isnan(ls).all()
+    inside(out, o, ob, "out")
+    inside(lse, ls, lb, "lse")
+
+
+def test_attn_nan_next_to_rows_that_see_nothing(kvc):  # noqa: F811
+    """Nothing cached and masks of holes: 0 and -inf where a row sees nothing, NaN where its only node
+    is NaN."""
+    for T, G in [(4, 4), (40, 4)]:
+        t = Tree(3, [0, 0], [T, T], 1, G, 128, 16, "self", poison=False)
+        t.mask[1] = 0
+        t.k[ref.slots(t.bt[0], 16, T)[2]] = NAN
+        out, lse = t.gpu().call(kvc)
+        o, ls, ob, lb = t.want()
+        assert torch.isinf(ls[1]).all() and torch.isnan(ls[2]).all()
+        inside(out, o, ob, "out")
+        inside(lse, ls, lb, "lse")
