@@ -343,7 +343,8 @@ k_tree_rows(TreeArgs a) {
       }
       // A node's V may hold infinities or NaN that some rows do not see, and a
       // product 0·inf would hand them to those rows.  A tile with such values
-      // takes the sum term by term, over the rows' visible keys only.
+      // takes the sum term by term, over the rows' visible keys only; there such a
+      // value is added as it is, for a weight too small for fp32 is not 0.
       bool odd = false;
       if (p0 + KT > c) {
         for (int e = lane; e < KT * CH; e += 32) {
@@ -359,8 +360,17 @@ k_tree_rows(TreeArgs a) {
         odd = __any_sync(0xFFFFFFFFu, odd);
       }
       if (odd) {
+        auto add = [](float w, float v, float &acc) {
+          acc = fabsf(v) < INFINITY ? fmaf(w, v, acc) : acc + v;
+        };
 #pragma unroll
-        for (int mt = 0; mt < MT; mt++)
+        for (int mt = 0; mt < MT; mt++) {
+          uint32_t vis[2];
+#pragma unroll
+          for (int hf = 0; hf < 2; hf++) {
+            const int x = rt * a.rstep + mt * 16 + hf * 8 + lane / 4;
+            vis[hf] = x < T * a.G ? visible_bits<KT>(a, x / a.G, q0, c, T, p0) & okb : 0u;
+          }
 #pragma unroll
           for (int kn = 0; kn < KT / 8; kn++)
             for (int kq = 0; kq < 4; kq++)
@@ -375,16 +385,17 @@ k_tree_rows(TreeArgs a) {
                   asm volatile("ld.shared.u32 %0, [%1];"
                                : "=r"(v)
                                : "r"(vb + swz<D>(8 * kn + 2 * kq + e, n) + 4 * (lane % 4)));
-                  if (w0 > 0.f) {
-                    o[mt][n][0] = fmaf(w0, bf16_lo(v), o[mt][n][0]);
-                    o[mt][n][1] = fmaf(w0, bf16_hi(v), o[mt][n][1]);
+                  if ((vis[0] >> (8 * kn + 2 * kq + e)) & 1u) {
+                    add(w0, bf16_lo(v), o[mt][n][0]);
+                    add(w0, bf16_hi(v), o[mt][n][1]);
                   }
-                  if (w1 > 0.f) {
-                    o[mt][n][2] = fmaf(w1, bf16_lo(v), o[mt][n][2]);
-                    o[mt][n][3] = fmaf(w1, bf16_hi(v), o[mt][n][3]);
+                  if ((vis[1] >> (8 * kn + 2 * kq + e)) & 1u) {
+                    add(w1, bf16_lo(v), o[mt][n][2]);
+                    add(w1, bf16_hi(v), o[mt][n][3]);
                   }
                 }
               }
+        }
       } else {
 #pragma unroll
         for (int kk = 0; kk < KT / 16; kk++) {
@@ -1314,7 +1325,9 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
           f1 = ex2(ml1.x - m_use);
           sum = fmaf(ml0.y, f0, ml1.y * f1);
         }
-        if (m == -INFINITY) f0 = f1 = 0.f;
+        // (a team that saw nothing of the row may hold anything; one whose weights
+        // are all below fp32 still holds NaN where a value is not finite)
+        const bool s0 = halves ? m > -INFINITY : ml0.x > -INFINITY, s1 = !halves && ml1.x > -INFINITY;
         const float inv = whole ? (m == -INFINITY ? 0.f : 1.f / sum) : 1.f;
         const bool two = !halves && t1 - t0 > 1;
         const int x = pos.rt() * a.rstep + row, i = x / a.G;
@@ -1327,8 +1340,8 @@ k_tree_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
           if (two) tmem_ld16(tmem + 256 + 128 + lanes + d0 + cc, u);
 #pragma unroll
           for (int e = 0; e < 16; e++) {
-            v[e] = f0 == 0.f ? 0.f : v[e] * f0;
-            if (two && f1 != 0.f) v[e] = fmaf(u[e], f1, v[e]);
+            v[e] = s0 ? v[e] * f0 : 0.f;
+            if (two && s1) v[e] = fmaf(u[e], f1, v[e]);
           }
           if (odd && mine) {  // infinities and NaN of the nodes this run covered that the row sees
             const int j1 = min(pos.T, t1 * kTtKeys - pos.c);

@@ -100,3 +100,45 @@ def test_attn_nan_next_to_rows_that_see_nothing(kvc):  # noqa: F811
         assert torch.isinf(ls[1]).all() and torch.isnan(ls[2]).all()
         inside(out, o, ob, "out")
         inside(lse, ls, lb, "lse")
+
+
+@pytest.mark.parametrize("T,G", [(1, 4), (3, 4), (8, 4), (20, 4), (64, 4)])
+@pytest.mark.parametrize("value", [NAN, float("inf")])
+@pytest.mark.parametrize("place", ["cached", "node"])
+def test_attn_values_that_are_not_finite_reach_far_rows(kvc, T, G, value, place):  # noqa: F811
+    """A NaN or infinite V whose weight is below the smallest fp32 is still a value the row sees: its
+    result is not finite."""
+    t = Tree(5, [900], [T], 1, G, 128, 16, "chain", poison=False)
+    s = ref.slots(t.bt[0], 16, 900 + T)
+    t.q.zero_()
+    t.q[..., 0] = 1.0
+    t.k[s, 0, 0] = 0.0
+    at = 100 if place == "cached" else 900
+    t.k[s[at], 0, 0] = -300.0 / t.scale
+    t.v[s[at], 0, 9] = value
+    out, lse = t.gpu().call(kvc)
+    o, ls, ob, lb = t.want()
+    out = out.float().cpu()
+    assert not torch.isfinite(out[:, :, 9]).any()
+    keep = torch.arange(128) != 9
+    inside(out[..., keep], o[..., keep], ob[..., keep], "out")
+    inside(lse, ls, lb, "lse")
+
+
+@pytest.mark.parametrize("tile", [0, 1])
+def test_attn_values_that_are_not_finite_in_a_tile_of_no_weight(kvc, tile):  # noqa: F811
+    """The same where all of a tile's weights are below the smallest fp32: whole units of two tiles, so
+    that one of a block's two groups of warps holds nothing else."""
+    T, G, n = 10, 4, 100
+    t = Tree(6, [246] * n, [T] * n, 2, G, 128, 16, "chain", poison=False)
+    t.q.zero_()
+    t.q[..., 0] = 1.0
+    t.k[:, :, 0] = 0.0
+    for r in range(n):
+        s = ref.slots(t.bt[r], 16, 256)
+        t.k[s[128 * tile:128 * tile + 128], :, 0] = -300.0 / t.scale
+        t.v[s[128 * tile + 7], r % 2, 11] = NAN
+    out, lse = t.gpu().call(kvc)
+    o, ls, ob, lb = t.want()
+    inside(out, o, ob, "out")
+    inside(lse, ls, lb, "lse")
