@@ -171,8 +171,7 @@ k_mass_rows(MassArgs a, int n_cta_max) {
     // this unit's rows: LSE and limits, then the queries.  A row that adds
     // nothing (past the request's rows, no limit, LSE ±inf) gets lse = +inf and
     // q = 0, so its weight is 0 wherever K is finite; `lo`, the least limit of
-    // the others, tells the tiles that every one of them sees (there a NaN key
-    // is a NaN result in any case).
+    // the others, tells the tiles that every one of them sees.
     const int n_rows = n * a.G;
     int lo = seq + 1;
     for (int row = tid; row < NT * 8; row += kMrThreads) {
@@ -267,27 +266,35 @@ k_mass_rows(MassArgs a, int n_cta_max) {
         }
       }
       // keys lane/4 and lane/4 + 8 of each m tile; rows 2·(lane%4) + {0, 1} of each n tile
-      const bool masked = p0 + KT > lo;  // some row stops inside or before the tile
+      // The tile's sums, with the rows' limits where some row stops inside or before
+      // it.  An infinite key makes 0·inf = NaN in the rows that add nothing: sums
+      // that are NaN are taken again with the limits, which leave those rows out.
       float sum[MT][2];
+      for (bool masked = p0 + KT > lo;; masked = true) {
 #pragma unroll
-      for (int mt = 0; mt < MT; mt++) sum[mt][0] = sum[mt][1] = 0.f;
+        for (int mt = 0; mt < MT; mt++) sum[mt][0] = sum[mt][1] = 0.f;
 #pragma unroll
-      for (int nt = 0; nt < NT; nt++) {
-        const float2 ls = *reinterpret_cast<const float2 *>(lse_s + nt * 8 + 2 * (lane & 3));
-        const int2 vs = *reinterpret_cast<const int2 *>(vis_s + nt * 8 + 2 * (lane & 3));
+        for (int nt = 0; nt < NT; nt++) {
+          const float2 ls = *reinterpret_cast<const float2 *>(lse_s + nt * 8 + 2 * (lane & 3));
+          const int2 vs = *reinterpret_cast<const int2 *>(vis_s + nt * 8 + 2 * (lane & 3));
 #pragma unroll
-        for (int mt = 0; mt < MT; mt++)
+          for (int mt = 0; mt < MT; mt++)
 #pragma unroll
-          for (int hf = 0; hf < 2; hf++) {
-            float w0 = ex2(fmaf(c[mt][nt][2 * hf], a.zscale, -ls.x));
-            float w1 = ex2(fmaf(c[mt][nt][2 * hf + 1], a.zscale, -ls.y));
-            if (masked) {
-              const int p = p0 + mt * 16 + hf * 8 + lane / 4;
-              w0 = p < vs.x ? w0 : 0.f;
-              w1 = p < vs.y ? w1 : 0.f;
+            for (int hf = 0; hf < 2; hf++) {
+              float w0 = ex2(fmaf(c[mt][nt][2 * hf], a.zscale, -ls.x));
+              float w1 = ex2(fmaf(c[mt][nt][2 * hf + 1], a.zscale, -ls.y));
+              if (masked) {
+                const int p = p0 + mt * 16 + hf * 8 + lane / 4;
+                w0 = p < vs.x ? w0 : 0.f;
+                w1 = p < vs.y ? w1 : 0.f;
+              }
+              sum[mt][hf] += w0 + w1;
             }
-            sum[mt][hf] += w0 + w1;
-          }
+        }
+        bool nan = false;
+#pragma unroll
+        for (int mt = 0; mt < MT; mt++) nan |= sum[mt][0] != sum[mt][0] || sum[mt][1] != sum[mt][1];
+        if (masked || !__any_sync(0xFFFFFFFFu, nan)) break;
       }
       float res = 0.f;
 #pragma unroll
@@ -872,7 +879,8 @@ k_mass_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
         tc_fence_after();
         const uint32_t taddr = tmem + lane_base + acc * NR;
         uint64_t s2[2] = {0, 0};  // keys lane/4 and lane/4 + 8, even and odd rows
-        if (p0 + kTcKeys <= lo) {
+        bool masked = p0 + kTcKeys > lo;
+        if (!masked) {
           // every row sees every key of the tile
           uint32_t z[2][16];
           tmem_frag4(taddr, z[0]);
@@ -901,7 +909,13 @@ k_mass_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
             s2[0] = add2(s2[0], t2[0]);
             s2[1] = add2(s2[1], t2[1]);
           }
-        } else {
+          // an infinite key is NaN in the rows that add nothing (0·inf): the sums
+          // again, without those rows
+          float x, y;
+          upk2(add2(s2[0], s2[1]), x, y);
+          masked = __any_sync(0xFFFFFFFFu, x + y != x + y);
+        }
+        if (masked) {
           // the rows' limits: 32 rows a lane-wide load, one exchange per two rows
           const int r0 = a.row_off[pos.r], n = a.row_off[pos.r + 1] - r0;
           const int i0 = RT == 1 ? 0 : (2 * (p.rg0 + pos.rg) + wg) * p.tokens;

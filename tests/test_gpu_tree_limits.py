@@ -11,7 +11,7 @@ if not torch.cuda.is_available():
     pytest.skip("needs a CUDA device", allow_module_level=True)
 
 import tree_ref as ref  # noqa: E402
-from test_gpu_tree_decode import Tree, inside, kvc  # noqa: E402,F401
+from test_gpu_tree_decode import Mass, Tree, inside, kvc  # noqa: E402,F401
 
 NAN = float("nan")
 
@@ -142,3 +142,27 @@ def test_attn_values_that_are_not_finite_in_a_tile_of_no_weight(kvc, tile):  # n
     o, ls, ob, lb = t.want()
     inside(out, o, ob, "out")
     inside(lse, ls, lb, "lse")
+
+
+# --------------------------------------------- infinite keys under the weights
+
+@pytest.mark.parametrize("m,G,kind", [(3, 4, "path"), (1, 1, "path"), (7, 3, "path"), (9, 4, "path"),
+                                      (20, 8, "path"), (48, 4, "window"), (33, 1, "window"),
+                                      (100, 3, "window"), (130, 4, "path")])
+def test_mass_infinite_keys(kvc, m, G, kind):  # noqa: F811
+    """A key with an infinite component that every row's query meets with the same sign: weight 0 where
+    that makes all logits -inf, infinite where +inf, and nothing else is touched."""
+    for sign in (-1.0, 1.0):
+        t = Mass(m + G, [300, 290], [m, m], 2, 2, G, 128, 16, kind, decay=0.5)
+        t.q[..., 0] = sign
+        want, bound = t.want()
+        cached = [5, 100, 150, 0]                     # (all rows of windows up to 130 see these)
+        for r in range(2):
+            s = ref.slots(t.bt[r], 16, t.seq[r])
+            t.k[:, s[cached], :, 0] = float("inf")
+            old = t.old[:, r, :, cached].double() * t.decay
+            want[:, r, :, cached] = old if sign < 0 else float("inf")
+            bound[:, r, :, cached] = 2 * ref.U32
+        got = t.gpu().call(kvc)
+        torch.cuda.synchronize()
+        inside(got, want, bound, f"mass {sign}")
