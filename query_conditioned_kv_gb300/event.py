@@ -49,6 +49,16 @@ def _ws(nbytes: int, device) -> torch.Tensor:
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
+def _on(stream, device):
+    """The context that sends torch's own calls to `stream` as the library takes it: None (the
+    current stream), a Stream, or a raw handle (0: the default stream)."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return torch.cuda.stream(stream)
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    return torch.cuda.stream(torch.cuda.ExternalStream(handle, device=device) if handle
+                             else torch.cuda.default_stream(device))
+
+
 def groups_hint(L: int) -> int:
     """Layer groups of the event.  One group (score all layers, then select,
     then pack) measures fastest on GB300 for the 8B-class event: the
@@ -529,8 +539,9 @@ class TreeDecodeEvent:
     the first eviction has something to go by.
 
     The launches depend on the constructor's sizes only, so a step can be captured
-    in a CUDA graph.  ``stream`` None is the current stream; the buffers belong to
-    the stream they are first used on."""
+    in a CUDA graph.  ``stream`` is None (the current stream), a Stream or a raw
+    handle, as in the library's calls; the buffers belong to the stream they are
+    first used on."""
 
     def __init__(self, n_req: int, max_blocks: int, block_size: int, L: int, H: int, Hq: int,
                  D: int, n_slots: int, n_q: int, max_tree: int, budget: int, n_sink: int = 0,
@@ -581,7 +592,7 @@ class TreeDecodeEvent:
                       self.n_slots, block_table, self.max_blocks, self.ctx, self.n_mass,
                       self.n_req, self.L, self.H, self.Hq, self.D, self.BS, self.scale,
                       self.decay, self.mass, self.ws, self.dev_status, stream)
-        with torch.cuda.stream(stream):
+        with _on(stream, self.device):
             self.n_mass.copy_(self.ctx)
 
     def attend(self, layer, q, kpool, vpool, block_table, q_off, tree_mask=None, stream=None):
@@ -617,10 +628,10 @@ class TreeDecodeEvent:
         """The step after the last layer, on the path accepted from its outputs."""
         self.commit(kpool, vpool, block_table, q_off, path, n_path, stream)
         self.accumulate(q, kpool, block_table, stream)
-        with torch.cuda.stream(stream):
+        with _on(stream, self.device):
             self.t_end.add_(self.seq).sub_(self.ctx)
         self.evict(kpool, vpool, block_table, stream)
-        with torch.cuda.stream(stream):
+        with _on(stream, self.device):
             for n in (self.ctx, self.n_mass, self.n_pos):
                 n.copy_(self.n_out)
 

@@ -11,8 +11,9 @@ if not torch.cuda.is_available():
     pytest.skip("needs a CUDA device", allow_module_level=True)
 
 import tree_ref as ref  # noqa: E402
-from test_gpu_tree_decode import Mass, Tree, inside, kvc  # noqa: E402,F401
+from test_gpu_tree_decode import Mass, Tree, i32, inside, kvc  # noqa: E402,F401
 
+DEV = "cuda"
 NAN = float("nan")
 
 
@@ -166,3 +167,29 @@ def test_mass_infinite_keys(kvc, m, G, kind):  # noqa: F811
         got = t.gpu().call(kvc)
         torch.cuda.synchronize()
         inside(got, want, bound, f"mass {sign}")
+
+
+# --------------------------------------------------------- streams by handle
+
+@pytest.mark.parametrize("raw", [True, False])
+def test_event_takes_a_stream_or_its_handle(kvc, raw):  # noqa: F811
+    from test_gpu_tree_event import Serving
+    a, b = Serving(5, [50, 7], 9, observe=4), Serving(5, [50, 7], 9, observe=4)
+    side = torch.cuda.Stream()
+    handle = side.cuda_stream if raw else 0           # (0: the default stream)
+    q = torch.randn(2, 8, a.Hq, a.D, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).to(DEV)
+    lse = torch.full((2, 8, a.Hq), 5.0, device=DEV)
+    vis, off = i32([47, 48, 49, 50, 4, 5, 6, 7]), i32([0, 4, 8])
+    torch.cuda.synchronize()
+    for sv, stream in ((a, None), (b, handle)):
+        sv.ev.observe(q, lse, vis, off, sv.kd, sv.btd, stream)
+        for _ in range(2):
+            s = sv.draw()
+            torch.cuda.synchronize()
+            sv.write_nodes(s)
+            torch.cuda.synchronize()
+            sv.step({"q": s["q"].to(DEV), "mask_d": i32(s["mask"].view(np.int32)), "path_d": i32(s["path"]),
+                     "m_d": i32(s["m"])}, stream)
+            torch.cuda.synchronize()
+    for x, y in zip(a.state(), b.state()):
+        assert torch.equal(x, y)
