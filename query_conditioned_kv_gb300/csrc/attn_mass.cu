@@ -334,12 +334,12 @@ cudaError_t launch_rows(const MassArgs &a, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(k_mass_rows<D, NT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  static int per_sm = 0;  // (a property of the kernel; the query takes as long as a launch)
+  static std::atomic<int> cached{0};  // (a property of the kernel; the query takes as long as a launch)
+  int per_sm = cached.load(std::memory_order_relaxed);
   if (!per_sm) {
-    int n = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k_mass_rows<D, NT>, kMrThreads, smem);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k_mass_rows<D, NT>, kMrThreads, smem);
     if (e != cudaSuccess) return e;
-    per_sm = n;
+    cached.store(per_sm, std::memory_order_relaxed);
   }
   constexpr int tile = kMrWarps * 2048 / D;
   const int64_t most = (int64_t)a.L * a.n_req * a.H * ((a.cap + tile - 1) / tile);
@@ -385,6 +385,7 @@ constexpr int kTcThreads = (kTcEpi + kTcProd + 4) * 32;  // (the last warps idle
 constexpr int kTcMore = 88, kTcLess = 64;
 constexpr int kTcKeys = 128;                    // keys of a tile
 constexpr int kTcMaxK = 8;                      // K slots, at most
+constexpr size_t kTcSmemMax = 232448;           // of a CTA
 constexpr size_t kTcPartBytes = size_t(1) << 29;  // partial sums of one launch, about
 
 struct MassTc {
@@ -1097,9 +1098,8 @@ MassTc tc_plan(int n_req, int cap, int max_rows, int L, int H, int G, int D, int
   p.tokens = std::min(max_rows, p.NR / G);
   // K tiles in flight: what the two row tiles leave.  Even for RT 1, so that a
   // slot's tiles are all one MMA warp's.
-  const size_t most = 232448;
   p.k_slots = kTcMaxK;
-  while (p.k_slots > 2 && (TcSmem(D, p.NR, p.k_slots).bytes > most || (one && (p.k_slots & 1))))
+  while (p.k_slots > 2 && (TcSmem(D, p.NR, p.k_slots).bytes > kTcSmemMax || (one && (p.k_slots & 1))))
     p.k_slots--;
   p.n_cta = device_sm_count();
   p.idesc = make_idesc(128, p.NR);
@@ -1149,8 +1149,10 @@ cudaError_t launch_tc(const MassArgs &a, void *ws, cudaStream_t s) {
     return cudaErrorUnknown;
   if (p.q_box && !q_map(&tm_q, a.q, (int64_t)a.L * a.n_q, a.Hq, D, a.G, p.tokens))
     return cudaErrorUnknown;
+  // (the limit is the process's: the largest, so that no thread's call lowers it
+  // under another's launch)
   cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTcSmemMax);
   if (e != cudaSuccess) return e;
   static std::atomic<int> regs[2];  // a thread's registers at launch (RT 1, RT 2)
   if (!regs[pairs != 0].load(std::memory_order_relaxed)) {

@@ -37,8 +37,14 @@ namespace {
 
 constexpr int kEvThreads = 512;      // few segments
 constexpr int kEvThreadsMany = 256;  // many: more CTAs per SM, one's copies under another's selection
-constexpr int kEvThreadsBig = 1024;  // segments of more than 16,384 rows
+constexpr int kEvThreadsBig = 1024;  // long segments
 constexpr int kEvList = 1024;        // keys listed after the first level
+constexpr int kEvBigFrom = 16384;    // rows past which a segment takes kEvThreadsBig
+
+// Dynamic shared memory of a staged segment of `rows` rows.
+constexpr size_t staged_bytes(int rows) {
+  return ((size_t)rows + rows / 32 + 2) * sizeof(uint32_t);
+}
 
 struct EvictArgs {
   uint16_t *kpool, *vpool;  // [L][n_slots][H][D]
@@ -369,16 +375,19 @@ cudaError_t launch_mass_evict(uint16_t *kpool, uint16_t *vpool, int64_t n_slots,
               n_sink,    n_recent, page_inverse(BS)};
   const int n_seg = L * n_req * H;
   const bool staged = a.cap <= KVC_EVICT_STAGED_ROWS, many = n_seg >= 4 * device_sm_count();
-  const int nt = a.cap > 16384 ? kEvThreadsBig : many ? kEvThreadsMany : kEvThreads;
+  const int nt = a.cap > kEvBigFrom ? kEvThreadsBig : many ? kEvThreadsMany : kEvThreads;
   auto *kern = !staged               ? k_mass_evict<false, kEvThreadsBig>
                : nt == kEvThreadsBig ? k_mass_evict<true, kEvThreadsBig>
                : many                ? k_mass_evict<true, kEvThreadsMany>
                                      : k_mass_evict<true, kEvThreads>;
   size_t smem = 0;
   if (staged) {
-    smem = ((size_t)a.cap + a.cap / 32 + 2) * sizeof(uint32_t);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
+    // the limit is the process's: the kernel's largest, so that no thread's call
+    // lowers it under another's launch
+    smem = staged_bytes(a.cap);
+    const int most = (int)staged_bytes(nt == kEvThreadsBig ? KVC_EVICT_STAGED_ROWS : kEvBigFrom);
+    cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
   }
   // a cluster per segment while segments are few: two CTAs per SM in all

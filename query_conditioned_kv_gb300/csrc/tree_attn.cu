@@ -33,6 +33,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "kvc_internal.cuh"
 #include "mma_ptx.cuh"
@@ -1569,17 +1570,20 @@ cudaError_t launch_tc(const TreeArgs &a, cudaStream_t s) {
   p.idesc_s = make_idesc(128, 0);
   p.idesc_o = make_idesc(128, D) | (1u << 16);  // B (V) MN-major
   const size_t smem = 1024 + TreeTcSmem(D, a.rows, p.NS).bytes;
-  cudaError_t e =
-      cudaFuncSetAttribute(k_tree_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // (the limit is the process's: the largest, so that no thread's call lowers it
+  // under another's launch)
+  cudaError_t e = cudaFuncSetAttribute(
+      k_tree_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
   if (e != cudaSuccess) return e;
-  static int regs = 0;  // a thread's registers at launch
-  if (!regs) {
+  static std::atomic<int> regs{0};  // a thread's registers at launch
+  if (!regs.load(std::memory_order_relaxed)) {
     cudaFuncAttributes fa{};
     if ((e = cudaFuncGetAttributes(&fa, k_tree_tc<D>)) != cudaSuccess) return e;
-    regs = fa.numRegs;
+    regs.store(fa.numRegs, std::memory_order_relaxed);
   }
   // setmaxnreg.inc draws on what the block was launched with
-  if (regs * kTtThreads < 256 * (kTtMore + kTtLess)) return cudaErrorLaunchOutOfResources;
+  if (regs.load(std::memory_order_relaxed) * kTtThreads < 256 * (kTtMore + kTtLess))
+    return cudaErrorLaunchOutOfResources;
   k_tree_tc<D><<<a.n_cta, kTtThreads, smem, s>>>(tm_k, tm_v, tm_q, a, p);
   return cudaGetLastError();
 }

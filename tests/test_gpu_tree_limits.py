@@ -11,7 +11,7 @@ if not torch.cuda.is_available():
     pytest.skip("needs a CUDA device", allow_module_level=True)
 
 import tree_ref as ref  # noqa: E402
-from test_gpu_tree_decode import Mass, Tree, i32, inside, kvc  # noqa: E402,F401
+from test_gpu_tree_decode import Evict, Mass, Tree, i32, inside, kvc  # noqa: E402,F401
 
 DEV = "cuda"
 NAN = float("nan")
@@ -193,3 +193,40 @@ def test_event_takes_a_stream_or_its_handle(kvc, raw):  # noqa: F811
             torch.cuda.synchronize()
     for x, y in zip(a.state(), b.state()):
         assert torch.equal(x, y)
+
+
+# --------------------------------------------------------------- host threads
+
+def test_calls_of_several_sizes_from_several_threads(kvc):  # noqa: F811
+    """Two host threads evict from tables of different lengths at once: the shared-memory limit that one
+    sets never refuses the other's launch."""
+    import threading
+    errors, results = [], {}
+
+    def work(name, n, budget):
+        try:
+            e = Evict(n, [n], budget, 1, 1, 64, 16)
+            st = torch.cuda.Stream()
+            with torch.cuda.stream(st):
+                kd, vd = (torch.from_numpy(x).to(DEV).view(torch.bfloat16) for x in (e.k, e.v))
+                m, p = torch.from_numpy(e.mass).to(DEV), torch.from_numpy(e.pos).to(DEV)
+                mo, po, no = torch.empty_like(m), torch.empty_like(p), i32([0])
+                bt, seq, n_pos, t_end = i32(e.bt), i32(e.seq), i32(e.n_pos), i32(e.t_end)
+                status = i32([0])
+                st.synchronize()
+                for _ in range(3000):
+                    kvc.kvc_mass_evict(kd, vd, e.n_slots, bt, e.max_blocks, seq, n_pos, t_end, m, p, mo, po,
+                                       no, 1, 1, 1, 64, 16, budget, e.n_sink, e.n_recent, None, status, st)
+                st.synchronize()
+                results[name] = int(no)
+        except Exception as x:  # noqa: BLE001
+            errors.append(f"{name}: {x}")
+
+    threads = [threading.Thread(target=work, args=a) for a in
+               [("long", 15000, 4000), ("short", 200, 100), ("other", 900, 100)]]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    assert results == {"long": 4000, "short": 100, "other": 100}
