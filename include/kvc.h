@@ -928,8 +928,10 @@ kvc_status kvc_tree_commit(kvc_bf16 *kpool, kvc_bf16 *vpool, int64_t n_slots,
  *   mass        device fp32 [L][n_req][H][max_blocks·block_size] in/out
  *   ws          device scratch of kvc_attn_mass_workspace_size() bytes (may
  *               be NULL when that is 0)
- * Accuracy: products, exponents and sums are fp32, each weight within 2^-18
- * relative for |z|, |lse| ≤ 16.  No atomics: repeated calls on the same
+ * Accuracy: products, exponents and sums are fp32.  With z = scale·q·k, a weight
+ * is within 2^-24·((D + 8)·|scale|·Σ_d |q_d·k_d| + 4·(|z| + |lse|)) + 2^-21 of its
+ * value, relative (first order: fp32 products and sums of the logit, the exponent,
+ * the exponential), and the sum of n weights adds n·2^-24.  No atomics: repeated calls on the same
  * inputs give the same bits.
  * A seqused_k or row_off out of range is recorded as KVC_ERR_BOUNDS and the
  * request skipped; a row_idx outside [0, n_q) is recorded and the row
