@@ -230,3 +230,77 @@ def test_calls_of_several_sizes_from_several_threads(kvc):  # noqa: F811
         t.join()
     assert not errors, errors
     assert results == {"long": 4000, "short": 100, "other": 100}
+
+
+# ------------------------------------------------------ forms few calls reach
+
+@pytest.mark.parametrize("rows,G,max_blocks", [(640, 8, 1 << 18), (2100, 2, 300000)])
+def test_mass_of_more_rows_than_one_pass_holds(kvc, rows, G, max_blocks):  # noqa: F811
+    """Partial sums past their 512 MB (a long table): the rows' tiles take several passes that add to
+    one another, the first on top of the decayed weight."""
+    t = Mass(rows, [rows, rows // 3], [rows, rows // 3], 1, 1, G, 64, 32, "window", decay=0.75)
+    old_cap, old = t.cap, t.old
+    t.max_blocks = max_blocks
+    t.cap = max_blocks * 32
+    bt = np.full((2, max_blocks), -1)
+    bt[:, :t.bt.shape[1]] = t.bt
+    t.bt = bt
+    t.old = torch.zeros(1, 2, 1, t.cap)
+    t.old[..., :old_cap] = old
+    per = 1 * 2 * 1 * 2 * t.cap * 4
+    pairs = -(-rows // (2 * (256 // G)))
+    assert pairs > max(8, (1 << 29) // per)
+    n = kvc.kvc_attn_mass_workspace_size(2, max_blocks, rows, 1, 1, G, 64, 32)
+    assert per * 8 <= n < per * pairs
+    got = t.gpu().call(kvc)
+    torch.cuda.synchronize()
+    assert kvc.kvc_device_status(t.d["status"]) == 0
+    t.old = old
+    want, bound = t.want()
+    inside(got[..., :old_cap], want, bound, "mass")
+    assert not got[..., old_cap:].any()
+
+
+@pytest.mark.parametrize("weights,sink,recent,carried", [("equal", 2, 3, 0.5), ("random", 2, 3, 1.0),
+                                                         ("mixed", 0, 64, 0.0), ("mixed", 64, 0, 1.0),
+                                                         ("nan", 2, 3, 0.5), ("mixed", 10, 54, 0.7)])
+def test_evict_past_the_staged_length(kvc, weights, sink, recent, carried):  # noqa: F811
+    """Tables past the length whose keys fit the chip, requests of many rows, few, and under the budget;
+    in place and into other buffers."""
+    for in_place in (True, False):
+        e = Evict(sink + recent, [50000, 3000, 900, 0], 1000, 1, 1, 64, 16, sink, recent, carried, weights)
+        assert e.cap > kvc.EVICT_STAGED_ROWS
+        check_evict(kvc, e, in_place, status=8 if weights == "nan" else 0)
+
+
+@pytest.mark.parametrize("H,G,D,BS", [(8, 4, 128, 16), (2, 3, 64, 8)])
+def test_the_lse_is_what_the_recovery_score_takes(kvc, H, G, D, BS):  # noqa: F811
+    """Plain decoding's LSE against a 64-bit one, through kvc_recover_score."""
+    ctx, L = [70, 3, 500], 2
+    seq = np.array(ctx) + 1
+    trees = [Tree(7 + layer, ctx, [1, 1, 1], H, G, D, BS, "chain", poison=False) for layer in range(L)]
+    for t in trees[1:]:
+        t.bt = trees[0].bt
+    lses, wants, bounds = [], [], []
+    for t in trees:
+        lses.append(t.gpu().call(kvc)[1])
+        _, ls, _, lb = t.want()
+        wants.append(ls.float().to(DEV))
+        bounds.append(lb)
+    t0 = trees[0]
+    k = torch.stack([t.k for t in trees]).to(DEV)
+    q = torch.stack([t.q for t in trees], 1).contiguous().to(DEV)        # [n_req][L][Hq][D]
+    state = []
+    for lse in (lses, wants):
+        st = torch.zeros(3, t0.max_blocks * BS, device=DEV)
+        status = i32([0])
+        kvc.kvc_recover_score(q, torch.stack(lse, 1).contiguous(), k, t0.n_slots, i32(t0.bt), t0.max_blocks,
+                              i32(seq), i32([1, 1, 1]), 3, L, H, H * G, D, BS, st, None, status)
+        torch.cuda.synchronize()
+        assert kvc.kvc_device_status(status) == 0
+        state.append(st.double().cpu())
+    # the same kernel on both: each weight moves by its lse's error and by the exponent's rounding
+    tol = float(torch.stack(bounds).max()) + 64 * ref.U32 + 2 ** -20
+    for r in range(3):
+        a, b = state[0][r, :seq[r]], state[1][r, :seq[r]]
+        assert float(b.max()) > 0 and float(((a - b).abs() / b.clamp(min=1e-30)).max()) <= tol
