@@ -11,7 +11,7 @@ if not torch.cuda.is_available():
     pytest.skip("needs a CUDA device", allow_module_level=True)
 
 import tree_ref as ref  # noqa: E402
-from test_gpu_tree_decode import Evict, Mass, Tree, i32, inside, kvc  # noqa: E402,F401
+from test_gpu_tree_decode import Evict, Mass, Tree, check_evict, i32, inside, kvc  # noqa: E402,F401
 
 DEV = "cuda"
 NAN = float("nan")
