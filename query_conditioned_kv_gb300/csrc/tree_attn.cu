@@ -1589,24 +1589,28 @@ cudaError_t launch_tc(const TreeArgs &a, cudaStream_t s) {
 }
 
 // CTAs of the cluster that shares a unit, 0: the tiles are dealt out and joined.
-// In tiles that a CTA takes one after another: dealing out costs an even share
-// and about 17 (the join's launch and dependent loads, a second start); a cluster
-// its share for every wave of CTAs (clusters of few tiles want one wave; 16 CTAs
-// leave some SMs empty) and 3.5.  One token, 8 KV heads, 1 request: 4K 10.8 us by
-// clusters of 16 and 12.6 dealt out, 16K 21.7 and 17.4; 4 requests of 4K 14.6
-// (clusters of 8) and 18.3; 32 of 8K 145 (clusters of two) and 133; 24 of 6K, 16
-// heads of D 64, 92 (of two) and 109.
-int tree_cluster(const TreeArgs &a) {
+// In tiles that a CTA takes one after another.  Dealt out: an even share, which at D
+// 64 and one row tile takes 1.2 times as long, and about 17 (the join's launch and
+// dependent loads, a second start).  Clusters: a share for every wave of CTAs, of
+// which the last is charged by what it holds and 0.6 of the rest (its CTAs begin as
+// the others end), 5 to start each wave after the first, and 3.5; 16 CTAs leave some
+// SMs empty.  Both sides measured at 1474 sizes, 1 to 64 requests of 300 to 16K, 2 to
+// 16 heads, 4 to 32 rows: the form chosen takes 0.7 % longer than the best one in the
+// mean, and over 5 % longer at 67 (the most with 32 rows of D 64).
+// One token, 8 KV heads, 1 request: 4K 10.8 us by clusters of 16 and 12.6 dealt out,
+// 16K 21.7 and 17.4.  12 rows, 16 heads of D 64: 24 requests of 6K 107 us by clusters
+// of two and 115, of 8K 130 and 140, 48 of 4K 133 by single CTAs and 144.
+int tree_cluster(const TreeArgs &a, int D) {
   const double units = (double)a.n_req * a.H, sms = device_sm_count();
   const double kt = ceil((double)a.max_blocks * a.BS / a.tile);
   int best = 0;
-  double least = units * kt / (2 * sms) + 17;
+  double least = (D == 64 && a.rows == 16 ? 1.2 : 1) * units * kt / (2 * sms) + 17;
   for (int S = 1; S <= 16 && S <= kt; S *= 2) {
     // (two CTAs per SM; a GPC's 16 to 20 SMs hold fewer large clusters)
     const double room = S == 16 ? 0.85 * sms : S == 8 ? 1.69 * sms : S == 4 ? 1.9 * sms : 2 * sms;
-    const double waves = ceil(units * S / room);
-    if (waves > 1 && S > 1 && kt / S < 24) break;
-    const double cost = waves * ceil(kt / S) * (S == 16 ? 1.25 : 1) + 3.5;
+    const double full = units * S / room, waves = ceil(full);
+    const double share = waves > 1 ? full + 0.6 * (waves - full) : 1;
+    const double cost = share * ceil(kt / S) * (S == 16 ? 1.25 : 1) + 5 * (waves - 1) + 3.5;
     if (cost < least) {
       least = cost;
       best = S;
@@ -1681,7 +1685,7 @@ cudaError_t launch_tree_attn(const uint16_t *q, const uint16_t *kpool, const uin
   a.part_o = reinterpret_cast<float *>(ws);
   a.part_ml = reinterpret_cast<float2 *>(a.part_o + (size_t)2 * a.n_cta * a.rows * D);
   cudaError_t e;
-  const int cluster = max_tree * a.G > kRowsMax ? 0 : tree_cluster(a);
+  const int cluster = max_tree * a.G > kRowsMax ? 0 : tree_cluster(a, D);
   if (max_tree * a.G > kRowsMax)
     e = D == 128 ? launch_tc<128>(a, s) : launch_tc<64>(a, s);
   else
