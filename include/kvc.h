@@ -850,8 +850,9 @@ kvc_status kvc_tail_compact(kvc_bf16 *kpool, kvc_bf16 *vpool, int64_t n_slots, i
  *               size depends on the current device's SM count)
  * Accuracy: logits, softmax statistics and the value sums are fp32; the
  * weights exp(z − max) are rounded to bf16 for the product with V (their sum
- * is taken before that rounding), out is rounded once to bf16.  Repeated
- * calls give the same bits.
+ * is taken before that rounding), out is rounded once to bf16.  That holds for
+ * logits up to 2^126, as finely as fp32 tells them apart; a NaN among the logits
+ * a row sees makes its out and lse NaN.  Repeated calls give the same bits.
  * A request whose ctx_len or q_off is out of range (negative, T > max_tree,
  * c + T > max_blocks·block_size, rows past n_q) is recorded as
  * KVC_ERR_BOUNDS and its rows are left untouched; a visible position whose
@@ -931,8 +932,8 @@ kvc_status kvc_tree_commit(kvc_bf16 *kpool, kvc_bf16 *vpool, int64_t n_slots,
  * Accuracy: products, exponents and sums are fp32.  With z = scale·q·k, a weight
  * is within 2^-24·((D + 8)·|scale|·Σ_d |q_d·k_d| + 4·(|z| + |lse|)) + 2^-21 of its
  * value, relative (first order: fp32 products and sums of the logit, the exponent,
- * the exponential), and the sum of n weights adds n·2^-24.  No atomics: repeated calls on the same
- * inputs give the same bits.
+ * the exponential), and the sum of n weights adds n·2^-24.  No atomics: repeated
+ * calls on the same inputs give the same bits.
  * A seqused_k or row_off out of range is recorded as KVC_ERR_BOUNDS and the
  * request skipped; a row_idx outside [0, n_q) is recorded and the row
  * ignored; a block id outside the pool is recorded and its positions gain

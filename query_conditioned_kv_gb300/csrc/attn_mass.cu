@@ -17,8 +17,8 @@
 // in equal contiguous runs to the CTAs; each of a CTA's four warps streams
 // its 16 (D 128) or 32 (D 64) keys of a tile through a private cp.async ring
 // (4 stages of 4 KB).  mma.sync m16n8k16, fp32 accumulators.  Measured: accepted
-// paths of up to 6 nodes × 4 heads, 8 requests of 4K to 8K, 12 layers: 223 us,
-// 5.6 TB/s, 84 % of a plain copy's rate.
+// paths of up to 6 nodes × 4 heads, 8 requests of 4K to 8K, 12 layers: 225 us,
+// 5.5 TB/s, 83 % of a plain copy's rate.
 #include <limits.h>
 #include <math.h>
 
@@ -368,11 +368,11 @@ cudaError_t launch_rows(const MassArgs &a, cudaStream_t s) {
 // where this moves 32 KB, and could not be kept ahead of the tensor core
 // (measured: 2080 cycles a product against 1008).
 //
-// Bound: RT = 1 the K stream (32 rows × 4 heads over 128K, four layers: 187 us,
-// 5.9 TB/s, 89 % of a plain copy's rate); RT = 2 the products (1008 cycles per 128
+// Bound: RT = 1 the K stream (32 rows × 4 heads over 128K, four layers: 191 us,
+// 5.8 TB/s, 87 % of a plain copy's rate); RT = 2 the products (1008 cycles per 128
 // keys × 256 rows) and the ex2s (1024), which cannot all overlap, for tensor
-// memory holds two accumulators of 256 columns: 8192 causal rows × 4 heads 324 us,
-// 850 TFLOP/s.  Four accumulators of 128 columns took 349 us (an instruction of
+// memory holds two accumulators of 256 columns: 8192 causal rows × 4 heads 326 us,
+// 845 TFLOP/s.  Four accumulators of 128 columns took 349 us (an instruction of
 // half the columns takes 105 cycles of 126), eight epilogue warps 337.
 //
 // Work is dealt out by key tile in equal contiguous runs, one per CTA.

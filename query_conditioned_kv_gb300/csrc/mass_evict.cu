@@ -22,9 +22,11 @@
 // Bound: few rows leave, latency (64 of 4160 rows, 288 segments: 16.5 us, 2.3 TB/s;
 // weights, levels, sweep, block ids and rows wait for one another, about 15
 // thousand cycles); many, random 256-byte pieces read and written (6K to 4K, 1152
-// segments: 206 to 237 us from one block table to another, 67 to 77 % of a plain
+// segments: 206 to 247 us from one block table to another, 64 to 77 % of a plain
 // copy's rate; 512 threads a CTA 5 % more, eight rows in flight a warp slower than
-// four).
+// four).  By the table's length, 64 of 4160 rows: up to 16K positions 17 us, to 48K 25
+// (one CTA of 1024 threads per SM), past the staged length 50 (weights and positions
+// read again at every level, one CTA per segment).
 #include <algorithm>
 
 #include "kvc_internal.cuh"

@@ -572,11 +572,14 @@ k_tree_rows(TreeArgs a) {
 // slot: a barrier's parity tells only two uses apart, and two consumers of one
 // ring may be further apart than that.
 //
-// Bound: with 128 rows the K and V stream (128K of one request, 108 us, 5.0
+// Bound: with 128 rows the K and V stream (128K of one request, 109 us, 4.9
 // TB/s); with 256 the products, about 105 cycles an instruction at N = 128 where
 // N = 256 would take 126 (tensor memory holds S 256 + O 256 columns, so S of 256
 // columns could not be worked on while the next is made): 64 nodes × 4 heads, 16
-// requests of 16K to 32K, 415 us, 745 TFLOP/s and 3.9 TB/s.
+// requests of 16K to 32K, 412 to 443 us from one batch of trees to another, 700 to
+// 750 TFLOP/s and 3.7 to 3.9 TB/s.  One stage at a time is in flight where a page has
+// no box: 20 nodes × 4 heads, 4 requests of 32K, 167 us with pages of 5 or 12 and 118
+// with pages of 16.
 
 constexpr int kTtKeys = 128;
 constexpr int kTtSoft = 8;
