@@ -62,9 +62,9 @@ __device__ __forceinline__ bool mass_request(const MassArgs &a, int r, int &seq,
 constexpr int kMrWarps = 4;
 constexpr int kMrThreads = kMrWarps * 32;
 // Widest row set (rows · G) of this path.  Both sides, 8 requests of 8K, 12
-// layers, 24 rows: D 128 222 us here and 222 on the tensor cores, D 64 132 and
-// 203; 512 positions of one request 6.1 and 8.6; 64 rows of a 128K window 322
-// and 178.
+// layers, 24 rows: D 128 238 us here and 240 on the tensor cores, D 64 140 and
+// 216; 32 rows, 512 positions of one request, 12 layers 13.2 and 13.1, 128K, four
+// layers 193 and 185; 64 rows of a 128K window 322 and 178.
 constexpr int kMrMaxRows = 32;
 constexpr int kMrStages = 4;
 constexpr int kMrStage = 4096;  // bytes of one warp's stage

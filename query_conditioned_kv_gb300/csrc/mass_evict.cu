@@ -91,7 +91,9 @@ k_mass_evict(EvictArgs a) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // a thread's first rows, asked for together with the sizes (any row below cap
   // may be read); the block ids on their way to L1, and the first level's
-  // histogram cleared, meanwhile
+  // histogram cleared, meanwhile.  (4, 6, 10 or 16 of them: 1100 rows 13.1, 13.3,
+  // 14.0 and 14.8 us, 8 requests of 2112 56, 55, 53 and 54, 4 of 6144 265, 263, 262
+  // and 260.)
   constexpr int U1 = 10;
   const int64_t base = (int64_t)seg * a.cap;
   float m[U1];

@@ -1539,8 +1539,9 @@ k_tree_join(TreeArgs a) {
 }
 
 // Rows up to which the narrow instruction is used.  Both sides, 64 requests of
-// 8K: 4 rows 251 us here and 294 on the tensor cores, 16 rows 256 and 304, 32
-// rows 294 and 310; 128K of one request, 32 rows 100 and 103.
+// 8K: 4 rows 250 us here and 294 on the tensor cores, 16 rows 256 and 298, 32
+// rows 287 and 303; 1K of one request, 16 rows 11 and 20; 128K, 32 rows 108 and
+// 105.
 constexpr int kRowsMax = 32;
 constexpr int kTcRowsMax = 256;
 
