@@ -1001,6 +1001,163 @@ kvc_status kvc_mass_evict(kvc_bf16 *kpool, kvc_bf16 *vpool, int64_t n_slots,
                           int32_t n_recent, void *ws, size_t ws_bytes, int32_t *dev_status,
                           cudaStream_t stream);
 
+/* ========================================================================
+ * Filling the paged cache, and a history held in 8 bits (no counterpart on the
+ * pages, which start from a filled cache).  What a serving loop runs before and
+ * beside the calls above, on the same pools, block table and position → slot
+ * rule:
+ *   kvc_qkv_rope     per layer: new tokens' queries and keys are normed and
+ *                    rotated, keys and values written into the cache;
+ *   kvc_prompt_attn  per layer: the new rows attend to the cache, causally;
+ *   kvc_q8_pack      all layers: blocks that have become history move to 8 bits;
+ *   kvc_q8_attn      per layer: kvc_tree_attn with a history in 8 bits before
+ *                    the bf16 rows.
+ * Any H in [1, 256], Hq a multiple of H with Hq ≤ 256, D ∈ {64, 128} and block_size in
+ * [1, 64].
+ * ====================================================================== */
+
+/* ------------------------------------------------------------------------
+ * New tokens of one layer on their way into the cache.  Token x of the call,
+ * with q_off[r] ≤ x < q_off[r+1], is request r's and takes the position
+ * p = ctx_len[r] + x − q_off[r].  Per head, in fp32:
+ *   y = u·w / sqrt(mean(u²) + eps)  for queries (w = wq) and keys (w = wk);
+ *       y = u where the weight is NULL;
+ *   (y_j, y_{j+D/2}) → (y_j·c − y_{j+D/2}·s, y_{j+D/2}·c + y_j·s), (c, s) the
+ *       j-th pair of row pos[x] of rope_tab (kvc_rope_table with pos0 = 0);
+ * queries go to q_out, keys to kpool and values, as they are, to vpool at p's
+ * slot.  k_raw takes the keys before the rotation (what kvc_build_meank and the
+ * packs take as raw keys).
+ *   q, k, v     device bf16: token x's heads at q + x·q_stride, k + x·k_stride,
+ *               v + x·v_stride (elements, multiples of 8; ≥ Hq·D, H·D, H·D), so
+ *               that the parts of one fused projection can be passed
+ *   wq, wk      device bf16 [D], either may be NULL
+ *   rope_tab    device fp32 [n_pos][D/2][2];  pos  device int32 [n_tok], the
+ *               position of the rotation (NULL: p, the place in the cache; the two
+ *               differ once a cache has evicted rows)
+ *   q_off       device int32 [n_req+1], ascending;  ctx_len device int32 [n_req]
+ *   q_out       device bf16 [n_tok][Hq][D]; may be q itself where q_stride = Hq·D
+ *   kpool, vpool device bf16 [n_slots][H][D]: one layer of the pools
+ *   k_raw       device bf16, token x of head h at k_raw + h·raw_stride + x·D
+ *               (raw_stride ≥ n_tok·D, a multiple of 8), may be NULL
+ * Of tokens outside every request (before q_off[0], from q_off[n_req] on) nothing is
+ * written.  Each value is rounded once to bf16.
+ * Repeated calls give the same bits.
+ * A request whose ctx_len or q_off is out of range (rows past n_tok or past
+ * max_blocks·block_size) is recorded as KVC_ERR_BOUNDS and left out; so is a token
+ * whose pos is outside [0, n_pos).  A block id outside the pool is recorded and the
+ * token's key and value are not stored.
+ * Errors: KVC_ERR_INVALID_ARG (NULL, sizes < 1, eps negative or not finite, outputs
+ * that overlap inputs or each other), KVC_ERR_SHAPE (D, Hq % H, Hq > 256, block_size
+ * > 64, strides), KVC_ERR_ALIGN (16 bytes).
+ * ---------------------------------------------------------------------- */
+kvc_status kvc_qkv_rope(const kvc_bf16 *q, int64_t q_stride, const kvc_bf16 *k,
+                        int64_t k_stride, const kvc_bf16 *v, int64_t v_stride, int32_t n_tok,
+                        const kvc_bf16 *wq, const kvc_bf16 *wk, float eps, const float *rope_tab,
+                        int32_t n_pos, const int32_t *pos, const int32_t *q_off,
+                        const int32_t *ctx_len, int32_t n_req, const int32_t *block_table,
+                        int32_t max_blocks, kvc_bf16 *kpool, kvc_bf16 *vpool, int64_t n_slots,
+                        int32_t H, int32_t Hq, int32_t D, int32_t block_size, kvc_bf16 *q_out,
+                        kvc_bf16 *k_raw, int64_t raw_stride, int32_t *dev_status,
+                        cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Causal attention of the new rows of packed prompts, one layer.  Request r has
+ * c = ctx_len[r] positions before the call (0: a whole prompt; more: a chunk, or
+ * a prompt behind a shared prefix) and T = q_off[r+1] − q_off[r] ≤ max_rows new
+ * rows, whose keys and values are in the pools at c … c + T − 1.  Row i sees the
+ * positions 0 … c + i:
+ *   z_p = scale · q·k_p;  lse = ln Σ exp z_p;  out = Σ exp(z_p − lse) · v_p
+ * which is kvc_tree_attn's chain without its limit on T, made for many rows.
+ *   q           device bf16 [n_q][Hq][D]
+ *   kpool, vpool device bf16 [n_slots][H][D]: one layer of the pools
+ *   block_table device int32 [n_req][max_blocks]
+ *   ctx_len     device int32 [n_req];  q_off  device int32 [n_req+1]
+ *   out         device bf16 [n_q][Hq][D];  lse  device fp32 [n_q][Hq] (natural
+ *               log; kvc_attn_mass and kvc_recover_score take it)
+ * Accuracy, NaN and infinities: as kvc_tree_attn; positions that a row does not
+ * see never reach its result, whatever they hold.  A row that sees nothing (every
+ * page of it outside the pool) gets out = 0 and lse = −inf.  Rows of q outside every
+ * request are left alone.  No workspace.  Repeated calls give the same bits.
+ * A request whose ctx_len or q_off is out of range (negative, T > max_rows, c + T >
+ * max_blocks·block_size, rows past n_q) is recorded as KVC_ERR_BOUNDS and its rows
+ * are left untouched; a visible position whose block id is outside the pool is
+ * recorded and treated as not visible.
+ * Errors: KVC_ERR_INVALID_ARG (NULL, sizes < 1, scale not finite), KVC_ERR_SHAPE (D,
+ * Hq % H, Hq > 256, block_size > 64, max_rows > KVC_TREE_MAX_TOKENS, too many
+ * positions), KVC_ERR_ALIGN (16 bytes; lse 4).
+ * ---------------------------------------------------------------------- */
+kvc_status kvc_prompt_attn(const kvc_bf16 *q, const kvc_bf16 *kpool, const kvc_bf16 *vpool,
+                           int64_t n_slots, const int32_t *block_table, int32_t max_blocks,
+                           const int32_t *ctx_len, const int32_t *q_off, int32_t n_req,
+                           int32_t n_q, int32_t max_rows, int32_t H, int32_t Hq, int32_t D,
+                           int32_t block_size, float scale, kvc_bf16 *out, float *lse,
+                           int32_t *dev_status, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Blocks of the cache in 8 bits, all layers.  For pair i < n with src = src_block[i]
+ * and dst = dst_block[i], every layer l and head h, K and V each on their own:
+ *   s = the least power of two, from 2^-126 on, with max|x| ≤ 448·s over the
+ *       block's block_size·D values of the head (1 where they are all 0)
+ *   k8[l][dst][h][j] = e4m3(kpool[l][src·block_size + j][h] / s),  kscale[l][dst][h] = s
+ * rounded to nearest even; the values stand for k8·kscale.
+ *   kpool, vpool device bf16 [L][n_slots][H][D]
+ *   k8, v8      device e4m3 [L][n_blocks8][H][block_size][D] (the bytes)
+ *   kscale, vscale device fp32 [L][n_blocks8][H]
+ *   src_block, dst_block device int32 [n]; a pair of two negative ids is left out
+ *               (so that a captured graph can pack fewer than n).  No dst twice.
+ * All block_size rows of a block are packed, so a block goes when it is full.  The
+ * bf16 rows are left as they are.
+ * An infinity is stored as ±448·s (s from the finite values) and a NaN as NaN; either
+ * is recorded as KVC_ERR_NAN.  A block id outside its pool is recorded as
+ * KVC_ERR_BOUNDS and the pair left out.
+ * Errors: KVC_ERR_INVALID_ARG (NULL, sizes < 1, outputs that overlap inputs or each
+ * other), KVC_ERR_SHAPE, KVC_ERR_ALIGN (16 bytes; scales 4).
+ * ---------------------------------------------------------------------- */
+kvc_status kvc_q8_pack(const kvc_bf16 *kpool, const kvc_bf16 *vpool, int64_t n_slots,
+                       uint8_t *k8, uint8_t *v8, float *kscale, float *vscale,
+                       int64_t n_blocks8, const int32_t *src_block, const int32_t *dst_block,
+                       int32_t n, int32_t L, int32_t H, int32_t D, int32_t block_size,
+                       int32_t *dev_status, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Attention over a history in 8 bits and the bf16 rows behind it, one layer: as
+ * kvc_tree_attn (T = 1 and no mask: plain decoding), where request r's rows also
+ * see all len8[r] positions of its history, position p in block table8[r][p /
+ * block_size]:
+ *   z_p = scale · kscale·(q·k8_p) and v_p = vscale·v8_p there.
+ *   k8, v8      device e4m3 [n_blocks8][H][block_size][D], kscale, vscale device
+ *               fp32 [n_blocks8][H]: one layer of what kvc_q8_pack writes (any
+ *               finite scales > 0)
+ *   table8      device int32 [n_req][max_blocks8];  len8 device int32 [n_req] (0: no
+ *               history; it may end inside a block)
+ *   the others  as kvc_tree_attn: kpool, vpool and block_table hold the ctx_len[r]
+ *               bf16 rows that follow the history and the nodes behind them
+ *   ws          device scratch of kvc_q8_attn_workspace_size() bytes (the size
+ *               depends on the current device's SM count)
+ * Made for few rows per KV head: every 32 of them read the cache once.
+ * Accuracy: the products with k8 and v8 are exact but for q's values below 2^-39
+ * of the row's largest; logits, softmax statistics and sums are fp32; the weights of
+ * the history's values are rounded to fp16 (a weight below 2^-14 of the row's largest
+ * weight times scale to 2^-25 of that), those of the bf16 rows to bf16, out once to
+ * bf16.  Repeated calls give the same bits.
+ * A request whose len8, ctx_len or q_off is out of range is recorded as
+ * KVC_ERR_BOUNDS and its rows are left untouched; a position whose block id is
+ * outside its pool is recorded and treated as not visible.
+ * Errors: as kvc_tree_attn (kscale, vscale: aligned to 4 bytes).
+ * ---------------------------------------------------------------------- */
+size_t kvc_q8_attn_workspace_size(int32_t n_req, int32_t max_blocks8, int32_t max_blocks,
+                                  int32_t max_tree, int32_t H, int32_t Hq, int32_t D,
+                                  int32_t block_size);
+kvc_status kvc_q8_attn(const kvc_bf16 *q, const uint8_t *k8, const uint8_t *v8,
+                       const float *kscale, const float *vscale, int64_t n_blocks8,
+                       const int32_t *table8, int32_t max_blocks8, const int32_t *len8,
+                       const kvc_bf16 *kpool, const kvc_bf16 *vpool, int64_t n_slots,
+                       const int32_t *block_table, int32_t max_blocks, const int32_t *ctx_len,
+                       const int32_t *q_off, const uint32_t *tree_mask, int32_t mask_words,
+                       int32_t n_req, int32_t n_q, int32_t max_tree, int32_t H, int32_t Hq,
+                       int32_t D, int32_t block_size, float scale, kvc_bf16 *out, float *lse,
+                       void *ws, size_t ws_bytes, int32_t *dev_status, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

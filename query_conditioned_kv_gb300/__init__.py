@@ -32,6 +32,8 @@ __all__ = [
     "kvc_tree_attn_workspace_size", "kvc_tree_attn", "kvc_tree_commit",
     "kvc_attn_mass_workspace_size", "kvc_attn_mass",
     "kvc_mass_evict_workspace_size", "kvc_mass_evict",
+    "kvc_qkv_rope", "kvc_prompt_attn", "kvc_q8_pack",
+    "kvc_q8_attn_workspace_size", "kvc_q8_attn",
     "kvc_pack_tiered_slots", "kvc_repo_plan", "KvcRepo",
 ]
 
@@ -147,6 +149,16 @@ _SIGS = {
     "kvc_mass_evict_workspace_size": (_SZ, [_I32] * 6),
     "kvc_mass_evict": (_c.c_int, [_P, _P, _I64, _P, _I32] + [_P] * 8 + [_I32] * 8
                        + [_P, _SZ, _P, _P]),
+    "kvc_qkv_rope": (_c.c_int, [_P, _I64, _P, _I64, _P, _I64, _I32, _P, _P, _c.c_float, _P, _I32,
+                                _P, _P, _P, _I32, _P, _I32, _P, _P, _I64] + [_I32] * 4
+                     + [_P, _P, _I64, _P, _P]),
+    "kvc_prompt_attn": (_c.c_int, [_P, _P, _P, _I64, _P, _I32, _P, _P] + [_I32] * 7
+                        + [_c.c_float, _P, _P, _P, _P]),
+    "kvc_q8_pack": (_c.c_int, [_P, _P, _I64] + [_P] * 4 + [_I64, _P, _P] + [_I32] * 5
+                    + [_P, _P]),
+    "kvc_q8_attn_workspace_size": (_SZ, [_I32] * 8),
+    "kvc_q8_attn": (_c.c_int, [_P] * 5 + [_I64, _P, _I32, _P, _P, _P, _I64, _P, _I32, _P, _P, _P]
+                    + [_I32] * 8 + [_c.c_float, _P, _P, _P, _SZ, _P, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(lib, _name)
@@ -640,3 +652,79 @@ def kvc_mass_evict(kpool, vpool, n_slots, block_table, max_blocks, seqused_k, n_
                            _ptr(mass_out), _ptr(pos_out), _ptr(n_out), n_req, L, H, D,
                            block_size, budget, n_sink, n_recent, _ptr(ws), _ws_bytes(ws),
                            _ptr(dev_status), _stream(stream)), "kvc_mass_evict")
+
+
+def _rows_ptr(t, row):
+    """Device pointer and row stride (elements) of a tensor [n][row] or [n][heads][D]
+    whose rows are packed; a part of a wider row, as of a fused projection, is one."""
+    if not t.is_cuda:
+        raise ValueError("libkvc takes device tensors only")
+    packed = t.dim() >= 2 and t[0].is_contiguous() and t[0].numel() == row
+    if not packed:
+        raise ValueError(f"libkvc takes rows of {row} packed elements "
+                         f"(got shape {tuple(t.shape)}, strides {t.stride()})")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else row
+
+
+def kvc_qkv_rope(q, k, v, n_tok, wq, wk, eps, rope_tab, n_pos, pos, q_off, ctx_len, n_req,
+                 block_table, max_blocks, kpool, vpool, n_slots, H, Hq, D, block_size, q_out,
+                 k_raw=None, dev_status=None, stream=None):
+    """Norms and rotates one layer's new queries and keys, and writes keys and values
+    into the paged cache.  q, k and v are [n_tok][heads·D] (or [n_tok][heads][D]) with
+    any row stride: slices of a fused projection's output are taken as they are.  wq or
+    wk None: no norm.  pos None: the rotation goes by the place in the cache.  k_raw
+    [H][≥ n_tok][D] takes the keys before the rotation."""
+    (qp, qs), (kp, ks), (vp, vs) = _rows_ptr(q, Hq * D), _rows_ptr(k, H * D), _rows_ptr(v, H * D)
+    if min(len(q), len(k), len(v)) < n_tok:
+        raise ValueError(f"kvc_qkv_rope: q, k and v hold fewer than {n_tok} rows")
+    raw = 0 if k_raw is None else k_raw.stride(0)
+    if k_raw is not None and not (k_raw.is_cuda and k_raw.dim() == 3 and k_raw.shape[0] == H
+                                  and k_raw.shape[1] >= n_tok and k_raw[0].is_contiguous()
+                                  and k_raw.shape[2] == D):
+        raise ValueError("kvc_qkv_rope: k_raw is a device tensor [H][>= n_tok][D], each head's "
+                         f"rows packed (got shape {tuple(k_raw.shape)}, strides {k_raw.stride()})")
+    if H == 1 and k_raw is not None:
+        raw = max(raw, n_tok * D)
+    _ok(lib.kvc_qkv_rope(qp, qs, kp, ks, vp, vs, n_tok, _ptr(wq), _ptr(wk), eps, _ptr(rope_tab),
+                         n_pos, _ptr(pos), _ptr(q_off), _ptr(ctx_len), n_req, _ptr(block_table),
+                         max_blocks, _ptr(kpool), _ptr(vpool), n_slots, H, Hq, D, block_size,
+                         _ptr(q_out), None if k_raw is None else k_raw.data_ptr(), raw,
+                         _ptr(dev_status), _stream(stream)), "kvc_qkv_rope")
+
+
+def kvc_prompt_attn(q, kpool, vpool, n_slots, block_table, max_blocks, ctx_len, q_off, n_req,
+                    n_q, max_rows, H, Hq, D, block_size, scale, out, lse, dev_status=None,
+                    stream=None):
+    """Causal attention of packed prompts' new rows over one layer of a paged cache that
+    holds their keys and values."""
+    _ok(lib.kvc_prompt_attn(_ptr(q), _ptr(kpool), _ptr(vpool), n_slots, _ptr(block_table),
+                            max_blocks, _ptr(ctx_len), _ptr(q_off), n_req, n_q, max_rows, H, Hq,
+                            D, block_size, scale, _ptr(out), _ptr(lse), _ptr(dev_status),
+                            _stream(stream)), "kvc_prompt_attn")
+
+
+def kvc_q8_pack(kpool, vpool, n_slots, k8, v8, kscale, vscale, n_blocks8, src_block, dst_block,
+                n, L, H, D, block_size, dev_status=None, stream=None):
+    """Blocks of a paged cache in 8 bits, all layers (k8, v8: uint8 or float8_e4m3fn)."""
+    _ok(lib.kvc_q8_pack(_ptr(kpool), _ptr(vpool), n_slots, _ptr(k8), _ptr(v8), _ptr(kscale),
+                        _ptr(vscale), n_blocks8, _ptr(src_block), _ptr(dst_block), n, L, H, D,
+                        block_size, _ptr(dev_status), _stream(stream)), "kvc_q8_pack")
+
+
+def kvc_q8_attn_workspace_size(n_req, max_blocks8, max_blocks, max_tree, H, Hq, D,
+                               block_size) -> int:
+    return int(lib.kvc_q8_attn_workspace_size(n_req, max_blocks8, max_blocks, max_tree, H, Hq, D,
+                                              block_size))
+
+
+def kvc_q8_attn(q, k8, v8, kscale, vscale, n_blocks8, table8, max_blocks8, len8, kpool, vpool,
+                n_slots, block_table, max_blocks, ctx_len, q_off, tree_mask, mask_words, n_req,
+                n_q, max_tree, H, Hq, D, block_size, scale, out, lse, ws, dev_status=None,
+                stream=None):
+    """kvc_tree_attn with a history in 8 bits before the bf16 rows."""
+    _ok(lib.kvc_q8_attn(_ptr(q), _ptr(k8), _ptr(v8), _ptr(kscale), _ptr(vscale), n_blocks8,
+                        _ptr(table8), max_blocks8, _ptr(len8), _ptr(kpool), _ptr(vpool), n_slots,
+                        _ptr(block_table), max_blocks, _ptr(ctx_len), _ptr(q_off),
+                        _ptr(tree_mask), mask_words, n_req, n_q, max_tree, H, Hq, D, block_size,
+                        scale, _ptr(out), _ptr(lse), _ptr(ws), _ws_bytes(ws), _ptr(dev_status),
+                        _stream(stream)), "kvc_q8_attn")

@@ -680,4 +680,143 @@ kvc_status kvc_mass_evict(kvc_bf16 *kpool, kvc_bf16 *vpool, int64_t n_slots,
                                           n_recent, ws, dev_status, stream));
 }
 
+// ---- filling the paged cache, and a history held in 8 bits
+
+kvc_status kvc_qkv_rope(const kvc_bf16 *q, int64_t q_stride, const kvc_bf16 *k,
+                        int64_t k_stride, const kvc_bf16 *v, int64_t v_stride, int32_t n_tok,
+                        const kvc_bf16 *wq, const kvc_bf16 *wk, float eps, const float *rope_tab,
+                        int32_t n_pos, const int32_t *pos, const int32_t *q_off,
+                        const int32_t *ctx_len, int32_t n_req, const int32_t *block_table,
+                        int32_t max_blocks, kvc_bf16 *kpool, kvc_bf16 *vpool, int64_t n_slots,
+                        int32_t H, int32_t Hq, int32_t D, int32_t block_size, kvc_bf16 *q_out,
+                        kvc_bf16 *k_raw, int64_t raw_stride, int32_t *dev_status,
+                        cudaStream_t stream) {
+  if (!q || !k || !v || !rope_tab || !q_off || !ctx_len || !block_table || !kpool || !vpool ||
+      !q_out || n_tok < 1 || n_pos < 1 || !(eps >= 0.f) || !isfinite(eps))
+    return KVC_ERR_INVALID_ARG;
+  const kvc_status st = paged_status(1, n_req, H, D, block_size, max_blocks, n_slots);
+  if (st != KVC_OK) return st;
+  if (!heads_ok(H, Hq)) return KVC_ERR_SHAPE;
+  const int64_t qrow = (int64_t)Hq * D, krow = (int64_t)H * D, raw = (int64_t)n_tok * D;
+  const int64_t most = INT64_MAX / 2 / INT32_MAX;  // (so that no offset below overflows)
+  if (q_stride < qrow || k_stride < krow || v_stride < krow || q_stride > most ||
+      k_stride > most || v_stride > most || (k_raw && (raw_stride < raw || raw_stride > most)) ||
+      q_stride % 8 || k_stride % 8 || v_stride % 8 || (k_raw && raw_stride % 8))
+    return KVC_ERR_SHAPE;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || (wq && !aligned16(wq)) ||
+      (wk && !aligned16(wk)) || !aligned16(rope_tab) || !aligned16(kpool) || !aligned16(vpool) ||
+      !aligned16(q_out) || (k_raw && !aligned16(k_raw)))
+    return KVC_ERR_ALIGN;
+  const size_t pool = (size_t)n_slots * H * D * 2, reqs = (size_t)n_req * 4;
+  auto rows = [&](int64_t stride, int64_t row) { return (size_t)((n_tok - 1) * stride + row) * 2; };
+  if (outputs_overlap({{kpool, pool},
+                       {vpool, pool},
+                       {q_out, (size_t)n_tok * qrow * 2},
+                       {k_raw, k_raw ? (size_t)((H - 1) * raw_stride + raw) * 2 : 0}},
+                      {{q_out == q && q_stride == qrow ? nullptr : q, rows(q_stride, qrow)},
+                       {k, rows(k_stride, krow)},
+                       {v, rows(v_stride, krow)},
+                       {wq, (size_t)D * 2},
+                       {wk, (size_t)D * 2},
+                       {rope_tab, (size_t)n_pos * D * 4},
+                       {pos, (size_t)n_tok * 4},
+                       {q_off, reqs + 4},
+                       {ctx_len, reqs},
+                       {block_table, reqs * max_blocks}}))
+    return KVC_ERR_INVALID_ARG;
+  return from_cuda(kvc::launch_qkv_rope(q, q_stride, k, k_stride, v, v_stride, n_tok, wq, wk, eps,
+                                        rope_tab, n_pos, pos, q_off, ctx_len, n_req, block_table,
+                                        max_blocks, kpool, vpool, n_slots, H, Hq, D, block_size,
+                                        q_out, k_raw, raw_stride, dev_status, stream));
+}
+
+kvc_status kvc_prompt_attn(const kvc_bf16 *q, const kvc_bf16 *kpool, const kvc_bf16 *vpool,
+                           int64_t n_slots, const int32_t *block_table, int32_t max_blocks,
+                           const int32_t *ctx_len, const int32_t *q_off, int32_t n_req,
+                           int32_t n_q, int32_t max_rows, int32_t H, int32_t Hq, int32_t D,
+                           int32_t block_size, float scale, kvc_bf16 *out, float *lse,
+                           int32_t *dev_status, cudaStream_t stream) {
+  if (!q || !kpool || !vpool || !block_table || !ctx_len || !q_off || !out || !lse)
+    return KVC_ERR_INVALID_ARG;
+  if (n_q < 1 || max_rows < 1 || !isfinite(scale)) return KVC_ERR_INVALID_ARG;
+  const kvc_status st = paged_status(1, n_req, H, D, block_size, max_blocks, n_slots);
+  if (st != KVC_OK) return st;
+  if (!heads_ok(H, Hq) || max_rows > KVC_TREE_MAX_TOKENS) return KVC_ERR_SHAPE;
+  if (!aligned16(q) || !aligned16(kpool) || !aligned16(vpool) || !aligned16(out) ||
+      reinterpret_cast<uintptr_t>(lse) % 4 != 0)
+    return KVC_ERR_ALIGN;
+  return from_cuda(kvc::launch_prompt_attn(q, kpool, vpool, n_slots, block_table, max_blocks,
+                                           ctx_len, q_off, n_req, n_q, max_rows, H, Hq, D,
+                                           block_size, scale, out, lse, dev_status, stream));
+}
+
+kvc_status kvc_q8_pack(const kvc_bf16 *kpool, const kvc_bf16 *vpool, int64_t n_slots,
+                       uint8_t *k8, uint8_t *v8, float *kscale, float *vscale,
+                       int64_t n_blocks8, const int32_t *src_block, const int32_t *dst_block,
+                       int32_t n, int32_t L, int32_t H, int32_t D, int32_t block_size,
+                       int32_t *dev_status, cudaStream_t stream) {
+  if (!kpool || !vpool || !k8 || !v8 || !kscale || !vscale || !src_block || !dst_block || n < 1 ||
+      n_blocks8 < 1)
+    return KVC_ERR_INVALID_ARG;
+  const kvc_status st = paged_status(L, 1, H, D, block_size, 1, n_slots);
+  if (st != KVC_OK) return st;
+  if (n_blocks8 > INT32_MAX || (int64_t)n * H > INT32_MAX) return KVC_ERR_SHAPE;
+  if (!aligned16(kpool) || !aligned16(vpool) || !aligned16(k8) || !aligned16(v8) ||
+      reinterpret_cast<uintptr_t>(kscale) % 4 != 0 || reinterpret_cast<uintptr_t>(vscale) % 4 != 0)
+    return KVC_ERR_ALIGN;
+  const size_t pool = (size_t)L * n_slots * H * D * 2, units = (size_t)L * n_blocks8 * H;
+  const size_t pool8 = units * block_size * D, ids = (size_t)n * 4;
+  if (outputs_overlap({{k8, pool8}, {v8, pool8}, {kscale, units * 4}, {vscale, units * 4}},
+                      {{kpool, pool}, {vpool, pool}, {src_block, ids}, {dst_block, ids}}))
+    return KVC_ERR_INVALID_ARG;
+  return from_cuda(kvc::launch_q8_pack(kpool, vpool, n_slots, k8, v8, kscale, vscale, n_blocks8,
+                                       src_block, dst_block, n, L, H, D, block_size, dev_status,
+                                       stream));
+}
+
+size_t kvc_q8_attn_workspace_size(int32_t n_req, int32_t max_blocks8, int32_t max_blocks,
+                                  int32_t max_tree, int32_t H, int32_t Hq, int32_t D,
+                                  int32_t block_size) {
+  if (max_tree < 1 || max_tree > KVC_TREE_MAX_NODES ||
+      paged_status(1, n_req, H, D, block_size, max_blocks, INT32_MAX) != KVC_OK ||
+      paged_status(1, n_req, H, D, block_size, max_blocks8, INT32_MAX) != KVC_OK ||
+      !heads_ok(H, Hq))
+    return 0;
+  return kvc::q8_attn_ws_bytes(n_req, max_blocks8, max_blocks, max_tree, H, Hq, D, block_size);
+}
+
+kvc_status kvc_q8_attn(const kvc_bf16 *q, const uint8_t *k8, const uint8_t *v8,
+                       const float *kscale, const float *vscale, int64_t n_blocks8,
+                       const int32_t *table8, int32_t max_blocks8, const int32_t *len8,
+                       const kvc_bf16 *kpool, const kvc_bf16 *vpool, int64_t n_slots,
+                       const int32_t *block_table, int32_t max_blocks, const int32_t *ctx_len,
+                       const int32_t *q_off, const uint32_t *tree_mask, int32_t mask_words,
+                       int32_t n_req, int32_t n_q, int32_t max_tree, int32_t H, int32_t Hq,
+                       int32_t D, int32_t block_size, float scale, kvc_bf16 *out, float *lse,
+                       void *ws, size_t ws_bytes, int32_t *dev_status, cudaStream_t stream) {
+  if (!q || !k8 || !v8 || !kscale || !vscale || !table8 || !len8 || !kpool || !vpool ||
+      !block_table || !ctx_len || !q_off || !out || !lse || !ws)
+    return KVC_ERR_INVALID_ARG;
+  if (n_q < 1 || max_tree < 1 || n_blocks8 < 1 || !isfinite(scale)) return KVC_ERR_INVALID_ARG;
+  kvc_status st = paged_status(1, n_req, H, D, block_size, max_blocks, n_slots);
+  if (st == KVC_OK) st = paged_status(1, n_req, H, D, block_size, max_blocks8, n_slots);
+  if (st != KVC_OK) return st;
+  if (!heads_ok(H, Hq) || max_tree > KVC_TREE_MAX_NODES || n_blocks8 > INT32_MAX ||
+      (tree_mask && mask_words < (max_tree + 31) / 32))
+    return KVC_ERR_SHAPE;
+  if (!aligned16(q) || !aligned16(k8) || !aligned16(v8) || !aligned16(kpool) ||
+      !aligned16(vpool) || !aligned16(out) || !aligned16(ws) ||
+      reinterpret_cast<uintptr_t>(kscale) % 4 != 0 ||
+      reinterpret_cast<uintptr_t>(vscale) % 4 != 0 || reinterpret_cast<uintptr_t>(lse) % 4 != 0)
+    return KVC_ERR_ALIGN;
+  if (ws_bytes < kvc_q8_attn_workspace_size(n_req, max_blocks8, max_blocks, max_tree, H, Hq, D,
+                                            block_size))
+    return KVC_ERR_WORKSPACE;
+  return from_cuda(kvc::launch_q8_attn(q, k8, v8, kscale, vscale, n_blocks8, table8, max_blocks8,
+                                       len8, kpool, vpool, n_slots, block_table, max_blocks,
+                                       ctx_len, q_off, tree_mask, mask_words, n_req, n_q,
+                                       max_tree, H, Hq, D, block_size, scale, out, lse, ws,
+                                       dev_status, stream));
+}
+
 }  // extern "C"

@@ -238,4 +238,35 @@ cudaError_t launch_mass_evict(uint16_t *kpool, uint16_t *vpool, int64_t n_slots,
                               int L, int H, int D, int BS, int budget, int n_sink, int n_recent,
                               void *ws, int32_t *status, cudaStream_t s);
 
+// Filling the paged cache and reading its 8-bit part (qkv_rope.cu, prompt_attn.cu,
+// q8_pack.cu, q8_attn.cu)
+cudaError_t launch_qkv_rope(const uint16_t *q, int64_t qs, const uint16_t *k, int64_t ks,
+                            const uint16_t *v, int64_t vs, int n_tok, const uint16_t *wq,
+                            const uint16_t *wk, float eps, const float *tab, int n_pos,
+                            const int32_t *pos, const int32_t *q_off, const int32_t *ctx_len,
+                            int n_req, const int32_t *block_table, int max_blocks,
+                            uint16_t *kpool, uint16_t *vpool, int64_t n_slots, int H, int Hq,
+                            int D, int BS, uint16_t *q_out, uint16_t *k_raw, int64_t raw_stride,
+                            int32_t *status, cudaStream_t s);
+cudaError_t launch_prompt_attn(const uint16_t *q, const uint16_t *kpool, const uint16_t *vpool,
+                               int64_t n_slots, const int32_t *block_table, int max_blocks,
+                               const int32_t *ctx_len, const int32_t *q_off, int n_req, int n_q,
+                               int max_rows, int H, int Hq, int D, int BS, float scale,
+                               uint16_t *out, float *lse, int32_t *status, cudaStream_t s);
+cudaError_t launch_q8_pack(const uint16_t *kpool, const uint16_t *vpool, int64_t n_slots,
+                           uint8_t *k8, uint8_t *v8, float *kscale, float *vscale,
+                           int64_t n_blocks8, const int32_t *src, const int32_t *dst, int n,
+                           int L, int H, int D, int BS, int32_t *status, cudaStream_t s);
+size_t q8_attn_ws_bytes(int n_req, int max_blocks8, int max_blocks, int max_tree, int H, int Hq,
+                        int D, int BS);
+cudaError_t launch_q8_attn(const uint16_t *q, const uint8_t *k8, const uint8_t *v8,
+                           const float *kscale, const float *vscale, int64_t n_blocks8,
+                           const int32_t *table8, int max_blocks8, const int32_t *len8,
+                           const uint16_t *kpool, const uint16_t *vpool, int64_t n_slots,
+                           const int32_t *block_table, int max_blocks, const int32_t *ctx_len,
+                           const int32_t *q_off, const uint32_t *tree_mask, int mask_words,
+                           int n_req, int n_q, int max_tree, int H, int Hq, int D, int BS,
+                           float scale, uint16_t *out, float *lse, void *ws, int32_t *status,
+                           cudaStream_t s);
+
 }  // namespace kvc

@@ -1,0 +1,230 @@
+// qkv_rope.cu — a layer's new tokens on their way into the paged cache: per
+// head, queries and keys are normed (y = x·w / sqrt(mean x² + eps)), rotated by
+// their position's table row and rounded once; keys and values go to their
+// slots.
+//
+// Bound by HBM: every row is read once and written once, and nothing else is
+// of that size (a token's table row serves all its heads and is read once).
+// A warp owns a token (or a part of its heads, where there are few tokens):
+// D/16 lanes hold a head, lane c the pairs (j, j + D/2) for j in [8c, 8c + 8),
+// so that a rotation needs no exchange and the norm only D/16 lanes'.  Its
+// cosines and sines stay in registers over all heads, and kAhead groups of
+// heads are in flight.
+#include "kvc_internal.cuh"
+
+namespace kvc {
+namespace {
+
+constexpr int kRopeWarps = 4;
+constexpr int kAhead = 4;
+
+struct RopeArgs {
+  const uint16_t *q, *k, *v, *wq, *wk;
+  const float *tab;
+  const int32_t *pos, *q_off, *ctx_len, *block_table;
+  uint16_t *q_out, *kpool, *vpool, *k_raw;
+  int32_t *status;
+  int64_t qs, ks, vs, raw_stride, n_slots;
+  float eps;
+  int n_tok, n_pos, n_req, max_blocks, H, Hq, BS;
+};
+
+// Request r's sizes; false when they are out of range.
+__device__ __forceinline__ bool rope_request(const RopeArgs &a, int r, int &c, int &q0, int &T) {
+  c = a.ctx_len[r];
+  q0 = a.q_off[r];
+  const int64_t t = (int64_t)a.q_off[r + 1] - q0;
+  T = (int)t;
+  return c >= 0 && q0 >= 0 && t >= 0 && q0 + t <= a.n_tok &&
+         c + t <= (int64_t)a.max_blocks * a.BS;
+}
+
+// The last r with off[r] ≤ x (off ascending, n + 1 entries), −1 if none; by a
+// whole warp, a 32nd of the range a step.
+__device__ __forceinline__ int warp_last_le(const int32_t *off, int n, int x) {
+  const int lane = threadIdx.x & 31;
+  int base = 0, len = n + 1;
+  for (;;) {
+    const int step = (len + 31) / 32;
+    const int64_t i = (int64_t)lane * step;
+    const uint32_t b = __ballot_sync(0xFFFFFFFFu, i < len && off[base + i] <= x);
+    if (!b) return -1;
+    const int at = (31 - __clz(b)) * step;
+    base += at;
+    if (step == 1) return base;
+    len = min(step, len - at);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kRopeWarps * 32)
+k_qkv_rope(RopeArgs a) {
+  constexpr int LPH = D / 16, HPW = 32 / LPH, HALF = D / 2;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x == 0 && blockIdx.y == 0)  // one report per bad request
+    for (int r = threadIdx.x; r < a.n_req; r += kRopeWarps * 32) {
+      int c, q0, T;
+      if (!rope_request(a, r, c, q0, T)) record_error(a.status, KVC_ERR_BOUNDS);
+    }
+  const int x = blockIdx.x * kRopeWarps + warp;
+  if (x >= a.n_tok) return;
+  // (parts of a token's heads: groups of HPW, an even share each)
+  const int heads = a.Hq + 2 * a.H, groups = (heads + HPW - 1) / HPW;
+  const int g0 = groups * (int)blockIdx.y / (int)gridDim.y;
+  const int g1 = groups * ((int)blockIdx.y + 1) / (int)gridDim.y;
+  const int sub = lane / LPH, c = lane % LPH;
+
+  auto source = [&](int hh) -> const uint16_t * {
+    return hh < a.Hq          ? a.q + x * a.qs + (int64_t)hh * D
+           : hh < a.Hq + a.H ? a.k + x * a.ks + (int64_t)(hh - a.Hq) * D
+                             : a.v + x * a.vs + (int64_t)(hh - a.Hq - a.H) * D;
+  };
+  uint4 lo[kAhead], hi[kAhead];
+  auto load = [&](int u, int g) {
+    const int hh = g * HPW + sub;
+    if (g < g1 && hh < heads) {
+      const uint16_t *p = source(hh);
+      lo[u] = ld_stream(p + 8 * c);
+      hi[u] = ld_stream(p + HALF + 8 * c);
+    }
+  };
+#pragma unroll
+  for (int u = 0; u < kAhead; u++) load(u, g0 + u);
+
+  // where the token goes
+  const int r = warp_last_le(a.q_off, a.n_req, x);
+  int ctx, q0, T;
+  if (r < 0 || r >= a.n_req || !rope_request(a, r, ctx, q0, T) || x - q0 >= T) return;
+  const int p = ctx + x - q0;
+  const int pos = a.pos ? a.pos[x] : p;
+  if (pos < 0 || pos >= a.n_pos) {
+    if (lane == 0) record_error(a.status, KVC_ERR_BOUNDS);
+    return;
+  }
+  const int page = p / a.BS;
+  const int32_t blk = a.block_table[(int64_t)r * a.max_blocks + page];
+  int64_t slot = -1;
+  if (blk >= 0 && blk < a.n_slots / a.BS) slot = (int64_t)blk * a.BS + (p - page * a.BS);
+  else if (lane == 0) record_error(a.status, KVC_ERR_BOUNDS);
+  float cs[8], sn[8];
+  {
+    const float4 *t = reinterpret_cast<const float4 *>(a.tab + ((int64_t)pos * HALF + 8 * c) * 2);
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+      const float4 f = __ldg(t + e);
+      cs[2 * e] = f.x;
+      sn[2 * e] = f.y;
+      cs[2 * e + 1] = f.z;
+      sn[2 * e + 1] = f.w;
+    }
+  }
+
+  for (int g = g0; g < g1; g += kAhead) {
+#pragma unroll
+    for (int u = 0; u < kAhead; u++) {
+      const int hh = (g + u) * HPW + sub;
+      const bool live = g + u < g1 && hh < heads;
+      const int kind = hh < a.Hq ? 0 : hh < a.Hq + a.H ? 1 : 2;
+      const uint32_t wl[4] = {lo[u].x, lo[u].y, lo[u].z, lo[u].w};
+      const uint32_t wh[4] = {hi[u].x, hi[u].y, hi[u].z, hi[u].w};
+      const uint4 vlo = lo[u], vhi = hi[u];
+      float xl[8], xh[8], sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        xl[2 * e] = bf16_lo(wl[e]);
+        xl[2 * e + 1] = bf16_hi(wl[e]);
+        xh[2 * e] = bf16_lo(wh[e]);
+        xh[2 * e + 1] = bf16_hi(wh[e]);
+      }
+      if (g + kAhead < g1) load(u, g + kAhead + u);
+#pragma unroll
+      for (int e = 0; e < 8; e++) sum = fmaf(xl[e], xl[e], fmaf(xh[e], xh[e], sum));
+#pragma unroll
+      for (int o = 1; o < LPH; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+      if (!live) continue;
+      if (kind == 2) {
+        if (slot >= 0) {
+          uint16_t *d = a.vpool + (slot * a.H + hh - a.Hq - a.H) * D + 8 * c;
+          *reinterpret_cast<uint4 *>(d) = vlo;
+          *reinterpret_cast<uint4 *>(d + HALF) = vhi;
+        }
+        continue;
+      }
+      const uint16_t *w = kind ? a.wk : a.wq;
+      if (w) {
+        const float f = 1.f / sqrtf(sum * (1.f / D) + a.eps);
+        const uint4 w0 = __ldg(reinterpret_cast<const uint4 *>(w + 8 * c));
+        const uint4 w1 = __ldg(reinterpret_cast<const uint4 *>(w + HALF + 8 * c));
+        const uint32_t a0[4] = {w0.x, w0.y, w0.z, w0.w}, a1[4] = {w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          xl[2 * e] = xl[2 * e] * f * bf16_lo(a0[e]);
+          xl[2 * e + 1] = xl[2 * e + 1] * f * bf16_hi(a0[e]);
+          xh[2 * e] = xh[2 * e] * f * bf16_lo(a1[e]);
+          xh[2 * e + 1] = xh[2 * e + 1] * f * bf16_hi(a1[e]);
+        }
+      }
+      if (kind == 1 && a.k_raw) {
+        uint32_t rl[4], rh[4];
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          rl[e] = pack_bf16x2(xl[2 * e], xl[2 * e + 1]);
+          rh[e] = pack_bf16x2(xh[2 * e], xh[2 * e + 1]);
+        }
+        uint16_t *d = a.k_raw + (hh - a.Hq) * a.raw_stride + (int64_t)x * D + 8 * c;
+        *reinterpret_cast<uint4 *>(d) = make_uint4(rl[0], rl[1], rl[2], rl[3]);
+        *reinterpret_cast<uint4 *>(d + HALF) = make_uint4(rh[0], rh[1], rh[2], rh[3]);
+      }
+      uint32_t ol[4], oh[4];
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        float u0[2], u1[2];
+#pragma unroll
+        for (int b = 0; b < 2; b++) {
+          const int j = 2 * e + b;
+          u0[b] = fmaf(xl[j], cs[j], -xh[j] * sn[j]);
+          u1[b] = fmaf(xh[j], cs[j], xl[j] * sn[j]);
+        }
+        ol[e] = pack_bf16x2(u0[0], u0[1]);
+        oh[e] = pack_bf16x2(u1[0], u1[1]);
+      }
+      uint16_t *d;
+      if (kind == 0) d = a.q_out + ((int64_t)x * a.Hq + hh) * D;
+      else if (slot >= 0) d = a.kpool + (slot * a.H + hh - a.Hq) * D;
+      else continue;
+      *reinterpret_cast<uint4 *>(d + 8 * c) = make_uint4(ol[0], ol[1], ol[2], ol[3]);
+      *reinterpret_cast<uint4 *>(d + HALF + 8 * c) = make_uint4(oh[0], oh[1], oh[2], oh[3]);
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_qkv_rope(const uint16_t *q, int64_t qs, const uint16_t *k, int64_t ks,
+                            const uint16_t *v, int64_t vs, int n_tok, const uint16_t *wq,
+                            const uint16_t *wk, float eps, const float *tab, int n_pos,
+                            const int32_t *pos, const int32_t *q_off, const int32_t *ctx_len,
+                            int n_req, const int32_t *block_table, int max_blocks,
+                            uint16_t *kpool, uint16_t *vpool, int64_t n_slots, int H, int Hq,
+                            int D, int BS, uint16_t *q_out, uint16_t *k_raw, int64_t raw_stride,
+                            int32_t *status, cudaStream_t s) {
+  RopeArgs a{};
+  a.q = q, a.k = k, a.v = v, a.wq = wq, a.wk = wk, a.tab = tab;
+  a.pos = pos, a.q_off = q_off, a.ctx_len = ctx_len, a.block_table = block_table;
+  a.q_out = q_out, a.kpool = kpool, a.vpool = vpool, a.k_raw = k_raw, a.status = status;
+  a.qs = qs, a.ks = ks, a.vs = vs, a.raw_stride = raw_stride, a.n_slots = n_slots;
+  a.eps = eps;
+  a.n_tok = n_tok, a.n_pos = n_pos, a.n_req = n_req, a.max_blocks = max_blocks;
+  a.H = H, a.Hq = Hq, a.BS = BS;
+  const int groups = (Hq + 2 * H + 512 / D - 1) / (512 / D);
+  // parts of a token's heads: one group of heads each while the GPU has room for them all
+  int parts = 1;
+  while (parts < groups && (int64_t)n_tok * 2 * parts <= 16 * (int64_t)device_sm_count()) parts *= 2;
+  const dim3 grid((unsigned)((n_tok + kRopeWarps - 1) / kRopeWarps),
+                  (unsigned)(parts < groups ? parts : groups));
+  if (D == 128) k_qkv_rope<128><<<grid, kRopeWarps * 32, 0, s>>>(a);
+  else k_qkv_rope<64><<<grid, kRopeWarps * 32, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace kvc
