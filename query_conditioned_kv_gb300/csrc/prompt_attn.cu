@@ -4,167 +4,635 @@
 //   z_p = scale·q·k_p,  lse = ln Σ_p exp z_p,  out = Σ_p exp(z_p − lse)·v_p
 //
 // The rows of a KV head are (token, head of the group) pairs, token by token: a
-// tile of them shares its keys whatever the group's size, and is causal in steps
-// of G rows.
+// tile of up to 128 of them shares its keys whatever the group's size, and is
+// causal in steps of a group.  (Groups of more than 128 heads are cut into equal
+// pieces of one token.)  A unit of work is a pair of neighbouring row tiles of one
+// KV head; keys pass in tiles of 128, and a unit ends with the last one its last
+// row sees.
 //
-// k_prompt_rows: a CTA takes 64 rows of one KV head, a warp 16 of them; tiles of 64
-// keys pass through two cp.async buffers, and mma.sync m16n8k16 makes both products.
+// k_prompt_tc, per row tile X and key tile t:
+//   S_X = Q_X·Kᵀ  (M 128 rows, N 128 keys, K D; both K-major in shared memory)
+//   O_X += P_X·V  (M 128 rows, N D, K 128 keys; P in tensor memory, V as it lies
+//                  in the pool, MN-major)
+// A softmax warpgroup per row tile, a thread per row: no exchange between threads.
+// The exponent's reference is not the running maximum but the row's maximum over
+// its first tile, raised only when a tile's weights sum to more than 2^30 (the sum
+// is needed anyway, so the loop takes no maximum): weights, sums and O stay far
+// inside fp32's and bf16's range, and the result does not depend on the reference.
+// The weights stay in registers until their sum has been looked at, so that a
+// tile can be worked out again on a raised reference from the S that is still there;
+// they then replace S.  A raised reference rescales O in tensor memory.
+//
+// One warp issues the products in the order S_A(0) S_B(0) | O_A(t) S_A(t+1) O_B(t)
+// S_B(t+1) | …: while one tile's weights are worked out the tensor core has the other
+// tile's two products.  Four warps load, 32 keys of a tile each: TMA boxes of whole
+// page rows, or cp.async row by row where a page size has no box, at the end, and for
+// the values that some row of the pair does not see.
+#include <float.h>
+
 #include <algorithm>
+#include <atomic>
 
 #include "tree_rows.cuh"
 
 namespace kvc {
 namespace {
 
-constexpr int kPrWarps = 4;
-constexpr int kPrThreads = kPrWarps * 32;
-constexpr int kPrKeys = 64;
+constexpr int kPaKeys = 128;
+constexpr int kPaThreads = 512;
+// Registers of a softmax thread, of the others: 256·176 + 256·80 is the launch's 512·128.
+constexpr int kPaMore = 176, kPaLess = 80;
+constexpr float kPaUnset = -FLT_MAX;      // reference of a row that has seen nothing
+constexpr float kPaMost = 1073741824.f;   // 2^30: sum of a tile's weights that raises the reference
+constexpr float kPaRound = 1048576.f;     // |reference| from which logits are rounded before the difference
+constexpr int kPaSlots = 8;               // ring slots, at most
+
+struct PromptTc {
+  int box;              // rows of a TMA box (a divisor of the page size), 0: no TMA
+  int gc, n_ch;         // heads of a row tile's piece of the group, pieces
+  int tpt;              // tokens of a row tile
+  int NS;               // ring slots
+  uint32_t idesc_s, idesc_o;
+};
+
+struct PromptHead {
+  uint64_t full[kPaSlots], empty[kPaSlots];  // ring slots
+  uint64_t qfull, sfull[2], pready[2], pvdone[2];
+  uint32_t tmem_holder;
+  volatile int failed, odd, bad;
+};
+constexpr uint32_t kPaHead = 1024;
+static_assert(sizeof(PromptHead) <= kPaHead, "the head's room");
+
+// K-major operand with the 128-byte swizzle, atoms of eight rows `sbo` bytes apart.
+__device__ __forceinline__ uint64_t desc_k(uint32_t addr, uint32_t sbo) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(sbo >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// MN-major: 64 MN elements by 8 K rows an atom, atoms along K `sbo` apart, along MN `lbo`.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) |
+         ((uint64_t)(sbo >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// tcgen05.mma with A in tensor memory, by the lanes with `lead` set.
+__device__ __forceinline__ void mma_ts_if(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_5d_if(uint32_t lead, uint32_t dst, const CUtensorMap *map, int x,
+                                               int y, int z, int w, int v, uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %8, 0;\n"
+      " @q cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n}\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(bar), "r"(lead)
+      : "memory");
+}
+// 32 columns of this thread's lane.
+__device__ __forceinline__ void tmem_put32(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+      "%28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_put_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Pairs of row tiles of request r (0: nothing to do).
+__device__ __forceinline__ int prompt_pairs(const TreeArgs &a, const PromptTc &p, int r) {
+  int c, q0, T;
+  if (!tree_request(a, r, c, q0, T)) return 0;
+  return ((T + p.tpt - 1) / p.tpt * p.n_ch + 1) / 2;
+}
 
 template <int D>
-__global__ void __launch_bounds__(kPrThreads, 2)
-k_prompt_rows(TreeArgs a) {
-  constexpr int KS = D / 16, NT = D / 8, CH = D / 8, HK = kPrKeys / 32;
-  constexpr uint32_t kTile = kPrKeys * D * 2;
-  extern __shared__ __align__(1024) uint8_t sm[];
-  __shared__ uint32_t ok_s[2][HK];
+__global__ void __launch_bounds__(kPaThreads, 1)
+k_prompt_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+            const __grid_constant__ CUtensorMap tm_q, TreeArgs a, PromptTc p) {
+  constexpr int CH = D / 8, KB = D / 64;
+  constexpr uint32_t kSlot = kPaKeys * D * 2, kQTile = 128 * D * 2, kAtoms = 1024 * KB;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *base = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  PromptHead &sm = *reinterpret_cast<PromptHead *>(base);
+  const uint32_t q_u = smem_u32(base) + kPaHead, ring_u = q_u + 2 * kQTile;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t base = smem_u32(sm);
-  const int r = blockIdx.z, h = blockIdx.y;
-  int c, q0, T;
-  if (!tree_request(a, r, c, q0, T)) {
-    if (blockIdx.x == 0 && h == 0 && tid == 0) record_error(a.status, KVC_ERR_BOUNDS);
-    return;
-  }
-  // (the last rows first: they see the most)
-  const int rt = (int)gridDim.x - 1 - blockIdx.x;
-  if ((int64_t)rt * 64 >= (int64_t)T * a.G) return;
-  const int n_rows = min(64, T * a.G - rt * 64), wrt = rt * 4 + warp;
-  const int end = c + (rt * 64 + n_rows - 1) / a.G + 1;  // positions some row sees
-  const int n_kt = (end + kPrKeys - 1) / kPrKeys;
-  const int32_t *bt = a.block_table + (int64_t)r * a.max_blocks;
-  const int64_t n_blocks = a.n_slots / a.BS;
 
-  auto issue = [&](int t, int st) {
-    constexpr int RPW = kPrKeys / kPrWarps, RPI = 32 / CH;  // rows of a warp, of an instruction
-    int32_t slot = -1;
-    const int p = t * kPrKeys + warp * RPW + (lane % RPW);
-    if (p < end) {
-      const int pg = page_of(p, a.bs_inv);
-      const int32_t b = bt[pg];
-      if (b >= 0 && b < n_blocks) slot = b * a.BS + p - pg * a.BS;
-      else record_error(a.status, KVC_ERR_BOUNDS);
+  if (blockIdx.x == 0)  // one report per bad request
+    for (int r = tid; r < a.n_req; r += kPaThreads) {
+      int c, q0, T;
+      if (!tree_request(a, r, c, q0, T)) record_error(a.status, KVC_ERR_BOUNDS);
     }
-    const uint32_t ok = __ballot_sync(0xFFFFFFFFu, slot >= 0) & 0xFFFFu;
-    if (lane == 0) reinterpret_cast<uint16_t *>(ok_s[st])[warp] = (uint16_t)ok;
-    const uint32_t dst = base + st * 2 * kTile;
-    const int col = lane % CH;
-#pragma unroll
-    for (int i = 0; i < RPW / RPI; i++) {
-      const int row = i * RPI + lane / CH;
-      const int32_t sl = __shfl_sync(0xFFFFFFFFu, slot, row);
-      const int64_t from = ((int64_t)max(sl, 0) * a.H + h) * D + col * 8;
-      cp_async16(dst + swz<D>(warp * RPW + row, col), a.kpool + from, sl >= 0);
-      cp_async16(dst + kTile + swz<D>(warp * RPW + row, col), a.vpool + from, sl >= 0);
-    }
+  // this CTA's unit: requests in order, a request's last rows first (they see the most)
+  auto units = [&](int r) { return (int64_t)a.H * prompt_pairs(a, p, r); };
+  const WarpSums sums = warp_sums(a.n_req, units);
+  if ((int64_t)blockIdx.x >= sums.total) return;
+  int r, c, q0, T;
+  int64_t before;
+  warp_find(sums, a.n_req, (int64_t)blockIdx.x, units, r, before);
+  tree_request(a, r, c, q0, T);
+  const int at = (int)((int64_t)blockIdx.x - before), h = at % a.H;
+  const int pair = prompt_pairs(a, p, r) - 1 - at / a.H;
+  // row tile x of the pair: pieces of the group inside, tokens outside
+  const int n_tiles = (T + p.tpt - 1) / p.tpt * p.n_ch;
+  auto token_of = [&](int x) { return (2 * pair + x) / p.n_ch * p.tpt; };
+  auto piece_of = [&](int x) { return (2 * pair + x) % p.n_ch; };
+  auto tiles_of = [&](int x) {  // key tiles that some row of row tile x sees
+    return 2 * pair + x < n_tiles ? (c + min(T, token_of(x) + p.tpt) + kPaKeys - 1) / kPaKeys : 0;
   };
-  issue(0, 0);
-  cp_commit();
-  uint32_t qf[KS][4];
-#pragma unroll
-  for (int hf = 0; hf < 2; hf++) {
-    const int row = warp * 16 + hf * 8 + lane / 4, x = rt * 64 + row;
-    const uint16_t *p =
-        a.q + ((int64_t)(q0 + x / a.G) * a.Hq + h * a.G + x % a.G) * D + 2 * (lane % 4);
-#pragma unroll
-    for (int ks = 0; ks < KS; ks++) {
-      qf[ks][hf] = row < n_rows ? __ldg(reinterpret_cast<const uint32_t *>(p + 16 * ks)) : 0u;
-      qf[ks][2 + hf] = row < n_rows ? __ldg(reinterpret_cast<const uint32_t *>(p + 16 * ks + 8)) : 0u;
-    }
-  }
-  float o[1][NT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-#pragma unroll
-  for (int n = 0; n < NT; n++) o[0][n][0] = o[0][n][1] = o[0][n][2] = o[0][n][3] = 0.f;
+  const int nA = tiles_of(0), nB = tiles_of(1), nT = max(nA, nB);
+  const int tok0 = token_of(0);
+  const int end = c + min(T, token_of(nB ? 1 : 0) + p.tpt);  // positions some row sees
 
-  for (int t = 0; t < n_kt; t++) {
-    if (t + 1 < n_kt) issue(t + 1, (t + 1) & 1);
-    cp_commit();
-    cp_wait<1>();
-    __syncthreads();
-    const uint32_t kb = base + (t & 1) * 2 * kTile, vb = kb + kTile;
+  if (tid == 0) {
+    sm.failed = sm.odd = sm.bad = 0;
+    for (int i = 0; i < p.NS; i++) {
+      mbar_init(smem_u32(sm.full + i), 4);
+      mbar_init(smem_u32(sm.empty + i), 1);
+    }
+    mbar_init(smem_u32(&sm.qfull), 1);
+    for (int i = 0; i < 2; i++) {
+      mbar_init(smem_u32(sm.sfull + i), 1);
+      mbar_init(smem_u32(sm.pready + i), 4);
+      mbar_init(smem_u32(sm.pvdone + i), 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 12) alloc_tmem_cols(&sm.tmem_holder, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_holder;  // S_A (P_A in its first half), S_B, O_A, O_B
+
+  bool ok = true;
+  if (warp >= 8 && warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPaLess));
+    // ------------------------------------------------------- producers
+    const int key0 = (warp & 3) * 32;  // this warp's keys of a tile
+    const int64_t n_blocks = a.n_slots / a.BS;
+    const int32_t *bt = a.block_table + (int64_t)r * a.max_blocks;
+    constexpr int RPI = 32 / CH;
+    const int col = lane % CH;
+    if (warp == 8 && lane == 0) {
+      const uint32_t bar = smem_u32(&sm.qfull);
+      mbar_expect_tx(bar, (nB ? 2 : 1) * p.tpt * p.gc * D * 2);
+      for (int x = 0; x < (nB ? 2 : 1); x++)
 #pragma unroll
-    for (int half = 0; half < HK; half++) {
-      const int p0 = t * kPrKeys + half * 32;
-      const uint32_t okb = ok_s[t & 1][half];
-      const uint32_t kh = kb + half * 32 * D * 2;
-      float s[1][4][4];
-#pragma unroll
-      for (int n = 0; n < 4; n++) s[0][n][0] = s[0][n][1] = s[0][n][2] = s[0][n][3] = 0.f;
-#pragma unroll
-      for (int ks = 0; ks < KS; ks++)
-#pragma unroll
-        for (int kk = 0; kk < 2; kk++) {
-          uint32_t b[4];
-          ldsm4(kh + swz<D>(kk * 16 + (lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1)), b);
-          mma16816(s[0][2 * kk], qf[ks], b[0], b[1]);
-          mma16816(s[0][2 * kk + 1], qf[ks], b[2], b[3]);
-        }
-      const bool masked = p0 + 32 > c || okb != 0xFFFFFFFFu;
-#pragma unroll
-      for (int hf = 0; hf < 2; hf++) {
-        uint32_t vis = 0xFFFFFFFFu;
-        if (masked) {
-          const int x = wrt * 16 + hf * 8 + lane / 4;
-          vis = x < T * a.G ? visible_bits<32>(a, x / a.G, q0, c, T, p0) & okb : 0u;
-        }
-        float mx = m[hf];
-#pragma unroll
-        for (int n = 0; n < 4; n++)
-#pragma unroll
-          for (int e = 0; e < 2; e++) {
-            float z = s[0][n][hf * 2 + e] * a.zscale;
-            if (!((vis >> (n * 8 + 2 * (lane % 4) + e)) & 1u)) z = -INFINITY;
-            s[0][n][hf * 2 + e] = z;
-            mx = fmaxf(mx, z);
+        for (int kb = 0; kb < KB; kb++)
+          tma_load_3d(q_u + x * kQTile + kb * (128 * 128), &tm_q, kb * 64,
+                      h * a.G + piece_of(x) * p.gc, q0 + token_of(x), bar);
+    }
+    __syncwarp();
+    // stages copied by cp.async and not yet handed over: up to two
+    uint32_t pend0 = 0, pend1 = 0;
+    auto hand_over = [&](uint32_t bar) {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    auto flush = [&]() {
+      if (!pend0) return;
+      cp_wait<0>();
+      hand_over(pend0);
+      if (pend1) hand_over(pend1);
+      pend0 = pend1 = 0;
+    };
+    int32_t blk, slot = -1;  // block id of the next tile's key, slot of this tile's
+    auto fetch = [&](int t) {
+      const int pp = t * kPaKeys + key0 + lane;
+      blk = pp < end && t < nT ? bt[page_of(pp, a.bs_inv)] : 0;
+    };
+    fetch(0);
+    uint32_t st = 0, round = 0;  // ring slot, times around
+    for (int i = 0; i < 2 * nT && ok; i++) {
+      const int t = i >> 1;
+      const bool is_v = i & 1;
+      const int pp = t * kPaKeys + key0 + lane;
+      if (!is_v) {
+        slot = -1;
+        if (pp < end) {
+          if (blk >= 0 && blk < n_blocks) {
+            slot = blk * a.BS + pp - page_of(pp, a.bs_inv) * a.BS;
+          } else {
+            sm.bad = 1;  // (read by the softmax warps after this stage's product)
+            record_error(a.status, KVC_ERR_BOUNDS);
           }
-        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-        const float ref = mx == -INFINITY ? 0.f : mx, f = ex2(m[hf] - ref);
-        m[hf] = mx;
-        float sum = 0.f;
-#pragma unroll
-        for (int n = 0; n < 4; n++)
-#pragma unroll
-          for (int e = 0; e < 2; e++) {
-            const float w = ex2(s[0][n][hf * 2 + e] - ref);
-            s[0][n][hf * 2 + e] = w;
-            sum += w;
-          }
-        l[hf] = l[hf] * f + sum;
-#pragma unroll
-        for (int n = 0; n < NT; n++) {
-          o[0][n][hf * 2] *= f;
-          o[0][n][hf * 2 + 1] *= f;
+        }
+        fetch(t + 1);
+      }
+      if (round > 0) {  // a full ring is waited for only after everything in flight is handed over
+        const uint32_t bar = smem_u32(sm.empty + st), parity = (round & 1) ^ 1;
+        if (!mbar_try(bar, parity)) {
+          flush();
+          if (!(ok = mbar_wait_bounded(bar, parity, &sm.failed))) break;
         }
       }
-      tile_values<D, 1, 32>(a, s, o, vb + half * 32 * D * 2, okb, wrt, q0, c, T, p0);
+      const uint32_t dst = ring_u + st * kSlot + (key0 >> 3) * kAtoms;
+      const uint32_t bar = smem_u32(sm.full + st);
+      if (++st == (uint32_t)p.NS) st = 0, round++;
+      // values past the first row's own position are looked at (below): not by TMA
+      const bool hidden = is_v && (t + 1) * kPaKeys > c + tok0 + 1;
+      if (p.box > 0 && !hidden && __all_sync(0xFFFFFFFFu, slot >= 0)) {
+        if (lane == 0) mbar_expect_tx(bar, kSlot / 4);
+        __syncwarp();
+        const uint32_t ubar = uniform32(bar), udst = uniform32(dst), uh = uniform32(h);
+        const CUtensorMap *tm = is_v ? &tm_v : &tm_k;
+        for (int k = 0; k < 32; k += p.box) {
+          const uint32_t sl = __shfl_sync(0xFFFFFFFFu, slot, k);
+          tma_load_5d_if(lane == 0, udst + (k >> 3) * kAtoms, tm, 0, 0, 0, uh, sl >> 3, ubar);
+        }
+        continue;
+      }
+      const uint16_t *pool = is_v ? a.vpool : a.kpool;
+      auto place = [&](int row) {
+        return dst + (row >> 3) * kAtoms + (col >> 3) * 1024 + (row & 7) * 128 + (((col & 7) ^ (row & 7)) << 4);
+      };
+#pragma unroll 4
+      for (int k = 0; k < 32 / RPI; k++) {
+        const int row = k * RPI + lane / CH;
+        const int32_t sl = __shfl_sync(0xFFFFFFFFu, slot, row);
+        cp_async16(place(row), pool + ((int64_t)max(sl, 0) * a.H + h) * D + col * 8, sl >= 0);
+      }
+      cp_commit();
+      if (!hidden) {
+        if (!pend0) {
+          pend0 = bar;
+        } else if (!pend1) {
+          pend1 = bar;
+        } else {
+          cp_wait<2>();
+          hand_over(pend0);
+          pend0 = pend1;
+          pend1 = bar;
+        }
+        continue;
+      }
+      // A later token's V may hold infinities or NaN that some rows do not see: the product
+      // gets zeros in their place, and the unit's end adds them to the rows that do.  Each
+      // thread looks at what it copied, before the stage is handed over.
+      flush();
+      cp_wait<0>();
+      bool odd = false;
+#pragma unroll 1
+      for (int k = 0; k < 32 / RPI; k++) {
+        const int row = k * RPI + lane / CH;
+        const uint32_t ad = place(row);
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(ad)
+                     : "memory");
+        bool mine = false;
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+          if ((w[u] & 0x7F80u) == 0x7F80u) mine = true, w[u] &= 0xFFFF0000u;
+          if ((w[u] & 0x7F800000u) == 0x7F800000u) mine = true, w[u] &= 0xFFFFu;
+        }
+        // (what every row of the pair sees stays)
+        if (mine && t * kPaKeys + key0 + row > c + tok0) {
+          odd = true;
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(ad), "r"(w[0]), "r"(w[1]),
+                       "r"(w[2]), "r"(w[3])
+                       : "memory");
+        }
+      }
+      if (odd) sm.odd = 1;
+      hand_over(bar);
     }
-    __syncthreads();
-  }
+    flush();
+    cp_wait<0>();
+    if (!ok) sm.failed = 1;
+  } else if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPaLess));
+    if (warp == 12) {
+      // ------------------------------------------------------- MMA issuer
+      // The whole warp runs the loop and one lane's products are enabled by a predicate:
+      // the descriptors then live in uniform registers.
+      const uint32_t lead = lane == 0;
+      uint32_t st = 0, round = 0;  // next stage to be waited for
+      uint32_t ks = 0, vs = 0;     // slots of the K and the V tile in use
+      auto stage = [&](uint32_t &slot) {
+        ok = mbar_wait_bounded(smem_u32(sm.full + st), round & 1, &sm.failed);
+        slot = st;
+        if (++st == (uint32_t)p.NS) st = 0, round++;
+      };
+      auto product_s = [&](int x) {
+        const uint64_t qd = uniform64(desc_k(q_u + x * kQTile, 1024));
+        const uint64_t kd = uniform64(desc_k(ring_u + ks * kSlot, kAtoms));
+        const uint32_t dst = uniform32(tmem + x * 128);
 #pragma unroll
-  for (int hf = 0; hf < 2; hf++) {
-    float sum = l[hf];
-    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-    const int row = warp * 16 + hf * 8 + lane / 4, x = rt * 64 + row;
-    if (row >= n_rows) continue;
-    const int64_t qr = (int64_t)(q0 + x / a.G) * a.Hq + h * a.G + x % a.G;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        for (int kk = 0; kk < 4 * KB; kk++)
+          mma_bf16_if(lead, dst, qd + (kk >> 2) * (128 * 8) + (kk & 3) * 2,
+                      kd + (kk >> 2) * (1024 / 16) + (kk & 3) * 2, p.idesc_s, kk > 0);
+        mma_commit_if(lead, smem_u32(sm.sfull + x));
+      };
+      ok = mbar_wait_bounded(smem_u32(&sm.qfull), 0, &sm.failed);
+      if (ok) stage(ks);
+      if (ok) {
+        tc_fence_after();
+        product_s(0);
+        if (nB) product_s(1);
+        mma_commit_if(lead, smem_u32(sm.empty + ks));
+      }
+      for (int t = 0; t < nT && ok; t++) {
+        stage(vs);
+        for (int x = 0; x < 2 && ok; x++) {
+          const int n = x ? nB : nA;
+          if (t >= n) continue;
+          ok = mbar_wait_bounded(smem_u32(sm.pready + x), t & 1, &sm.failed);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t vd = uniform64(desc_mn(ring_u + vs * kSlot, 1024, kAtoms));
+          const uint32_t dst = uniform32(tmem + 256 + x * 128), src = uniform32(tmem + x * 128);
 #pragma unroll
-    for (int n = 0; n < NT; n++)
-      *reinterpret_cast<uint32_t *>(a.out + qr * D + n * 8 + 2 * (lane % 4)) =
-          pack_bf16x2(o[0][n][hf * 2] * inv, o[0][n][hf * 2 + 1] * inv);
-    if (lane % 4 == 0) a.lse[qr] = sum == 0.f ? -INFINITY : (m[hf] + log2f(sum)) * kLn2;
+          for (int kk = 0; kk < kPaKeys / 16; kk++)
+            mma_ts_if(lead, dst, src + kk * 8, vd + kk * (2 * kAtoms / 16), p.idesc_o, t > 0 || kk > 0);
+          mma_commit_if(lead, smem_u32(sm.pvdone + x));
+          const bool last = x == 1 || t >= nB;  // no other row tile takes this key tile
+          if (last) mma_commit_if(lead, smem_u32(sm.empty + vs));
+          if (t + 1 < n) {
+            // (the next K tile is waited for by the first row tile that takes it)
+            if (x == 0 || t + 1 >= nA) stage(ks);
+            if (!ok) break;
+            // S takes the place of P, which the product just issued reads
+            ok = mbar_wait_bounded(smem_u32(sm.pvdone + x), t & 1, &sm.failed);
+            if (!ok) break;
+            tc_fence_after();
+            product_s(x);
+            if (x == 1 || t + 1 >= nB) mma_commit_if(lead, smem_u32(sm.empty + ks));
+          }
+        }
+      }
+      if (!ok) sm.failed = 1;
+      __syncwarp();
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPaMore));
+    // --------------------------------------------------------- softmax
+    const int x = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+    const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+    const uint32_t ts = tmem + x * 128 + lanes, to = tmem + 256 + x * 128 + lanes;
+    const int n = x ? nB : nA;
+    const int tx = token_of(x), token = tx + row / p.gc, head = piece_of(x) * p.gc + row % p.gc;
+    const bool active = n > 0 && row < p.tpt * p.gc && token < T && head < a.G;
+    const int32_t *bt = a.block_table + (int64_t)r * a.max_blocks;
+    const int64_t n_blocks = a.n_slots / a.BS;
+    const float zs = a.zscale, hidden = zs < 0.f ? INFINITY : -INFINITY;  // −inf once scaled
+    float nref = -kPaUnset, l = 0.f;
+    bool rounded = false;  // (warp-uniform) some reference is so large that differences need care
+    for (int t = 0; t < n && ok; t++) {
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.sfull + x), t & 1, &sm.failed));
+      if (!ok) break;
+      tc_fence_after();
+      // which keys this row sees, where it is not all of them
+      const bool masked = (t + 1) * kPaKeys > c + tx + 1 || sm.bad;
+      uint32_t see[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
+      if (masked) {
+        const int lim = c + token + 1 - t * kPaKeys;
+#pragma unroll
+        for (int w = 0; w < 4; w++) {
+          const int pp = t * kPaKeys + 32 * w + lane;
+          bool valid = pp < end;
+          if (valid) {
+            const int32_t b = bt[page_of(pp, a.bs_inv)];
+            valid = b >= 0 && b < n_blocks;
+          }
+          const int m = min(max(lim - 32 * w, 0), 32);
+          see[w] = __ballot_sync(0xFFFFFFFFu, valid) & (m == 32 ? 0xFFFFFFFFu : (1u << m) - 1u);
+        }
+      }
+      auto hide = [&](uint32_t (&z)[32], uint32_t bits) {
+#pragma unroll
+        for (int e = 0; e < 32; e++)
+          if (!((bits >> e) & 1u)) z[e] = __float_as_uint(hidden);
+      };
+      // The references first: before the first tile, where weights came out too large, and
+      // for every tile while they are large.
+      auto raise = [&]() {
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int w = 0; w < 4; w++) {
+          uint32_t z[32];
+          tmem_issue32(ts + 32 * w, z);
+          tmem_wait32(z);
+          const uint32_t bits = w < 2 ? (w ? see[1] : see[0]) : (w > 2 ? see[3] : see[2]);
+          if (masked) hide(z, bits);
+#pragma unroll
+          for (int e = 0; e < 32; e++) mx = fmaxf(mx, __fmul_rn(__uint_as_float(z[e]), zs));
+        }
+        const float was = -nref, now = fmaxf(was, mx);
+        const float f = ex2(was - now);
+        if (t > 0 && __any_sync(0xFFFFFFFFu, active && f != 1.f)) {
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.pvdone + x), (t - 1) & 1, &sm.failed));
+          if (!ok) return;
+          tc_fence_after();
+#pragma unroll 1
+          for (int cc = 0; cc < D; cc += 32) {
+            uint32_t v[32];
+            tmem_issue32(to + cc, v);
+            tmem_wait32(v);
+#pragma unroll
+            for (int e = 0; e < 32; e++) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+            tmem_put32(to + cc, v);
+            tmem_put_wait();
+          }
+        }
+        l *= f;
+        nref = -now;
+        rounded = __any_sync(0xFFFFFFFFu, active && now != kPaUnset && !(fabsf(now) < kPaRound));
+      };
+      uint32_t pk[64];
+      float sum;
+      bool raised = t == 0 || rounded;
+      if (raised) raise();
+      while (ok) {
+        const uint64_t zs2 = pk2(zs, zs), nr2 = pk2(nref, nref);
+        uint64_t s2[2] = {0, 0};
+        uint32_t z[2][32];
+        tmem_issue32(ts, z[0]);
+#pragma unroll
+        for (int w = 0; w < 4; w++) {
+          tmem_wait32(z[w & 1]);
+          if (w < 3) tmem_issue32(ts + 32 * (w + 1), z[(w + 1) & 1]);
+          if (masked) hide(z[w & 1], see[w]);
+          uint64_t d[16];
+#pragma unroll
+          for (int e = 0; e < 16; e++)
+            d[e] = pk2(__uint_as_float(z[w & 1][2 * e]), __uint_as_float(z[w & 1][2 * e + 1]));
+          // after a raise the largest rounded product is the reference: the difference is taken
+          // from rounded products and is at most 0, however large they are
+          if (raised) {
+#pragma unroll
+            for (int e = 0; e < 16; e++) {
+              float u, v;
+              upk2(d[e], u, v);
+              d[e] = pk2(__fadd_rn(__fmul_rn(u, zs), nref), __fadd_rn(__fmul_rn(v, zs), nref));
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; e++) d[e] = fma2(d[e], zs2, nr2);
+          }
+#pragma unroll
+          for (int e = 0; e < 16; e++) {
+            float u, v;
+            upk2(d[e], u, v);
+            u = ex2(u);
+            v = ex2(v);
+            s2[e & 1] = add2(s2[e & 1], pk2(u, v));
+            pk[16 * w + e] = pack_bf16x2(u, v);
+          }
+        }
+        float u, v;
+        upk2(add2(s2[0], s2[1]), u, v);
+        sum = u + v;
+        if (raised || __all_sync(0xFFFFFFFFu, !active || sum <= kPaMost)) break;
+        raise();
+        raised = true;
+      }
+      if (!ok) break;
+      l += sum;
+      tmem_put32(ts, pk);
+      tmem_put32(ts + 32, pk + 32);
+      tmem_put_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(sm.pready + x));
+    }
+    // ---- the unit's result
+    if (ok && n > 0) {
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.pvdone + x), (n - 1) & 1, &sm.failed));
+      tc_fence_after();
+    }
+    if (ok && n > 0) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const int64_t qr = (int64_t)(q0 + token) * a.Hq + h * a.G + head;
+      const bool odd = sm.odd != 0;
+#pragma unroll 1
+      for (int cc = 0; cc < D; cc += 32) {
+        uint32_t z[32];
+        float v[32];
+        tmem_issue32(to + cc, z);
+        tmem_wait32(z);
+#pragma unroll
+        for (int e = 0; e < 32; e++) v[e] = l == 0.f ? 0.f : __uint_as_float(z[e]) * inv;
+        if (odd && active) {  // infinities and NaN of later tokens that the row sees
+#pragma unroll 1
+          for (int pn = c + tok0 + 1; pn <= c + token; pn++) {
+            const int pg = page_of(pn, a.bs_inv);
+            const int32_t b = bt[pg];
+            if (b < 0 || b >= n_blocks) continue;
+            const uint16_t *vr = a.vpool + (((int64_t)b * a.BS + pn - pg * a.BS) * a.H + h) * D + cc;
+#pragma unroll
+            for (int e = 0; e < 32; e++) {
+              const float vn = bf16_lo(vr[e]);
+              if (!(fabsf(vn) < INFINITY)) v[e] += vn;
+            }
+          }
+        }
+        if (active) {
+          uint4 *dst = reinterpret_cast<uint4 *>(a.out + qr * D + cc);
+#pragma unroll
+          for (int e = 0; e < 4; e++)
+            dst[e] = make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]), pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
+                                pack_bf16x2(v[8 * e + 4], v[8 * e + 5]), pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
+        }
+      }
+      if (active) a.lse[qr] = l == 0.f ? -INFINITY : (log2f(l) - nref) * kLn2;
+    }
+    if (!ok) {
+      sm.failed = 1;
+      if (lane == 0) record_error(a.status, KVC_ERR_TIMEOUT);
+    }
   }
+
+  // -------------------------------------------------------- teardown
+  tc_fence_before();
+  __syncthreads();
+  if (sm.failed && tid == 0) {
+    record_error(a.status, KVC_ERR_TIMEOUT);
+    // let this CTA's copies and products finish before its memory is released
+    for (int i = 0; i < p.NS; i++) {
+      mbar_drain(smem_u32(sm.full + i), 0);
+      mbar_drain(smem_u32(sm.full + i), 1);
+    }
+    mbar_drain(smem_u32(&sm.qfull), 0);
+    for (int i = 0; i < 2; i++) {
+      mbar_drain(smem_u32(sm.sfull + i), 0);
+      mbar_drain(smem_u32(sm.sfull + i), 1);
+      mbar_drain(smem_u32(sm.pvdone + i), 0);
+      mbar_drain(smem_u32(sm.pvdone + i), 1);
+    }
+  }
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    free_tmem_cols(tmem, 512);
+  }
+}
+
+// Boxes of `box` consecutive slots (a multiple of 8) of one head, both halves of a row of
+// 128 elements: [group of 8 slots][half][slot][64 columns], 128-byte swizzle.
+bool rows_map(CUtensorMap *m, const void *pool, int64_t n_slots, int H, int D, int box) {
+  auto fn = tc::encode_fn();
+  if (!fn) return false;
+  const cuuint64_t row = (cuuint64_t)H * D * 2;
+  cuuint64_t dims[5] = {64, 8, (cuuint64_t)D / 64, (cuuint64_t)H, (cuuint64_t)n_slots / 8};
+  cuuint64_t strides[4] = {row, 128, (cuuint64_t)D * 2, 8 * row};
+  cuuint32_t bx[5] = {64, 8, (cuuint32_t)D / 64, 1, (cuuint32_t)box / 8}, es[5] = {1, 1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(pool), dims, strides, bx, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch_prompt_tc(const TreeArgs &a, int max_rows, cudaStream_t s) {
+  constexpr size_t kSmemMax = 232448;
+  constexpr size_t kSlot = kPaKeys * D * 2, kFixed = 1024 + kPaHead + 2 * 128 * D * 2;
+  PromptTc p{};
+  p.n_ch = (a.G + 127) / 128;
+  p.gc = (a.G + p.n_ch - 1) / p.n_ch;
+  p.tpt = 128 / p.gc;
+  p.NS = (int)std::min<size_t>(kPaSlots, (kSmemMax - kFixed) / kSlot);
+  p.box = a.BS % 32 == 0 ? 32 : a.BS % 16 == 0 ? 16 : a.BS % 8 == 0 ? 8 : 0;
+  p.idesc_s = make_idesc(128, kPaKeys);
+  p.idesc_o = make_idesc(128, D) | (1u << 16);  // B (V) MN-major
+  CUtensorMap tm_k{}, tm_v{}, tm_q{};
+  if (p.box && !(rows_map(&tm_k, a.kpool, a.n_slots, a.H, D, p.box) &&
+                 rows_map(&tm_v, a.vpool, a.n_slots, a.H, D, p.box)))
+    return cudaErrorUnknown;
+  if (!q_map(&tm_q, a.q, a.n_q, a.Hq, D, p.gc, p.tpt)) return cudaErrorUnknown;
+  // (the limit is the process's: the largest, so that no thread's call lowers it under
+  // another's launch)
+  cudaError_t e = cudaFuncSetAttribute(k_prompt_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)kSmemMax);
+  if (e != cudaSuccess) return e;
+  static std::atomic<int> regs{0};  // a thread's registers at launch
+  if (!regs.load(std::memory_order_relaxed)) {
+    cudaFuncAttributes fa{};
+    if ((e = cudaFuncGetAttributes(&fa, k_prompt_tc<D>)) != cudaSuccess) return e;
+    regs.store(fa.numRegs, std::memory_order_relaxed);
+  }
+  // setmaxnreg.inc draws on what the block was launched with
+  if (regs.load(std::memory_order_relaxed) * kPaThreads < 256 * (kPaMore + kPaLess))
+    return cudaErrorLaunchOutOfResources;
+  // units at most: every request's last pair may be part empty
+  const int64_t each = ((int64_t)(max_rows + p.tpt - 1) / p.tpt * p.n_ch + 1) / 2;
+  const int64_t rows = std::min<int64_t>(a.n_q, (int64_t)a.n_req * max_rows);
+  const int64_t pairs = std::min<int64_t>(a.n_req * each, rows * p.n_ch / (2 * p.tpt) + 2 * (int64_t)a.n_req);
+  if (pairs * a.H > INT32_MAX) return cudaErrorInvalidConfiguration;
+  k_prompt_tc<D><<<(unsigned)(pairs * a.H), kPaThreads, kFixed + p.NS * kSlot, s>>>(tm_k, tm_v, tm_q, a, p);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -179,15 +647,8 @@ cudaError_t launch_prompt_attn(const uint16_t *q, const uint16_t *kpool, const u
   a.ctx_len = ctx_len, a.q_off = q_off, a.out = out, a.lse = lse, a.status = status;
   a.n_slots = n_slots, a.max_blocks = max_blocks, a.n_req = n_req, a.n_q = n_q;
   a.max_tree = max_rows, a.H = H, a.Hq = Hq, a.G = Hq / H, a.BS = BS, a.bs_inv = page_inverse(BS);
-  a.rstep = 16;
   a.zscale = scale != 0.f ? scale * kLog2e : 1e-30f;  // (so that −inf stays −inf when scaled)
-  auto *kern = D == 128 ? k_prompt_rows<128> : k_prompt_rows<64>;
-  const int smem = 4 * kPrKeys * D * 2;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)(((int64_t)max_rows * a.G + 63) / 64), (unsigned)H, (unsigned)n_req);
-  kern<<<grid, kPrThreads, smem, s>>>(a);
-  return cudaGetLastError();
+  return D == 128 ? launch_prompt_tc<128>(a, max_rows, s) : launch_prompt_tc<64>(a, max_rows, s);
 }
 
 }  // namespace kvc
