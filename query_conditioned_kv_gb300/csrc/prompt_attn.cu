@@ -32,6 +32,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "tree_rows.cuh"
 
@@ -74,14 +75,20 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t lbo, uint32_
   return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) |
          ((uint64_t)(sbo >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
-// tcgen05.mma with A in tensor memory, by the lanes with `lead` set.
-__device__ __forceinline__ void mma_ts_if(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
-                                          uint32_t idesc, uint32_t accumulate) {
+// tcgen05.mma with A in tensor memory.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t x;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(x));
+  return x != 0;
 }
 __device__ __forceinline__ void tma_load_5d_if(uint32_t lead, uint32_t dst, const CUtensorMap *map, int x,
                                                int y, int z, int w, int v, uint32_t bar) {
@@ -317,9 +324,9 @@ k_prompt_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPaLess));
     if (warp == 12) {
       // ------------------------------------------------------- MMA issuer
-      // The whole warp runs the loop and one lane's products are enabled by a predicate:
-      // the descriptors then live in uniform registers.
-      const uint32_t lead = lane == 0;
+      // The whole warp runs the loop, and the lane that elect.sync names issues: the compiler
+      // then knows that one thread runs and keeps the descriptors in uniform registers.  (64
+      // cycles a product at N = 128; enabled by a predicate of the whole warp, 67 to 105.)
       uint32_t st = 0, round = 0;  // next stage to be waited for
       uint32_t ks = 0, vs = 0;     // slots of the K and the V tile in use
       auto stage = [&](uint32_t &slot) {
@@ -328,14 +335,20 @@ k_prompt_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         if (++st == (uint32_t)p.NS) st = 0, round++;
       };
       auto product_s = [&](int x) {
-        const uint64_t qd = uniform64(desc_k(q_u + x * kQTile, 1024));
-        const uint64_t kd = uniform64(desc_k(ring_u + ks * kSlot, kAtoms));
-        const uint32_t dst = uniform32(tmem + x * 128);
+        const uint64_t qd = desc_k(q_u + x * kQTile, 1024), kd = desc_k(ring_u + ks * kSlot, kAtoms);
+        const uint32_t dst = tmem + x * 128;
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < 4 * KB; kk++)
-          mma_bf16_if(lead, dst, qd + (kk >> 2) * (128 * 8) + (kk & 3) * 2,
-                      kd + (kk >> 2) * (1024 / 16) + (kk & 3) * 2, p.idesc_s, kk > 0);
-        mma_commit_if(lead, smem_u32(sm.sfull + x));
+          for (int kk = 0; kk < 4 * KB; kk++)
+            mma_bf16(dst, qd + (kk >> 2) * (128 * 8) + (kk & 3) * 2,
+                     kd + (kk >> 2) * (1024 / 16) + (kk & 3) * 2, p.idesc_s, kk > 0);
+          mma_commit(smem_u32(sm.sfull + x));
+        }
+        __syncwarp();
+      };
+      auto done = [&](uint32_t bar) {  // arrives when everything issued so far is done
+        if (elect_one()) mma_commit(bar);
+        __syncwarp();
       };
       ok = mbar_wait_bounded(smem_u32(&sm.qfull), 0, &sm.failed);
       if (ok) stage(ks);
@@ -343,7 +356,7 @@ k_prompt_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         tc_fence_after();
         product_s(0);
         if (nB) product_s(1);
-        mma_commit_if(lead, smem_u32(sm.empty + ks));
+        done(smem_u32(sm.empty + ks));
       }
       for (int t = 0; t < nT && ok; t++) {
         stage(vs);
@@ -353,14 +366,17 @@ k_prompt_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
           ok = mbar_wait_bounded(smem_u32(sm.pready + x), t & 1, &sm.failed);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t vd = uniform64(desc_mn(ring_u + vs * kSlot, 1024, kAtoms));
-          const uint32_t dst = uniform32(tmem + 256 + x * 128), src = uniform32(tmem + x * 128);
-#pragma unroll
-          for (int kk = 0; kk < kPaKeys / 16; kk++)
-            mma_ts_if(lead, dst, src + kk * 8, vd + kk * (2 * kAtoms / 16), p.idesc_o, t > 0 || kk > 0);
-          mma_commit_if(lead, smem_u32(sm.pvdone + x));
+          const uint64_t vd = desc_mn(ring_u + vs * kSlot, 1024, kAtoms);
+          const uint32_t dst = tmem + 256 + x * 128, src = tmem + x * 128;
           const bool last = x == 1 || t >= nB;  // no other row tile takes this key tile
-          if (last) mma_commit_if(lead, smem_u32(sm.empty + vs));
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < kPaKeys / 16; kk++)
+              mma_ts(dst, src + kk * 8, vd + kk * (2 * kAtoms / 16), p.idesc_o, t > 0 || kk > 0);
+            mma_commit(smem_u32(sm.pvdone + x));
+            if (last) mma_commit(smem_u32(sm.empty + vs));
+          }
+          __syncwarp();
           if (t + 1 < n) {
             // (the next K tile is waited for by the first row tile that takes it)
             if (x == 0 || t + 1 >= nA) stage(ks);
@@ -370,7 +386,7 @@ k_prompt_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             if (!ok) break;
             tc_fence_after();
             product_s(x);
-            if (x == 1 || t + 1 >= nB) mma_commit_if(lead, smem_u32(sm.empty + ks));
+            if (x == 1 || t + 1 >= nB) done(smem_u32(sm.empty + ks));
           }
         }
       }
@@ -454,9 +470,10 @@ k_prompt_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
       };
       uint32_t pk[64];
       float sum;
-      bool raised = t == 0 || rounded;
-      if (raised) raise();
-      while (ok) {
+      // The weights on the references at hand and their sum.  `General`: keys may be hidden,
+      // and after a raise the largest rounded product is the reference, so the difference is
+      // taken from rounded products and is at most 0, however large they are.
+      auto weights = [&](auto General, bool raised) {
         const uint64_t zs2 = pk2(zs, zs), nr2 = pk2(nref, nref);
         uint64_t s2[2] = {0, 0};
         uint32_t z[2][32];
@@ -465,28 +482,16 @@ k_prompt_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         for (int w = 0; w < 4; w++) {
           tmem_wait32(z[w & 1]);
           if (w < 3) tmem_issue32(ts + 32 * (w + 1), z[(w + 1) & 1]);
-          if (masked) hide(z[w & 1], see[w]);
-          uint64_t d[16];
-#pragma unroll
-          for (int e = 0; e < 16; e++)
-            d[e] = pk2(__uint_as_float(z[w & 1][2 * e]), __uint_as_float(z[w & 1][2 * e + 1]));
-          // after a raise the largest rounded product is the reference: the difference is taken
-          // from rounded products and is at most 0, however large they are
-          if (raised) {
-#pragma unroll
-            for (int e = 0; e < 16; e++) {
-              float u, v;
-              upk2(d[e], u, v);
-              d[e] = pk2(__fadd_rn(__fmul_rn(u, zs), nref), __fadd_rn(__fmul_rn(v, zs), nref));
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; e++) d[e] = fma2(d[e], zs2, nr2);
-          }
+          if (General.value && masked) hide(z[w & 1], see[w]);
 #pragma unroll
           for (int e = 0; e < 16; e++) {
-            float u, v;
-            upk2(d[e], u, v);
+            float u = __uint_as_float(z[w & 1][2 * e]), v = __uint_as_float(z[w & 1][2 * e + 1]);
+            if (General.value && raised) {
+              u = __fadd_rn(__fmul_rn(u, zs), nref);
+              v = __fadd_rn(__fmul_rn(v, zs), nref);
+            } else {
+              upk2(fma2(pk2(u, v), zs2, nr2), u, v);
+            }
             u = ex2(u);
             v = ex2(v);
             s2[e & 1] = add2(s2[e & 1], pk2(u, v));
@@ -496,11 +501,18 @@ k_prompt_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         float u, v;
         upk2(add2(s2[0], s2[1]), u, v);
         sum = u + v;
-        if (raised || __all_sync(0xFFFFFFFFu, !active || sum <= kPaMost)) break;
-        raise();
-        raised = true;
+        return __all_sync(0xFFFFFFFFu, !active || sum <= kPaMost);
+      };
+      bool fine = false;
+      if (t > 0 && !rounded) {
+        if (masked) fine = weights(std::true_type(), false);
+        else fine = weights(std::false_type(), false);
       }
-      if (!ok) break;
+      if (!fine) {
+        raise();
+        if (!ok) break;
+        weights(std::true_type(), true);
+      }
       l += sum;
       tmem_put32(ts, pk);
       tmem_put32(ts + 32, pk + 32);
