@@ -659,11 +659,19 @@ def _rows_ptr(t, row):
     whose rows are packed; a part of a wider row, as of a fused projection, is one."""
     if not t.is_cuda:
         raise ValueError("libkvc takes device tensors only")
-    packed = t.dim() >= 2 and t[0].is_contiguous() and t[0].numel() == row
-    if not packed:
+    shape, strides = t.shape, t.stride()
+    if len(strides) == 2 and strides[1] == 1 and shape[1] == row and shape[0] > 1:
+        return t.data_ptr(), strides[0]
+    n = 1  # elements of a row so far, from its end
+    for size, stride in zip(shape[:0:-1], strides[:0:-1]):
+        if size != 1 and stride != n:
+            n = -1
+            break
+        n *= size
+    if n != row:
         raise ValueError(f"libkvc takes rows of {row} packed elements "
-                         f"(got shape {tuple(t.shape)}, strides {t.stride()})")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else row
+                         f"(got shape {tuple(shape)}, strides {strides})")
+    return t.data_ptr(), strides[0] if shape[0] > 1 else row
 
 
 def kvc_qkv_rope(q, k, v, n_tok, wq, wk, eps, rope_tab, n_pos, pos, q_off, ctx_len, n_req,
@@ -677,18 +685,15 @@ def kvc_qkv_rope(q, k, v, n_tok, wq, wk, eps, rope_tab, n_pos, pos, q_off, ctx_l
     (qp, qs), (kp, ks), (vp, vs) = _rows_ptr(q, Hq * D), _rows_ptr(k, H * D), _rows_ptr(v, H * D)
     if min(len(q), len(k), len(v)) < n_tok:
         raise ValueError(f"kvc_qkv_rope: q, k and v hold fewer than {n_tok} rows")
-    raw = 0 if k_raw is None else k_raw.stride(0)
-    if k_raw is not None and not (k_raw.is_cuda and k_raw.dim() == 3 and k_raw.shape[0] == H
-                                  and k_raw.shape[1] >= n_tok and k_raw[0].is_contiguous()
-                                  and k_raw.shape[2] == D):
-        raise ValueError("kvc_qkv_rope: k_raw is a device tensor [H][>= n_tok][D], each head's "
-                         f"rows packed (got shape {tuple(k_raw.shape)}, strides {k_raw.stride()})")
-    if H == 1 and k_raw is not None:
-        raw = max(raw, n_tok * D)
+    rp, raw = None, 0
+    if k_raw is not None:
+        if k_raw.dim() != 3 or k_raw.shape[0] != H or k_raw.shape[1] < n_tok or k_raw.shape[2] != D:
+            raise ValueError(f"kvc_qkv_rope: k_raw is [{H}][>= {n_tok}][{D}] (got {tuple(k_raw.shape)})")
+        rp, raw = _rows_ptr(k_raw, k_raw.shape[1] * D)
     _ok(lib.kvc_qkv_rope(qp, qs, kp, ks, vp, vs, n_tok, _ptr(wq), _ptr(wk), eps, _ptr(rope_tab),
                          n_pos, _ptr(pos), _ptr(q_off), _ptr(ctx_len), n_req, _ptr(block_table),
                          max_blocks, _ptr(kpool), _ptr(vpool), n_slots, H, Hq, D, block_size,
-                         _ptr(q_out), None if k_raw is None else k_raw.data_ptr(), raw,
+                         _ptr(q_out), rp, raw,
                          _ptr(dev_status), _stream(stream)), "kvc_qkv_rope")
 
 

@@ -8,15 +8,23 @@
 // group of one, two or four warps holds a head's block in registers between
 // the maximum and the conversion (16 bytes a load, BS·D/8 of them), so that
 // nothing is read twice; neighbouring heads lie in neighbouring warps, for a
-// row of a page is contiguous over its heads.
+// row of a page is contiguous over its heads.  The CTAs stay and take blocks in
+// turn, the next block's loads under the present one's work: 2048 blocks of 16 rows, 12
+// layers, 8 heads (2.4 GB) 369 us, 6.55 TB/s, 96 % of a copy's rate; a CTA per eight
+// blocks, without the loads ahead, 467; three CTAs per SM instead of two, which spill,
+// 394.
 #include <cuda_fp8.h>
 
+#include <algorithm>
+
 #include "kvc_internal.cuh"
+#include "mma_ptx.cuh"
 
 namespace kvc {
 namespace {
 
 constexpr int kPackWarps = 8;
+constexpr int kPackCtas = 2;   // per SM
 constexpr int kPackLoads = 8;  // 16-byte loads of a lane
 
 struct Q8PackArgs {
@@ -26,77 +34,121 @@ struct Q8PackArgs {
   const int32_t *src, *dst;
   int32_t *status;
   int64_t n_blocks, n_blocks8;
-  int H, BS, hgroups;  // CTAs of one (pair, layer, pool)
+  int64_t units, groups;  // heads' blocks in all, CTAs' worth of them
+  int n, H, BS;
 };
 
-template <int D, int WPU>  // WPU warps hold a head's block
-__global__ void __launch_bounds__(kPackWarps * 32)
+// Largest of two 16-bit halves each.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// A unit: one head's block of one pool and layer, held by WPU warps.
+struct Q8Unit {
+  int64_t at;  // (layer, destination block, head)
+  const uint16_t *from;
+  bool live, v;
+};
+
+template <int D, int WPU>
+__global__ void __launch_bounds__(kPackWarps * 32, kPackCtas)
 k_q8_pack(Q8PackArgs a) {
   constexpr int CH = D / 8, UPC = kPackWarps / WPU;
-  __shared__ uint32_t sh[kPackWarps];
+  __shared__ uint32_t sh[2][kPackWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int pair = blockIdx.x / a.hgroups, l = blockIdx.y;
-  const int h = (blockIdx.x % a.hgroups) * UPC + warp / WPU;
   const int part = (warp % WPU) * 32 + lane;  // thread of the head's block
-  const int32_t src = a.src[pair], dst = a.dst[pair];
-  if (src < 0 && dst < 0) return;  // (a pair that is left out)
-  if (src < 0 || src >= a.n_blocks || dst < 0 || dst >= a.n_blocks8) {
-    if (threadIdx.x == 0) record_error(a.status, KVC_ERR_BOUNDS);
-    return;
-  }
-  const bool live = h < a.H;
-  const int chunks = live ? a.BS * CH : 0;
-  const uint16_t *pool = (blockIdx.z ? a.vpool : a.kpool) +
-                         (((int64_t)l * a.n_blocks + src) * a.BS * a.H + h) * D;
-  uint4 x[kPackLoads];
+  const int chunks = a.BS * CH;
+  // unit i: heads inside, then the pairs, (layer, pool) outside
+  auto find = [&](int64_t i) {
+    Q8Unit u{};
+    i = i * UPC + warp / WPU;
+    if (i >= a.units) return u;
+    const int64_t pl = div64(i, a.H), lv = div64(pl, a.n);
+    const int h = (int)(i - pl * a.H), pair = (int)(pl - lv * a.n), l = (int)(lv >> 1);
+    u.v = lv & 1;
+    const int32_t src = a.src[pair], dst = a.dst[pair];
+    u.live = src >= 0 && src < a.n_blocks && dst >= 0 && dst < a.n_blocks8;
+    if (!u.live && !(src < 0 && dst < 0) && part == 0) record_error(a.status, KVC_ERR_BOUNDS);
+    u.at = ((int64_t)l * a.n_blocks8 + dst) * a.H + h;
+    u.from = (u.v ? a.vpool : a.kpool) + (((int64_t)l * a.n_blocks + src) * a.BS * a.H + h) * D;
+    return u;
+  };
+  uint4 nx[kPackLoads];
+  auto load = [&](const Q8Unit &u) {
 #pragma unroll
-  for (int i = 0; i < kPackLoads; i++) {
-    const int e = i * WPU * 32 + part;
-    x[i] = make_uint4(0, 0, 0, 0);
-    if (e < chunks) x[i] = ld_stream(pool + (int64_t)(e / CH) * a.H * D + (e % CH) * 8);
-  }
-  // the largest finite magnitude, as bf16 bits (their order is the values')
-  uint32_t top = 0;
-  bool odd = false;
-#pragma unroll
-  for (int i = 0; i < kPackLoads; i++) {
-    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-    for (int e = 0; e < 4; e++) {
-      const uint32_t a0 = w[e] & 0x7FFFu, a1 = (w[e] >> 16) & 0x7FFFu;
-      odd |= a0 >= 0x7F80u || a1 >= 0x7F80u;
-      top = max(top, max(a0 < 0x7F80u ? a0 : 0u, a1 < 0x7F80u ? a1 : 0u));
+    for (int i = 0; i < kPackLoads; i++) {
+      const int e = i * WPU * 32 + part;
+      nx[i] = make_uint4(0, 0, 0, 0);
+      if (u.live && e < chunks) nx[i] = ld_stream(u.from + (int64_t)(e / CH) * a.H * D + (e % CH) * 8);
     }
-  }
-  top = __reduce_max_sync(0xFFFFFFFFu, top);
-  if (WPU > 1) {
-    if (lane == 0) sh[warp] = top;
-    __syncthreads();
+  };
+  int64_t g = blockIdx.x;
+  if (g >= a.groups) return;
+  Q8Unit next = find(g);
+  load(next);
+  for (int it = 0; g < a.groups; it++) {
+    const Q8Unit u = next;
+    uint4 x[kPackLoads];
 #pragma unroll
-    for (int w = 0; w < WPU; w++) top = max(top, sh[warp / WPU * WPU + w]);
-  }
-  if (odd) record_error(a.status, KVC_ERR_NAN);
-  if (!live) return;
-  // top = m·2^x with m in [1, 2): 448 = 1.75·2^8, so s = 2^(x − 8), or twice that past 1.75
-  int ex = (int)(top >> 7) - 127 - 8 + ((top & 0x7Fu) > 0x60u);
-  ex = top == 0 ? 0 : max(ex, -126);
-  const float scale = __uint_as_float((uint32_t)(ex + 127) << 23);
-  const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
-  const int64_t at = ((int64_t)l * a.n_blocks8 + dst) * a.H + h;
-  uint8_t *out = (blockIdx.z ? a.v8 : a.k8) + at * a.BS * D;
+    for (int i = 0; i < kPackLoads; i++) x[i] = nx[i];
+    g += gridDim.x;
+    if (g < a.groups) {  // (the next unit is on its way while this one is worked out)
+      next = find(g);
+      load(next);
+    }
+    // the largest magnitude, as bf16 bits (their order is the values')
+    uint32_t top2 = 0;
 #pragma unroll
-  for (int i = 0; i < kPackLoads; i++) {
-    const int e = i * WPU * 32 + part;
-    if (e >= chunks) break;
-    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-    uint32_t y[4];
+    for (int i = 0; i < kPackLoads; i++) {
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
-    for (int u = 0; u < 4; u++)
-      y[u] = __nv_cvt_float2_to_fp8x2(make_float2(bf16_lo(w[u]) * inv, bf16_hi(w[u]) * inv),
-                                      __NV_SATFINITE, __NV_E4M3);
-    *reinterpret_cast<uint2 *>(out + e * 8) = make_uint2(y[0] | y[1] << 16, y[2] | y[3] << 16);
+      for (int e = 0; e < 4; e++) top2 = max_u16x2(top2, w[e] & 0x7FFF7FFFu);
+    }
+    uint32_t top = max(top2 & 0xFFFFu, top2 >> 16);
+    const bool odd = top >= 0x7F80u;
+    if (odd) {  // infinities or NaN: the largest finite one
+      record_error(a.status, KVC_ERR_NAN);
+      top = 0;
+#pragma unroll
+      for (int i = 0; i < kPackLoads; i++) {
+        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          const uint32_t a0 = w[e] & 0x7FFFu, a1 = (w[e] >> 16) & 0x7FFFu;
+          top = max(top, max(a0 < 0x7F80u ? a0 : 0u, a1 < 0x7F80u ? a1 : 0u));
+        }
+      }
+    }
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    if (WPU > 1) {
+      if (lane == 0) sh[it & 1][warp] = top;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < WPU; w++) top = max(top, sh[it & 1][warp / WPU * WPU + w]);
+    }
+    if (!u.live) continue;
+    // top = m·2^x with m in [1, 2): 448 = 1.75·2^8, so s = 2^(x − 8), or twice that past 1.75
+    int ex = (int)(top >> 7) - 127 - 8 + ((top & 0x7Fu) > 0x60u);
+    ex = top == 0 ? 0 : max(ex, -126);
+    const float scale = __uint_as_float((uint32_t)(ex + 127) << 23);
+    const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
+    uint8_t *out = (u.v ? a.v8 : a.k8) + u.at * a.BS * D;
+#pragma unroll
+    for (int i = 0; i < kPackLoads; i++) {
+      const int e = i * WPU * 32 + part;
+      if (e >= chunks) break;
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      uint32_t y[4];
+#pragma unroll
+      for (int k = 0; k < 4; k++)
+        y[k] = __nv_cvt_float2_to_fp8x2(make_float2(bf16_lo(w[k]) * inv, bf16_hi(w[k]) * inv),
+                                        __NV_SATFINITE, __NV_E4M3);
+      *reinterpret_cast<uint2 *>(out + e * 8) = make_uint2(y[0] | y[1] << 16, y[2] | y[3] << 16);
+    }
+    if (part == 0) (u.v ? a.vscale : a.kscale)[u.at] = scale;
   }
-  if (part == 0) (blockIdx.z ? a.vscale : a.kscale)[at] = scale;
 }
 
 }  // namespace
@@ -111,8 +163,10 @@ cudaError_t launch_q8_pack(const uint16_t *kpool, const uint16_t *vpool, int64_t
   a.n_blocks = n_slots / BS, a.n_blocks8 = n_blocks8, a.H = H, a.BS = BS;
   const int warps = (BS * D / 8 + kPackLoads * 32 - 1) / (kPackLoads * 32);
   const int wpu = warps <= 1 ? 1 : warps <= 2 ? 2 : 4;
-  a.hgroups = (H * wpu + kPackWarps - 1) / kPackWarps;
-  const dim3 grid((unsigned)(n * a.hgroups), (unsigned)L, 2);
+  a.n = n;
+  a.units = (int64_t)n * H * L * 2;
+  a.groups = (a.units * wpu + kPackWarps - 1) / kPackWarps;
+  const unsigned grid = (unsigned)std::min<int64_t>(a.groups, kPackCtas * device_sm_count());
   auto *kern = D == 128 ? (wpu == 1 ? k_q8_pack<128, 1> : wpu == 2 ? k_q8_pack<128, 2> : k_q8_pack<128, 4>)
                         : (wpu == 1 ? k_q8_pack<64, 1> : k_q8_pack<64, 2>);
   kern<<<grid, kPackWarps * 32, 0, s>>>(a);

@@ -8,15 +8,20 @@
 // A warp owns a token (or a part of its heads, where there are few tokens):
 // D/16 lanes hold a head, lane c the pairs (j, j + D/2) for j in [8c, 8c + 8),
 // so that a rotation needs no exchange and the norm only D/16 lanes'.  Its
-// cosines and sines stay in registers over all heads, and kAhead groups of
-// heads are in flight.
+// cosines and sines stay in registers over all heads.  What counts is how many
+// warps an SM holds (a warp waits for lookups, its row and the norm's sum in turn):
+// 32 warps with one group of heads ahead take 44 us for 8192 tokens of 48 heads with
+// norms and raw keys (222 MB, 5.05 TB/s) and 127 us for 22K tokens of 64 heads without
+// (5.98 TB/s, 88 % of a copy's rate); 24 warps with two ahead 52 and 143, 16 with four
+// 55 and 158; bulk copies into a ring of shared memory (24 warps) 47 and 137.
 #include "kvc_internal.cuh"
 
 namespace kvc {
 namespace {
 
-constexpr int kRopeWarps = 4;
-constexpr int kAhead = 4;
+constexpr int kRopeWarps = 2;
+constexpr int kRopeCtas = 16;  // per SM
+constexpr int kAhead = 1;    // groups of heads in flight
 
 struct RopeArgs {
   const uint16_t *q, *k, *v, *wq, *wk;
@@ -57,7 +62,7 @@ __device__ __forceinline__ int warp_last_le(const int32_t *off, int n, int x) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kRopeWarps * 32)
+__global__ void __launch_bounds__(kRopeWarps * 32, kRopeCtas)
 k_qkv_rope(RopeArgs a) {
   constexpr int LPH = D / 16, HPW = 32 / LPH, HALF = D / 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -152,7 +157,7 @@ k_qkv_rope(RopeArgs a) {
       }
       const uint16_t *w = kind ? a.wk : a.wq;
       if (w) {
-        const float f = 1.f / sqrtf(sum * (1.f / D) + a.eps);
+        const float f = rsqrtf(sum * (1.f / D) + a.eps);
         const uint4 w0 = __ldg(reinterpret_cast<const uint4 *>(w + 8 * c));
         const uint4 w1 = __ldg(reinterpret_cast<const uint4 *>(w + HALF + 8 * c));
         const uint32_t a0[4] = {w0.x, w0.y, w0.z, w0.w}, a1[4] = {w1.x, w1.y, w1.z, w1.w};
