@@ -10,16 +10,28 @@
 // unit's tiles are those of its history and then those of its bf16 rows.  The
 // bound is the stream: 2·D bytes per position of the history.
 //
-// e4m3 is a subset of fp16, so a byte becomes an fp16 operand by one conversion of
-// two and the products are exact; q, a bf16 value, is exact in fp16 once each row
-// is shifted by a power of two that puts its largest value just below 2^15 (what
-// falls below fp16's range is 2^-39 of that value).  The scales stay out of the
-// operands: a logit is multiplied by s_k, and the weight of V is
-// 2^(z + log2 s_v − reference), on a running maximum of its own, so that no scale
-// takes it out of fp16's range; the softmax's sum has its own exponent.
+// k_q8_rows: each of a CTA's four warps streams its own quarter of every tile (32
+// positions of the history, or 4 KB of bf16 keys) through a private ring of shared memory,
+// by TMA boxes of rows of a block where every position of the quarter is there, else by
+// cp.async; no barrier until the run ends.  Positions are the products' M dimension
+//   Sᵀ[position][row] = K·Qᵀ,   Oᵀ[d][row] += Vᵀ·Pᵀ
+// (mma.sync m16n8k16), so that rows come in eights and a token of four heads does not pay
+// for sixteen rows: 64 products a quarter tile and eight rows, half of what rows as M take.
+// e4m3 is a subset of fp16, so a byte becomes an fp16 operand by a conversion of two and
+// the products are exact; q, a bf16 value, is exact in fp16 once each row is shifted by a
+// power of two that puts its largest value just below 2^15 (what falls below fp16's range
+// is 2^-39 of that value).  V's operand is read by the transposing ldmatrix, two bytes a
+// number: a register then holds two columns of two positions, and O's columns come in
+// pairs until usual() puts them in order.
+//
+// The scales stay out of the operands: a logit is multiplied by s_k, and P is the weight
+// times s_v on a reference of its own.  References are a row's largest over its first
+// tile (less kQ8Room, in log2), raised when a weight passes 2^15: weights fit fp16 whatever the
+// scales, and a tile needs no maximum.
 #include <float.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "tree_rows.cuh"
 
@@ -31,6 +43,10 @@ constexpr int kQ8Threads = kQ8Warps * 32;
 constexpr int kQ8Stages = 3;
 constexpr int kQ8Stage = 8192;  // bytes of one warp's stage: K rows, then V rows
 constexpr int kQ8Keys = 32;     // positions of a warp's stage of the history
+constexpr float kQ8Unset = -FLT_MAX;   // reference of a row that has seen nothing
+constexpr float kQ8Room = 8.f;         // log2 of the largest weight of a row's first tile
+constexpr float kQ8Most = 32768.f;     // weight, and sum of a thread's four, that raises the references
+constexpr float kQ8Round = 1048576.f;  // |reference| from which logits are rounded before the difference
 
 struct Q8Args : TreeArgs {
   const uint8_t *k8, *v8;
@@ -38,6 +54,7 @@ struct Q8Args : TreeArgs {
   const int32_t *table8, *len8;
   int64_t n_blocks8;
   int max_blocks8;
+  int box8;  // rows of a TMA box of the 8-bit pools (a divisor of the page size), 0: no TMA
 };
 
 // Request r's sizes; false when they are out of range.
@@ -57,26 +74,41 @@ __device__ __forceinline__ void tree_tiles(const Q8Args &a, int r, int &n_rt, in
   n_kt = q8_tiles(n) + (c + T + a.tile - 1) / a.tile;
 }
 
-template <int D, int MT>
+template <int D, int NR>
 struct Q8Smem {
+  static constexpr int R = 8 * NR;
   static constexpr int kRing = kQ8Warps * kQ8Stages * kQ8Stage;
-  static constexpr int kQh = kRing;                      // MT·16 rows of q in fp16, in the products' order
-  static constexpr int kScale = kQh + MT * 16 * D * 2;   // (s_k, s_v) of a stage's positions
+  static constexpr int kQh = kRing;              // the rows of q in fp16, in the products' order
+  static constexpr int kScale = kQh + R * D * 2; // (s_k, s_v) of a stage's positions
   static constexpr int kRow = kScale + kQ8Warps * kQ8Stages * kQ8Keys * 8;  // a row's power of two
-  static constexpr int kValid = kRow + MT * 16 * 4;      // valid positions per (warp, stage)
-  static constexpr int kMl = kValid + (kQ8Warps * kQ8Stages * 4 + 15) / 16 * 16;  // (max, sum) per (warp, row)
-  static constexpr int kBytes = kMl + kQ8Warps * MT * 16 * 8;
+  static constexpr int kValid = kRow + R * 4;    // valid positions per (warp, stage)
+  static constexpr int kMl = kValid + (kQ8Warps * kQ8Stages * 4 + 15) / 16 * 16;  // (reference, sum) per (warp, row)
+  static constexpr int kFull = kMl + kQ8Warps * R * 8;  // barriers per (warp, stage), then a word
+  static constexpr int kBytes = kFull + kQ8Warps * kQ8Stages * 8 + 16;
   static_assert(2 * (kBytes + 1024) <= 228 * 1024, "two CTAs fit an SM");
-  static_assert(kQ8Warps * MT * 16 * D * 4 <= kRing, "the warps' O fit the ring");
+  static_assert(kQ8Warps * R * D * 4 <= kRing, "the warps' O fit the ring");
   static_assert(2 * kQ8Keys * D <= kQ8Stage, "a stage of the history fits");
 };
 
-// Byte offset of 16-byte chunk c of 8-bit row `row`: eight rows of one chunk, and two
-// rows of four chunks, hit distinct banks.
+// Byte offset of 16-byte chunk c of 8-bit row `row`: the 128- and 64-byte swizzles of TMA.
 template <int D>
 __device__ __forceinline__ uint32_t swz8(int row, int c) {
-  const int f = D == 128 ? ((row & 1) << 2) | ((row >> 1) & 3) : (row >> 1) & 3;
-  return (uint32_t)(row * D + ((c ^ f) << 4));
+  return (uint32_t)(row * D + ((c ^ (D == 128 ? row & 7 : (row >> 1) & 3)) << 4));
+}
+__device__ __forceinline__ void tma_load_2d_if(uint32_t lead, uint32_t dst, const CUtensorMap *map, int x,
+                                               int y, uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %5, 0;\n"
+      " @q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];\n}\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"(lead)
+      : "memory");
+}
+// An 8×8 matrix of 16-bit values (row t/4, columns 2·(t%4) + {0, 1} in thread t), transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(x));
+  return d;
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, bool valid) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
@@ -119,22 +151,29 @@ __device__ __forceinline__ float lg2(float x) {
   return y;
 }
 
-template <int D, int MT>
+template <int D, int NR>
 __global__ void __launch_bounds__(kQ8Threads, 2)
-k_q8_rows(Q8Args a) {
-  using S = Q8Smem<D, MT>;
-  constexpr int KT = 2048 / D, KS = D / 16, NT = D / 8, CH = D / 8, CH8 = D / 16;
-  constexpr int R = MT * 16;
+k_q8_rows(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, Q8Args a) {
+  using S = Q8Smem<D, NR>;
+  constexpr int KT = 2048 / D, KS = D / 16, CH = D / 8, CH8 = D / 16;
+  constexpr int R = 8 * NR;
   extern __shared__ __align__(1024) uint8_t sm[];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = lane & 3;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = lane & 3, g8 = lane >> 2;
   const uint32_t ring = smem_u32(sm) + warp * kQ8Stages * kQ8Stage;
   uint32_t *valid_s = reinterpret_cast<uint32_t *>(sm + S::kValid) + warp * kQ8Stages;
   const float2 *scale_s = reinterpret_cast<const float2 *>(sm + S::kScale) + warp * kQ8Stages * kQ8Keys;
   const uint32_t qhbase = smem_u32(sm + S::kQh);
+  const uint32_t full = smem_u32(sm + S::kFull) + warp * kQ8Stages * 8;
+  volatile int *failed = reinterpret_cast<volatile int *>(sm + S::kFull + kQ8Warps * kQ8Stages * 8);
   float *row_s = reinterpret_cast<float *>(sm + S::kRow);
   float2 *ml_s = reinterpret_cast<float2 *>(sm + S::kMl);
 
   asm volatile("griddepcontrol.launch_dependents;");
+  if (lane == 0) {
+    for (int i = 0; i < kQ8Stages; i++) mbar_init(full + 8 * i, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (tid == 0) *failed = 0;
   if (blockIdx.x == 0)  // one report per bad request
     for (int r = tid; r < a.n_req; r += kQ8Threads) {
       int n, c, q0, T;
@@ -149,6 +188,7 @@ k_q8_rows(Q8Args a) {
   const int64_t total = sums.total;
   const int n_cta = (int)min((int64_t)a.n_cta, total);  // every run holds a tile
   if ((int)blockIdx.x >= n_cta) return;
+  __syncthreads();
   const int64_t run0 = run_start(total, n_cta, blockIdx.x);
   const int64_t run1 = run_start(total, n_cta, blockIdx.x + 1);
   int64_t g = run0, before;  // next tile of the run
@@ -160,6 +200,7 @@ k_q8_rows(Q8Args a) {
   int t0 = (int)(g - before - (int64_t)unit * n_kt);
 
   const int64_t n_blocks = a.n_slots / a.BS;
+  uint32_t boxed = 0, phase = 0;  // bits of the stages: filled by TMA, the barrier's parity
   while (g < run1) {
     const int h = unit / n_rt, rt = unit % n_rt;
     const int t1 = (int)min((int64_t)n_kt, t0 + (run1 - g));
@@ -169,20 +210,30 @@ k_q8_rows(Q8Args a) {
     const int32_t *bt8 = a.table8 + (int64_t)r * a.max_blocks8;
     const int end = c + T;
 
+    // the block id of this lane's position of tile t, looked up a tile ahead
+    int32_t next_blk;
+    auto look = [&](int t) {
+      next_blk = -1;
+      if (t < th) {
+        const int p = (t * kQ8Warps + warp) * kQ8Keys + lane;
+        if (p < n8) next_blk = bt8[page_of(p, a.bs_inv)];
+      } else if (t < t1) {
+        const int p = (t - th) * a.tile + warp * KT + lane;
+        if (lane < KT && p < end) next_blk = bt[page_of(p, a.bs_inv)];
+      }
+    };
     // issue one stage: this warp's positions of tile t
     auto issue = [&](int t, int st) {
       const uint32_t dst = ring + st * kQ8Stage;
+      int32_t blk = next_blk;
+      look(t + 1);
+      boxed &= ~(1u << st);
       if (t < th) {
-        const int p = t * (kQ8Warps * kQ8Keys) + warp * kQ8Keys + lane;
-        int32_t blk = -1, at = 0;
-        if (p < n8) {
-          const int pg = page_of(p, a.bs_inv);
-          blk = bt8[pg];
-          at = p - pg * a.BS;
-          if (blk < 0 || blk >= a.n_blocks8) {
-            record_error(a.status, KVC_ERR_BOUNDS);
-            blk = -1;
-          }
+        const int p = (t * kQ8Warps + warp) * kQ8Keys + lane;
+        const int at = p - page_of(p, a.bs_inv) * a.BS;
+        if (p < n8 && (blk < 0 || blk >= a.n_blocks8)) {
+          record_error(a.status, KVC_ERR_BOUNDS);
+          blk = -1;
         }
         const uint32_t ok = __ballot_sync(0xFFFFFFFFu, blk >= 0);
         if (lane == 0) valid_s[st] = ok;
@@ -190,30 +241,43 @@ k_q8_rows(Q8Args a) {
         const uint32_t sc = smem_u32(sm + S::kScale) + ((warp * kQ8Stages + st) * kQ8Keys + lane) * 8;
         cp_async4(sc, a.kscale + unit8, blk >= 0);
         cp_async4(sc + 4, a.vscale + unit8, blk >= 0);
-        constexpr int RPI = 32 / CH8;  // rows one instruction of the warp copies
-        const int col = lane % CH8;
-#pragma unroll
-        for (int i = 0; i < kQ8Keys / RPI; i++) {
-          const int row = i * RPI + lane / CH8;
-          const int32_t b = __shfl_sync(0xFFFFFFFFu, blk, row), o = __shfl_sync(0xFFFFFFFFu, at, row);
-          const int64_t from = (((int64_t)max(b, 0) * a.H + h) * a.BS + o) * D + col * 16;
-          cp_async16(dst + swz8<D>(row, col), a.k8 + from, b >= 0);
-          cp_async16(dst + kQ8Keys * D + swz8<D>(row, col), a.v8 + from, b >= 0);
+        if (a.box8 && ok == 0xFFFFFFFFu) {
+          const uint32_t bar = full + 8 * st;
+          // (what was written and read here before is ordered before the copies)
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          if (lane == 0) mbar_expect_tx(bar, 2 * kQ8Keys * D);
+          __syncwarp();
+          boxed |= 1u << st;
+          const int row = (int)unit8 * a.BS + at;
+          for (int k = 0; k < kQ8Keys; k += a.box8) {
+            const int y = __shfl_sync(0xFFFFFFFFu, row, k);
+            tma_load_2d_if(lane == 0, dst + k * D, &tm_k, 0, y, bar);
+            tma_load_2d_if(lane == 0, dst + (kQ8Keys + k) * D, &tm_v, 0, y, bar);
+          }
+        } else {
+          constexpr int RPI = 32 / CH8;  // rows one instruction of the warp copies
+          const int col = lane % CH8;
+#pragma unroll 2
+          for (int i = 0; i < kQ8Keys / RPI; i++) {
+            const int row = i * RPI + lane / CH8;
+            const int32_t b = __shfl_sync(0xFFFFFFFFu, blk, row), o = __shfl_sync(0xFFFFFFFFu, at, row);
+            const int64_t from = (((int64_t)max(b, 0) * a.H + h) * a.BS + o) * D + col * 16;
+            cp_async16(dst + swz8<D>(row, col), a.k8 + from, b >= 0);
+            cp_async16(dst + kQ8Keys * D + swz8<D>(row, col), a.v8 + from, b >= 0);
+          }
         }
       } else {
-        const int p0 = (t - th) * a.tile + warp * KT;
+        const int p = (t - th) * a.tile + warp * KT + lane;
         int32_t slot = -1;
-        if (lane < KT && p0 + lane < end) {
-          const int p = p0 + lane;
-          const int32_t b = bt[page_of(p, a.bs_inv)];
-          if (b >= 0 && b < n_blocks) slot = b * a.BS + p - page_of(p, a.bs_inv) * a.BS;
+        if (lane < KT && p < end) {
+          if (blk >= 0 && blk < n_blocks) slot = blk * a.BS + p - page_of(p, a.bs_inv) * a.BS;
           else record_error(a.status, KVC_ERR_BOUNDS);
         }
         const uint32_t ok = __ballot_sync(0xFFFFFFFFu, slot >= 0);
         if (lane == 0) valid_s[st] = ok;
         constexpr int RPI = 32 / CH;
         const int col = lane % CH;
-#pragma unroll
+#pragma unroll 2
         for (int i = 0; i < KT / RPI; i++) {
           const int row = i * RPI + lane / CH;
           const int32_t sl = __shfl_sync(0xFFFFFFFFu, slot, row);
@@ -224,6 +288,7 @@ k_q8_rows(Q8Args a) {
       }
     };
     const int n_t = t1 - t0;
+    look(t0);
 #pragma unroll
     for (int s = 0; s < kQ8Stages - 1; s++) {
       if (s < n_t) issue(t0 + s, s);
@@ -242,7 +307,7 @@ k_q8_rows(Q8Args a) {
 #pragma unroll
       for (int u = 0; u < 4; u++) top = max(top, max(w[u] & 0x7FFFu, (w[u] >> 16) & 0x7FFFu));
 #pragma unroll
-      for (int o = 1; o < CH; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+      for (int o = 1; o < CH; o <<= 1) top = max(top, __shfl_xor_sync(__activemask(), top, o));
       const int ex = max((int)(top >> 7) - 127 - 14, -126);
       if (col == 0) row_s[row] = __uint_as_float((uint32_t)(ex + 127) << 23);
       const float f = __uint_as_float((uint32_t)(127 - ex) << 23);
@@ -256,85 +321,148 @@ k_q8_rows(Q8Args a) {
             pack_f16x2(bf16_lo(w[u]) * f, bf16_hi(w[u]) * f);
     }
     __syncthreads();
-    // one row tile of 16 keeps q in registers, in fp16 until the bf16 rows begin
-    uint32_t qf[MT == 1 ? KS : 1][4];
-    auto query16 = [&](int mt, int ks, uint32_t (&f)[4]) {  // a fragment of the bf16 queries
-#pragma unroll
-      for (int hf = 0; hf < 2; hf++) {
-        const int row = mt * 16 + hf * 8 + lane / 4, x = rt * a.rstep + row;
-        const uint16_t *p = a.q + ((int64_t)(q0 + x / a.G) * a.Hq + h * a.G + x % a.G) * D + 16 * ks + 2 * quad;
-        f[hf] = row < n_rows ? __ldg(reinterpret_cast<const uint32_t *>(p)) : 0u;
-        f[2 + hf] = row < n_rows ? __ldg(reinterpret_cast<const uint32_t *>(p + 8)) : 0u;
-      }
+    // two products' operands of eight rows' queries (products ks and ks + 1)
+    auto query8 = [&](int nr, int ks, uint32_t (&f)[4]) {
+      ldsm4(qhbase + swz<D>(8 * nr + (lane & 7), 2 * ks + (lane >> 3)), f);
     };
-    auto queries = [&](bool eight) {
-      if (MT == 1)
-#pragma unroll
-        for (int ks = 0; ks < KS; ks++) {
-          if (eight) ldsm4(qhbase + swz<D>(lane % 16, 2 * ks + lane / 16), qf[MT == 1 ? ks : 0]);
-          else query16(0, ks, qf[MT == 1 ? ks : 0]);
-        }
+    auto query16 = [&](int nr, int ks, uint32_t &b0, uint32_t &b1) {  // one product's, bf16
+      const int row = 8 * nr + g8, x = rt * a.rstep + row;
+      const uint16_t *p = a.q + ((int64_t)(q0 + x / a.G) * a.Hq + h * a.G + x % a.G) * D + 16 * ks + 2 * quad;
+      b0 = row < n_rows ? __ldg(reinterpret_cast<const uint32_t *>(p)) : 0u;
+      b1 = row < n_rows ? __ldg(reinterpret_cast<const uint32_t *>(p + 8)) : 0u;
     };
+    uint32_t qf[NR == 1 ? KS / 2 : 1][4];  // eight rows keep q in registers
+    if (NR == 1)
+#pragma unroll
+      for (int i = 0; i < KS / 2; i++) query8(0, 2 * i, qf[NR == 1 ? i : 0]);
     bool hist = t0 < th;  // O's columns lie as the history's products leave them
-    queries(hist);
 
-    // m: largest logit, l: sum of the weights on it; mo: O's reference
-    float o[MT][NT][4], m[MT][2], l[MT][2], mo[MT][2];
+    // This thread's rows 8·nr + 2·quad + {0, 1}: the softmax's reference, its part of the sum,
+    // how far O's reference lies above the softmax's; O of its columns.  References are the
+    // warp's own.
+    float o[CH8][NR][4], ref[NR][2], l[NR][2], off[NR][2], rs[NR][2];
+    bool rounded = false;  // (warp-uniform) some reference is so large that differences need care
 #pragma unroll
-    for (int mt = 0; mt < MT; mt++) {
-      m[mt][0] = m[mt][1] = mo[mt][0] = mo[mt][1] = -INFINITY;
-      l[mt][0] = l[mt][1] = 0.f;
+    for (int nr = 0; nr < NR; nr++) {
 #pragma unroll
-      for (int n = 0; n < NT; n++) o[mt][n][0] = o[mt][n][1] = o[mt][n][2] = o[mt][n][3] = 0.f;
+      for (int e = 0; e < 2; e++) {
+        ref[nr][e] = kQ8Unset;
+        l[nr][e] = off[nr][e] = 0.f;
+        rs[nr][e] = row_s[8 * nr + 2 * quad + e];
+      }
+#pragma unroll
+      for (int n = 0; n < CH8; n++) o[n][nr][0] = o[n][nr][1] = o[n][nr][2] = o[n][nr][3] = 0.f;
     }
-    // The running maxima take in one row's new ones; O is rescaled.
-    auto raise = [&](int mt, int hf, float mx, float mv, float &base, float &baseo) {
-      mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-      mv = fmaxf(mv, __shfl_xor_sync(0xFFFFFFFFu, mv, 1));
-      mv = fmaxf(mv, __shfl_xor_sync(0xFFFFFFFFu, mv, 2));
-      base = mx == -INFINITY ? 0.f : mx;
-      baseo = mv == -INFINITY ? 0.f : mv;
-      l[mt][hf] *= ex2(m[mt][hf] - base);
-      const float f = ex2(mo[mt][hf] - baseo);
-      m[mt][hf] = mx;
-      mo[mt][hf] = mv;
-      if (!__all_sync(0xFFFFFFFFu, f == 1.f))
-#pragma unroll
-        for (int n = 0; n < NT; n++) {
-          o[mt][n][hf * 2] *= f;
-          o[mt][n][hf * 2 + 1] *= f;
-        }
-    };
-    // From the columns of the history's products (thread j of a quad: 16c + 4j + {0, 2} in
-    // tile 2c, + {1, 3} in tile 2c + 1) to the usual ones (8n + 2j + {0, 1}).
+    // From the columns of the history's products (16n + 2·g8 and the next one, in elements
+    // 0, 1 and 2, 3) to the usual ones (16n + g8 and 16n + 8 + g8).
     auto usual = [&]() {
-      const int base = (lane & ~3) | (quad >> 1);
+      const int from = ((lane >> 3) << 2) | quad;
 #pragma unroll
-      for (int mt = 0; mt < MT; mt++)
+      for (int n = 0; n < CH8; n++)
 #pragma unroll
-        for (int cc = 0; cc < NT / 2; cc++)
+        for (int nr = 0; nr < NR; nr++)
 #pragma unroll
-          for (int hf = 0; hf < 2; hf++) {
-            const float v[4] = {o[mt][2 * cc][hf * 2], o[mt][2 * cc + 1][hf * 2],
-                                o[mt][2 * cc][hf * 2 + 1], o[mt][2 * cc + 1][hf * 2 + 1]};
-            float x[4], y[4];
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-              x[e] = __shfl_sync(0xFFFFFFFFu, v[e], base);
-              y[e] = __shfl_sync(0xFFFFFFFFu, v[e], base + 2);
-            }
-            o[mt][2 * cc][hf * 2] = quad & 1 ? x[2] : x[0];
-            o[mt][2 * cc][hf * 2 + 1] = quad & 1 ? x[3] : x[1];
-            o[mt][2 * cc + 1][hf * 2] = quad & 1 ? y[2] : y[0];
-            o[mt][2 * cc + 1][hf * 2 + 1] = quad & 1 ? y[3] : y[1];
+          for (int e = 0; e < 2; e++) {
+            const float v0 = o[n][nr][e], v1 = o[n][nr][2 + e];
+            const float x0 = __shfl_sync(0xFFFFFFFFu, v0, from), x1 = __shfl_sync(0xFFFFFFFFu, v1, from);
+            const float y0 = __shfl_sync(0xFFFFFFFFu, v0, from + 16), y1 = __shfl_sync(0xFFFFFFFFu, v1, from + 16);
+            o[n][nr][e] = g8 & 1 ? x1 : x0;
+            o[n][nr][2 + e] = g8 & 1 ? y1 : y0;
           }
       hist = false;
+    };
+    // Logits s become weights in place.  The factor of a logit is kz[key]·rs[row] (one of
+    // them 1), that of V sv[key]; keys 8i + g8 of the tile, NK eights.
+    auto softmax = [&](auto Nk, auto &s, const auto &kz, const auto &sv, bool scaled, bool masked,
+                       const auto &vis) {
+      constexpr int NK = decltype(Nk)::value;
+      auto weights = [&](bool raised, float (&sum)[NR][2], float (&w)[NK / 2][NR][4]) {
+        bool fine = true;
+#pragma unroll
+        for (int nr = 0; nr < NR; nr++)
+#pragma unroll
+          for (int e = 0; e < 2; e++) {
+            const float f = ex2(-off[nr][e]);
+            float most = 0.f;
+            sum[nr][e] = 0.f;
+#pragma unroll
+            for (int i = 0; i < NK; i++) {
+              float &x = s[i / 2][nr][2 * (i & 1) + e];
+              const float k = scaled ? kz[i] * rs[nr][e] : a.zscale;
+              float z = raised ? __fsub_rn(__fmul_rn(x, k), ref[nr][e]) : fmaf(x, k, -ref[nr][e]);
+              if (masked && !((vis[nr][e] >> (8 * i + g8)) & 1u)) z = -INFINITY;
+              z = ex2(z);
+              sum[nr][e] += z;
+              z *= scaled ? sv[i] * f : f;
+              most = fmaxf(most, z);
+              w[i / 2][nr][2 * (i & 1) + e] = z;
+            }
+            fine = fine && sum[nr][e] <= kQ8Most && most <= kQ8Most;
+          }
+        return __all_sync(0xFFFFFFFFu, fine);
+      };
+      float sum[NR][2], w[NK / 2][NR][4];
+      // (a row that has seen nothing makes an infinite weight of the first key it sees)
+      if (rounded || !weights(false, sum, w)) {
+        bool large = false;
+#pragma unroll
+        for (int nr = 0; nr < NR; nr++)
+#pragma unroll
+          for (int e = 0; e < 2; e++) {
+            float z[NK], mx = -INFINITY, mv = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < NK; i++) {
+              z[i] = __fmul_rn(s[i / 2][nr][2 * (i & 1) + e], scaled ? kz[i] * rs[nr][e] : a.zscale);
+              if (masked && !((vis[nr][e] >> (8 * i + g8)) & 1u)) z[i] = -INFINITY;
+              mx = fmaxf(mx, z[i]);
+            }
+#pragma unroll
+            for (int o2 = 4; o2 < 32; o2 <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o2));
+            // (a large reference is the largest rounded product itself: its difference is 0)
+            const float now = fmaxf(ref[nr][e], fabsf(mx) < kQ8Round ? mx - kQ8Room : mx);
+#pragma unroll
+            for (int i = 0; i < NK; i++)
+              if (z[i] > -INFINITY) mv = fmaxf(mv, __fsub_rn(z[i], now) + (scaled ? lg2(sv[i]) : 0.f));
+#pragma unroll
+            for (int o2 = 4; o2 < 32; o2 <<= 1) mv = fmaxf(mv, __shfl_xor_sync(0xFFFFFFFFu, mv, o2));
+            const float d = ref[nr][e] - now;
+            const float up = fminf(fmaxf(fmaxf(mv - kQ8Room, d + off[nr][e]), -125.f), 125.f);
+            const float f = ex2(d + off[nr][e] - up);
+            l[nr][e] *= ex2(d);
+#pragma unroll
+            for (int n = 0; n < CH8; n++) {
+              o[n][nr][e] *= f;
+              o[n][nr][2 + e] *= f;
+            }
+            ref[nr][e] = now;
+            off[nr][e] = up;
+            large = large || (now != kQ8Unset && !(fabsf(now) < kQ8Round));
+          }
+        rounded = __any_sync(0xFFFFFFFFu, large);
+        weights(true, sum, w);
+      }
+#pragma unroll
+      for (int nr = 0; nr < NR; nr++)
+#pragma unroll
+        for (int e = 0; e < 2; e++) l[nr][e] += sum[nr][e];
+#pragma unroll
+      for (int i = 0; i < NK / 2; i++)
+#pragma unroll
+        for (int nr = 0; nr < NR; nr++)
+#pragma unroll
+          for (int e = 0; e < 4; e++) s[i][nr][e] = w[i][nr][e];
     };
 
     int st = 0;
     for (int t = t0; t < t1; t++) {
       cp_wait<kQ8Stages - 2>();
+      if ((boxed >> st) & 1u) {
+        if (!mbar_wait_bounded(full + 8 * st, (phase >> st) & 1u, failed)) {
+          *failed = 1;
+          record_error(a.status, KVC_ERR_TIMEOUT);
+        }
+        phase ^= 1u << st;
+      }
       __syncwarp();  // the stage has landed, and every lane is done with the one before it
       const int nx = t + kQ8Stages - 1;
       if (nx < t1) issue(nx, (st + kQ8Stages - 1) % kQ8Stages);
@@ -343,173 +471,171 @@ k_q8_rows(Q8Args a) {
       const uint32_t kb = ring + st * kQ8Stage;
       if (t < th) {
         const uint32_t vb = kb + kQ8Keys * D;
-        constexpr int N8 = kQ8Keys / 8;
-        float s[MT][N8][4];
+        constexpr int MK = kQ8Keys / 16;  // sixteens of positions
+        float s[MK][NR][4];
 #pragma unroll
-        for (int mt = 0; mt < MT; mt++)
+        for (int i = 0; i < MK; i++)
 #pragma unroll
-          for (int n = 0; n < N8; n++) s[mt][n][0] = s[mt][n][1] = s[mt][n][2] = s[mt][n][3] = 0.f;
-        uint32_t kw[N8][KS];
+          for (int nr = 0; nr < NR; nr++) s[i][nr][0] = s[i][nr][1] = s[i][nr][2] = s[i][nr][3] = 0.f;
 #pragma unroll
-        for (int n = 0; n < N8; n++)
+        for (int hi = 0; hi < KS / 4; hi++) {  // four products from a 16-byte piece of each row
+          uint32_t kw[2 * MK][4];
 #pragma unroll
-          for (int hi = 0; hi < KS / 4; hi++)
-            lds128(kb + swz8<D>(8 * n + lane / 4, 4 * hi + quad), kw[n] + 4 * hi);
+          for (int i = 0; i < 2 * MK; i++) lds128(kb + swz8<D>(8 * i + g8, 4 * hi + quad), kw[i]);
 #pragma unroll
-        for (int ks = 0; ks < KS; ks++) {
-          uint32_t qa[MT][4];
+          for (int k2 = 0; k2 < 2; k2++) {
+            uint32_t qb[NR][4];
 #pragma unroll
-          for (int mt = 0; mt < MT; mt++) {
-            if (MT == 1) {
+            for (int nr = 0; nr < NR; nr++) {
+              if (NR == 1) {
 #pragma unroll
-              for (int e = 0; e < 4; e++) qa[mt][e] = qf[MT == 1 ? ks : 0][e];
-            } else {
-              ldsm4(qhbase + swz<D>(mt * 16 + lane % 16, 2 * ks + lane / 16), qa[mt]);
+                for (int e = 0; e < 4; e++) qb[nr][e] = qf[NR == 1 ? 2 * hi + k2 : 0][e];
+              } else {
+                query8(nr, 4 * hi + 2 * k2, qb[nr]);
+              }
+            }
+#pragma unroll
+            for (int k1 = 0; k1 < 2; k1++) {
+              const int ks = 2 * k2 + k1;
+#pragma unroll
+              for (int i = 0; i < MK; i++) {
+                const uint32_t ka[4] = {e4m3x2_f16x2(kw[2 * i][ks]), e4m3x2_f16x2(kw[2 * i + 1][ks]),
+                                        e4m3x2_f16x2_hi(kw[2 * i][ks]), e4m3x2_f16x2_hi(kw[2 * i + 1][ks])};
+#pragma unroll
+                for (int nr = 0; nr < NR; nr++) mma16816h(s[i][nr], ka, qb[nr][2 * k1], qb[nr][2 * k1 + 1]);
+              }
             }
           }
-#pragma unroll
-          for (int n = 0; n < N8; n++) {
-            const uint32_t b0 = e4m3x2_f16x2(kw[n][ks]), b1 = e4m3x2_f16x2_hi(kw[n][ks]);
-#pragma unroll
-            for (int mt = 0; mt < MT; mt++) mma16816h(s[mt][n], qa[mt], b0, b1);
-          }
         }
-        float kz[2 * N8], lv[2 * N8];  // scale·s_k·log2 e and log2 s_v of this thread's positions
+        float kz[2 * MK], sv[2 * MK];  // scale·s_k·log2 e and s_v of this thread's positions
 #pragma unroll
-        for (int n = 0; n < N8; n++) {
-          const float4 f = *reinterpret_cast<const float4 *>(scale_s + st * kQ8Keys + 8 * n + 2 * quad);
-          kz[2 * n] = f.x * a.zscale;
-          lv[2 * n] = lg2(f.y);
-          kz[2 * n + 1] = f.z * a.zscale;
-          lv[2 * n + 1] = lg2(f.w);
+        for (int i = 0; i < 2 * MK; i++) {
+          const float2 f = scale_s[st * kQ8Keys + 8 * i + g8];
+          kz[i] = f.x * a.zscale;
+          sv[i] = f.y;
         }
+        uint32_t vis[NR][2];
 #pragma unroll
-        for (int mt = 0; mt < MT; mt++)
+        for (int nr = 0; nr < NR; nr++) vis[nr][0] = vis[nr][1] = okb;
+        if (okb == 0xFFFFFFFFu) softmax(std::integral_constant<int, 2 * MK>(), s, kz, sv, true, false, vis);
+        else softmax(std::integral_constant<int, 2 * MK>(), s, kz, sv, true, true, vis);
 #pragma unroll
-          for (int hf = 0; hf < 2; hf++) {
-            const float rs = row_s[mt * 16 + hf * 8 + lane / 4];
-            float mx = m[mt][hf], mv = mo[mt][hf];
+        for (int i = 0; i < MK; i++) {
+          uint32_t pb[NR][2];
 #pragma unroll
-            for (int n = 0; n < N8; n++)
-#pragma unroll
-              for (int e = 0; e < 2; e++) {
-                float z = s[mt][n][hf * 2 + e] * rs * kz[2 * n + e];
-                if (!((okb >> (8 * n + 2 * quad + e)) & 1u)) z = -INFINITY;
-                s[mt][n][hf * 2 + e] = z;
-                mx = fmaxf(mx, z);
-                mv = fmaxf(mv, z + lv[2 * n + e]);
-              }
-            float base, baseo, sum = 0.f;
-            raise(mt, hf, mx, mv, base, baseo);
-#pragma unroll
-            for (int n = 0; n < N8; n++)
-#pragma unroll
-              for (int e = 0; e < 2; e++) {
-                const float z = s[mt][n][hf * 2 + e];
-                sum += ex2(z - base);
-                s[mt][n][hf * 2 + e] = ex2(z + lv[2 * n + e] - baseo);
-              }
-            l[mt][hf] += sum;
+          for (int nr = 0; nr < NR; nr++) {
+            pb[nr][0] = transpose8(pack_f16x2(s[i][nr][0], s[i][nr][1]));
+            pb[nr][1] = transpose8(pack_f16x2(s[i][nr][2], s[i][nr][3]));
           }
 #pragma unroll
-        for (int kk = 0; kk < kQ8Keys / 16; kk++) {
-          uint32_t pa[MT][4];
-#pragma unroll
-          for (int mt = 0; mt < MT; mt++) {
-            pa[mt][0] = pack_f16x2(s[mt][2 * kk][0], s[mt][2 * kk][1]);
-            pa[mt][1] = pack_f16x2(s[mt][2 * kk][2], s[mt][2 * kk][3]);
-            pa[mt][2] = pack_f16x2(s[mt][2 * kk + 1][0], s[mt][2 * kk + 1][1]);
-            pa[mt][3] = pack_f16x2(s[mt][2 * kk + 1][2], s[mt][2 * kk + 1][3]);
-          }
-#pragma unroll
-          for (int cc = 0; cc < CH8; cc += 2) {
-            // two keys by two neighbouring columns a register; after the exchange of the
+          for (int n = 0; n < CH8; n += 2) {
+            // two positions by two neighbouring columns a register; after the exchange of the
             // middle bytes its halves are the operands of the even and of the odd columns
             uint32_t b[4];
-            ldsm4t(vb + swz8<D>(kk * 16 + (lane & 15), cc + (lane >> 4)), b);
+            ldsm4t(vb + swz8<D>(i * 16 + (lane & 15), n + (lane >> 4)), b);
 #pragma unroll
             for (int u = 0; u < 4; u++) b[u] = __byte_perm(b[u], 0, 0x3120);
 #pragma unroll
             for (int u = 0; u < 2; u++) {
-              const uint32_t e0 = e4m3x2_f16x2(b[2 * u]), e1 = e4m3x2_f16x2(b[2 * u + 1]);
-              const uint32_t o0 = e4m3x2_f16x2_hi(b[2 * u]), o1 = e4m3x2_f16x2_hi(b[2 * u + 1]);
+              const uint32_t va[4] = {e4m3x2_f16x2(b[2 * u]), e4m3x2_f16x2_hi(b[2 * u]),
+                                      e4m3x2_f16x2(b[2 * u + 1]), e4m3x2_f16x2_hi(b[2 * u + 1])};
 #pragma unroll
-              for (int mt = 0; mt < MT; mt++) {
-                mma16816h(o[mt][2 * (cc + u)], pa[mt], e0, e1);
-                mma16816h(o[mt][2 * (cc + u) + 1], pa[mt], o0, o1);
-              }
+              for (int nr = 0; nr < NR; nr++) mma16816h(o[n + u][nr], va, pb[nr][0], pb[nr][1]);
             }
           }
         }
       } else {
-        if (hist) {
-          usual();
-          queries(false);
-        }
+        if (hist) usual();
         const uint32_t vb = kb + KT * D * 2;
         const int p0 = (t - th) * a.tile + warp * KT;
-        float s[MT][KT / 8][4];
+        constexpr int MK = KT / 16;
+        float s[MK][NR][4];
 #pragma unroll
-        for (int mt = 0; mt < MT; mt++)
+        for (int i = 0; i < MK; i++)
 #pragma unroll
-          for (int n = 0; n < KT / 8; n++) s[mt][n][0] = s[mt][n][1] = s[mt][n][2] = s[mt][n][3] = 0.f;
+          for (int nr = 0; nr < NR; nr++) s[i][nr][0] = s[i][nr][1] = s[i][nr][2] = s[i][nr][3] = 0.f;
 #pragma unroll
         for (int ks = 0; ks < KS; ks++) {
-          uint32_t qa[MT][4];
+          uint32_t qb[NR][2];
 #pragma unroll
-          for (int mt = 0; mt < MT; mt++) {
-            if (MT == 1) {
+          for (int nr = 0; nr < NR; nr++) query16(nr, ks, qb[nr][0], qb[nr][1]);
 #pragma unroll
-              for (int e = 0; e < 4; e++) qa[mt][e] = qf[MT == 1 ? ks : 0][e];
-            } else {
-              query16(mt, ks, qa[mt]);
-            }
+          for (int i = 0; i < MK; i++) {
+            uint32_t ka[4];
+            ldsm4(kb + swz<D>(i * 16 + (lane & 15), 2 * ks + (lane >> 4)), ka);
+#pragma unroll
+            for (int nr = 0; nr < NR; nr++) mma16816(s[i][nr], ka, qb[nr][0], qb[nr][1]);
           }
+        }
+        uint32_t vis[NR][2];
 #pragma unroll
-          for (int kk = 0; kk < KT / 16; kk++) {
-            uint32_t b[4];
-            ldsm4(kb + swz<D>(kk * 16 + (lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1)), b);
+        for (int nr = 0; nr < NR; nr++)
 #pragma unroll
-            for (int mt = 0; mt < MT; mt++) {
-              mma16816(s[mt][2 * kk], qa[mt], b[0], b[1]);
-              mma16816(s[mt][2 * kk + 1], qa[mt], b[2], b[3]);
+          for (int e = 0; e < 2; e++) {
+            const int x = rt * a.rstep + 8 * nr + 2 * quad + e;
+            vis[nr][e] = x < T * a.G ? visible_bits<KT>(a, x / a.G, q0, c, T, p0) & okb : 0u;
+          }
+        const float one[2 * MK] = {};  // (not read)
+        softmax(std::integral_constant<int, 2 * MK>(), s, one, one, false, true, vis);
+        // A node's V may hold infinities or NaN that some rows do not see, and a product 0·inf
+        // would hand them to those rows.  A tile with such values takes the sum term by term,
+        // over the rows' visible keys only; there such a value is added as it is, for a weight
+        // too small for fp32 is not 0.
+        bool odd = false;
+        if (p0 + KT > c) {
+          for (int e = lane; e < KT * CH; e += 32) {
+            uint32_t w[4];
+            lds128(vb + swz<D>(e / CH, e % CH), w);
+#pragma unroll
+            for (int u = 0; u < 4; u++)
+              odd |= (w[u] & 0x7F80u) == 0x7F80u || (w[u] & 0x7F800000u) == 0x7F800000u;
+          }
+          odd = __any_sync(0xFFFFFFFFu, odd);
+        }
+        if (odd) {
+          auto add = [](float w, float v, float &acc) {
+            acc = fabsf(v) < INFINITY ? fmaf(w, v, acc) : acc + v;
+          };
+#pragma unroll
+          for (int nr = 0; nr < NR; nr++)
+#pragma unroll
+            for (int i = 0; i < 2 * MK; i++)
+#pragma unroll 1
+              for (int k = 0; k < 8; k++) {  // key 8i + k, its weights in the lanes 4k + quad
+                const float w0 = __shfl_sync(0xFFFFFFFFu, s[i / 2][nr][2 * (i & 1)], 4 * k + quad);
+                const float w1 = __shfl_sync(0xFFFFFFFFu, s[i / 2][nr][2 * (i & 1) + 1], 4 * k + quad);
+                const bool s0 = (vis[nr][0] >> (8 * i + k)) & 1u, s1 = (vis[nr][1] >> (8 * i + k)) & 1u;
+#pragma unroll
+                for (int n = 0; n < CH8; n++)
+#pragma unroll
+                  for (int hf = 0; hf < 2; hf++) {
+                    uint16_t v;
+                    asm volatile("ld.shared.u16 %0, [%1];"
+                                 : "=h"(v)
+                                 : "r"(vb + swz<D>(8 * i + k, 2 * n + hf) + 2 * g8));
+                    const float vf = bf16_lo(v);
+                    if (s0) add(w0, vf, o[n][nr][2 * hf]);
+                    if (s1) add(w1, vf, o[n][nr][2 * hf + 1]);
+                  }
+              }
+        } else {
+#pragma unroll
+          for (int i = 0; i < MK; i++) {
+            uint32_t pb[NR][2];
+#pragma unroll
+            for (int nr = 0; nr < NR; nr++) {
+              pb[nr][0] = transpose8(pack_bf16x2(s[i][nr][0], s[i][nr][1]));
+              pb[nr][1] = transpose8(pack_bf16x2(s[i][nr][2], s[i][nr][3]));
+            }
+#pragma unroll
+            for (int n = 0; n < CH8; n++) {
+              uint32_t va[4];
+              ldsm4t(vb + swz<D>(i * 16 + (lane & 7) + ((lane >> 4) << 3), 2 * n + ((lane >> 3) & 1)), va);
+#pragma unroll
+              for (int nr = 0; nr < NR; nr++) mma16816(o[n][nr], va, pb[nr][0], pb[nr][1]);
             }
           }
         }
-        const bool masked = p0 + KT > c || okb != (KT == 32 ? 0xFFFFFFFFu : (1u << (KT & 31)) - 1u);
-#pragma unroll
-        for (int mt = 0; mt < MT; mt++)
-#pragma unroll
-          for (int hf = 0; hf < 2; hf++) {
-            uint32_t vis = 0xFFFFFFFFu;
-            if (masked) {  // warp-uniform
-              const int x = rt * a.rstep + mt * 16 + hf * 8 + lane / 4;
-              vis = x < T * a.G ? visible_bits<KT>(a, x / a.G, q0, c, T, p0) & okb : 0u;
-            }
-            float mx = m[mt][hf], mv = mo[mt][hf];
-#pragma unroll
-            for (int n = 0; n < KT / 8; n++)
-#pragma unroll
-              for (int e = 0; e < 2; e++) {
-                float z = s[mt][n][hf * 2 + e] * a.zscale;
-                if (!((vis >> (n * 8 + 2 * quad + e)) & 1u)) z = -INFINITY;
-                s[mt][n][hf * 2 + e] = z;
-                mx = fmaxf(mx, z);
-                mv = fmaxf(mv, z);
-              }
-            float base, baseo, sum = 0.f;
-            raise(mt, hf, mx, mv, base, baseo);
-#pragma unroll
-            for (int n = 0; n < KT / 8; n++)
-#pragma unroll
-              for (int e = 0; e < 2; e++) {
-                const float z = s[mt][n][hf * 2 + e];
-                sum += ex2(z - base);
-                s[mt][n][hf * 2 + e] = ex2(z - baseo);
-              }
-            l[mt][hf] += sum;
-          }
-        tile_values<D, MT, KT>(a, s, o, vb, okb, rt, q0, c, T, p0);
       }
       st = (st + 1) % kQ8Stages;
     }
@@ -519,20 +645,21 @@ k_q8_rows(Q8Args a) {
 
     float *o_s = reinterpret_cast<float *>(sm) + warp * R * D;
 #pragma unroll
-    for (int mt = 0; mt < MT; mt++)
+    for (int nr = 0; nr < NR; nr++)
 #pragma unroll
-      for (int hf = 0; hf < 2; hf++) {
-        float sum = l[mt][hf];
-        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+      for (int e = 0; e < 2; e++) {
+        float sum = l[nr][e];
+#pragma unroll
+        for (int o2 = 4; o2 < 32; o2 <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o2);
         // O on the sum's reference
-        const float f = m[mt][hf] == -INFINITY || mo[mt][hf] == -INFINITY ? 1.f : ex2(mo[mt][hf] - m[mt][hf]);
-        const int row = mt * 16 + hf * 8 + lane / 4;
-        if (quad == 0) ml_s[warp * R + row] = make_float2(m[mt][hf], sum);
+        const float f = ex2(off[nr][e]);
+        const int row = 8 * nr + 2 * quad + e;
+        if (g8 == 0) ml_s[warp * R + row] = make_float2(ref[nr][e] == kQ8Unset ? -INFINITY : ref[nr][e], sum);
 #pragma unroll
-        for (int n = 0; n < NT; n++)
-          *reinterpret_cast<float2 *>(o_s + row * D + ((n * 8 + 2 * quad) ^ ((row & 3) << 3))) =
-              make_float2(o[mt][n][hf * 2] * f, o[mt][n][hf * 2 + 1] * f);
+        for (int n = 0; n < CH8; n++)
+#pragma unroll
+          for (int hf = 0; hf < 2; hf++)
+            o_s[row * D + ((16 * n + 8 * hf + g8) ^ (quad << 3))] = o[n][nr][2 * hf + e] * f;
       }
     __syncthreads();
     const bool whole = t0 == 0 && t1 == n_kt;
@@ -553,7 +680,7 @@ k_q8_rows(Q8Args a) {
         const float f = ex2(ml.x - base);
         sum = fmaf(ml.y, f, sum);
         const float4 v = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(sm) +
-                                                           (w * R + row) * D + (d4 ^ ((row & 3) << 3)));
+                                                           (w * R + row) * D + (d4 ^ (((row >> 1) & 3) << 3)));
         acc.x = fmaf(v.x, f, acc.x);
         acc.y = fmaf(v.y, f, acc.y);
         acc.z = fmaf(v.z, f, acc.z);
@@ -582,16 +709,22 @@ k_q8_rows(Q8Args a) {
         } while (n_rt == 0);  // g < run1 ≤ total: a later request holds tile g
         q8_request(a, r, n8, c, q0, T);
       }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (O's place is the ring again)
       __syncthreads();
     }
   }
+  if (*failed)  // this warp's copies finish before its memory is released
+    for (int i = 0; i < kQ8Stages; i++) {
+      mbar_drain(full + 8 * i, 0);
+      mbar_drain(full + 8 * i, 1);
+    }
 }
 
 // Rows per tile and grid of a call.
 void q8_plan(int n_req, int max_blocks8, int max_blocks, int max_tree, int H, int Hq, int D, int BS,
              int &rows, int &tile, int &n_cta, int &max_rt) {
   const int64_t R = (int64_t)max_tree * (Hq / H);
-  rows = R <= 16 ? 16 : 32;
+  rows = (int)std::min<int64_t>((R + 7) / 8 * 8, 32);
   tile = kQ8Warps * (2048 / D);
   max_rt = (int)((R + rows - 1) / rows);
   const int64_t kt = ((int64_t)max_blocks8 * BS + kQ8Warps * kQ8Keys - 1) / (kQ8Warps * kQ8Keys) +
@@ -599,13 +732,37 @@ void q8_plan(int n_req, int max_blocks8, int max_blocks, int max_tree, int H, in
   n_cta = (int)std::min<int64_t>(2 * device_sm_count(), (int64_t)n_req * H * max_rt * kt);
 }
 
-template <int D, int MT>
-cudaError_t launch_q8_rows(const Q8Args &a, cudaStream_t s) {
-  constexpr int smem = Q8Smem<D, MT>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(k_q8_rows<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+// Boxes of `box` rows of a head's block, D bytes, swizzled as swz8 says.
+bool rows8_map(CUtensorMap *m, const void *pool, int64_t rows, int D, int box) {
+  auto fn = tc::encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)D};
+  cuuint32_t bx[2] = {(cuuint32_t)D, (cuuint32_t)box}, es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(pool), dims, strides, bx, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int NR>
+cudaError_t launch_q8_rows(const Q8Args &a, const CUtensorMap &tm_k, const CUtensorMap &tm_v, cudaStream_t s) {
+  constexpr int smem = Q8Smem<D, NR>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(k_q8_rows<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  k_q8_rows<D, MT><<<a.n_cta, kQ8Threads, smem, s>>>(a);
+  k_q8_rows<D, NR><<<a.n_cta, kQ8Threads, smem, s>>>(tm_k, tm_v, a);
   return cudaGetLastError();
+}
+template <int D>
+cudaError_t launch_q8(const Q8Args &a, cudaStream_t s) {
+  CUtensorMap tm_k{}, tm_v{};
+  const int64_t rows = a.n_blocks8 * a.H * a.BS;
+  if (a.box8 && !(rows8_map(&tm_k, a.k8, rows, D, a.box8) && rows8_map(&tm_v, a.v8, rows, D, a.box8)))
+    return cudaErrorUnknown;
+  switch (a.rows / 8) {
+    case 1: return launch_q8_rows<D, 1>(a, tm_k, tm_v, s);
+    case 2: return launch_q8_rows<D, 2>(a, tm_k, tm_v, s);
+    case 3: return launch_q8_rows<D, 3>(a, tm_k, tm_v, s);
+    default: return launch_q8_rows<D, 4>(a, tm_k, tm_v, s);
+  }
 }
 
 }  // namespace
@@ -639,8 +796,9 @@ cudaError_t launch_q8_attn(const uint16_t *q, const uint8_t *k8, const uint8_t *
   a.rstep = a.rows;
   a.part_o = reinterpret_cast<float *>(ws);
   a.part_ml = reinterpret_cast<float2 *>(a.part_o + (size_t)2 * a.n_cta * a.rows * D);
-  const cudaError_t e = D == 128 ? (a.rows == 16 ? launch_q8_rows<128, 1>(a, s) : launch_q8_rows<128, 2>(a, s))
-                                 : (a.rows == 16 ? launch_q8_rows<64, 1>(a, s) : launch_q8_rows<64, 2>(a, s));
+  // (a box's rows lie in one block, and a row's number fits the box's coordinate)
+  a.box8 = n_blocks8 * H * BS > INT32_MAX ? 0 : BS % 32 == 0 ? 32 : BS % 16 == 0 ? 16 : BS % 8 == 0 ? 8 : 0;
+  const cudaError_t e = D == 128 ? launch_q8<128>(a, s) : launch_q8<64>(a, s);
   if (e != cudaSuccess) return e;
   return launch_join(a, D, max_rt, s);
 }
