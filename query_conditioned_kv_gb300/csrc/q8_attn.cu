@@ -40,7 +40,9 @@ namespace {
 
 constexpr int kQ8Warps = 4;
 constexpr int kQ8Threads = kQ8Warps * 32;
-constexpr int kQ8Stages = 3;
+// CTAs per SM and stages of a warp's ring, by the row tile's eights of rows.
+constexpr int q8_ctas(int nr) { return nr <= 2 ? 3 : 2; }
+constexpr int q8_stages(int nr) { return nr <= 2 ? 2 : 3; }
 constexpr int kQ8Stage = 8192;  // bytes of one warp's stage: K rows, then V rows
 constexpr int kQ8Keys = 32;     // positions of a warp's stage of the history
 constexpr float kQ8Unset = -FLT_MAX;   // reference of a row that has seen nothing
@@ -76,7 +78,7 @@ __device__ __forceinline__ void tree_tiles(const Q8Args &a, int r, int &n_rt, in
 
 template <int D, int NR>
 struct Q8Smem {
-  static constexpr int R = 8 * NR;
+  static constexpr int R = 8 * NR, kQ8Stages = q8_stages(NR);
   static constexpr int kRing = kQ8Warps * kQ8Stages * kQ8Stage;
   static constexpr int kQh = kRing;              // the rows of q in fp16, in the products' order
   static constexpr int kScale = kQh + R * D * 2; // (s_k, s_v) of a stage's positions
@@ -85,7 +87,7 @@ struct Q8Smem {
   static constexpr int kMl = kValid + (kQ8Warps * kQ8Stages * 4 + 15) / 16 * 16;  // (reference, sum) per (warp, row)
   static constexpr int kFull = kMl + kQ8Warps * R * 8;  // barriers per (warp, stage), then a word
   static constexpr int kBytes = kFull + kQ8Warps * kQ8Stages * 8 + 16;
-  static_assert(2 * (kBytes + 1024) <= 228 * 1024, "two CTAs fit an SM");
+  static_assert(q8_ctas(NR) * (kBytes + 1024) <= 228 * 1024, "the CTAs fit an SM");
   static_assert(kQ8Warps * R * D * 4 <= kRing, "the warps' O fit the ring");
   static_assert(2 * kQ8Keys * D <= kQ8Stage, "a stage of the history fits");
 };
@@ -152,11 +154,11 @@ __device__ __forceinline__ float lg2(float x) {
 }
 
 template <int D, int NR>
-__global__ void __launch_bounds__(kQ8Threads, 2)
+__global__ void __launch_bounds__(kQ8Threads, q8_ctas(NR))
 k_q8_rows(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, Q8Args a) {
   using S = Q8Smem<D, NR>;
   constexpr int KT = 2048 / D, KS = D / 16, CH = D / 8, CH8 = D / 16;
-  constexpr int R = 8 * NR;
+  constexpr int R = 8 * NR, kQ8Stages = S::kQ8Stages;
   extern __shared__ __align__(1024) uint8_t sm[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = lane & 3, g8 = lane >> 2;
   const uint32_t ring = smem_u32(sm) + warp * kQ8Stages * kQ8Stage;
@@ -729,7 +731,7 @@ void q8_plan(int n_req, int max_blocks8, int max_blocks, int max_tree, int H, in
   max_rt = (int)((R + rows - 1) / rows);
   const int64_t kt = ((int64_t)max_blocks8 * BS + kQ8Warps * kQ8Keys - 1) / (kQ8Warps * kQ8Keys) +
                      ((int64_t)max_blocks * BS + tile - 1) / tile;
-  n_cta = (int)std::min<int64_t>(2 * device_sm_count(), (int64_t)n_req * H * max_rt * kt);
+  n_cta = (int)std::min<int64_t>(q8_ctas(rows / 8) * device_sm_count(), (int64_t)n_req * H * max_rt * kt);
 }
 
 // Boxes of `box` rows of a head's block, D bytes, swizzled as swz8 says.
