@@ -53,6 +53,7 @@ struct PromptTc {
   int gc, n_ch;         // heads of a row tile's piece of the group, pieces
   int tpt;              // tokens of a row tile
   int NS;               // ring slots
+  int wide;             // out is aligned to 32 bytes
   uint32_t idesc_s, idesc_o;
 };
 
@@ -112,6 +113,12 @@ __device__ __forceinline__ void tmem_put32(uint32_t taddr, const uint32_t *r) {
       "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+// 32 bytes, a whole sector (dst aligned to 32 bytes).
+__device__ __forceinline__ void st_global32(void *dst, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]),
+               "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_put_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -123,7 +130,9 @@ __device__ __forceinline__ int prompt_pairs(const TreeArgs &a, const PromptTc &p
   return ((T + p.tpt - 1) / p.tpt * p.n_ch + 1) / 2;
 }
 
-template <int D>
+// CL: a cluster shares a unit, each CTA a part of its keys, and joins the parts from one
+// another's shared memory.
+template <int D, bool CL>
 __global__ void __launch_bounds__(kPaThreads, 1)
 k_prompt_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
             const __grid_constant__ CUtensorMap tm_q, TreeArgs a, PromptTc p) {
@@ -144,12 +153,14 @@ k_prompt_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
   // this CTA's unit: requests in order, a request's last rows first (they see the most)
   auto units = [&](int r) { return (int64_t)a.H * prompt_pairs(a, p, r); };
   const WarpSums sums = warp_sums(a.n_req, units);
-  if ((int64_t)blockIdx.x >= sums.total) return;
+  const int S = CL ? (int)cluster_nrank() : 1, rank = CL ? (int)cluster_rank() : 0;
+  const int64_t unit = CL ? blockIdx.x / S : blockIdx.x;
+  if (unit >= sums.total) return;  // (the whole cluster)
   int r, c, q0, T;
   int64_t before;
-  warp_find(sums, a.n_req, (int64_t)blockIdx.x, units, r, before);
+  warp_find(sums, a.n_req, unit, units, r, before);
   tree_request(a, r, c, q0, T);
-  const int at = (int)((int64_t)blockIdx.x - before), h = at % a.H;
+  const int at = (int)(unit - before), h = at % a.H;
   const int pair = prompt_pairs(a, p, r) - 1 - at / a.H;
   // row tile x of the pair: pieces of the group inside, tokens outside
   const int n_tiles = (T + p.tpt - 1) / p.tpt * p.n_ch;
@@ -158,9 +169,11 @@ k_prompt_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
   auto tiles_of = [&](int x) {  // key tiles that some row of row tile x sees
     return 2 * pair + x < n_tiles ? (c + min(T, token_of(x) + p.tpt) + kPaKeys - 1) / kPaKeys : 0;
   };
-  const int nA = tiles_of(0), nB = tiles_of(1), nT = max(nA, nB);
   const int tok0 = token_of(0);
-  const int end = c + min(T, token_of(nB ? 1 : 0) + p.tpt);  // positions some row sees
+  const int end = c + min(T, token_of(tiles_of(1) ? 1 : 0) + p.tpt);  // positions some row sees
+  // this CTA's key tiles: from t0 on, nA of them for row tile A and nB for B
+  const int all = max(tiles_of(0), tiles_of(1)), t0 = all * rank / S, t1 = all * (rank + 1) / S;
+  const int nA = max(min(tiles_of(0), t1) - t0, 0), nB = max(min(tiles_of(1), t1) - t0, 0), nT = max(nA, nB);
 
   if (tid == 0) {
     sm.failed = sm.odd = sm.bad = 0;
@@ -191,10 +204,11 @@ k_prompt_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     const int32_t *bt = a.block_table + (int64_t)r * a.max_blocks;
     constexpr int RPI = 32 / CH;
     const int col = lane % CH;
-    if (warp == 8 && lane == 0) {
+    if (warp == 8 && lane == 0 && nT > 0) {
       const uint32_t bar = smem_u32(&sm.qfull);
-      mbar_expect_tx(bar, (nB ? 2 : 1) * p.tpt * p.gc * D * 2);
-      for (int x = 0; x < (nB ? 2 : 1); x++)
+      const int n = 2 * pair + 1 < n_tiles ? 2 : 1;
+      mbar_expect_tx(bar, n * p.tpt * p.gc * D * 2);
+      for (int x = 0; x < n; x++)
 #pragma unroll
         for (int kb = 0; kb < KB; kb++)
           tma_load_3d(q_u + x * kQTile + kb * (128 * 128), &tm_q, kb * 64,
@@ -217,7 +231,7 @@ k_prompt_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     };
     int32_t blk, slot = -1;  // block id of the next tile's key, slot of this tile's
     auto fetch = [&](int t) {
-      const int pp = t * kPaKeys + key0 + lane;
+      const int pp = (t0 + t) * kPaKeys + key0 + lane;
       blk = pp < end && t < nT ? bt[page_of(pp, a.bs_inv)] : 0;
     };
     fetch(0);
@@ -225,7 +239,7 @@ k_prompt_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     for (int i = 0; i < 2 * nT && ok; i++) {
       const int t = i >> 1;
       const bool is_v = i & 1;
-      const int pp = t * kPaKeys + key0 + lane;
+      const int pp = (t0 + t) * kPaKeys + key0 + lane;
       if (!is_v) {
         slot = -1;
         if (pp < end) {
@@ -249,7 +263,7 @@ k_prompt_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
       const uint32_t bar = smem_u32(sm.full + st);
       if (++st == (uint32_t)p.NS) st = 0, round++;
       // values past the first row's own position are looked at (below): not by TMA
-      const bool hidden = is_v && (t + 1) * kPaKeys > c + tok0 + 1;
+      const bool hidden = is_v && (t0 + t + 1) * kPaKeys > c + tok0 + 1;
       if (p.box > 0 && !hidden && __all_sync(0xFFFFFFFFu, slot >= 0)) {
         if (lane == 0) mbar_expect_tx(bar, kSlot / 4);
         __syncwarp();
@@ -307,7 +321,7 @@ k_prompt_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
           if ((w[u] & 0x7F800000u) == 0x7F800000u) mine = true, w[u] &= 0xFFFFu;
         }
         // (what every row of the pair sees stays)
-        if (mine && t * kPaKeys + key0 + row > c + tok0) {
+        if (mine && (t0 + t) * kPaKeys + key0 + row > c + tok0) {
           odd = true;
           asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(ad), "r"(w[0]), "r"(w[1]),
                        "r"(w[2]), "r"(w[3])
@@ -350,11 +364,11 @@ k_prompt_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         if (elect_one()) mma_commit(bar);
         __syncwarp();
       };
-      ok = mbar_wait_bounded(smem_u32(&sm.qfull), 0, &sm.failed);
-      if (ok) stage(ks);
-      if (ok) {
+      if (nT > 0) ok = mbar_wait_bounded(smem_u32(&sm.qfull), 0, &sm.failed);
+      if (ok && nT > 0) stage(ks);
+      if (ok && nT > 0) {
         tc_fence_after();
-        product_s(0);
+        if (nA) product_s(0);
         if (nB) product_s(1);
         done(smem_u32(sm.empty + ks));
       }
@@ -401,7 +415,7 @@ k_prompt_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     const uint32_t ts = tmem + x * 128 + lanes, to = tmem + 256 + x * 128 + lanes;
     const int n = x ? nB : nA;
     const int tx = token_of(x), token = tx + row / p.gc, head = piece_of(x) * p.gc + row % p.gc;
-    const bool active = n > 0 && row < p.tpt * p.gc && token < T && head < a.G;
+    const bool active = 2 * pair + x < n_tiles && row < p.tpt * p.gc && token < T && head < a.G;
     const int32_t *bt = a.block_table + (int64_t)r * a.max_blocks;
     const int64_t n_blocks = a.n_slots / a.BS;
     const float zs = a.zscale, hidden = zs < 0.f ? INFINITY : -INFINITY;  // −inf once scaled
@@ -412,13 +426,13 @@ k_prompt_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
       if (!ok) break;
       tc_fence_after();
       // which keys this row sees, where it is not all of them
-      const bool masked = (t + 1) * kPaKeys > c + tx + 1 || sm.bad;
+      const bool masked = (t0 + t + 1) * kPaKeys > c + tx + 1 || sm.bad;
       uint32_t see[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
       if (masked) {
-        const int lim = c + token + 1 - t * kPaKeys;
+        const int lim = c + token + 1 - (t0 + t) * kPaKeys;
 #pragma unroll
         for (int w = 0; w < 4; w++) {
-          const int pp = t * kPaKeys + 32 * w + lane;
+          const int pp = (t0 + t) * kPaKeys + 32 * w + lane;
           bool valid = pp < end;
           if (valid) {
             const int32_t b = bt[page_of(pp, a.bs_inv)];
@@ -526,21 +540,30 @@ k_prompt_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
       ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(sm.pvdone + x), (n - 1) & 1, &sm.failed));
       tc_fence_after();
     }
-    if (ok && n > 0) {
-      const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (CL) named_sync(1, 256);  // both row tiles' products are done: the ring takes O
+    if (ok && (CL || n > 0)) {
+      const float inv = CL ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      const bool none = n == 0 || l == 0.f;
       const int64_t qr = (int64_t)(q0 + token) * a.Hq + h * a.G + head;
       const bool odd = sm.odd != 0;
+      float4 *part = reinterpret_cast<float4 *>(base + (ring_u - smem_u32(base))) + (x * 128 + row) * (D / 4);
 #pragma unroll 1
       for (int cc = 0; cc < D; cc += 32) {
-        uint32_t z[32];
         float v[32];
-        tmem_issue32(to + cc, z);
-        tmem_wait32(z);
+        if (CL && n == 0) {
 #pragma unroll
-        for (int e = 0; e < 32; e++) v[e] = l == 0.f ? 0.f : __uint_as_float(z[e]) * inv;
-        if (odd && active) {  // infinities and NaN of later tokens that the row sees
+          for (int e = 0; e < 32; e++) v[e] = 0.f;
+        } else {
+          uint32_t z[32];
+          tmem_issue32(to + cc, z);
+          tmem_wait32(z);
+#pragma unroll
+          for (int e = 0; e < 32; e++) v[e] = none ? 0.f : __uint_as_float(z[e]) * inv;
+        }
+        if (odd && active) {  // infinities and NaN of later tokens, among this CTA's keys, that the row sees
+          const int last = min(c + token, (t0 + nT) * kPaKeys - 1);
 #pragma unroll 1
-          for (int pn = c + tok0 + 1; pn <= c + token; pn++) {
+          for (int pn = max(c + tok0 + 1, t0 * kPaKeys); pn <= last; pn++) {
             const int pg = page_of(pn, a.bs_inv);
             const int32_t b = bt[pg];
             if (b < 0 || b >= n_blocks) continue;
@@ -552,15 +575,30 @@ k_prompt_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             }
           }
         }
-        if (active) {
-          uint4 *dst = reinterpret_cast<uint4 *>(a.out + qr * D + cc);
+        if (CL) {
+          // (16-byte pieces, turned by the row so that a warp's rows lie in distinct banks)
 #pragma unroll
-          for (int e = 0; e < 4; e++)
-            dst[e] = make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]), pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
-                                pack_bf16x2(v[8 * e + 4], v[8 * e + 5]), pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
+          for (int e = 0; e < 8; e++)
+            part[(cc / 4 + e) ^ (row & 7)] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+        } else if (active) {
+          uint16_t *dst = a.out + qr * D + cc;
+#pragma unroll
+          for (int e = 0; e < 2; e++) {
+            uint32_t w[8];
+#pragma unroll
+            for (int k = 0; k < 8; k++) w[k] = pack_bf16x2(v[16 * e + 2 * k], v[16 * e + 2 * k + 1]);
+            if (p.wide) {
+              st_global32(dst + 16 * e, w);
+            } else {
+              *reinterpret_cast<uint4 *>(dst + 16 * e) = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4 *>(dst + 16 * e + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+          }
         }
       }
-      if (active) a.lse[qr] = l == 0.f ? -INFINITY : (log2f(l) - nref) * kLn2;
+      // (per row of the part, the reference and the sum, in Q's place)
+      if (CL) reinterpret_cast<float2 *>(base + kPaHead)[x * 128 + row] = make_float2(none ? -INFINITY : -nref, none ? 0.f : l);
+      else if (active) a.lse[qr] = l == 0.f ? -INFINITY : (log2f(l) - nref) * kLn2;
     }
     if (!ok) {
       sm.failed = 1;
@@ -568,6 +606,39 @@ k_prompt_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     }
   }
 
+  if constexpr (CL) {
+    // The unit's parts are in the cluster's CTAs: added up in order, the rows dealt out to all.
+    __syncwarp();
+    cluster_sync_all();
+    const uint32_t ml_at = q_u;
+    for (int e = rank * kPaThreads + tid; e < 256 * (D / 4); e += S * kPaThreads) {
+      const int xr = e / (D / 4), d4 = e % (D / 4), x = xr >> 7, row = xr & 127;
+      const int token = token_of(x) + row / p.gc, head = piece_of(x) * p.gc + row % p.gc;
+      if (2 * pair + x >= n_tiles || row >= p.tpt * p.gc || token >= T || head >= a.G) continue;
+      float mx = -INFINITY;
+      for (int k = 0; k < S; k++) mx = fmaxf(mx, ld_cluster_f2(mapa_u32(ml_at + xr * 8, k)).x);
+      float sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < S; k++) {
+        const float2 ml = ld_cluster_f2(mapa_u32(ml_at + xr * 8, k));
+        // (a part that saw nothing of the row may still hold what is not finite)
+        const float4 v = ld_cluster_f4(mapa_u32(ring_u + (xr * (D / 4) + (d4 ^ (row & 7))) * 16, k));
+        const float f = ml.x == -INFINITY ? 1.f : ex2(ml.x - mx);
+        sum = fmaf(ml.y, ml.x == -INFINITY ? 0.f : f, sum);
+        acc.x = fmaf(v.x, f, acc.x);
+        acc.y = fmaf(v.y, f, acc.y);
+        acc.z = fmaf(v.z, f, acc.z);
+        acc.w = fmaf(v.w, f, acc.w);
+      }
+      const int64_t qr = (int64_t)(q0 + token) * a.Hq + h * a.G + head;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      *reinterpret_cast<uint2 *>(a.out + qr * D + 4 * d4) =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+      if (d4 == 0) a.lse[qr] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+    }
+    __syncwarp();
+    cluster_sync_all();  // (no CTA leaves while another reads its part)
+  }
   // -------------------------------------------------------- teardown
   tc_fence_before();
   __syncthreads();
@@ -607,16 +678,37 @@ bool rows_map(CUtensorMap *m, const void *pool, int64_t n_slots, int H, int D, i
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// CTAs that share a unit (1, 2, 4 or 8), in key tiles that a CTA takes one after another:
+// waves of CTAs, each with its share of a unit's keys, a beginning and an end worth about
+// four tiles, and the join's two.  An SM holds one CTA, and clusters of 4 and 8 leave
+// some SMs of a GPC empty.
+int prompt_cluster(int64_t units, int64_t kt) {
+  const double sms = device_sm_count();
+  int best = 1;
+  double least = 0;
+  for (int S = 1; S <= 8 && S <= kt; S *= 2) {
+    const double room = S == 8 ? 0.84 * sms : S == 4 ? 0.94 * sms : sms;
+    const double cost = ceil(units * S / room) * (ceil((double)kt / S) + (S > 1 ? 6 : 4));
+    if (S == 1 || cost < least) {
+      least = cost;
+      best = S;
+    }
+  }
+  return best;
+}
+
 template <int D>
 cudaError_t launch_prompt_tc(const TreeArgs &a, int max_rows, cudaStream_t s) {
   constexpr size_t kSmemMax = 232448;
   constexpr size_t kSlot = kPaKeys * D * 2, kFixed = 1024 + kPaHead + 2 * 128 * D * 2;
+  static_assert(kFixed + 4 * kSlot <= kSmemMax && 4 * kSlot >= 256 * D * 4, "the parts' O fit the ring");
   PromptTc p{};
   p.n_ch = (a.G + 127) / 128;
   p.gc = (a.G + p.n_ch - 1) / p.n_ch;
   p.tpt = 128 / p.gc;
   p.NS = (int)std::min<size_t>(kPaSlots, (kSmemMax - kFixed) / kSlot);
   p.box = a.BS % 32 == 0 ? 32 : a.BS % 16 == 0 ? 16 : a.BS % 8 == 0 ? 8 : 0;
+  p.wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
   p.idesc_s = make_idesc(128, kPaKeys);
   p.idesc_o = make_idesc(128, D) | (1u << 16);  // B (V) MN-major
   CUtensorMap tm_k{}, tm_v{}, tm_q{};
@@ -624,27 +716,40 @@ cudaError_t launch_prompt_tc(const TreeArgs &a, int max_rows, cudaStream_t s) {
                  rows_map(&tm_v, a.vpool, a.n_slots, a.H, D, p.box)))
     return cudaErrorUnknown;
   if (!q_map(&tm_q, a.q, a.n_q, a.Hq, D, p.gc, p.tpt)) return cudaErrorUnknown;
+  // units at most: every request's last pair may be part empty
+  const int64_t each = ((int64_t)(max_rows + p.tpt - 1) / p.tpt * p.n_ch + 1) / 2;
+  const int64_t rows = std::min<int64_t>(a.n_q, (int64_t)a.n_req * max_rows);
+  const int64_t pairs = std::min<int64_t>(a.n_req * each, rows * p.n_ch / (2 * p.tpt) + 2 * (int64_t)a.n_req);
+  const int64_t units = pairs * a.H;
+  const int S = prompt_cluster(units, ((int64_t)a.max_blocks * a.BS + kPaKeys - 1) / kPaKeys);
+  if (units * S > INT32_MAX) return cudaErrorInvalidConfiguration;
+  auto *kern = S > 1 ? k_prompt_tc<D, true> : k_prompt_tc<D, false>;
   // (the limit is the process's: the largest, so that no thread's call lowers it under
   // another's launch)
-  cudaError_t e = cudaFuncSetAttribute(k_prompt_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)kSmemMax);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
   if (e != cudaSuccess) return e;
-  static std::atomic<int> regs{0};  // a thread's registers at launch
+  static std::atomic<int> known[2];  // a thread's registers at launch
+  std::atomic<int> &regs = known[S > 1];
   if (!regs.load(std::memory_order_relaxed)) {
     cudaFuncAttributes fa{};
-    if ((e = cudaFuncGetAttributes(&fa, k_prompt_tc<D>)) != cudaSuccess) return e;
+    if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
     regs.store(fa.numRegs, std::memory_order_relaxed);
   }
   // setmaxnreg.inc draws on what the block was launched with
   if (regs.load(std::memory_order_relaxed) * kPaThreads < 256 * (kPaMore + kPaLess))
     return cudaErrorLaunchOutOfResources;
-  // units at most: every request's last pair may be part empty
-  const int64_t each = ((int64_t)(max_rows + p.tpt - 1) / p.tpt * p.n_ch + 1) / 2;
-  const int64_t rows = std::min<int64_t>(a.n_q, (int64_t)a.n_req * max_rows);
-  const int64_t pairs = std::min<int64_t>(a.n_req * each, rows * p.n_ch / (2 * p.tpt) + 2 * (int64_t)a.n_req);
-  if (pairs * a.H > INT32_MAX) return cudaErrorInvalidConfiguration;
-  k_prompt_tc<D><<<(unsigned)(pairs * a.H), kPaThreads, kFixed + p.NS * kSlot, s>>>(tm_k, tm_v, tm_q, a, p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(units * S));
+  cfg.blockDim = dim3(kPaThreads);
+  cfg.dynamicSmemBytes = kFixed + p.NS * kSlot;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)S;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = S > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, tm_k, tm_v, tm_q, a, p);
 }
 
 }  // namespace

@@ -58,14 +58,15 @@ def status(kvc, t):
 
 
 class Batch:
-    """Requests with ctx cached rows and T new ones, over a paged pool, on the host."""
+    """Requests with ctx cached rows and T new ones, over a paged pool, on the host.  `room`: pages of
+    a request's table past what it needs."""
 
-    def __init__(self, seed, ctx, T, H, G, D, BS, pad=0, kscale=1.0, poison=True):
+    def __init__(self, seed, ctx, T, H, G, D, BS, pad=0, kscale=1.0, poison=True, room=0):
         self.rng = np.random.default_rng(seed)
         self.ctx, self.T, self.H, self.G, self.D, self.BS = list(ctx), list(T), H, G, D, BS
         self.n_req, self.Hq = len(ctx), H * G
         self.max_rows = max(max(T), 1)
-        self.max_blocks = max(1, max(-(-(c + t) // BS) for c, t in zip(ctx, T)))
+        self.max_blocks = max(1, max(-(-(c + t) // BS) for c, t in zip(ctx, T))) + room
         self.bt, n_blocks = table(self.rng, self.n_req, self.max_blocks)
         self.n_slots = n_blocks * BS
         self.q_off = np.concatenate([[0], np.cumsum(T)])
@@ -362,6 +363,23 @@ def test_prompt_long(kvc, T, ctx, H, G, D):
     go(kvc, Prompt(T, [ctx], [T], H, G, D, 16))
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T,ctx", [([5], [700]), ([130, 3], [300, 1900]), ([40, 0, 64, 1], [0, 900, 127, 2049]),
+                                   ([65, 200], [1000, 0])])
+@pytest.mark.parametrize("G", [1, 4, 5])
+def test_prompt_few_rows_behind_long_caches(kvc, D, T, ctx, G):
+    """Few units, whose keys a cluster's CTAs share; some parts hold no key that a row sees."""
+    go(kvc, Prompt(D + G + T[0], ctx, T, 2, G, D, 16, pad=1))
+
+
+@pytest.mark.parametrize("room", [1, 6, 40, 200])
+def test_prompt_room_in_the_table(kvc, room):
+    """Tables longer than the requests: clusters of every size over few keys, most parts empty."""
+    for D, G, BS in ((128, 4, 16), (64, 2, 5)):
+        t = Prompt(room, [0, 31], [70, 140], 1, G, D, BS, room=room * 16 // BS, pad=1)
+        go(kvc, t)
+
+
 def test_prompt_equals_chain_rows(kvc):
     """The rows of a whole prompt are those of its pieces (within both bounds)."""
     t = Prompt(31, [0], [400], 2, 4, 128, 16).gpu()
@@ -381,8 +399,8 @@ def test_prompt_equals_chain_rows(kvc):
 @pytest.mark.parametrize("kscale", [0.0, 1e-20, 30.0, 3000.0, 1e18])
 def test_prompt_logit_ranges(kvc, kscale):
     """Flat, peaked and huge logits, whose maxima move from tile to tile."""
-    t = Prompt(41, [3, 0], [333, 290], 2, 2, 128, 16, kscale=kscale)
-    go(kvc, t)
+    for room in (0, 100):
+        go(kvc, Prompt(41, [3, 0], [333, 290], 2, 2, 128, 16, kscale=kscale, room=room))
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.3, 2.0 ** -100])
@@ -406,8 +424,8 @@ def test_prompt_rising_maxima(kvc):
 
 def test_prompt_values_not_seen_never_reach_a_row(kvc):
     """Infinite and NaN keys and values of later tokens reach exactly the rows that see them."""
-    for D, G in ((128, 4), (64, 1), (128, 3)):
-        t = Prompt(53 + D, [10, 0], [200, 150], 2, G, D, 16)
+    for D, G, room in ((128, 4, 0), (64, 1, 0), (128, 3, 0), (128, 4, 60), (64, 2, 200)):
+        t = Prompt(53 + D, [10, 0], [200, 150], 2, G, D, 16, room=room)
         for r, at, val in ((0, 90, NAN), (0, 150, INF), (1, 40, -INF), (1, 149, NAN)):
             s = tree_ref.slots(t.bt[r], 16, t.ctx[r] + t.T[r])
             t.v[s[t.ctx[r] + at], 1, 5] = val
@@ -434,8 +452,8 @@ def test_prompt_values_not_seen_never_reach_a_row(kvc):
 
 
 def test_prompt_bad_pages(kvc):
-    for BS in (16, 5):
-        t = Prompt(59, [40, 0, 16], [100, 64, 1], 2, 2, 128, BS)
+    for BS, room in ((16, 0), (5, 0), (16, 100)):
+        t = Prompt(59, [40, 0, 16], [100, 64, 1], 2, 2, 128, BS, room=room)
         t.bt[0, 1], t.bt[1, 0], t.bt[1, 2] = t.n_slots // BS, -1, 1 << 30
         go(kvc, t, BOUNDS, bad_blocks={t.n_slots // BS, -1, 1 << 30})
     t = Prompt(61, [0], [30], 1, 2, 64, 16)     # nothing to see at all
