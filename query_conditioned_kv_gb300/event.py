@@ -9,6 +9,10 @@
 ``TreeDecodeEvent`` a decoding step with drafted trees on a paged cache: tree
                  attention per layer → commit of the accepted path →
                  accumulated weight → eviction to a budget
+``HistoryEvent`` prompts and decoding on a paged cache whose older blocks are
+                 held in 8 bits: norms, rotation and storing per layer →
+                 attention over the prompt, or over history and cache → full
+                 blocks packed to 8 bits
 
 All only allocate caller-side buffers with torch and call the library's
 entry points; an event can be captured in a CUDA graph (``capture()``) so
@@ -36,6 +40,8 @@ from . import (BLOCK_TOKENS, kvc_pack_rerope, kvc_pack_tiered, kvc_pack_tiered_s
                kvc_redirect_free_workspace_size, kvc_rope_table, kvc_score,
                kvc_lrfu_update, kvc_score_qmem, kvc_score_qmem_workspace_size,
                kvc_score_workspace_size, kvc_select, kvc_tail_compact, kvc_tail_plan,
+               TREE_MAX_NODES, kvc_prompt_attn, kvc_q8_attn, kvc_q8_attn_workspace_size,
+               kvc_q8_pack, kvc_qkv_rope,
                kvc_attn_mass, kvc_attn_mass_workspace_size, kvc_mass_evict,
                kvc_mass_evict_workspace_size, kvc_tree_attn, kvc_tree_attn_workspace_size,
                kvc_tree_commit)
@@ -634,6 +640,131 @@ class TreeDecodeEvent:
         with _on(stream, self.device):
             for n in (self.ctx, self.n_mass, self.n_pos):
                 n.copy_(self.n_out)
+
+
+
+class HistoryEvent:
+    """Buffers and calls of prompts and decoding on a paged KV cache whose older blocks
+    are held in 8 bits.
+
+    A step, of prompts or of few rows per request: per layer ``write`` (the new tokens'
+    queries and keys are normed and rotated, keys and values stored behind the cache;
+    kvc_qkv_rope), then ``prompt`` (kvc_prompt_attn: many rows, requests without a history)
+    or ``attend`` (kvc_q8_attn: few rows, or a drafted tree, over history and cache);
+    after the last layer ``finish``, which takes the rows into the cache and moves every
+    full block that is older than the last `recent` rows to 8 bits (kvc_q8_pack).
+
+    Per request, on the device: ``ctx`` rows in bf16, ``len8`` positions in 8 bits,
+    ``t_end`` tokens seen (the rotation goes by it).  The caller owns the pools, the
+    8-bit pools (``k8``, ``v8`` [L][n_blocks8][H][block_size][D] uint8, ``kscale``,
+    ``vscale`` [L][n_blocks8][H] fp32), ``block_table`` and ``table8``; a request's pages
+    are its own.  ``finish`` turns its row of block_table so that the pages of packed
+    blocks come last and are written again, and uses table8's entries in order.  One
+    step moves at most `max_move` blocks of a request (the rest follow in later steps);
+    `max_blocks` has room for the recent rows, a block, and what one step adds beyond
+    what it moves.
+
+    The launches depend on the constructor's sizes only, so a step can be captured in a
+    CUDA graph.  ``stream`` is None (the current stream), a Stream or a raw handle, as in
+    the library's calls; the buffers belong to the stream they are first used on."""
+
+    def __init__(self, n_req: int, max_blocks: int, max_blocks8: int, block_size: int, L: int,
+                 H: int, Hq: int, D: int, n_slots: int, n_blocks8: int, n_q: int, max_rows: int,
+                 n_pos: int, recent: int = 0, max_move: Optional[int] = None,
+                 theta: float = 1e6, eps: float = 1e-6, scale: Optional[float] = None,
+                 device="cuda"):
+        self.n_req, self.max_blocks, self.max_blocks8, self.BS = n_req, max_blocks, max_blocks8, block_size
+        self.L, self.H, self.Hq, self.D = L, H, Hq, D
+        self.n_slots, self.n_blocks8, self.n_q, self.max_rows = n_slots, n_blocks8, n_q, max_rows
+        self.n_pos, self.recent, self.eps = n_pos, recent, eps
+        self.max_move = max_blocks if max_move is None else min(max_move, max_blocks)
+        self.scale = D ** -0.5 if scale is None else scale
+        dev = self.device = torch.device(device)
+        i32 = dict(dtype=torch.int32, device=dev)
+        self.q = torch.empty(L, n_q, Hq, D, dtype=torch.bfloat16, device=dev)
+        self.out = torch.empty(L, n_q, Hq, D, dtype=torch.bfloat16, device=dev)
+        self.lse = torch.empty(L, n_q, Hq, dtype=torch.float32, device=dev)
+        self.ctx = torch.zeros(n_req, **i32)
+        self.len8 = torch.zeros(n_req, **i32)
+        self.t_end = torch.zeros(n_req, **i32)
+        self.src = torch.empty(n_req, self.max_move, **i32)
+        self.dst = torch.empty(n_req, self.max_move, **i32)
+        self._page = torch.arange(max_blocks, dtype=torch.int64, device=dev)
+        self.rope = torch.empty(n_pos, D // 2, 2, dtype=torch.float32, device=dev)
+        with torch.cuda.device(dev):
+            kvc_rope_table(self.rope, n_pos, 0, D, theta)
+        self.pos = torch.empty(n_q, **i32)
+        self.tree_rows = min(max_rows, TREE_MAX_NODES)
+        self.ws = _ws(kvc_q8_attn_workspace_size(n_req, max_blocks8, max_blocks, self.tree_rows, H,
+                                                 Hq, D, block_size), dev)
+        self.dev_status = torch.zeros(1, **i32)
+
+    def begin(self, q_off, pos=None, stream=None):
+        """A step whose requests' new tokens are q_off's, at the positions that follow
+        t_end, or at pos [n_q] (a drafted tree's depths)."""
+        self.q_off = q_off
+        with _on(stream, self.device):
+            if pos is not None:
+                self.pos.copy_(pos)
+                return
+            x = torch.arange(self.n_q, dtype=torch.int32, device=self.device)
+            r = torch.bucketize(x, q_off[1:], right=True, out_int32=True).clamp_(max=self.n_req - 1)
+            self.pos.copy_(self.t_end[r] + x - q_off[r])
+
+    def write(self, layer, q, k, v, kpool, vpool, block_table, wq=None, wk=None, k_raw=None,
+              stream=None):
+        """One layer's projections q, k, v ([n_q][heads·D], any row stride); the layer's
+        pools.  The rotated queries are in self.q[layer]."""
+        kvc_qkv_rope(q, k, v, self.n_q, wq, wk, self.eps, self.rope, self.n_pos, self.pos,
+                     self.q_off, self.ctx, self.n_req, block_table, self.max_blocks, kpool, vpool,
+                     self.n_slots, self.H, self.Hq, self.D, self.BS, self.q[layer], k_raw,
+                     self.dev_status, stream)
+
+    def prompt(self, layer, kpool, vpool, block_table, stream=None):
+        """Causal attention of the new rows over cache and new rows, of requests that hold
+        nothing in 8 bits."""
+        kvc_prompt_attn(self.q[layer], kpool, vpool, self.n_slots, block_table, self.max_blocks,
+                        self.ctx, self.q_off, self.n_req, self.n_q, self.max_rows, self.H, self.Hq,
+                        self.D, self.BS, self.scale, self.out[layer], self.lse[layer],
+                        self.dev_status, stream)
+        return self.out[layer]
+
+    def attend(self, layer, kpool, vpool, block_table, k8, v8, kscale, vscale, table8,
+               tree_mask=None, stream=None):
+        """Attention of the new rows (at most 1024 of a request) over history, cache and new
+        rows; tree_mask None: chains."""
+        words = 0 if tree_mask is None else tree_mask.shape[1]
+        kvc_q8_attn(self.q[layer], k8, v8, kscale, vscale, self.n_blocks8, table8,
+                    self.max_blocks8, self.len8, kpool, vpool, self.n_slots, block_table,
+                    self.max_blocks, self.ctx, self.q_off, tree_mask, words, self.n_req, self.n_q,
+                    self.tree_rows, self.H, self.Hq, self.D, self.BS, self.scale,
+                    self.out[layer], self.lse[layer], self.ws, self.dev_status, stream)
+        return self.out[layer]
+
+    def finish(self, kpool, vpool, block_table, k8, v8, kscale, vscale, table8, n_rows=None,
+               stream=None):
+        """The step after the last layer: n_rows [n_req] of the new rows (None: all) join the
+        cache, full blocks move to 8 bits, all layers."""
+        BS = self.BS
+        with _on(stream, self.device):
+            n = self.q_off[1:] - self.q_off[:-1] if n_rows is None else n_rows
+            self.ctx.add_(n)
+            self.t_end.add_(n)
+            room = self.max_blocks8 - self.len8 // BS
+            move = ((self.ctx - self.recent).clamp(min=0) // BS).clamp(max=self.max_move)
+            move = torch.minimum(move, room)
+            i = self._page[:self.max_move]
+            some = i < move[:, None]
+            at = ((self.len8 // BS)[:, None] + i).clamp(max=self.max_blocks8 - 1)
+            self.src.copy_(torch.where(some, block_table[:, :self.max_move], -1))
+            self.dst.copy_(torch.where(some, table8.gather(1, at), -1))
+        kvc_q8_pack(kpool, vpool, self.n_slots, k8, v8, kscale, vscale, self.n_blocks8, self.src,
+                    self.dst, self.n_req * self.max_move, self.L, self.H, self.D, BS,
+                    self.dev_status, stream)
+        with _on(stream, self.device):
+            block_table.copy_(block_table.gather(1, (self._page + move[:, None]) % self.max_blocks))
+            self.ctx.sub_(move * BS)
+            self.len8.add_(move * BS)
 
 
 def paged_bytes(n_req: int, seq: int, L: int, H: int, Hq: int, D: int, n_pairs: int) -> dict:
