@@ -207,14 +207,21 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_current = None  # (raw stream of a device, current device) once torch has started CUDA
+
+
 def _stream(stream):
+    global _current
     if stream is None:
-        import torch
-        # (a Stream object costs 3 us a call: as much as a launch)
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is None or not torch.cuda.is_initialized():
-            return torch.cuda.current_stream().cuda_stream
-        return raw(torch.cuda.current_device())
+        if _current is None:
+            import torch
+            # (a Stream object costs 3 us a call: as much as a launch)
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            device = getattr(torch._C, "_cuda_getDevice", None)
+            if raw is None or device is None or not torch.cuda.is_initialized():
+                return torch.cuda.current_stream().cuda_stream
+            _current = raw, device
+        return _current[0](_current[1]())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -655,13 +662,13 @@ def kvc_mass_evict(kpool, vpool, n_slots, block_table, max_blocks, seqused_k, n_
 
 
 def _rows_ptr(t, row):
-    """Device pointer and row stride (elements) of a tensor [n][row] or [n][heads][D]
+    """Device pointer, row stride (elements) and rows of a tensor [n][row] or [n][heads][D]
     whose rows are packed; a part of a wider row, as of a fused projection, is one."""
     if not t.is_cuda:
         raise ValueError("libkvc takes device tensors only")
     shape, strides = t.shape, t.stride()
     if len(strides) == 2 and strides[1] == 1 and shape[1] == row and shape[0] > 1:
-        return t.data_ptr(), strides[0]
+        return t.data_ptr(), strides[0], shape[0]
     n = 1  # elements of a row so far, from its end
     for size, stride in zip(shape[:0:-1], strides[:0:-1]):
         if size != 1 and stride != n:
@@ -671,7 +678,7 @@ def _rows_ptr(t, row):
     if n != row:
         raise ValueError(f"libkvc takes rows of {row} packed elements "
                          f"(got shape {tuple(shape)}, strides {strides})")
-    return t.data_ptr(), strides[0] if shape[0] > 1 else row
+    return t.data_ptr(), strides[0] if shape[0] > 1 else row, shape[0]
 
 
 def kvc_qkv_rope(q, k, v, n_tok, wq, wk, eps, rope_tab, n_pos, pos, q_off, ctx_len, n_req,
@@ -682,14 +689,16 @@ def kvc_qkv_rope(q, k, v, n_tok, wq, wk, eps, rope_tab, n_pos, pos, q_off, ctx_l
     any row stride: slices of a fused projection's output are taken as they are.  wq or
     wk None: no norm.  pos None: the rotation goes by the place in the cache.  k_raw
     [H][≥ n_tok][D] takes the keys before the rotation."""
-    (qp, qs), (kp, ks), (vp, vs) = _rows_ptr(q, Hq * D), _rows_ptr(k, H * D), _rows_ptr(v, H * D)
-    if min(len(q), len(k), len(v)) < n_tok:
+    qp, qs, qn = _rows_ptr(q, Hq * D)
+    kp, ks, kn = _rows_ptr(k, H * D)
+    vp, vs, vn = _rows_ptr(v, H * D)
+    if qn < n_tok or kn < n_tok or vn < n_tok:
         raise ValueError(f"kvc_qkv_rope: q, k and v hold fewer than {n_tok} rows")
     rp, raw = None, 0
     if k_raw is not None:
         if k_raw.dim() != 3 or k_raw.shape[0] != H or k_raw.shape[1] < n_tok or k_raw.shape[2] != D:
             raise ValueError(f"kvc_qkv_rope: k_raw is [{H}][>= {n_tok}][{D}] (got {tuple(k_raw.shape)})")
-        rp, raw = _rows_ptr(k_raw, k_raw.shape[1] * D)
+        rp, raw, _ = _rows_ptr(k_raw, k_raw.shape[1] * D)
     _ok(lib.kvc_qkv_rope(qp, qs, kp, ks, vp, vs, n_tok, _ptr(wq), _ptr(wk), eps, _ptr(rope_tab),
                          n_pos, _ptr(pos), _ptr(q_off), _ptr(ctx_len), n_req, _ptr(block_table),
                          max_blocks, _ptr(kpool), _ptr(vpool), n_slots, H, Hq, D, block_size,
