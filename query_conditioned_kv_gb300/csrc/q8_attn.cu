@@ -85,10 +85,12 @@ struct Q8Smem {
   static constexpr int kRow = kScale + kQ8Warps * kQ8Stages * kQ8Keys * 8;  // a row's power of two
   static constexpr int kValid = kRow + R * 4;    // valid positions per (warp, stage)
   static constexpr int kMl = kValid + (kQ8Warps * kQ8Stages * 4 + 15) / 16 * 16;  // (reference, sum) per (warp, row)
-  static constexpr int kFull = kMl + kQ8Warps * R * 8;  // barriers per (warp, stage), then a word
+  static constexpr int kClMl = kMl + kQ8Warps * R * 8;   // (reference, sum) of the CTA, per row
+  static constexpr int kFull = kClMl + R * 8;            // barriers per (warp, stage), then a word
   static constexpr int kBytes = kFull + kQ8Warps * kQ8Stages * 8 + 16;
   static_assert(q8_ctas(NR) * (kBytes + 1024) <= 228 * 1024, "the CTAs fit an SM");
-  static_assert(kQ8Warps * R * D * 4 <= kRing, "the warps' O fit the ring");
+  static constexpr int kClO = kQ8Warps * R * D * 4;      // the CTA's O, behind the warps'
+  static_assert(kClO + R * D * 4 <= kRing, "the warps' and the CTA's O fit the ring");
   static_assert(2 * kQ8Keys * D <= kQ8Stage, "a stage of the history fits");
 };
 
@@ -153,7 +155,9 @@ __device__ __forceinline__ float lg2(float x) {
   return y;
 }
 
-template <int D, int NR>
+// CL: a cluster takes a unit, each CTA a part of its tiles, and joins the parts from one
+// another's shared memory.
+template <int D, int NR, bool CL>
 __global__ void __launch_bounds__(kQ8Threads, q8_ctas(NR))
 k_q8_rows(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, Q8Args a) {
   using S = Q8Smem<D, NR>;
@@ -170,40 +174,54 @@ k_q8_rows(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
   float *row_s = reinterpret_cast<float *>(sm + S::kRow);
   float2 *ml_s = reinterpret_cast<float2 *>(sm + S::kMl);
 
-  asm volatile("griddepcontrol.launch_dependents;");
+  if (!CL) asm volatile("griddepcontrol.launch_dependents;");
   if (lane == 0) {
     for (int i = 0; i < kQ8Stages; i++) mbar_init(full + 8 * i, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (tid == 0) *failed = 0;
-  if (blockIdx.x == 0)  // one report per bad request
-    for (int r = tid; r < a.n_req; r += kQ8Threads) {
-      int n, c, q0, T;
-      if (!q8_request(a, r, n, c, q0, T)) record_error(a.status, KVC_ERR_BOUNDS);
-    }
-  auto tiles = [&](int x) {
-    int n_rt, n_kt;
-    tree_tiles(a, x, n_rt, n_kt);
-    return (int64_t)a.H * n_rt * n_kt;
-  };
-  const WarpSums sums = warp_sums(a.n_req, tiles);
-  const int64_t total = sums.total;
-  const int n_cta = (int)min((int64_t)a.n_cta, total);  // every run holds a tile
-  if ((int)blockIdx.x >= n_cta) return;
+  int r, n8, c, q0, T, n_rt, n_kt, unit, t0;
+  int64_t g, run0, run1;  // next tile of the run, its begin and end
+  if constexpr (CL) {
+    const int S = (int)cluster_nrank(), rank = (int)cluster_rank(), u = blockIdx.x / S;
+    r = u / a.H;
+    unit = u % a.H;
+    const bool valid = q8_request(a, r, n8, c, q0, T);
+    if (!valid && unit == 0 && rank == 0 && tid == 0) record_error(a.status, KVC_ERR_BOUNDS);
+    tree_tiles(a, r, n_rt, n_kt);
+    if (n_rt == 0) return;  // (the whole cluster)
+    t0 = n_kt * rank / S;
+    g = run0 = 0;
+    run1 = n_kt * (rank + 1) / S - t0;
+  } else {
+    if (blockIdx.x == 0)  // one report per bad request
+      for (int r = tid; r < a.n_req; r += kQ8Threads) {
+        int n, c, q0, T;
+        if (!q8_request(a, r, n, c, q0, T)) record_error(a.status, KVC_ERR_BOUNDS);
+      }
+    auto tiles = [&](int x) {
+      int n_rt, n_kt;
+      tree_tiles(a, x, n_rt, n_kt);
+      return (int64_t)a.H * n_rt * n_kt;
+    };
+    const WarpSums sums = warp_sums(a.n_req, tiles);
+    const int64_t total = sums.total;
+    int64_t before;
+    const int n_cta = (int)min((int64_t)a.n_cta, total);  // every run holds a tile
+    if ((int)blockIdx.x >= n_cta) return;
+    run0 = g = run_start(total, n_cta, blockIdx.x);
+    run1 = run_start(total, n_cta, blockIdx.x + 1);
+    warp_find(sums, a.n_req, run0, tiles, r, before);
+    q8_request(a, r, n8, c, q0, T);
+    tree_tiles(a, r, n_rt, n_kt);
+    unit = (int)div64(g - before, n_kt);  // h·n_rt + row tile
+    t0 = (int)(g - before - (int64_t)unit * n_kt);
+  }
   __syncthreads();
-  const int64_t run0 = run_start(total, n_cta, blockIdx.x);
-  const int64_t run1 = run_start(total, n_cta, blockIdx.x + 1);
-  int64_t g = run0, before;  // next tile of the run
-  int r, n8, c, q0, T, n_rt, n_kt;
-  warp_find(sums, a.n_req, run0, tiles, r, before);
-  q8_request(a, r, n8, c, q0, T);
-  tree_tiles(a, r, n_rt, n_kt);
-  int unit = (int)div64(g - before, n_kt);  // h·n_rt + row tile
-  int t0 = (int)(g - before - (int64_t)unit * n_kt);
 
   const int64_t n_blocks = a.n_slots / a.BS;
   uint32_t boxed = 0, phase = 0;  // bits of the stages: filled by TMA, the barrier's parity
-  while (g < run1) {
+  while (CL || g < run1) {
     const int h = unit / n_rt, rt = unit % n_rt;
     const int t1 = (int)min((int64_t)n_kt, t0 + (run1 - g));
     const int th = q8_tiles(n8);  // tiles of the history
@@ -664,7 +682,7 @@ k_q8_rows(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
             o_s[row * D + ((16 * n + 8 * hf + g8) ^ (quad << 3))] = o[n][nr][2 * hf + e] * f;
       }
     __syncthreads();
-    const bool whole = t0 == 0 && t1 == n_kt;
+    const bool whole = !CL && t0 == 0 && t1 == n_kt;
     const int64_t slot = 2 * (int64_t)blockIdx.x + (g != run0);
     for (int e = tid; e < n_rows * (D / 4); e += kQ8Threads) {
       const int row = e / (D / 4), d4 = (e % (D / 4)) * 4;
@@ -695,10 +713,50 @@ k_q8_rows(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
         *reinterpret_cast<uint2 *>(a.out + qr * D + d4) =
             make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
         if (d4 == 0) a.lse[qr] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+      } else if (CL) {
+        *reinterpret_cast<float4 *>(sm + S::kClO + (row * D + d4) * 4) = acc;
+        if (d4 == 0) reinterpret_cast<float2 *>(sm + S::kClMl)[row] = make_float2(mx, sum);
       } else {
         *reinterpret_cast<float4 *>(a.part_o + (slot * R + row) * D + d4) = acc;
         if (d4 == 0) a.part_ml[slot * R + row] = make_float2(mx, sum);
       }
+    }
+    if constexpr (CL) {
+      // the cluster's CTAs hold the unit's parts: added up in order, the elements dealt out to
+      // all of them
+      __syncwarp();
+      cluster_sync_all();
+      const int n_cl = (int)cluster_nrank();
+      const uint32_t o_at = smem_u32(sm + S::kClO), ml_at = smem_u32(sm + S::kClMl);
+      for (int e = (int)cluster_rank() * kQ8Threads + tid; e < n_rows * (D / 4); e += n_cl * kQ8Threads) {
+        const int row = e / (D / 4), d4 = (e % (D / 4)) * 4;
+        float mx = -INFINITY;
+#pragma unroll 4
+        for (int k = 0; k < n_cl; k++) mx = fmaxf(mx, ld_cluster_f2(mapa_u32(ml_at + row * 8, k)).x);
+        const float base = mx == -INFINITY ? 0.f : mx;
+        float sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = 0; k < n_cl; k++) {
+          const float2 ml = ld_cluster_f2(mapa_u32(ml_at + row * 8, k));
+          const float4 v = ld_cluster_f4(mapa_u32(o_at + (row * D + d4) * 4, k));
+          const float f = ex2(ml.x - base);
+          sum = fmaf(ml.y, f, sum);
+          acc.x = fmaf(v.x, f, acc.x);
+          acc.y = fmaf(v.y, f, acc.y);
+          acc.z = fmaf(v.z, f, acc.z);
+          acc.w = fmaf(v.w, f, acc.w);
+        }
+        const int x = rt * a.rstep + row;
+        const int64_t qr = (int64_t)(q0 + x / a.G) * a.Hq + h * a.G + x % a.G;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        *reinterpret_cast<uint2 *>(a.out + qr * D + d4) =
+            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        if (d4 == 0) a.lse[qr] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+      }
+      __syncwarp();
+      cluster_sync_all();  // (no CTA leaves while another reads its part)
+      break;
     }
     g += n_t;
     t0 = 0;
@@ -745,25 +803,68 @@ bool rows8_map(CUtensorMap *m, const void *pool, int64_t rows, int D, int box) {
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int NR>
-cudaError_t launch_q8_rows(const Q8Args &a, const CUtensorMap &tm_k, const CUtensorMap &tm_v, cudaStream_t s) {
+// CTAs of the cluster that shares a unit, 0: the tiles are dealt out and joined by a second
+// launch.  In tiles that a CTA takes one after another, with what the two forms cost besides
+// (as tree_cluster in tree_attn.cu): dealt out, an even share and 17; clusters, a share for
+// every wave of CTAs, 8 a wave after the first, and 3.5.  One token, 8 KV heads, D 128: one
+// request of 1K 8.4 us by clusters of 8 and 9.2 dealt out, of 16K 18.8 and 18.2; 4 of 8K
+// 19.4 by clusters of 8 and 21.8; 16 of 4K 32.1 by two and 34.6; 64 of 1K 47 by two and 38.9.
+int q8_cluster(const Q8Args &a, int max_rt) {
+  if (max_rt > 1 || a.rows > 16) return 0;  // (a cluster takes one row tile; more rows leave it to the even deal)
+  const double units = (double)a.n_req * a.H, sms = device_sm_count(), per = q8_ctas(a.rows / 8);
+  const double kt = ceil((double)a.max_blocks8 * a.BS / (kQ8Warps * kQ8Keys)) +
+                    ceil((double)a.max_blocks * a.BS / a.tile);
+  int best = 0;
+  double least = units * kt / (per * sms) + 17;
+  for (int S = 1; S <= 16 && S <= kt; S *= 2) {
+    // (a GPC's 16 to 20 SMs hold fewer large clusters)
+    const double room = per * sms * (S == 16 ? 0.42 : S == 8 ? 0.84 : S == 4 ? 0.95 : 1);
+    const double full = units * S / room, waves = ceil(full);
+    const double share = waves > 1 ? full + 0.6 * (waves - full) : 1;
+    const double cost = share * ceil(kt / S) * (S == 16 ? 1.25 : 1) + 8 * (waves - 1) + 3.5;
+    if (cost < least) {
+      least = cost;
+      best = S;
+    }
+  }
+  return units * best <= INT32_MAX ? best : 0;
+}
+
+template <int D, int NR, bool CL>
+cudaError_t launch_q8_rows(const Q8Args &a, const CUtensorMap &tm_k, const CUtensorMap &tm_v, int cluster,
+                           cudaStream_t s) {
   constexpr int smem = Q8Smem<D, NR>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(k_q8_rows<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  auto *kern = k_q8_rows<D, NR, CL>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess && cluster > 8)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
-  k_q8_rows<D, NR><<<a.n_cta, kQ8Threads, smem, s>>>(tm_k, tm_v, a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(CL ? (unsigned)(a.n_req * a.H * cluster) : (unsigned)a.n_cta);
+  cfg.blockDim = dim3(kQ8Threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)cluster;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, tm_k, tm_v, a);
 }
 template <int D>
-cudaError_t launch_q8(const Q8Args &a, cudaStream_t s) {
+cudaError_t launch_q8(const Q8Args &a, int cluster, cudaStream_t s) {
   CUtensorMap tm_k{}, tm_v{};
   const int64_t rows = a.n_blocks8 * a.H * a.BS;
   if (a.box8 && !(rows8_map(&tm_k, a.k8, rows, D, a.box8) && rows8_map(&tm_v, a.v8, rows, D, a.box8)))
     return cudaErrorUnknown;
   switch (a.rows / 8) {
-    case 1: return launch_q8_rows<D, 1>(a, tm_k, tm_v, s);
-    case 2: return launch_q8_rows<D, 2>(a, tm_k, tm_v, s);
-    case 3: return launch_q8_rows<D, 3>(a, tm_k, tm_v, s);
-    default: return launch_q8_rows<D, 4>(a, tm_k, tm_v, s);
+    case 1: return cluster ? launch_q8_rows<D, 1, true>(a, tm_k, tm_v, cluster, s)
+                           : launch_q8_rows<D, 1, false>(a, tm_k, tm_v, 0, s);
+    case 2: return cluster ? launch_q8_rows<D, 2, true>(a, tm_k, tm_v, cluster, s)
+                           : launch_q8_rows<D, 2, false>(a, tm_k, tm_v, 0, s);
+    case 3: return launch_q8_rows<D, 3, false>(a, tm_k, tm_v, 0, s);
+    default: return launch_q8_rows<D, 4, false>(a, tm_k, tm_v, 0, s);
   }
 }
 
@@ -800,8 +901,9 @@ cudaError_t launch_q8_attn(const uint16_t *q, const uint8_t *k8, const uint8_t *
   a.part_ml = reinterpret_cast<float2 *>(a.part_o + (size_t)2 * a.n_cta * a.rows * D);
   // (a box's rows lie in one block, and a row's number fits the box's coordinate)
   a.box8 = n_blocks8 * H * BS > INT32_MAX ? 0 : BS % 32 == 0 ? 32 : BS % 16 == 0 ? 16 : BS % 8 == 0 ? 8 : 0;
-  const cudaError_t e = D == 128 ? launch_q8<128>(a, s) : launch_q8<64>(a, s);
-  if (e != cudaSuccess) return e;
+  const int cluster = q8_cluster(a, max_rt);
+  const cudaError_t e = D == 128 ? launch_q8<128>(a, cluster, s) : launch_q8<64>(a, cluster, s);
+  if (e != cudaSuccess || cluster) return e;
   return launch_join(a, D, max_rt, s);
 }
 

@@ -714,6 +714,14 @@ def test_q8_long_and_many(kvc, n_req, len8, H, G, D):
     go(kvc, Q8(len8, n, [33] * n_req, [1] * n_req, H, G, D, 16))
 
 
+@pytest.mark.parametrize("len8", [40, 130, 600, 1500, 5000])
+@pytest.mark.parametrize("n_req,H,G,T,D", [(1, 2, 4, 1, 128), (3, 8, 2, 2, 64), (2, 4, 16, 1, 128), (5, 1, 1, 9, 64)])
+def test_q8_clusters(kvc, len8, n_req, H, G, T, D):
+    """Units that clusters of every size share, some parts without a tile; one row tile and more."""
+    n = [len8] + [max(0, len8 - 300 * i) for i in range(1, n_req)]
+    go(kvc, Q8(len8 + T, n, [20, 0, 65, 3, 130][:n_req], [T] * n_req, H, G, D, 16, pad=1))
+
+
 @pytest.mark.parametrize("spread,kscale", [(0, 1.0), (1, 0.0), (3, 30.0), (20, 1e-6), (5, 1e12)])
 def test_q8_scales(kvc, spread, kscale):
     """Blocks' scales 2^±spread apart under flat and peaked logits."""
