@@ -8,6 +8,8 @@
 #include <cudaTypedefs.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace kvc {
 namespace tc {
 
@@ -450,16 +452,34 @@ __device__ __forceinline__ float ex2(float x) {
 
 // ---------------------------------------------------------------- host
 
+// cuTensorMapEncodeTiled, for a thread with a current context: a host thread that has made
+// no runtime call yet has none, and gets the one that the runtime would give it (the
+// primary context of its device).
 inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> encode{nullptr};
+  static std::atomic<PFN_cuCtxGetCurrent_v4000> current{nullptr};
+  auto find = [](const char *name, unsigned version) -> void * {
     void *p = nullptr;
     cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    return cudaGetDriverEntryPointByVersion(name, &p, version, cudaEnableDefault, &q) == cudaSuccess &&
+                   q == cudaDriverEntryPointSuccess
+               ? p
+               : nullptr;
+  };
+  auto fn = encode.load(std::memory_order_relaxed);
+  if (!fn) {
+    fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(find("cuTensorMapEncodeTiled", 12000));
+    encode.store(fn, std::memory_order_relaxed);
   }
+  auto get = current.load(std::memory_order_relaxed);
+  if (!get) {
+    get = reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(find("cuCtxGetCurrent", 4000));
+    current.store(get, std::memory_order_relaxed);
+  }
+  CUcontext ctx = nullptr;
+  int dev = 0;
+  if (get && get(&ctx) == CUDA_SUCCESS && !ctx && cudaGetDevice(&dev) == cudaSuccess)
+    (void)cudaSetDevice(dev);
   return fn;
 }
 
