@@ -1013,7 +1013,8 @@ kvc_status kvc_mass_evict(kvc_bf16 *kpool, kvc_bf16 *vpool, int64_t n_slots,
  *   kvc_q8_attn      per layer: kvc_tree_attn with a history in 8 bits before
  *                    the bf16 rows.
  * Any H in [1, 256], Hq a multiple of H with Hq ≤ 256, D ∈ {64, 128} and block_size in
- * [1, 64].
+ * [1, 64].  A page that kvc_qkv_rope writes is one page of one request; pages that are
+ * only read may be several requests'.
  * ====================================================================== */
 
 /* ------------------------------------------------------------------------
@@ -1071,9 +1072,10 @@ kvc_status kvc_qkv_rope(const kvc_bf16 *q, int64_t q_stride, const kvc_bf16 *k,
  *   q           device bf16 [n_q][Hq][D]
  *   kpool, vpool device bf16 [n_slots][H][D]: one layer of the pools
  *   block_table device int32 [n_req][max_blocks]
- *   ctx_len     device int32 [n_req];  q_off  device int32 [n_req+1]
+ *   ctx_len     device int32 [n_req];  q_off  device int32 [n_req+1], ascending
  *   out         device bf16 [n_q][Hq][D];  lse  device fp32 [n_q][Hq] (natural
- *               log; kvc_attn_mass and kvc_recover_score take it)
+ *               log; kvc_attn_mass and kvc_recover_score take it); neither shares
+ *               memory with the inputs
  * Accuracy, NaN and infinities: as kvc_tree_attn; positions that a row does not
  * see never reach its result, whatever they hold.  A row that sees nothing (every
  * page of it outside the pool) gets out = 0 and lse = −inf.  Rows of q outside every
@@ -1081,9 +1083,10 @@ kvc_status kvc_qkv_rope(const kvc_bf16 *q, int64_t q_stride, const kvc_bf16 *k,
  * A request whose ctx_len or q_off is out of range (negative, T > max_rows, c + T >
  * max_blocks·block_size, rows past n_q) is recorded as KVC_ERR_BOUNDS and its rows
  * are left untouched; a visible position whose block id is outside the pool is
- * recorded and treated as not visible.
- * Errors: KVC_ERR_INVALID_ARG (NULL, sizes < 1, scale not finite), KVC_ERR_SHAPE (D,
- * Hq % H, Hq > 256, block_size > 64, max_rows > KVC_TREE_MAX_TOKENS, too many
+ * recorded and treated as not visible.  (Where q_off descends, requests beside the bad
+ * one may be left out too.)
+ * Errors: KVC_ERR_INVALID_ARG (NULL, sizes < 1, scale not finite, outputs that overlap
+ * inputs or each other), KVC_ERR_SHAPE (D, Hq % H, Hq > 256, block_size > 64, max_rows > KVC_TREE_MAX_TOKENS, too many
  * positions), KVC_ERR_ALIGN (16 bytes; lse 4).
  * ---------------------------------------------------------------------- */
 kvc_status kvc_prompt_attn(const kvc_bf16 *q, const kvc_bf16 *kpool, const kvc_bf16 *vpool,
@@ -1143,7 +1146,8 @@ kvc_status kvc_q8_pack(const kvc_bf16 *kpool, const kvc_bf16 *vpool, int64_t n_s
  * A request whose len8, ctx_len or q_off is out of range is recorded as
  * KVC_ERR_BOUNDS and its rows are left untouched; a position whose block id is
  * outside its pool is recorded and treated as not visible.
- * Errors: as kvc_tree_attn (kscale, vscale: aligned to 4 bytes).
+ * Errors: as kvc_tree_attn (kscale, vscale: aligned to 4 bytes), and KVC_ERR_INVALID_ARG
+ * for outputs or scratch that overlap inputs or each other.
  * ---------------------------------------------------------------------- */
 size_t kvc_q8_attn_workspace_size(int32_t n_req, int32_t max_blocks8, int32_t max_blocks,
                                   int32_t max_tree, int32_t H, int32_t Hq, int32_t D,

@@ -745,6 +745,15 @@ kvc_status kvc_prompt_attn(const kvc_bf16 *q, const kvc_bf16 *kpool, const kvc_b
   if (!aligned16(q) || !aligned16(kpool) || !aligned16(vpool) || !aligned16(out) ||
       reinterpret_cast<uintptr_t>(lse) % 4 != 0)
     return KVC_ERR_ALIGN;
+  const size_t rows = (size_t)n_q * Hq, pool = (size_t)n_slots * H * D * 2, reqs = (size_t)n_req * 4;
+  if (outputs_overlap({{out, rows * D * 2}, {lse, rows * 4}},
+                      {{q, rows * D * 2},
+                       {kpool, pool},
+                       {vpool, pool},
+                       {block_table, reqs * max_blocks},
+                       {ctx_len, reqs},
+                       {q_off, reqs + 4}}))
+    return KVC_ERR_INVALID_ARG;
   return from_cuda(kvc::launch_prompt_attn(q, kpool, vpool, n_slots, block_table, max_blocks,
                                            ctx_len, q_off, n_req, n_q, max_rows, H, Hq, D,
                                            block_size, scale, out, lse, dev_status, stream));
@@ -809,9 +818,26 @@ kvc_status kvc_q8_attn(const kvc_bf16 *q, const uint8_t *k8, const uint8_t *v8,
       reinterpret_cast<uintptr_t>(kscale) % 4 != 0 ||
       reinterpret_cast<uintptr_t>(vscale) % 4 != 0 || reinterpret_cast<uintptr_t>(lse) % 4 != 0)
     return KVC_ERR_ALIGN;
-  if (ws_bytes < kvc_q8_attn_workspace_size(n_req, max_blocks8, max_blocks, max_tree, H, Hq, D,
-                                            block_size))
-    return KVC_ERR_WORKSPACE;
+  const size_t need =
+      kvc_q8_attn_workspace_size(n_req, max_blocks8, max_blocks, max_tree, H, Hq, D, block_size);
+  if (ws_bytes < need) return KVC_ERR_WORKSPACE;
+  const size_t rows = (size_t)n_q * Hq, pool = (size_t)n_slots * H * D * 2, reqs = (size_t)n_req * 4;
+  const size_t units = (size_t)n_blocks8 * H, pool8 = units * block_size * D;
+  if (outputs_overlap({{out, rows * D * 2}, {lse, rows * 4}, {ws, need}},
+                      {{q, rows * D * 2},
+                       {k8, pool8},
+                       {v8, pool8},
+                       {kscale, units * 4},
+                       {vscale, units * 4},
+                       {table8, reqs * max_blocks8},
+                       {len8, reqs},
+                       {kpool, pool},
+                       {vpool, pool},
+                       {block_table, reqs * max_blocks},
+                       {ctx_len, reqs},
+                       {q_off, reqs + 4},
+                       {tree_mask, (size_t)n_q * mask_words * 4}}))
+    return KVC_ERR_INVALID_ARG;
   return from_cuda(kvc::launch_q8_attn(q, k8, v8, kscale, vscale, n_blocks8, table8, max_blocks8,
                                        len8, kpool, vpool, n_slots, block_table, max_blocks,
                                        ctx_len, q_off, tree_mask, mask_words, n_req, n_q,

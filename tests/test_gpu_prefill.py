@@ -483,6 +483,54 @@ def test_prompt_bad_requests(kvc):
     t.compare(live=range(70))
 
 
+def test_prompt_out_off_a_sector(kvc):
+    """out on a 16-byte boundary that is no 32-byte one, lse on a 4-byte one."""
+    t = Prompt(69, [0, 40], [140, 33], 2, 4, 128, 16).gpu()
+    room = torch.full((t.n_q * t.Hq * t.D + 8,), 7.0, dtype=torch.bfloat16, device=DEV)
+    t.d["out"] = room[8:].view(t.n_q, t.Hq, t.D)
+    t.d["lse"] = torch.full((t.n_q * t.Hq + 1,), 7.0, device=DEV)[1:].view(t.n_q, t.Hq)
+    t.call(kvc)
+    assert status(kvc, t.d["status"]) == 0
+    t.compare()
+    assert bool((room[:8] == 7).all())
+
+
+def test_calls_from_several_threads(kvc):
+    """Calls of different sizes from several host threads on streams of their own."""
+    import threading
+    jobs = [Prompt(200, [0], [600], 2, 4, 128, 16), Prompt(201, [900], [40], 1, 2, 64, 8),
+            Q8(202, [700], [20], [1], 4, 4, 128, 16), Q8(203, [100, 40], [3, 90], [4, 2], 2, 8, 64, 16),
+            Rope(204, [5, 0], [40, 9], 2, 4, 128, 16), Prompt(205, [0, 3], [100, 257], 1, 3, 128, 5)]
+    want = []
+    for t in jobs:
+        t.gpu().call(kvc)
+        torch.cuda.synchronize()
+        want.append([t.d["out"].clone()] + ([t.d["lse"].clone()] if "lse" in t.d else []))
+        t.gpu()
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(t, w):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(10):
+                    t.call(kvc, stream=s)
+            s.synchronize()
+            got = [t.d["out"]] + ([t.d["lse"]] if "lse" in t.d else [])
+            if not all(torch.equal(a, b) for a, b in zip(got, w)):
+                failed.append(type(t).__name__)
+        except Exception as e:  # noqa: BLE001
+            failed.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=x) for x in zip(jobs, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+
+
 def test_prompt_repeats_replays_and_streams(kvc):
     t = Prompt(71, [0, 33, 5], [260, 100, 3], 2, 4, 128, 16).gpu()
     want = [x.clone() for x in t.call(kvc)]

@@ -72,7 +72,9 @@ REFUSED = {
         (dict(q_out=1 * M), INVALID), (dict(q_out=2 * M + 512), INVALID), (dict(kpool=3 * M), INVALID),
         (dict(vpool=11 * M + 1024), INVALID), (dict(k_raw=13 * M + 64), INVALID), (dict(k_raw=6 * M), INVALID)],
     "kvc_prompt_attn": PAGED + TABLE + HEADS + ATTENTION + [
-        (dict(max_rows=0), INVALID), (dict(max_rows=(1 << 24) + 1), SHAPE)],
+        (dict(max_rows=0), INVALID), (dict(max_rows=(1 << 24) + 1), SHAPE),
+        (dict(out=1 * M), INVALID), (dict(out=3 * M - 16), INVALID), (dict(lse=7 * M + 4), INVALID),
+        (dict(lse=4 * M + 60), INVALID)],
     "kvc_q8_pack": PAGED + [
         (dict(H=257), SHAPE),        (dict(k8=None), INVALID), (dict(v8=None), INVALID), (dict(kscale=None), INVALID),
         (dict(vscale=None), INVALID), (dict(src_block=None), INVALID), (dict(dst_block=None), INVALID),
@@ -88,7 +90,9 @@ REFUSED = {
         (dict(n_blocks8=1 << 31), SHAPE), (dict(max_tree=0), INVALID),
         (dict(max_tree=1025, mask_words=64), SHAPE), (dict(mask_words=1), SHAPE), (dict(ws=None), INVALID),
         (dict(ws=16 * M + 8), ALIGN), (dict(ws_bytes=64), WORKSPACE), (dict(k8=2 * M + 4), ALIGN),
-        (dict(v8=3 * M + 8), ALIGN), (dict(kscale=4 * M + 2), ALIGN), (dict(vscale=5 * M + 3), ALIGN)],
+        (dict(v8=3 * M + 8), ALIGN), (dict(kscale=4 * M + 2), ALIGN), (dict(vscale=5 * M + 3), ALIGN),
+        (dict(out=1 * M + 256), INVALID), (dict(out=3 * M + 64), INVALID), (dict(lse=5 * M + 8), INVALID),
+        (dict(ws=14 * M + 64), INVALID), (dict(lse=16 * M + 32), INVALID), (dict(out=13 * M), INVALID)],
 }
 
 
