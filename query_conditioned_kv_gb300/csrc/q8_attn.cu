@@ -402,7 +402,7 @@ k_q8_rows(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
         for (int nr = 0; nr < NR; nr++)
 #pragma unroll
           for (int e = 0; e < 2; e++) {
-            const float f = ex2(-off[nr][e]);
+            const float f = ex2(-0.5f * off[nr][e]);
             float most = 0.f;
             sum[nr][e] = 0.f;
 #pragma unroll
@@ -413,7 +413,9 @@ k_q8_rows(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
               if (masked && !((vis[nr][e] >> (8 * i + g8)) & 1u)) z = -INFINITY;
               z = ex2(z);
               sum[nr][e] += z;
-              z *= scaled ? sv[i] * f : f;
+              // (in halves: the scale times the whole factor may pass fp32; times a half, only
+              // where the weight is 0, and 0·inf is 0.  A NaN is in the sum.)
+              z = scaled ? fmaxf((z * f) * (sv[i] * f), 0.f) : z * f * f;
               most = fmaxf(most, z);
               w[i / 2][nr][2 * (i & 1) + e] = z;
             }

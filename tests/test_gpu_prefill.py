@@ -798,6 +798,20 @@ def test_q8_extreme_scales_and_queries(kvc):
     go(kvc, t)
 
 
+def test_q8_no_weight_on_far_larger_scales(kvc):
+    """A CTA's first tile has the least scale of values, its next one scales 2^146 times as large at
+    positions of no weight: they add nothing."""
+    t = Q8(37, [160] * 16, [5] * 16, [1] * 16, 32, 1, 64, 16)
+    t.q[:] = t.q.abs()
+    for r in range(16):
+        t.ks[t.t8[r][:8]] = 2.0 ** -20
+        t.vs[t.t8[r][:8]] = 2.0 ** -126
+        t.ks[t.t8[r][8:]] = 0.5
+        t.vs[t.t8[r][8:]] = 2.0 ** 20
+        t.k8.view(torch.uint8)[t.t8[r][8:]] = torch.tensor([-448.0]).to(F8).view(torch.uint8)
+    go(kvc, t)
+
+
 def test_q8_bad_pages_and_requests(kvc):
     for BS in (16, 5):
         t = Q8(25, [100, 64, 40], [40, 0, 16], [2, 2, 1], 2, 2, 128, BS)
