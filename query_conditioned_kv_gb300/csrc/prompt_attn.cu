@@ -426,7 +426,7 @@ k_prompt_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
       if (!ok) break;
       tc_fence_after();
       // which keys this row sees, where it is not all of them
-      const bool masked = (t0 + t + 1) * kPaKeys > c + tx + 1 || sm.bad;
+      const bool masked = (t0 + t + 1) * kPaKeys > c + tx + 1 || __any_sync(0xFFFFFFFFu, sm.bad);
       uint32_t see[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
       if (masked) {
         const int lim = c + token + 1 - (t0 + t) * kPaKeys;
