@@ -9,18 +9,34 @@
 // D/16 lanes hold a head, lane c the pairs (j, j + D/2) for j in [8c, 8c + 8),
 // so that a rotation needs no exchange and the norm only D/16 lanes'.  Its
 // cosines and sines stay in registers over all heads.  What counts is how many
-// warps an SM holds (a warp waits for lookups, its row and the norm's sum in turn):
-// 32 warps with one group of heads ahead take 44 us for 8192 tokens of 48 heads with
-// norms and raw keys (222 MB, 5.05 TB/s) and 127 us for 22K tokens of 64 heads without
-// (5.98 TB/s, 88 % of a copy's rate); 24 warps with two ahead 52 and 143, 16 with four
-// 55 and 158; bulk copies into a ring of shared memory (24 warps) 47 and 137.
+// warps an SM holds (a warp waits for lookups, its row and the norm's sum in turn) and
+// how many instructions a row takes, so columns go in pairs through packed products:
+// 28 warps with one group of heads ahead take 41 us for 8192 tokens of 48 heads with
+// norms and raw keys (222 MB, 5.40 TB/s) and 125 us for 22K tokens of 64 heads without
+// (6.10 TB/s, 90 % of a copy's rate).  24 warps take 45 and 129, 30 to 32 warps 43 and
+// 125; one column an instruction, 32 warps, 43 and 127; that with 24 warps and two
+// groups ahead 52 and 143, with bulk copies into a ring of shared memory 47 and 137.
 #include "kvc_internal.cuh"
+#include "tc_ptx.cuh"
 
 namespace kvc {
 namespace {
 
+using namespace tc;
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack2(uint64_t x) {
+  float a, b;
+  upk2(x, a, b);
+  return pack_bf16x2(a, b);
+}
+
 constexpr int kRopeWarps = 2;
-constexpr int kRopeCtas = 16;  // per SM
+constexpr int kRopeCtas = 14;  // per SM
 constexpr int kAhead = 1;    // groups of heads in flight
 
 struct RopeArgs {
@@ -111,18 +127,18 @@ k_qkv_rope(RopeArgs a) {
   int64_t slot = -1;
   if (blk >= 0 && blk < a.n_slots / a.BS) slot = (int64_t)blk * a.BS + (p - page * a.BS);
   else if (lane == 0) record_error(a.status, KVC_ERR_BOUNDS);
-  float cs[8], sn[8];
+  // (pairs of columns: two products or sums an instruction)
+  uint64_t cs[4], sn[4];
   {
     const float4 *t = reinterpret_cast<const float4 *>(a.tab + ((int64_t)pos * HALF + 8 * c) * 2);
 #pragma unroll
     for (int e = 0; e < 4; e++) {
       const float4 f = __ldg(t + e);
-      cs[2 * e] = f.x;
-      sn[2 * e] = f.y;
-      cs[2 * e + 1] = f.z;
-      sn[2 * e + 1] = f.w;
+      cs[e] = pk2(f.x, f.z);
+      sn[e] = pk2(f.y, f.w);
     }
   }
+  const uint64_t minus = pk2(-1.f, -1.f);
 
   for (int g = g0; g < g1; g += kAhead) {
 #pragma unroll
@@ -133,17 +149,18 @@ k_qkv_rope(RopeArgs a) {
       const uint32_t wl[4] = {lo[u].x, lo[u].y, lo[u].z, lo[u].w};
       const uint32_t wh[4] = {hi[u].x, hi[u].y, hi[u].z, hi[u].w};
       const uint4 vlo = lo[u], vhi = hi[u];
-      float xl[8], xh[8], sum = 0.f;
+      uint64_t xl[4], xh[4], sq = 0;
 #pragma unroll
       for (int e = 0; e < 4; e++) {
-        xl[2 * e] = bf16_lo(wl[e]);
-        xl[2 * e + 1] = bf16_hi(wl[e]);
-        xh[2 * e] = bf16_lo(wh[e]);
-        xh[2 * e + 1] = bf16_hi(wh[e]);
+        xl[e] = pk2(bf16_lo(wl[e]), bf16_hi(wl[e]));
+        xh[e] = pk2(bf16_lo(wh[e]), bf16_hi(wh[e]));
       }
       if (g + kAhead < g1) load(u, g + kAhead + u);
 #pragma unroll
-      for (int e = 0; e < 8; e++) sum = fmaf(xl[e], xl[e], fmaf(xh[e], xh[e], sum));
+      for (int e = 0; e < 4; e++) sq = fma2(xl[e], xl[e], fma2(xh[e], xh[e], sq));
+      float sum, sum1;
+      upk2(sq, sum, sum1);
+      sum += sum1;
 #pragma unroll
       for (int o = 1; o < LPH; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
       if (!live) continue;
@@ -161,37 +178,23 @@ k_qkv_rope(RopeArgs a) {
         const uint4 w0 = __ldg(reinterpret_cast<const uint4 *>(w + 8 * c));
         const uint4 w1 = __ldg(reinterpret_cast<const uint4 *>(w + HALF + 8 * c));
         const uint32_t a0[4] = {w0.x, w0.y, w0.z, w0.w}, a1[4] = {w1.x, w1.y, w1.z, w1.w};
+        const uint64_t f2 = pk2(f, f);
 #pragma unroll
         for (int e = 0; e < 4; e++) {
-          xl[2 * e] = xl[2 * e] * f * bf16_lo(a0[e]);
-          xl[2 * e + 1] = xl[2 * e + 1] * f * bf16_hi(a0[e]);
-          xh[2 * e] = xh[2 * e] * f * bf16_lo(a1[e]);
-          xh[2 * e + 1] = xh[2 * e + 1] * f * bf16_hi(a1[e]);
+          xl[e] = mul2(mul2(xl[e], f2), pk2(bf16_lo(a0[e]), bf16_hi(a0[e])));
+          xh[e] = mul2(mul2(xh[e], f2), pk2(bf16_lo(a1[e]), bf16_hi(a1[e])));
         }
       }
       if (kind == 1 && a.k_raw) {
-        uint32_t rl[4], rh[4];
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-          rl[e] = pack_bf16x2(xl[2 * e], xl[2 * e + 1]);
-          rh[e] = pack_bf16x2(xh[2 * e], xh[2 * e + 1]);
-        }
         uint16_t *d = a.k_raw + (hh - a.Hq) * a.raw_stride + (int64_t)x * D + 8 * c;
-        *reinterpret_cast<uint4 *>(d) = make_uint4(rl[0], rl[1], rl[2], rl[3]);
-        *reinterpret_cast<uint4 *>(d + HALF) = make_uint4(rh[0], rh[1], rh[2], rh[3]);
+        *reinterpret_cast<uint4 *>(d) = make_uint4(pack2(xl[0]), pack2(xl[1]), pack2(xl[2]), pack2(xl[3]));
+        *reinterpret_cast<uint4 *>(d + HALF) = make_uint4(pack2(xh[0]), pack2(xh[1]), pack2(xh[2]), pack2(xh[3]));
       }
       uint32_t ol[4], oh[4];
 #pragma unroll
       for (int e = 0; e < 4; e++) {
-        float u0[2], u1[2];
-#pragma unroll
-        for (int b = 0; b < 2; b++) {
-          const int j = 2 * e + b;
-          u0[b] = fmaf(xl[j], cs[j], -xh[j] * sn[j]);
-          u1[b] = fmaf(xh[j], cs[j], xl[j] * sn[j]);
-        }
-        ol[e] = pack_bf16x2(u0[0], u0[1]);
-        oh[e] = pack_bf16x2(u1[0], u1[1]);
+        ol[e] = pack2(fma2(xl[e], cs[e], mul2(mul2(xh[e], minus), sn[e])));
+        oh[e] = pack2(fma2(xh[e], cs[e], mul2(xl[e], sn[e])));
       }
       uint16_t *d;
       if (kind == 0) d = a.q_out + ((int64_t)x * a.Hq + hh) * D;
@@ -222,9 +225,13 @@ cudaError_t launch_qkv_rope(const uint16_t *q, int64_t qs, const uint16_t *k, in
   a.n_tok = n_tok, a.n_pos = n_pos, a.n_req = n_req, a.max_blocks = max_blocks;
   a.H = H, a.Hq = Hq, a.BS = BS;
   const int groups = (Hq + 2 * H + 512 / D - 1) / (512 / D);
-  // parts of a token's heads: one group of heads each while the GPU has room for them all
+  // parts of a token's heads: up to one group of heads each, while the GPU has room
+  // for all the warps at once.  48 heads, D 128: one token 7.5 us in one part and 3.3 in
+  // twelve; 512 tokens 7.9 in one, 5.2 in eight; 2048 11.4 in one, 9.9 in two, 11.6 in
+  // four; 4096 17.4 in one and 18.6 in two.
+  const int64_t room = kRopeWarps * kRopeCtas * (int64_t)device_sm_count();
   int parts = 1;
-  while (parts < groups && (int64_t)n_tok * 2 * parts <= 16 * (int64_t)device_sm_count()) parts *= 2;
+  while (parts < groups && 2 * (int64_t)n_tok * parts <= room) parts *= 2;
   const dim3 grid((unsigned)((n_tok + kRopeWarps - 1) / kRopeWarps),
                   (unsigned)(parts < groups ? parts : groups));
   if (D == 128) k_qkv_rope<128><<<grid, kRopeWarps * 32, 0, s>>>(a);
