@@ -28,6 +28,14 @@
 // tile's two products.  Four warps load, 32 keys of a tile each: TMA boxes of whole
 // page rows, or cp.async row by row where a page size has no box, at the end, and for
 // the values that some row of the pair does not see.
+//
+// Bound by the tensor core and by what hangs on its results: a pair of row tiles and 128
+// keys are 32 products of 64 cycles, and S(t + 1) waits for the end of the product that
+// reads P.  8192 tokens of 8 KV and 32 query heads, D 128: 414 us, 1.33 PFLOP/s, 69 % of
+// a library product's burst rate; 2048 behind 131072 3215 us, 1.36 PFLOP/s.  Without any
+// softmax the latter would take 2960, without the loads too no less: so neither is what a
+// step is spent on.  An issuer per row tile lets the two fall into step (3758 us), the
+// weights handed over 64 keys at a time cost 3380, two threads a row 3247.
 #include <float.h>
 
 #include <algorithm>
@@ -681,7 +689,9 @@ bool rows_map(CUtensorMap *m, const void *pool, int64_t n_slots, int H, int D, i
 // CTAs that share a unit (1, 2, 4 or 8), in key tiles that a CTA takes one after another:
 // waves of CTAs, each with its share of a unit's keys, a beginning and an end worth about
 // four tiles, and the join's two.  An SM holds one CTA, and clusters of 4 and 8 leave
-// some SMs of a GPC empty.
+// some SMs of a GPC empty.  8 KV and 32 query heads, D 128, in us by 1, 2, 4 and 8: 17
+// rows behind 8192 95, 60, 36, 25; 256 behind 65536 792, 422, 222, 351; 512 (twice) behind
+// 16384 213, 245, 272, 380; a prompt of 300 14, 21, 20, 21; of 1024 23, 43, 71, 154.
 int prompt_cluster(int64_t units, int64_t kt) {
   const double sms = device_sm_count();
   int best = 1;
@@ -707,6 +717,7 @@ cudaError_t launch_prompt_tc(const TreeArgs &a, int max_rows, cudaStream_t s) {
   p.gc = (a.G + p.n_ch - 1) / p.n_ch;
   p.tpt = 128 / p.gc;
   p.NS = (int)std::min<size_t>(kPaSlots, (kSmemMax - kFixed) / kSlot);
+  // (8192 tokens: pages of 32 and 16 400 us, of 8 405; of 12, row by row, 467)
   p.box = a.BS % 32 == 0 ? 32 : a.BS % 16 == 0 ? 16 : a.BS % 8 == 0 ? 8 : 0;
   p.wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
   p.idesc_s = make_idesc(128, kPaKeys);

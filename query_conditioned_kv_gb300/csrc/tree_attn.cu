@@ -60,6 +60,94 @@ struct RowSmem {
   static_assert(kClO + MT * 16 * D * 4 <= kRing, "the warps' and the CTA's O fit the ring");
 };
 
+// O += W·V for the KT keys of a warp's tile (V rows at vb, the first key's position
+// p0), weights in the score registers of MT row tiles of 16.
+template <int D, int MT, int KT>
+__device__ __forceinline__ void tile_values(const TreeArgs &a, const float (&s)[MT][KT / 8][4],
+                                            float (&o)[MT][D / 8][4], uint32_t vb, uint32_t okb,
+                                            int rt, int q0, int c, int T, int p0) {
+  constexpr int NT = D / 8, CH = D / 8;
+  const int lane = threadIdx.x & 31;
+  // A node's V may hold infinities or NaN that some rows do not see, and a
+  // product 0·inf would hand them to those rows.  A tile with such values
+  // takes the sum term by term, over the rows' visible keys only; there such a
+  // value is added as it is, for a weight too small for fp32 is not 0.
+  bool odd = false;
+  if (p0 + KT > c) {
+    for (int e = lane; e < KT * CH; e += 32) {
+      const int row = e / CH;
+      uint32_t w[4];
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                   : "r"(vb + swz<D>(row, e % CH)));
+#pragma unroll
+      for (int u = 0; u < 4; u++)
+        odd |= (w[u] & 0x7F80u) == 0x7F80u || (w[u] & 0x7F800000u) == 0x7F800000u;
+    }
+    odd = __any_sync(0xFFFFFFFFu, odd);
+  }
+  if (odd) {
+    auto add = [](float w, float v, float &acc) {
+      acc = fabsf(v) < INFINITY ? fmaf(w, v, acc) : acc + v;
+    };
+#pragma unroll
+    for (int mt = 0; mt < MT; mt++) {
+      uint32_t vis[2];
+#pragma unroll
+      for (int hf = 0; hf < 2; hf++) {
+        const int x = rt * a.rstep + mt * 16 + hf * 8 + lane / 4;
+        vis[hf] = x < T * a.G ? visible_bits<KT>(a, x / a.G, q0, c, T, p0) & okb : 0u;
+      }
+#pragma unroll
+      for (int kn = 0; kn < KT / 8; kn++)
+        for (int kq = 0; kq < 4; kq++)
+#pragma unroll
+          for (int e = 0; e < 2; e++) {  // key 8·kn + 2·kq + e
+            const int src = (lane & ~3) | kq;
+            const float w0 = __shfl_sync(0xFFFFFFFFu, s[mt][kn][e], src);
+            const float w1 = __shfl_sync(0xFFFFFFFFu, s[mt][kn][2 + e], src);
+#pragma unroll
+            for (int n = 0; n < NT; n++) {
+              uint32_t v;
+              asm volatile("ld.shared.u32 %0, [%1];"
+                           : "=r"(v)
+                           : "r"(vb + swz<D>(8 * kn + 2 * kq + e, n) + 4 * (lane % 4)));
+              if ((vis[0] >> (8 * kn + 2 * kq + e)) & 1u) {
+                add(w0, bf16_lo(v), o[mt][n][0]);
+                add(w0, bf16_hi(v), o[mt][n][1]);
+              }
+              if ((vis[1] >> (8 * kn + 2 * kq + e)) & 1u) {
+                add(w1, bf16_lo(v), o[mt][n][2]);
+                add(w1, bf16_hi(v), o[mt][n][3]);
+              }
+            }
+          }
+    }
+  } else {
+#pragma unroll
+    for (int kk = 0; kk < KT / 16; kk++) {
+      uint32_t pa[MT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; mt++) {
+        pa[mt][0] = pack_bf16x2(s[mt][2 * kk][0], s[mt][2 * kk][1]);
+        pa[mt][1] = pack_bf16x2(s[mt][2 * kk][2], s[mt][2 * kk][3]);
+        pa[mt][2] = pack_bf16x2(s[mt][2 * kk + 1][0], s[mt][2 * kk + 1][1]);
+        pa[mt][3] = pack_bf16x2(s[mt][2 * kk + 1][2], s[mt][2 * kk + 1][3]);
+      }
+#pragma unroll
+      for (int n = 0; n < NT; n += 2) {
+        uint32_t b[4];
+        ldsm4t(vb + swz<D>(kk * 16 + (lane & 15), n + (lane >> 4)), b);
+#pragma unroll
+        for (int mt = 0; mt < MT; mt++) {
+          mma16816(o[mt][n], pa[mt], b[0], b[1]);
+          mma16816(o[mt][n + 1], pa[mt], b[2], b[3]);
+        }
+      }
+    }
+  }
+}
+
 template <int D, int MT, bool CL>
 __global__ void __launch_bounds__(kRowThreads, 2)
 k_tree_rows(TreeArgs a) {
