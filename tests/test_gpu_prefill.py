@@ -380,6 +380,13 @@ def test_prompt_room_in_the_table(kvc, room):
         go(kvc, t)
 
 
+@pytest.mark.parametrize("T,ctx,H,G,D", [([3, 20, 7], [3000, 2900, 3100], 64, 1, 64), ([9, 0, 40, 1], [2500, 9, 2400, 0], 80, 2, 64),
+                                         ([70, 33], [4000, 4100], 40, 4, 128)])
+def test_prompt_more_units_than_sms(kvc, T, ctx, H, G, D):
+    """More units of about a size than the GPU holds at once."""
+    go(kvc, Prompt(83, ctx, T, H, G, D, 16, pad=2))
+
+
 def test_prompt_equals_chain_rows(kvc):
     """The rows of a whole prompt are those of its pieces (within both bounds)."""
     t = Prompt(31, [0], [400], 2, 4, 128, 16).gpu()
