@@ -1,8 +1,8 @@
 // mma_ptx.cuh — building blocks of the kernels that stream paged rows into
-// tensor-core products (tree_attn.cu, attn_mass.cu): cp.async and mma.sync,
-// tcgen05 and TMA issued under a predicate, tensor maps of the pools and of
-// the queries, the shared-memory row layout, and block-wide sums and searches
-// over the requests of a batch.
+// tensor-core products (tree_attn.cu, attn_mass.cu, prompt_attn.cu, q8_attn.cu):
+// cp.async and mma.sync, tcgen05 and TMA issued under a predicate, tensor maps of
+// the pools and of the queries, the shared-memory row layout, and block-wide sums
+// and searches over the requests of a batch.
 #pragma once
 
 #include "tc_ptx.cuh"
