@@ -667,8 +667,8 @@ def _rows_ptr(t, row):
     if not t.is_cuda:
         raise ValueError("libkvc takes device tensors only")
     shape, strides = t.shape, t.stride()
-    if len(strides) == 2 and strides[1] == 1 and shape[1] == row and shape[0] > 1:
-        return t.data_ptr(), strides[0], shape[0]
+    if len(strides) == 2 and strides[1] == 1 and shape[1] == row:
+        return t.data_ptr(), strides[0] if shape[0] > 1 else row, shape[0]
     n = 1  # elements of a row so far, from its end
     for size, stride in zip(shape[:0:-1], strides[:0:-1]):
         if size != 1 and stride != n:
