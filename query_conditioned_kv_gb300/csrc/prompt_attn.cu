@@ -31,10 +31,10 @@
 //
 // Bound by the tensor core and by what hangs on its results: a pair of row tiles and 128
 // keys are 32 products of 64 cycles, and S(t + 1) waits for the end of the product that
-// reads P.  8192 tokens of 8 KV and 32 query heads, D 128: 414 us, 1.33 PFLOP/s, 69 % of
-// a library product's burst rate; 2048 behind 131072 3215 us, 1.36 PFLOP/s.  Without any
-// softmax the latter would take 2960, without the loads too no less: so neither is what a
-// step is spent on.  An issuer per row tile lets the two fall into step (3758 us), the
+// reads P.  8192 tokens of 8 KV and 32 query heads, D 128: 414 to 418 us, 1.32 PFLOP/s, 69
+// % of a library product's burst rate; 2048 behind 131072 3215 to 3250 us, 1.35 PFLOP/s.
+// Without any softmax the latter would take 2960, without the loads too no less: so neither
+// is what a step is spent on.  An issuer per row tile lets the two fall into step (3758 us), the
 // weights handed over 64 keys at a time cost 3380, two threads a row 3247.
 #include <float.h>
 
