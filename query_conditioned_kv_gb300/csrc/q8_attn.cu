@@ -30,7 +30,7 @@
 // scales, and a tile needs no maximum.
 //
 // One token, 8 KV and 32 query heads, D 128: 64 requests of up to 8192 140 us, 6.0 TB/s, 88 % of
-// a copy's rate; one of 4096 13.9, latency.  18 rows per KV head over two requests of 131072 125
+// a copy's rate; one of 4096 12.7, latency.  18 rows per KV head over two requests of 131072 125
 // us, 4.3 TB/s, bound by products and conversions.  Rows as the products' M took 166 and 179.
 #include <float.h>
 
@@ -739,15 +739,23 @@ k_q8_rows(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
       for (int e = (int)cluster_rank() * kQ8Threads + tid; e < n_rows * (D / 4); e += n_cl * kQ8Threads) {
         const int row = e / (D / 4), d4 = (e % (D / 4)) * 4;
         float mx = -INFINITY;
-#pragma unroll 4
-        for (int k = 0; k < n_cl; k++) mx = fmaxf(mx, ld_cluster_f2(mapa_u32(ml_at + row * 8, k)).x);
+        float2 mls[16];  // (asked for at once)
+        float4 vs[16];
+#pragma unroll
+        for (int k = 0; k < 16; k++)
+          if (k < n_cl) {
+            mls[k] = ld_cluster_f2(mapa_u32(ml_at + row * 8, k));
+            vs[k] = ld_cluster_f4(mapa_u32(o_at + (row * D + d4) * 4, k));
+            mx = fmaxf(mx, mls[k].x);
+          }
         const float base = mx == -INFINITY ? 0.f : mx;
         float sum = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int k = 0; k < n_cl; k++) {
-          const float2 ml = ld_cluster_f2(mapa_u32(ml_at + row * 8, k));
-          const float4 v = ld_cluster_f4(mapa_u32(o_at + (row * D + d4) * 4, k));
+#pragma unroll
+        for (int k = 0; k < 16; k++) {
+          if (k >= n_cl) break;
+          const float2 ml = mls[k];
+          const float4 v = vs[k];
           const float f = ex2(ml.x - base);
           sum = fmaf(ml.y, f, sum);
           acc.x = fmaf(v.x, f, acc.x);
@@ -812,24 +820,28 @@ bool rows8_map(CUtensorMap *m, const void *pool, int64_t rows, int D, int box) {
 }
 
 // CTAs of the cluster that shares a unit, 0: the tiles are dealt out and joined by a second
-// launch.  In tiles that a CTA takes one after another, with what the two forms cost besides
-// (as tree_cluster in tree_attn.cu): dealt out, an even share and 17; clusters, a share for
-// every wave of CTAs, 8 a wave after the first, and 3.5.  One token, 8 KV heads, D 128: one
-// request of 1K 8.4 us by clusters of 8 and 9.2 dealt out, of 16K 18.8 and 18.2; 4 of 8K
-// 19.4 by clusters of 8 and 21.8; 16 of 4K 32.1 by two and 34.6; 64 of 1K 47 by two and 38.9.
-int q8_cluster(const Q8Args &a, int max_rt) {
+// launch.  In the time of a tile that a CTA works on alone (1.05 us; `beat` tiles are what the
+// memory takes to give one to every CTA that the GPU holds).  Dealt out: an even share, 10 for
+// the two launches, 4.5 for every unit that a CTA meets.  Clusters: waves of CTAs, each its
+// share of a unit's tiles, 6 to begin and end where it waits for itself, 4 where for memory.
+// One token, 8 KV and 32 query heads, D 128, in us dealt out and by 1, 2, 4, 8 and 16: one
+// request of 200 9, 9, 8, 6.5, 6.6, 8; of 4096 12, 42, 25, 16, 12, 11; 4 of 8192 22, 77, 42,
+// 25, 19, 28; 16 of 4096 35, 44, 32, 45, 45, 76; 57 of 1024 (a CTA each) 29, 26, 33, 54, 85,
+// 178; 64 of 1024 36, 43, 45, 58, 97, 200; 128 of 200 38, 30, 46, 72, 142, 369.
+int q8_cluster(const Q8Args &a, int max_rt, int D) {
   if (max_rt > 1 || a.rows > 16) return 0;  // (a cluster takes one row tile; more rows leave it to the even deal)
-  const double units = (double)a.n_req * a.H, sms = device_sm_count(), per = q8_ctas(a.rows / 8);
+  const double units = (double)a.n_req * a.H, all = q8_ctas(a.rows / 8) * (double)device_sm_count();
   const double kt = ceil((double)a.max_blocks8 * a.BS / (kQ8Warps * kQ8Keys)) +
                     ceil((double)a.max_blocks * a.BS / a.tile);
+  const double beat = 2.33 * D / 128, even = units * kt / all;
   int best = 0;
-  double least = units * kt / (per * sms) + 17;
-  for (int S = 1; S <= 16 && S <= kt; S *= 2) {
+  double least = std::max(even * beat, ceil(even)) + 10 + 4.5 * units / all;
+  for (int S = 1; S <= 16 && S < 2 * kt; S *= 2) {
     // (a GPC's 16 to 20 SMs hold fewer large clusters)
-    const double room = per * sms * (S == 16 ? 0.42 : S == 8 ? 0.84 : S == 4 ? 0.95 : 1);
-    const double full = units * S / room, waves = ceil(full);
-    const double share = waves > 1 ? full + 0.6 * (waves - full) : 1;
-    const double cost = share * ceil(kt / S) * (S == 16 ? 1.25 : 1) + 8 * (waves - 1) + 3.5;
+    const double room = all * (S == 16 ? 0.42 : S == 8 ? 0.84 : S == 4 ? 0.95 : 1);
+    const double share = ceil(kt / S), waves = units * S / room, rest = waves - floor(waves);
+    auto wave = [&](double full) { return std::max(share + 6, full * room / all * beat * share + 4); };
+    const double cost = floor(waves) * wave(1) + (rest > 0 ? wave(rest) : 0) + (S == 16 ? 1.5 : 0);
     if (cost < least) {
       least = cost;
       best = S;
@@ -910,7 +922,7 @@ cudaError_t launch_q8_attn(const uint16_t *q, const uint8_t *k8, const uint8_t *
   // (a box's rows lie in one block, and a row's number fits the box's coordinate)
   // (64 requests of 4096: pages of 32 and 16 95 us, of 8 98, of 12 and 4 by cp.async 99 and 100)
   a.box8 = n_blocks8 * H * BS > INT32_MAX ? 0 : BS % 32 == 0 ? 32 : BS % 16 == 0 ? 16 : BS % 8 == 0 ? 8 : 0;
-  const int cluster = q8_cluster(a, max_rt);
+  const int cluster = q8_cluster(a, max_rt, D);
   const cudaError_t e = D == 128 ? launch_q8<128>(a, cluster, s) : launch_q8<64>(a, cluster, s);
   if (e != cudaSuccess || cluster) return e;
   return launch_join(a, D, max_rt, s);
