@@ -33,7 +33,7 @@ struct Q8PackArgs {
   float *kscale, *vscale;
   const int32_t *src, *dst;
   int32_t *status;
-  int64_t n_blocks, n_blocks8;
+  int64_t n_slots, n_blocks, n_blocks8;
   int64_t units, groups;  // heads' blocks in all, CTAs' worth of them
   int n, H, BS;
 };
@@ -72,7 +72,8 @@ k_q8_pack(Q8PackArgs a) {
     u.live = src >= 0 && src < a.n_blocks && dst >= 0 && dst < a.n_blocks8;
     if (!u.live && !(src < 0 && dst < 0) && part == 0) record_error(a.status, KVC_ERR_BOUNDS);
     u.at = ((int64_t)l * a.n_blocks8 + dst) * a.H + h;
-    u.from = (u.v ? a.vpool : a.kpool) + (((int64_t)l * a.n_blocks + src) * a.BS * a.H + h) * D;
+    // (a layer has n_slots rows, of which the last few may make no whole block)
+    u.from = (u.v ? a.vpool : a.kpool) + ((l * a.n_slots + (int64_t)src * a.BS) * a.H + h) * D;
     return u;
   };
   uint4 nx[kPackLoads];
@@ -160,7 +161,7 @@ cudaError_t launch_q8_pack(const uint16_t *kpool, const uint16_t *vpool, int64_t
   Q8PackArgs a{};
   a.kpool = kpool, a.vpool = vpool, a.k8 = k8, a.v8 = v8, a.kscale = kscale, a.vscale = vscale;
   a.src = src, a.dst = dst, a.status = status;
-  a.n_blocks = n_slots / BS, a.n_blocks8 = n_blocks8, a.H = H, a.BS = BS;
+  a.n_slots = n_slots, a.n_blocks = n_slots / BS, a.n_blocks8 = n_blocks8, a.H = H, a.BS = BS;
   const int warps = (BS * D / 8 + kPackLoads * 32 - 1) / (kPackLoads * 32);
   const int wpu = warps <= 1 ? 1 : warps <= 2 ? 2 : 4;
   a.n = n;

@@ -212,3 +212,14 @@ def test_captured_step_repeats():
             assert torch.equal(getattr(a.ev, n), getattr(b.ev, n))
     assert torch.equal(a.k8, b.k8) and torch.equal(a.ks, b.ks) and torch.equal(a.bt, b.bt)
     assert int(a.ev.len8.sum()) > 0
+
+
+def test_pools_with_spare_rows():
+    """A step on pools with a few rows behind the last whole block: every layer's blocks move."""
+    s = Serving(8, recent=0)
+    s.n_slots += 3
+    s.ev.n_slots = s.n_slots
+    s.k, s.v = (torch.zeros(s.L, s.n_slots, s.H, s.D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    s.step([30, 25, 8], prompt=True)
+    for _ in range(2):
+        s.step([3, 1, 1])

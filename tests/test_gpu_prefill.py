@@ -668,6 +668,23 @@ def test_pack_left_out_and_bad_pairs(kvc):
         t.check(left_out={4})
 
 
+@pytest.mark.parametrize("spare", [1, 3, 15])
+@pytest.mark.parametrize("L", [1, 2, 5])
+def test_pack_spare_rows_behind_the_blocks(kvc, L, spare):
+    """Pools whose rows make no whole number of blocks: a layer begins n_slots rows after the last."""
+    t = Pack(11 + L, 4, L, 3, 64, 16).gpu()
+    n = t.n_src * t.BS
+    for name in ("k", "v"):
+        pool = torch.full((L, n + spare, t.H, t.D), NAN, dtype=torch.bfloat16, device=DEV)
+        pool[:, :n] = t.d[name]
+        t.d[name] = pool
+    d = t.d
+    kvc.kvc_q8_pack(d["k"], d["v"], n + spare, d["k8"], d["v8"], d["ks"], d["vs"], t.n_dst, d["src"], d["dst"],
+                    t.n, L, t.H, t.D, t.BS, d["status"])
+    assert status(kvc, d["status"]) == 0
+    t.check()
+
+
 # ---------------------------------------------------------- 8-bit attention
 
 class Q8(Batch):
