@@ -700,16 +700,14 @@ class HistoryEvent:
         self.dev_status = torch.zeros(1, **i32)
 
     def begin(self, q_off, pos=None, stream=None):
-        """A step whose requests' new tokens are q_off's, at the positions that follow
-        t_end, or at pos [n_q] (a drafted tree's depths)."""
+        """A step whose requests' new tokens are q_off's: at the positions that follow t_end,
+        or pos [n_q] behind it (a drafted tree's depths: 0 for the next position)."""
         self.q_off = q_off
         with _on(stream, self.device):
-            if pos is not None:
-                self.pos.copy_(pos)
-                return
             x = torch.arange(self.n_q, dtype=torch.int32, device=self.device)
             r = torch.bucketize(x, q_off[1:], right=True, out_int32=True).clamp_(max=self.n_req - 1)
-            self.pos.copy_(self.t_end[r] + x - q_off[r])
+            self.pos.copy_(x - q_off[r] if pos is None else pos)
+            self.pos.add_(self.t_end[r])
 
     def write(self, layer, q, k, v, kpool, vpool, block_table, wq=None, wk=None, k_raw=None,
               stream=None):
@@ -743,8 +741,9 @@ class HistoryEvent:
 
     def finish(self, kpool, vpool, block_table, k8, v8, kscale, vscale, table8, n_rows=None,
                stream=None):
-        """The step after the last layer: n_rows [n_req] of the new rows (None: all) join the
-        cache, full blocks move to 8 bits, all layers."""
+        """The step after the last layer: the first n_rows [n_req] of a request's new rows (None:
+        all) join the cache, full blocks move to 8 bits, all layers.  The accepted nodes of
+        a drafted tree are brought to the front before (kvc_tree_commit, ctx_len = ctx)."""
         BS = self.BS
         with _on(stream, self.device):
             n = self.q_off[1:] - self.q_off[:-1] if n_rows is None else n_rows

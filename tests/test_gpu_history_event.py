@@ -223,3 +223,90 @@ def test_pools_with_spare_rows():
     s.step([30, 25, 8], prompt=True)
     for _ in range(2):
         s.step([3, 1, 1])
+
+
+def drafted(rng, T):
+    """A tree of T nodes (parents before children, -1: a root) and one accepted path of it."""
+    parent = [int(rng.integers(-1 if i % 3 == 0 else max(0, i - 3), i)) if i else -1 for i in range(T)]
+    chain = lambda i: [] if i < 0 else chain(parent[i]) + [i]  # noqa: E731
+    lines = [chain(i) for i in range(T)]
+    return lines, (lines[int(rng.integers(0, T))] if T else [])
+
+
+def draft_step(s, rng, T, tree=True):
+    """Drafted nodes through begin(pos), attend(tree_mask), kvc_tree_commit and finish(n_rows): rotations,
+    rows and attention of the step, the accepted rows' places after it.  Not a tree: a chain of which the
+    first few are accepted."""
+    import query_conditioned_kv_gb300 as kvc
+    q_off, x = s.inputs(T)
+    trees = [drafted(rng, t) for t in T]
+    if not tree:
+        trees = [([list(range(i + 1)) for i in range(t)], list(range(int(rng.integers(0, t + 1))))) for t in T]
+    words = (s.ev.max_rows + 31) // 32
+    mask = np.zeros((s.n_q, words), np.uint32)
+    depth = np.zeros(s.n_q, int)
+    for r, (lines, _) in enumerate(trees):
+        for i, line in enumerate(lines):
+            depth[q_off[r] + i] = len(line) - 1
+            for j in line:
+                mask[q_off[r] + i, j // 32] |= np.uint32(1 << (j % 32))
+    qd, xd, path = i32(q_off), x.to(DEV), np.zeros((s.n_req, 8), int)
+    n_path = [min(len(p), 8) for _, p in trees]
+    for r, (_, p) in enumerate(trees):
+        path[r, :n_path[r]] = p[:n_path[r]]
+    s.ev.begin(qd, pos=i32(depth))
+    for l in range(s.L):
+        s.ev.write(l, *s.parts(xd[l]), s.k[l], s.v[l], s.bt, s.wq, s.wk)
+        s.ev.attend(l, s.k[l], s.v[l], s.bt, s.k8[l], s.v8[l], s.ks[l], s.vs[l], s.t8d,
+                    tree_mask=i32(mask.view(np.int32)) if tree else None)
+    torch.cuda.synchronize()
+    tab, bt = ref.rope_table(200, s.D), s.bt.cpu().numpy()
+    seen = [len(s.rows[r][0]) for r in range(s.n_req)]
+    took = [[[torch.zeros(s.L, s.H, s.D, dtype=torch.bfloat16) for _ in range(n)] for n in n_path] for _ in (0, 1)]
+    for l in range(s.L):
+        q, k, v = (p.reshape(s.n_q, -1, s.D) for p in s.parts(x[l]))
+        for r in range(s.n_req):
+            a, b = q_off[r], q_off[r + 1]
+            at = tree_ref.slots(bt[r], s.BS, s.ctx[r] + b - a)[s.ctx[r]:]
+            for y, w, got in ((q, s.wq, s.ev.q[l, a:b]), (k, s.wk, s.k[l].cpu()[at])):
+                y, rel = ref.normed(y[a:b], w.cpu(), EPS)
+                inside(got, *ref.rotated(y, rel, tab[seen[r] + depth[a:b]]), "rotated rows")
+            assert torch.equal(s.v[l].cpu()[at], v[a:b])
+            for i, j in enumerate(path[r, :n_path[r]]):
+                took[0][r][i][l], took[1][r][i][l] = s.k[l].cpu()[at[j]], v[a + j]
+        o, ls, ob, lb = ref.q8(s.ev.q[l].cpu(), s.k8[l].cpu().view(F8).float(), s.v8[l].cpu().view(F8).float(),
+                               s.ks[l].cpu(), s.vs[l].cpu(), s.t8, s.len8, s.k[l].cpu(), s.v[l].cpu(), bt, s.BS,
+                               s.ctx, q_off, mask, s.H, s.ev.scale)
+        n = int(q_off[-1])
+        inside(s.ev.out[l, :n], o[:n], ob[:n], "out")
+        inside(s.ev.lse[l, :n], ls[:n], lb[:n], "lse")
+    if tree:
+        kvc.kvc_tree_commit(s.k, s.v, s.n_slots, s.bt, s.max_blocks, s.ev.ctx, qd, i32(path), i32(n_path), 8,
+                            s.n_req, s.L, s.H, s.D, s.BS, torch.zeros(s.n_req, dtype=torch.int32, device=DEV),
+                            None, None, s.ev.dev_status)
+    s.ev.finish(s.k, s.v, s.bt, s.k8, s.v8, s.ks, s.vs, s.t8d, n_rows=i32(n_path))
+    torch.cuda.synchronize()
+    assert kvc.kvc_device_status(s.ev.dev_status) == 0
+    for r in range(s.n_req):
+        for kind in (0, 1):
+            s.rows[r][kind] += took[kind][r]
+        s.ctx[r] += n_path[r]
+        move = min(max(0, s.ctx[r] - s.recent) // s.BS, s.ev.max_move, s.mb8 - s.len8[r] // s.BS)
+        s.ctx[r] -= move * s.BS
+        s.len8[r] += move * s.BS
+    assert s.ev.ctx.tolist() == list(s.ctx) and s.ev.len8.tolist() == list(s.len8)
+    assert s.ev.t_end.tolist() == [len(r[0]) for r in s.rows]
+    s.check_residence()
+
+
+@pytest.mark.parametrize("tree", [True, False])
+@pytest.mark.parametrize("D,BS", [(64, 8), (128, 16)])
+def test_drafted_steps(tree, D, BS):
+    """Drafted trees, or chains of which a part is accepted, over history and cache, and plain steps
+    after them: every node's rotation is that of its depth behind the tokens seen."""
+    s, rng = Serving(9 + D, D=D, BS=BS, recent=3, max_blocks=-(-88 // BS)), np.random.default_rng(D + tree)
+    s.step([37, 0, 19], prompt=True)
+    for T in ([7, 3, 12], [1, 9, 0], [20, 5, 4]):
+        draft_step(s, rng, T, tree)
+        s.step([1, 2, 1])
+    assert int(s.ev.len8.max()) > 0
