@@ -642,7 +642,6 @@ class TreeDecodeEvent:
                 n.copy_(self.n_out)
 
 
-
 class HistoryEvent:
     """Buffers and calls of prompts and decoding on a paged KV cache whose older blocks
     are held in 8 bits.
@@ -664,9 +663,11 @@ class HistoryEvent:
     `max_blocks` has room for the recent rows, a block, and what one step adds beyond
     what it moves.
 
-    The launches depend on the constructor's sizes only, so a step can be captured in a
-    CUDA graph.  ``stream`` is None (the current stream), a Stream or a raw handle, as in
-    the library's calls; the buffers belong to the stream they are first used on."""
+    The constructor's n_q and max_rows are the largest step's; ``begin`` takes those of the
+    step at hand, which its launches are planned by (one event serves long prompts and
+    single tokens).  The launches depend on these host sizes only, so a step can be captured
+    in a CUDA graph.  ``stream`` is None (the current stream), a Stream or a raw handle, as
+    in the library's calls; the buffers belong to the stream they are first used on."""
 
     def __init__(self, n_req: int, max_blocks: int, max_blocks8: int, block_size: int, L: int,
                  H: int, Hq: int, D: int, n_slots: int, n_blocks8: int, n_q: int, max_rows: int,
@@ -694,26 +695,36 @@ class HistoryEvent:
         with torch.cuda.device(dev):
             kvc_rope_table(self.rope, n_pos, 0, D, theta)
         self.pos = torch.empty(n_q, **i32)
-        self.tree_rows = min(max_rows, TREE_MAX_NODES)
-        self.ws = _ws(kvc_q8_attn_workspace_size(n_req, max_blocks8, max_blocks, self.tree_rows, H,
-                                                 Hq, D, block_size), dev)
+        # (steps of fewer rows need no more)
+        self.ws = _ws(kvc_q8_attn_workspace_size(n_req, max_blocks8, max_blocks,
+                                                 min(max_rows, TREE_MAX_NODES), H, Hq, D, block_size), dev)
         self.dev_status = torch.zeros(1, **i32)
+        self.step_q, self.step_rows = n_q, max_rows
 
-    def begin(self, q_off, pos=None, stream=None):
+    def begin(self, q_off, pos=None, stream=None, n_q: Optional[int] = None,
+              max_rows: Optional[int] = None):
         """A step whose requests' new tokens are q_off's: at the positions that follow t_end,
-        or pos [n_q] behind it (a drafted tree's depths: 0 for the next position)."""
-        self.q_off = q_off
+        or pos [n_q] behind it (a drafted tree's depths: 0 for the next position).  n_q: the
+        rows of the step's buffers, max_rows: the most that a request brings (None: the
+        constructor's); a request that brings more is recorded as KVC_ERR_BOUNDS and gets no
+        attention."""
+        n = self.n_q if n_q is None else n_q
+        most = min(self.max_rows, n) if max_rows is None else max_rows
+        if not (1 <= n <= self.n_q and 1 <= most <= self.max_rows):
+            raise ValueError(f"HistoryEvent.begin: a step of {n} rows, {most} of a request, in an event made "
+                             f"for {self.n_q} and {self.max_rows}")
+        self.q_off, self.step_q, self.step_rows = q_off, n, most
         with _on(stream, self.device):
-            x = torch.arange(self.n_q, dtype=torch.int32, device=self.device)
+            x = torch.arange(n, dtype=torch.int32, device=self.device)
             r = torch.bucketize(x, q_off[1:], right=True, out_int32=True).clamp_(max=self.n_req - 1)
-            self.pos.copy_(x - q_off[r] if pos is None else pos)
-            self.pos.add_(self.t_end[r])
+            self.pos[:n].copy_(x - q_off[r] if pos is None else pos)
+            self.pos[:n].add_(self.t_end[r])
 
     def write(self, layer, q, k, v, kpool, vpool, block_table, wq=None, wk=None, k_raw=None,
               stream=None):
-        """One layer's projections q, k, v ([n_q][heads·D], any row stride); the layer's
-        pools.  The rotated queries are in self.q[layer]."""
-        kvc_qkv_rope(q, k, v, self.n_q, wq, wk, self.eps, self.rope, self.n_pos, self.pos,
+        """One layer's projections q, k, v ([the step's n_q][heads·D], any row stride); the
+        layer's pools.  The rotated queries are in self.q[layer]."""
+        kvc_qkv_rope(q, k, v, self.step_q, wq, wk, self.eps, self.rope, self.n_pos, self.pos,
                      self.q_off, self.ctx, self.n_req, block_table, self.max_blocks, kpool, vpool,
                      self.n_slots, self.H, self.Hq, self.D, self.BS, self.q[layer], k_raw,
                      self.dev_status, stream)
@@ -722,10 +733,10 @@ class HistoryEvent:
         """Causal attention of the new rows over cache and new rows, of requests that hold
         nothing in 8 bits."""
         kvc_prompt_attn(self.q[layer], kpool, vpool, self.n_slots, block_table, self.max_blocks,
-                        self.ctx, self.q_off, self.n_req, self.n_q, self.max_rows, self.H, self.Hq,
-                        self.D, self.BS, self.scale, self.out[layer], self.lse[layer],
+                        self.ctx, self.q_off, self.n_req, self.step_q, self.step_rows, self.H,
+                        self.Hq, self.D, self.BS, self.scale, self.out[layer], self.lse[layer],
                         self.dev_status, stream)
-        return self.out[layer]
+        return self.out[layer, :self.step_q]
 
     def attend(self, layer, kpool, vpool, block_table, k8, v8, kscale, vscale, table8,
                tree_mask=None, stream=None):
@@ -734,10 +745,11 @@ class HistoryEvent:
         words = 0 if tree_mask is None else tree_mask.shape[1]
         kvc_q8_attn(self.q[layer], k8, v8, kscale, vscale, self.n_blocks8, table8,
                     self.max_blocks8, self.len8, kpool, vpool, self.n_slots, block_table,
-                    self.max_blocks, self.ctx, self.q_off, tree_mask, words, self.n_req, self.n_q,
-                    self.tree_rows, self.H, self.Hq, self.D, self.BS, self.scale,
-                    self.out[layer], self.lse[layer], self.ws, self.dev_status, stream)
-        return self.out[layer]
+                    self.max_blocks, self.ctx, self.q_off, tree_mask, words, self.n_req,
+                    self.step_q, min(self.step_rows, TREE_MAX_NODES), self.H, self.Hq, self.D,
+                    self.BS, self.scale, self.out[layer], self.lse[layer], self.ws,
+                    self.dev_status, stream)
+        return self.out[layer, :self.step_q]
 
     def finish(self, kpool, vpool, block_table, k8, v8, kscale, vscale, table8, n_rows=None,
                stream=None):

@@ -310,3 +310,67 @@ def test_drafted_steps(tree, D, BS):
         draft_step(s, rng, T, tree)
         s.step([1, 2, 1])
     assert int(s.ev.len8.max()) > 0
+
+
+def test_steps_of_their_own_sizes():
+    """One event for prompts and for single tokens: a step's buffers and launches go by the sizes that
+    begin is given, and give what the largest ones give."""
+    a, b = (Serving(10, n_q=70, max_rows=40) for _ in range(2))
+    for s in (a, b):
+        s.step([37, 0, 19], prompt=True)
+    for T in ([1, 1, 1], [2, 0, 1], [1, 1, 1], [4, 4, 4], [1, 1, 1], [0, 1, 0]):
+        n, most = sum(T), max(T)
+        q_off, x = a.inputs(T)
+        qd, xd = i32(q_off), x[:, :n].contiguous().to(DEV)
+        a.ev.begin(qd, n_q=n, max_rows=most)
+        for l in range(a.L):
+            a.ev.write(l, *a.parts(xd[l]), a.k[l], a.v[l], a.bt, a.wq, a.wk)
+            got = a.ev.attend(l, a.k[l], a.v[l], a.bt, a.k8[l], a.v8[l], a.ks[l], a.vs[l], a.t8d)
+            assert got.shape == (n, a.Hq, a.D) and got.data_ptr() == a.ev.out[l].data_ptr()
+        torch.cuda.synchronize()
+        a.check_rows(T, q_off, x)
+        a.check_attention(T, q_off)
+        a.finish()
+        b.launch(qd, x.to(DEV), False)
+        b.finish()
+        torch.cuda.synchronize()
+        import query_conditioned_kv_gb300 as kvc
+        for s in (a, b):
+            assert kvc.kvc_device_status(s.ev.dev_status) == 0
+        a.ctx, a.len8 = a.ev.ctx.cpu().numpy(), a.ev.len8.cpu().numpy()
+        a.check_residence()
+        for name in ("ctx", "len8", "t_end"):
+            assert torch.equal(getattr(a.ev, name), getattr(b.ev, name))
+    # a prompt of a few rows again, in an event that has taken steps of other sizes
+    s = Serving(11)
+    s.step([20, 33, 1], prompt=True)
+    q_off, x = s.inputs([0, 0, 5])
+    s.ev.begin(i32(q_off), n_q=5, max_rows=5)
+    for l in range(s.L):
+        s.ev.write(l, *s.parts(x[l, :5].to(DEV)), s.k[l], s.v[l], s.bt, s.wq, s.wk)
+        s.ev.prompt(l, s.k[l], s.v[l], s.bt)
+    torch.cuda.synchronize()
+    s.check_rows([0, 0, 5], q_off, x)
+    s.check_attention([0, 0, 5], q_off)
+    s.finish()
+    assert s.ev.t_end.tolist() == [20, 33, 6]
+
+
+def test_steps_past_the_largest_are_refused():
+    import query_conditioned_kv_gb300 as kvc
+    s = Serving(12)
+    q_off = i32([0, 2, 3, 4])
+    for n, most in ((71, 3), (0, 3), (4, 41), (4, 0)):
+        with pytest.raises(ValueError, match="event made"):
+            s.ev.begin(q_off, n_q=n, max_rows=most)
+    # a request that brings more rows than the step's is left out and recorded
+    x = s.inputs([2, 1, 1])[1].to(DEV)
+    s.ev.out.fill_(7.0)
+    s.ev.begin(q_off, n_q=4, max_rows=1)
+    s.ev.write(0, *s.parts(x[0, :4]), s.k[0], s.v[0], s.bt)
+    torch.cuda.synchronize()
+    assert kvc.kvc_device_status(s.ev.dev_status) == 0
+    s.ev.attend(0, s.k[0], s.v[0], s.bt, s.k8[0], s.v8[0], s.ks[0], s.vs[0], s.t8d)
+    torch.cuda.synchronize()
+    assert kvc.kvc_device_status(s.ev.dev_status) == 7
+    assert bool((s.ev.out[0, :2] == 7.0).all()) and not bool((s.ev.out[0, 2:4] == 7.0).any(-1).all())

@@ -113,6 +113,14 @@ def test_workspace_query(kvc):
         assert kvc.kvc_q8_attn_workspace_size(*bad) == 0
 
 
+def test_workspace_of_fewer_rows_is_no_larger(kvc):
+    """A buffer made for a call of many rows serves calls of fewer (what a step's sizes rely on)."""
+    for n_req, mb8, mb, H, G, D in [(1, 8, 4, 1, 1, 64), (3, 200, 20, 2, 4, 128), (64, 512, 64, 8, 4, 128),
+                                    (2, 1, 1, 4, 33, 64), (500, 3, 2, 1, 256, 128), (1, 8192, 9, 8, 6, 128)]:
+        sizes = [kvc.kvc_q8_attn_workspace_size(n_req, mb8, mb, t, H, H * G, D, 16) for t in range(1, 1025)]
+        assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+
+
 def test_binding_refuses_wrong_rows(kvc):
     """Rows of a fused projection may be strided; columns may not, and host tensors are refused."""
     t = torch.zeros(4, 256)
