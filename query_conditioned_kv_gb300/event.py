@@ -700,6 +700,9 @@ class HistoryEvent:
                                                  min(max_rows, TREE_MAX_NODES), H, Hq, D, block_size), dev)
         self.dev_status = torch.zeros(1, **i32)
         self.step_q, self.step_rows = n_q, max_rows
+        # ctx as prompt takes it: −1, which no call accepts, where new rows have a history before them
+        self._prompt_ctx = torch.zeros(n_req, **i32)
+        self._refused = torch.full((n_req,), -1, **i32)
 
     def begin(self, q_off, pos=None, stream=None, n_q: Optional[int] = None,
               max_rows: Optional[int] = None):
@@ -719,6 +722,8 @@ class HistoryEvent:
             r = torch.bucketize(x, q_off[1:], right=True, out_int32=True).clamp_(max=self.n_req - 1)
             self.pos[:n].copy_(x - q_off[r] if pos is None else pos)
             self.pos[:n].add_(self.t_end[r])
+            held = (self.len8 > 0) & (q_off[1:] > q_off[:-1])
+            torch.where(held, self._refused, self.ctx, out=self._prompt_ctx)
 
     def write(self, layer, q, k, v, kpool, vpool, block_table, wq=None, wk=None, k_raw=None,
               stream=None):
@@ -731,9 +736,10 @@ class HistoryEvent:
 
     def prompt(self, layer, kpool, vpool, block_table, stream=None):
         """Causal attention of the new rows over cache and new rows, of requests that hold
-        nothing in 8 bits."""
+        nothing in 8 bits.  A request with new rows behind a history is recorded as
+        KVC_ERR_BOUNDS and its rows are left alone (attend takes it)."""
         kvc_prompt_attn(self.q[layer], kpool, vpool, self.n_slots, block_table, self.max_blocks,
-                        self.ctx, self.q_off, self.n_req, self.step_q, self.step_rows, self.H,
+                        self._prompt_ctx, self.q_off, self.n_req, self.step_q, self.step_rows, self.H,
                         self.Hq, self.D, self.BS, self.scale, self.out[layer], self.lse[layer],
                         self.dev_status, stream)
         return self.out[layer, :self.step_q]

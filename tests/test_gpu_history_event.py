@@ -374,3 +374,37 @@ def test_steps_past_the_largest_are_refused():
     torch.cuda.synchronize()
     assert kvc.kvc_device_status(s.ev.dev_status) == 7
     assert bool((s.ev.out[0, :2] == 7.0).all()) and not bool((s.ev.out[0, 2:4] == 7.0).any(-1).all())
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_prompt_behind_a_history_is_recorded(captured):
+    """prompt does not see what lies in 8 bits: a request with new rows behind a history is recorded and
+    left alone, the others get their attention; a history without new rows is nothing to record."""
+    import query_conditioned_kv_gb300 as kvc
+    s = Serving(13, recent=0)
+    s.step([37, 0, 5], prompt=True)          # 32, 0 and 0 positions in 8 bits
+    assert s.len8.tolist() == [32, 0, 0]
+    T = [0, 9, 3]
+    q_off, x = s.inputs(T)
+    s.ev.out.fill_(7.0)
+    qd, xd, graph = i32(q_off), x.to(DEV), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    if captured:
+        with torch.cuda.graph(graph):
+            s.launch(qd, xd, True)
+        graph.replay()
+    else:
+        s.launch(qd, xd, True)
+    torch.cuda.synchronize()
+    assert kvc.kvc_device_status(s.ev.dev_status) == 0
+    s.check_rows(T, q_off, x)
+    s.check_attention(T, q_off)
+    qd.copy_(i32([0, 4, 4, 7]))
+    s.ev.out.fill_(7.0)
+    if captured:
+        graph.replay()
+    else:
+        s.launch(qd, xd, True)
+    torch.cuda.synchronize()
+    assert kvc.kvc_device_status(s.ev.dev_status) == 7
+    assert bool((s.ev.out[:, :4] == 7.0).all()) and bool((s.ev.out[:, 4:7] != 7.0).any(-1).all())
