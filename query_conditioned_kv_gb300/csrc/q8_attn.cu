@@ -57,6 +57,7 @@ constexpr float kQ8Most = 32768.f;     // weight, and sum of a thread's four, th
 constexpr float kQ8Round = 1048576.f;  // |reference| from which logits are rounded before the difference
 
 struct Q8Args : TreeArgs {
+  static constexpr bool kMeans = true;  // a sum of values times 2^8 to 2^15 may pass fp32
   const uint8_t *k8, *v8;
   const float *kscale, *vscale;
   const int32_t *table8, *len8;
@@ -679,15 +680,16 @@ k_q8_rows(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
         float sum = l[nr][e];
 #pragma unroll
         for (int o2 = 4; o2 < 32; o2 <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o2);
-        // O on the sum's reference
-        const float f = ex2(off[nr][e]);
+        // O, on its own reference so far, becomes the mean of the warp's values: sums on the
+        // softmax's reference would pass fp32 where |v| passes 2^113
+        const float inv = sum == 0.f ? 0.f : 1.f / sum, f = ex2(off[nr][e]);
         const int row = 8 * nr + 2 * quad + e;
         if (g8 == 0) ml_s[warp * R + row] = make_float2(ref[nr][e] == kQ8Unset ? -INFINITY : ref[nr][e], sum);
 #pragma unroll
         for (int n = 0; n < CH8; n++)
 #pragma unroll
           for (int hf = 0; hf < 2; hf++)
-            o_s[row * D + ((16 * n + 8 * hf + g8) ^ (quad << 3))] = o[n][nr][2 * hf + e] * f;
+            o_s[row * D + ((16 * n + 8 * hf + g8) ^ (quad << 3))] = o[n][nr][2 * hf + e] * inv * f;
       }
     __syncthreads();
     const bool whole = !CL && t0 == 0 && t1 == n_kt;
@@ -698,15 +700,21 @@ k_q8_rows(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
 #pragma unroll
       for (int w = 0; w < kQ8Warps; w++) mx = fmaxf(mx, ml_s[w * R + row].x);
       const float base = mx == -INFINITY ? 0.f : mx;
-      float sum = 0.f;
+      float sum = 0.f, share[kQ8Warps];
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kQ8Warps; w++) {
+        const float2 ml = ml_s[w * R + row];
+        share[w] = ml.y == 0.f ? 0.f : ml.y * ex2(ml.x - base);
+        sum += share[w];
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
       for (int w = 0; w < kQ8Warps; w++) {
         const float2 ml = ml_s[w * R + row];
         // (this warp saw nothing of the row; logits that are all NaN leave a NaN sum)
         if (ml.x == -INFINITY && ml.y == 0.f) continue;
-        const float f = ex2(ml.x - base);
-        sum = fmaf(ml.y, f, sum);
+        const float f = share[w] * inv;
         const float4 v = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(sm) +
                                                            (w * R + row) * D + (d4 ^ (((row >> 1) & 3) << 3)));
         acc.x = fmaf(v.x, f, acc.x);
@@ -717,9 +725,8 @@ k_q8_rows(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
       if (whole) {
         const int x = rt * a.rstep + row;
         const int64_t qr = (int64_t)(q0 + x / a.G) * a.Hq + h * a.G + x % a.G;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
         *reinterpret_cast<uint2 *>(a.out + qr * D + d4) =
-            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+            make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
         if (d4 == 0) a.lse[qr] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
       } else if (CL) {
         *reinterpret_cast<float4 *>(sm + S::kClO + (row * D + d4) * 4) = acc;
@@ -754,10 +761,15 @@ k_q8_rows(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
 #pragma unroll
         for (int k = 0; k < 16; k++) {
           if (k >= n_cl) break;
-          const float2 ml = mls[k];
+          mls[k].y *= ex2(mls[k].x - base);
+          sum += mls[k].y;
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+        for (int k = 0; k < 16; k++) {
+          if (k >= n_cl) break;
           const float4 v = vs[k];
-          const float f = ex2(ml.x - base);
-          sum = fmaf(ml.y, f, sum);
+          const float f = mls[k].y * inv;
           acc.x = fmaf(v.x, f, acc.x);
           acc.y = fmaf(v.y, f, acc.y);
           acc.z = fmaf(v.z, f, acc.z);
@@ -765,9 +777,8 @@ k_q8_rows(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
         }
         const int x = rt * a.rstep + row;
         const int64_t qr = (int64_t)(q0 + x / a.G) * a.Hq + h * a.G + x % a.G;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
         *reinterpret_cast<uint2 *>(a.out + qr * D + d4) =
-            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+            make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
         if (d4 == 0) a.lse[qr] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
       }
       __syncwarp();

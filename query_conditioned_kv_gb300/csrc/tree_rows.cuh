@@ -17,6 +17,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct TreeArgs {
+  static constexpr bool kMeans = false;  // part_o holds sums, not means
   const uint16_t *q, *kpool, *vpool;
   const int32_t *block_table, *ctx_len, *q_off;
   const uint32_t *mask;  // [n_q][mask_words] or NULL (a chain)
@@ -102,7 +103,8 @@ __device__ __forceinline__ uint32_t visible_bits(const TreeArgs &a, int i, int q
 // group of rows.  W warps share a row's partials (W 4: warp w takes the parts w,
 // w + 4, …, all in flight at once; their results are added in order), or each
 // takes join_rows / 4 rows of its own (W 1).  Bound by latency, so the fewest
-// dependent loads: sizes, then maxima and sums, then O.
+// dependent loads: sizes, then maxima and sums, then O.  Where the parts are means of
+// the values (O over the part's sum: Args::kMeans), so is what is joined at every step.
 template <class Args, int D, int W>
 __global__ void __launch_bounds__(128)
 k_tree_join(Args a) {
@@ -163,16 +165,25 @@ k_tree_join(Args a) {
       float s = ml.y * f;
 #pragma unroll
       for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+      float keep_o = keep * sum, fo = f * ml.y;  // a part's share of O
       sum = fmaf(sum, keep, s);
+      if constexpr (Args::kMeans) {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        keep_o *= inv;
+        fo *= inv;
+      } else {
+        keep_o = keep;
+        fo = f;
+      }
 #pragma unroll
-      for (int e = 0; e < E; e++) acc[e] *= keep;
+      for (int e = 0; e < E; e++) acc[e] *= keep_o;
       mx = now;
       const int n = min(32, (n_part - i0 + W - 1) / W);
 #pragma unroll 8
       for (int k = 0; k < n; k++) {
         const int i = i0 + W * k;
         const float *o = a.part_o + ((i == 0 ? first : 2 * (int64_t)(c0 + i)) * a.rows + row) * D + d0;
-        const float fk = __shfl_sync(0xFFFFFFFFu, f, k);
+        const float fk = __shfl_sync(0xFFFFFFFFu, fo, k);
         float v[E];
         if constexpr (E == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(o);
         else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(o);
@@ -193,14 +204,18 @@ k_tree_join(Args a) {
 #pragma unroll
       for (int e = 0; e < E; e++) acc[e] = 0.f;
 #pragma unroll
+      for (int w = 0; w < W; w++)
+        sum = fmaf(sh_ml[w].y, sh_ml[w].x == -INFINITY ? 0.f : ex2(sh_ml[w].x - mx), sum);
+      const float inv = !Args::kMeans ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
       for (int w = 0; w < W; w++) {
-        const float f = sh_ml[w].x == -INFINITY ? 0.f : ex2(sh_ml[w].x - mx);
-        sum = fmaf(sh_ml[w].y, f, sum);
+        float f = sh_ml[w].x == -INFINITY ? 0.f : ex2(sh_ml[w].x - mx);
+        if constexpr (Args::kMeans) f *= sh_ml[w].y * inv;
 #pragma unroll
         for (int e = 0; e < E; e++) acc[e] = fmaf(sh_o[w][d0 + e], f, acc[e]);
       }
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float inv = Args::kMeans ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
     const int x = rt * a.rstep + row;
     const int64_t qr = (int64_t)(q0 + x / a.G) * a.Hq + h * a.G + x % a.G;
     uint32_t w[E / 2];

@@ -836,6 +836,21 @@ def test_q8_no_weight_on_far_larger_scales(kvc):
     go(kvc, t)
 
 
+@pytest.mark.parametrize("top", [104, 115, 118])
+@pytest.mark.parametrize("n_req,len8,H,G,T,D", [(1, 200, 2, 4, 1, 128), (1, 20000, 2, 4, 1, 64), (3, 700, 4, 2, 1, 64),
+                                                 (1, 5000, 1, 4, 5, 128), (40, 600, 8, 4, 5, 64), (2, 130, 1, 8, 4, 128)])
+def test_q8_values_near_the_end_of_fp32(kvc, n_req, len8, H, G, T, D, top):
+    """Blocks of values under scales that kvc_q8_pack makes of bf16's largest: out is finite, however
+    many positions and parts add to it."""
+    t = Q8(top + len8, [len8 - 3 * r for r in range(n_req)], [3] * n_req, [T] * n_req, H, G, D, 16)
+    t.ks[:] = 2.0 ** -7
+    t.vs[:] = 2.0 ** top
+    t.vs[::5] = 2.0 ** -100
+    # (all of one sign, so that sums grow; none past 400·2^118)
+    t.v8.copy_(t.v8.float().abs().clamp(max=400).nan_to_num(0).to(F8))
+    go(kvc, t)
+
+
 def test_q8_bad_pages_and_requests(kvc):
     for BS in (16, 5):
         t = Q8(25, [100, 64, 40], [40, 0, 16], [2, 2, 1], 2, 2, 128, BS)
