@@ -1076,8 +1076,10 @@ kvc_status kvc_qkv_rope(const kvc_bf16 *q, int64_t q_stride, const kvc_bf16 *k,
  *   out         device bf16 [n_q][Hq][D];  lse  device fp32 [n_q][Hq] (natural
  *               log; kvc_attn_mass and kvc_recover_score take it); neither shares
  *               memory with the inputs
- * Accuracy, NaN and infinities: as kvc_tree_attn; positions that a row does not
- * see never reach its result, whatever they hold.  A row that sees nothing (every
+ * Accuracy and NaN: as kvc_tree_attn; positions that a row does not see never reach
+ * its result, whatever they hold.  An infinite value reaches the rows that see it as it
+ * is or, where its weight is less than fp32 holds, as NaN (which of the two may depend
+ * on the sizes).  A row that sees nothing (every
  * page of it outside the pool) gets out = 0 and lse = −inf.  Rows of q outside every
  * request are left alone.  No workspace.  Repeated calls give the same bits.
  * A request whose ctx_len or q_off is out of range (negative, T > max_rows, c + T >
@@ -1142,7 +1144,9 @@ kvc_status kvc_q8_pack(const kvc_bf16 *kpool, const kvc_bf16 *vpool, int64_t n_s
  * of the row's largest; logits, softmax statistics and sums are fp32; the weights of
  * the history's values are rounded to fp16 (a weight below 2^-14 of the row's largest
  * weight times scale to 2^-25 of that), those of the bf16 rows to bf16, out once to
- * bf16.  Repeated calls give the same bits.
+ * bf16.  Repeated calls give the same bits.  An infinite value of a new row reaches the
+ * rows that see it as it is, however small its weight; one of a cached row does so, or as
+ * NaN where fp32 has no such weight.
  * A request whose len8, ctx_len or q_off is out of range is recorded as
  * KVC_ERR_BOUNDS and its rows are left untouched; a position whose block id is
  * outside its pool is recorded and treated as not visible.

@@ -633,10 +633,10 @@ k_prompt_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         const float4 v = ld_cluster_f4(mapa_u32(ring_u + (xr * (D / 4) + (d4 ^ (row & 7))) * 16, k));
         const float f = ml.x == -INFINITY ? 1.f : ex2(ml.x - mx);
         sum = fmaf(ml.y, ml.x == -INFINITY ? 0.f : f, sum);
-        acc.x = fmaf(v.x, f, acc.x);
-        acc.y = fmaf(v.y, f, acc.y);
-        acc.z = fmaf(v.z, f, acc.z);
-        acc.w = fmaf(v.w, f, acc.w);
+        acc.x = fmaf(v.x, share_of(v.x, f), acc.x);
+        acc.y = fmaf(v.y, share_of(v.y, f), acc.y);
+        acc.z = fmaf(v.z, share_of(v.z, f), acc.z);
+        acc.w = fmaf(v.w, share_of(v.w, f), acc.w);
       }
       const int64_t qr = (int64_t)(q0 + token) * a.Hq + h * a.G + head;
       const float inv = sum == 0.f ? 0.f : 1.f / sum;

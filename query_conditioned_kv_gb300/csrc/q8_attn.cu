@@ -156,10 +156,50 @@ __device__ __forceinline__ void mma16816h(float (&d)[4], const uint32_t (&a)[4],
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void add_part(float4 &acc, const float4 &v, float f) {
+  acc.x = fmaf(v.x, f, acc.x);
+  acc.y = fmaf(v.y, f, acc.y);
+  acc.z = fmaf(v.z, f, acc.z);
+  acc.w = fmaf(v.w, f, acc.w);
+}
+__device__ __forceinline__ void add_part_inf(float4 &acc, const float4 &v, float f) {
+  acc.x = fmaf(v.x, share_of(v.x, f), acc.x);
+  acc.y = fmaf(v.y, share_of(v.y, f), acc.y);
+  acc.z = fmaf(v.z, share_of(v.z, f), acc.z);
+  acc.w = fmaf(v.w, share_of(v.w, f), acc.w);
+}
+__device__ __forceinline__ bool any_nan(const float4 &v) { return isnan(v.x) || isnan(v.y) || isnan(v.z) || isnan(v.w); }
 __device__ __forceinline__ float lg2(float x) {
   float y;
   asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// The values of nodes that are not finite, among a warp's keys of the tiles t0 … t1, to the
+// rows of its means that see them.  (Apart: seldom called.)
+template <int D, int KT>
+__device__ __noinline__ void add_infinite(const Q8Args &a, float *o_s, const int32_t *bt, int t0, int t1,
+                                          int th, int h, int rt, int n_rows, int q0, int c, int T) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t n_blocks = a.n_slots / a.BS;
+  __syncwarp();
+  for (int t = max(t0, th); t < t1; t++) {
+    const int p0 = (t - th) * a.tile + warp * KT;
+    if (p0 + KT <= c) continue;  // (cached rows only: left to the products)
+    for (int p = p0; p < min(p0 + KT, c + T); p++) {
+      const int pg = page_of(p, a.bs_inv);
+      const int32_t b = bt[pg];
+      if (b < 0 || b >= n_blocks) continue;
+      const uint16_t *vr = a.vpool + (((int64_t)b * a.BS + p - pg * a.BS) * a.H + h) * D;
+      for (int d = lane; d < D; d += 32) {
+        const float v = bf16_lo(vr[d]);
+        if (fabsf(v) < INFINITY) continue;
+        for (int row = 0; row < n_rows; row++)
+          if ((visible_bits<KT>(a, (rt * a.rstep + row) / a.G, q0, c, T, p0) >> (p - p0)) & 1u)
+            o_s[row * D + (d ^ (((row >> 1) & 3) << 3))] += v;
+      }
+    }
+  }
 }
 
 // CL: a cluster takes a unit, each CTA a part of its tiles, and joins the parts from one
@@ -369,6 +409,7 @@ k_q8_rows(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
     // warp's own.
     float o[CH8][NR][4], ref[NR][2], l[NR][2], off[NR][2], rs[NR][2];
     bool rounded = false;  // (warp-uniform) some reference is so large that differences need care
+    bool infinite = false;  // (warp-uniform) values of nodes were left out that are not finite
 #pragma unroll
     for (int nr = 0; nr < NR; nr++) {
 #pragma unroll
@@ -608,8 +649,8 @@ k_q8_rows(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
         softmax(std::integral_constant<int, 2 * MK>(), s, one, one, false, true, vis);
         // A node's V may hold infinities or NaN that some rows do not see, and a product 0·inf
         // would hand them to those rows.  A tile with such values takes the sum term by term,
-        // over the rows' visible keys only; there such a value is added as it is, for a weight
-        // too small for fp32 is not 0.
+        // over the rows' visible keys only, and leaves such a value to the run's end, where it is
+        // added as it is, for a weight too small for fp32 is not 0.
         bool odd = false;
         if (p0 + KT > c) {
           for (int e = lane; e < KT * CH; e += 32) {
@@ -622,8 +663,9 @@ k_q8_rows(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
           odd = __any_sync(0xFFFFFFFFu, odd);
         }
         if (odd) {
+          infinite = true;
           auto add = [](float w, float v, float &acc) {
-            acc = fabsf(v) < INFINITY ? fmaf(w, v, acc) : acc + v;
+            acc = fabsf(v) < INFINITY ? fmaf(w, v, acc) : acc;
           };
 #pragma unroll
           for (int nr = 0; nr < NR; nr++)
@@ -691,6 +733,7 @@ k_q8_rows(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
           for (int hf = 0; hf < 2; hf++)
             o_s[row * D + ((16 * n + 8 * hf + g8) ^ (quad << 3))] = o[n][nr][2 * hf + e] * inv * f;
       }
+    if (infinite) add_infinite<D, KT>(a, o_s, bt, t0, t1, th, h, rt, n_rows, q0, c, T);
     __syncthreads();
     const bool whole = !CL && t0 == 0 && t1 == n_kt;
     const int64_t slot = 2 * (int64_t)blockIdx.x + (g != run0);
@@ -709,18 +752,25 @@ k_q8_rows(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
         sum += share[w];
       }
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      auto part = [&](int w) {
+        return *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(sm) + (w * R + row) * D +
+                                                 (d4 ^ (((row >> 1) & 3) << 3)));
+      };
 #pragma unroll
       for (int w = 0; w < kQ8Warps; w++) {
         const float2 ml = ml_s[w * R + row];
         // (this warp saw nothing of the row; logits that are all NaN leave a NaN sum)
         if (ml.x == -INFINITY && ml.y == 0.f) continue;
-        const float f = share[w] * inv;
-        const float4 v = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(sm) +
-                                                           (w * R + row) * D + (d4 ^ (((row >> 1) & 3) << 3)));
-        acc.x = fmaf(v.x, f, acc.x);
-        acc.y = fmaf(v.y, f, acc.y);
-        acc.z = fmaf(v.z, f, acc.z);
-        acc.w = fmaf(v.w, f, acc.w);
+        add_part(acc, part(w), share[w] * inv);
+      }
+      if (any_nan(acc)) {  // perhaps an infinity of no weight
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kQ8Warps; w++) {
+          const float2 ml = ml_s[w * R + row];
+          if (ml.x == -INFINITY && ml.y == 0.f) continue;
+          add_part_inf(acc, part(w), share[w] * inv);
+        }
       }
       if (whole) {
         const int x = rt * a.rstep + row;
@@ -768,12 +818,15 @@ k_q8_rows(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUte
 #pragma unroll
         for (int k = 0; k < 16; k++) {
           if (k >= n_cl) break;
-          const float4 v = vs[k];
-          const float f = mls[k].y * inv;
-          acc.x = fmaf(v.x, f, acc.x);
-          acc.y = fmaf(v.y, f, acc.y);
-          acc.z = fmaf(v.z, f, acc.z);
-          acc.w = fmaf(v.w, f, acc.w);
+          add_part(acc, vs[k], mls[k].y * inv);
+        }
+        if (any_nan(acc)) {
+          acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int k = 0; k < 16; k++) {
+            if (k >= n_cl) break;
+            add_part_inf(acc, vs[k], mls[k].y * inv);
+          }
         }
         const int x = rt * a.rstep + row;
         const int64_t qr = (int64_t)(q0 + x / a.G) * a.Hq + h * a.G + x % a.G;

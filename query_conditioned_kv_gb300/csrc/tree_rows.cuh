@@ -5,6 +5,8 @@
 
 #include <math.h>
 
+#include <type_traits>
+
 #include "kvc_internal.cuh"
 #include "mma_ptx.cuh"
 
@@ -98,6 +100,12 @@ __device__ __forceinline__ uint32_t visible_bits(const TreeArgs &a, int i, int q
   return bits & full;
 }
 
+// The factor under which a part's O, v, joins a row: a share below fp32 is not 0, and an
+// infinity stays one under it.
+__device__ __forceinline__ float share_of(float v, float f) {
+  return f == 0.f && fabsf(v) == INFINITY ? 1.f : f;
+}
+
 // Joins the partials of one (request, KV head, row tile) that was split over
 // CTAs: blockIdx.x = (request, KV head), blockIdx.y = row tile, blockIdx.z a
 // group of rows.  W warps share a row's partials (W 4: warp w takes the parts w,
@@ -147,49 +155,60 @@ k_tree_join(Args a) {
   const int row0 = W == 1 ? blockIdx.z * a.join_rows + warp : blockIdx.z;
   const int row1 = W == 1 ? min(n_rows, (int)(blockIdx.z + 1) * a.join_rows) : min(n_rows, row0 + 1);
   for (int row = row0; row < row1; row += 4) {
-    float mx = -INFINITY, sum = 0.f, acc[E];
+    float mx, sum, acc[E];
+    auto gather = [&](auto Inf) {  // Inf: a part may hold an infinity of no share
+      mx = -INFINITY;
+      sum = 0.f;
 #pragma unroll
-    for (int e = 0; e < E; e++) acc[e] = 0.f;
-    for (int i0 = W == 1 ? 0 : warp; i0 < n_part; i0 += 32 * W) {
-      // part i is slot first (i = 0) or 2·(c0 + i): later CTAs begin inside the unit
-      const int mine = i0 + W * lane;
-      float2 ml = make_float2(-INFINITY, 0.f);
-      if (mine < n_part)
-        ml = a.part_ml[(mine == 0 ? first : 2 * (int64_t)(c0 + mine)) * a.rows + row];
-      float m = ml.x;
+      for (int e = 0; e < E; e++) acc[e] = 0.f;
+      for (int i0 = W == 1 ? 0 : warp; i0 < n_part; i0 += 32 * W) {
+        // part i is slot first (i = 0) or 2·(c0 + i): later CTAs begin inside the unit
+        const int mine = i0 + W * lane;
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (mine < n_part)
+          ml = a.part_ml[(mine == 0 ? first : 2 * (int64_t)(c0 + mine)) * a.rows + row];
+        float m = ml.x;
 #pragma unroll
-      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-      const float now = fmaxf(mx, m), base = now == -INFINITY ? 0.f : now;
-      const float keep = mx == -INFINITY ? 0.f : ex2(mx - base);
-      const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - base);
-      float s = ml.y * f;
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        const float now = fmaxf(mx, m), base = now == -INFINITY ? 0.f : now;
+        const float keep = mx == -INFINITY ? 0.f : ex2(mx - base);
+        const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - base);
+        float s = ml.y * f;
 #pragma unroll
-      for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-      float keep_o = keep * sum, fo = f * ml.y;  // a part's share of O
-      sum = fmaf(sum, keep, s);
-      if constexpr (Args::kMeans) {
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        keep_o *= inv;
-        fo *= inv;
-      } else {
-        keep_o = keep;
-        fo = f;
-      }
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+        float keep_o = keep * sum, fo = f * ml.y;  // a part's share of O
+        sum = fmaf(sum, keep, s);
+        if constexpr (Args::kMeans) {
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          keep_o *= inv;
+          fo *= inv;
+        } else {
+          keep_o = keep;
+          fo = f;
+        }
 #pragma unroll
-      for (int e = 0; e < E; e++) acc[e] *= keep_o;
-      mx = now;
-      const int n = min(32, (n_part - i0 + W - 1) / W);
+        for (int e = 0; e < E; e++) acc[e] *= Inf.value ? share_of(acc[e], keep_o) : keep_o;
+        mx = now;
+        const int n = min(32, (n_part - i0 + W - 1) / W);
 #pragma unroll 8
-      for (int k = 0; k < n; k++) {
-        const int i = i0 + W * k;
-        const float *o = a.part_o + ((i == 0 ? first : 2 * (int64_t)(c0 + i)) * a.rows + row) * D + d0;
-        const float fk = __shfl_sync(0xFFFFFFFFu, fo, k);
-        float v[E];
-        if constexpr (E == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(o);
-        else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(o);
+        for (int k = 0; k < n; k++) {
+          const int i = i0 + W * k;
+          const float *o = a.part_o + ((i == 0 ? first : 2 * (int64_t)(c0 + i)) * a.rows + row) * D + d0;
+          const float fk = __shfl_sync(0xFFFFFFFFu, fo, k);
+          float v[E];
+          if constexpr (E == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(o);
+          else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(o);
 #pragma unroll
-        for (int e = 0; e < E; e++) acc[e] = fmaf(v[e], fk, acc[e]);
+          for (int e = 0; e < E; e++) acc[e] = fmaf(v[e], Inf.value ? share_of(v[e], fk) : fk, acc[e]);
+        }
       }
+    };
+    gather(std::false_type());
+    if constexpr (Args::kMeans) {  // (0·inf is NaN: only then looked at)
+      bool nan = false;
+#pragma unroll
+      for (int e = 0; e < E; e++) nan |= isnan(acc[e]);
+      if (__any_sync(0xFFFFFFFFu, nan)) gather(std::true_type());
     }
     if constexpr (W > 1) {
 #pragma unroll
@@ -212,7 +231,10 @@ k_tree_join(Args a) {
         float f = sh_ml[w].x == -INFINITY ? 0.f : ex2(sh_ml[w].x - mx);
         if constexpr (Args::kMeans) f *= sh_ml[w].y * inv;
 #pragma unroll
-        for (int e = 0; e < E; e++) acc[e] = fmaf(sh_o[w][d0 + e], f, acc[e]);
+        for (int e = 0; e < E; e++) {
+          const float v = sh_o[w][d0 + e];
+          acc[e] = fmaf(v, Args::kMeans ? share_of(v, f) : f, acc[e]);
+        }
       }
     }
     const float inv = Args::kMeans ? 1.f : sum == 0.f ? 0.f : 1.f / sum;

@@ -458,6 +458,25 @@ def test_prompt_values_not_seen_never_reach_a_row(kvc):
                         inside(t.d["lse"][a + i, g][None], ls1, lb1, f"lse {r} {i} {g}")
 
 
+@pytest.mark.parametrize("n_req", [1, 90])
+def test_prompt_infinities_of_no_weight(kvc, n_req):
+    """An infinite value of a new row is the result of the rows that see it, also where their weights lie
+    elsewhere, whether one CTA takes a request's keys or a cluster."""
+    t = Prompt(83, [700] * n_req, [5] * n_req, 2, 2, 64, 16)
+    t.q[:] = 1.0
+    for r in range(n_req):
+        s = tree_ref.slots(t.bt[r], 16, 705)
+        t.k[s] = 0.0
+        t.k[s[:384]] = 37.5             # logits of 300, all others 0
+        t.v[s[702], 1, 5], t.v[s[703], 1, 6] = INF, -INF
+    t.gpu().call(kvc)
+    assert status(kvc, t.d["status"]) == 0
+    o = t.d["out"].float().cpu().view(n_req, 5, 2, 2, 64)
+    assert bool((o[:, 2:, 1, :, 5] == INF).all()) and bool((o[:, 3:, 1, :, 6] == -INF).all())
+    o[:, 2:, 1, :, 5], o[:, 3:, 1, :, 6] = 0.0, 0.0
+    assert bool(torch.isfinite(o).all()) and bool(torch.isfinite(t.d["lse"]).all())
+
+
 def test_prompt_bad_pages(kvc):
     for BS, room in ((16, 0), (5, 0), (16, 100)):
         t = Prompt(59, [40, 0, 16], [100, 64, 1], 2, 2, 128, BS, room=room)
@@ -877,6 +896,42 @@ def test_q8_values_not_seen_never_reach_a_row(kvc):
     out = t.d["out"].float().cpu()
     assert bool(torch.isfinite(out[:2]).all()) and bool((out[2:4, :, 3] == INF).all())
     assert bool(torch.isnan(out[4:, :, 9]).all()) and bool(torch.isfinite(out[4:, :, :9]).all())
+
+
+@pytest.mark.parametrize("n_req,G,len8", [(1, 1, 300), (1, 2, 3000), (1, 8, 900), (200, 1, 300), (40, 8, 300)])
+def test_q8_infinities_of_no_weight(kvc, n_req, G, len8):
+    """As in the prompt: rows whose weights lie in the history, by single CTAs, clusters and joined parts."""
+    t = Q8(85, [len8] * n_req, [5] * n_req, [4] * n_req, 2, G, 64, 16)
+    t.q[:] = 1.0
+    t.ks[:], t.vs[:] = 1.0, 2.0 ** -6
+    t.k8.view(torch.uint8)[:] = torch.tensor([40.0]).to(F8).view(torch.uint8)   # logits of 320
+    for r in range(n_req):
+        s = tree_ref.slots(t.bt[r], 16, 9)
+        t.k[s] = 0.0
+        t.v[s[7], 1, 5], t.v[s[8], 1, 6] = INF, -INF
+    t.gpu().call(kvc)
+    assert status(kvc, t.d["status"]) == 0
+    o = t.d["out"].float().cpu().view(n_req, 4, 2, G, 64)
+    assert bool((o[:, 2:, 1, :, 5] == INF).all()) and bool((o[:, 3:, 1, :, 6] == -INF).all())
+    o[:, 2:, 1, :, 5], o[:, 3:, 1, :, 6] = 0.0, 0.0
+    assert bool(torch.isfinite(o).all()) and bool(torch.isfinite(t.d["lse"]).all())
+
+
+def test_q8_infinity_before_a_key_that_takes_all_weight(kvc):
+    """A node's infinite value, and a later node whose logit raises the reference past it."""
+    t = Q8(87, [40], [0], [200], 1, 1, 64, 16)
+    s = tree_ref.slots(t.bt[0], 16, 200)
+    t.q[:] = 1.0
+    t.ks[:], t.vs[:] = 2.0 ** -20, 2.0 ** -6
+    t.k[s] = 0.0
+    t.k[s[130]] = 37.5
+    t.v[s[2], 0, 5] = INF
+    t.gpu().call(kvc)
+    assert status(kvc, t.d["status"]) == 0
+    o = t.d["out"].float().cpu()
+    assert bool((o[2:, 0, 5] == INF).all())
+    o[2:, 0, 5] = 0.0
+    assert bool(torch.isfinite(o).all())
 
 
 def test_q8_repeats_replays_and_streams(kvc):
