@@ -1140,11 +1140,12 @@ kvc_status kvc_q8_pack(const kvc_bf16 *kpool, const kvc_bf16 *vpool, int64_t n_s
  *   ws          device scratch of kvc_q8_attn_workspace_size() bytes (the size
  *               depends on the current device's SM count)
  * Made for few rows per KV head: every 32 of them read the cache once.
- * Accuracy: the products with k8 and v8 are exact but for q's values below 2^-39
- * of the row's largest; logits, softmax statistics and sums are fp32; the weights of
- * the history's values are rounded to fp16 (a weight below 2^-14 of the row's largest
- * weight times scale to 2^-25 of that), those of the bf16 rows to bf16, out once to
- * bf16.  Repeated calls give the same bits.  An infinite value of a new row reaches the
+ * Accuracy: a product with k8 takes q's value exactly from 2^-31 of the row's largest
+ * on, a smaller one to within 2^-39 of the largest; products with v8 are exact; logits,
+ * softmax statistics and sums are fp32; the weights of the history's values are rounded
+ * to fp16 (a weight below 2^-14 of the row's largest weight times scale to 2^-25 of
+ * that), those of the bf16 rows to bf16, out once to bf16.  That holds for any scales;
+ * for logits and the bf16 rows' values as in kvc_tree_attn.  Repeated calls give the same bits.  An infinite value of a new row reaches the
  * rows that see it as it is, however small its weight; one of a cached row does so, or as
  * NaN where fp32 has no such weight.
  * A request whose len8, ctx_len or q_off is out of range is recorded as

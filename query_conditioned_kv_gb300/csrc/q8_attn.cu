@@ -18,9 +18,9 @@
 // (mma.sync m16n8k16), so that rows come in eights and a token of four heads does not pay
 // for sixteen rows: 64 products a quarter tile and eight rows, half of what rows as M take.
 // e4m3 is a subset of fp16, so a byte becomes an fp16 operand by a conversion of two and
-// the products are exact; q, a bf16 value, is exact in fp16 once each row is shifted by a
-// power of two that puts its largest value just below 2^15 (what falls below fp16's range
-// is 2^-39 of that value).  V's operand is read by the transposing ldmatrix, two bytes a
+// the products are exact.  q, bf16 values of 8 bits, becomes fp16 under a power of two per
+// row that puts its largest value into [2^14, 2^15): exact while a value's last bit is 2^-24
+// or more (from 2^-31 of the largest on), below that rounded by up to 2^-25 (2^-39 of it).  V's operand is read by the transposing ldmatrix, two bytes a
 // number: a register then holds two columns of two positions, and O's columns come in
 // pairs until usual() puts them in order.
 //

@@ -871,6 +871,48 @@ def test_q8_values_near_the_end_of_fp32(kvc, n_req, len8, H, G, T, D, top):
 
 
 def test_q8_bad_pages_and_requests(kvc):
+@pytest.mark.parametrize("T,G", [(1, 4), (4, 2), (5, 6)])
+def test_q8_largest_values_of_bf16_rows(kvc, T, G):
+    """Values of 2^72 in the cached rows and nodes, whose logits rise past the history's."""
+    for step in (0.05, 4.0):
+        t = Q8(91, [200], [150], [T], 2, G, 64, 16)
+        n = 150 + T
+        s = tree_ref.slots(t.bt[0], 16, n)
+        t.q[:] = 1.0
+        t.scale = 1.0
+        t.ks[:] = 2.0 ** -20
+        t.k[s] = (torch.arange(n, dtype=torch.float32) * (step / 64)).to(torch.bfloat16)[:, None, None]
+        t.v[s] = (t.v[s].abs() + 0.5) * 2.0 ** 71
+        go(kvc, t)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_q8_queries_far_below_a_rows_largest(kvc, D):
+    """q enters the products exactly from 2^-31 of a row's largest value on, and to within 2^-39 of it
+    below: the largest meets keys of 0, so that the logits are the others'."""
+    for low, off in ((-31, 0.0), (-34, 2.0 ** -39), (-40, 2.0 ** -39)):
+        t = Q8(93, [150], [0], [1], 1, 4, D, 16)
+        t.scale = 1.0
+        t.q[:] = (torch.rand(t.q.shape, generator=torch.Generator().manual_seed(1)) + 1).bfloat16() * 2.0 ** low
+        t.q[..., 0] = 1.0
+        t.k8.view(torch.uint8)[..., 0] = 0
+        t.ks[:] = 2.0 ** (-low - 10)        # (logits of some units)
+        t.k[:] = 0.0
+        t.gpu().call(kvc)
+        assert status(kvc, t.d["status"]) == 0
+        o, ls, ob, lb = ref.q8(t.q, t.k8.float(), t.v8.float(), t.ks, t.vs, t.t8, t.len8, t.k, t.v, t.bt, 16,
+                               t.ctx, t.q_off, None, 1, 1.0)
+        # a logit's error, and what that makes of weights and values
+        blk = torch.from_numpy(t.t8[0])
+        k = t.k8.float()[blk].transpose(1, 2).reshape(-1, D)[:150].double()
+        v = (t.v8.float()[blk].double() * t.vs[blk].double()[..., None, None]).transpose(1, 2).reshape(-1, D)[:150]
+        ez = off * float((k.abs().sum(1) * t.ks[0, 0]).max())
+        # (every weight within exp(±2·ez) of its own, and any two means of the values within twice the top)
+        top = torch.cat([v.abs(), t.v[tree_ref.slots(t.bt[0], 16, 1)].double()[:, 0].abs()]).amax(0)
+        inside(t.d["lse"], ls, lb + ez, "lse")
+        inside(t.d["out"], o, ob + min(math.expm1(2 * ez), 2.0) * top, "out")
+
+
     for BS in (16, 5):
         t = Q8(25, [100, 64, 40], [40, 0, 16], [2, 2, 1], 2, 2, 128, BS)
         t.t8[0, 1], t.t8[1, 0], t.t8[2, 2] = t.n_blocks8, -1, 1 << 30
