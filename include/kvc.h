@@ -851,8 +851,10 @@ kvc_status kvc_tail_compact(kvc_bf16 *kpool, kvc_bf16 *vpool, int64_t n_slots, i
  * Accuracy: logits, softmax statistics and the value sums are fp32; the
  * weights exp(z − max) are rounded to bf16 for the product with V (their sum
  * is taken before that rounding), out is rounded once to bf16.  That holds for
- * logits up to 2^126, as finely as fp32 tells them apart; a NaN among the logits
- * a row sees makes its out and lse NaN.  Repeated calls give the same bits.
+ * logits up to 2^126, as finely as fp32 tells them apart, and for values up to 2^72
+ * (weights of up to 2^30, before the division by their sum, add up in fp32); a NaN
+ * among the logits a row sees makes its out and lse NaN.  Repeated calls give the same
+ * bits.
  * A request whose ctx_len or q_off is out of range (negative, T > max_tree,
  * c + T > max_blocks·block_size, rows past n_q) is recorded as
  * KVC_ERR_BOUNDS and its rows are left untouched; a visible position whose

@@ -445,6 +445,20 @@ def test_prompt_values_not_seen_never_reach_a_row(kvc):
         for r in range(2):
             c, a = t.ctx[r], int(t.q_off[r])
             for i in (0, 39, 40, 89, 90, 99, 100, 149, 150, 199):
+@pytest.mark.parametrize("T,ctx", [([600], [0]), ([40], [900]), ([5], [3000])])
+def test_prompt_largest_values(kvc, T, ctx):
+    """Values of 2^72 of one sign under logits that rise by up to 2^29 within a reference, and past it."""
+    for step in (0.05, 4.0):
+        t = Prompt(89, ctx, T, 1, 4, 64, 16, poison=False)
+        n = ctx[0] + T[0]
+        s = tree_ref.slots(t.bt[0], 16, n)
+        t.q[:] = 1.0
+        t.scale = 1.0
+        t.k[s, 0] = (torch.arange(n, dtype=torch.float32) * (step / 64)).to(torch.bfloat16)[:, None]
+        t.v[s] = (t.v[s].abs() + 0.5) * 2.0 ** 71
+        go(kvc, t)
+
+
                 if i >= t.T[r]:
                     continue
                 s = tree_ref.slots(t.bt[r], 16, c + i + 1)
