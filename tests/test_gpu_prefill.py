@@ -266,6 +266,22 @@ def test_rope_bad_pages_positions_and_requests(kvc):
     t.check(skip=range(29, 33))
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_rope_raw_keys_make_the_block_means(kvc, D):
+    """k_raw as kvc_build_meank takes it: the means of the keys that the projection's norm gives."""
+    t = Rope(69, [0], [96], 3, 2, D, 16, fused=False).gpu()
+    t.d["raw"] = torch.empty(3, 96, D, dtype=torch.bfloat16, device=DEV)
+    t.call(kvc)
+    mean = torch.empty(1, 3, 3, D, dtype=torch.bfloat16, device=DEV)
+    kvc.kvc_build_meank(t.d["raw"][None], mean, 1, 3, D, 96, t.d["status"])
+    assert status(kvc, t.d["status"]) == 0
+    y, rel = ref.normed(t.parts(t.qkv)[1].reshape(96, 3, D), t.wk, t.eps)
+    y = y.transpose(0, 1).reshape(3, 3, 32, D)
+    want = y.mean(2)
+    bound = (rel + ref.UBF * (1 + rel)) * y.abs().mean(2)
+    inside(mean[0], want, bound + ref.UBF * (want.abs() + bound) + 1e-38, "block means")
+
+
 def test_rope_repeats_replays_and_streams(kvc):
     t = Rope(15, [40, 3], [1, 1], 8, 4, 128, 16).gpu()
     t.call(kvc)
