@@ -1081,17 +1081,17 @@ kvc_status kvc_qkv_rope(const kvc_bf16 *q, int64_t q_stride, const kvc_bf16 *k,
  * Accuracy and NaN: as kvc_tree_attn; positions that a row does not see never reach
  * its result, whatever they hold.  An infinite value reaches the rows that see it as it
  * is or, where its weight is less than fp32 holds, as NaN (which of the two may depend
- * on the sizes).  A row that sees nothing (every
- * page of it outside the pool) gets out = 0 and lse = −inf.  Rows of q outside every
- * request are left alone.  No workspace.  Repeated calls give the same bits.
+ * on the sizes).  A row that sees nothing (every page of it outside the pool) gets out =
+ * 0 and lse = −inf.  Rows of q outside every request are left alone.  No workspace.
+ * Repeated calls give the same bits.
  * A request whose ctx_len or q_off is out of range (negative, T > max_rows, c + T >
  * max_blocks·block_size, rows past n_q) is recorded as KVC_ERR_BOUNDS and its rows
  * are left untouched; a visible position whose block id is outside the pool is
  * recorded and treated as not visible.  (Where q_off descends, requests beside the bad
  * one may be left out too.)
  * Errors: KVC_ERR_INVALID_ARG (NULL, sizes < 1, scale not finite, outputs that overlap
- * inputs or each other), KVC_ERR_SHAPE (D, Hq % H, Hq > 256, block_size > 64, max_rows > KVC_TREE_MAX_TOKENS, too many
- * positions), KVC_ERR_ALIGN (16 bytes; lse 4).
+ * inputs or each other), KVC_ERR_SHAPE (D, Hq % H, Hq > 256, block_size > 64, max_rows >
+ * KVC_TREE_MAX_TOKENS, too many positions), KVC_ERR_ALIGN (16 bytes; lse 4).
  * ---------------------------------------------------------------------- */
 kvc_status kvc_prompt_attn(const kvc_bf16 *q, const kvc_bf16 *kpool, const kvc_bf16 *vpool,
                            int64_t n_slots, const int32_t *block_table, int32_t max_blocks,

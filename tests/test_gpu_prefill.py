@@ -445,6 +445,20 @@ def test_prompt_rising_maxima(kvc):
     go(kvc, t)
 
 
+@pytest.mark.parametrize("T,ctx", [([600], [0]), ([40], [900]), ([5], [3000])])
+def test_prompt_largest_values(kvc, T, ctx):
+    """Values of 2^72 of one sign under logits that rise by up to 2^29 within a reference, and past it."""
+    for step in (0.05, 4.0):
+        t = Prompt(89, ctx, T, 1, 4, 64, 16, poison=False)
+        n = ctx[0] + T[0]
+        s = tree_ref.slots(t.bt[0], 16, n)
+        t.q[:] = 1.0
+        t.scale = 1.0
+        t.k[s, 0] = (torch.arange(n, dtype=torch.float32) * (step / 64)).to(torch.bfloat16)[:, None]
+        t.v[s] = (t.v[s].abs() + 0.5) * 2.0 ** 71
+        go(kvc, t)
+
+
 def test_prompt_values_not_seen_never_reach_a_row(kvc):
     """Infinite and NaN keys and values of later tokens reach exactly the rows that see them."""
     for D, G, room in ((128, 4, 0), (64, 1, 0), (128, 3, 0), (128, 4, 60), (64, 2, 200)):
@@ -461,20 +475,6 @@ def test_prompt_values_not_seen_never_reach_a_row(kvc):
         for r in range(2):
             c, a = t.ctx[r], int(t.q_off[r])
             for i in (0, 39, 40, 89, 90, 99, 100, 149, 150, 199):
-@pytest.mark.parametrize("T,ctx", [([600], [0]), ([40], [900]), ([5], [3000])])
-def test_prompt_largest_values(kvc, T, ctx):
-    """Values of 2^72 of one sign under logits that rise by up to 2^29 within a reference, and past it."""
-    for step in (0.05, 4.0):
-        t = Prompt(89, ctx, T, 1, 4, 64, 16, poison=False)
-        n = ctx[0] + T[0]
-        s = tree_ref.slots(t.bt[0], 16, n)
-        t.q[:] = 1.0
-        t.scale = 1.0
-        t.k[s, 0] = (torch.arange(n, dtype=torch.float32) * (step / 64)).to(torch.bfloat16)[:, None]
-        t.v[s] = (t.v[s].abs() + 0.5) * 2.0 ** 71
-        go(kvc, t)
-
-
                 if i >= t.T[r]:
                     continue
                 s = tree_ref.slots(t.bt[r], 16, c + i + 1)
@@ -871,36 +871,6 @@ def test_q8_extreme_scales_and_queries(kvc):
     go(kvc, t)
 
 
-def test_q8_no_weight_on_far_larger_scales(kvc):
-    """A CTA's first tile has the least scale of values, its next one scales 2^146 times as large at
-    positions of no weight: they add nothing."""
-    t = Q8(37, [160] * 16, [5] * 16, [1] * 16, 32, 1, 64, 16)
-    t.q[:] = t.q.abs()
-    for r in range(16):
-        t.ks[t.t8[r][:8]] = 2.0 ** -20
-        t.vs[t.t8[r][:8]] = 2.0 ** -126
-        t.ks[t.t8[r][8:]] = 0.5
-        t.vs[t.t8[r][8:]] = 2.0 ** 20
-        t.k8.view(torch.uint8)[t.t8[r][8:]] = torch.tensor([-448.0]).to(F8).view(torch.uint8)
-    go(kvc, t)
-
-
-@pytest.mark.parametrize("top", [104, 115, 118])
-@pytest.mark.parametrize("n_req,len8,H,G,T,D", [(1, 200, 2, 4, 1, 128), (1, 20000, 2, 4, 1, 64), (3, 700, 4, 2, 1, 64),
-                                                 (1, 5000, 1, 4, 5, 128), (40, 600, 8, 4, 5, 64), (2, 130, 1, 8, 4, 128)])
-def test_q8_values_near_the_end_of_fp32(kvc, n_req, len8, H, G, T, D, top):
-    """Blocks of values under scales that kvc_q8_pack makes of bf16's largest: out is finite, however
-    many positions and parts add to it."""
-    t = Q8(top + len8, [len8 - 3 * r for r in range(n_req)], [3] * n_req, [T] * n_req, H, G, D, 16)
-    t.ks[:] = 2.0 ** -7
-    t.vs[:] = 2.0 ** top
-    t.vs[::5] = 2.0 ** -100
-    # (all of one sign, so that sums grow; none past 400·2^118)
-    t.v8.copy_(t.v8.float().abs().clamp(max=400).nan_to_num(0).to(F8))
-    go(kvc, t)
-
-
-def test_q8_bad_pages_and_requests(kvc):
 @pytest.mark.parametrize("T,G", [(1, 4), (4, 2), (5, 6)])
 def test_q8_largest_values_of_bf16_rows(kvc, T, G):
     """Values of 2^72 in the cached rows and nodes, whose logits rise past the history's."""
@@ -943,6 +913,36 @@ def test_q8_queries_far_below_a_rows_largest(kvc, D):
         inside(t.d["out"], o, ob + min(math.expm1(2 * ez), 2.0) * top, "out")
 
 
+def test_q8_no_weight_on_far_larger_scales(kvc):
+    """A CTA's first tile has the least scale of values, its next one scales 2^146 times as large at
+    positions of no weight: they add nothing."""
+    t = Q8(37, [160] * 16, [5] * 16, [1] * 16, 32, 1, 64, 16)
+    t.q[:] = t.q.abs()
+    for r in range(16):
+        t.ks[t.t8[r][:8]] = 2.0 ** -20
+        t.vs[t.t8[r][:8]] = 2.0 ** -126
+        t.ks[t.t8[r][8:]] = 0.5
+        t.vs[t.t8[r][8:]] = 2.0 ** 20
+        t.k8.view(torch.uint8)[t.t8[r][8:]] = torch.tensor([-448.0]).to(F8).view(torch.uint8)
+    go(kvc, t)
+
+
+@pytest.mark.parametrize("top", [104, 115, 118])
+@pytest.mark.parametrize("n_req,len8,H,G,T,D", [(1, 200, 2, 4, 1, 128), (1, 20000, 2, 4, 1, 64), (3, 700, 4, 2, 1, 64),
+                                                 (1, 5000, 1, 4, 5, 128), (40, 600, 8, 4, 5, 64), (2, 130, 1, 8, 4, 128)])
+def test_q8_values_near_the_end_of_fp32(kvc, n_req, len8, H, G, T, D, top):
+    """Blocks of values under scales that kvc_q8_pack makes of bf16's largest: out is finite, however
+    many positions and parts add to it."""
+    t = Q8(top + len8, [len8 - 3 * r for r in range(n_req)], [3] * n_req, [T] * n_req, H, G, D, 16)
+    t.ks[:] = 2.0 ** -7
+    t.vs[:] = 2.0 ** top
+    t.vs[::5] = 2.0 ** -100
+    # (all of one sign, so that sums grow; none past 400·2^118)
+    t.v8.copy_(t.v8.float().abs().clamp(max=400).nan_to_num(0).to(F8))
+    go(kvc, t)
+
+
+def test_q8_bad_pages_and_requests(kvc):
     for BS in (16, 5):
         t = Q8(25, [100, 64, 40], [40, 0, 16], [2, 2, 1], 2, 2, 128, BS)
         t.t8[0, 1], t.t8[1, 0], t.t8[2, 2] = t.n_blocks8, -1, 1 << 30
