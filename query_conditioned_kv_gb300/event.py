@@ -677,6 +677,8 @@ class HistoryEvent:
         self.n_req, self.max_blocks, self.max_blocks8, self.BS = n_req, max_blocks, max_blocks8, block_size
         self.L, self.H, self.Hq, self.D = L, H, Hq, D
         self.n_slots, self.n_blocks8, self.n_q, self.max_rows = n_slots, n_blocks8, n_q, max_rows
+        if recent < 0 or (max_move is not None and max_move < 1):
+            raise ValueError(f"HistoryEvent: recent {recent}, max_move {max_move}")
         self.n_pos, self.recent, self.eps = n_pos, recent, eps
         self.max_move = max_blocks if max_move is None else min(max_move, max_blocks)
         self.scale = D ** -0.5 if scale is None else scale

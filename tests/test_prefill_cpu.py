@@ -132,6 +132,13 @@ def test_binding_refuses_wrong_rows(kvc):
         kvc.kvc_q8_pack(t.t(), t, 16, t, t, t, t, 1, t, t, 1, 1, 2, 64, 16)
 
 
+@pytest.mark.parametrize("change", [dict(recent=-1), dict(max_move=0), dict(max_move=-3)])
+def test_history_event_refuses(kvc, change):
+    from query_conditioned_kv_gb300.event import HistoryEvent
+    with pytest.raises(ValueError, match="HistoryEvent"):
+        HistoryEvent(1, 4, 4, 16, 1, 1, 1, 64, 64, 4, 4, 4, 8, **change)
+
+
 def test_reference_rotation_keeps_lengths_and_offsets():
     g = torch.Generator().manual_seed(3)
     x = torch.randn(2, 3, 64, generator=g, dtype=torch.float64)
