@@ -692,6 +692,9 @@ bool rows_map(CUtensorMap *m, const void *pool, int64_t n_slots, int H, int D, i
 // some SMs of a GPC empty.  8 KV and 32 query heads, D 128, in us by 1, 2, 4 and 8: 17
 // rows behind 8192 95, 60, 36, 25; 256 behind 65536 792, 422, 222, 351; 512 (twice) behind
 // 16384 213, 245, 272, 380; a prompt of 300 14, 21, 20, 21; of 1024 23, 43, 71, 154.
+// The keys are the table's width, for the lengths lie on the device; these figures are of
+// tables as long as the requests.  In wide ones a short prompt may go to a cluster: 300 rows,
+// a call alone after an L2 flush, 20 us in an exact table, 26 in one of 8K, 58 in one of 32K.
 int prompt_cluster(int64_t units, int64_t kt) {
   const double sms = device_sm_count();
   int best = 1;
@@ -717,7 +720,8 @@ cudaError_t launch_prompt_tc(const TreeArgs &a, int max_rows, cudaStream_t s) {
   p.gc = (a.G + p.n_ch - 1) / p.n_ch;
   p.tpt = 128 / p.gc;
   p.NS = (int)std::min<size_t>(kPaSlots, (kSmemMax - kFixed) / kSlot);
-  // (8192 tokens: pages of 32 and 16 400 us, of 8 405; of 12, row by row, 467)
+  // (8192 tokens, a call alone after an L2 flush: pages of 64 to 16 408 us, of 8 411; of 12, row
+  // by row, 469)
   p.box = a.BS % 32 == 0 ? 32 : a.BS % 16 == 0 ? 16 : a.BS % 8 == 0 ? 8 : 0;
   p.wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
   p.idesc_s = make_idesc(128, kPaKeys);

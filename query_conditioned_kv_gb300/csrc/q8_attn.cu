@@ -20,18 +20,24 @@
 // e4m3 is a subset of fp16, so a byte becomes an fp16 operand by a conversion of two and
 // the products are exact.  q, bf16 values of 8 bits, becomes fp16 under a power of two per
 // row that puts its largest value into [2^14, 2^15): exact while a value's last bit is 2^-24
-// or more (from 2^-31 of the largest on), below that rounded by up to 2^-25 (2^-39 of it).  V's operand is read by the transposing ldmatrix, two bytes a
-// number: a register then holds two columns of two positions, and O's columns come in
-// pairs until usual() puts them in order.
+// or more (from 2^-31 of the largest on), below that rounded by up to 2^-25 (2^-39 of it).
+// V's operand is read by the transposing ldmatrix, two bytes a number: a register then holds
+// two columns of two positions, and O's columns come in pairs until usual() puts them in order.
 //
 // The scales stay out of the operands: a logit is multiplied by s_k, and P is the weight
 // times s_v on a reference of its own.  References are a row's largest over its first
 // tile (less kQ8Room, in log2), raised when a weight passes 2^15: weights fit fp16 whatever the
 // scales, and a tile needs no maximum.
 //
-// One token, 8 KV and 32 query heads, D 128: 64 requests of up to 8192 140 us, 6.0 TB/s, 88 % of
-// a copy's rate; one of 4096 12.7, latency.  18 rows per KV head over two requests of 131072 125
-// us, 4.3 TB/s, bound by products and conversions.  Rows as the products' M took 166 and 179.
+// What leaves a warp is the mean of its values, and every join adds means by their shares
+// (sums on the softmax's reference would pass fp32 where |v| passes 2^113).  Infinite values of
+// nodes stay out of the products and are added to the means; an infinity under a share that
+// fp32 loses is looked for where a join gives NaN.
+//
+// One token, 8 KV and 32 query heads, D 128: 64 requests of up to 8192 142 us, 5.9 TB/s, 87 % of
+// a copy's rate; one of 4096 13, latency.  18 rows per KV head over two requests of 131072 129
+// us, 4.2 TB/s, bound by products and conversions (125 with sums for means and infinities in the
+// products).  Rows as the products' M took 166 and 179.
 #include <float.h>
 
 #include <algorithm>
@@ -889,9 +895,11 @@ bool rows8_map(CUtensorMap *m, const void *pool, int64_t rows, int D, int box) {
 // the two launches, 4.5 for every unit that a CTA meets.  Clusters: waves of CTAs, each its
 // share of a unit's tiles, 6 to begin and end where it waits for itself, 4 where for memory.
 // One token, 8 KV and 32 query heads, D 128, in us dealt out and by 1, 2, 4, 8 and 16: one
-// request of 200 9, 9, 8, 6.5, 6.6, 8; of 4096 12, 42, 25, 16, 12, 11; 4 of 8192 22, 77, 42,
-// 25, 19, 28; 16 of 4096 35, 44, 32, 45, 45, 76; 57 of 1024 (a CTA each) 29, 26, 33, 54, 85,
-// 178; 64 of 1024 36, 43, 45, 58, 97, 200; 128 of 200 38, 30, 46, 72, 142, 369.
+// request of 200 10, 9, 9, 7, 7, 8; of 4096 12, 43, 25, 16, 12, 11; 4 of 8192 23, 77, 43,
+// 25, 19, 28; 16 of 4096 36, 44, 32, 45, 46, 77; 57 of 1024 (a CTA each) 29, 26, 34, 55, 88,
+// 183; 64 of 1024 38, 44, 46, 59, 100, 206; 128 of 200 40, 30, 49, 78, 151, 382.  The tiles are
+// the tables' width, for the lengths lie on the device; these figures are of tables as long as
+// the requests.
 int q8_cluster(const Q8Args &a, int max_rt, int D) {
   if (max_rt > 1 || a.rows > 16) return 0;  // (a cluster takes one row tile; more rows leave it to the even deal)
   const double units = (double)a.n_req * a.H, all = q8_ctas(a.rows / 8) * (double)device_sm_count();
