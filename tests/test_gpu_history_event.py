@@ -408,3 +408,18 @@ def test_prompt_behind_a_history_is_recorded(captured):
     torch.cuda.synchronize()
     assert kvc.kvc_device_status(s.ev.dev_status) == 7
     assert bool((s.ev.out[:, :4] == 7.0).all()) and bool((s.ev.out[:, 4:7] != 7.0).any(-1).all())
+
+
+def test_write_keeps_the_raw_keys():
+    """write(k_raw): the step's keys before the rotation, head by head, in a buffer with room behind them."""
+    import query_conditioned_kv_gb300 as kvc
+    s = Serving(14)
+    q_off, x = s.inputs([9, 0, 4])
+    s.ev.begin(i32(q_off), n_q=13, max_rows=9)
+    raw = torch.full((s.H, 16, s.D), 7.0, dtype=torch.bfloat16, device=DEV)
+    s.ev.write(0, *s.parts(x[0, :13].to(DEV)), s.k[0], s.v[0], s.bt, s.wq, s.wk, k_raw=raw)
+    torch.cuda.synchronize()
+    assert kvc.kvc_device_status(s.ev.dev_status) == 0
+    y, rel = ref.normed(s.parts(x[0])[1].reshape(s.n_q, s.H, s.D)[:13], s.wk.cpu(), EPS)
+    inside(raw[:, :13], y.transpose(0, 1), (rel + ref.UBF * (1 + rel)) * y.transpose(0, 1).abs() + 1e-38, "raw keys")
+    assert bool((raw[:, 13:] == 7.0).all())
