@@ -1089,9 +1089,9 @@ kvc_status kvc_qkv_rope(const kvc_bf16 *q, int64_t q_stride, const kvc_bf16 *k,
  * are left untouched; a visible position whose block id is outside the pool is
  * recorded and treated as not visible.  (Where q_off descends, requests beside the bad
  * one may be left out too.)
- * Errors: KVC_ERR_INVALID_ARG (NULL, sizes < 1, scale not finite, outputs that overlap
- * inputs or each other), KVC_ERR_SHAPE (D, Hq % H, Hq > 256, block_size > 64, max_rows >
- * KVC_TREE_MAX_TOKENS, too many positions), KVC_ERR_ALIGN (16 bytes; lse 4).
+ * Errors: KVC_ERR_INVALID_ARG (NULL, sizes < 1, scale or scale·log2 e not finite, outputs
+ * that overlap inputs or each other), KVC_ERR_SHAPE (D, Hq % H, Hq > 256, block_size > 64,
+ * max_rows > KVC_TREE_MAX_TOKENS, too many positions), KVC_ERR_ALIGN (16 bytes; lse 4).
  * ---------------------------------------------------------------------- */
 kvc_status kvc_prompt_attn(const kvc_bf16 *q, const kvc_bf16 *kpool, const kvc_bf16 *vpool,
                            int64_t n_slots, const int32_t *block_table, int32_t max_blocks,
@@ -1154,7 +1154,8 @@ kvc_status kvc_q8_pack(const kvc_bf16 *kpool, const kvc_bf16 *vpool, int64_t n_s
  * KVC_ERR_BOUNDS and its rows are left untouched; a position whose block id is
  * outside its pool is recorded and treated as not visible.
  * Errors: as kvc_tree_attn (kscale, vscale: aligned to 4 bytes), and KVC_ERR_INVALID_ARG
- * for outputs or scratch that overlap inputs or each other.
+ * for a scale·log2 e that is not finite and for outputs or scratch that overlap inputs or
+ * each other.
  * ---------------------------------------------------------------------- */
 size_t kvc_q8_attn_workspace_size(int32_t n_req, int32_t max_blocks8, int32_t max_blocks,
                                   int32_t max_tree, int32_t H, int32_t Hq, int32_t D,

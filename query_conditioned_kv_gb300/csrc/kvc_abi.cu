@@ -57,6 +57,8 @@ bool outputs_overlap(std::initializer_list<Span> out, std::initializer_list<Span
   return false;
 }
 bool heads_ok(int H, int Hq) { return Hq >= H && Hq % H == 0 && Hq <= 256; }
+// (logits are taken in log2: an infinite factor would make NaN of products that are 0)
+bool scale_ok(float scale) { return isfinite(scale * 1.4426950408889634f); }
 
 bool score_kernel_ok(kvc_kernel k) {
   return k == KVC_KERNEL_AUTO || (k >= KVC_KERNEL_SCORE_FUSED && k <= KVC_KERNEL_SCORE_GROUP);
@@ -738,7 +740,7 @@ kvc_status kvc_prompt_attn(const kvc_bf16 *q, const kvc_bf16 *kpool, const kvc_b
                            int32_t *dev_status, cudaStream_t stream) {
   if (!q || !kpool || !vpool || !block_table || !ctx_len || !q_off || !out || !lse)
     return KVC_ERR_INVALID_ARG;
-  if (n_q < 1 || max_rows < 1 || !isfinite(scale)) return KVC_ERR_INVALID_ARG;
+  if (n_q < 1 || max_rows < 1 || !scale_ok(scale)) return KVC_ERR_INVALID_ARG;
   const kvc_status st = paged_status(1, n_req, H, D, block_size, max_blocks, n_slots);
   if (st != KVC_OK) return st;
   if (!heads_ok(H, Hq) || max_rows > KVC_TREE_MAX_TOKENS) return KVC_ERR_SHAPE;
@@ -806,7 +808,7 @@ kvc_status kvc_q8_attn(const kvc_bf16 *q, const uint8_t *k8, const uint8_t *v8,
   if (!q || !k8 || !v8 || !kscale || !vscale || !table8 || !len8 || !kpool || !vpool ||
       !block_table || !ctx_len || !q_off || !out || !lse || !ws)
     return KVC_ERR_INVALID_ARG;
-  if (n_q < 1 || max_tree < 1 || n_blocks8 < 1 || !isfinite(scale)) return KVC_ERR_INVALID_ARG;
+  if (n_q < 1 || max_tree < 1 || n_blocks8 < 1 || !scale_ok(scale)) return KVC_ERR_INVALID_ARG;
   kvc_status st = paged_status(1, n_req, H, D, block_size, max_blocks, n_slots);
   if (st == KVC_OK) st = paged_status(1, n_req, H, D, block_size, max_blocks8, n_slots);
   if (st != KVC_OK) return st;

@@ -105,6 +105,13 @@ def test_refused_before_any_launch(kvc, name, change, status):
     assert getattr(kvc.lib, name)(*args.values()) == status
 
 
+@pytest.mark.parametrize("name", ["kvc_prompt_attn", "kvc_q8_attn"])
+@pytest.mark.parametrize("scale", [3e38, -2.5e38])
+def test_scales_that_pass_fp32_in_log2_are_refused(kvc, name, scale):
+    args = dict(CALLS[name], scale=F(scale))
+    assert getattr(kvc.lib, name)(*args.values()) == INVALID
+
+
 def test_workspace_query(kvc):
     assert kvc.kvc_q8_attn_workspace_size(2, 4, 8, 40, 2, 8, 128, 16) > 0
     for bad in [(0, 4, 8, 40, 2, 8, 128, 16), (2, 0, 8, 40, 2, 8, 128, 16), (2, 4, 0, 40, 2, 8, 128, 16),
